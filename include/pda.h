@@ -69,6 +69,9 @@ enum {
 #define PDA_DEVERR_BAD_LENGTH   0x2u  /* seq_len < 0, a length beyond table width * block
                                          size, or a tile count outside [0, tile_capacity];
                                          the length was clamped                           */
+#define PDA_DEVERR_BAD_POSITION 0x8u  /* a rotation position outside [0, max_positions), or a new token
+                                         past its table row's width; the position was clamped,
+                                         the token's keys and values were not written           */
 #define PDA_DEVERR_TIMEOUT      0x4u  /* a bounded wait inside a kernel gave up (the kernel
                                          returned early; its output is not valid)         */
 
@@ -484,6 +487,151 @@ pda_status pda_decode_noalloc(const pda_bf16* q, const pda_bf16* k_pool, const p
                               int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                               float scale, pda_bf16* out, uint32_t* device_flags,
                               pda_stream stream);
+
+/* ---------------------------------------------------------------------------
+ * Around the decode: q / k preparation, writing and reading the cache, and
+ * decode over a cache held in 8 bits.  Not on the pages; the conventions are
+ * this library's own (pool layouts, block tables, seq_lens, flags).
+ */
+
+/*
+ * A paged KV cache in one of three formats.
+ *   format      PDA_CACHE_BF16, or one byte per element with a scale per
+ *               (token, kv head) for K and one for V:
+ *               PDA_CACHE_E4M3  OCP e4m3 (finite, largest magnitude 448),
+ *               PDA_CACHE_INT8  two's complement in -127 .. 127.
+ *               An element's value is its code's number times the scale.
+ *   k_pool,
+ *   v_pool      elements, placed by the stride triple (block, token, kv head)
+ *               in elements; rows are D-contiguous, bases are 16-byte aligned
+ *               and strides positive multiples of 16 bytes.  pda_paged_strides
+ *               and pda_slot_strides serve every format.
+ *   scales      [num_blocks, Hkv, 2, block_size] fp32, dense, 16-byte aligned:
+ *               [.., 0, t] the K scale and [.., 1, t] the V scale of block slot
+ *               t, side by side so that one copy fetches both.  Scales are
+ *               >= 0 and at most 2^120; 0 makes every element of the row 0, NaN
+ *               makes every element NaN.  NULL for PDA_CACHE_BF16.
+ */
+enum { PDA_CACHE_BF16 = 0, PDA_CACHE_E4M3 = 1, PDA_CACHE_INT8 = 2 };
+typedef struct pda_cache {
+    int32_t format;
+    int32_t reserved;  /* 0 */
+    void* k_pool;
+    void* v_pool;
+    float* scales;
+    int64_t num_blocks;
+    int64_t blk_stride, tok_stride, kvh_stride;
+} pda_cache;
+
+/*
+ * Heads of a run of tokens: bf16 [tokens, heads, D] with D-contiguous rows,
+ * 8-byte aligned base and strides (elements) that are multiples of 4 -- q, k
+ * or v inside a fused projection's output, for instance.
+ */
+typedef struct pda_heads {
+    pda_bf16* data;
+    int64_t tok_stride;
+    int64_t head_stride;
+} pda_heads;
+
+/*
+ * What happens to the query and key heads of pda_norm_rope and pda_append, in
+ * fp32 from the bf16 input to the one rounding of the output:
+ *   norm      y = x * rsqrt(mean(x^2) + eps) * weight over each head's D
+ *             elements, where q_weight / k_weight is not NULL ([D], bf16, or
+ *             fp32 when weights_f32; 8-byte aligned);
+ *   rotation  of the first rotary_dim columns where cos_sin is not NULL:
+ *             cos_sin is [max_positions, rotary_dim] fp32, 16-byte aligned, a
+ *             row holding rotary_dim / 2 cosines and then as many sines;
+ *             rotary_dim is a multiple of 8 up to D.  Pair i is columns
+ *             (i, i + rotary_dim / 2), or (2i, 2i + 1) when interleaved:
+ *             (a, b) -> (a cos - b sin, b cos + a sin).
+ */
+typedef struct pda_prep {
+    const void* q_weight;
+    const void* k_weight;
+    int32_t weights_f32;
+    float eps;
+    const float* cos_sin;
+    int32_t max_positions;
+    int32_t rotary_dim;
+    int32_t interleaved;
+    int32_t reserved;  /* 0 */
+} pda_prep;
+
+/*
+ * Norm and rotation of query and key heads in one pass.
+ *   q, q_out    num_tokens x Hq heads, k, k_out num_tokens x Hkv heads; an
+ *               output may be its input (in place), and must not overlap an
+ *               input otherwise.  q or k may be NULL (with its output).
+ *   positions   [num_tokens] int32 (device), one per token; needed when
+ *               prep->cos_sin is given.
+ * Heads of different tokens are independent; num_tokens 0 returns PDA_OK.
+ */
+pda_status pda_norm_rope(pda_ctx* ctx, const pda_heads* q, const pda_heads* k,
+                         const int32_t* positions, int64_t num_tokens, const pda_prep* prep,
+                         const pda_heads* q_out, const pda_heads* k_out, pda_stream stream);
+
+/*
+ * Writes the keys and values of new tokens into a cache (any format).
+ *   k, v        [num_tokens, Hkv, D]: the new tokens of each sequence in turn.
+ *   starts      [batch + 1] int32 (device): sequence b's new tokens are rows
+ *               starts[b] .. starts[b+1] - 1; rows from starts[batch] on are
+ *               padding.  NULL: every sequence has num_tokens / batch (exact).
+ *   seq_lens    [batch] int32 (device), the new tokens counted: sequence b's n
+ *               new tokens are its tokens seq_lens[b] - n .. seq_lens[b] - 1,
+ *               as pda_decode_multi counts them; token t goes to slot t % bs
+ *               of block block_table[b, t / bs].  Tokens before 0 are padding.
+ *   prep        norm and rotation of k (and q) on the way, or NULL.  The
+ *               rotation position is positions[row] ([num_tokens] int32,
+ *               device), or the token's index in its sequence when NULL.
+ *   q, q_out    optional: the new tokens' query heads, normed and rotated
+ *               into q_out in the same launch (q_out may be q).
+ * 8-bit formats: scale = amax / M with amax = max |x| over the row's D fp32
+ * values and M the format's largest magnitude; code = x * (M / amax) rounded
+ * to nearest even.  A row with amax below 2^-100 is stored as zeros with scale
+ * 0, a row that holds an infinity or a NaN as zeros with scale NaN.
+ * Padding rows write nothing, in the cache or q_out.  Two new tokens must not
+ * share a slot.  As a kernel between two tile steps of one
+ * step this counts as one that triggers its dependents early; on the context
+ * of the tile steps the next one waits for it.
+ */
+pda_status pda_append(pda_ctx* ctx, const pda_heads* k, const pda_heads* v, const pda_cache* cache,
+                      const int32_t* block_table, int32_t max_blocks, const int32_t* seq_lens,
+                      int32_t batch, const int32_t* starts, const int32_t* positions,
+                      int64_t num_tokens, const pda_prep* prep, const pda_heads* q,
+                      const pda_heads* q_out, pda_stream stream);
+
+/*
+ * Reads sequences back out of a cache: their first seq_lens[b] tokens,
+ * gathered from their blocks (and dequantised) into dense rows.
+ *   k_out, v_out  [num_rows, Hkv, D] bf16 (round to nearest even), or fp32
+ *                 when out_f32; 16-byte aligned.  Either may be NULL.
+ *   starts        [batch + 1] int32 (device), not decreasing: token t of
+ *                 sequence b is row starts[b] + t, and rows of sequence b end
+ *                 before starts[b+1].  NULL: num_rows / batch (exact) rows for
+ *                 each sequence.  Rows of no token are left as they were.
+ * A block id outside the pool reads as zeros, with the flag set.
+ */
+pda_status pda_read_cache(pda_ctx* ctx, const pda_cache* cache, const int32_t* block_table,
+                          int32_t max_blocks, const int32_t* seq_lens, int32_t batch,
+                          const int32_t* starts, int64_t num_rows, void* k_out, void* v_out,
+                          int32_t out_f32, pda_stream stream);
+
+/*
+ * Decode over a cache of any format: pda_decode (q_len 1) or, with the causal
+ * mask of pda_decode_multi, the last q_len tokens of each sequence.
+ *   q     [batch, q_len, Hq, D] bf16; out the same shape, bf16, or fp32 (o / l
+ *         unrounded) when out_f32, which PDA_CACHE_BF16 has for q_len 1 only.
+ *   batch * q_len <= max_seqs.  Other arguments as pda_decode.
+ * 8-bit caches are read as they are: HBM sees one byte per element and 4 per
+ * row; codes become fp16 in registers (exactly), K scales multiply the scores
+ * and V scales the softmax weights, in fp32.
+ */
+pda_status pda_decode_cache(pda_ctx* ctx, const pda_bf16* q, const pda_cache* cache,
+                            const int32_t* block_table, int32_t max_blocks,
+                            const int32_t* seq_lens, int32_t batch, int32_t q_len, float scale,
+                            void* out, int32_t out_f32, pda_stream stream);
 
 #ifdef __cplusplus
 }

@@ -19,6 +19,13 @@ Tiled lifecycle (tiled_attention.rs: begin_step / step_tile / finalize)::
     for tile_blocks, counts, last_valid in tiles:
         ctx.step_tile(q, k_pool, v_pool, tile_blocks, counts, last_valid)
     out = ctx.finalize(B)
+
+A layer's step over a cache in 8 bits (one scale per token and kv head)::
+
+    k_pool, v_pool, scales = ctx.new_cache(num_blocks, torch.float8_e4m3fn)   # or torch.int8
+    q = ctx.append(k, v, k_pool, v_pool, block_table, seq_lens, scales=scales, q=q,
+                   q_weight=wq, k_weight=wk, cos_sin=pda.rope_table(max_len, 128))
+    out = ctx.decode(q, k_pool, v_pool, block_table, seq_lens, scales=scales)
 """
 from __future__ import annotations
 
@@ -27,14 +34,15 @@ import os
 from typing import Optional, Sequence, Tuple
 
 __all__ = ["Context", "PdaError", "lib", "library_path", "check_dims", "paged_strides",
-           "slot_strides", "plan_units", "gather_states", "DEVERR_BAD_BLOCK_ID",
-           "DEVERR_BAD_LENGTH", "DEVERR_TIMEOUT"]
+           "slot_strides", "plan_units", "gather_states", "rope_table", "DEVERR_BAD_BLOCK_ID",
+           "DEVERR_BAD_LENGTH", "DEVERR_BAD_POSITION", "DEVERR_TIMEOUT"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIBPATH = os.path.join(_HERE, "libpda.so")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_NO_DEVICE, ERR_DEVICE_DATA = range(6)
-DEVERR_BAD_BLOCK_ID, DEVERR_BAD_LENGTH, DEVERR_TIMEOUT = 0x1, 0x2, 0x4
+DEVERR_BAD_BLOCK_ID, DEVERR_BAD_LENGTH, DEVERR_TIMEOUT, DEVERR_BAD_POSITION = 0x1, 0x2, 0x4, 0x8
+CACHE_BF16, CACHE_E4M3, CACHE_INT8 = range(3)
 
 
 class PdaError(RuntimeError):
@@ -62,6 +70,22 @@ class MultiInfo(ctypes.Structure):
     _fields_ = [("form", ctypes.c_int32), ("queries_per_walk", ctypes.c_int32),
                 ("rows_per_walk", ctypes.c_int32), ("walks_per_seq", ctypes.c_int32),
                 ("split_ctas", ctypes.c_int32), ("stages", ctypes.c_int32)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("reserved", ctypes.c_int32), ("k_pool", ctypes.c_void_p),
+                ("v_pool", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("num_blocks", ctypes.c_int64),
+                ("blk_stride", ctypes.c_int64), ("tok_stride", ctypes.c_int64), ("kvh_stride", ctypes.c_int64)]
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("tok_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class _Prep(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("weights_f32", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("cos_sin", ctypes.c_void_p), ("max_positions", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 _LIB: Optional[ctypes.CDLL] = None
@@ -103,6 +127,10 @@ def lib() -> ctypes.CDLL:
         "pda_export_state": (I32, [P, I32, P, P, P, P]),
         "pda_merge_states": (I32, [P, I32, I32, P, P, P, P, P]),
         "pda_merge_states_f32": (I32, [P, I32, I32, P, P, P, P, P]),
+        "pda_norm_rope": (I32, [P, P, P, P, I64, P, P, P, P]),
+        "pda_append": (I32, [P, P, P, P, P, I32, P, I32, P, P, I64, P, P, P, P]),
+        "pda_read_cache": (I32, [P, P, P, I32, P, I32, P, I64, P, P, I32, P]),
+        "pda_decode_cache": (I32, [P, P, P, P, I32, P, I32, I32, F, P, I32, P]),
         "pda_debug_gather": (I32, [P, P, P, I64, I64, I64, I64, P, I32, P, I32, P, P, P]),
         "pda_read_device_errors": (I32, [P, ctypes.POINTER(ctypes.c_uint32), I32, P]),
         "pda_set_timing_events": (I32, [P, P, P, P]),
@@ -175,6 +203,20 @@ def plan_units(lens: Sequence[int], *, block_size: int, num_kv_heads: int, split
                                 num_kv_heads, split_ctas, unit_cost, stage_tokens, first.ctypes.data,
                                 last.ctypes.data, ctypes.byref(total)))
     return first[:n], last[:n], int(total.value)
+
+
+def rope_table(max_positions: int, rotary_dim: int, base: float = 10000.0, inv_freq=None, device="cuda"):
+    """The cos_sin table of norm_rope and append: [max_positions, rotary_dim] fp32, a row's
+    rotary_dim / 2 cosines before its sines, of the angles position * inv_freq (by default
+    base ** (-2 i / rotary_dim)).  Angles are taken in fp64: far positions lose nothing."""
+    torch = _torch()
+    if inv_freq is None:
+        inv_freq = float(base) ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64) / rotary_dim)
+    inv_freq = torch.as_tensor(inv_freq).to(device=device, dtype=torch.float64)
+    if inv_freq.shape != (rotary_dim // 2,):
+        raise ValueError("inv_freq must hold rotary_dim / 2 values")
+    a = torch.arange(max_positions, dtype=torch.float64, device=inv_freq.device)[:, None] * inv_freq
+    return torch.cat([a.cos(), a.sin()], 1).float()
 
 
 def _torch():
@@ -284,18 +326,102 @@ class Context:
                 raise ValueError("num_blocks is required with explicit strides")
         return tuple(int(s) for s in strides), int(num_blocks)
 
+    def _cache(self, k_pool, v_pool, scales, strides, num_blocks) -> _Cache:
+        """The pda_cache of pools of any format; 8-bit pools come with their scales."""
+        torch = _torch()
+        d = self.dims
+        formats = {torch.bfloat16: CACHE_BF16, torch.float8_e4m3fn: CACHE_E4M3, torch.int8: CACHE_INT8}
+        fmt = formats.get(k_pool.dtype)
+        if fmt is None or v_pool.dtype != k_pool.dtype:
+            raise ValueError("k_pool / v_pool must both be bfloat16, float8_e4m3fn or int8")
+        self._here(k_pool, "k_pool")
+        self._here(v_pool, "v_pool")
+        if strides is None:
+            shape = (k_pool.shape[0], d.block_size, d.num_kv_heads, d.head_dim)
+            for t, name in ((k_pool, "k_pool"), (v_pool, "v_pool")):
+                if tuple(t.shape) != shape or not t.is_contiguous():
+                    raise ValueError(f"{name} must be contiguous [num_blocks, {shape[1]}, {shape[2]}, {shape[3]}]")
+            num_blocks = shape[0]
+            strides = (shape[1] * shape[2] * shape[3], shape[2] * shape[3], shape[3])
+        elif num_blocks is None:
+            raise ValueError("num_blocks is required with explicit strides")
+        if fmt == CACHE_BF16:
+            if scales is not None:
+                raise ValueError("a bfloat16 cache has no scales")
+        else:
+            shape = (int(num_blocks), d.num_kv_heads, 2, d.block_size)
+            if scales is None or scales.dtype != torch.float32 or tuple(scales.shape) != shape or \
+                    not scales.is_contiguous():
+                raise ValueError(f"scales of an 8-bit cache must be a contiguous float32 tensor of shape {shape}")
+            self._here(scales, "scales")
+        return _Cache(fmt, 0, _ptr(k_pool), _ptr(v_pool), _ptr(scales), int(num_blocks), *(int(x) for x in strides))
+
+    def _here(self, t, name):
+        if t.device != self.device:
+            raise ValueError(f"{name} must be on {self.device}, the context's device")
+        return t
+
+    def _heads(self, t, name, tokens, heads) -> _Heads:
+        if t.dtype != _torch().bfloat16 or tuple(t.shape) != (tokens, heads, self.dims.head_dim) or t.stride(2) != 1:
+            raise ValueError(f"{name} must be bfloat16 [{tokens}, {heads}, {self.dims.head_dim}] with contiguous rows")
+        self._here(t, name)
+        # the strides of an axis of one entry say nothing
+        return _Heads(_ptr(t), t.stride(0) if tokens > 1 else heads * self.dims.head_dim,
+                      t.stride(1) if heads > 1 else self.dims.head_dim)
+
+    def _prep(self, q_weight, k_weight, eps, cos_sin, interleaved) -> _Prep:
+        torch = _torch()
+        given = [w for w in (q_weight, k_weight) if w is not None]
+        for w in given:
+            if w.dtype not in (torch.bfloat16, torch.float32) or w.dtype != given[0].dtype or \
+                    tuple(w.shape) != (self.dims.head_dim,) or not w.is_contiguous():
+                raise ValueError("q_weight / k_weight must be contiguous bfloat16 or float32 (both the same) "
+                                 f"[{self.dims.head_dim}]")
+            self._here(w, "norm weights")
+        rows = cols = 0
+        if cos_sin is not None:
+            if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+                raise ValueError("cos_sin must be a contiguous float32 [max_positions, rotary_dim] tensor")
+            self._here(cos_sin, "cos_sin")
+            rows, cols = cos_sin.shape
+        return _Prep(_ptr(q_weight), _ptr(k_weight), int(bool(given) and given[0].dtype == torch.float32), float(eps),
+                     _ptr(cos_sin), int(rows), int(cols), int(bool(interleaved)), 0)
+
+    def _sequences(self, block_table, seq_lens, starts):
+        """Checks a block table, its lengths and token starts; returns (table width, sequences)."""
+        B = int(seq_lens.shape[0])
+        self._here(self._i32(block_table, "block_table", 2), "block_table")
+        self._here(self._i32(seq_lens, "seq_lens", 1), "seq_lens")
+        if block_table.shape[0] != B:
+            raise ValueError("block_table must have one row per sequence")
+        if starts is not None:
+            self._here(self._i32(starts, "starts", 1), "starts")
+            if starts.shape[0] != B + 1:
+                raise ValueError("starts must hold one entry per sequence and the end")
+        return int(block_table.shape[1]), B
+
     def _scale(self, scale) -> float:
         return float("nan") if scale is None else float(scale)
 
     # -- one-shot decode
     def decode(self, q, k_pool, v_pool, block_table, seq_lens, scale: Optional[float] = None,
                out=None, strides: Optional[Sequence[int]] = None, num_blocks: Optional[int] = None,
-               stream=None, out_dtype=None):
+               stream=None, out_dtype=None, scales=None):
         """softmax(scale * q K^T) V over each sequence's paged KV -> [B, Hq, D].
 
         ``out_dtype=torch.float32`` returns the fp32 quotient o / l (no bf16 rounding).
+        Pools in 8 bits (float8_e4m3fn, int8) come with their ``scales``
+        [num_blocks, Hkv, 2, block_size] (pda_decode_cache).
         """
         torch = _torch()
+        if scales is not None or k_pool.dtype in (torch.float8_e4m3fn, torch.int8):
+            B = int(seq_lens.shape[0])
+            self._bf16(q, "q", (B, self.dims.num_q_heads, self.dims.head_dim))
+            if out is None:
+                out = torch.empty(q.shape, device=q.device,
+                                  dtype=torch.float32 if out_dtype == torch.float32 else torch.bfloat16)
+            return self._decode_cache(q, 1, k_pool, v_pool, scales, block_table, seq_lens, scale, out, strides,
+                                      num_blocks, stream)()
         d = self.dims
         B = int(seq_lens.shape[0])
         self._bf16(q, "q", (B, d.num_q_heads, d.head_dim))
@@ -324,7 +450,7 @@ class Context:
 
     def bind_decode(self, q, k_pool, v_pool, block_table, seq_lens, out,
                     scale: Optional[float] = None, strides: Optional[Sequence[int]] = None,
-                    num_blocks: Optional[int] = None, stream=None):
+                    num_blocks: Optional[int] = None, stream=None, scales=None):
         """Validates one decode's tensors once and returns a zero-argument callable
         that reruns it (the same buffers, their contents free to change between
         calls) with only the C call: for decode loops over persistent buffers
@@ -332,6 +458,10 @@ class Context:
         context alive, launches on the stream current at binding (or `stream`),
         and raises once the context is closed."""
         d = self.dims
+        if scales is not None or k_pool.dtype in (_torch().float8_e4m3fn, _torch().int8):
+            self._bf16(q, "q", (int(seq_lens.shape[0]), d.num_q_heads, d.head_dim))
+            return self._decode_cache(q, 1, k_pool, v_pool, scales, block_table, seq_lens, scale, out, strides,
+                                      num_blocks, stream)
         B = int(seq_lens.shape[0])
         self._bf16(q, "q", (B, d.num_q_heads, d.head_dim))
         self._i32(block_table, "block_table", 2)
@@ -347,15 +477,21 @@ class Context:
                       (q, k_pool, v_pool, block_table, seq_lens, out))
 
     def decode_multi(self, q, k_pool, v_pool, block_table, seq_lens, scale: Optional[float] = None,
-                     out=None, stream=None):
+                     out=None, stream=None, scales=None):
         """Causal multi-query decode: q [B, q_len, Hq, D] are each sequence's last q_len
-        tokens; query i sees tokens up to seq_lens[b] - q_len + i.  Returns [B, q_len, Hq, D]."""
+        tokens; query i sees tokens up to seq_lens[b] - q_len + i.  Returns [B, q_len, Hq, D].
+        Pools in 8 bits come with their ``scales``, as for decode."""
         torch = _torch()
         d = self.dims
         B = int(seq_lens.shape[0])
         if q.dim() != 4 or q.shape[0] != B or q.shape[2:] != (d.num_q_heads, d.head_dim):
             raise ValueError("q must be [B, q_len, Hq, D]")
         self._bf16(q, "q")
+        if scales is not None or k_pool.dtype in (torch.float8_e4m3fn, torch.int8):
+            if out is None:
+                out = torch.empty_like(q)
+            return self._decode_cache(q, int(q.shape[1]), k_pool, v_pool, scales, block_table, seq_lens, scale, out,
+                                      None, None, stream)()
         self._i32(block_table, "block_table", 2)
         self._i32(seq_lens, "seq_lens", 1)
         (bs_, ts_, hs_), nblk = self._pool(k_pool, v_pool, None, None)
@@ -387,6 +523,156 @@ class Context:
                                            _ptr(seq_lens), B, self._scale(scale), _ptr(out),
                                            _stream(stream)))
         return out
+
+    def _decode_cache(self, q, q_len, k_pool, v_pool, scales, block_table, seq_lens, scale, out, strides,
+                      num_blocks, stream):
+        torch = _torch()
+        width, B = self._sequences(block_table, seq_lens, None)
+        cache = self._cache(k_pool, v_pool, scales, strides, num_blocks)
+        self._here(q, "q")
+        if out.dtype not in (torch.bfloat16, torch.float32) or out.shape != q.shape or not out.is_contiguous():
+            raise ValueError(f"out must be a contiguous bfloat16 or float32 tensor of shape {tuple(q.shape)}")
+        self._here(out, "out")
+        args = (_ptr(q), ctypes.addressof(cache), _ptr(block_table), width, _ptr(seq_lens), B, q_len,
+                self._scale(scale), _ptr(out), int(out.dtype == torch.float32), self._stream_of(stream))
+        return _Bound(self, lib().pda_decode_cache, args,
+                      (cache, q, k_pool, v_pool, scales, block_table, seq_lens, out), out)
+
+    def _stream_of(self, stream):
+        """`stream`, or the current stream of this context's device."""
+        return _stream(_torch().cuda.current_stream(self.device) if stream is None else stream)
+
+    # -- around the decode: q / k preparation, cache writes and read-backs
+    def new_cache(self, num_blocks: int, dtype=None):
+        """A zeroed cache of num_blocks blocks: (k_pool, v_pool, scales), pools
+        [num_blocks, block_size, Hkv, D] of `dtype` (bfloat16, float8_e4m3fn or int8) and
+        scales [num_blocks, Hkv, 2, block_size] float32 (None for bfloat16)."""
+        torch = _torch()
+        d = self.dims
+        dtype = torch.bfloat16 if dtype is None else dtype
+        if dtype not in (torch.bfloat16, torch.float8_e4m3fn, torch.int8):
+            raise ValueError("a cache is bfloat16, float8_e4m3fn or int8")
+        shape = (int(num_blocks), d.block_size, d.num_kv_heads, d.head_dim)
+        size = torch.empty((), dtype=dtype).element_size()
+        pools = [torch.zeros((*shape[:3], shape[3] * size), dtype=torch.int8, device=self.device).view(dtype)
+                 for _ in range(2)]
+        scales = None if dtype == torch.bfloat16 else torch.zeros((shape[0], d.num_kv_heads, 2, d.block_size),
+                                                                  device=self.device)
+        return pools[0], pools[1], scales
+
+    def norm_rope(self, q, k, positions=None, *, q_weight=None, k_weight=None, eps: float = 1e-6, cos_sin=None,
+                  interleaved: bool = False, q_out=None, k_out=None, stream=None):
+        """RMS norm of each query and key head (where its weight [D] is given) and rotation by
+        cos_sin[positions] (rope_table), in one pass: q [T, Hq, D], k [T, Hkv, D] bf16, of any
+        token and head strides (slices of a fused projection); q or k may be None.  Returns
+        (q_out, k_out), new tensors unless given (they may be q and k themselves)."""
+        return self.bind_norm_rope(q, k, positions, q_weight=q_weight, k_weight=k_weight, eps=eps, cos_sin=cos_sin,
+                                   interleaved=interleaved, q_out=q_out, k_out=k_out, stream=stream)()
+
+    def bind_norm_rope(self, q, k, positions=None, *, q_weight=None, k_weight=None, eps: float = 1e-6, cos_sin=None,
+                       interleaved: bool = False, q_out=None, k_out=None, stream=None):
+        """norm_rope with its tensors validated once: a callable as bind_decode's."""
+        torch = _torch()
+        d = self.dims
+        if q is None and k is None:
+            raise ValueError("neither q nor k given")
+        T = int((k if q is None else q).shape[0])
+        prep = self._prep(q_weight, k_weight, eps, cos_sin, interleaved)
+        self._positions(positions, T)
+        if cos_sin is not None and positions is None:
+            raise ValueError("the rotation needs positions")
+        pairs, outs = [], []
+        for x, out, name, heads in ((q, q_out, "q", d.num_q_heads), (k, k_out, "k", d.num_kv_heads)):
+            if x is not None and out is None:
+                out = torch.empty(x.shape, dtype=torch.bfloat16, device=self.device)
+            pairs.append((None, None) if x is None else
+                         (self._heads(x, name, T, heads), self._heads(out, name + "_out", T, heads)))
+            outs.append(None if x is None else out)
+        (qh, qo), (kh, ko) = pairs
+        at = [None if h is None else ctypes.addressof(h) for h in (qh, kh, qo, ko)]
+        args = (at[0], at[1], _ptr(positions), T, ctypes.addressof(prep), at[2], at[3], self._stream_of(stream))
+        return _Bound(self, lib().pda_norm_rope, args,
+                      (prep, pairs, q, k, positions, q_weight, k_weight, cos_sin), tuple(outs))
+
+    def _positions(self, positions, tokens):
+        if positions is not None:
+            self._here(self._i32(positions, "positions", 1), "positions")
+            if positions.shape[0] != tokens:
+                raise ValueError("positions must hold one entry per token")
+
+    def append(self, k, v, k_pool, v_pool, block_table, seq_lens, *, scales=None, starts=None, positions=None, q=None,
+               q_out=None, q_weight=None, k_weight=None, eps: float = 1e-6, cos_sin=None, interleaved: bool = False,
+               strides: Optional[Sequence[int]] = None, num_blocks: Optional[int] = None, stream=None):
+        """Writes the new tokens' k, v [T, Hkv, D] into the cache (quantised where its pools are
+        8-bit), k normed and rotated on the way as in norm_rope where k_weight / cos_sin are
+        given; with q [T, Hq, D] the queries too, returned as q_out (None without q).
+
+        seq_lens counts the new tokens: sequence b's are its last starts[b+1] - starts[b]
+        (starts [B+1] int32; None: T / B each).  The rotation position is positions[row], or
+        the token's index in its sequence (pda_append)."""
+        return self.bind_append(k, v, k_pool, v_pool, block_table, seq_lens, scales=scales, starts=starts,
+                                positions=positions, q=q, q_out=q_out, q_weight=q_weight, k_weight=k_weight, eps=eps,
+                                cos_sin=cos_sin, interleaved=interleaved, strides=strides, num_blocks=num_blocks,
+                                stream=stream)()
+
+    def bind_append(self, k, v, k_pool, v_pool, block_table, seq_lens, *, scales=None, starts=None, positions=None,
+                    q=None, q_out=None, q_weight=None, k_weight=None, eps: float = 1e-6, cos_sin=None,
+                    interleaved: bool = False, strides: Optional[Sequence[int]] = None,
+                    num_blocks: Optional[int] = None, stream=None):
+        """append with its tensors validated once: a callable as bind_decode's."""
+        torch = _torch()
+        d = self.dims
+        T = int(k.shape[0])
+        width, B = self._sequences(block_table, seq_lens, starts)
+        cache = self._cache(k_pool, v_pool, scales, strides, num_blocks)
+        prep = self._prep(q_weight, k_weight, eps, cos_sin, interleaved)
+        self._positions(positions, T)
+        kh, vh = self._heads(k, "k", T, d.num_kv_heads), self._heads(v, "v", T, d.num_kv_heads)
+        qh = qo = None
+        if q is not None:
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=self.device)
+            qh, qo = self._heads(q, "q", T, d.num_q_heads), self._heads(q_out, "q_out", T, d.num_q_heads)
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        at = [None if h is None else ctypes.addressof(h) for h in (kh, vh, cache, prep, qh, qo)]
+        args = (at[0], at[1], at[2], _ptr(block_table), width, _ptr(seq_lens), B, _ptr(starts), _ptr(positions), T,
+                at[3], at[4], at[5], self._stream_of(stream))
+        return _Bound(self, lib().pda_append, args,
+                      (kh, vh, cache, prep, qh, qo, k, v, q, k_pool, v_pool, scales, block_table, seq_lens, starts,
+                       positions, q_weight, k_weight, cos_sin), q_out)
+
+    def read_cache(self, k_pool, v_pool, block_table, seq_lens, *, scales=None, starts=None, k_out=None, v_out=None,
+                   out_dtype=None, strides: Optional[Sequence[int]] = None, num_blocks: Optional[int] = None,
+                   stream=None):
+        """The first seq_lens[b] tokens of every sequence, gathered and dequantised.  With starts
+        [B+1] int32 token t of sequence b is row starts[b] + t of k_out, v_out [rows, Hkv, D]
+        (given); without, the outputs are [B, S, Hkv, D], by default S the table's width in
+        tokens (the layout of decode_contiguous).  bf16, or fp32; rows of no token are left as
+        they were (zeros in new outputs)."""
+        torch = _torch()
+        d = self.dims
+        width, B = self._sequences(block_table, seq_lens, starts)
+        cache = self._cache(k_pool, v_pool, scales, strides, num_blocks)
+        if k_out is None and v_out is None:
+            if starts is not None:
+                raise ValueError("starts needs k_out / v_out")
+            k_out, v_out = (torch.zeros((B, width * d.block_size, d.num_kv_heads, d.head_dim), device=self.device,
+                                        dtype=out_dtype or torch.bfloat16) for _ in range(2))
+        outs = [t for t in (k_out, v_out) if t is not None]
+        for t in outs:
+            if t.dtype not in (torch.bfloat16, torch.float32) or t.dtype != (out_dtype or outs[0].dtype) or \
+                    t.shape != outs[0].shape or not t.is_contiguous() or \
+                    t.dim() != (4 if starts is None else 3) or t.shape[-2:] != (d.num_kv_heads, d.head_dim) or \
+                    (starts is None and t.shape[0] != B):
+                raise ValueError("k_out / v_out must be contiguous bfloat16 or float32 "
+                                 f"[{'B, S' if starts is None else 'rows'}, {d.num_kv_heads}, {d.head_dim}], alike")
+            self._here(t, "k_out / v_out")
+        rows = outs[0].shape[0] * (outs[0].shape[1] if starts is None else 1)
+        _check(lib().pda_read_cache(self._ctx, ctypes.addressof(cache), _ptr(block_table), width, _ptr(seq_lens), B,
+                                    _ptr(starts), rows, _ptr(k_out), _ptr(v_out),
+                                    int(outs[0].dtype == torch.float32), self._stream_of(stream)))
+        return k_out, v_out
 
     # -- tiled lifecycle
     def set_tile_overlap(self, enable: bool) -> None:
@@ -502,18 +788,21 @@ class Context:
 
 
 class _Bound:
-    """A decode with its arguments marshalled once (Context.bind_decode)."""
+    """A call with its arguments marshalled once (Context.bind_decode and its like)."""
 
-    __slots__ = ("_owner", "_fn", "_args", "_keep")
+    __slots__ = ("_owner", "_fn", "_args", "_keep", "_out")
 
-    def __init__(self, owner, fn, args, keep):
-        self._owner, self._fn, self._args, self._keep = owner, fn, args, keep
+    def __init__(self, owner, fn, args, keep, out=None):
+        self._owner, self._fn, self._args, self._keep, self._out = owner, fn, args, keep, out
 
-    def __call__(self) -> None:
+    def __call__(self):
         ctx = self._owner._ctx
         if not ctx:
-            raise PdaError(ERR_INVALID_ARG, "the context of this bound decode is closed")
-        _check(self._fn(ctx, *self._args))
+            raise PdaError(ERR_INVALID_ARG, "the context of this bound call is closed")
+        status = self._fn(ctx, *self._args)
+        if status:
+            _check(status)
+        return self._out
 
 
 def gather_states(m, l, o, group=None):

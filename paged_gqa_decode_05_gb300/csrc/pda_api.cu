@@ -16,14 +16,13 @@
 #include <mutex>
 #include <string>
 
-#include "pda.h"
-#include "pda_launch.h"
-
-#define PDA_EXPORT extern "C" __attribute__((visibility("default")))
+#include "pda_ctx.h"
 
 namespace {
-
 thread_local std::string g_last_error;
+}  // namespace
+
+namespace pda {
 
 pda_status fail(pda_status st, const char* fmt, ...) {
     char buf[512];
@@ -39,8 +38,6 @@ pda_status cuda_fail(cudaError_t e, const char* what) {
     return fail(PDA_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     static std::once_flag once;
@@ -55,61 +52,34 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     return fn;
 }
 
-constexpr float kLog2e = 1.4426950408889634f;
+pda_status check_scale(float scale, int D, float* scale_log2) {
+    constexpr float kLog2e = 1.4426950408889634f;
+    if (std::isnan(scale)) scale = 1.0f / std::sqrt((float)D);
+    if (std::isinf(scale)) return fail(PDA_ERR_INVALID_ARG, "scale must be finite (NaN = default)");
+    *scale_log2 = scale * kLog2e;
+    return PDA_OK;
+}
 
-}  // namespace
+// The kernels keep a launch's plan-block prefix in int32: up to
+// kMaxLaunchBatch rows of at most table_width + unit_cost plan blocks each.
+pda_status check_plan_size(int64_t rows, int32_t table_width, int32_t unit_cost) {
+    const int64_t most = std::min<int64_t>(rows, kMaxLaunchBatch) * ((int64_t)table_width + unit_cost);
+    if (most > 0x7fffffffLL)
+        return fail(PDA_ERR_INVALID_ARG,
+                    "block table width %d is too large: %lld rows per launch could hold %lld "
+                    "blocks, more than a 32-bit prefix holds",
+                    table_width, (long long)std::min<int64_t>(rows, kMaxLaunchBatch), (long long)most);
+    return PDA_OK;
+}
 
-struct pda_pool_key {  // what a pool's tensor maps are encoded from
-    const void* k = nullptr;
-    const void* v = nullptr;
-    int64_t num_blocks = 0, blk = 0, tok = 0, kvh = 0;
-};
+}  // namespace pda
 
-struct pda_ctx {
-    pda_dims dims;
-    int32_t G = 0;
-    int device = 0;
-    int num_sms = 0;
-    int stages = 0;
-    int stage_rows = 64;  // split-kernel shape: KV rows per stage
-    int ctas_per_sm = 0;
-    int split_ctas = 0;
-    int smem_max = 0;
-    int64_t slots = 0;
-    int64_t part_rows = 0;  // q rows the partial-state buffers hold (all slots)
-    // Row form of multi-query (one / two 16-row q tiles): grid and pipeline
-    // depth; a grid of 0 when the shape does not exist (head size 256).
-    int rows_ctas[2] = {0, 0};
-    int rows_stages[2] = {0, 0};
-    // The tcgen05 row form (launch rows of 17 to 32 q rows): grid and depth
-    // (0: not on this shape), and whether calls take it (pda_set_multi_tc; off
-    // by default: measured slower than the mma.sync row form).
-    int tc_ctas = 0;
-    int tc_stages = 0;
-    bool multi_tc = false;
-    float* part_o = nullptr;
-    float* part_ml = nullptr;
-    int32_t* unit_sync = nullptr;  // [chunk_b*Hkv][2] split-unit tickets and stored counts
-    int64_t unit_sync_bytes = 0;
-    uint32_t* err = nullptr;
-    float* m_state = nullptr;
-    float* l_state = nullptr;
-    float* o_state = nullptr;
-    cudaEvent_t ev_begin = nullptr, ev_split = nullptr, ev_end = nullptr;
-    // Tiled lifecycle: tile steps since the last begin_step and the stream of
-    // the last one; a tile step right behind another on the same stream reads
-    // its inputs early (pda_set_tile_overlap turns that off).
-    int64_t tile_steps = 0;
-    cudaStream_t tile_stream = nullptr;
-    bool tile_overlap = true;
-    // The last pool's tensor maps: a decode loop over one cache encodes them
-    // once (encoding costs host time on every call otherwise).
-    bool maps_valid = false;
-    pda_pool_key maps_key;
-    int32_t maps_row_mode = 0;
-    CUtensorMap map_k, map_v;
-    CUtensorMap map_k1, map_v1;  // one-slab boxes (head size 128, block boxes): the tcgen05 form
-};
+using pda::aligned;
+using pda::check_plan_size;
+using pda::check_scale;
+using pda::cuda_fail;
+using pda::fail;
+using pda::tensor_map_encoder;
 
 namespace {
 
@@ -238,13 +208,6 @@ pda_status set_split_attributes(int D, int st, int optin) {
     return PDA_OK;
 }
 
-pda_status check_scale(float scale, int D, float* scale_log2) {
-    if (std::isnan(scale)) scale = 1.0f / std::sqrt((float)D);
-    if (std::isinf(scale)) return fail(PDA_ERR_INVALID_ARG, "scale must be finite (NaN = default)");
-    *scale_log2 = scale * kLog2e;
-    return PDA_OK;
-}
-
 struct RunArgs {
     int mode;
     const pda_bf16* q;
@@ -265,18 +228,6 @@ struct RunArgs {
     int32_t q_len = 1;        // causal queries per sequence (q, out: [batch, q_len, Hq, D])
     bool early_inputs = false;  // tiled: a tile step right behind another of the same step
 };
-
-// The kernels keep a launch's plan-block prefix in int32: up to
-// kMaxLaunchBatch rows of at most table_width + unit_cost plan blocks each.
-pda_status check_plan_size(int64_t rows, int32_t table_width, int32_t unit_cost) {
-    const int64_t most = std::min<int64_t>(rows, pda::kMaxLaunchBatch) * ((int64_t)table_width + unit_cost);
-    if (most > 0x7fffffffLL)
-        return fail(PDA_ERR_INVALID_ARG,
-                    "block table width %d is too large: %lld rows per launch could hold %lld "
-                    "blocks, more than a 32-bit prefix holds",
-                    table_width, (long long)std::min<int64_t>(rows, pda::kMaxLaunchBatch), (long long)most);
-    return PDA_OK;
-}
 
 // The launch shape of a call: the mode, queries per launch row (qp), grid
 // and pipeline depth.  Multi-query calls with more than 8 q rows per
@@ -932,6 +883,17 @@ PDA_EXPORT pda_status pda_decode_multi(pda_ctx* ctx, const pda_bf16* q, const pd
     // one query per sequence is plain decode; more take the causal kernels
     RunArgs r = {q_len > 1 ? pda::kMulti : pda::kOneShot, q,
                  {k_pool, v_pool, num_blocks, s[0], s[1], s[2]},
+                 block_table, max_blocks, seq_lens, 0, nullptr, batch, scale, out, nullptr,
+                 nullptr, nullptr, (cudaStream_t)stream, false, q_len};
+    return run(ctx, r);
+}
+
+pda_status pda::decode_bf16_multi(pda_ctx* ctx, const pda_bf16* q, const pda_cache* c, const int32_t* block_table,
+                                  int32_t max_blocks, const int32_t* seq_lens, int32_t batch, int32_t q_len,
+                                  float scale, pda_bf16* out, pda_stream stream) {
+    RunArgs r = {pda::kMulti, q,
+                 {static_cast<const pda_bf16*>(c->k_pool), static_cast<const pda_bf16*>(c->v_pool), c->num_blocks,
+                  c->blk_stride, c->tok_stride, c->kvh_stride},
                  block_table, max_blocks, seq_lens, 0, nullptr, batch, scale, out, nullptr,
                  nullptr, nullptr, (cudaStream_t)stream, false, q_len};
     return run(ctx, r);
