@@ -536,18 +536,23 @@ PDA_EXPORT pda_status pda_create(const pda_dims* dims, pda_ctx** out_ctx) {
         ctx->tc_ctas = n * ctx->num_sms;
         ctx->tc_stages = pda::split_stages(D, ctx->stage_rows, pda::kMultiTc);
     }
+    if ((st = pda::quant_setup(ctx, (int)prop.sharedMemPerBlockOptin)) != PDA_OK) {
+        delete ctx;
+        return st;
+    }
     // Partial states: slots of G <= 8 rows for plain decode and the n8 form
     // (chunk_b x Hkv units plus one slot per CTA).  The row form's launch
     // rows hold up to 32 q rows, but a full batch of max_seqs <= 1024
     // sequences has launch rows x Hkv x rows per slot below 2 x max_seqs x
     // Hq <= 16 x chunk_b x Hkv, plus 32 rows per CTA of its grid: with that
     // room every call runs in one launch.
+    ctx->slots = std::max(ctx->slots, (int64_t)chunk_b * dims->num_kv_heads + ctx->quant_ctas[0]);
     ctx->part_rows = ctx->slots * pda::kMaxGroup;
     if (ctx->rows_ctas[1] > 0)
         ctx->part_rows = std::max<int64_t>(ctx->part_rows,
                                            (int64_t)chunk_b * dims->num_kv_heads * 2 * pda::kMaxGroup +
                                                (int64_t)std::max({ctx->rows_ctas[0], ctx->rows_ctas[1],
-                                                                  ctx->tc_ctas}) *
+                                                                  ctx->tc_ctas, ctx->quant_ctas[1]}) *
                                                    pda::kMaxRowsPerWalk);
 
     const int64_t nq = (int64_t)dims->max_seqs * dims->num_q_heads;

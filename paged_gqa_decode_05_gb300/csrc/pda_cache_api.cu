@@ -1,6 +1,7 @@
 // pda_cache_api.cu -- the C ABI around the decode: q / k preparation, cache
 // writes and read-backs, and decode over a cache of any format: argument
 // checks and launches.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstring>
@@ -124,7 +125,132 @@ void set_prep(pda::HeadsParams& p, const pda_prep* prep) {
     p.interleaved = prep->interleaved;
 }
 
+// A pool of 8-bit rows as a 5-D view {bytes of a slab, bs slots, slabs, Hkv,
+// num_blocks}, box {.., bs, slabs, 1, 1}: one kv head's rows of one block land
+// as [slab][slot][128 bytes] (64 at head size 64) with the swizzle of that
+// width.
+pda_status encode_quant_pool(const pda_dims& d, void* base, const pda_cache* c, CUtensorMap* tm) {
+    const int row = d.head_dim < 128 ? d.head_dim : 128;
+    const cuuint64_t dims[5] = {(cuuint64_t)row, (cuuint64_t)d.block_size, (cuuint64_t)(d.head_dim / row),
+                                (cuuint64_t)d.num_kv_heads, (cuuint64_t)c->num_blocks};
+    const cuuint64_t strides[4] = {(cuuint64_t)c->tok_stride, (cuuint64_t)row, (cuuint64_t)c->kvh_stride,
+                                   (cuuint64_t)c->blk_stride};
+    const cuuint32_t box[5] = {(cuuint32_t)row, (cuuint32_t)d.block_size, (cuuint32_t)(d.head_dim / row), 1, 1};
+    const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+    const CUresult r = pda::tensor_map_encoder()(
+        tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, base, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+        row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(PDA_ERR_INVALID_ARG, "cuTensorMapEncodeTiled rejected the pool layout (CUresult %d)", (int)r);
+    return PDA_OK;
+}
+
+pda_status run_quant(pda_ctx* ctx, const pda_bf16* q, const pda_cache* c, const int32_t* table, int32_t max_blocks,
+                     const int32_t* lens, int32_t batch, int32_t q_len, float scale, void* out, bool f32,
+                     cudaStream_t stream) {
+    pda::QuantParams p = {};
+    pda_status st = pda::check_scale(scale, ctx->dims.head_dim, &p.scale_log2);
+    if (st != PDA_OK) return st;
+    const pda_dims& d = ctx->dims;
+    const int D = d.head_dim, G = ctx->G, Hq = d.num_q_heads, Hkv = d.num_kv_heads, bs = d.block_size;
+    // Queries of a sequence share one walk over its KV, 8 q rows of it or, where
+    // there are more and the shape has it, 16.
+    const int tiles = q_len * G > 8 && ctx->quant_ctas[1] > 0 ? 2 : 1;
+    const int qp = std::max(1, std::min(q_len, 8 * tiles / G));
+    const int Qr = (q_len + qp - 1) / qp, SR = qp * G;
+    const bool multi = q_len > 1;
+    const pda::QuantShape shape = pda::quant_shape(D, c->format, tiles, multi);
+    const int grid = ctx->quant_ctas[tiles - 1];
+    if (Qr > grid) return fail(PDA_ERR_INVALID_ARG, "q_len %d: more launch rows per sequence than CTAs (%d)", q_len, grid);
+    p.unit_cost = pda::quant_unit_cost(D, tiles, bs, multi);
+    if ((st = pda::check_plan_size((int64_t)batch * q_len, max_blocks, p.unit_cost)) != PDA_OK) return st;
+
+    const pda_pool_key key = {c->k_pool, c->v_pool, c->num_blocks, c->blk_stride, c->tok_stride, c->kvh_stride};
+    const pda_pool_key& was = ctx->quant_key;
+    if (!(ctx->quant_maps_valid && was.k == key.k && was.v == key.v && was.num_blocks == key.num_blocks &&
+          was.blk == key.blk && was.tok == key.tok && was.kvh == key.kvh)) {
+        ctx->quant_maps_valid = false;
+        ctx->quant_row_mode = pda::quant_boxes(D, bs) ? 0 : 2;
+        if (ctx->quant_row_mode == 0 && ((st = encode_quant_pool(d, c->k_pool, c, &ctx->quant_k)) != PDA_OK ||
+                                         (st = encode_quant_pool(d, c->v_pool, c, &ctx->quant_v)) != PDA_OK))
+            return st;
+        ctx->quant_key = key;
+        ctx->quant_maps_valid = true;
+    }
+    p.tm_k = ctx->quant_k;
+    p.tm_v = ctx->quant_v;
+    p.row_gather = ctx->quant_row_mode;
+    p.num_blocks = c->num_blocks;
+    p.k_base = static_cast<const uint16_t*>(c->k_pool);
+    p.v_base = static_cast<const uint16_t*>(c->v_pool);
+    p.blk_s = c->blk_stride;
+    p.tok_s = c->tok_stride;
+    p.kvh_s = c->kvh_stride;
+    p.scales = c->scales;
+    p.part_o = ctx->part_o;
+    p.part_ml = ctx->part_ml;
+    p.unit_sync = ctx->unit_sync;
+    p.err = ctx->err;
+    p.table_stride = max_blocks;
+    p.q_len = q_len;
+    p.qp = qp;
+    p.rows_per_slot = SR;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.G = G;
+    p.bs = bs;
+    p.prefetch = ctx->quant_row_mode == 0 && bs >= 8 && Qr == 1;
+
+    // launch rows per chunk (whole sequences), as many as the partial states allow
+    const int64_t fit = (ctx->part_rows / SR - grid) / Hkv;
+    const int32_t rows_total = batch * Qr;
+    const int32_t chunk = (int32_t)(std::min<int64_t>(pda::kMaxLaunchBatch, fit) / Qr) * Qr;
+    if (chunk < 1)
+        return fail(PDA_ERR_UNSUPPORTED, "q_len %d: a sequence's %d launch rows exceed the partial-state buffers", q_len,
+                    Qr);
+    for (int32_t c0 = 0; c0 < rows_total; c0 += chunk) {
+        const int64_t s0 = c0 / Qr;  // first sequence of the chunk
+        p.B = std::min(chunk, rows_total - c0);
+        p.q = q + s0 * q_len * Hq * D;
+        p.table = table + s0 * max_blocks;
+        p.lens = lens + s0;
+        p.out = f32 ? nullptr : static_cast<uint16_t*>(out) + s0 * q_len * Hq * D;
+        p.out_f32 = f32 ? static_cast<float*>(out) + s0 * q_len * Hq * D : nullptr;
+        const cudaError_t e = pda::launch_quant(D, c->format, tiles, multi, p, grid, shape.smem(p.B), stream);
+        if (e != cudaSuccess) return cuda_fail(e, "decode_cache launch");
+    }
+    ctx->tile_steps = 0;
+    return PDA_OK;
+}
+
 }  // namespace
+
+pda_status pda::quant_setup(pda_ctx* ctx, int optin) {
+    const int D = ctx->dims.head_dim;
+    for (int tiles = 1; tiles <= 2; ++tiles) {
+        int per_sm = 1 << 30;
+        for (int format : {PDA_CACHE_E4M3, PDA_CACHE_INT8})
+            for (int multi = 0; multi < 2; ++multi) {
+                const QuantShape s = quant_shape(D, format, tiles, multi != 0);
+                if (!s.fn) { per_sm = 0; continue; }
+                const int limit = (int)s.smem(kMaxLaunchBatch);
+                if (limit > optin)
+                    return fail(PDA_ERR_UNSUPPORTED, "needs %d bytes of shared memory per CTA (device allows %d)", limit,
+                                optin);
+                int n = 0;
+                cudaError_t e = cudaFuncSetAttribute(s.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, limit);
+                if (e == cudaSuccess)
+                    e = cudaFuncSetAttribute(s.fn, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                             cudaSharedmemCarveoutMaxShared);
+                if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, s.fn, s.threads, limit);
+                if (e != cudaSuccess) return cuda_fail(e, "8-bit kernel attributes");
+                per_sm = std::min(per_sm, n);
+            }
+        ctx->quant_ctas[tiles - 1] = per_sm * ctx->num_sms;
+    }
+    return ctx->quant_ctas[0] > 0 ? PDA_OK : fail(PDA_ERR_UNSUPPORTED, "8-bit kernel does not fit on an SM");
+}
 
 PDA_EXPORT pda_status pda_norm_rope(pda_ctx* ctx, const pda_heads* q, const pda_heads* k, const int32_t* positions,
                                     int64_t num_tokens, const pda_prep* prep, const pda_heads* q_out,
@@ -250,18 +376,6 @@ PDA_EXPORT pda_status pda_decode_cache(pda_ctx* ctx, const pda_bf16* q, const pd
     if (!block_table || !seq_lens || !aligned(block_table, 4) || !aligned(seq_lens, 4))
         return fail(PDA_ERR_INVALID_ARG, "block_table / seq_lens must be non-NULL and 4-byte aligned");
     if (max_blocks < 1) return fail(PDA_ERR_INVALID_ARG, "block table width must be >= 1 (got %d)", max_blocks);
-    pda::QuantParams p = {};
-    if ((st = pda::check_scale(scale, d.head_dim, &p.scale_log2)) != PDA_OK) return st;
-    p.q = q;
-    p.c = cache_ref(ctx, cache, block_table, max_blocks, seq_lens, batch, nullptr, 0);
-    p.out = out;
-    p.out_f32 = out_f32 != 0;
-    p.q_len = q_len;
-    p.Hq = d.num_q_heads;
-    p.Hkv = d.num_kv_heads;
-    p.G = ctx->G;
-    p.err = ctx->err;
-    ctx->tile_steps = 0;
-    const cudaError_t e = pda::launch_quant(d.head_dim, cache->format, p, (cudaStream_t)stream);
-    return e == cudaSuccess ? PDA_OK : cuda_fail(e, "decode_cache launch");
+    return run_quant(ctx, q, cache, block_table, max_blocks, seq_lens, batch, q_len, scale, out, out_f32 != 0,
+                     (cudaStream_t)stream);
 }

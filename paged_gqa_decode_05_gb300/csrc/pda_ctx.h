@@ -72,9 +72,18 @@ struct pda_ctx {
     int32_t maps_row_mode = 0;
     CUtensorMap map_k, map_v;
     CUtensorMap map_k1, map_v1;  // one-slab boxes (head size 128, block boxes): the tcgen05 form
+    // Decode over 8-bit caches: grids with up to 8 and 16 packed q rows per
+    // walk (0: not on this shape) and the last pool's tensor maps.
+    int quant_ctas[2] = {0, 0};
+    bool quant_maps_valid = false;
+    pda_pool_key quant_key;
+    int32_t quant_row_mode = 0;
+    CUtensorMap quant_k, quant_v;
 };
 
 namespace pda {
+// Launch attributes and grids of the 8-bit kernels of a context's shape.
+pda_status quant_setup(pda_ctx* ctx, int smem_optin);
 // Causal multi-query decode over a bf16 cache of any stride triple.
 pda_status decode_bf16_multi(pda_ctx* ctx, const pda_bf16* q, const pda_cache* cache, const int32_t* block_table,
                              int32_t max_blocks, const int32_t* seq_lens, int32_t batch, int32_t q_len, float scale,

@@ -113,7 +113,8 @@ struct Cfg {
     static constexpr int kHalves = D / 64;               // 64-column swizzled slabs per row
     static constexpr int kHalfBytes = ST * 128;          // ST rows of one slab
     static constexpr int kTileBytes = kHalves * kHalfBytes;
-    static constexpr int kStageBytes = 2 * kTileBytes + stage_q_rows(MODE) * D * 2;
+    static constexpr int kQOff = 2 * kTileBytes;         // the q rows, behind the K and V tiles
+    static constexpr int kStageBytes = kQOff + stage_q_rows(MODE) * D * 2;
     static constexpr int kStages = kTc ? PDA_STAGES_TC_D128
                                  : kQTiles == 1 ? (D == 64 ? PDA_STAGES_ROWS16_D64 : PDA_STAGES_ROWS16_D128)
                                  : kQTiles == 2 ? (D == 64 ? PDA_STAGES_ROWS32_D64 : PDA_STAGES_ROWS32_D128)
@@ -285,7 +286,111 @@ __device__ __forceinline__ int32_t build_prefix(const SplitParams& p, int32_t* p
 
 // ------------------------------------------------------------------ producer
 
+// The copies of one stage into shared memory (bf16 pools).  A loader's issue()
+// is called by the whole warp: n blocks of the unit (rows valid rows), block i
+// being window entry rel + i of win_id (lane-varying index), to the stage at
+// sK, completing on the barrier `full`; tx_bytes() is what its bulk copies
+// bring.
 template <int D, int ST, int MODE>
+struct Bf16Loader {
+    using C = Cfg<D, ST, MODE>;
+    static __device__ __forceinline__ int blocks_per_stage(int bs) { return C::kST / bs; }  // the host keeps bs <= ST
+    static __device__ __forceinline__ uint32_t tx_bytes(const SplitParams& p, int32_t n, int rows) {
+        return p.row_gather == 0 ? (uint32_t)n * 2u * (uint32_t)p.bs * D * 2u
+             : p.row_gather == 1 ? (uint32_t)((rows + 3) >> 2) * 2u * 4u * D * 2u
+                                 : 0u;  // cp.async completions arrive instead
+    }
+    template <typename WinId>
+    static __device__ __forceinline__ void issue(const SplitParams& p, uint32_t sK, int32_t n, int rows, int32_t rel,
+                                                 int kvh, uint32_t full, uint64_t pol, int lane,
+                                                 const WinId& win_id) {
+        const int bs = p.bs;
+        const uint32_t sV = sK + C::kTileBytes;
+        if (p.row_gather == 1) {
+            // Rows of small blocks, 4 per TMA gather4 copy of one 64-column slab:
+            // group g covers stage rows 4g..4g+3 (the tail repeats the last row,
+            // which the consumers mask), written as one ST-row block.
+            constexpr int H = C::kHalves;
+            const int lbs = 31 - __clz(bs);
+            const int groups = (rows + 3) >> 2;
+            for (int o0 = 0; o0 < (C::kST / 4) * H; o0 += 32) {
+                const int o = o0 + lane;
+                const int g = o / H, h = o - g * H;
+                int32_t r[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int t = min(4 * g + k, rows - 1);
+                    const int i = t >> lbs;  // block of the stage (< ST)
+                    int32_t id = win_id(rel + i);
+                    if (o < groups * H && (id < 0 || (int64_t)id >= p.num_blocks)) {
+                        atomicOr(p.err, PDA_DEVERR_BAD_BLOCK_ID_);
+                        id = 0;
+                    }
+                    r[k] = (int32_t)((int64_t)id * p.row_blk + (int64_t)(t & (bs - 1)) * p.row_tok +
+                                     (int64_t)kvh * p.row_kvh);
+                }
+                if (o < groups * H) {
+                    const uint32_t dst = (uint32_t)h * C::kHalfBytes + (uint32_t)(4 * g) * 128u;
+                    tma_gather4(sK + dst, &p.tm_k, h * 64, r[0], r[1], r[2], r[3], full, pol);
+                    tma_gather4(sV + dst, &p.tm_v, h * 64, r[0], r[1], r[2], r[3], full, pol);
+                }
+            }
+        } else if (p.row_gather == 2) {
+            // Rows of small blocks: 16-byte cp.async chunks, CH per row, written
+            // in the layout of one ST-row block ([slab][row][128 B], swizzled).
+            constexpr int CH = D / 8;
+            constexpr int RPI = 32 / CH;  // rows per pass of the warp
+            const int c = lane % CH, sub = lane / CH;
+            const int lbs = 31 - __clz(bs);
+            const uint16_t* kb = p.k_base + (int64_t)kvh * p.kvh_s + c * 8;
+            const uint16_t* vb = p.v_base + (int64_t)kvh * p.kvh_s + c * 8;
+            for (int t0 = 0; t0 < rows; t0 += RPI) {
+                const int t = t0 + sub;
+                const int i = min(t, rows - 1) >> lbs;  // block of the stage (< ST)
+                const int32_t wid = win_id(rel + i);
+                if (t < rows) {
+                    int32_t id = wid;
+                    if (id < 0 || (int64_t)id >= p.num_blocks) {
+                        atomicOr(p.err, PDA_DEVERR_BAD_BLOCK_ID_);
+                        id = 0;
+                    }
+                    const int64_t off = (int64_t)id * p.blk_s + (int64_t)(t & (bs - 1)) * p.tok_s;
+                    const uint32_t dst = (uint32_t)(c >> 3) * C::kHalfBytes + (uint32_t)t * 128u +
+                                         (uint32_t)(((c & 7) ^ (t & 7)) << 4);
+                    cp_async_16(sK + dst, kb + off);
+                    cp_async_16(sV + dst, vb + off);
+                }
+            }
+            cp_async_mbar_arrive_noinc(full);
+        } else
+        // lane i copies block i of the stage (its id comes from the window)
+        {
+            const int32_t wid = win_id(rel + min(lane, n - 1));
+            if (lane < n) {
+                int32_t id = wid;
+                if (id < 0 || (int64_t)id >= p.num_blocks) {
+                    atomicOr(p.err, PDA_DEVERR_BAD_BLOCK_ID_);
+                    id = 0;  // stays in bounds; the flag marks the result invalid
+                }
+                if constexpr (is_tc(MODE) && D == 128) {
+                    // one box per slab: the stage tile is [slab][64 rows][128 B]
+                    const uint32_t off = (uint32_t)(lane * bs) * 128u;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        tma_load_5d(sK + off + (uint32_t)h * C::kHalfBytes, &p.tm_k1, 0, 0, h, kvh, id, full, pol);
+                        tma_load_5d(sV + off + (uint32_t)h * C::kHalfBytes, &p.tm_v1, 0, 0, h, kvh, id, full, pol);
+                    }
+                } else {
+                    const uint32_t off = (uint32_t)(lane * bs) * (uint32_t)(D * 2);
+                    tma_load_5d(sK + off, &p.tm_k, 0, 0, 0, kvh, id, full, pol);
+                    tma_load_5d(sV + off, &p.tm_v, 0, 0, 0, kvh, id, full, pol);
+                }
+            }
+        }
+    }
+};
+
+template <class C, class Loader, int D, int MODE>
 __device__ __forceinline__ void run_producer(const SplitParams& p, uint32_t base_s, const SmemLayout& L,
                                              const int32_t* pfx, StageMeta* meta,
                                              volatile int* abort_flag, int64_t begin, int64_t end,
@@ -298,7 +403,6 @@ __device__ __forceinline__ void run_producer(const SplitParams& p, uint32_t base
     // 128 entries of the current sequence's row (the next kv head starts
     // there) and nx[] those of the next non-empty sequence, loaded one unit
     // ahead together with the entry its last block's valid slots come from.
-    using C = Cfg<D, ST, MODE>;
     constexpr int S = C::kStages;
     constexpr bool MQ = is_multi(MODE);
     const uint32_t full0 = base_s + L.bars, empty0 = full0 + 8 * S;
@@ -308,7 +412,7 @@ __device__ __forceinline__ void run_producer(const SplitParams& p, uint32_t base
     // it normal.
     const uint64_t pol = rows_per_seq<MQ>(p) > 1 ? policy_evict_normal() : policy_evict_first();
     const int bs = p.bs, Hkv = p.Hkv;
-    const int NB = C::kST / bs;  // blocks per stage (the host keeps bs <= ST)
+    const int NB = Loader::blocks_per_stage(bs);
 
     int stage = 0;
     uint32_t phase = 0;
@@ -347,7 +451,7 @@ __device__ __forceinline__ void run_producer(const SplitParams& p, uint32_t base
         return s;
     };
     // The id of window entry idx (lane-varying).  A stage reads entries
-    // j - win .. j - win + n - 1 < 64: the blocks per stage NB = ST / bs is a
+    // j - win .. j - win + n - 1 < 64: the blocks per stage NB <= 64 is a
     // power of two, j - win stays a multiple of NB (the window starts at a
     // segment start or a unit start and slides by 64) and n <= NB.  So only
     // w[0] and w[1] are read; w[2] and w[3], loaded at a slide, are first read
@@ -442,7 +546,6 @@ __device__ __forceinline__ void run_producer(const SplitParams& p, uint32_t base
 
         const uint32_t full = full0 + 8 * stage;
         const uint32_t sK = base_s + (uint32_t)stage * C::kStageBytes;
-        const uint32_t sV = sK + C::kTileBytes;
         if (leader) {
             StageMeta m;
             m.b = b;
@@ -455,109 +558,22 @@ __device__ __forceinline__ void run_producer(const SplitParams& p, uint32_t base
             m.nr = MQ ? ri.cnt * p.G : p.G;
             meta[stage] = m;
             const bool load_q = seg_begin && MODE != kGather;
-            const int rows = (n - 1) * bs + lastv;
-            const uint32_t kv_bytes =
-                p.row_gather == 0 ? (uint32_t)n * 2u * (uint32_t)bs * D * 2u
-                : p.row_gather == 1 ? (uint32_t)((rows + 3) >> 2) * 2u * 4u * D * 2u
-                                    : 0u;  // cp.async completions arrive instead
-            const uint32_t bytes = kv_bytes + (load_q ? (uint32_t)(m.nr * D * 2) : 0u);
+            const uint32_t bytes = Loader::tx_bytes(p, n, (n - 1) * bs + lastv) + (load_q ? (uint32_t)(m.nr * D * 2) : 0u);
             mbar_arrive_expect_tx(full, bytes);
             if (load_q) {  // the G q rows of kv head kvh for each packed query
                 if constexpr (MQ) {
                     for (int k = 0; k < ri.cnt; ++k)
-                        bulk_load(sV + C::kTileBytes + (uint32_t)(k * p.G * D * 2),
+                        bulk_load(sK + C::kQOff + (uint32_t)(k * p.G * D * 2),
                                   p.q + qo_offset<MQ>(p, ri.b, ri.first + k, kvh * p.G, D),
                                   (uint32_t)(p.G * D * 2), full);
                 } else {
-                    bulk_load(sV + C::kTileBytes, p.q + qo_offset<MQ>(p, b, 0, kvh * p.G, D),
+                    bulk_load(sK + C::kQOff, p.q + qo_offset<MQ>(p, b, 0, kvh * p.G, D),
                               (uint32_t)(p.G * D * 2), full);
                 }
             }
         }
         __syncwarp();
-        if (p.row_gather == 1) {
-            // Rows of small blocks, 4 per TMA gather4 copy of one 64-column slab:
-            // group g covers stage rows 4g..4g+3 (the tail repeats the last row,
-            // which the consumers mask), written as one ST-row block.
-            constexpr int H = C::kHalves;
-            const int lbs = 31 - __clz(bs);
-            const int rows = (n - 1) * bs + lastv;
-            const int groups = (rows + 3) >> 2;
-            for (int o0 = 0; o0 < (C::kST / 4) * H; o0 += 32) {
-                const int o = o0 + lane;
-                const int g = o / H, h = o - g * H;
-                int32_t r[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int t = min(4 * g + k, rows - 1);
-                    const int i = t >> lbs;  // block of the stage (< ST)
-                    int32_t id = win_id(j - win + i);
-                    if (o < groups * H && (id < 0 || (int64_t)id >= p.num_blocks)) {
-                        atomicOr(p.err, PDA_DEVERR_BAD_BLOCK_ID_);
-                        id = 0;
-                    }
-                    r[k] = (int32_t)((int64_t)id * p.row_blk + (int64_t)(t & (bs - 1)) * p.row_tok +
-                                     (int64_t)kvh * p.row_kvh);
-                }
-                if (o < groups * H) {
-                    const uint32_t dst = (uint32_t)h * C::kHalfBytes + (uint32_t)(4 * g) * 128u;
-                    tma_gather4(sK + dst, &p.tm_k, h * 64, r[0], r[1], r[2], r[3], full, pol);
-                    tma_gather4(sV + dst, &p.tm_v, h * 64, r[0], r[1], r[2], r[3], full, pol);
-                }
-            }
-        } else if (p.row_gather == 2) {
-            // Rows of small blocks: 16-byte cp.async chunks, CH per row, written
-            // in the layout of one ST-row block ([slab][row][128 B], swizzled).
-            constexpr int CH = D / 8;
-            constexpr int RPI = 32 / CH;  // rows per pass of the warp
-            const int c = lane % CH, sub = lane / CH;
-            const int lbs = 31 - __clz(bs);
-            const int rows = (n - 1) * bs + lastv;
-            const uint16_t* kb = p.k_base + (int64_t)kvh * p.kvh_s + c * 8;
-            const uint16_t* vb = p.v_base + (int64_t)kvh * p.kvh_s + c * 8;
-            for (int t0 = 0; t0 < rows; t0 += RPI) {
-                const int t = t0 + sub;
-                const int i = min(t, rows - 1) >> lbs;  // block of the stage (< ST)
-                const int32_t wid = win_id(j - win + i);
-                if (t < rows) {
-                    int32_t id = wid;
-                    if (id < 0 || (int64_t)id >= p.num_blocks) {
-                        atomicOr(p.err, PDA_DEVERR_BAD_BLOCK_ID_);
-                        id = 0;
-                    }
-                    const int64_t off = (int64_t)id * p.blk_s + (int64_t)(t & (bs - 1)) * p.tok_s;
-                    const uint32_t dst = (uint32_t)(c >> 3) * C::kHalfBytes + (uint32_t)t * 128u +
-                                         (uint32_t)(((c & 7) ^ (t & 7)) << 4);
-                    cp_async_16(sK + dst, kb + off);
-                    cp_async_16(sV + dst, vb + off);
-                }
-            }
-            cp_async_mbar_arrive_noinc(full);
-        } else
-        // lane i copies block i of the stage (its id comes from the window)
-        {
-            const int32_t wid = win_id(j - win + min(lane, n - 1));
-            if (lane < n) {
-                int32_t id = wid;
-                if (id < 0 || (int64_t)id >= p.num_blocks) {
-                    atomicOr(p.err, PDA_DEVERR_BAD_BLOCK_ID_);
-                    id = 0;  // stays in bounds; the flag marks the result invalid
-                }
-                if constexpr (is_tc(MODE) && D == 128) {
-                    // one box per slab: the stage tile is [slab][64 rows][128 B]
-                    const uint32_t off = (uint32_t)(lane * bs) * 128u;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        tma_load_5d(sK + off + (uint32_t)h * C::kHalfBytes, &p.tm_k1, 0, 0, h, kvh, id, full, pol);
-                        tma_load_5d(sV + off + (uint32_t)h * C::kHalfBytes, &p.tm_v1, 0, 0, h, kvh, id, full, pol);
-                    }
-                } else {
-                    const uint32_t off = (uint32_t)(lane * bs) * (uint32_t)(D * 2);
-                    tma_load_5d(sK + off, &p.tm_k, 0, 0, 0, kvh, id, full, pol);
-                    tma_load_5d(sV + off, &p.tm_v, 0, 0, 0, kvh, id, full, pol);
-                }
-            }
-        }
+        Loader::issue(p, sK, n, (n - 1) * bs + lastv, j - win, kvh, full, pol, lane, win_id);
         issued |= 1u << stage;
         issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
 
@@ -1115,8 +1131,9 @@ __device__ __forceinline__ void zero_empty_rows(const SplitParams& p, const int3
 // role (whole unit, stored partial, or the last piece, which merges every
 // stored partial with its own); each (row, 4 columns) of the tile is then
 // combined over the slices and written (bf16 o / l, or the fp32 partial).
-// Returns false when the CTA aborts.
-template <int D, int kSlices, int kThreadsC>
+// Returns false when the CTA aborts.  kTileRows rows make a tile, kRowStride
+// rows a slice of st_m / st_l; kNan: a NaN sum of weights gives NaN, not 0.
+template <int D, int kSlices, int kThreadsC, int kTileRows = 16, int kRowStride = kMaxRowsPerWalk, bool kNan = false>
 __device__ __forceinline__ bool rows_tile_merge(const SplitParams& p, const StageMeta& m, int tile, int ct,
                                                 int32_t ticket, const UnitPieces& pc, const GroupRange& grs,
                                                 const RowInfo& ri, const float* st_m, const float* st_l,
@@ -1151,22 +1168,22 @@ __device__ __forceinline__ bool rows_tile_merge(const SplitParams& p, const Stag
         if (!consumer_sync(cbar, cphase, p.err, abort_flag)) return false;
         role = *st_role;
         if (role == kRoleAbort) return false;
-        const int h0 = tile * 16, nrt = min(16, NR - h0);
+        const int h0 = tile * kTileRows, nrt = min(kTileRows, NR - h0);
         for (int i4 = ct; i4 < nrt * D / 4; i4 += kThreadsC) {
             const int hr = (4 * i4) / D, d4 = 4 * i4 - hr * D;
             const int h = h0 + hr;  // q row of the unit
             float M = kNegInf;
 #pragma unroll
-            for (int w = 0; w < kSlices; ++w) M = fmaxf(M, st_m[w * kMaxRowsPerWalk + h]);
+            for (int w = 0; w < kSlices; ++w) M = fmaxf(M, st_m[w * kRowStride + h]);
             float Ls = 0.f;
             float4 Os = make_float4(0.f, 0.f, 0.f, 0.f);
             if (M != kNegInf) {
 #pragma unroll
                 for (int w = 0; w < kSlices; ++w) {
-                    const float f = ex2(st_m[w * kMaxRowsPerWalk + h] - M);
+                    const float f = ex2(st_m[w * kRowStride + h] - M);
                     const float4 v =
-                        *reinterpret_cast<const float4*>(st_o + (size_t)(w * 16 + hr) * kOStride + d4);
-                    Ls += st_l[w * kMaxRowsPerWalk + h] * f;
+                        *reinterpret_cast<const float4*>(st_o + (size_t)(w * kTileRows + hr) * kOStride + d4);
+                    Ls += st_l[w * kRowStride + h] * f;
                     Os.x += v.x * f; Os.y += v.y * f; Os.z += v.z * f; Os.w += v.w * f;
                 }
             }
@@ -1212,7 +1229,7 @@ __device__ __forceinline__ bool rows_tile_merge(const SplitParams& p, const Stag
                 Ls = Lr;
                 Os = Or;
             }
-            const float4 v = Ls > 0.f ? make_float4(Os.x / Ls, Os.y / Ls, Os.z / Ls, Os.w / Ls)
+            const float4 v = (kNan ? Ls != 0.f : Ls > 0.f) ? make_float4(Os.x / Ls, Os.y / Ls, Os.z / Ls, Os.w / Ls)
                                       : make_float4(0.f, 0.f, 0.f, 0.f);
             const int64_t oo = qo_offset<true>(p, ri.b, ri.first + h / G, m.kvh * G + h % G, D) + d4;
             if (p.out_f32) {
@@ -1917,9 +1934,8 @@ constexpr int kPrefetchStages = PDA_PREFETCH_STAGES;  // stages of blocks prefet
 // prefetch, every index is kept inside the CTA's table row and the pool, and
 // the decode itself reads everything after the wait.  Single-query launches
 // of block boxes (multi-query with one launch row per sequence).
-template <int D, int ST, int MODE, int KPER>
+template <int ST, int KPER, class Touch>
 __device__ __noinline__ void prefetch_first_stages_k(const SplitParams& p, int lane) {
-    using C = Cfg<D, ST, MODE>;
     const int per = (p.B + 31) / 32;  // <= KPER
     const int lo = min(p.B, lane * per), hi = min(p.B, lo + per);
     const int lbs = 31 - __clz(p.bs);  // block sizes are powers of two
@@ -1948,7 +1964,7 @@ __device__ __noinline__ void prefetch_first_stages_k(const SplitParams& p, int l
     const int64_t units = (int64_t)p.B * Hkv, c = blockIdx.x;
     int64_t begin, end;
     int32_t b = 0, nvb = 0, pfb = 0;
-    if (unit_mode(units, gridDim.x, real_blocks(big, p.unit_cost), C::kST, p.bs)) {
+    if (unit_mode(units, gridDim.x, real_blocks(big, p.unit_cost), ST, p.bs)) {
         if (c >= units) return;
         b = (int32_t)(c / Hkv);
         int32_t pf = base;
@@ -1987,14 +2003,13 @@ __device__ __noinline__ void prefetch_first_stages_k(const SplitParams& p, int l
     const int64_t kvh = rem / nvb, j = rem % nvb;
     if (kvh >= p.Hkv || j >= p.table_stride) return;
     const int64_t n = min(min(min((int64_t)real_blocks(nvb, p.unit_cost) - j, end - begin),
-                              (int64_t)(kPrefetchStages * (C::kST / p.bs))),
+                              (int64_t)(kPrefetchStages * (ST / p.bs))),
                           (int64_t)p.table_stride - j);
     const int64_t row = (int64_t)b * p.table_stride + j;
     for (int64_t i = lane; i < n; i += 32) {  // the unit's next n blocks (one unit at most)
         const int64_t id = p.table ? (int64_t)__ldcg(p.table + row + i) : row + i;
         if (id >= 0 && id < p.num_blocks) {
-            tma_prefetch_5d(&p.tm_k, 0, 0, 0, (int32_t)kvh, (int32_t)id);
-            tma_prefetch_5d(&p.tm_v, 0, 0, 0, (int32_t)kvh, (int32_t)id);
+            Touch::block(p, (int32_t)kvh, (int32_t)id);
         }
     }
 }
@@ -2002,14 +2017,21 @@ __device__ __noinline__ void prefetch_first_stages_k(const SplitParams& p, int l
 // The plan in registers is sized to the batch (up to 1, 4 or 32 sequences a
 // lane).  Not inlined: kept out of the split kernel's own code, whose start
 // every launch fetches (inlined, it cost small batches 0.4 us a call).
-template <int D, int ST, int MODE>
+struct TouchBoxes {  // a block's K and V rows of one kv head
+    static __device__ __forceinline__ void block(const SplitParams& p, int32_t kvh, int32_t id) {
+        tma_prefetch_5d(&p.tm_k, 0, 0, 0, kvh, id);
+        tma_prefetch_5d(&p.tm_v, 0, 0, 0, kvh, id);
+    }
+};
+
+template <int ST, int MODE, class Touch = TouchBoxes>
 __device__ __noinline__ void prefetch_first_stages(const SplitParams& p, int lane) {
     // multi-query: one launch row per sequence only (then row s is sequence s
     // and reads its whole length, like plain decode)
     if (is_multi(MODE) && rows_per_seq<is_multi(MODE)>(p) != 1) return;
-    if (p.B <= 32) prefetch_first_stages_k<D, ST, MODE, 1>(p, lane);
-    else if (p.B <= 128) prefetch_first_stages_k<D, ST, MODE, 4>(p, lane);
-    else prefetch_first_stages_k<D, ST, MODE, kMaxLaunchBatch / 32>(p, lane);
+    if (p.B <= 32) prefetch_first_stages_k<ST, 1, Touch>(p, lane);
+    else if (p.B <= 128) prefetch_first_stages_k<ST, 4, Touch>(p, lane);
+    else prefetch_first_stages_k<ST, kMaxLaunchBatch / 32, Touch>(p, lane);
 }
 
 // Register cap: for D <= 128 two CTAs share an SM (two 3-stage rings keep as
@@ -2079,7 +2101,7 @@ __global__ void __maxnreg__(split_max_regs(D, MODE)) split_kernel(const __grid_c
         // (not in the two-q-tile row forms: the call alone costs its main loop
         // registers, and its consumers set its time)
         if constexpr (MODE != kGather && MODE != kMultiRows32 && !C::kTc)
-            if (!early && p.prefetch) prefetch_first_stages<D, ST, MODE>(p, lane);
+            if (!early && p.prefetch) prefetch_first_stages<ST, MODE>(p, lane);
         return;
     }
     if constexpr (C::kTc) {
@@ -2099,7 +2121,7 @@ __global__ void __maxnreg__(split_max_regs(D, MODE)) split_kernel(const __grid_c
     const GroupRange gr = cta_range<MODE>(p, pfx, nv_max, C::kST, &begin, &end);
 
     if (warp == C::kConsumerWarps) {
-        run_producer<D, ST, MODE>(p, base_s, L, pfx, meta, &abort_flag, begin, end, lane);
+        run_producer<C, Bf16Loader<D, ST, MODE>, D, MODE>(p, base_s, L, pfx, meta, &abort_flag, begin, end, lane);
         return;
     }
     if constexpr (C::kTc) {

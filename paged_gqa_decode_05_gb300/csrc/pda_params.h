@@ -143,9 +143,9 @@ PDA_HD uint32_t stage_bytes(int D, int st, int mode) {
 // 2 * ST * D * 2 bytes; row form, one q tile at a time, ST/16 warps x 16 rows
 // x (D+4) floats <= the stage with its q area.  st_m / st_l hold one (m, l)
 // per consumer warp and q row: [ST/16 token slices][32 rows] in the row form.
-PDA_HD SmemLayout smem_layout(int D, int st, int mode, int stages, int B) {
+PDA_HD SmemLayout smem_layout_of(uint32_t bytes_per_stage, int mode, int stages, int B) {
     SmemLayout L;
-    uint32_t off = (uint32_t)stages * stage_bytes(D, st, mode);
+    uint32_t off = (uint32_t)stages * bytes_per_stage;
     L.bars = off;  off += 2u * stages * 8u;
     L.cbar = off;  off += 8u;
     L.tcb = off;   off += is_tc(mode) ? 96u : 0u;  // tcgen05 form: 10 barriers, the tensor-memory base
@@ -159,6 +159,9 @@ PDA_HD SmemLayout smem_layout(int D, int st, int mode, int stages, int B) {
     L.pfx = off;   off += (uint32_t)(B + 1) * 4u;
     L.total = off + 1024u;
     return L;
+}
+PDA_HD SmemLayout smem_layout(int D, int st, int mode, int stages, int B) {
+    return smem_layout_of(stage_bytes(D, st, mode), mode, stages, B);
 }
 
 }  // namespace pda

@@ -1,0 +1,590 @@
+// pda_quant.cuh -- the split kernel of decode over an 8-bit cache.
+//
+// The plan, the producer warp, the prefetch warp and the merge of split units
+// are those of the bf16 split kernel (pda_kernels.cuh); the stage loader and
+// the consumers are this file's.  With codes k, v and row scales ks, vs,
+//   s_t = scale ks_t (q . k_t),   o = sum_t e^(s_t) vs_t v_t / sum_t e^(s_t),
+// so nothing is dequantised: K scales multiply the scores, V scales the
+// weights.  HBM sees D + 4 bytes per row and the tensor cores see codes:
+//   * e4m3, S^T = K q^T: q, scaled by a power of two per row into [128, 256),
+//     splits into two e4m3 parts, hi + lo, which hold all eight significant
+//     bits of a bf16 value (values below 2^-15 of the row's largest keep an
+//     absolute 2^-18 of it): two m16n8k32 products take K's bytes as they lie
+//     in shared memory.
+//   * int8: codes become fp16 exactly (the byte placed under 0x64 reads as
+//     1024 + u) for m16n8k16, q in fp16 with the same power-of-two scale.
+//   * O^T += V^T P^T (m16n8k16): ldmatrix transposes pairs of bytes, so a lane
+//     gets columns 2g, 2g + 1 of two tokens; they become rows g and g + 8 of
+//     the product's A operand, which only permutes the rows of O.
+// A weight that multiplies V is p' = 2^(s + log2 vs - m'), with the reference
+// m' following the maximum of s + log2 vs, so that p' stays inside fp16
+// whatever the V scales are; the sum of weights adds p' / vs.  (m', l, o) is
+// an online-softmax state like any other: o / l and merges do not depend on
+// the reference.  p' enters the product as fp16, 2^-11 of it at most: an
+// eighth of the output's own bf16 half step.  References sit kRefBias below
+// the maximum they were taken at and move when a maximum passes them by more
+// than kRefBias + kLazyLog2, so p' < 2^14 and what fp16 flushes is 2^-31 of
+// the largest weight.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "pda_kernels.cuh"
+#include "pda_quant.h"
+
+namespace pda {
+
+constexpr float kRefBias = 6.f;
+constexpr float kLeastScale = 7.7037198e-34f;  // 2^-110: a scale of 0 counts as this, its codes are 0
+
+template <int D, int NT>
+struct QuantCfg {
+    static constexpr int kWarps = quant_warps(D, NT);
+    static constexpr int kRT = quant_row_tiles(D);
+    static constexpr int kST = quant_stage_rows(D, NT);
+    static constexpr int kMainThreads = (kWarps + 1) * 32;
+    static constexpr int kThreads = kMainThreads + 32;  // + the prefetch warp
+    static constexpr int kRB = D < 128 ? D : 128;       // bytes of a row in one swizzled slab
+    static constexpr int kSlabs = D / kRB;
+    static constexpr int kTileBytes = kST * D;
+    static constexpr int kSOff = 2 * kTileBytes;        // the rows' scales: per block [K bs][V bs] floats
+    static constexpr int kQOff = kSOff + kST * 8;
+    static constexpr int kStageBytes = quant_stage_bytes(D, NT);
+    static constexpr int kStages = quant_stages(D, NT);
+    static constexpr int kK = D / 32;                   // 32-column steps of a row
+    static_assert(kStageBytes % 1024 == 0, "stages start on swizzle spans");
+    static_assert(kWarps * 8 * NT * (D + 8) * 4 <= kStageBytes, "the staged states fit a stage");
+};
+
+template <int D, int NT>
+struct QuantLoader {
+    using C = QuantCfg<D, NT>;
+    // at most 64 blocks (the producer's window of block ids)
+    static __device__ __forceinline__ int blocks_per_stage(int bs) { return min(C::kST / bs, 64); }
+    static __device__ __forceinline__ uint32_t tx_bytes(const SplitParams& p, int32_t n, int) {
+        return p.row_gather == 0 ? (uint32_t)(n * p.bs) * (2u * D + 8u) : 0u;
+    }
+    template <typename WinId>
+    static __device__ __forceinline__ void issue(const SplitParams& sp, uint32_t sK, int32_t n, int rows, int32_t rel,
+                                                 int kvh, uint32_t full, uint64_t pol, int lane, const WinId& win_id) {
+        const QuantParams& p = static_cast<const QuantParams&>(sp);
+        const int bs = p.bs;
+        const uint32_t sV = sK + C::kTileBytes, sS = sK + C::kSOff;
+        auto checked = [&](int32_t id) {
+            if (id < 0 || (int64_t)id >= p.num_blocks) {
+                atomicOr(p.err, PDA_DEVERR_BAD_BLOCK_ID_);
+                id = 0;  // stays in bounds; the flag marks the result invalid
+            }
+            return id;
+        };
+        if (p.row_gather == 0) {
+            // lane i copies block i: a box per pool and the block's scales
+            const int32_t wid = win_id(rel + min(lane, n - 1));
+            if (lane < n) {
+                const int32_t id = checked(wid);
+                const uint32_t off = (uint32_t)(lane * bs) * (uint32_t)D;
+                tma_load_5d(sK + off, &p.tm_k, 0, 0, 0, kvh, id, full, pol);
+                tma_load_5d(sV + off, &p.tm_v, 0, 0, 0, kvh, id, full, pol);
+                bulk_load(sS + (uint32_t)(lane * bs) * 8u, p.scales + ((int64_t)id * p.Hkv + kvh) * 2 * bs, 8u * bs,
+                          full);
+            }
+            return;
+        }
+        // rows of small blocks (or of strides a box cannot have): 16-byte
+        // chunks, written as one kST-row block
+        constexpr int CH = D / 16, RPI = 32 / CH;
+        const int c = lane % CH, sub = lane / CH;
+        const int lbs = 31 - __clz(bs);
+        const uint8_t* kb = reinterpret_cast<const uint8_t*>(p.k_base) + (int64_t)kvh * p.kvh_s + c * 16;
+        const uint8_t* vb = reinterpret_cast<const uint8_t*>(p.v_base) + (int64_t)kvh * p.kvh_s + c * 16;
+        for (int t0 = 0; t0 < rows; t0 += RPI) {
+            const int t = t0 + sub;
+            const int32_t wid = win_id(rel + (min(t, rows - 1) >> lbs));
+            if (t < rows) {
+                const int64_t off = (int64_t)checked(wid) * p.blk_s + (int64_t)(t & (bs - 1)) * p.tok_s;
+                const int sw = C::kRB == 128 ? (c & 7) ^ (t & 7) : c ^ ((t >> 1) & 3);
+                const uint32_t dst = (uint32_t)(c >> 3) * (C::kST * 128u) + (uint32_t)t * C::kRB + (uint32_t)(sw << 4);
+                cp_async_16(sK + dst, kb + off);
+                cp_async_16(sV + dst, vb + off);
+            }
+        }
+        const int pieces = bs > 1 ? bs / 2 : 1;  // 16-byte pieces of a block's scales (8 bytes for one token)
+        for (int i0 = 0; i0 < n * pieces; i0 += 32) {
+            const int i = min(i0 + lane, n * pieces - 1), blk = i / pieces;
+            const int32_t wid = win_id(rel + blk);
+            if (i0 + lane < n * pieces) {
+                const float* s = p.scales + ((int64_t)checked(wid) * p.Hkv + kvh) * 2 * bs;
+                if (bs > 1) cp_async_16(sS + 16u * i, s + 4 * (i - blk * pieces));
+                else cp_async_8(sS + 8u * i, s);
+            }
+        }
+        cp_async_mbar_arrive_noinc(full);
+    }
+};
+
+struct TouchQuant {  // a block's rows of one kv head and their scales, towards L2
+    static __device__ __forceinline__ void block(const SplitParams& sp, int32_t kvh, int32_t id) {
+        const QuantParams& p = static_cast<const QuantParams&>(sp);
+        tma_prefetch_5d(&p.tm_k, 0, 0, 0, kvh, id);
+        tma_prefetch_5d(&p.tm_v, 0, 0, 0, kvh, id);
+        bulk_prefetch(p.scales + ((int64_t)id * p.Hkv + kvh) * 2 * p.bs, 8u * p.bs);
+    }
+};
+
+// Two fp16 values from bytes lo, hi (0..3) of x.  int8: x holds code ^ 0x80;
+// the byte under 0x64 reads as 1024 + code + 128.
+template <int FMT, int lo, int hi>
+__device__ __forceinline__ uint32_t half2_of(uint32_t x) {
+    static_assert(FMT == kInt8, "int8");
+    uint32_t h = __byte_perm(x, 0x64646464u, 0x4040 | lo | (hi << 8)), d;
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(d) : "r"(h), "r"(0x64806480u));  // 1152
+    return d;
+}
+
+// The A fragment of 16 rows x 16 columns of K from the two registers of one
+// 16-byte chunk (rows 0-7, rows 8-15): bytes 0, 1 are k slots 2t, 2t + 1 and
+// bytes 2, 3 slots 2t + 8, 2t + 9, the order q's fragments follow.
+__device__ __forceinline__ void k_fragment_int8(uint32_t r0, uint32_t r1, uint32_t (&a)[4]) {
+    r0 ^= 0x80808080u;
+    r1 ^= 0x80808080u;
+    a[0] = half2_of<kInt8, 0, 1>(r0);
+    a[1] = half2_of<kInt8, 0, 1>(r1);
+    a[2] = half2_of<kInt8, 2, 3>(r0);
+    a[3] = half2_of<kInt8, 2, 3>(r1);
+}
+
+// The A fragment of V^T, 16 columns x 16 tokens, from the transposed registers
+// of one 16-byte chunk (tokens 0-7, tokens 8-15): bytes 0, 2 are column 2g of
+// tokens 2t, 2t + 1 (row g), bytes 1, 3 column 2g + 1 (row g + 8).
+template <int FMT>
+__device__ __forceinline__ void v_fragment(uint32_t r0, uint32_t r1, uint32_t (&a)[4]) {
+    if constexpr (FMT == kE4m3) {
+        const uint32_t x = __byte_perm(r0, 0, 0x3120), y = __byte_perm(r1, 0, 0x3120);
+        a[0] = e4m3x2_to_f16x2((uint16_t)x);
+        a[1] = e4m3x2_to_f16x2((uint16_t)(x >> 16));
+        a[2] = e4m3x2_to_f16x2((uint16_t)y);
+        a[3] = e4m3x2_to_f16x2((uint16_t)(y >> 16));
+    } else {
+        r0 ^= 0x80808080u;
+        r1 ^= 0x80808080u;
+        a[0] = half2_of<kInt8, 0, 2>(r0);
+        a[1] = half2_of<kInt8, 1, 3>(r0);
+        a[2] = half2_of<kInt8, 0, 2>(r1);
+        a[3] = half2_of<kInt8, 1, 3>(r1);
+    }
+}
+
+// Byte offset of row t of a stage tile (slab 0, chunk 0) and the XOR of its
+// chunk index in slab h; blocks of 1 << lbs rows lie back to back, each
+// [slabs][rows][kRB bytes].
+template <int D>
+__device__ __forceinline__ uint32_t quant_row_off(int t, int lbs) {
+    constexpr int RB = D < 128 ? D : 128;
+    return ((uint32_t)(t >> lbs) << lbs) * D + (uint32_t)(t & ((1 << lbs) - 1)) * RB;
+}
+template <int D>
+__device__ __forceinline__ int quant_swz(int t, int h, int lbs) {
+    return D == 64 ? (t >> 1) & 3 : swz(t, h, lbs);
+}
+
+template <int D, int FMT, int NT, int MODE>
+__device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_t base_s, uint8_t* base,
+                                                   const SmemLayout& L, const StageMeta* meta, const int32_t* pfx,
+                                                   volatile int* abort_flag, int warp, int lane) {
+    using C = QuantCfg<D, NT>;
+    constexpr int S = C::kStages, RT = C::kRT, K = C::kK;
+    constexpr int kThreadsC = C::kWarps * 32, kRows = 8 * NT, kOStride = D + 8;
+    constexpr bool MQ = is_multi(MODE);
+    const uint32_t full0 = base_s + L.bars, empty0 = full0 + 8 * S;
+    const int g = lane >> 2, t = lane & 3;
+    const int r0 = warp * 16 * RT;
+    const int G = p.G;
+    const int lbr = 31 - __clz(p.bs);                       // the cache's blocks
+    const int lbs = p.row_gather ? 31 - __clz(C::kST) : lbr;  // the tile's blocks
+    const uint32_t hs = (uint32_t)C::kRB << lbs;            // bytes between slabs of a block
+    // ldmatrix lane addresses, alike for K and (transposed) V: matrices are rows
+    // 0-7, rows 8-15 of chunk c, then of chunk c + 1
+    const int row = r0 + (lane & 15), cpar = lane >> 4;
+    uint32_t off[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) off[r] = quant_row_off<D>(row + 16 * r, lbs);
+    int swh[C::kSlabs];  // rows 16 apart share their swizzle
+#pragma unroll
+    for (int h = 0; h < C::kSlabs; ++h) swh[h] = quant_swz<D>(row, h, lbs);
+    constexpr int CPS = C::kRB / 16;  // chunks per slab row
+    auto chunk = [&](int kk) { return (uint32_t)((2 * kk) / CPS) * hs + (uint32_t)((((2 * kk) % CPS + cpar) ^ swh[(2 * kk) / CPS]) << 4); };
+
+    float o[NT][2 * K][4];
+    uint32_t qf[NT][K][4];
+    float f[NT][2], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        m[n][0] = m[n][1] = kNegInf;
+        l[n][0] = l[n][1] = f[n][0] = f[n][1] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2 * K; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
+#pragma unroll
+        for (int i = 0; i < K; ++i) qf[n][i][0] = qf[n][i][1] = qf[n][i][2] = qf[n][i][3] = 0u;
+    }
+    // causal queries of this lane's score columns
+    int qc[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        qc[n][0] = MQ ? (8 * n + 2 * t) / G : 0;
+        qc[n][1] = MQ ? (8 * n + 2 * t + 1) / G : 0;
+    }
+    const uint32_t cbar = base_s + L.cbar;
+    uint32_t cphase = 0;
+    int stage = 0;
+    uint32_t phase = 0;
+    int32_t ticket = 0;
+    const int ct = warp * 32 + lane;
+    zero_empty_rows<D, kThreadsC>(p, pfx, ct);
+
+    while (true) {
+        if (*abort_flag) break;
+        if (!mbar_wait_bounded(full0 + 8 * stage, phase, kWaitLimitNs)) {
+            atomicOr(p.err, PDA_DEVERR_TIMEOUT_);
+            *abort_flag = 1;
+            break;
+        }
+        const StageMeta md = meta[stage];
+        if (md.flags & kDone) break;
+        // the last stage of a piece of a split unit draws the piece's ticket (see run_consumer)
+        if (warp == 0 && lane == 0 && (md.flags & kSegEnd) && !(md.flags & kWholeUnit))
+            ticket = atomicAdd(p.unit_sync + 2 * (md.b * p.Hkv + md.kvh), 1);
+        const uint32_t sK = base_s + (uint32_t)stage * C::kStageBytes;
+        const uint32_t sV = sK + C::kTileBytes;
+        const uint8_t* bytes = base + (sK - base_s);
+
+        if (md.flags & kSegBegin) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int qr = 8 * n + g;
+                const bool any = qr < (MQ ? md.nr : G);
+                uint2 raw[K][2];
+                uint32_t top = 0;
+#pragma unroll
+                for (int kk = 0; kk < K; ++kk)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint8_t* s = bytes + C::kQOff + (size_t)(qr * D + 32 * kk + 16 * i + 4 * t) * 2;
+                        raw[kk][i] = any ? *reinterpret_cast<const uint2*>(s) : make_uint2(0u, 0u);
+                        const uint32_t x = raw[kk][i].x, y = raw[kk][i].y;
+                        top = max(top, max(max(x & 0x7fffu, (x >> 16) & 0x7fffu), max(y & 0x7fffu, (y >> 16) & 0x7fffu)));
+                    }
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // the row's largest magnitude lies in [2^e, 2^(e+1)): multiply by 2^(7-e)
+                const int e = max((int)(top >> 7) - 127, -119);
+                const float mult = __int_as_float((127 + 7 - e) << 23);
+                const float back = top < 0x7f80u ? __int_as_float((127 - 7 + e) << 23)
+                                                 : __int_as_float(0x7fffffff);  // infinities and NaN: NaN
+#pragma unroll
+                for (int kk = 0; kk < K; ++kk)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float x0 = bf16_lo(raw[kk][i].x) * mult, x1 = bf16_hi(raw[kk][i].x) * mult;
+                        const float x2 = bf16_lo(raw[kk][i].y) * mult, x3 = bf16_hi(raw[kk][i].y) * mult;
+                        if constexpr (FMT == kE4m3) {
+                            const uint32_t h01 = pack_e4m3x2(x0, x1), h23 = pack_e4m3x2(x2, x3);
+                            const uint32_t b01 = e4m3x2_to_f16x2((uint16_t)h01), b23 = e4m3x2_to_f16x2((uint16_t)h23);
+                            const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&b01));
+                            const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&b23));
+                            qf[n][kk][i] = h01 | (h23 << 16);
+                            qf[n][kk][2 + i] = pack_e4m3x2(x0 - u.x, x1 - u.y) | (pack_e4m3x2(x2 - w.x, x3 - w.y) << 16);
+                        } else {
+                            qf[n][kk][2 * i] = pack_f16x2(x0, x1);
+                            qf[n][kk][2 * i + 1] = pack_f16x2(x2, x3);
+                        }
+                    }
+                f[n][0] = p.scale_log2 * __shfl_sync(0xffffffffu, back, 8 * t);
+                f[n][1] = p.scale_log2 * __shfl_sync(0xffffffffu, back, 8 * t + 4);
+                m[n][0] = m[n][1] = kNegInf;
+                l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+                for (int i = 0; i < 2 * K; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
+            }
+        }
+        if (r0 < md.n_valid) {
+            const bool partial = r0 + 16 * RT > md.n_valid;
+            if (FMT == kE4m3 && partial) {
+                // rows behind the end may hold NaN codes, and 0 * NaN would poison P V
+                for (int u = lane; u < (r0 + 16 * RT - md.n_valid) * (D / 16); u += 32) {
+                    const int r = md.n_valid + u / (D / 16), c = u % (D / 16);
+                    const uint32_t a = sV + quant_row_off<D>(r, lbs) + (uint32_t)(c / CPS) * hs + (uint32_t)((c % CPS) << 4);
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
+                }
+                __syncwarp();
+            }
+            // this lane's rows: g and g + 8 of each row tile
+            float ks[RT][2], lv[RT][2], iv[RT][2];
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int tr = r0 + 16 * r + 8 * i + g;
+                    const float* s = reinterpret_cast<const float*>(bytes + C::kSOff) + ((tr >> lbr) << (lbr + 1)) +
+                                     (tr & (p.bs - 1));
+                    const bool in = tr < md.n_valid;
+                    ks[r][i] = s[0];
+                    float vs = in ? s[p.bs] : 1.f;
+                    vs = vs < kLeastScale ? kLeastScale : vs;
+                    lv[r][i] = lg2(vs);
+                    iv[r][i] = ex2(-lv[r][i]);
+                }
+            float x[RT][NT][4];
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                float acc[2][NT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[0][n][i] = acc[1][n][i] = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < K; ++kk) {
+                    uint32_t w[4];
+                    ldsm_x4(sK + off[r] + chunk(kk), w);
+                    if constexpr (FMT == kE4m3) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            mma_e4m3_16832(acc[0][n], w, qf[n][kk][0], qf[n][kk][1]);
+                            mma_e4m3_16832(acc[1][n], w, qf[n][kk][2], qf[n][kk][3]);
+                        }
+                    } else {
+                        uint32_t a[4], b[4];
+                        k_fragment_int8(w[0], w[1], a);
+                        k_fragment_int8(w[2], w[3], b);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            mma_f16_16816(acc[0][n], a, qf[n][kk][0], qf[n][kk][1]);
+                            mma_f16_16816(acc[1][n], b, qf[n][kk][2], qf[n][kk][3]);
+                        }
+                    }
+                }
+                // x: the score in base-2 units plus log2 of the row's V scale
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        x[r][n][i] = fmaf(acc[0][n][i] + acc[1][n][i], ks[r][i >> 1] * f[n][i & 1], lv[r][i >> 1]);
+            }
+            if (partial) {
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (r0 + 16 * r + 8 * (i >> 1) + g >= md.n_valid)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) x[r][n][i] = kNegInf;
+            }
+            if constexpr (MQ) {  // column c is query c / G of the row: no later tokens
+                const int pos0 = md.j0 * p.bs + r0;
+                if (pos0 + 16 * RT - 1 > md.lim) {
+#pragma unroll
+                    for (int r = 0; r < RT; ++r)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (pos0 + 16 * r + 8 * (i >> 1) + g > md.lim + qc[n][i & 1]) x[r][n][i] = kNegInf;
+                }
+            }
+            uint32_t pb[RT][NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float top[2];
+                bool up[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    top[c] = fmaxf(x[0][n][c], x[0][n][c + 2]);
+#pragma unroll
+                    for (int r = 1; r < RT; ++r) top[c] = fmaxf(top[c], fmaxf(x[r][n][c], x[r][n][c + 2]));
+#pragma unroll
+                    for (int s = 4; s < 32; s <<= 1) top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], s));
+                    up[c] = top[c] > m[n][c] + (kLazyLog2 + kRefBias);
+                }
+                if (__any_sync(0xffffffffu, up[0] || up[1])) {
+                    float a[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float to = top[c] - kRefBias;
+                        a[c] = up[c] ? ex2(m[n][c] - to) : 1.f;  // an empty column (m = -inf): 0
+                        if (up[c]) m[n][c] = to;
+                        l[n][c] *= a[c];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2 * K; ++i) {
+                        o[n][i][0] *= a[0]; o[n][i][1] *= a[1]; o[n][i][2] *= a[0]; o[n][i][3] *= a[1];
+                    }
+                }
+                const float u0 = m[n][0] == kNegInf ? 0.f : m[n][0];
+                const float u1 = m[n][1] == kNegInf ? 0.f : m[n][1];
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    const float p0 = ex2(x[r][n][0] - u0), p1 = ex2(x[r][n][1] - u1);
+                    const float p2 = ex2(x[r][n][2] - u0), p3 = ex2(x[r][n][3] - u1);
+                    l[n][0] += fmaf(p2, iv[r][1], p0 * iv[r][0]);
+                    l[n][1] += fmaf(p3, iv[r][1], p1 * iv[r][0]);
+                    pb[r][n][0] = movmatrix_trans(pack_f16x2(p0, p1));
+                    pb[r][n][1] = movmatrix_trans(pack_f16x2(p2, p3));
+                }
+            }
+#pragma unroll
+            for (int kk = 0; kk < K; ++kk)
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    uint32_t w[4], a[4], b[4];
+                    ldsm_x4_trans(sV + off[r] + chunk(kk), w);
+                    v_fragment<FMT>(w[0], w[1], a);
+                    v_fragment<FMT>(w[2], w[3], b);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma_f16_16816(o[n][2 * kk], a, pb[r][n][0], pb[r][n][1]);
+                        mma_f16_16816(o[n][2 * kk + 1], b, pb[r][n][0], pb[r][n][1]);
+                    }
+                }
+            if (FMT == kE4m3 && partial) fence_proxy_async_smem();  // generic writes before the next TMA
+        }
+        if (md.flags & kSegEnd) {
+            // the warps' states merge through this stage's memory; roles as in run_consumer
+            float* st_m = reinterpret_cast<float*>(base + L.st_m);  // [warp][16 rows]
+            float* st_l = reinterpret_cast<float*>(base + L.st_l);
+            int32_t* st_role = reinterpret_cast<int32_t*>(base + L.st_x) + 2 * kMaxGroup;
+            float* st_o = reinterpret_cast<float*>(base + (sK - base_s));  // [warp][kRows][kOStride]
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int s = 4; s < 32; s <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], s);
+            if (!consumer_sync(cbar, cphase, p.err, abort_flag)) break;  // all reads of the stage done
+            const int NR = MQ ? md.nr : G;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int h = 8 * n + 2 * t + c;
+                    if (h >= NR) continue;
+                    if (g == 0) {
+                        // a NaN sum must not hide behind an empty reference
+                        st_m[warp * 16 + h] = l[n][c] == l[n][c] ? m[n][c] : 0.f;
+                        st_l[warp * 16 + h] = l[n][c];
+                    }
+                    float* r = st_o + (size_t)(warp * kRows + h) * kOStride + 2 * g;
+#pragma unroll
+                    for (int i = 0; i < 2 * K; ++i)
+                        *reinterpret_cast<float2*>(r + 16 * i) = make_float2(o[n][i][c], o[n][i][2 + c]);
+                }
+            UnitPieces pc;
+            pc.cf = 0; pc.su = 0; pc.n = 1; pc.every = true;
+            const GroupRange grs = group_of_cta(blockIdx.x, pfx, p.B, rows_per_seq<MQ>(p), p.Hkv, gridDim.x);
+            if (!(md.flags & kWholeUnit)) pc = unit_pieces(pfx, md.b, md.kvh, p.Hkv, p.unit_cost, grs);
+            const RowInfo ri = row_info<MQ>(p, md.b);
+            StageMeta me = md;
+            me.nr = NR;
+            int role = kRoleAbort;
+            if (!rows_tile_merge<D, C::kWarps, kThreadsC, kRows, 16, true>(p, me, 0, ct, ticket, pc, grs, ri, st_m, st_l,
+                                                                          st_o, st_role, cbar, cphase, abort_flag, role))
+                break;
+            if (!consumer_sync(cbar, cphase, p.err, abort_flag)) break;
+            if (role == kRoleStore && ct == 0) red_release_gpu_add(p.unit_sync + 2 * (md.b * p.Hkv + md.kvh) + 1, 1);
+            fence_proxy_async_smem();  // staging writes before the next TMA into this stage
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty0 + 8 * stage);
+        if (++stage == S) { stage = 0; phase ^= 1u; }
+    }
+}
+
+template <int D, int FMT, int NT, int MODE>
+__global__ void __maxnreg__(168) quant_split_kernel(const __grid_constant__ QuantParams p) {
+    using C = QuantCfg<D, NT>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int abort_flag;
+    const uint32_t raw_s = smem_u32(smem_raw);
+    const uint32_t base_s = (raw_s + 1023u) & ~1023u;
+    uint8_t* base = smem_raw + (base_s - raw_s);
+    const SmemLayout L = smem_layout_of(C::kStageBytes, kOneShot, C::kStages, p.B);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int32_t* pfx = reinterpret_cast<int32_t*>(base + L.pfx);
+    int32_t* scan = reinterpret_cast<int32_t*>(base + L.scan);
+    StageMeta* meta = reinterpret_cast<StageMeta*>(base + L.meta);
+    if (tid == 0) {
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(base_s + L.bars + 8 * s, p.row_gather ? 33 : 1);
+            mbar_init(base_s + L.bars + 8 * (C::kStages + s), C::kWarps);
+        }
+        mbar_init(base_s + L.cbar, C::kWarps * 32);
+        fence_mbar_init();
+        abort_flag = 0;
+    }
+    if (tid == C::kWarps * 32) {
+        prefetch_tensormap(&p.tm_k);
+        prefetch_tensormap(&p.tm_v);
+    }
+    if (warp == C::kMainThreads / 32) {  // the prefetch warp: joins nothing below
+        if (p.prefetch) prefetch_first_stages<C::kST, MODE, TouchQuant>(p, lane);
+        return;
+    }
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    const int32_t nv_max = build_prefix<is_multi(MODE), C::kMainThreads>(p, pfx, scan);
+    int64_t begin, end;
+    cta_range<MODE>(p, pfx, nv_max, C::kST, &begin, &end);
+    if (warp == C::kWarps) {
+        run_producer<C, QuantLoader<D, NT>, D, MODE>(p, base_s, L, pfx, meta, &abort_flag, begin, end, lane);
+        return;
+    }
+    run_quant_consumer<D, FMT, NT, MODE>(p, base_s, base, L, meta, pfx, &abort_flag, warp, lane);
+}
+
+template <int D, int FMT, int NT, int MODE>
+cudaError_t launch_quant_as(const QuantParams& p, int grid, size_t smem, cudaStream_t stream) {
+    using C = QuantCfg<D, NT>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3(p.prefetch ? C::kThreads : C::kMainThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, quant_split_kernel<D, FMT, NT, MODE>, p);
+}
+
+template <int D, int FMT, int NT>
+const void* quant_fn_of(bool multi) {
+    if constexpr (NT == 1)
+        if (!multi) return reinterpret_cast<const void*>(&quant_split_kernel<D, FMT, 1, kOneShot>);
+    return reinterpret_cast<const void*>(&quant_split_kernel<D, FMT, NT, kMulti>);
+}
+
+template <int D>
+const void* quant_fn(int format, int n_tiles, bool multi) {
+    if (n_tiles == 2) {
+        if constexpr (D <= 128) return format == kE4m3 ? quant_fn_of<D, kE4m3, 2>(true) : quant_fn_of<D, kInt8, 2>(true);
+        return nullptr;
+    }
+    return format == kE4m3 ? quant_fn_of<D, kE4m3, 1>(multi) : quant_fn_of<D, kInt8, 1>(multi);
+}
+
+template <int D, int FMT>
+cudaError_t launch_quant_fmt(int n_tiles, bool multi, const QuantParams& p, int grid, size_t smem, cudaStream_t s) {
+    if constexpr (D <= 128)
+        if (n_tiles == 2) return launch_quant_as<D, FMT, 2, kMulti>(p, grid, smem, s);
+    if (n_tiles != 1) return cudaErrorInvalidValue;
+    return multi ? launch_quant_as<D, FMT, 1, kMulti>(p, grid, smem, s)
+                 : launch_quant_as<D, FMT, 1, kOneShot>(p, grid, smem, s);
+}
+
+template <int D>
+cudaError_t launch_quant_of(int format, int n_tiles, bool multi, const QuantParams& p, int grid, size_t smem,
+                            cudaStream_t stream) {
+    return format == kE4m3 ? launch_quant_fmt<D, kE4m3>(n_tiles, multi, p, grid, smem, stream)
+                           : launch_quant_fmt<D, kInt8>(n_tiles, multi, p, grid, smem, stream);
+}
+
+}  // namespace pda

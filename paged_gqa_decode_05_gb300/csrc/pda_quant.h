@@ -1,22 +1,50 @@
-// pda_quant.h -- parameter block and launch entry point of decode over an
-// 8-bit cache.
+// pda_quant.h -- decode over an 8-bit cache: the split kernel's shapes,
+// parameters and launch entry points (kernels in pda_quant.cuh, one
+// translation unit per head size).
 #pragma once
 
 #include "pda_cache.h"
+#include "pda_params.h"
 
 namespace pda {
 
-struct QuantParams {
-    const uint16_t* q;  // [B, q_len, Hq, D] bf16
-    CacheRef c;
-    void* out;          // [B, q_len, Hq, D] bf16, or fp32
-    int32_t out_f32;
-    int32_t q_len;
-    int32_t Hq, Hkv, G;
-    float scale_log2;
-    uint32_t* err;
+// Shapes.  A consumer warp takes 16 KV rows of a stage per row tile; head
+// sizes up to 128 with 8 packed q rows run two CTAs of 4 consumer warps per
+// SM, two row tiles each (128-row stages: as many bytes as 64 bf16 rows, two
+// independent chains per warp); 16 packed q rows (n_tiles 2) and head size
+// 256 run one CTA of 8 consumer warps.
+PDA_HD constexpr int quant_warps(int D, int n_tiles) { return D == 256 || n_tiles == 2 ? 8 : 4; }
+PDA_HD constexpr int quant_row_tiles(int D) { return D == 256 ? 1 : 2; }
+PDA_HD constexpr int quant_stage_rows(int D, int n_tiles) { return 16 * quant_warps(D, n_tiles) * quant_row_tiles(D); }
+PDA_HD constexpr int quant_stage_bytes(int D, int n_tiles) {
+    return quant_stage_rows(D, n_tiles) * (2 * D + 8) + 8 * n_tiles * D * 2;
+}
+PDA_HD constexpr int quant_stages(int D, int n_tiles) { return D == 64 ? (n_tiles == 2 ? 5 : 5) : 3; }
+// Whether a block's rows load as one TMA box per pool: the box must fill whole
+// spans of the swizzle (1024 bytes of 128-byte rows, 512 of 64-byte rows).
+PDA_HD constexpr bool quant_boxes(int D, int bs) { return bs >= 8 || (D == 256 && bs == 4); }
+// Plan blocks added to every unit (see pda_plan.h), in quarter stages.
+PDA_HD int32_t quant_unit_cost(int D, int n_tiles, int bs, bool multi) {
+    const int nb = quant_stage_rows(D, n_tiles) / bs;
+    const int x4 = !quant_boxes(D, bs) ? 2 : multi ? 12 : 6;
+    return (nb < 1 ? 1 : nb) * x4 / 4;
+}
+
+struct QuantParams : SplitParams {
+    const float* scales;  // [num_blocks, Hkv, 2, bs]
 };
 
-cudaError_t launch_quant(int D, int format, const QuantParams& p, cudaStream_t stream);
+struct QuantShape {
+    const void* fn;
+    int threads;      // with the prefetch warp
+    int stage_rows, stages, stage_bytes;
+    uint32_t smem(int B) const { return smem_layout_of((uint32_t)stage_bytes, kOneShot, stages, B).total; }
+};
+
+// format kE4m3 / kInt8; n_tiles 1 (up to 8 q rows per walk) or 2 (16, head
+// sizes up to 128); multi: several causal queries per sequence.
+QuantShape quant_shape(int D, int format, int n_tiles, bool multi);
+cudaError_t launch_quant(int D, int format, int n_tiles, bool multi, const QuantParams& p, int grid,
+                         size_t smem, cudaStream_t stream);
 
 }  // namespace pda

@@ -1,0 +1,13 @@
+// 8-bit split-kernel instantiations for head_dim 64.
+#include "pda_quant.cuh"
+
+namespace pda {
+
+const void* quant_fn_d64(int format, int n_tiles, bool multi) { return quant_fn<64>(format, n_tiles, multi); }
+
+cudaError_t launch_quant_d64(int format, int n_tiles, bool multi, const QuantParams& p, int grid, size_t smem,
+                            cudaStream_t stream) {
+    return launch_quant_of<64>(format, n_tiles, multi, p, grid, smem, stream);
+}
+
+}  // namespace pda

@@ -83,7 +83,15 @@ def rows64(pool, scales, which, table_row, n, bs):
 
 def decode64(q, k_pool, v_pool, scales, table, lens, bs, scale=None):
     """(out, size) of causal decode, q [B, n, Hq, D]: fp64 attention and, for each element,
-    sum p |v|, which rounding errors of the weights are relative to."""
+    what rounding errors of the weights are relative to.
+
+    That is sum p |v| while a weight's error is relative to it.  Weights p vs (vs the row's V
+    scale) enter the product as fp16, whose numbers below 2^-14 have an absolute half step of
+    2^-25; the largest weight of a column is at least 2^6 there, so a weight's error is at most
+    2^-31 of the largest, times its code.  Where the largest weight meets a code of 0, that is
+    all there is: an int8 row of D = 64 with p = 1 - 6e-8 and code 0 leaves size 6.5e-8 (weights
+    of 1e-6 in fp16) and an error of 6.4e-11 where 2^-10 of the size is 6.3e-11.  So with a
+    tolerance of 2^-10, size counts 2^-21 of the largest weight times the sum of |codes| too."""
     B, n, hq, d = q.shape
     hkv = k_pool.shape[2]
     scale = d ** -0.5 if scale is None else scale
@@ -92,6 +100,9 @@ def decode64(q, k_pool, v_pool, scales, table, lens, bs, scale=None):
     for b in range(B):
         L = int(lens[b])
         k, v = (rows64(p, scales, i, table[b], max(L, 0), bs) for i, p in enumerate((k_pool, v_pool)))
+        vs = torch.ones(v.shape[:2], dtype=torch.float64) if scales is None else \
+            scales[table[b].long(), :, 1].double().transpose(1, 2).flatten(0, 1)[:v.shape[0]]
+        code = v.abs() / torch.where(vs == 0, 1.0, vs)[..., None]
         for i in range(n):
             m = L - n + i + 1
             if m <= 0:
@@ -99,7 +110,9 @@ def decode64(q, k_pool, v_pool, scales, table, lens, bs, scale=None):
             qq = q[b, i].double().reshape(hkv, hq // hkv, d)
             p = torch.softmax(scale * qq @ k[:m].permute(1, 2, 0), -1)
             out[b, i] = (p @ v[:m].transpose(0, 1)).reshape(hq, d)
-            size[b, i] = (p @ v[:m].abs().transpose(0, 1)).reshape(hq, d)
+            top = (p * vs[:m].T[:, None]).amax(-1, keepdim=True)
+            flushed = 2.0 ** -21 * top * code[:m].sum(0)[:, None]
+            size[b, i] = (p @ v[:m].abs().transpose(0, 1) + flushed).reshape(hq, d)
     return out, size
 
 
