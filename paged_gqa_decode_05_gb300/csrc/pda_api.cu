@@ -546,14 +546,19 @@ PDA_EXPORT pda_status pda_create(const pda_dims* dims, pda_ctx** out_ctx) {
     // sequences has launch rows x Hkv x rows per slot below 2 x max_seqs x
     // Hq <= 16 x chunk_b x Hkv, plus 32 rows per CTA of its grid: with that
     // room every call runs in one launch.
-    ctx->slots = std::max(ctx->slots, (int64_t)chunk_b * dims->num_kv_heads + ctx->quant_ctas[0]);
     ctx->part_rows = ctx->slots * pda::kMaxGroup;
     if (ctx->rows_ctas[1] > 0)
         ctx->part_rows = std::max<int64_t>(ctx->part_rows,
                                            (int64_t)chunk_b * dims->num_kv_heads * 2 * pda::kMaxGroup +
                                                (int64_t)std::max({ctx->rows_ctas[0], ctx->rows_ctas[1],
-                                                                  ctx->tc_ctas, ctx->quant_ctas[1]}) *
+                                                                  ctx->tc_ctas}) *
                                                    pda::kMaxRowsPerWalk);
+
+    // 8-bit decode: 8 or 16 packed q rows.
+    for (int k = 0; k < 2; ++k)
+        if (ctx->quant_ctas[k] > 0)
+            ctx->part_rows = std::max<int64_t>(ctx->part_rows, (int64_t)chunk_b * dims->num_kv_heads * 8 * (k + 1) +
+                                                                   (int64_t)ctx->quant_ctas[k] * 8 * (k + 1));
 
     const int64_t nq = (int64_t)dims->max_seqs * dims->num_q_heads;
     struct { void** ptr; size_t bytes; } allocs[] = {

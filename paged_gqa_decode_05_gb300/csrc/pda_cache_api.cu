@@ -125,25 +125,68 @@ void set_prep(pda::HeadsParams& p, const pda_prep* prep) {
     p.interleaved = prep->interleaved;
 }
 
-// A pool of 8-bit rows as a 5-D view {bytes of a slab, bs slots, slabs, Hkv,
-// num_blocks}, box {.., bs, slabs, 1, 1}: one kv head's rows of one block land
-// as [slab][slot][128 bytes] (64 at head size 64) with the swizzle of that
-// width.
-pda_status encode_quant_pool(const pda_dims& d, void* base, const pda_cache* c, CUtensorMap* tm) {
-    const int row = d.head_dim < 128 ? d.head_dim : 128;
-    const cuuint64_t dims[5] = {(cuuint64_t)row, (cuuint64_t)d.block_size, (cuuint64_t)(d.head_dim / row),
-                                (cuuint64_t)d.num_kv_heads, (cuuint64_t)c->num_blocks};
-    const cuuint64_t strides[4] = {(cuuint64_t)c->tok_stride, (cuuint64_t)row, (cuuint64_t)c->kvh_stride,
-                                   (cuuint64_t)c->blk_stride};
-    const cuuint32_t box[5] = {(cuuint32_t)row, (cuuint32_t)d.block_size, (cuuint32_t)(d.head_dim / row), 1, 1};
+// 5-D views of 8-bit pools for TMA boxes that land as [head][slab][slot][128
+// bytes] (64 at head size 64) with the swizzle of that width.
+bool encode_view(const void* base, const cuuint64_t (&dims)[5], const cuuint64_t (&strides)[4],
+                 const cuuint32_t (&box)[5], CUtensorMap* tm) {
     const cuuint32_t one[5] = {1, 1, 1, 1, 1};
-    const CUresult r = pda::tensor_map_encoder()(
-        tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, base, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-        row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS)
-        return fail(PDA_ERR_INVALID_ARG, "cuTensorMapEncodeTiled rejected the pool layout (CUresult %d)", (int)r);
-    return PDA_OK;
+    return pda::tensor_map_encoder()(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void*>(base), dims, strides, box,
+                                     one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                     box[0] == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                                     CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Joined: the distance between the pools is one more axis, {bytes of a row,
+// bs slots, heads, K|V, num_blocks}, so that one copy brings a block's K and V
+// rows; head size 256 has two slabs a row and puts slabs and heads on one
+// axis, where heads lie side by side.  Returns false where the layout does
+// not fit (or the driver refuses it).
+bool encode_joined(const pda_dims& d, const pda_cache* c, CUtensorMap* tm) {
+    const uintptr_t k = reinterpret_cast<uintptr_t>(c->k_pool), v = reinterpret_cast<uintptr_t>(c->v_pool);
+    const uintptr_t first = std::min(k, v), apart = std::max(k, v) - first;
+    if (apart == 0 || apart >= (uintptr_t(1) << 40)) return false;
+    const cuuint64_t bs = (cuuint64_t)d.block_size, nb = (cuuint64_t)c->num_blocks, slabs = d.head_dim == 256 ? 2 : 1;
+    const cuuint64_t tok = (cuuint64_t)c->tok_stride, kvh = (cuuint64_t)c->kvh_stride, blk = (cuuint64_t)c->blk_stride;
+    const cuuint32_t row = d.head_dim < 128 ? (cuuint32_t)d.head_dim : 128u;
+    if (slabs == 2 && kvh != 256) return false;
+    return encode_view(reinterpret_cast<void*>(first), {row, bs, slabs * (cuuint64_t)d.num_kv_heads, 2, nb},
+                       {tok, slabs == 2 ? 128 : kvh, apart, blk},
+                       {row, (cuuint32_t)bs, (cuuint32_t)slabs, 2, 1}, tm);
+}
+
+// A view of one pool, {bytes of a slab, bs slots, slabs, heads, num_blocks}.
+bool encode_apart(const pda_dims& d, const void* base, const pda_cache* c, CUtensorMap* tm) {
+    const cuuint32_t row = d.head_dim < 128 ? (cuuint32_t)d.head_dim : 128u, slabs = (cuuint32_t)d.head_dim / row;
+    return encode_view(base,
+                       {row, (cuuint64_t)d.block_size, slabs, (cuuint64_t)d.num_kv_heads, (cuuint64_t)c->num_blocks},
+                       {(cuuint64_t)c->tok_stride, row, (cuuint64_t)c->kvh_stride, (cuuint64_t)c->blk_stride},
+                       {row, (cuuint32_t)d.block_size, slabs, 1, 1}, tm);
+}
+
+// The scales as rows of 2 bs floats, one per (block, kv head), for gathers.
+bool encode_scales(const pda_dims& d, const pda_cache* c, CUtensorMap* tm) {
+    const int64_t rows = c->num_blocks * d.num_kv_heads;
+    if (rows > INT32_MAX) return false;
+    const cuuint64_t floats = 2 * (cuuint64_t)d.block_size;
+    const cuuint64_t dims[2] = {floats, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {4 * floats};
+    const cuuint32_t box[2] = {(cuuint32_t)floats, 1}, one[2] = {1, 1};
+    return pda::tensor_map_encoder()(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, c->scales, dims, strides, box, one,
+                                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                                     CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// How a call's pools load: encodes the context's maps, or returns false where
+// boxes do not fit (then rows are copied one by one).
+bool encode_boxes(pda_ctx* ctx, const pda_cache* c) {
+    const pda_dims& d = ctx->dims;
+    if (d.block_size < 4) return false;  // four blocks' scales must fill the 128 bytes a copy starts on
+    if (!encode_scales(d, c, &ctx->quant_s)) return false;
+    ctx->quant_joined = pda::quant_boxes(d.head_dim, d.block_size, true) && encode_joined(d, c, &ctx->quant_k);
+    return ctx->quant_joined ||
+           (pda::quant_boxes(d.head_dim, d.block_size, false) && encode_apart(d, c->k_pool, c, &ctx->quant_k) &&
+            encode_apart(d, c->v_pool, c, &ctx->quant_v));
 }
 
 pda_status run_quant(pda_ctx* ctx, const pda_bf16* q, const pda_cache* c, const int32_t* table, int32_t max_blocks,
@@ -158,29 +201,30 @@ pda_status run_quant(pda_ctx* ctx, const pda_bf16* q, const pda_cache* c, const 
     // there are more and the shape has it, 16.
     const int tiles = q_len * G > 8 && ctx->quant_ctas[1] > 0 ? 2 : 1;
     const int qp = std::max(1, std::min(q_len, 8 * tiles / G));
-    const int Qr = (q_len + qp - 1) / qp, SR = qp * G;
+    const int Qr = (q_len + qp - 1) / qp;
     const bool multi = q_len > 1;
     const pda::QuantShape shape = pda::quant_shape(D, c->format, tiles, multi);
     const int grid = ctx->quant_ctas[tiles - 1];
     if (Qr > grid) return fail(PDA_ERR_INVALID_ARG, "q_len %d: more launch rows per sequence than CTAs (%d)", q_len, grid);
     p.unit_cost = pda::quant_unit_cost(D, tiles, bs, multi);
     if ((st = pda::check_plan_size((int64_t)batch * q_len, max_blocks, p.unit_cost)) != PDA_OK) return st;
-
     const pda_pool_key key = {c->k_pool, c->v_pool, c->num_blocks, c->blk_stride, c->tok_stride, c->kvh_stride};
     const pda_pool_key& was = ctx->quant_key;
-    if (!(ctx->quant_maps_valid && was.k == key.k && was.v == key.v && was.num_blocks == key.num_blocks &&
-          was.blk == key.blk && was.tok == key.tok && was.kvh == key.kvh)) {
+    if (!(ctx->quant_maps_valid && ctx->quant_scales == c->scales && was.k == key.k && was.v == key.v &&
+          was.num_blocks == key.num_blocks && was.blk == key.blk && was.tok == key.tok && was.kvh == key.kvh)) {
         ctx->quant_maps_valid = false;
-        ctx->quant_row_mode = pda::quant_boxes(D, bs) ? 0 : 2;
-        if (ctx->quant_row_mode == 0 && ((st = encode_quant_pool(d, c->k_pool, c, &ctx->quant_k)) != PDA_OK ||
-                                         (st = encode_quant_pool(d, c->v_pool, c, &ctx->quant_v)) != PDA_OK))
-            return st;
+        ctx->quant_row_mode = encode_boxes(ctx, c) ? 0 : 2;
+        ctx->quant_scales = c->scales;
         ctx->quant_key = key;
         ctx->quant_maps_valid = true;
     }
     p.tm_k = ctx->quant_k;
     p.tm_v = ctx->quant_v;
+    p.tm_k1 = ctx->quant_s;
     p.row_gather = ctx->quant_row_mode;
+    p.joined = ctx->quant_joined;
+    p.v_first = ctx->quant_joined && c->v_pool < c->k_pool;
+    p.box_head = D == 256 ? 2 : 1;
     p.num_blocks = c->num_blocks;
     p.k_base = static_cast<const uint16_t*>(c->k_pool);
     p.v_base = static_cast<const uint16_t*>(c->v_pool);
@@ -195,15 +239,15 @@ pda_status run_quant(pda_ctx* ctx, const pda_bf16* q, const pda_cache* c, const 
     p.table_stride = max_blocks;
     p.q_len = q_len;
     p.qp = qp;
-    p.rows_per_slot = SR;
     p.Hq = Hq;
     p.Hkv = Hkv;
     p.G = G;
+    p.rows_per_slot = qp * G;
     p.bs = bs;
     p.prefetch = ctx->quant_row_mode == 0 && bs >= 8 && Qr == 1;
 
     // launch rows per chunk (whole sequences), as many as the partial states allow
-    const int64_t fit = (ctx->part_rows / SR - grid) / Hkv;
+    const int64_t fit = (ctx->part_rows / p.rows_per_slot - grid) / p.Hkv;
     const int32_t rows_total = batch * Qr;
     const int32_t chunk = (int32_t)(std::min<int64_t>(pda::kMaxLaunchBatch, fit) / Qr) * Qr;
     if (chunk < 1)

@@ -78,7 +78,9 @@ struct pda_ctx {
     bool quant_maps_valid = false;
     pda_pool_key quant_key;
     int32_t quant_row_mode = 0;
-    CUtensorMap quant_k, quant_v;
+    bool quant_joined = false;  // quant_k brings K and V rows
+    const void* quant_scales = nullptr;
+    CUtensorMap quant_k, quant_v, quant_s;
 };
 
 namespace pda {

@@ -294,11 +294,19 @@ __device__ __forceinline__ int32_t build_prefix(const SplitParams& p, int32_t* p
 template <int D, int ST, int MODE>
 struct Bf16Loader {
     using C = Cfg<D, ST, MODE>;
-    static __device__ __forceinline__ int blocks_per_stage(int bs) { return C::kST / bs; }  // the host keeps bs <= ST
+    static __device__ __forceinline__ int blocks_per_stage(const SplitParams& p) { return C::kST / p.bs; }  // the host keeps bs <= ST
+    // every arrival a stage's barrier expects (33 for cp.async rows)
+    static __device__ __forceinline__ uint32_t arrivals(const SplitParams& p) { return p.row_gather == 2 ? 33u : 1u; }
     static __device__ __forceinline__ uint32_t tx_bytes(const SplitParams& p, int32_t n, int rows) {
         return p.row_gather == 0 ? (uint32_t)n * 2u * (uint32_t)p.bs * D * 2u
              : p.row_gather == 1 ? (uint32_t)((rows + 3) >> 2) * 2u * 4u * D * 2u
                                  : 0u;  // cp.async completions arrive instead
+    }
+    // bytes of a unit's nr q rows, and the copy of query k's G rows
+    static __device__ __forceinline__ uint32_t q_bytes(const SplitParams&, int nr) { return (uint32_t)(nr * D * 2); }
+    static __device__ __forceinline__ void load_q(const SplitParams& p, uint32_t sK, int k, const uint16_t* q,
+                                                  uint32_t full) {
+        bulk_load(sK + C::kQOff + (uint32_t)(k * p.G * D * 2), q, (uint32_t)(p.G * D * 2), full);
     }
     template <typename WinId>
     static __device__ __forceinline__ void issue(const SplitParams& p, uint32_t sK, int32_t n, int rows, int32_t rel,
@@ -412,7 +420,7 @@ __device__ __forceinline__ void run_producer(const SplitParams& p, uint32_t base
     // it normal.
     const uint64_t pol = rows_per_seq<MQ>(p) > 1 ? policy_evict_normal() : policy_evict_first();
     const int bs = p.bs, Hkv = p.Hkv;
-    const int NB = Loader::blocks_per_stage(bs);
+    const int NB = Loader::blocks_per_stage(p);
 
     int stage = 0;
     uint32_t phase = 0;
@@ -558,17 +566,14 @@ __device__ __forceinline__ void run_producer(const SplitParams& p, uint32_t base
             m.nr = MQ ? ri.cnt * p.G : p.G;
             meta[stage] = m;
             const bool load_q = seg_begin && MODE != kGather;
-            const uint32_t bytes = Loader::tx_bytes(p, n, (n - 1) * bs + lastv) + (load_q ? (uint32_t)(m.nr * D * 2) : 0u);
-            mbar_arrive_expect_tx(full, bytes);
+            mbar_arrive_expect_tx(full, Loader::tx_bytes(p, n, (n - 1) * bs + lastv) +
+                                            (load_q ? Loader::q_bytes(p, m.nr) : 0u));
             if (load_q) {  // the G q rows of kv head kvh for each packed query
                 if constexpr (MQ) {
                     for (int k = 0; k < ri.cnt; ++k)
-                        bulk_load(sK + C::kQOff + (uint32_t)(k * p.G * D * 2),
-                                  p.q + qo_offset<MQ>(p, ri.b, ri.first + k, kvh * p.G, D),
-                                  (uint32_t)(p.G * D * 2), full);
+                        Loader::load_q(p, sK, k, p.q + qo_offset<MQ>(p, ri.b, ri.first + k, kvh * p.G, D), full);
                 } else {
-                    bulk_load(sK + C::kQOff, p.q + qo_offset<MQ>(p, b, 0, kvh * p.G, D),
-                              (uint32_t)(p.G * D * 2), full);
+                    Loader::load_q(p, sK, 0, p.q + qo_offset<MQ>(p, b, 0, kvh * p.G, D), full);
                 }
             }
         }
@@ -598,8 +603,7 @@ __device__ __forceinline__ void run_producer(const SplitParams& p, uint32_t base
     if (ok) {
         if (mbar_wait_bounded(empty0 + 8 * stage, phase ^ 1u, kWaitLimitNs)) {
             meta[stage].flags = kDone;
-            // every arrival the stage's barrier expects (33 for cp.async rows)
-            mbar_arrive_count(full0 + 8 * stage, p.row_gather == 2 ? 33u : 1u);
+            mbar_arrive_count(full0 + 8 * stage, Loader::arrivals(p));
         } else {
             ok = false;
         }
@@ -1125,21 +1129,40 @@ __device__ __forceinline__ void zero_empty_rows(const SplitParams& p, const int3
     }
 }
 
-// One 16-row q tile of a row-form segment end, once the consumers have
-// staged their token slices' states: st_m / st_l [slice][32 q rows], st_o
-// [slice][16 rows of the tile][D + 8].  The first tile decides the piece's
+// The token slices' states of a row-form q tile, staged as st_m / st_l
+// [slice][32 q rows] and st_o [slice][16 rows of the tile][D + 8]: the
+// combined state of q row h (row hr of the tile), columns d4 .. d4 + 3.
+template <int D, int kSlices>
+struct RowSlices {
+    const float *st_m, *st_l, *st_o;
+    __device__ __forceinline__ void operator()(int h, int hr, int d4, float& M, float& Ls, float4& Os) const {
+        constexpr int kOStride = D + 8;
+#pragma unroll
+        for (int w = 0; w < kSlices; ++w) M = fmaxf(M, st_m[w * kMaxRowsPerWalk + h]);
+        if (M != kNegInf) {
+#pragma unroll
+            for (int w = 0; w < kSlices; ++w) {
+                const float f = ex2(st_m[w * kMaxRowsPerWalk + h] - M);
+                const float4 v = *reinterpret_cast<const float4*>(st_o + (size_t)(w * 16 + hr) * kOStride + d4);
+                Ls += st_l[w * kMaxRowsPerWalk + h] * f;
+                Os.x += v.x * f; Os.y += v.y * f; Os.z += v.z * f; Os.w += v.w * f;
+            }
+        }
+    }
+};
+
+// One q tile of kTileRows rows of a segment end, once the consumers have
+// staged their states (combined by `own`).  The first tile decides the piece's
 // role (whole unit, stored partial, or the last piece, which merges every
 // stored partial with its own); each (row, 4 columns) of the tile is then
 // combined over the slices and written (bf16 o / l, or the fp32 partial).
-// Returns false when the CTA aborts.  kTileRows rows make a tile, kRowStride
-// rows a slice of st_m / st_l; kNan: a NaN sum of weights gives NaN, not 0.
-template <int D, int kSlices, int kThreadsC, int kTileRows = 16, int kRowStride = kMaxRowsPerWalk, bool kNan = false>
+// Returns false when the CTA aborts.  kNan: a NaN sum of weights gives NaN,
+// not 0.
+template <int D, int kThreadsC, int kTileRows = 16, bool kNan = false, class Own>
 __device__ __forceinline__ bool rows_tile_merge(const SplitParams& p, const StageMeta& m, int tile, int ct,
                                                 int32_t ticket, const UnitPieces& pc, const GroupRange& grs,
-                                                const RowInfo& ri, const float* st_m, const float* st_l,
-                                                const float* st_o, int32_t* st_role, uint32_t cbar,
+                                                const RowInfo& ri, const Own& own, int32_t* st_role, uint32_t cbar,
                                                 uint32_t& cphase, volatile int* abort_flag, int& role) {
-    constexpr int kOStride = D + 8;
     const bool whole = (m.flags & kWholeUnit) != 0;
     const int u = m.b * p.Hkv + m.kvh;
     const int NR = m.nr, SR = p.rows_per_slot, G = p.G;
@@ -1172,21 +1195,9 @@ __device__ __forceinline__ bool rows_tile_merge(const SplitParams& p, const Stag
         for (int i4 = ct; i4 < nrt * D / 4; i4 += kThreadsC) {
             const int hr = (4 * i4) / D, d4 = 4 * i4 - hr * D;
             const int h = h0 + hr;  // q row of the unit
-            float M = kNegInf;
-#pragma unroll
-            for (int w = 0; w < kSlices; ++w) M = fmaxf(M, st_m[w * kRowStride + h]);
-            float Ls = 0.f;
+            float M = kNegInf, Ls = 0.f;
             float4 Os = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (M != kNegInf) {
-#pragma unroll
-                for (int w = 0; w < kSlices; ++w) {
-                    const float f = ex2(st_m[w * kRowStride + h] - M);
-                    const float4 v =
-                        *reinterpret_cast<const float4*>(st_o + (size_t)(w * kTileRows + hr) * kOStride + d4);
-                    Ls += st_l[w * kRowStride + h] * f;
-                    Os.x += v.x * f; Os.y += v.y * f; Os.z += v.z * f; Os.w += v.w * f;
-                }
-            }
+            own(h, hr, d4, M, Ls, Os);
             if (role == kRoleStore) {
                 const int64_t r = (int64_t)(u + (int)blockIdx.x) * SR + h;
                 *reinterpret_cast<float4*>(p.part_o + r * D + d4) = Os;
@@ -1205,15 +1216,15 @@ __device__ __forceinline__ bool rows_tile_merge(const SplitParams& p, const Stag
                 for (int i0 = 0; i0 < pc.n; i0 += 4) {
                     float mi[4], li[4];
                     float4 oi[4];
-                    bool own[4];
+                    bool mine[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         mi[k] = kNegInf;
                         li[k] = 0.f;
                         oi[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                         const int64_t c = piece_cta(pc, i0 + k, grs);
-                        own[k] = i0 + k < pc.n && c == (int64_t)blockIdx.x;
-                        if (i0 + k >= pc.n || own[k]) continue;
+                        mine[k] = i0 + k < pc.n && c == (int64_t)blockIdx.x;
+                        if (i0 + k >= pc.n || mine[k]) continue;
                         const int64_t r = (u + c) * SR + h;
                         mi[k] = ld_cg(p.part_ml + r * 2);
                         li[k] = ld_cg(p.part_ml + r * 2 + 1);
@@ -1221,7 +1232,7 @@ __device__ __forceinline__ bool rows_tile_merge(const SplitParams& p, const Stag
                     }
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        if (own[k]) merge_state(Mr, Lr, Or, M, Ls, Os);
+                        if (mine[k]) merge_state(Mr, Lr, Or, M, Ls, Os);
                         else merge_state(Mr, Lr, Or, mi[k], li[k], oi[k]);
                     }
                 }
@@ -1470,8 +1481,9 @@ __device__ __forceinline__ void run_consumer_rows(const SplitParams& p, uint32_t
                     m0 = m1 = kNegInf;
                     l0 = l1 = 0.f;
                 }
-                if (!rows_tile_merge<D, kSlices, kThreadsC>(p, m, tile, ct, ticket, pc, grs, ri, st_m, st_l, st_o,
-                                                            st_role, cbar, cphase, abort_flag, role)) {
+                if (!rows_tile_merge<D, kThreadsC>(p, m, tile, ct, ticket, pc, grs, ri,
+                                                   RowSlices<D, kSlices>{st_m, st_l, st_o}, st_role, cbar, cphase,
+                                                   abort_flag, role)) {
                     stop = true;
                     break;
                 }
@@ -1872,9 +1884,10 @@ __device__ __forceinline__ void run_consumer_tc(const SplitParams& p, uint32_t b
             int role = kRoleAbort;
             bool stop = false;
             for (int tile = 0; tile < 2; ++tile) {
-                const bool merged = rows_tile_merge<D, 2, kThreadsC>(p, m, tile, ct, ticket, pc, grs, ri, st_m, st_l,
-                                                                     st_o + (size_t)tile * 2 * 16 * kOStride, st_role,
-                                                                     cbar, cphase, abort_flag, role);
+                const bool merged = rows_tile_merge<D, kThreadsC>(
+                    p, m, tile, ct, ticket, pc, grs, ri,
+                    RowSlices<D, 2>{st_m, st_l, st_o + (size_t)tile * 2 * 16 * kOStride}, st_role, cbar, cphase,
+                    abort_flag, role);
                 if (!__all_sync(0xffffffffu, merged ? 1 : 0)) { stop = true; break; }
             }
             if (stop) break;
@@ -1934,8 +1947,9 @@ constexpr int kPrefetchStages = PDA_PREFETCH_STAGES;  // stages of blocks prefet
 // prefetch, every index is kept inside the CTA's table row and the pool, and
 // the decode itself reads everything after the wait.  Single-query launches
 // of block boxes (multi-query with one launch row per sequence).
-template <int ST, int KPER, class Touch>
+template <int KPER, class Touch>
 __device__ __noinline__ void prefetch_first_stages_k(const SplitParams& p, int lane) {
+    const int ST = Touch::stage_rows(p);
     const int per = (p.B + 31) / 32;  // <= KPER
     const int lo = min(p.B, lane * per), hi = min(p.B, lo + per);
     const int lbs = 31 - __clz(p.bs);  // block sizes are powers of two
@@ -2017,21 +2031,23 @@ __device__ __noinline__ void prefetch_first_stages_k(const SplitParams& p, int l
 // The plan in registers is sized to the batch (up to 1, 4 or 32 sequences a
 // lane).  Not inlined: kept out of the split kernel's own code, whose start
 // every launch fetches (inlined, it cost small batches 0.4 us a call).
+template <int ST>
 struct TouchBoxes {  // a block's K and V rows of one kv head
+    static __device__ __forceinline__ int stage_rows(const SplitParams&) { return ST; }
     static __device__ __forceinline__ void block(const SplitParams& p, int32_t kvh, int32_t id) {
         tma_prefetch_5d(&p.tm_k, 0, 0, 0, kvh, id);
         tma_prefetch_5d(&p.tm_v, 0, 0, 0, kvh, id);
     }
 };
 
-template <int ST, int MODE, class Touch = TouchBoxes>
+template <int MODE, class Touch>
 __device__ __noinline__ void prefetch_first_stages(const SplitParams& p, int lane) {
     // multi-query: one launch row per sequence only (then row s is sequence s
     // and reads its whole length, like plain decode)
     if (is_multi(MODE) && rows_per_seq<is_multi(MODE)>(p) != 1) return;
-    if (p.B <= 32) prefetch_first_stages_k<ST, 1, Touch>(p, lane);
-    else if (p.B <= 128) prefetch_first_stages_k<ST, 4, Touch>(p, lane);
-    else prefetch_first_stages_k<ST, kMaxLaunchBatch / 32, Touch>(p, lane);
+    if (p.B <= 32) prefetch_first_stages_k<1, Touch>(p, lane);
+    else if (p.B <= 128) prefetch_first_stages_k<4, Touch>(p, lane);
+    else prefetch_first_stages_k<kMaxLaunchBatch / 32, Touch>(p, lane);
 }
 
 // Register cap: for D <= 128 two CTAs share an SM (two 3-stage rings keep as
@@ -2101,7 +2117,7 @@ __global__ void __maxnreg__(split_max_regs(D, MODE)) split_kernel(const __grid_c
         // (not in the two-q-tile row forms: the call alone costs its main loop
         // registers, and its consumers set its time)
         if constexpr (MODE != kGather && MODE != kMultiRows32 && !C::kTc)
-            if (!early && p.prefetch) prefetch_first_stages<ST, MODE>(p, lane);
+            if (!early && p.prefetch) prefetch_first_stages<MODE, TouchBoxes<ST>>(p, lane);
         return;
     }
     if constexpr (C::kTc) {

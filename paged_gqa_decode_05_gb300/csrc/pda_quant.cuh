@@ -48,28 +48,55 @@ struct QuantCfg {
     static constexpr int kSlabs = D / kRB;
     static constexpr int kTileBytes = kST * D;
     static constexpr int kSOff = 2 * kTileBytes;        // the rows' scales: per block [K bs][V bs] floats
-    static constexpr int kQOff = kSOff + kST * 8;
+    static constexpr int kQOff = kSOff + kST * 8;       // the q rows
     static constexpr int kStageBytes = quant_stage_bytes(D, NT);
     static constexpr int kStages = quant_stages(D, NT);
     static constexpr int kK = D / 32;                   // 32-column steps of a row
     static_assert(kStageBytes % 1024 == 0, "stages start on swizzle spans");
-    static_assert(kWarps * 8 * NT * (D + 8) * 4 <= kStageBytes, "the staged states fit a stage");
+    static_assert(kWarps * 8 * NT * (D + 4) * 4 <= kStageBytes, "the staged states fit a stage");
 };
+
+// A stage holds blocks of 1 << lbs rows back to back (one of kST rows when the
+// rows came one by one), each [K][V] (or V first) of [slabs][rows][kRB bytes].
+// Row t's offset within the K or V parts, slab 0, and the XOR of the chunk
+// index in a row at byte offset `off` of the stage: the TMA swizzle takes it
+// from address bits 7.. (three of them for 128-byte rows, two for 64-byte
+// rows); stages start on 1024-byte spans.
+template <int D>
+__device__ __forceinline__ uint32_t quant_row_off(int t, int lbs) {
+    constexpr int RB = D < 128 ? D : 128;
+    return ((uint32_t)(t >> lbs) << lbs) * (2u * D) + (uint32_t)(t & ((1 << lbs) - 1)) * RB;
+}
+template <int D>
+__device__ __forceinline__ int quant_swz(uint32_t off) {
+    return (int)(off >> 7) & (D == 64 ? 3 : 7);
+}
 
 template <int D, int NT>
 struct QuantLoader {
     using C = QuantCfg<D, NT>;
-    // at most 64 blocks (the producer's window of block ids)
-    static __device__ __forceinline__ int blocks_per_stage(int bs) { return min(C::kST / bs, 64); }
+    // at most 64 blocks (the producer's window of block ids), 32 where a lane takes one
+    static __device__ __forceinline__ int blocks_per_stage(const SplitParams& p) {
+        return min(C::kST / p.bs, p.row_gather ? 64 : 32);
+    }
+    static __device__ __forceinline__ uint32_t arrivals(const SplitParams& p) { return p.row_gather ? 33u : 1u; }
+    // scales come four blocks to a copy where a stage has room for four
+    static __device__ __forceinline__ bool four(const SplitParams& p) { return 4 * p.bs <= C::kST; }
     static __device__ __forceinline__ uint32_t tx_bytes(const SplitParams& p, int32_t n, int) {
-        return p.row_gather == 0 ? (uint32_t)(n * p.bs) * (2u * D + 8u) : 0u;
+        const uint32_t scaled = four(p) ? (uint32_t)(n + 3) & ~3u : (uint32_t)n;
+        return p.row_gather == 0 ? ((uint32_t)n * (2u * D) + scaled * 8u) * p.bs : 0u;
+    }
+    static __device__ __forceinline__ uint32_t q_bytes(const SplitParams&, int nr) { return (uint32_t)(nr * D * 2); }
+    static __device__ __forceinline__ void load_q(const SplitParams& p, uint32_t sK, int k, const uint16_t* q,
+                                                  uint32_t full) {
+        bulk_load(sK + C::kQOff + (uint32_t)(k * p.G * D * 2), q, (uint32_t)(p.G * D * 2), full);
     }
     template <typename WinId>
     static __device__ __forceinline__ void issue(const SplitParams& sp, uint32_t sK, int32_t n, int rows, int32_t rel,
                                                  int kvh, uint32_t full, uint64_t pol, int lane, const WinId& win_id) {
         const QuantParams& p = static_cast<const QuantParams&>(sp);
         const int bs = p.bs;
-        const uint32_t sV = sK + C::kTileBytes, sS = sK + C::kSOff;
+        const uint32_t sS = sK + C::kSOff;
         auto checked = [&](int32_t id) {
             if (id < 0 || (int64_t)id >= p.num_blocks) {
                 atomicOr(p.err, PDA_DEVERR_BAD_BLOCK_ID_);
@@ -77,57 +104,98 @@ struct QuantLoader {
             }
             return id;
         };
+        const int lbs = 31 - __clz(bs);
         if (p.row_gather == 0) {
-            // lane i copies block i: a box per pool and the block's scales
-            const int32_t wid = win_id(rel + min(lane, n - 1));
+            // lane i copies block i.  A warp's copies go out one lane after another, 80
+            // to 100 cycles each, and with three a block (K, V, scales) that alone was
+            // 2100 of a stage's 3000 cycles at block size 16: hence one joined box for
+            // K and V, and the scales of four blocks to a copy.  (Scales by cp.async
+            // took 900 cycles a stage; a uniform loop with one elected lane issuing
+            // was slower than the lanes.)
+            const int32_t id = checked(win_id(rel + min(lane, n - 1)));
             if (lane < n) {
-                const int32_t id = checked(wid);
-                const uint32_t off = (uint32_t)(lane * bs) * (uint32_t)D;
-                tma_load_5d(sK + off, &p.tm_k, 0, 0, 0, kvh, id, full, pol);
-                tma_load_5d(sV + off, &p.tm_v, 0, 0, 0, kvh, id, full, pol);
-                bulk_load(sS + (uint32_t)(lane * bs) * 8u, p.scales + ((int64_t)id * p.Hkv + kvh) * 2 * bs, 8u * bs,
+                const uint32_t dst = sK + ((uint32_t)lane << lbs) * (2u * D);
+                if (p.joined) {
+                    tma_load_5d(dst, &p.tm_k, 0, 0, p.box_head * kvh, 0, id, full, pol);
+                } else {
+                    tma_load_5d(dst, &p.tm_k, 0, 0, 0, kvh, id, full, pol);
+                    tma_load_5d(dst + (uint32_t)bs * D, &p.tm_v, 0, 0, 0, kvh, id, full, pol);
+                }
+            }
+            if (four(p)) {
+                const int32_t row = id * p.Hkv + kvh;  // lanes from n on repeat the last
+                const int32_t r1 = __shfl_down_sync(0xffffffffu, row, 1), r2 = __shfl_down_sync(0xffffffffu, row, 2);
+                const int32_t r3 = __shfl_down_sync(0xffffffffu, row, 3);
+                if ((lane & 3) == 0 && lane < n)
+                    tma_gather4(sS + ((uint32_t)lane << (lbs + 3)), &p.tm_k1, 0, row, r1, r2, r3, full, pol);
+            } else if (lane < n) {
+                bulk_load(sS + ((uint32_t)lane << (lbs + 3)), p.scales + (((int64_t)id * p.Hkv + kvh) << (lbs + 1)), 8u * bs,
                           full);
             }
-            return;
-        }
-        // rows of small blocks (or of strides a box cannot have): 16-byte
-        // chunks, written as one kST-row block
-        constexpr int CH = D / 16, RPI = 32 / CH;
-        const int c = lane % CH, sub = lane / CH;
-        const int lbs = 31 - __clz(bs);
-        const uint8_t* kb = reinterpret_cast<const uint8_t*>(p.k_base) + (int64_t)kvh * p.kvh_s + c * 16;
-        const uint8_t* vb = reinterpret_cast<const uint8_t*>(p.v_base) + (int64_t)kvh * p.kvh_s + c * 16;
-        for (int t0 = 0; t0 < rows; t0 += RPI) {
-            const int t = t0 + sub;
-            const int32_t wid = win_id(rel + (min(t, rows - 1) >> lbs));
-            if (t < rows) {
-                const int64_t off = (int64_t)checked(wid) * p.blk_s + (int64_t)(t & (bs - 1)) * p.tok_s;
-                const int sw = C::kRB == 128 ? (c & 7) ^ (t & 7) : c ^ ((t >> 1) & 3);
-                const uint32_t dst = (uint32_t)(c >> 3) * (C::kST * 128u) + (uint32_t)t * C::kRB + (uint32_t)(sw << 4);
-                cp_async_16(sK + dst, kb + off);
-                cp_async_16(sV + dst, vb + off);
+        } else {
+            const int lp = lbs > 0 ? lbs - 1 : 0;  // log2 of a block's 16-byte pieces (8 bytes for one token)
+            for (int i0 = 0; i0 < n << lp; i0 += 32) {
+                const int i = min(i0 + lane, (n << lp) - 1), blk = i >> lp;
+                const int32_t id = checked(win_id(rel + blk));
+                const float* s = p.scales + (((int64_t)id * p.Hkv + kvh) << (lbs + 1));
+                if (i0 + lane < n << lp) {
+                    if (lbs > 0) cp_async_16(sS + 16u * i, s + 4 * (i - (blk << lp)));
+                    else cp_async_8(sS + 8u * i, s);
+                }
             }
-        }
-        const int pieces = bs > 1 ? bs / 2 : 1;  // 16-byte pieces of a block's scales (8 bytes for one token)
-        for (int i0 = 0; i0 < n * pieces; i0 += 32) {
-            const int i = min(i0 + lane, n * pieces - 1), blk = i / pieces;
-            const int32_t wid = win_id(rel + blk);
-            if (i0 + lane < n * pieces) {
-                const float* s = p.scales + ((int64_t)checked(wid) * p.Hkv + kvh) * 2 * bs;
-                if (bs > 1) cp_async_16(sS + 16u * i, s + 4 * (i - blk * pieces));
-                else cp_async_8(sS + 8u * i, s);
+            // rows one by one in 16-byte chunks, written as one block of kST rows
+            constexpr int CH = D / 16, RPI = 32 / CH;
+            const int c = lane % CH, sub = lane / CH;
+            const uint8_t* kb = reinterpret_cast<const uint8_t*>(p.k_base) + (int64_t)kvh * p.kvh_s + c * 16;
+            const uint8_t* vb = reinterpret_cast<const uint8_t*>(p.v_base) + (int64_t)kvh * p.kvh_s + c * 16;
+            constexpr int CPS = C::kRB / 16;
+            for (int t0 = 0; t0 < rows; t0 += RPI) {
+                const int t = t0 + sub;
+                const int32_t wid = win_id(rel + (min(t, rows - 1) >> lbs));
+                if (t < rows) {
+                    const int64_t off = (int64_t)checked(wid) * p.blk_s + (int64_t)(t & (bs - 1)) * p.tok_s;
+                    const uint32_t r = (uint32_t)(c / CPS) * (C::kST * C::kRB) + (uint32_t)t * C::kRB;
+                    const uint32_t dst = sK + r + (uint32_t)(((c % CPS) ^ quant_swz<D>(r)) << 4);
+                    cp_async_16(dst, kb + off);
+                    cp_async_16(dst + C::kTileBytes, vb + off);
+                }
             }
+            cp_async_mbar_arrive_noinc(full);
         }
-        cp_async_mbar_arrive_noinc(full);
     }
 };
 
-struct TouchQuant {  // a block's rows of one kv head and their scales, towards L2
+template <int D, int NT>
+struct TouchQuant {  // a block's rows of a kv head and their scales, towards L2
+    static __device__ __forceinline__ int stage_rows(const SplitParams&) { return QuantCfg<D, NT>::kST; }
     static __device__ __forceinline__ void block(const SplitParams& sp, int32_t kvh, int32_t id) {
         const QuantParams& p = static_cast<const QuantParams&>(sp);
-        tma_prefetch_5d(&p.tm_k, 0, 0, 0, kvh, id);
-        tma_prefetch_5d(&p.tm_v, 0, 0, 0, kvh, id);
+        if (p.joined) {
+            tma_prefetch_5d(&p.tm_k, 0, 0, p.box_head * kvh, 0, id);
+        } else {
+            tma_prefetch_5d(&p.tm_k, 0, 0, 0, kvh, id);
+            tma_prefetch_5d(&p.tm_v, 0, 0, 0, kvh, id);
+        }
         bulk_prefetch(p.scales + ((int64_t)id * p.Hkv + kvh) * 2 * p.bs, 8u * p.bs);
+    }
+};
+
+// The states that the W warps of a segment staged, st_m / st_l [warp][16 rows]
+// and st_o [warp][kRows][D + 4]: the combined state of q row h.
+template <int D, int W, int kRows>
+struct UnitSlices {
+    const float *st_m, *st_l, *st_o;
+    __device__ __forceinline__ void operator()(int h, int, int d4, float& M, float& Ls, float4& Os) const {
+#pragma unroll
+        for (int w = 0; w < W; ++w) M = fmaxf(M, st_m[w * 16 + h]);
+        if (M == kNegInf) return;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const float f = ex2(st_m[w * 16 + h] - M);
+            const float4 v = *reinterpret_cast<const float4*>(st_o + (size_t)(w * kRows + h) * (D + 4) + d4);
+            Ls += st_l[w * 16 + h] * f;
+            Os.x += v.x * f; Os.y += v.y * f; Os.z += v.z * f; Os.w += v.w * f;
+        }
     }
 };
 
@@ -174,26 +242,13 @@ __device__ __forceinline__ void v_fragment(uint32_t r0, uint32_t r1, uint32_t (&
     }
 }
 
-// Byte offset of row t of a stage tile (slab 0, chunk 0) and the XOR of its
-// chunk index in slab h; blocks of 1 << lbs rows lie back to back, each
-// [slabs][rows][kRB bytes].
-template <int D>
-__device__ __forceinline__ uint32_t quant_row_off(int t, int lbs) {
-    constexpr int RB = D < 128 ? D : 128;
-    return ((uint32_t)(t >> lbs) << lbs) * D + (uint32_t)(t & ((1 << lbs) - 1)) * RB;
-}
-template <int D>
-__device__ __forceinline__ int quant_swz(int t, int h, int lbs) {
-    return D == 64 ? (t >> 1) & 3 : swz(t, h, lbs);
-}
-
 template <int D, int FMT, int NT, int MODE>
 __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_t base_s, uint8_t* base,
                                                    const SmemLayout& L, const StageMeta* meta, const int32_t* pfx,
                                                    volatile int* abort_flag, int warp, int lane) {
     using C = QuantCfg<D, NT>;
     constexpr int S = C::kStages, RT = C::kRT, K = C::kK;
-    constexpr int kThreadsC = C::kWarps * 32, kRows = 8 * NT, kOStride = D + 8;
+    constexpr int kThreadsC = C::kWarps * 32, kRows = 8 * NT, kOStride = D + 4;
     constexpr bool MQ = is_multi(MODE);
     const uint32_t full0 = base_s + L.bars, empty0 = full0 + 8 * S;
     const int g = lane >> 2, t = lane & 3;
@@ -205,14 +260,22 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
     // ldmatrix lane addresses, alike for K and (transposed) V: matrices are rows
     // 0-7, rows 8-15 of chunk c, then of chunk c + 1
     const int row = r0 + (lane & 15), cpar = lane >> 4;
+    const uint32_t part = (uint32_t)D << lbs;               // bytes between a block's K and V
+    const uint32_t k_at = p.v_first ? part : 0u, v_at = p.v_first ? 0u : part;
     uint32_t off[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) off[r] = quant_row_off<D>(row + 16 * r, lbs);
-    int swh[C::kSlabs];  // rows 16 apart share their swizzle
+    // the chunk swizzle of the lane's rows in slab h (rows 16 apart share it)
+    int swk[C::kSlabs], swv[C::kSlabs];
 #pragma unroll
-    for (int h = 0; h < C::kSlabs; ++h) swh[h] = quant_swz<D>(row, h, lbs);
+    for (int h = 0; h < C::kSlabs; ++h) {
+        swk[h] = quant_swz<D>(off[0] + k_at + h * hs);
+        swv[h] = quant_swz<D>(off[0] + v_at + h * hs);
+    }
     constexpr int CPS = C::kRB / 16;  // chunks per slab row
-    auto chunk = [&](int kk) { return (uint32_t)((2 * kk) / CPS) * hs + (uint32_t)((((2 * kk) % CPS + cpar) ^ swh[(2 * kk) / CPS]) << 4); };
+    auto chunk = [&](int kk, const int (&sw)[C::kSlabs]) {
+        return (uint32_t)((2 * kk) / CPS) * hs + (uint32_t)((((2 * kk) % CPS + cpar) ^ sw[(2 * kk) / CPS]) << 4);
+    };
 
     float o[NT][2 * K][4];
     uint32_t qf[NT][K][4];
@@ -253,23 +316,27 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
         // the last stage of a piece of a split unit draws the piece's ticket (see run_consumer)
         if (warp == 0 && lane == 0 && (md.flags & kSegEnd) && !(md.flags & kWholeUnit))
             ticket = atomicAdd(p.unit_sync + 2 * (md.b * p.Hkv + md.kvh), 1);
-        const uint32_t sK = base_s + (uint32_t)stage * C::kStageBytes;
-        const uint32_t sV = sK + C::kTileBytes;
-        const uint8_t* bytes = base + (sK - base_s);
+        const uint32_t s0 = base_s + (uint32_t)stage * C::kStageBytes;
+        const uint32_t sK = s0 + k_at, sV = s0 + v_at;
+        const uint8_t* bytes = base + (s0 - base_s);
 
         if (md.flags & kSegBegin) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const int qr = 8 * n + g;
                 const bool any = qr < (MQ ? md.nr : G);
+                const uint8_t* qp = bytes + C::kQOff + (size_t)(qr * D + 4 * t) * 2;
                 uint2 raw[K][2];
                 uint32_t top = 0;
 #pragma unroll
                 for (int kk = 0; kk < K; ++kk)
 #pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        raw[kk][i] = any ? *reinterpret_cast<const uint2*>(qp + 64 * kk + 32 * i) : make_uint2(0u, 0u);
+#pragma unroll
+                for (int kk = 0; kk < K; ++kk)
+#pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const uint8_t* s = bytes + C::kQOff + (size_t)(qr * D + 32 * kk + 16 * i + 4 * t) * 2;
-                        raw[kk][i] = any ? *reinterpret_cast<const uint2*>(s) : make_uint2(0u, 0u);
                         const uint32_t x = raw[kk][i].x, y = raw[kk][i].y;
                         top = max(top, max(max(x & 0x7fffu, (x >> 16) & 0x7fffu), max(y & 0x7fffu, (y >> 16) & 0x7fffu)));
                     }
@@ -324,8 +391,8 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int tr = r0 + 16 * r + 8 * i + g;
-                    const float* s = reinterpret_cast<const float*>(bytes + C::kSOff) + ((tr >> lbr) << (lbr + 1)) +
-                                     (tr & (p.bs - 1));
+                    const float* s = reinterpret_cast<const float*>(bytes + C::kSOff) +
+                                     ((tr >> lbr) << (lbr + 1)) + (tr & (p.bs - 1));
                     const bool in = tr < md.n_valid;
                     ks[r][i] = s[0];
                     float vs = in ? s[p.bs] : 1.f;
@@ -344,7 +411,7 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
 #pragma unroll
                 for (int kk = 0; kk < K; ++kk) {
                     uint32_t w[4];
-                    ldsm_x4(sK + off[r] + chunk(kk), w);
+                    ldsm_x4(sK + off[r] + chunk(kk, swk), w);
                     if constexpr (FMT == kE4m3) {
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
@@ -393,24 +460,26 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
             uint32_t pb[RT][NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
+                // the references move only when a weight would pass 2^(kRefBias + kLazyLog2);
+                // the columns' maxima are taken only then
                 float top[2];
-                bool up[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     top[c] = fmaxf(x[0][n][c], x[0][n][c + 2]);
 #pragma unroll
                     for (int r = 1; r < RT; ++r) top[c] = fmaxf(top[c], fmaxf(x[r][n][c], x[r][n][c + 2]));
-#pragma unroll
-                    for (int s = 4; s < 32; s <<= 1) top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], s));
-                    up[c] = top[c] > m[n][c] + (kLazyLog2 + kRefBias);
                 }
-                if (__any_sync(0xffffffffu, up[0] || up[1])) {
+                if (__any_sync(0xffffffffu, top[0] > m[n][0] + (kLazyLog2 + kRefBias) ||
+                                                top[1] > m[n][1] + (kLazyLog2 + kRefBias))) {
                     float a[2];
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                        for (int s = 4; s < 32; s <<= 1) top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], s));
+                        const bool up = top[c] > m[n][c] + (kLazyLog2 + kRefBias);
                         const float to = top[c] - kRefBias;
-                        a[c] = up[c] ? ex2(m[n][c] - to) : 1.f;  // an empty column (m = -inf): 0
-                        if (up[c]) m[n][c] = to;
+                        a[c] = up ? ex2(m[n][c] - to) : 1.f;  // an empty column (m = -inf): 0
+                        if (up) m[n][c] = to;
                         l[n][c] *= a[c];
                     }
 #pragma unroll
@@ -435,7 +504,7 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
                     uint32_t w[4], a[4], b[4];
-                    ldsm_x4_trans(sV + off[r] + chunk(kk), w);
+                    ldsm_x4_trans(sV + off[r] + chunk(kk, swv), w);
                     v_fragment<FMT>(w[0], w[1], a);
                     v_fragment<FMT>(w[2], w[3], b);
 #pragma unroll
@@ -451,7 +520,7 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
             float* st_m = reinterpret_cast<float*>(base + L.st_m);  // [warp][16 rows]
             float* st_l = reinterpret_cast<float*>(base + L.st_l);
             int32_t* st_role = reinterpret_cast<int32_t*>(base + L.st_x) + 2 * kMaxGroup;
-            float* st_o = reinterpret_cast<float*>(base + (sK - base_s));  // [warp][kRows][kOStride]
+            float* st_o = reinterpret_cast<float*>(base + (s0 - base_s));  // [warp][kRows][kOStride]
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -459,7 +528,8 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
 #pragma unroll
                     for (int s = 4; s < 32; s <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], s);
             if (!consumer_sync(cbar, cphase, p.err, abort_flag)) break;  // all reads of the stage done
-            const int NR = MQ ? md.nr : G;
+            const RowInfo ri = row_info<MQ>(p, md.b);
+            const int NR = ri.cnt * G;  // q rows of the unit
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -480,12 +550,12 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
             pc.cf = 0; pc.su = 0; pc.n = 1; pc.every = true;
             const GroupRange grs = group_of_cta(blockIdx.x, pfx, p.B, rows_per_seq<MQ>(p), p.Hkv, gridDim.x);
             if (!(md.flags & kWholeUnit)) pc = unit_pieces(pfx, md.b, md.kvh, p.Hkv, p.unit_cost, grs);
-            const RowInfo ri = row_info<MQ>(p, md.b);
             StageMeta me = md;
             me.nr = NR;
             int role = kRoleAbort;
-            if (!rows_tile_merge<D, C::kWarps, kThreadsC, kRows, 16, true>(p, me, 0, ct, ticket, pc, grs, ri, st_m, st_l,
-                                                                          st_o, st_role, cbar, cphase, abort_flag, role))
+            if (!rows_tile_merge<D, kThreadsC, kRows, true>(p, me, 0, ct, ticket, pc, grs, ri,
+                                                            UnitSlices<D, C::kWarps, kRows>{st_m, st_l, st_o}, st_role,
+                                                            cbar, cphase, abort_flag, role))
                 break;
             if (!consumer_sync(cbar, cphase, p.err, abort_flag)) break;
             if (role == kRoleStore && ct == 0) red_release_gpu_add(p.unit_sync + 2 * (md.b * p.Hkv + md.kvh) + 1, 1);
@@ -512,7 +582,7 @@ __global__ void __maxnreg__(168) quant_split_kernel(const __grid_constant__ Quan
     StageMeta* meta = reinterpret_cast<StageMeta*>(base + L.meta);
     if (tid == 0) {
         for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(base_s + L.bars + 8 * s, p.row_gather ? 33 : 1);
+            mbar_init(base_s + L.bars + 8 * s, QuantLoader<D, NT>::arrivals(p));
             mbar_init(base_s + L.bars + 8 * (C::kStages + s), C::kWarps);
         }
         mbar_init(base_s + L.cbar, C::kWarps * 32);
@@ -524,7 +594,7 @@ __global__ void __maxnreg__(168) quant_split_kernel(const __grid_constant__ Quan
         prefetch_tensormap(&p.tm_v);
     }
     if (warp == C::kMainThreads / 32) {  // the prefetch warp: joins nothing below
-        if (p.prefetch) prefetch_first_stages<C::kST, MODE, TouchQuant>(p, lane);
+        if (p.prefetch) prefetch_first_stages<MODE, TouchQuant<D, NT>>(p, lane);
         return;
     }
     pdl_wait_primary();

@@ -8,30 +8,35 @@
 
 namespace pda {
 
-// Shapes.  A consumer warp takes 16 KV rows of a stage per row tile; head
+// Shapes.  A consumer warp takes 16 KV rows of a stage per row tile.  Head
 // sizes up to 128 with 8 packed q rows run two CTAs of 4 consumer warps per
-// SM, two row tiles each (128-row stages: as many bytes as 64 bf16 rows, two
-// independent chains per warp); 16 packed q rows (n_tiles 2) and head size
-// 256 run one CTA of 8 consumer warps.
+// SM, two row tiles each; 16 packed q rows (n_tiles 2) and head size 256 run
+// one CTA of 8.
 PDA_HD constexpr int quant_warps(int D, int n_tiles) { return D == 256 || n_tiles == 2 ? 8 : 4; }
 PDA_HD constexpr int quant_row_tiles(int D) { return D == 256 ? 1 : 2; }
 PDA_HD constexpr int quant_stage_rows(int D, int n_tiles) { return 16 * quant_warps(D, n_tiles) * quant_row_tiles(D); }
 PDA_HD constexpr int quant_stage_bytes(int D, int n_tiles) {
     return quant_stage_rows(D, n_tiles) * (2 * D + 8) + 8 * n_tiles * D * 2;
 }
-PDA_HD constexpr int quant_stages(int D, int n_tiles) { return D == 64 ? (n_tiles == 2 ? 5 : 5) : 3; }
-// Whether a block's rows load as one TMA box per pool: the box must fill whole
-// spans of the swizzle (1024 bytes of 128-byte rows, 512 of 64-byte rows).
-PDA_HD constexpr bool quant_boxes(int D, int bs) { return bs >= 8 || (D == 256 && bs == 4); }
+PDA_HD constexpr int quant_stages(int D, int) { return D == 64 ? 5 : 3; }
+// Whether blocks load as boxes: a block's K and V rows of one kv head must
+// fill whole 1024-byte spans (one box brings both where the pools' layout
+// allows it, with `joined`; else a box each).
+PDA_HD constexpr bool quant_boxes(int D, int bs, bool joined) { return (bs * D * (joined ? 2 : 1)) % 1024 == 0; }
 // Plan blocks added to every unit (see pda_plan.h), in quarter stages.
 PDA_HD int32_t quant_unit_cost(int D, int n_tiles, int bs, bool multi) {
     const int nb = quant_stage_rows(D, n_tiles) / bs;
-    const int x4 = !quant_boxes(D, bs) ? 2 : multi ? 12 : 6;
-    return (nb < 1 ? 1 : nb) * x4 / 4;
+    const int x4 = bs < 8 ? 2 : multi ? 12 : 6;
+    return nb * x4 / 4 < 1 ? 1 : nb * x4 / 4;
 }
 
 struct QuantParams : SplitParams {
     const float* scales;  // [num_blocks, Hkv, 2, bs]
+    // Box loads: tm_k brings a block's K and V rows of a kv head (V first when
+    // v_first), head h at coordinate 2 of box_head * h; or, when !joined, tm_k
+    // and tm_v bring them apart, h at coordinate 3.  tm_k1 views the scales as
+    // [num_blocks * Hkv][2 bs] for row gathers.
+    int32_t joined, v_first, box_head;
 };
 
 struct QuantShape {

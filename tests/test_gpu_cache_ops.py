@@ -290,7 +290,10 @@ LENS = {"tiny": [37, 80], "edges": [0, 1, 15, 16, 17, 63, 64, 65, 127, 128, 129]
 @pytest.mark.parametrize("hq,hkv,d,bs,lens", [
     (4, 2, 64, 16, "tiny"), (8, 2, 128, 16, "edges"), (16, 2, 256, 16, "edges"), (8, 1, 64, 8, "edges"),
     (5, 1, 128, 32, "long"), (12, 4, 128, 1, "edges"), (2, 2, 64, 2, "edges"), (8, 4, 256, 4, "edges"),
-    (3, 1, 256, 64, "long"), (16, 8, 128, 16, "many"), (8, 8, 128, 4, "edges")])
+    (3, 1, 256, 64, "long"), (16, 8, 128, 16, "many"), (8, 8, 128, 4, "edges"),
+    # batches whose units hold two or four kv heads
+    (12, 6, 64, 32, "many"), (16, 4, 256, 8, "many"), (8, 8, 64, 64, "many"), (32, 4, 128, 32, "many"),
+    (8, 4, 256, 4, "many"), (4, 4, 128, 4, "many"), (6, 2, 128, 64, "many")])
 def test_decode(dtype, q_len, hq, hkv, d, bs, lens):
     lens = LENS[lens]
     rng, g = np.random.default_rng(d + bs), gen(d + bs)
