@@ -15,51 +15,115 @@ namespace pda {
 #define PDA_DEVERR_BAD_POSITION_ 0x8u
 constexpr int kHeadsThreads = 256;
 
-// The sequence that owns row t: the largest b in [0, B) with starts[b] <= t.
-// Warp-wide: the lanes fetch 32 evenly spaced entries at once and search them
-// with shuffles, so up to 32 sequences cost one round trip; a longer list
-// leaves a span of B / 32 entries for a serial search.
-__device__ __forceinline__ int32_t find_seq(const int32_t* starts, int32_t B, int64_t t, int lane) {
-    const int32_t step = (B + 31) / 32;
-    const int32_t at = lane * step;
-    const int32_t v = at < B ? starts[at] : 0x7fffffff;
+// Where row t of a packed batch belongs: its sequence b, the end of the
+// sequence's rows and its length.  Warp-wide.  Up to 32 sequences the lanes
+// fetch every start and length at once (one round trip) and search the starts
+// with shuffles; a longer list leaves a span of B / 32 entries to a serial
+// search.
+struct Place {
+    int32_t b, begin, end, len;
+};
+__device__ __forceinline__ Place find_seq(const CacheRef& c, int64_t t, int lane) {
+    const int32_t step = (c.B + 31) / 32, at = lane * step;
+    const int32_t v = at < c.B ? c.starts[at] : 0x7fffffff;
+    const int32_t len = at < c.B ? c.lens[at] : 0;
+    const int32_t last = c.starts[c.B];
     int32_t i = 0;
 #pragma unroll
     for (int w = 16; w > 0; w >>= 1) {
         const int32_t x = __shfl_sync(0xffffffffu, v, i + w);
-        if (x <= t && (i + w) * step < B) i += w;
+        if (x <= t && (i + w) * step < c.B) i += w;
     }
-    int32_t lo = i * step, hi = min(lo + step, B) - 1;
+    Place p;
+    p.b = i;
+    p.begin = __shfl_sync(0xffffffffu, v, i);
+    p.end = __shfl_sync(0xffffffffu, v, (i + 1) & 31);
+    p.len = __shfl_sync(0xffffffffu, len, i);
+    if (step == 1) {
+        if (i + 1 >= c.B) p.end = last;
+        return p;
+    }
+    int32_t lo = i * step, hi = min(lo + step, c.B) - 1;
     while (lo < hi) {
         const int32_t mid = (lo + hi + 1) >> 1;
-        if (starts[mid] <= t) lo = mid; else hi = mid - 1;
+        if (c.starts[mid] <= t) lo = mid; else hi = mid - 1;
     }
-    return lo;
+    p.b = lo;
+    p.begin = c.starts[lo];
+    p.end = c.starts[lo + 1];
+    p.len = c.lens[lo];
+    return p;
+}
+// The same for equal shares.
+__device__ __forceinline__ Place share_of(const CacheRef& c, int64_t t, bool in) {
+    Place p;
+    p.b = (int32_t)(in ? div_floor(t, c.rows_each) : 0);
+    p.begin = (int32_t)(p.b * c.rows_each);
+    p.end = (int32_t)(p.begin + c.rows_each);
+    p.len = c.lens[p.b];
+    return p;
 }
 
-// A row's 8 elements of this lane, as two runs a, b of four.
-struct Eight {
-    float a[4], b[4];
+// Pairs of fp32 values in one register pair: two operations an instruction.
+struct F2 {
+    uint64_t v;
 };
-
-__device__ __forceinline__ Eight unpack(uint2 a, uint2 b) {
-    Eight x;
-    x.a[0] = bf16_lo(a.x); x.a[1] = bf16_hi(a.x); x.a[2] = bf16_lo(a.y); x.a[3] = bf16_hi(a.y);
-    x.b[0] = bf16_lo(b.x); x.b[1] = bf16_hi(b.x); x.b[2] = bf16_lo(b.y); x.b[3] = bf16_hi(b.y);
-    return x;
+__device__ __forceinline__ F2 f2(float x, float y) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void split(F2 a, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v)); }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 unpack2(uint32_t x) { return f2(bf16_lo(x), bf16_hi(x)); }
+__device__ __forceinline__ uint32_t pack2(F2 a) {
+    float x, y;
+    split(a, x, y);
+    return pack_bf16x2(x, y);
 }
 
-__device__ __forceinline__ uint2 pack4(const float (&x)[4]) {
-    return make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-}
-
-__device__ __forceinline__ void load_weight(const void* w, bool f32, int c, float (&out)[4]) {
-    if (f32) {
-        const float2 x = reinterpret_cast<const float2*>(w)[2 * c], y = reinterpret_cast<const float2*>(w)[2 * c + 1];
-        out[0] = x.x; out[1] = x.y; out[2] = y.x; out[3] = y.y;
+// E elements (4 or 8) of bf16 as they lie in memory.
+template <int E>
+struct Run {
+    uint32_t w[E / 2];
+};
+template <int E>
+__device__ __forceinline__ Run<E> load_run(const uint16_t* s) {
+    Run<E> r;
+    if constexpr (E == 8) {
+        const uint4 x = *reinterpret_cast<const uint4*>(s);
+        r.w[0] = x.x; r.w[1] = x.y; r.w[2] = x.z; r.w[3] = x.w;
     } else {
-        const uint2 x = reinterpret_cast<const uint2*>(w)[c];
-        out[0] = bf16_lo(x.x); out[1] = bf16_hi(x.x); out[2] = bf16_lo(x.y); out[3] = bf16_hi(x.y);
+        const uint2 x = *reinterpret_cast<const uint2*>(s);
+        r.w[0] = x.x; r.w[1] = x.y;
+    }
+    return r;
+}
+template <int E>
+__device__ __forceinline__ void store_run(void* d, const uint32_t* w) {
+    if constexpr (E == 8) *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
+    else *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[1]);
+}
+
+template <int E>
+__device__ __forceinline__ void load_weight(const void* w, bool f32, int at, F2 (&out)[E / 2]) {
+    if (f32) {
+        const float2* s = reinterpret_cast<const float2*>(static_cast<const float*>(w) + at);
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) out[e] = f2(s[e].x, s[e].y);
+    } else {
+        const uint32_t* s = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(w) + at);
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) out[e] = unpack2(s[e]);
     }
 }
 
@@ -75,192 +139,405 @@ __device__ __forceinline__ float row_scale(uint32_t amax_bits, float* inv, bool*
     return *keep ? __fdiv_rn(amax, kMax) : amax_bits < kTiny ? 0.f : __uint_as_float(0x7fffffffu);
 }
 
+// Four codes from two pairs.
 template <int FMT>
-__device__ __forceinline__ uint32_t codes4(const float (&x)[4], float inv) {
+__device__ __forceinline__ uint32_t codes4(F2 p, F2 q, F2 inv) {
+    float x[4];
+    split(mul2(p, inv), x[0], x[1]);
+    split(mul2(q, inv), x[2], x[3]);
     if constexpr (FMT == kE4m3) {
-        return pack_e4m3x2(x[0] * inv, x[1] * inv) | (pack_e4m3x2(x[2] * inv, x[3] * inv) << 16);
+        return pack_e4m3x2(x[0], x[1]) | (pack_e4m3x2(x[2], x[3]) << 16);
     } else {
         uint32_t r = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int c = max(-127, min(127, __float2int_rn(x[i] * inv)));
+            const int c = max(-127, min(127, __float2int_rn(x[i])));
             r |= (uint32_t)(c & 0xff) << (8 * i);
         }
         return r;
     }
 }
 
-// Norm, rotation and cache write.  D / 8 lanes share a row; a lane holds two
-// runs of four columns, chosen so that it owns both halves of its four
-// rotation pairs (columns 4l.. and rotary/2 + 4l.. when the pairs are half a
-// rotation apart), so the rotation moves nothing between lanes and a lane
-// reads four cosines and four sines.  A group of lanes takes HC rows of one
-// token: their loads are in flight together, and the token's sequence, block
-// and rotation are looked up once for them.
-template <int D, int FMT, int HC>
-__global__ void __launch_bounds__(kHeadsThreads) heads_kernel(const __grid_constant__ HeadsParams p) {
-    constexpr int TPR = D / 8;
-    const int lane = threadIdx.x & 31, l = threadIdx.x % TPR;
-    const uint32_t gmask = TPR == 32 ? 0xffffffffu : ((1u << TPR) - 1u) << (lane & ~(TPR - 1));
-    const int nq = p.q.p ? p.Hq : 0, nk = p.k.p ? p.Hkv : 0, nv = FMT != kNoCache ? p.Hkv : 0;
-    const int rows = nq + nk + nv;
-    const int chunks = (rows + HC - 1) / HC;
-    const int64_t item = (int64_t)blockIdx.x * (kHeadsThreads / TPR) + threadIdx.x / TPR;
-    pdl_wait_primary();
-    pdl_launch_dependents();
-    const int64_t t = div_floor(item, chunks);
-    const bool in = t < p.T;
-    const int r0 = (int)(item - t * chunks) * HC;
+// ---- norm, rotation and cache write
+//
+// D / (2 E) lanes share a row; a lane holds two runs of E columns, chosen so
+// that it owns both halves of its E rotation pairs (columns E l.. and
+// rotary/2 + E l.. when the pairs are half a rotation apart), so the rotation
+// moves nothing between lanes and a lane reads E cosines and E sines.
+// Arithmetic is on pairs of fp32 values, two to an instruction.
 
-    // columns of the two runs
-    const int rl = p.rotary >> 3;  // lanes that rotate
-    const bool turn = p.cos_sin != nullptr && l < rl;
-    const int c0 = p.interleaved || l >= rl || !p.cos_sin ? 2 * l : l;  // past the rotation: 2 rl + 2 (l - rl)
-    const int c1 = p.interleaved || l >= rl || !p.cos_sin ? c0 + 1 : l + rl;
+// Where a token's keys and values go.
+struct Spot {
+    int64_t off;   // elements into the pools, of kv head 0
+    int32_t blk, slot;
+    bool write;    // false: no such place (flagged)
+};
 
-    uint2 xa[HC], xb[HC];
+template <int D, int FMT, int E>
+struct RowWork {
+    static constexpr int TPR = D / (2 * E), H = E / 2;
+    const HeadsParams& p;
+    int l;               // lane of the row
+    uint32_t gmask;      // the row's lanes
+    bool turn;           // this lane's columns rotate
+    int a_at, b_at;      // first columns of the two runs
+    F2 cs[H], sn[H];
+    const void* weight = nullptr;
+    F2 wa[H], wb[H];     // the norm weights in use
+    F2 a[H], b[H];       // this lane's part of a row
+
+    __device__ __forceinline__ RowWork(const HeadsParams& p_, int thread) : p(p_) {
+        const int lane = thread & 31;
+        l = thread % TPR;
+        gmask = TPR == 32 ? 0xffffffffu : ((1u << TPR) - 1u) << (lane & ~(TPR - 1));
+        const int rl = p.rotary / (2 * E);  // lanes that rotate
+        turn = l < rl;
+        const bool halves = turn && !p.interleaved;
+        a_at = E * (halves ? l : 2 * l);
+        b_at = E * (halves ? l + rl : 2 * l + 1);
+    }
+    // cosines and sines from a row of the table (global or shared memory)
+    __device__ __forceinline__ void load_turn(const float* row) {
+        if (!turn) return;
 #pragma unroll
-    for (int i = 0; i < HC; ++i) {
-        const int r = r0 + i;
-        if (in && r < rows) {
-            const uint16_t* s = r < nq ? p.q.p + t * p.q.tok + r * p.q.head
-                              : r < nq + nk ? p.k.p + t * p.k.tok + (r - nq) * p.k.head
-                                            : p.v.p + t * p.v.tok + (r - nq - nk) * p.v.head;
-            xa[i] = *reinterpret_cast<const uint2*>(s + 4 * c0);
-            xb[i] = *reinterpret_cast<const uint2*>(s + 4 * c1);
+        for (int e = 0; e < E / 4; ++e) {
+            const float4 c = reinterpret_cast<const float4*>(row + E * l)[e];
+            const float4 s = reinterpret_cast<const float4*>(row + E * l + p.rotary / 2)[e];
+            cs[2 * e] = f2(c.x, c.y);
+            cs[2 * e + 1] = f2(c.z, c.w);
+            sn[2 * e] = f2(s.x, s.y);
+            sn[2 * e + 1] = f2(s.z, s.w);
         }
     }
-
-    // the token's place
-    int32_t pos = 0;
-    bool live = in;
-    int64_t slot_off = 0;
-    int32_t blk = 0, slot = 0;
-    bool write = false;
-    if constexpr (FMT != kNoCache) {
-        int32_t b;
-        int64_t end;
-        if (p.c.starts) {
-            b = find_seq(p.c.starts, p.c.B, t, lane);
-            end = p.c.starts[b + 1];
-            live = live && t < end && t >= p.c.starts[0];
-        } else {
-            b = (int32_t)(in ? div_floor(t, p.c.rows_each) : 0);
-            end = (b + 1) * p.c.rows_each;
+    __device__ __forceinline__ void set(const Run<E>& x, const Run<E>& y) {
+#pragma unroll
+        for (int e = 0; e < H; ++e) {
+            a[e] = unpack2(x.w[e]);
+            b[e] = unpack2(y.w[e]);
         }
-        const int64_t at = (int64_t)p.c.lens[b] - end + t;
-        live = live && at >= 0;
-        pos = (int32_t)at;
-        const int64_t j = at >> p.c.lbs;
-        slot = pos & ((1 << p.c.lbs) - 1);
-        if (live && r0 + HC > nq) {
-            bool bad = j >= p.c.table_stride;
-            if (bad) {
-                if (l == 0) atomicOr(p.err, PDA_DEVERR_BAD_POSITION_);
-            } else {
-                blk = p.c.table[(int64_t)b * p.c.table_stride + j];
-                bad = blk < 0 || blk >= p.c.num_blocks;
-                if (bad && l == 0) atomicOr(p.err, PDA_DEVERR_BAD_BLOCK_ID_);
+    }
+    __device__ __forceinline__ void prepare(const void* w) {
+        if (w) {
+            if (weight != w) {
+                load_weight<E>(w, p.weights_f32 != 0, a_at, wa);
+                load_weight<E>(w, p.weights_f32 != 0, b_at, wb);
+                weight = w;
             }
-            write = !bad;
-            slot_off = (int64_t)blk * p.c.blk + (int64_t)slot * p.c.tok;
-        }
-    }
-    if (!live) return;
-    float cs[4], sn[4];
-    if (p.cos_sin) {
-        if (p.positions) pos = p.positions[t];
-        if (pos < 0 || pos >= p.max_pos) {
-            if (l == 0) atomicOr(p.err, PDA_DEVERR_BAD_POSITION_);
-            pos = pos < 0 ? 0 : p.max_pos - 1;
-        }
-        if (turn) {
-            const float* row = p.cos_sin + (int64_t)pos * p.rotary + 4 * l;
-            const float4 c = *reinterpret_cast<const float4*>(row);
-            const float4 s = *reinterpret_cast<const float4*>(row + p.rotary / 2);
-            cs[0] = c.x; cs[1] = c.y; cs[2] = c.z; cs[3] = c.w;
-            sn[0] = s.x; sn[1] = s.y; sn[2] = s.z; sn[3] = s.w;
-        }
-    }
-    // `x`: this lane's part of a q or k head
-    auto prepare = [&](Eight& x, const void* weight) {
-        if (weight) {
-            float ss = 0.f;
+            F2 sq = f2(0.f, 0.f);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) ss += x.a[e] * x.a[e] + x.b[e] * x.b[e];
+            for (int e = 0; e < H; ++e) sq = fma2(b[e], b[e], fma2(a[e], a[e], sq));
+            float s0, s1;
+            split(sq, s0, s1);
+            float ss = s0 + s1;
 #pragma unroll
             for (int o = 1; o < TPR; o <<= 1) ss += __shfl_xor_sync(gmask, ss, o);
             const float inv = rsqrtf(ss * (1.f / D) + p.eps);
-            float wa[4], wb[4];
-            load_weight(weight, p.weights_f32 != 0, c0, wa);
-            load_weight(weight, p.weights_f32 != 0, c1, wb);
+            const F2 i2 = f2(inv, inv);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x.a[e] = x.a[e] * inv * wa[e];
-                x.b[e] = x.b[e] * inv * wb[e];
+            for (int e = 0; e < H; ++e) {
+                a[e] = mul2(mul2(a[e], i2), wa[e]);
+                b[e] = mul2(mul2(b[e], i2), wb[e]);
             }
         }
         if (!turn) return;
+        const F2 minus = f2(-1.f, -1.f);
         if (p.interleaved) {
+            // pairs lie side by side: gather two of them into (evens, odds)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float& u = e < 2 ? x.a[2 * e] : x.b[2 * e - 4];
-                float& w = e < 2 ? x.a[2 * e + 1] : x.b[2 * e - 3];
-                const float y = u * cs[e] - w * sn[e];
-                w = w * cs[e] + u * sn[e];
-                u = y;
+            for (int e = 0; e < H; ++e) {
+                F2& u = 2 * e < H ? a[2 * e] : b[2 * e - H];
+                F2& v = 2 * e + 1 < H ? a[2 * e + 1] : b[2 * e + 1 - H];
+                float u0, u1, v0, v1;
+                split(u, u0, u1);
+                split(v, v0, v1);
+                const F2 x = f2(u0, v0), y = f2(u1, v1);
+                const F2 nx = fma2(mul2(y, sn[e]), minus, mul2(x, cs[e])), ny = fma2(x, sn[e], mul2(y, cs[e]));
+                float x0, x1, y0, y1;
+                split(nx, x0, x1);
+                split(ny, y0, y1);
+                u = f2(x0, y0);
+                v = f2(x1, y1);
             }
         } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float y = x.a[e] * cs[e] - x.b[e] * sn[e];
-                x.b[e] = x.b[e] * cs[e] + x.a[e] * sn[e];
-                x.a[e] = y;
+            for (int e = 0; e < H; ++e) {
+                const F2 x = a[e];
+                a[e] = fma2(mul2(b[e], sn[e]), minus, mul2(x, cs[e]));
+                b[e] = fma2(x, sn[e], mul2(b[e], cs[e]));
             }
         }
-    };
-    auto put_heads = [&](const Heads& h, int64_t head, const Eight& x) {
-        uint16_t* d = h.p + t * h.tok + head * h.head;
-        *reinterpret_cast<uint2*>(d + 4 * c0) = pack4(x.a);
-        *reinterpret_cast<uint2*>(d + 4 * c1) = pack4(x.b);
-    };
-    // a K (which 0) or V (which 1) row of kv head `h` into its slot
-    auto put_cache = [&](int which, int h, const Eight& x) {
+    }
+    __device__ __forceinline__ void put16(uint16_t* d) const {
+        uint32_t w[H];
+#pragma unroll
+        for (int e = 0; e < H; ++e) w[e] = pack2(a[e]);
+        store_run<E>(d + a_at, w);
+#pragma unroll
+        for (int e = 0; e < H; ++e) w[e] = pack2(b[e]);
+        store_run<E>(d + b_at, w);
+    }
+    // a K (which 0) or V (which 1) row of kv head h into its slot
+    __device__ __forceinline__ void put_cache(int which, int h, const Spot& at) const {
         if constexpr (FMT == kBf16) {
-            uint16_t* d = reinterpret_cast<uint16_t*>(which ? p.c.v : p.c.k) + slot_off + (int64_t)h * p.c.kvh;
-            *reinterpret_cast<uint2*>(d + 4 * c0) = pack4(x.a);
-            *reinterpret_cast<uint2*>(d + 4 * c1) = pack4(x.b);
+            put16(reinterpret_cast<uint16_t*>(which ? p.c.v : p.c.k) + at.off + (int64_t)h * p.c.kvh);
         } else if constexpr (FMT != kNoCache) {
             uint32_t top = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                top = max(top, max(__float_as_uint(x.a[e]) & 0x7fffffffu, __float_as_uint(x.b[e]) & 0x7fffffffu));
+            for (int e = 0; e < H; ++e) {
+                float x, y;
+                split(a[e], x, y);
+                top = max(top, max(__float_as_uint(x) & 0x7fffffffu, __float_as_uint(y) & 0x7fffffffu));
+                split(b[e], x, y);
+                top = max(top, max(__float_as_uint(x) & 0x7fffffffu, __float_as_uint(y) & 0x7fffffffu));
+            }
 #pragma unroll
             for (int o = 1; o < TPR; o <<= 1) top = max(top, __shfl_xor_sync(gmask, top, o));
             float inv;
             bool keep;
             const float scale = row_scale<FMT>(top, &inv, &keep);
-            uint8_t* d = (which ? p.c.v : p.c.k) + slot_off + (int64_t)h * p.c.kvh;
-            *reinterpret_cast<uint32_t*>(d + 4 * c0) = keep ? codes4<FMT>(x.a, inv) : 0u;
-            *reinterpret_cast<uint32_t*>(d + 4 * c1) = keep ? codes4<FMT>(x.b, inv) : 0u;
-            if (l == 0) p.c.scales[((((int64_t)blk * p.Hkv + h) * 2 + which) << p.c.lbs) + slot] = scale;
-        }
-    };
+            const F2 i2 = f2(inv, inv);
+            uint8_t* d = (which ? p.c.v : p.c.k) + at.off + (int64_t)h * p.c.kvh;
+            uint32_t ca[E / 4], cb[E / 4];
 #pragma unroll
-    for (int i = 0; i < HC; ++i) {
-        const int r = r0 + i;
-        if (r >= rows) break;
-        Eight x = unpack(xa[i], xb[i]);
-        if (r < nq) {
-            prepare(x, p.q_weight);
-            put_heads(p.q_out, r, x);
-        } else if (r < nq + nk) {
-            prepare(x, p.k_weight);
-            if constexpr (FMT == kNoCache) put_heads(p.k_out, r - nq, x);
-            else if (write) put_cache(0, r - nq, x);
-        } else {
-            if (write) put_cache(1, r - nq - nk, x);
+            for (int e = 0; e < E / 4; ++e) {
+                ca[e] = keep ? codes4<FMT>(a[2 * e], a[2 * e + 1], i2) : 0u;
+                cb[e] = keep ? codes4<FMT>(b[2 * e], b[2 * e + 1], i2) : 0u;
+            }
+            if constexpr (E == 8) {
+                *reinterpret_cast<uint2*>(d + a_at) = make_uint2(ca[0], ca[1]);
+                *reinterpret_cast<uint2*>(d + b_at) = make_uint2(cb[0], cb[1]);
+            } else {
+                *reinterpret_cast<uint32_t*>(d + a_at) = ca[0];
+                *reinterpret_cast<uint32_t*>(d + b_at) = cb[0];
+            }
+            if (l == 0) p.c.scales[((((int64_t)at.blk * p.Hkv + h) * 2 + which) << p.c.lbs) + at.slot] = scale;
         }
+    }
+    // row r of token t (its elements set) to where it goes
+    __device__ __forceinline__ void finish(int64_t t, int r, int nq, int nk, const Spot& at) {
+        if (r < nq) {
+            prepare(p.q_weight);
+            put16(p.q_out.p + t * p.q_out.tok + r * p.q_out.head);
+        } else if (r < nq + nk) {
+            prepare(p.k_weight);
+            if constexpr (FMT == kNoCache) put16(p.k_out.p + t * p.k_out.tok + (r - nq) * p.k_out.head);
+            else if (at.write) put_cache(0, r - nq, at);
+        } else {
+            if (at.write) put_cache(1, r - nq - nk, at);
+        }
+    }
+};
+
+// A new token's index in its sequence (negative: padding) and its spot, given
+// its place in the batch.  `flag`: this thread reports what is wrong.
+__device__ __forceinline__ Spot spot_of(const HeadsParams& p, const Place& at, int64_t idx, bool flag) {
+    Spot s = {0, 0, (int32_t)idx & ((1 << p.c.lbs) - 1), false};
+    const int64_t j = idx >> p.c.lbs;
+    if (j >= p.c.table_stride) {
+        if (flag) atomicOr(p.err, PDA_DEVERR_BAD_POSITION_);
+        return s;
+    }
+    s.blk = p.c.table[(int64_t)at.b * p.c.table_stride + j];
+    s.write = s.blk >= 0 && s.blk < p.c.num_blocks;
+    if (!s.write && flag) atomicOr(p.err, PDA_DEVERR_BAD_BLOCK_ID_);
+    s.off = (int64_t)s.blk * p.c.blk + (int64_t)s.slot * p.c.tok;
+    return s;
+}
+// The rotation row of token t at index idx of its sequence.
+__device__ __forceinline__ int32_t turn_row(const HeadsParams& p, int64_t t, int64_t idx, bool flag) {
+    int64_t pos = p.positions ? p.positions[t] : idx;
+    if (pos < 0 || pos >= p.max_pos) {
+        if (flag) atomicOr(p.err, PDA_DEVERR_BAD_POSITION_);
+        pos = pos < 0 ? 0 : p.max_pos - 1;
+    }
+    return (int32_t)pos;
+}
+
+// Few tokens, or any alignment: a group of lanes takes kRows rows of one token
+// straight from memory.  Latency counts (loads of the rows go out before the
+// token's place is looked up), and many small groups hide it better than few
+// with more rows each: a 32-token step of 48 rows takes 3.7 us with two rows a
+// group, 4.8 with four.
+constexpr int kRows = 2;
+template <int D, int FMT>
+__global__ void __launch_bounds__(kHeadsThreads, 4) heads_kernel(const __grid_constant__ HeadsParams p) {
+    constexpr int E = 4;
+    using Work = RowWork<D, FMT, E>;
+    const int nq = p.q.p ? p.Hq : 0, nk = p.k.p ? p.Hkv : 0, nv = FMT != kNoCache ? p.Hkv : 0;
+    const int rows = nq + nk + nv, spans = (rows + kRows - 1) / kRows;
+    const int64_t item = (int64_t)blockIdx.x * (kHeadsThreads / Work::TPR) + threadIdx.x / Work::TPR;
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    const int64_t t = div_floor(item, spans);
+    const bool in = t < p.T;
+    const int first = (int)(item - t * spans) * kRows, last = min(first + kRows, rows);
+    Work work(p, threadIdx.x);
+    Run<E> xa[kRows], xb[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int r = first + i;
+        if (in && r < last) {
+            const uint16_t* s = r < nq ? p.q.p + t * p.q.tok + r * p.q.head
+                              : r < nq + nk ? p.k.p + t * p.k.tok + (r - nq) * p.k.head
+                                            : p.v.p + t * p.v.tok + (r - nq - nk) * p.v.head;
+            xa[i] = load_run<E>(s + work.a_at);
+            xb[i] = load_run<E>(s + work.b_at);
+        }
+    }
+    bool live = in;
+    int64_t idx = 0;
+    Spot at = {0, 0, 0, false};
+    if constexpr (FMT != kNoCache) {
+        const Place place = p.c.starts ? find_seq(p.c, t, threadIdx.x & 31) : share_of(p.c, t, in);
+        idx = (int64_t)place.len - place.end + t;
+        live = live && t < place.end && t >= place.begin && idx >= 0;
+        if (live && last > nq) at = spot_of(p, place, idx, work.l == 0);
+    }
+    if (!live) return;
+    if (p.cos_sin) work.load_turn(p.cos_sin + (int64_t)turn_row(p, t, idx, work.l == 0) * p.rotary);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        if (first + i >= last) break;
+        work.set(xa[i], xb[i]);
+        work.finish(t, first + i, nq, nk, at);
+    }
+}
+
+// Many tokens: one persistent CTA per SM streams them through a ring of
+// shared-memory slots, a token's rows (and its row of cosines and sines) to a
+// slot.  A producer warp looks 32 tokens up at a time and issues their bulk
+// copies, kTeams teams of kTeamWarps warps take the slots in turn and write
+// straight to memory.  The copies in flight (the ring less the slots being
+// worked on, 100 KB and more a SM) do not depend on occupancy; loading rows to
+// registers instead, with 32 warps an SM, came to 3.9 TB/s on 8191 tokens of
+// 72 heads of 128 and no arrangement of rows per thread passed it.
+//
+// A slot belongs to one team (slots are a multiple of the teams at work): the
+// team that waits for a slot's next token has itself seen the previous one
+// land.  Copies land in any order, so another team could be a whole turn of
+// the slot ahead and take the barrier's older phase for the one it waits for.
+constexpr int kTeams = 5, kTeamWarps = 3, kMaxSlots = 20;
+constexpr int kRingThreads = (kTeams * kTeamWarps + 1) * 32;
+struct SlotMeta {
+    Spot at;
+    int32_t t;  // -1: padding
+};
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kRingThreads) heads_ring_kernel(const __grid_constant__ HeadsParams p) {
+    constexpr int E = 8;
+    using Work = RowWork<D, FMT, E>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t bars[2 * kMaxSlots];
+    __shared__ SlotMeta meta[kMaxSlots];
+    __shared__ int abort_flag;
+    const uint32_t ring = (smem_u32(smem_raw) + 127u) & ~127u;
+    const uint8_t* ring_p = smem_raw + (ring - smem_u32(smem_raw));
+    const uint32_t bars0 = smem_u32(bars);
+    const int nq = p.q.p ? p.Hq : 0, nk = p.k.p ? p.Hkv : 0, nv = FMT != kNoCache ? p.Hkv : 0;
+    const int rows = nq + nk + nv, S = p.slots;
+    const uint32_t turn_bytes = (uint32_t)p.rotary * 4u, slot_bytes = (uint32_t)rows * (2u * D) + turn_bytes;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(bars0 + 8 * s, 1);
+            mbar_init(bars0 + 8 * (S + s), kTeamWarps);
+        }
+        fence_mbar_init();
+        abort_flag = 0;
+    }
+    __syncthreads();
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    const int32_t n = (int32_t)((p.T - blockIdx.x + gridDim.x - 1) / gridDim.x);  // tokens blockIdx.x, + gridDim.x, ..
+    if (warp == kTeams * kTeamWarps) {
+        // side by side (one fused projection's output): one copy brings all of a token
+        const bool joined = nq && nk && p.k.p == p.q.p + nq * D && p.k.tok == p.q.tok &&
+                            (!nv || (p.v.p == p.k.p + nk * D && p.v.tok == p.q.tok));
+        for (int32_t i0 = 0; i0 < n; i0 += 32) {
+            // lane i: token i0 + i
+            const int32_t mine = i0 + lane;
+            const int64_t t = (int64_t)blockIdx.x + (int64_t)mine * gridDim.x;
+            bool live = mine < n;
+            int64_t idx = 0;
+            Spot at = {0, 0, 0, false};
+            if constexpr (FMT != kNoCache) {
+                const Place place = p.c.starts ? find_seq(p.c, t, lane) : share_of(p.c, t, live);
+                idx = (int64_t)place.len - place.end + t;
+                live = live && t < place.end && t >= place.begin && idx >= 0;
+                if (live) at = spot_of(p, place, idx, true);
+            }
+            const int32_t turn = live && p.rotary ? turn_row(p, t, idx, true) : 0;
+            for (int i = 0; i < 32 && i0 + i < n; ++i) {
+                const int s = (i0 + i) % S;
+                int stop = 0;
+                if (lane == i) {
+                    const uint32_t full = bars0 + 8 * s;
+                    if (*(volatile int*)&abort_flag ||
+                        !mbar_wait_bounded(bars0 + 8 * (S + s), (((i0 + i) / S) & 1) ^ 1, kWaitLimitNs)) {
+                        stop = 1;
+                    } else {
+                        meta[s].at = at;
+                        meta[s].t = live ? (int32_t)t : -1;
+                        const uint32_t dst = ring + (uint32_t)s * slot_bytes;
+                        mbar_arrive_expect_tx(full, live ? slot_bytes : 0u);
+                        if (live) {
+                            uint32_t to = dst;
+                            if (joined) {
+                                bulk_load(to, p.q.p + t * p.q.tok, (uint32_t)(rows * 2 * D), full);
+                            } else {
+                                if (nq) bulk_load(to, p.q.p + t * p.q.tok, (uint32_t)(nq * 2 * D), full);
+                                to += (uint32_t)(nq * 2 * D);
+                                if (nk) bulk_load(to, p.k.p + t * p.k.tok, (uint32_t)(nk * 2 * D), full);
+                                to += (uint32_t)(nk * 2 * D);
+                                if (nv) bulk_load(to, p.v.p + t * p.v.tok, (uint32_t)(nv * 2 * D), full);
+                            }
+                            if (turn_bytes)
+                                bulk_load(dst + (uint32_t)(rows * 2 * D), p.cos_sin + (int64_t)turn * p.rotary, turn_bytes,
+                                          full);
+                        }
+                    }
+                }
+                if (__any_sync(0xffffffffu, stop)) {
+                    // a wait ran out: report it, and leave once the copies issued have landed
+                    if (lane == 0) {
+                        atomicOr(p.err, PDA_DEVERR_TIMEOUT_);
+                        abort_flag = 1;
+                        for (int32_t k = max(0, i0 + i - S); k < i0 + i; ++k)
+                            mbar_wait_bounded(bars0 + 8 * (k % S), (k / S) & 1, kWaitLimitNs);
+                    }
+                    return;
+                }
+            }
+        }
+        return;
+    }
+    const int team = warp / kTeamWarps, member = warp % kTeamWarps;
+    constexpr int G = 32 / Work::TPR;  // rows a warp takes at once
+    Work work(p, threadIdx.x);
+    const int teams = min(kTeams, S);
+    if (team >= teams) return;
+    for (int32_t i = team; i < n; i += teams) {
+        const int s = i % S;
+        if (!mbar_wait_bounded(bars0 + 8 * s, (i / S) & 1, kWaitLimitNs)) {
+            if (lane == 0) {
+                atomicOr(p.err, PDA_DEVERR_TIMEOUT_);
+                *(volatile int*)&abort_flag = 1;
+            }
+            return;
+        }
+        const SlotMeta m = meta[s];
+        if (m.t >= 0) {
+            const uint8_t* slot = ring_p + (size_t)s * slot_bytes;
+            if (p.rotary) work.load_turn(reinterpret_cast<const float*>(slot + (size_t)rows * 2 * D));
+            for (int r = member * G + lane / Work::TPR; r < rows; r += kTeamWarps * G) {
+                const uint16_t* x = reinterpret_cast<const uint16_t*>(slot) + r * D;
+                work.set(load_run<E>(x + work.a_at), load_run<E>(x + work.b_at));
+                work.finish(m.t, r, nq, nk, m.at);
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars0 + 8 * (S + s));
     }
 }
 
@@ -278,19 +555,10 @@ __global__ void __launch_bounds__(kHeadsThreads) read_kernel(const __grid_consta
     const int64_t t = div_floor(item, chunks);
     const int r0 = (int)(item - t * chunks) * HC;
     bool live = t < p.rows;
-    int32_t b;
-    int64_t begin, end;
-    if (p.c.starts) {
-        b = find_seq(p.c.starts, p.c.B, t, lane);
-        begin = p.c.starts[b];
-        end = p.c.starts[b + 1];
-    } else {
-        b = (int32_t)(live ? div_floor(t, p.c.rows_each) : 0);
-        begin = b * p.c.rows_each;
-        end = begin + p.c.rows_each;
-    }
-    const int64_t at = t - begin;
-    live = live && at >= 0 && t < end && at < p.c.lens[b];
+    const Place place = p.c.starts ? find_seq(p.c, t, lane) : share_of(p.c, t, live);
+    const int32_t b = place.b;
+    const int64_t at = t - place.begin;
+    live = live && at >= 0 && t < place.end && at < place.len;
     if (!live) return;
     const int64_t j = at >> p.c.lbs;
     const int slot = (int)at & ((1 << p.c.lbs) - 1);
@@ -370,14 +638,14 @@ __global__ void __launch_bounds__(kHeadsThreads) read_kernel(const __grid_consta
 
 namespace {
 
-// `items` groups of D / per_lane lanes.
 template <typename P>
-cudaError_t launch_rows(void (*kernel)(const P), const P& p, int64_t items, int lanes, cudaStream_t stream) {
-    const int64_t grid = (items * lanes + kHeadsThreads - 1) / kHeadsThreads;
+cudaError_t launch_grid(void (*kernel)(const P), const P& p, int64_t grid, int threads, size_t smem,
+                        cudaStream_t stream) {
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid, 1, 1);
-    cfg.blockDim = dim3(kHeadsThreads, 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -387,11 +655,47 @@ cudaError_t launch_rows(void (*kernel)(const P), const P& p, int64_t items, int 
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// `items` groups of `lanes` lanes.
+template <typename P>
+cudaError_t launch_rows(void (*kernel)(const P), const P& p, int64_t items, int lanes, cudaStream_t stream) {
+    return launch_grid(kernel, p, (items * lanes + kHeadsThreads - 1) / kHeadsThreads, kHeadsThreads, 0, stream);
+}
+
+// A token's heads as one bulk copy: side by side, on 16-byte boundaries.
+bool one_copy(const Heads& h, int D) {
+    return !h.p || (h.head == D && h.tok % 8 == 0 && reinterpret_cast<uintptr_t>(h.p) % 16 == 0);
+}
+bool runs_of_8(const Heads& h) {
+    return !h.p || (h.tok % 8 == 0 && h.head % 8 == 0 && reinterpret_cast<uintptr_t>(h.p) % 16 == 0);
+}
+
+constexpr int kRingBytes = 200 * 1024;  // of an SM's 227 KB
+constexpr int kRingTokens = 1024;       // tokens from which the ring pays (see launch_heads_of)
+
 template <int D, int FMT>
-cudaError_t launch_heads_of(const HeadsParams& p, cudaStream_t stream) {
+cudaError_t launch_heads_of(HeadsParams p, cudaStream_t stream) {
     const int rows = (p.q.p ? p.Hq : 0) + (p.k.p ? p.Hkv : 0) + (FMT != kNoCache ? p.Hkv : 0);
-    constexpr int HC = 4;
-    return launch_rows(heads_kernel<D, FMT, HC>, p, p.T * ((rows + HC - 1) / HC), D / 8, stream);
+    const int slot = rows * 2 * D + p.rotary * 4;
+    p.slots = kRingBytes / slot < kMaxSlots ? kRingBytes / slot : kMaxSlots;
+    if (p.slots > kTeams) p.slots -= p.slots % kTeams;
+    if (p.T >= kRingTokens && p.slots >= 4 && p.rotary % 16 == 0 && one_copy(p.q, D) && one_copy(p.k, D) &&
+        one_copy(p.v, D) && runs_of_8(p.q_out) && runs_of_8(p.k_out)) {
+        return launch_grid(heads_ring_kernel<D, FMT>, p, p.sms, kRingThreads, (size_t)p.slots * slot + 128, stream);
+    }
+    return launch_rows(heads_kernel<D, FMT>, p, p.T * ((rows + kRows - 1) / kRows), D / 8, stream);
+}
+
+template <int D, int FMT>
+cudaError_t ring_attributes() {
+    return cudaFuncSetAttribute(heads_ring_kernel<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes + 128);
+}
+template <int D>
+cudaError_t heads_setup_of() {
+    cudaError_t e = ring_attributes<D, kNoCache>();
+    if (e == cudaSuccess) e = ring_attributes<D, kBf16>();
+    if (e == cudaSuccess) e = ring_attributes<D, kE4m3>();
+    if (e == cudaSuccess) e = ring_attributes<D, kInt8>();
+    return e;
 }
 
 template <int D>
@@ -425,6 +729,10 @@ cudaError_t launch_read_fmt(int format, bool f32, const ReadParams& p, cudaStrea
 }
 
 }  // namespace
+
+cudaError_t heads_setup(int D) {
+    return D == 64 ? heads_setup_of<64>() : D == 128 ? heads_setup_of<128>() : heads_setup_of<256>();
+}
 
 cudaError_t launch_heads(int D, int format, const HeadsParams& p, cudaStream_t stream) {
     switch (D) {

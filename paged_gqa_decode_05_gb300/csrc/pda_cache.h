@@ -45,6 +45,8 @@ struct HeadsParams {
     int32_t weights_f32;
     float eps;
     int32_t max_pos, rotary, interleaved;
+    int32_t sms;
+    int32_t slots;            // of the ring (set at launch)
     uint32_t* err;
 };
 
@@ -57,6 +59,8 @@ struct ReadParams {
     uint32_t* err;
 };
 
+// Launch attributes for a head size on the current device.
+cudaError_t heads_setup(int D);
 // format kNoCache: norm_rope (outputs q_out, k_out); otherwise append.
 cudaError_t launch_heads(int D, int format, const HeadsParams& p, cudaStream_t stream);
 cudaError_t launch_read(int D, int format, bool out_f32, const ReadParams& p, cudaStream_t stream);

@@ -272,6 +272,7 @@ pda_status run_quant(pda_ctx* ctx, const pda_bf16* q, const pda_cache* c, const 
 
 pda_status pda::quant_setup(pda_ctx* ctx, int optin) {
     const int D = ctx->dims.head_dim;
+    if (const cudaError_t e = heads_setup(D); e != cudaSuccess) return cuda_fail(e, "norm_rope / append attributes");
     for (int tiles = 1; tiles <= 2; ++tiles) {
         int per_sm = 1 << 30;
         for (int format : {PDA_CACHE_E4M3, PDA_CACHE_INT8})
@@ -323,6 +324,7 @@ PDA_EXPORT pda_status pda_norm_rope(pda_ctx* ctx, const pda_heads* q, const pda_
     p.Hq = ctx->dims.num_q_heads;
     p.Hkv = ctx->dims.num_kv_heads;
     p.err = ctx->err;
+    p.sms = ctx->num_sms;
     DeviceGuard on(ctx->device);
     ctx->tile_steps = 0;
     const cudaError_t e = pda::launch_heads(ctx->dims.head_dim, pda::kNoCache, p, (cudaStream_t)stream);
@@ -357,6 +359,7 @@ PDA_EXPORT pda_status pda_append(pda_ctx* ctx, const pda_heads* k, const pda_hea
     p.Hq = ctx->dims.num_q_heads;
     p.Hkv = ctx->dims.num_kv_heads;
     p.err = ctx->err;
+    p.sms = ctx->num_sms;
     DeviceGuard on(ctx->device);
     ctx->tile_steps = 0;  // a following tile step reads what this writes: it must wait
     const cudaError_t e = pda::launch_heads(ctx->dims.head_dim, cache->format, p, (cudaStream_t)stream);

@@ -45,7 +45,9 @@ def qkv_of(g, tokens, hq, hkv, d):
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("hq,hkv,d,rotary,tokens", [
     (4, 2, 64, 64, 1), (32, 8, 128, 128, 33), (5, 1, 128, 64, 257), (16, 4, 256, 256, 7), (3, 3, 64, 8, 100),
-    (8, 8, 256, 24, 65), (64, 8, 128, 120, 19)])
+    (8, 8, 256, 24, 65), (64, 8, 128, 120, 19),
+    # enough tokens for the streaming form, and (rotary 24) for the other at that size
+    (32, 8, 128, 128, 1500), (4, 2, 64, 32, 1111), (16, 4, 256, 128, 1024), (2, 1, 64, 24, 1300)])
 def test_norm_rope(hq, hkv, d, rotary, tokens, interleaved):
     g = gen(tokens)
     ctx = ctx_of(hq, hkv, d, 16)
@@ -155,6 +157,68 @@ def test_append(dtype, hq, hkv, d, bs, lens, news):
         want_s[blk, :, 1, slot] = scale[row]
     assert torch.equal(vc.view(torch.uint8), want_v.view(torch.uint8))
     assert torch.equal(ss[:, :, 1], want_s[:, :, 1])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16] + ref.FORMATS)
+@pytest.mark.parametrize("hq,hkv,d,bs,rotary", [(32, 8, 128, 16, 128), (4, 4, 64, 32, 16), (2, 1, 256, 64, 0), (5, 1, 64, 1, 64)])
+def test_append_prompts(dtype, hq, hkv, d, bs, rotary):
+    """Prompts of a prefill batch, streamed: empty sequences, a block that does not exist, a table too narrow, padding
+    behind the last sequence; and the same bits as the tokens appended a few at a time."""
+    g, rng = gen(31), np.random.default_rng(31)
+    lens = [600, 0, 1, 411, 0, 37, 250]
+    table, pool = ref.sequences(rng, lens, bs)
+    bad = table.clone()
+    bad[5, 0] = pool + 4  # sequence 5's first block
+    width = -(-411 // bs)  # sequence 0 does not fit
+    bad = bad[:, :width].contiguous()
+    total = sum(lens)
+    starts = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32)
+    qkv = qkv_of(g, total + 70, hq, hkv, d)
+    ctx = ctx_of(hq, hkv, d, bs)
+    wq, wk = ((1 + 0.1 * torch.randn(d, generator=g)).bfloat16().cuda() for _ in range(2))
+    cs = pda.rope_table(600, rotary) if rotary else None
+    prep = dict(q_weight=wq, k_weight=wk, cos_sin=cs)
+    caches = [ctx.new_cache(pool, dtype) for _ in range(2)]
+    outs = [torch.full((total + 70, hq, d), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+    lens_d = torch.tensor(lens, dtype=torch.int32).cuda()
+    kp, vp, sc = caches[0]
+    ctx.append(k, v, kp, vp, bad.cuda(), lens_d, scales=sc, starts=starts.cuda(), q=q, q_out=outs[0], **prep)
+    assert ctx.read_device_errors() == pda.DEVERR_BAD_POSITION | pda.DEVERR_BAD_BLOCK_ID
+    assert (outs[0][total:] == 3).all()
+    kp, vp, sc = caches[1]
+    for b, n in enumerate(lens):  # one sequence at a time, 500 tokens at most: the other form of the kernel
+        for at in range(0, n, 500):
+            m, lo = min(500, n - at), int(starts[b]) + at
+            rows = slice(lo, lo + m)
+            ctx.append(k[rows], v[rows], kp, vp, bad[b:b + 1].cuda(), torch.tensor([at + m], dtype=torch.int32).cuda(),
+                       scales=sc, q=q[rows], q_out=outs[1][rows], **prep)
+    assert ctx.read_device_errors() == pda.DEVERR_BAD_POSITION | pda.DEVERR_BAD_BLOCK_ID
+    # the sum of squares is taken in another order: a bf16 or code step apart here and there
+    assert (outs[0].float() - outs[1].float()).abs().max() <= 2.0 ** -7 * outs[1].float().abs().max()
+    for x, y in zip(caches[0][:2], caches[1][:2]):
+        x, y = x.float(), y.float()
+        assert torch.equal(x.abs().sum((2, 3)) > 0, y.abs().sum((2, 3)) > 0)
+        assert (x != y).float().mean() < 1e-3
+    assert torch.equal(caches[0][1].view(torch.uint8), caches[1][1].view(torch.uint8))
+    # against the definition, where everything is in place
+    kp, vp, sc = ctx.new_cache(pool, dtype)
+    before = kp.cpu()
+    out = ctx.append(k, v, kp, vp, table.cuda(), lens_d, scales=sc, starts=starts.cuda(), q=q, **prep)
+    assert ctx.read_device_errors() == 0
+    places = ref.place(table, lens, starts, bs)
+    pos = torch.zeros(total, dtype=torch.int64)
+    for _, at, _, _, row in places:
+        pos[row] = at
+    want, size = ref.norm_rope64(q[:total], wq, cos_sin=cs, positions=pos)
+    within(out[:total], want, BF16 * want.abs() + 2.0 ** -20 * size)
+    want, size = ref.norm_rope64(k[:total], wk, cos_sin=cs, positions=pos)
+    if dtype == torch.bfloat16:
+        got = torch.stack([kp[blk, slot] for _, _, blk, slot, _ in places])
+        rows = torch.tensor([row for *_, row in places])
+        within(got, want[rows], BF16 * want[rows].abs() + 2.0 ** -20 * size[rows])
+    else:
+        check_written(kp.cpu(), sc.cpu(), 0, before, want, size, places, bs)
 
 
 @pytest.mark.parametrize("dtype", ref.FORMATS)
