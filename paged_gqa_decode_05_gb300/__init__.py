@@ -245,6 +245,7 @@ class Context:
         self.dims = _dims(max_seqs, num_q_heads, num_kv_heads, head_dim, block_size, tile_capacity)
         self.device = torch.device("cuda", torch.cuda.current_device() if device is None
                                    else torch.device(device).index or 0)
+        self._index = self.device.index
         self._ctx = ctypes.c_void_p()
         with torch.cuda.device(self.device):
             _check(lib().pda_create(ctypes.byref(self.dims), ctypes.byref(self._ctx)))
@@ -330,34 +331,34 @@ class Context:
         """The pda_cache of pools of any format; 8-bit pools come with their scales."""
         torch = _torch()
         d = self.dims
-        formats = {torch.bfloat16: CACHE_BF16, torch.float8_e4m3fn: CACHE_E4M3, torch.int8: CACHE_INT8}
-        fmt = formats.get(k_pool.dtype)
-        if fmt is None or v_pool.dtype != k_pool.dtype:
+        dtype = k_pool.dtype
+        fmt = CACHE_E4M3 if dtype is torch.float8_e4m3fn else CACHE_INT8 if dtype is torch.int8 else \
+            CACHE_BF16 if dtype is torch.bfloat16 else None
+        if fmt is None or v_pool.dtype is not dtype:
             raise ValueError("k_pool / v_pool must both be bfloat16, float8_e4m3fn or int8")
         self._here(k_pool, "k_pool")
         self._here(v_pool, "v_pool")
+        bs, hkv, hd = d.block_size, d.num_kv_heads, d.head_dim
         if strides is None:
-            shape = (k_pool.shape[0], d.block_size, d.num_kv_heads, d.head_dim)
-            for t, name in ((k_pool, "k_pool"), (v_pool, "v_pool")):
-                if tuple(t.shape) != shape or not t.is_contiguous():
-                    raise ValueError(f"{name} must be contiguous [num_blocks, {shape[1]}, {shape[2]}, {shape[3]}]")
-            num_blocks = shape[0]
-            strides = (shape[1] * shape[2] * shape[3], shape[2] * shape[3], shape[3])
+            num_blocks = k_pool.size(0)
+            shape = (num_blocks, bs, hkv, hd)
+            if k_pool.shape != shape or v_pool.shape != shape or not k_pool.is_contiguous() or not v_pool.is_contiguous():
+                raise ValueError(f"k_pool / v_pool must be contiguous [num_blocks, {bs}, {hkv}, {hd}], alike")
+            strides = (bs * hkv * hd, hkv * hd, hd)
         elif num_blocks is None:
             raise ValueError("num_blocks is required with explicit strides")
         if fmt == CACHE_BF16:
             if scales is not None:
                 raise ValueError("a bfloat16 cache has no scales")
         else:
-            shape = (int(num_blocks), d.num_kv_heads, 2, d.block_size)
-            if scales is None or scales.dtype != torch.float32 or tuple(scales.shape) != shape or \
-                    not scales.is_contiguous():
+            shape = (num_blocks, hkv, 2, bs)
+            if scales is None or scales.dtype is not torch.float32 or scales.shape != shape or not scales.is_contiguous():
                 raise ValueError(f"scales of an 8-bit cache must be a contiguous float32 tensor of shape {shape}")
             self._here(scales, "scales")
-        return _Cache(fmt, 0, _ptr(k_pool), _ptr(v_pool), _ptr(scales), int(num_blocks), *(int(x) for x in strides))
+        return _Cache(fmt, 0, k_pool.data_ptr(), v_pool.data_ptr(), _ptr(scales), num_blocks, *strides)
 
     def _here(self, t, name):
-        if t.device != self.device:
+        if t.get_device() != self._index:
             raise ValueError(f"{name} must be on {self.device}, the context's device")
         return t
 
@@ -389,16 +390,19 @@ class Context:
 
     def _sequences(self, block_table, seq_lens, starts):
         """Checks a block table, its lengths and token starts; returns (table width, sequences)."""
-        B = int(seq_lens.shape[0])
-        self._here(self._i32(block_table, "block_table", 2), "block_table")
-        self._here(self._i32(seq_lens, "seq_lens", 1), "seq_lens")
-        if block_table.shape[0] != B:
+        self._i32(block_table, "block_table", 2)
+        self._i32(seq_lens, "seq_lens", 1)
+        self._here(block_table, "block_table")
+        self._here(seq_lens, "seq_lens")
+        B = seq_lens.size(0)
+        rows, width = block_table.shape
+        if rows != B:
             raise ValueError("block_table must have one row per sequence")
         if starts is not None:
             self._here(self._i32(starts, "starts", 1), "starts")
-            if starts.shape[0] != B + 1:
+            if starts.size(0) != B + 1:
                 raise ValueError("starts must hold one entry per sequence and the end")
-        return int(block_table.shape[1]), B
+        return width, B
 
     def _scale(self, scale) -> float:
         return float("nan") if scale is None else float(scale)
@@ -540,7 +544,7 @@ class Context:
 
     def _stream_of(self, stream):
         """`stream`, or the current stream of this context's device."""
-        return _stream(_torch().cuda.current_stream(self.device) if stream is None else stream)
+        return _torch()._C._cuda_getCurrentRawStream(self._index) if stream is None else _stream(stream)
 
     # -- around the decode: q / k preparation, cache writes and read-backs
     def new_cache(self, num_blocks: int, dtype=None):
@@ -659,19 +663,23 @@ class Context:
                 raise ValueError("starts needs k_out / v_out")
             k_out, v_out = (torch.zeros((B, width * d.block_size, d.num_kv_heads, d.head_dim), device=self.device,
                                         dtype=out_dtype or torch.bfloat16) for _ in range(2))
-        outs = [t for t in (k_out, v_out) if t is not None]
-        for t in outs:
-            if t.dtype not in (torch.bfloat16, torch.float32) or t.dtype != (out_dtype or outs[0].dtype) or \
-                    t.shape != outs[0].shape or not t.is_contiguous() or \
-                    t.dim() != (4 if starts is None else 3) or t.shape[-2:] != (d.num_kv_heads, d.head_dim) or \
-                    (starts is None and t.shape[0] != B):
+        like = v_out if k_out is None else k_out
+        shape, dtype = like.shape, like.dtype
+        for t in (k_out, v_out):
+            if t is None:
+                continue
+            if (dtype is not torch.bfloat16 and dtype is not torch.float32) or t.dtype is not (out_dtype or dtype) or \
+                    t.shape != shape or not t.is_contiguous() or len(shape) != (4 if starts is None else 3) or \
+                    shape[-2] != d.num_kv_heads or shape[-1] != d.head_dim or (starts is None and shape[0] != B):
                 raise ValueError("k_out / v_out must be contiguous bfloat16 or float32 "
                                  f"[{'B, S' if starts is None else 'rows'}, {d.num_kv_heads}, {d.head_dim}], alike")
             self._here(t, "k_out / v_out")
-        rows = outs[0].shape[0] * (outs[0].shape[1] if starts is None else 1)
-        _check(lib().pda_read_cache(self._ctx, ctypes.addressof(cache), _ptr(block_table), width, _ptr(seq_lens), B,
-                                    _ptr(starts), rows, _ptr(k_out), _ptr(v_out),
-                                    int(outs[0].dtype == torch.float32), self._stream_of(stream)))
+        rows = shape[0] * shape[1] if starts is None else shape[0]
+        status = lib().pda_read_cache(self._ctx, ctypes.addressof(cache), block_table.data_ptr(), width,
+                                      seq_lens.data_ptr(), B, _ptr(starts), rows, _ptr(k_out), _ptr(v_out),
+                                      int(dtype is torch.float32), self._stream_of(stream))
+        if status:
+            _check(status)
         return k_out, v_out
 
     # -- tiled lifecycle

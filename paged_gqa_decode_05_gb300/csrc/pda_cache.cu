@@ -711,7 +711,8 @@ cudaError_t launch_heads_fmt(int format, const HeadsParams& p, cudaStream_t stre
 
 template <int D, int FMT>
 cudaError_t launch_read_of(bool f32, const ReadParams& p, cudaStream_t stream) {
-    constexpr int HC = 4;
+    // two rows a group: 414 us for 377k tokens of 8 heads of 128 (1.4 GB), four 437, one 556
+    constexpr int HC = 2;
     const int rows = (p.k_out ? p.Hkv : 0) + (p.v_out ? p.Hkv : 0);
     const int64_t items = p.rows * ((rows + HC - 1) / HC);
     return f32 ? launch_rows(read_kernel<D, FMT, true, HC>, p, items, D / 16, stream)

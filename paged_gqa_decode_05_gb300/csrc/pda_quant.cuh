@@ -40,7 +40,7 @@ constexpr float kLeastScale = 7.7037198e-34f;  // 2^-110: a scale of 0 counts as
 template <int D, int NT>
 struct QuantCfg {
     static constexpr int kWarps = quant_warps(D, NT);
-    static constexpr int kRT = quant_row_tiles(D);
+    static constexpr int kRT = quant_row_tiles(D, NT);
     static constexpr int kST = quant_stage_rows(D, NT);
     static constexpr int kMainThreads = (kWarps + 1) * 32;
     static constexpr int kThreads = kMainThreads + 32;  // + the prefetch warp
@@ -53,7 +53,7 @@ struct QuantCfg {
     static constexpr int kStages = quant_stages(D, NT);
     static constexpr int kK = D / 32;                   // 32-column steps of a row
     static_assert(kStageBytes % 1024 == 0, "stages start on swizzle spans");
-    static_assert(kWarps * 8 * NT * (D + 4) * 4 <= kStageBytes, "the staged states fit a stage");
+    static_assert(kWarps * 8 * (D + 4) * 4 <= kStageBytes, "the staged states fit a stage");
 };
 
 // A stage holds blocks of 1 << lbs rows back to back (one of kST rows when the
@@ -181,18 +181,19 @@ struct TouchQuant {  // a block's rows of a kv head and their scales, towards L2
 };
 
 // The states that the W warps of a segment staged, st_m / st_l [warp][16 rows]
-// and st_o [warp][kRows][D + 4]: the combined state of q row h.
-template <int D, int W, int kRows>
+// and, of the tile's 8 rows, st_o [warp][8][D + 4]: the combined state of q row
+// h, row hr of the tile.
+template <int D, int W>
 struct UnitSlices {
     const float *st_m, *st_l, *st_o;
-    __device__ __forceinline__ void operator()(int h, int, int d4, float& M, float& Ls, float4& Os) const {
+    __device__ __forceinline__ void operator()(int h, int hr, int d4, float& M, float& Ls, float4& Os) const {
 #pragma unroll
         for (int w = 0; w < W; ++w) M = fmaxf(M, st_m[w * 16 + h]);
         if (M == kNegInf) return;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
             const float f = ex2(st_m[w * 16 + h] - M);
-            const float4 v = *reinterpret_cast<const float4*>(st_o + (size_t)(w * kRows + h) * (D + 4) + d4);
+            const float4 v = *reinterpret_cast<const float4*>(st_o + (size_t)(w * 8 + hr) * (D + 4) + d4);
             Ls += st_l[w * 16 + h] * f;
             Os.x += v.x * f; Os.y += v.y * f; Os.z += v.z * f; Os.w += v.w * f;
         }
@@ -248,7 +249,7 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
                                                    volatile int* abort_flag, int warp, int lane) {
     using C = QuantCfg<D, NT>;
     constexpr int S = C::kStages, RT = C::kRT, K = C::kK;
-    constexpr int kThreadsC = C::kWarps * 32, kRows = 8 * NT, kOStride = D + 4;
+    constexpr int kThreadsC = C::kWarps * 32, kOStride = D + 4;
     constexpr bool MQ = is_multi(MODE);
     const uint32_t full0 = base_s + L.bars, empty0 = full0 + 8 * S;
     const int g = lane >> 2, t = lane & 3;
@@ -520,7 +521,7 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
             float* st_m = reinterpret_cast<float*>(base + L.st_m);  // [warp][16 rows]
             float* st_l = reinterpret_cast<float*>(base + L.st_l);
             int32_t* st_role = reinterpret_cast<int32_t*>(base + L.st_x) + 2 * kMaxGroup;
-            float* st_o = reinterpret_cast<float*>(base + (s0 - base_s));  // [warp][kRows][kOStride]
+            float* st_o = reinterpret_cast<float*>(base + (s0 - base_s));  // [warp][8][kOStride]
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -529,34 +530,39 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
                     for (int s = 4; s < 32; s <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], s);
             if (!consumer_sync(cbar, cphase, p.err, abort_flag)) break;  // all reads of the stage done
             const RowInfo ri = row_info<MQ>(p, md.b);
-            const int NR = ri.cnt * G;  // q rows of the unit
+            StageMeta me = md;
+            me.nr = ri.cnt * G;
+            UnitPieces pc;
+            pc.cf = 0; pc.su = 0; pc.n = 1; pc.every = true;
+            const GroupRange grs = group_of_cta(blockIdx.x, pfx, p.B, rows_per_seq<MQ>(p), p.Hkv, gridDim.x);
+            if (!(md.flags & kWholeUnit)) pc = unit_pieces(pfx, md.b, md.kvh, p.Hkv, p.unit_cost, grs);
+            int role = kRoleAbort;
+            bool stop = false;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n) {  // eight rows at a time
+                if (stop || 8 * n >= me.nr) continue;
+                // the previous tile's staged states are read: overwrite them
+                if (n > 0 && !consumer_sync(cbar, cphase, p.err, abort_flag)) { stop = true; continue; }
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const int h = 8 * n + 2 * t + c;
-                    if (h >= NR) continue;
+                    const int hr = 2 * t + c, h = 8 * n + hr;
+                    if (h >= me.nr) continue;
                     if (g == 0) {
                         // a NaN sum must not hide behind an empty reference
                         st_m[warp * 16 + h] = l[n][c] == l[n][c] ? m[n][c] : 0.f;
                         st_l[warp * 16 + h] = l[n][c];
                     }
-                    float* r = st_o + (size_t)(warp * kRows + h) * kOStride + 2 * g;
+                    float* r = st_o + (size_t)(warp * 8 + hr) * kOStride + 2 * g;
 #pragma unroll
                     for (int i = 0; i < 2 * K; ++i)
                         *reinterpret_cast<float2*>(r + 16 * i) = make_float2(o[n][i][c], o[n][i][2 + c]);
                 }
-            UnitPieces pc;
-            pc.cf = 0; pc.su = 0; pc.n = 1; pc.every = true;
-            const GroupRange grs = group_of_cta(blockIdx.x, pfx, p.B, rows_per_seq<MQ>(p), p.Hkv, gridDim.x);
-            if (!(md.flags & kWholeUnit)) pc = unit_pieces(pfx, md.b, md.kvh, p.Hkv, p.unit_cost, grs);
-            StageMeta me = md;
-            me.nr = NR;
-            int role = kRoleAbort;
-            if (!rows_tile_merge<D, kThreadsC, kRows, true>(p, me, 0, ct, ticket, pc, grs, ri,
-                                                            UnitSlices<D, C::kWarps, kRows>{st_m, st_l, st_o}, st_role,
-                                                            cbar, cphase, abort_flag, role))
-                break;
+                if (!rows_tile_merge<D, kThreadsC, 8, true>(p, me, n, ct, ticket, pc, grs, ri,
+                                                            UnitSlices<D, C::kWarps>{st_m, st_l, st_o}, st_role, cbar,
+                                                            cphase, abort_flag, role))
+                    stop = true;
+            }
+            if (stop) break;
             if (!consumer_sync(cbar, cphase, p.err, abort_flag)) break;
             if (role == kRoleStore && ct == 0) red_release_gpu_add(p.unit_sync + 2 * (md.b * p.Hkv + md.kvh) + 1, 1);
             fence_proxy_async_smem();  // staging writes before the next TMA into this stage

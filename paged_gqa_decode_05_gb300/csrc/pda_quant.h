@@ -13,12 +13,12 @@ namespace pda {
 // SM, two row tiles each; 16 packed q rows (n_tiles 2) and head size 256 run
 // one CTA of 8.
 PDA_HD constexpr int quant_warps(int D, int n_tiles) { return D == 256 || n_tiles == 2 ? 8 : 4; }
-PDA_HD constexpr int quant_row_tiles(int D) { return D == 256 ? 1 : 2; }
-PDA_HD constexpr int quant_stage_rows(int D, int n_tiles) { return 16 * quant_warps(D, n_tiles) * quant_row_tiles(D); }
+PDA_HD constexpr int quant_row_tiles(int D, int n_tiles) { return D == 256 || n_tiles == 2 ? 1 : 2; }
+PDA_HD constexpr int quant_stage_rows(int D, int n_tiles) { return 16 * quant_warps(D, n_tiles) * quant_row_tiles(D, n_tiles); }
 PDA_HD constexpr int quant_stage_bytes(int D, int n_tiles) {
     return quant_stage_rows(D, n_tiles) * (2 * D + 8) + 8 * n_tiles * D * 2;
 }
-PDA_HD constexpr int quant_stages(int D, int) { return D == 64 ? 5 : 3; }
+PDA_HD constexpr int quant_stages(int D, int n_tiles) { return n_tiles == 2 ? (D == 64 ? 8 : 5) : D == 64 ? 5 : 3; }
 // Whether blocks load as boxes: a block's K and V rows of one kv head must
 // fill whole 1024-byte spans (one box brings both where the pools' layout
 // allows it, with `joined`; else a box each).
