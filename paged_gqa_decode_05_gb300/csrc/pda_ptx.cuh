@@ -347,6 +347,13 @@ __device__ __forceinline__ float lg2(float x) {
     return y;
 }
 
+// The larger of two values; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
 // Packs (lo, hi) as fp16x2 with round-to-nearest-even; lo in the low half.
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t d;

@@ -263,20 +263,29 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
     const int row = r0 + (lane & 15), cpar = lane >> 4;
     const uint32_t part = (uint32_t)D << lbs;               // bytes between a block's K and V
     const uint32_t k_at = p.v_first ? part : 0u, v_at = p.v_first ? 0u : part;
-    uint32_t off[RT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) off[r] = quant_row_off<D>(row + 16 * r, lbs);
-    // the chunk swizzle of the lane's rows in slab h (rows 16 apart share it)
-    int swk[C::kSlabs], swv[C::kSlabs];
+    constexpr int CPS = C::kRB / 16;  // 16-byte chunks per slab row
+    // Byte offsets in a stage of this lane's chunk `cpar` of its row, slab h, in K
+    // and V; chunk 2 kk + cpar of a 32-column step lies at the offset XOR 32 kk
+    // (rows start on multiples of their slab's bytes).  Row tiles are `tile_at`
+    // apart and share the swizzle.
+    uint32_t k_off[C::kSlabs], v_off[C::kSlabs];
 #pragma unroll
     for (int h = 0; h < C::kSlabs; ++h) {
-        swk[h] = quant_swz<D>(off[0] + k_at + h * hs);
-        swv[h] = quant_swz<D>(off[0] + v_at + h * hs);
+        const uint32_t ro = quant_row_off<D>(row, lbs) + h * hs;
+        k_off[h] = ro + k_at + (uint32_t)((cpar ^ quant_swz<D>(ro + k_at)) << 4);
+        v_off[h] = ro + v_at + (uint32_t)((cpar ^ quant_swz<D>(ro + v_at)) << 4);
     }
-    constexpr int CPS = C::kRB / 16;  // chunks per slab row
-    auto chunk = [&](int kk, const int (&sw)[C::kSlabs]) {
-        return (uint32_t)((2 * kk) / CPS) * hs + (uint32_t)((((2 * kk) % CPS + cpar) ^ sw[(2 * kk) / CPS]) << 4);
-    };
+    const uint32_t tile_at = quant_row_off<D>(row + 16, lbs) - quant_row_off<D>(row, lbs);
+    auto step = [](const uint32_t (&at)[C::kSlabs], int kk) { return at[(2 * kk) / CPS] ^ (uint32_t)((2 * kk) % CPS << 4); };
+    // this lane's rows g, g + 8 of each tile: where their K scale is, in floats
+    uint32_t s_off[RT][2];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int tr = r0 + 16 * r + 8 * i + g;
+            s_off[r][i] = (uint32_t)(((tr >> lbr) << (lbr + 1)) + (tr & (p.bs - 1)));
+        }
 
     float o[NT][2 * K][4];
     uint32_t qf[NT][K][4];
@@ -318,7 +327,7 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
         if (warp == 0 && lane == 0 && (md.flags & kSegEnd) && !(md.flags & kWholeUnit))
             ticket = atomicAdd(p.unit_sync + 2 * (md.b * p.Hkv + md.kvh), 1);
         const uint32_t s0 = base_s + (uint32_t)stage * C::kStageBytes;
-        const uint32_t sK = s0 + k_at, sV = s0 + v_at;
+        const uint32_t sV = s0 + v_at;
         const uint8_t* bytes = base + (s0 - base_s);
 
         if (md.flags & kSegBegin) {
@@ -385,20 +394,16 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
                 }
                 __syncwarp();
             }
-            // this lane's rows: g and g + 8 of each row tile
             float ks[RT][2], lv[RT][2], iv[RT][2];
+            const float* sp = reinterpret_cast<const float*>(bytes + C::kSOff);
 #pragma unroll
             for (int r = 0; r < RT; ++r)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int tr = r0 + 16 * r + 8 * i + g;
-                    const float* s = reinterpret_cast<const float*>(bytes + C::kSOff) +
-                                     ((tr >> lbr) << (lbr + 1)) + (tr & (p.bs - 1));
-                    const bool in = tr < md.n_valid;
-                    ks[r][i] = s[0];
-                    float vs = in ? s[p.bs] : 1.f;
-                    vs = vs < kLeastScale ? kLeastScale : vs;
-                    lv[r][i] = lg2(vs);
+                    ks[r][i] = sp[s_off[r][i]];
+                    float vs = sp[s_off[r][i] + p.bs];
+                    if (partial && r0 + 16 * r + 8 * i + g >= md.n_valid) vs = 1.f;
+                    lv[r][i] = lg2(max_nan(vs, kLeastScale));
                     iv[r][i] = ex2(-lv[r][i]);
                 }
             float x[RT][NT][4];
@@ -412,7 +417,7 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
 #pragma unroll
                 for (int kk = 0; kk < K; ++kk) {
                     uint32_t w[4];
-                    ldsm_x4(sK + off[r] + chunk(kk, swk), w);
+                    ldsm_x4(s0 + r * tile_at + step(k_off, kk), w);
                     if constexpr (FMT == kE4m3) {
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
@@ -505,7 +510,7 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
                     uint32_t w[4], a[4], b[4];
-                    ldsm_x4_trans(sV + off[r] + chunk(kk, swv), w);
+                    ldsm_x4_trans(s0 + r * tile_at + step(v_off, kk), w);
                     v_fragment<FMT>(w[0], w[1], a);
                     v_fragment<FMT>(w[2], w[3], b);
 #pragma unroll

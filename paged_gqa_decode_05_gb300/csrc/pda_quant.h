@@ -26,7 +26,7 @@ PDA_HD constexpr bool quant_boxes(int D, int bs, bool joined) { return (bs * D *
 // Plan blocks added to every unit (see pda_plan.h), in quarter stages.
 PDA_HD int32_t quant_unit_cost(int D, int n_tiles, int bs, bool multi) {
     const int nb = quant_stage_rows(D, n_tiles) / bs;
-    const int x4 = bs < 8 ? 2 : multi ? 12 : 6;
+    const int x4 = bs < 8 ? 2 : multi ? 16 : 12;
     return nb * x4 / 4 < 1 ? 1 : nb * x4 / 4;
 }
 

@@ -459,3 +459,147 @@ def test_a_layer_step_by_step(dtype):
     again = ctx.decode_contiguous(q, k, v, lens)
     # read-back rounds to bf16: 2^-8 of every value, and scores off by 2^-8 |q||k| at most
     assert (again.float() - out.float()).abs().max() < 0.05
+
+
+@pytest.mark.parametrize("dtype", ref.FORMATS)
+def test_a_captured_step_replays(dtype):
+    """Append and decode captured into one graph: replays read the buffers' contents of the moment and repeat to the
+    bit, beside eager calls of another context on another stream."""
+    g = gen(40)
+    B, hq, hkv, d, bs = 5, 8, 2, 128, 16
+    ctx, other = (ctx_of(hq, hkv, d, bs) for _ in range(2))
+    table = torch.randperm(B * 3, generator=g).int().reshape(B, 3).cuda()
+    caches = [ctx.new_cache(B * 3, dtype) for _ in range(2)]
+    for kp, vp, sc in caches:  # the same contents
+        k0, v0, s0 = ref.random_cache(gen(41), B * 3, bs, hkv, d, dtype)
+        kp.copy_(k0), vp.copy_(v0), sc.copy_(s0)
+    qkv = qkv_of(g, B, hq, hkv, d)
+    cs = pda.rope_table(48, d)
+    lens = torch.tensor([7, 17, 30, 1, 45], dtype=torch.int32).cuda()
+    q_out, out = (torch.empty((B, hq, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+
+    def step(c, cache, stream=None):
+        kp, vp, sc = cache
+        c.append(qkv[:, hq:hq + hkv], qkv[:, hq + hkv:], kp, vp, table, lens, scales=sc, q=qkv[:, :hq], q_out=q_out,
+                 cos_sin=cs, stream=stream)
+        return c.decode(q_out, kp, vp, table, lens, scales=sc, out=out, stream=stream)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(ctx, caches[0])
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            step(ctx, caches[0])
+    for i in range(3):
+        qkv.copy_(qkv_of(g, B, hq, hkv, d))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            graph.replay()
+            first = out.clone()
+            graph.replay()
+        side.synchronize()
+        assert torch.equal(out, first)
+        replayed = out.clone()
+        out.zero_()
+        assert torch.equal(step(other, caches[1]), replayed)
+        assert torch.equal(caches[0][0].view(torch.uint8), caches[1][0].view(torch.uint8))
+        lens += 1
+    assert ctx.read_device_errors() == 0 and other.read_device_errors() == 0
+
+
+def test_decode_more_rows_than_a_launch_holds():
+    """1100 sequences (two launches), and 300 of 5 queries each."""
+    g, rng = gen(50), np.random.default_rng(50)
+    hq, hkv, d, bs = 4, 2, 64, 8
+    for B, q_len in ((1100, 1), (300, 5)):
+        lens = [int(x) for x in rng.integers(0, 40, B)]
+        table, pool = ref.sequences(rng, lens, bs)
+        kp, vp, sc = ref.random_cache(g, pool, bs, hkv, d, torch.float8_e4m3fn)
+        q = torch.randn((B, q_len, hq, d), generator=g).bfloat16()
+        ctx = ctx_of(hq, hkv, d, bs, max_seqs=B * q_len)
+        out = torch.empty(q.shape, dtype=torch.float32, device="cuda")
+        args = (kp.cuda(), vp.cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda())
+        if q_len == 1:
+            ctx.decode(q[:, 0].cuda(), *args, scales=sc.cuda(), out=out[:, 0])
+        else:
+            ctx.decode_multi(q.cuda(), *args, scales=sc.cuda(), out=out)
+        want, size = ref.decode64(q, kp, vp, sc, table, lens, bs)
+        within(out, want, DECODE * size)
+        assert ctx.read_device_errors() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_decode_values_before_keys(d):
+    """V's pool below K's in memory, and K and V in one pool, give the same bits as any other placement."""
+    g, rng = gen(60), np.random.default_rng(60)
+    hq, hkv, bs, lens = 4, 2, 16, [100, 33, 5]
+    table, pool = ref.sequences(rng, lens, bs)
+    kp, vp, sc = ref.random_cache(g, pool, bs, hkv, d, torch.int8)
+    q = torch.randn((3, hq, d), generator=g).bfloat16().cuda()
+    rest = (table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda())
+    ctx = ctx_of(hq, hkv, d, bs)
+    both = torch.stack([kp, vp]).cuda()
+    want = ctx.decode(q, both[0], both[1], *rest, scales=sc.cuda())
+    both = torch.stack([vp, kp]).cuda()
+    assert torch.equal(ctx.decode(q, both[1], both[0], *rest, scales=sc.cuda()), want)
+    same = sc.clone()
+    same[:, :, 0] = sc[:, :, 1]
+    got = ctx.decode(q, both[0], both[0], *rest, scales=same.cuda(), out_dtype=torch.float32)
+    ref_out, size = ref.decode64(q[:, None].cpu(), vp, vp, same, table, lens, bs)
+    within(got, ref_out[:, 0], DECODE * size[:, 0])
+
+
+@pytest.mark.parametrize("dtype", ref.FORMATS)
+def test_offsets_past_32_bits(dtype):
+    """A pool whose last blocks lie past 2^31 elements: written, decoded and read back there."""
+    hq, hkv, d, bs = 4, 8, 128, 16
+    blocks = (1 << 31) // (bs * hkv * d) + 3
+    ctx = ctx_of(8, hkv, d, bs)
+    kp, vp, sc = ctx.new_cache(blocks, dtype)
+    g = gen(70)
+    qkv = qkv_of(g, 40, 8, hkv, d)
+    table = torch.tensor([[blocks - 1, 0, blocks - 3]], dtype=torch.int32).cuda()
+    lens = torch.tensor([40], dtype=torch.int32).cuda()
+    q = ctx.append(qkv[:, 8:16], qkv[:, 16:], kp, vp, table, lens, scales=sc, q=qkv[:, :8])
+    k, v = ctx.read_cache(kp, vp, table, lens, scales=sc, out_dtype=torch.float32)
+    codes, scale = ref.codes32(qkv[:, 16:], dtype)
+    assert torch.equal(v[0, :40].cpu(), codes.float() * scale[..., None])
+    out = ctx.decode(q[-1:].contiguous(), kp, vp, table, lens, scales=sc, out_dtype=torch.float32)
+    near = [t.cpu()[:, [0]] for t in (k, v)]
+    small = [pool[[blocks - 1, 0, blocks - 3]].cpu() if dtype == torch.int8 else
+             pool.view(torch.uint8)[[blocks - 1, 0, blocks - 3]].cpu().view(dtype) for pool in (kp, vp)]
+    want, size = ref.decode64(q[-1:][:, None].cpu(), *small, sc[[blocks - 1, 0, blocks - 3]].cpu(),
+                              torch.tensor([[0, 1, 2]]), [40], bs)
+    within(out, want[:, 0], DECODE * size[:, 0])
+    assert ctx.read_device_errors() == 0 and near
+
+
+def test_bound_calls_and_closed_contexts():
+    ctx = ctx_of(4, 2, 64, 16)
+    kp, vp, sc = ctx.new_cache(2, torch.int8)
+    qkv = qkv_of(gen(80), 2, 4, 2, 64)
+    table, lens = torch.tensor([[0], [1]], dtype=torch.int32).cuda(), torch.tensor([3, 9], dtype=torch.int32).cuda()
+    put = ctx.bind_append(qkv[:, 4:6], qkv[:, 6:], kp, vp, table, lens, scales=sc, q=qkv[:, :4])
+    q = put()
+    run = ctx.bind_decode(q, kp, vp, table, lens, torch.empty_like(q), scales=sc)
+    assert torch.equal(run(), ctx.decode(q, kp, vp, table, lens, scales=sc))
+    for bad in (dict(scales=None), dict(scales=sc[:1]), dict(scales=sc.double()), dict(scales=sc.cpu())):
+        with pytest.raises(ValueError):
+            ctx.decode(q, kp, vp, table, lens, **bad)
+    with pytest.raises(ValueError):
+        ctx.decode(q, kp.float(), vp.float(), table, lens, scales=sc)
+    with pytest.raises(ValueError):
+        ctx.append(qkv[:, 4:6], qkv[:, 6:], kp, vp.view(torch.uint8), table, lens, scales=sc)
+    with pytest.raises(ValueError):
+        ctx.norm_rope(qkv[:, :4], qkv[:, 4:6], cos_sin=pda.rope_table(4, 64))
+    with pytest.raises(ValueError):
+        ctx.read_cache(kp, vp, table, lens, scales=sc, starts=torch.zeros(3, dtype=torch.int32).cuda())
+    with pytest.raises(ValueError):
+        ctx.new_cache(1, torch.float16)
+    ctx.close()
+    with pytest.raises(pda.PdaError):
+        run()
+    with pytest.raises(pda.PdaError):
+        put()
