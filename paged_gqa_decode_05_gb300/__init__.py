@@ -219,9 +219,15 @@ def rope_table(max_positions: int, rotary_dim: int, base: float = 10000.0, inv_f
     return torch.cat([a.cos(), a.sin()], 1).float()
 
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _ptr(t) -> Optional[int]:

@@ -15,8 +15,8 @@ namespace pda {
 PDA_HD constexpr int quant_warps(int D, int n_tiles) { return D == 256 || n_tiles == 2 ? 8 : 4; }
 PDA_HD constexpr int quant_row_tiles(int D, int n_tiles) { return D == 256 || n_tiles == 2 ? 1 : 2; }
 PDA_HD constexpr int quant_stage_rows(int D, int n_tiles) { return 16 * quant_warps(D, n_tiles) * quant_row_tiles(D, n_tiles); }
-PDA_HD constexpr int quant_stage_bytes(int D, int n_tiles) {
-    return quant_stage_rows(D, n_tiles) * (2 * D + 8) + 8 * n_tiles * D * 2;
+PDA_HD constexpr int quant_stage_bytes(int D, int n_tiles) {  // whole swizzle spans
+    return (quant_stage_rows(D, n_tiles) * (2 * D + 8) + 8 * n_tiles * D * 2 + 1023) / 1024 * 1024;
 }
 PDA_HD constexpr int quant_stages(int D, int n_tiles) { return n_tiles == 2 ? (D == 64 ? 8 : 5) : D == 64 ? 5 : 3; }
 // Whether blocks load as boxes: a block's K and V rows of one kv head must
