@@ -353,11 +353,12 @@ __device__ __forceinline__ int32_t turn_row(const HeadsParams& p, int64_t t, int
     return (int32_t)pos;
 }
 
-// Few tokens, or any alignment: a group of lanes takes kRows rows of one token
+// Little work, or any alignment: a group of lanes takes kRows rows of one token
 // straight from memory.  Latency counts (loads of the rows go out before the
 // token's place is looked up), and many small groups hide it better than few
 // with more rows each: a 32-token step of 48 rows takes 3.7 us with two rows a
-// group, 4.8 with four.
+// group, 4.8 with four.  What is left of such a step is one chain of dependent
+// loads and the launch itself.
 constexpr int kRows = 2;
 template <int D, int FMT>
 __global__ void __launch_bounds__(kHeadsThreads, 4) heads_kernel(const __grid_constant__ HeadsParams p) {
@@ -407,17 +408,30 @@ __global__ void __launch_bounds__(kHeadsThreads, 4) heads_kernel(const __grid_co
 // shared-memory slots, a token's rows (and its row of cosines and sines) to a
 // slot.  A producer warp looks 32 tokens up at a time and issues their bulk
 // copies, kTeams teams of kTeamWarps warps take the slots in turn and write
-// straight to memory.  The copies in flight (the ring less the slots being
-// worked on, 100 KB and more a SM) do not depend on occupancy; loading rows to
-// registers instead, with 32 warps an SM, came to 3.9 TB/s on 8191 tokens of
-// 72 heads of 128 and no arrangement of rows per thread passed it.
+// straight to memory.  The copies in flight do not depend on occupancy;
+// loading rows to registers instead, with 32 warps an SM, came to 3.9 TB/s on
+// 8191 tokens of 72 heads of 128 and no arrangement of rows per thread passed
+// it.  HBM bounds it: 8191 tokens of 64 + 8 heads of 128 take 51 us (5.9 TB/s
+// read and written), ragged prompts of 24 sequences (20k tokens of 32 + 2 * 8
+// heads, e4m3 cache) 79 us (5.9 TB/s).  Teams of 2, 3 and 4 warps (8, 5, 4 of
+// them): 53.5, 51, 52 us on the first.
+//
+// The first fill is paced: kFillPace bytes a cycle and SM are about the share
+// of HBM that reads get once stores run too.  Issued all at once, the copies
+// delay each other, the first slot lands late and the stores start late (4096
+// tokens of 40 heads of 128: 19.4 us at once, 18.1 paced; 12 bytes 18.0, 9
+// bytes 18.6).  Slots below kSmallSlot bytes are issued kIssue at a time,
+// since one lane's issue (0.3 us a token) is slower than their traffic (4096
+// tokens of 9 heads of 128: 8.6 us, one at a time 11.4).
 //
 // A slot belongs to one team (slots are a multiple of the teams at work): the
 // team that waits for a slot's next token has itself seen the previous one
 // land.  Copies land in any order, so another team could be a whole turn of
 // the slot ahead and take the barrier's older phase for the one it waits for.
 constexpr int kTeams = 5, kTeamWarps = 3, kMaxSlots = 20;
+constexpr uint32_t kFillPace = 16, kSmallSlot = 4096, kIssue = 4;
 constexpr int kRingThreads = (kTeams * kTeamWarps + 1) * 32;
+static_assert(kMaxSlots <= 32, "the first fill is the producer's first 32 tokens");
 struct SlotMeta {
     Spot at;
     int32_t t;  // -1: padding
@@ -468,18 +482,18 @@ __global__ void __launch_bounds__(kRingThreads) heads_ring_kernel(const __grid_c
                 if (live) at = spot_of(p, place, idx, true);
             }
             const int32_t turn = live && p.rotary ? turn_row(p, t, idx, true) : 0;
-            for (int i = 0; i < 32 && i0 + i < n; ++i) {
-                const int s = (i0 + i) % S;
-                int stop = 0;
-                if (lane == i) {
-                    const uint32_t full = bars0 + 8 * s;
-                    if (*(volatile int*)&abort_flag ||
-                        !mbar_wait_bounded(bars0 + 8 * (S + s), (((i0 + i) / S) & 1) ^ 1, kWaitLimitNs)) {
+            const int s = mine % S;
+            const uint32_t phase = (uint32_t)(mine / S) & 1u, full = bars0 + 8 * s, dst = ring + (uint32_t)s * slot_bytes;
+            // lanes i .. i + w - 1 issue their tokens; false: a wait ran out
+            const auto issue = [&](int i, int w) -> bool {
+                int issued = 0, stop = 0;
+                if (lane >= i && lane < i + w && mine < n) {
+                    if (*(volatile int*)&abort_flag || !mbar_wait_bounded(bars0 + 8 * (S + s), phase ^ 1u, kWaitLimitNs)) {
                         stop = 1;
                     } else {
                         meta[s].at = at;
                         meta[s].t = live ? (int32_t)t : -1;
-                        const uint32_t dst = ring + (uint32_t)s * slot_bytes;
+                        issued = 1;
                         mbar_arrive_expect_tx(full, live ? slot_bytes : 0u);
                         if (live) {
                             uint32_t to = dst;
@@ -498,17 +512,30 @@ __global__ void __launch_bounds__(kRingThreads) heads_ring_kernel(const __grid_c
                         }
                     }
                 }
-                if (__any_sync(0xffffffffu, stop)) {
-                    // a wait ran out: report it, and leave once the copies issued have landed
-                    if (lane == 0) {
-                        atomicOr(p.err, PDA_DEVERR_TIMEOUT_);
-                        abort_flag = 1;
-                        for (int32_t k = max(0, i0 + i - S); k < i0 + i; ++k)
+                if (!__any_sync(0xffffffffu, stop)) return true;
+                // report it, and leave once the copies issued have landed
+                const uint32_t out = __ballot_sync(0xffffffffu, issued);
+                if (lane == 0) {
+                    atomicOr(p.err, PDA_DEVERR_TIMEOUT_);
+                    abort_flag = 1;
+                    for (int32_t k = max(0, i0 + i - S); k < i0 + i + w; ++k)
+                        if (k < i0 + i || (out >> (k - i0)) & 1u)
                             mbar_wait_bounded(bars0 + 8 * (k % S), (k / S) & 1, kWaitLimitNs);
+                }
+                return false;
+            };
+            int i = 0;
+            if (i0 == 0) {
+                const int w = slot_bytes < kSmallSlot ? (int)kIssue : 1;
+                const int64_t t0 = clock64();
+                for (; i + w <= S && i < n; i += w) {
+                    while (clock64() - t0 < (int64_t)(i * slot_bytes / kFillPace)) {
                     }
-                    return;
+                    if (!issue(i, w)) return;
                 }
             }
+            for (; i < 32 && i0 + i < n; ++i)
+                if (!issue(i, 1)) return;
         }
         return;
     }
@@ -542,7 +569,11 @@ __global__ void __launch_bounds__(kRingThreads) heads_ring_kernel(const __grid_c
 }
 
 // Read-back: D / 16 lanes share a row of 16 elements each; a group takes HC
-// of a token's 2 Hkv rows.
+// of a token's 2 Hkv rows, whose loads go out together.  Two bytes are written
+// for each byte read, and HBM bounds it: 377k tokens of 8 heads of 128 (int8,
+// blocks of 32; 1.4 GB read, 2.8 with what is written) take 416 us, the rate
+// of a plain copy.  A small call is bound by its chain of loads: lengths, block
+// id, codes.
 template <int D, int FMT, bool F32, int HC>
 __global__ void __launch_bounds__(kHeadsThreads) read_kernel(const __grid_constant__ ReadParams p) {
     constexpr int TPR = D / 16;
@@ -670,7 +701,11 @@ bool runs_of_8(const Heads& h) {
 }
 
 constexpr int kRingBytes = 200 * 1024;  // of an SM's 227 KB
-constexpr int kRingTokens = 1024;       // tokens from which the ring pays (see launch_heads_of)
+// Bytes of heads from which the ring pays.  Short of it a launch is over before
+// the ring is under way: 512 tokens of 40 heads of 128 (5.2 MB) take 4.6 us
+// straight, 4.9 through the ring; 1024 (10.5 MB) 8.9 and 7.9; 4096 26.0 and
+// 18.1.  Tokens of 9 such heads: 2048 (4.7 MB) 5.3 and 5.2, 4096 10.0 and 8.6.
+constexpr int64_t kRingWork = 8 << 20;
 
 template <int D, int FMT>
 cudaError_t launch_heads_of(HeadsParams p, cudaStream_t stream) {
@@ -678,7 +713,7 @@ cudaError_t launch_heads_of(HeadsParams p, cudaStream_t stream) {
     const int slot = rows * 2 * D + p.rotary * 4;
     p.slots = kRingBytes / slot < kMaxSlots ? kRingBytes / slot : kMaxSlots;
     if (p.slots > kTeams) p.slots -= p.slots % kTeams;
-    if (p.T >= kRingTokens && p.slots >= 4 && p.rotary % 16 == 0 && one_copy(p.q, D) && one_copy(p.k, D) &&
+    if (p.T * rows * 2 * D >= kRingWork && p.slots >= 4 && p.rotary % 16 == 0 && one_copy(p.q, D) && one_copy(p.k, D) &&
         one_copy(p.v, D) && runs_of_8(p.q_out) && runs_of_8(p.k_out)) {
         return launch_grid(heads_ring_kernel<D, FMT>, p, p.sms, kRingThreads, (size_t)p.slots * slot + 128, stream);
     }

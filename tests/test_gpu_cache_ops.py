@@ -47,7 +47,8 @@ def qkv_of(g, tokens, hq, hkv, d):
     (4, 2, 64, 64, 1), (32, 8, 128, 128, 33), (5, 1, 128, 64, 257), (16, 4, 256, 256, 7), (3, 3, 64, 8, 100),
     (8, 8, 256, 24, 65), (64, 8, 128, 120, 19),
     # enough tokens for the streaming form, and (rotary 24) for the other at that size
-    (32, 8, 128, 128, 1500), (4, 2, 64, 32, 1111), (16, 4, 256, 128, 1024), (2, 1, 64, 24, 1300)])
+    (32, 8, 128, 128, 1500), (4, 2, 64, 32, 11111), (16, 4, 256, 128, 1024), (8, 1, 128, 128, 4001), (48, 16, 256, 64, 257),
+    (2, 1, 64, 24, 23000)])
 def test_norm_rope(hq, hkv, d, rotary, tokens, interleaved):
     g = gen(tokens)
     ctx = ctx_of(hq, hkv, d, 16)
@@ -160,23 +161,24 @@ def test_append(dtype, hq, hkv, d, bs, lens, news):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16] + ref.FORMATS)
-@pytest.mark.parametrize("hq,hkv,d,bs,rotary", [(32, 8, 128, 16, 128), (4, 4, 64, 32, 16), (2, 1, 256, 64, 0), (5, 1, 64, 1, 64)])
-def test_append_prompts(dtype, hq, hkv, d, bs, rotary):
+@pytest.mark.parametrize("hq,hkv,d,bs,rotary,times", [
+    (32, 8, 128, 16, 128, 1), (4, 4, 64, 32, 16, 5), (2, 1, 256, 64, 0, 4), (5, 1, 64, 1, 64, 8)])
+def test_append_prompts(dtype, hq, hkv, d, bs, rotary, times):
     """Prompts of a prefill batch, streamed: empty sequences, a block that does not exist, a table too narrow, padding
     behind the last sequence; and the same bits as the tokens appended a few at a time."""
     g, rng = gen(31), np.random.default_rng(31)
-    lens = [600, 0, 1, 411, 0, 37, 250]
+    lens = [600 * times, 0, 1, 411 * times, 0, 37 * times, 250 * times]
     table, pool = ref.sequences(rng, lens, bs)
     bad = table.clone()
     bad[5, 0] = pool + 4  # sequence 5's first block
-    width = -(-411 // bs)  # sequence 0 does not fit
+    width = -(-411 * times // bs)  # sequence 0 does not fit
     bad = bad[:, :width].contiguous()
     total = sum(lens)
     starts = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32)
     qkv = qkv_of(g, total + 70, hq, hkv, d)
     ctx = ctx_of(hq, hkv, d, bs)
     wq, wk = ((1 + 0.1 * torch.randn(d, generator=g)).bfloat16().cuda() for _ in range(2))
-    cs = pda.rope_table(600, rotary) if rotary else None
+    cs = pda.rope_table(600 * times, rotary) if rotary else None
     prep = dict(q_weight=wq, k_weight=wk, cos_sin=cs)
     caches = [ctx.new_cache(pool, dtype) for _ in range(2)]
     outs = [torch.full((total + 70, hq, d), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
