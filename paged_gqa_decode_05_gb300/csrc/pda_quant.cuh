@@ -40,6 +40,7 @@ constexpr float kLeastScale = 7.7037198e-34f;  // 2^-110: a scale of 0 counts as
 template <int D, int NT>
 struct QuantCfg {
     static constexpr int kWarps = quant_warps(D, NT);
+    static constexpr int kRW = kWarps / NT;             // warps of a q tile
     static constexpr int kRT = quant_row_tiles(D, NT);
     static constexpr int kST = quant_stage_rows(D, NT);
     static constexpr int kMainThreads = (kWarps + 1) * 32;
@@ -53,7 +54,7 @@ struct QuantCfg {
     static constexpr int kStages = quant_stages(D, NT);
     static constexpr int kK = D / 32;                   // 32-column steps of a row
     static_assert(kStageBytes % 1024 == 0, "stages start on swizzle spans");
-    static_assert(kWarps * 8 * (D + 4) * 4 <= kStageBytes, "the staged states fit a stage");
+    static_assert(kWarps * 8 * (D + 4) * 4 <= kStageBytes && kRW * 16 <= 4 * kMaxRowsPerWalk, "the staged states fit a stage");
 };
 
 // A stage holds blocks of 1 << lbs rows back to back (one of kST rows when the
@@ -243,17 +244,88 @@ __device__ __forceinline__ void v_fragment(uint32_t r0, uint32_t r1, uint32_t (&
     }
 }
 
+// A unit's q rows in the stage (bf16, 8 NT of them, those from nr on zero),
+// scaled by a power of two each and turned in place into the lanes' B
+// fragments [tile of 8 rows][32-column step][lane] of 16 bytes: e4m3, four high
+// parts of columns 4t .. and 16 + 4t .., then their low parts; int8, the same
+// columns in fp16.  `back` takes the factor that undoes each row's power of
+// two, times the score scale.  A warp takes a row, an eighth of the work of
+// every warp preparing all of its own fragments, whose reads at a row's stride
+// also met on the same banks; both run once a unit and are fetched cold (16 q
+// rows, 2550 tokens: 67.5 -> 66.7 us).
+template <int D, int FMT, int NT, int W>
+__device__ __forceinline__ bool quant_q_fragments(uint8_t* at, float* back, int nr, float scale, int warp, int lane,
+                                                  uint32_t cbar, uint32_t& cphase, uint32_t* err,
+                                                  volatile int* abort_flag) {
+    constexpr int R = 8 * NT / W, N4 = D / 4, J = (N4 + 31) / 32;  // rows a warp, runs of four columns a row, and a lane
+    static_assert(R * W == 8 * NT, "the rows divide over the warps");
+    uint2 raw[R][J];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int row = r * W + warp, c4 = lane + 32 * j;
+            raw[r][j] = row < nr && c4 < N4 ? *reinterpret_cast<const uint2*>(at + (row * D + 4 * c4) * 2) : make_uint2(0u, 0u);
+        }
+    if (!consumer_sync(cbar, cphase, err, abort_flag)) return false;  // every row is read
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int row = r * W + warp;
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const uint32_t x = raw[r][j].x, y = raw[r][j].y;
+            top = max(top, max(max(x & 0x7fffu, (x >> 16) & 0x7fffu), max(y & 0x7fffu, (y >> 16) & 0x7fffu)));
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        // the row's largest magnitude lies in [2^e, 2^(e+1)): multiply by 2^(7-e)
+        const int e = max((int)(top >> 7) - 127, -119);
+        const float mult = __int_as_float((127 + 7 - e) << 23);
+        if (lane == 0)  // infinities and NaN: NaN
+            back[row] = top < 0x7f80u ? scale * __int_as_float((127 - 7 + e) << 23) : __int_as_float(0x7fffffff);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int c4 = lane + 32 * j;
+            const float x0 = bf16_lo(raw[r][j].x) * mult, x1 = bf16_hi(raw[r][j].x) * mult;
+            const float x2 = bf16_lo(raw[r][j].y) * mult, x3 = bf16_hi(raw[r][j].y) * mult;
+            uint32_t u, v;
+            if constexpr (FMT == kE4m3) {
+                const uint32_t h01 = pack_e4m3x2(x0, x1), h23 = pack_e4m3x2(x2, x3);
+                const uint32_t b01 = e4m3x2_to_f16x2((uint16_t)h01), b23 = e4m3x2_to_f16x2((uint16_t)h23);
+                const float2 s = __half22float2(*reinterpret_cast<const __half2*>(&b01));
+                const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&b23));
+                u = h01 | (h23 << 16);
+                v = pack_e4m3x2(x0 - s.x, x1 - s.y) | (pack_e4m3x2(x2 - w.x, x3 - w.y) << 16);
+            } else {
+                u = pack_f16x2(x0, x1);
+                v = pack_f16x2(x2, x3);
+            }
+            if (c4 < N4) {
+                const int i = (c4 >> 2) & 1;
+                uint32_t* d = reinterpret_cast<uint32_t*>(at) +
+                              (((row >> 3) * (D / 32) + (c4 >> 3)) * 32 + (row & 7) * 4 + (c4 & 3)) * 4;
+                d[FMT == kE4m3 ? i : 2 * i] = u;
+                d[FMT == kE4m3 ? 2 + i : 2 * i + 1] = v;
+            }
+        }
+    }
+    fence_proxy_async_smem();  // generic writes before the next TMA into this stage
+    return consumer_sync(cbar, cphase, err, abort_flag);
+}
+
 template <int D, int FMT, int NT, int MODE>
 __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_t base_s, uint8_t* base,
                                                    const SmemLayout& L, const StageMeta* meta, const int32_t* pfx,
-                                                   volatile int* abort_flag, int warp, int lane) {
+                                                   volatile int* abort_flag, GroupRange* group, int warp, int lane) {
     using C = QuantCfg<D, NT>;
     constexpr int S = C::kStages, RT = C::kRT, K = C::kK;
     constexpr int kThreadsC = C::kWarps * 32, kOStride = D + 4;
     constexpr bool MQ = is_multi(MODE);
     const uint32_t full0 = base_s + L.bars, empty0 = full0 + 8 * S;
     const int g = lane >> 2, t = lane & 3;
-    const int r0 = warp * 16 * RT;
+    // warps 0 .. kRW - 1 take the first eight q rows, the next kRW the others, all of a stage's KV rows
+    const int tile = NT > 1 ? warp / C::kRW : 0, rw = NT > 1 ? warp % C::kRW : warp;
+    const int r0 = rw * 16 * RT;
     const int G = p.G;
     const int lbr = 31 - __clz(p.bs);                       // the cache's blocks
     const int lbs = p.row_gather ? 31 - __clz(C::kST) : lbr;  // the tile's blocks
@@ -287,31 +359,24 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
             s_off[r][i] = (uint32_t)(((tr >> lbr) << (lbr + 1)) + (tr & (p.bs - 1)));
         }
 
-    float o[NT][2 * K][4];
-    uint32_t qf[NT][K][4];
-    float f[NT][2], m[NT][2], l[NT][2];
+    float o[2 * K][4];
+    uint32_t qf[K][4];
+    float f[2] = {0.f, 0.f}, m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        m[n][0] = m[n][1] = kNegInf;
-        l[n][0] = l[n][1] = f[n][0] = f[n][1] = 0.f;
+    for (int i = 0; i < 2 * K; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 2 * K; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
-#pragma unroll
-        for (int i = 0; i < K; ++i) qf[n][i][0] = qf[n][i][1] = qf[n][i][2] = qf[n][i][3] = 0u;
-    }
+    for (int i = 0; i < K; ++i) qf[i][0] = qf[i][1] = qf[i][2] = qf[i][3] = 0u;
     // causal queries of this lane's score columns
-    int qc[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        qc[n][0] = MQ ? (8 * n + 2 * t) / G : 0;
-        qc[n][1] = MQ ? (8 * n + 2 * t + 1) / G : 0;
-    }
+    const int qc[2] = {MQ ? (8 * tile + 2 * t) / G : 0, MQ ? (8 * tile + 2 * t + 1) / G : 0};
     const uint32_t cbar = base_s + L.cbar;
+    float* q_back = reinterpret_cast<float*>(base + L.st_x);  // [16 rows]
     uint32_t cphase = 0;
     int stage = 0;
     uint32_t phase = 0;
     int32_t ticket = 0;
     const int ct = warp * 32 + lane;
+    // out of the loop (600 cycles a unit); the syncs of the first unit's q rows order it
+    if (ct == 0) *group = group_of_cta(blockIdx.x, pfx, p.B, rows_per_seq<MQ>(p), p.Hkv, gridDim.x);
     zero_empty_rows<D, kThreadsC>(p, pfx, ct);
 
     while (true) {
@@ -331,59 +396,23 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
         const uint8_t* bytes = base + (s0 - base_s);
 
         if (md.flags & kSegBegin) {
+            if (!quant_q_fragments<D, FMT, NT, C::kWarps>(base + (s0 - base_s) + C::kQOff, q_back, MQ ? md.nr : G,
+                                                          p.scale_log2, warp, lane, cbar, cphase, p.err, abort_flag))
+                break;
+            const uint4* frags = reinterpret_cast<const uint4*>(bytes + C::kQOff) + tile * K * 32 + lane;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int qr = 8 * n + g;
-                const bool any = qr < (MQ ? md.nr : G);
-                const uint8_t* qp = bytes + C::kQOff + (size_t)(qr * D + 4 * t) * 2;
-                uint2 raw[K][2];
-                uint32_t top = 0;
-#pragma unroll
-                for (int kk = 0; kk < K; ++kk)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        raw[kk][i] = any ? *reinterpret_cast<const uint2*>(qp + 64 * kk + 32 * i) : make_uint2(0u, 0u);
-#pragma unroll
-                for (int kk = 0; kk < K; ++kk)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t x = raw[kk][i].x, y = raw[kk][i].y;
-                        top = max(top, max(max(x & 0x7fffu, (x >> 16) & 0x7fffu), max(y & 0x7fffu, (y >> 16) & 0x7fffu)));
-                    }
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                // the row's largest magnitude lies in [2^e, 2^(e+1)): multiply by 2^(7-e)
-                const int e = max((int)(top >> 7) - 127, -119);
-                const float mult = __int_as_float((127 + 7 - e) << 23);
-                const float back = top < 0x7f80u ? __int_as_float((127 - 7 + e) << 23)
-                                                 : __int_as_float(0x7fffffff);  // infinities and NaN: NaN
-#pragma unroll
-                for (int kk = 0; kk < K; ++kk)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float x0 = bf16_lo(raw[kk][i].x) * mult, x1 = bf16_hi(raw[kk][i].x) * mult;
-                        const float x2 = bf16_lo(raw[kk][i].y) * mult, x3 = bf16_hi(raw[kk][i].y) * mult;
-                        if constexpr (FMT == kE4m3) {
-                            const uint32_t h01 = pack_e4m3x2(x0, x1), h23 = pack_e4m3x2(x2, x3);
-                            const uint32_t b01 = e4m3x2_to_f16x2((uint16_t)h01), b23 = e4m3x2_to_f16x2((uint16_t)h23);
-                            const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&b01));
-                            const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&b23));
-                            qf[n][kk][i] = h01 | (h23 << 16);
-                            qf[n][kk][2 + i] = pack_e4m3x2(x0 - u.x, x1 - u.y) | (pack_e4m3x2(x2 - w.x, x3 - w.y) << 16);
-                        } else {
-                            qf[n][kk][2 * i] = pack_f16x2(x0, x1);
-                            qf[n][kk][2 * i + 1] = pack_f16x2(x2, x3);
-                        }
-                    }
-                f[n][0] = p.scale_log2 * __shfl_sync(0xffffffffu, back, 8 * t);
-                f[n][1] = p.scale_log2 * __shfl_sync(0xffffffffu, back, 8 * t + 4);
-                m[n][0] = m[n][1] = kNegInf;
-                l[n][0] = l[n][1] = 0.f;
-#pragma unroll
-                for (int i = 0; i < 2 * K; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
+            for (int kk = 0; kk < K; ++kk) {
+                const uint4 w = frags[kk * 32];
+                qf[kk][0] = w.x; qf[kk][1] = w.y; qf[kk][2] = w.z; qf[kk][3] = w.w;
             }
+            f[0] = q_back[8 * tile + 2 * t];
+            f[1] = q_back[8 * tile + 2 * t + 1];
+            m[0] = m[1] = kNegInf;
+            l[0] = l[1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 2 * K; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         }
-        if (r0 < md.n_valid) {
+        if (r0 < md.n_valid && (NT == 1 || 8 * tile < md.nr)) {
             const bool partial = r0 + 16 * RT > md.n_valid;
             if (FMT == kE4m3 && partial) {
                 // rows behind the end may hold NaN codes, and 0 * NaN would poison P V
@@ -406,50 +435,38 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
                     lv[r][i] = lg2(max_nan(vs, kLeastScale));
                     iv[r][i] = ex2(-lv[r][i]);
                 }
-            float x[RT][NT][4];
+            float x[RT][4];
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-                float acc[2][NT][4];
+                float acc[2][4];
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[0][n][i] = acc[1][n][i] = 0.f;
+                for (int i = 0; i < 4; ++i) acc[0][i] = acc[1][i] = 0.f;
 #pragma unroll
                 for (int kk = 0; kk < K; ++kk) {
                     uint32_t w[4];
                     ldsm_x4(s0 + r * tile_at + step(k_off, kk), w);
                     if constexpr (FMT == kE4m3) {
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            mma_e4m3_16832(acc[0][n], w, qf[n][kk][0], qf[n][kk][1]);
-                            mma_e4m3_16832(acc[1][n], w, qf[n][kk][2], qf[n][kk][3]);
-                        }
+                        mma_e4m3_16832(acc[0], w, qf[kk][0], qf[kk][1]);
+                        mma_e4m3_16832(acc[1], w, qf[kk][2], qf[kk][3]);
                     } else {
                         uint32_t a[4], b[4];
                         k_fragment_int8(w[0], w[1], a);
                         k_fragment_int8(w[2], w[3], b);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            mma_f16_16816(acc[0][n], a, qf[n][kk][0], qf[n][kk][1]);
-                            mma_f16_16816(acc[1][n], b, qf[n][kk][2], qf[n][kk][3]);
-                        }
+                        mma_f16_16816(acc[0], a, qf[kk][0], qf[kk][1]);
+                        mma_f16_16816(acc[1], b, qf[kk][2], qf[kk][3]);
                     }
                 }
                 // x: the score in base-2 units plus log2 of the row's V scale
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        x[r][n][i] = fmaf(acc[0][n][i] + acc[1][n][i], ks[r][i >> 1] * f[n][i & 1], lv[r][i >> 1]);
+                for (int i = 0; i < 4; ++i)
+                    x[r][i] = fmaf(acc[0][i] + acc[1][i], ks[r][i >> 1] * f[i & 1], lv[r][i >> 1]);
             }
             if (partial) {
 #pragma unroll
                 for (int r = 0; r < RT; ++r)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (r0 + 16 * r + 8 * (i >> 1) + g >= md.n_valid)
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) x[r][n][i] = kNegInf;
+                        if (r0 + 16 * r + 8 * (i >> 1) + g >= md.n_valid) x[r][i] = kNegInf;
             }
             if constexpr (MQ) {  // column c is query c / G of the row: no later tokens
                 const int pos0 = md.j0 * p.bs + r0;
@@ -457,53 +474,47 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
 #pragma unroll
                     for (int r = 0; r < RT; ++r)
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (pos0 + 16 * r + 8 * (i >> 1) + g > md.lim + qc[n][i & 1]) x[r][n][i] = kNegInf;
+                        for (int i = 0; i < 4; ++i)
+                            if (pos0 + 16 * r + 8 * (i >> 1) + g > md.lim + qc[i & 1]) x[r][i] = kNegInf;
                 }
             }
-            uint32_t pb[RT][NT][2];
+            // the references move only when a weight would pass 2^(kRefBias + kLazyLog2);
+            // the columns' maxima are taken only then
+            float top[2];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                // the references move only when a weight would pass 2^(kRefBias + kLazyLog2);
-                // the columns' maxima are taken only then
-                float top[2];
+            for (int c = 0; c < 2; ++c) {
+                top[c] = fmaxf(x[0][c], x[0][c + 2]);
+#pragma unroll
+                for (int r = 1; r < RT; ++r) top[c] = fmaxf(top[c], fmaxf(x[r][c], x[r][c + 2]));
+            }
+            if (__any_sync(0xffffffffu, top[0] > m[0] + (kLazyLog2 + kRefBias) || top[1] > m[1] + (kLazyLog2 + kRefBias))) {
+                float a[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    top[c] = fmaxf(x[0][n][c], x[0][n][c + 2]);
 #pragma unroll
-                    for (int r = 1; r < RT; ++r) top[c] = fmaxf(top[c], fmaxf(x[r][n][c], x[r][n][c + 2]));
+                    for (int s = 4; s < 32; s <<= 1) top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], s));
+                    const bool up = top[c] > m[c] + (kLazyLog2 + kRefBias);
+                    const float to = top[c] - kRefBias;
+                    a[c] = up ? ex2(m[c] - to) : 1.f;  // an empty column (m = -inf): 0
+                    if (up) m[c] = to;
+                    l[c] *= a[c];
                 }
-                if (__any_sync(0xffffffffu, top[0] > m[n][0] + (kLazyLog2 + kRefBias) ||
-                                                top[1] > m[n][1] + (kLazyLog2 + kRefBias))) {
-                    float a[2];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-#pragma unroll
-                        for (int s = 4; s < 32; s <<= 1) top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], s));
-                        const bool up = top[c] > m[n][c] + (kLazyLog2 + kRefBias);
-                        const float to = top[c] - kRefBias;
-                        a[c] = up ? ex2(m[n][c] - to) : 1.f;  // an empty column (m = -inf): 0
-                        if (up) m[n][c] = to;
-                        l[n][c] *= a[c];
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2 * K; ++i) {
-                        o[n][i][0] *= a[0]; o[n][i][1] *= a[1]; o[n][i][2] *= a[0]; o[n][i][3] *= a[1];
-                    }
+                for (int i = 0; i < 2 * K; ++i) {
+                    o[i][0] *= a[0]; o[i][1] *= a[1]; o[i][2] *= a[0]; o[i][3] *= a[1];
                 }
-                const float u0 = m[n][0] == kNegInf ? 0.f : m[n][0];
-                const float u1 = m[n][1] == kNegInf ? 0.f : m[n][1];
+            }
+            const float u0 = m[0] == kNegInf ? 0.f : m[0];
+            const float u1 = m[1] == kNegInf ? 0.f : m[1];
+            uint32_t pb[RT][2];
 #pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    const float p0 = ex2(x[r][n][0] - u0), p1 = ex2(x[r][n][1] - u1);
-                    const float p2 = ex2(x[r][n][2] - u0), p3 = ex2(x[r][n][3] - u1);
-                    l[n][0] += fmaf(p2, iv[r][1], p0 * iv[r][0]);
-                    l[n][1] += fmaf(p3, iv[r][1], p1 * iv[r][0]);
-                    pb[r][n][0] = movmatrix_trans(pack_f16x2(p0, p1));
-                    pb[r][n][1] = movmatrix_trans(pack_f16x2(p2, p3));
-                }
+            for (int r = 0; r < RT; ++r) {
+                const float p0 = ex2(x[r][0] - u0), p1 = ex2(x[r][1] - u1);
+                const float p2 = ex2(x[r][2] - u0), p3 = ex2(x[r][3] - u1);
+                l[0] += fmaf(p2, iv[r][1], p0 * iv[r][0]);
+                l[1] += fmaf(p3, iv[r][1], p1 * iv[r][0]);
+                pb[r][0] = movmatrix_trans(pack_f16x2(p0, p1));
+                pb[r][1] = movmatrix_trans(pack_f16x2(p2, p3));
             }
 #pragma unroll
             for (int kk = 0; kk < K; ++kk)
@@ -513,11 +524,8 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
                     ldsm_x4_trans(s0 + r * tile_at + step(v_off, kk), w);
                     v_fragment<FMT>(w[0], w[1], a);
                     v_fragment<FMT>(w[2], w[3], b);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        mma_f16_16816(o[n][2 * kk], a, pb[r][n][0], pb[r][n][1]);
-                        mma_f16_16816(o[n][2 * kk + 1], b, pb[r][n][0], pb[r][n][1]);
-                    }
+                    mma_f16_16816(o[2 * kk], a, pb[r][0], pb[r][1]);
+                    mma_f16_16816(o[2 * kk + 1], b, pb[r][0], pb[r][1]);
                 }
             if (FMT == kE4m3 && partial) fence_proxy_async_smem();  // generic writes before the next TMA
         }
@@ -528,44 +536,43 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
             int32_t* st_role = reinterpret_cast<int32_t*>(base + L.st_x) + 2 * kMaxGroup;
             float* st_o = reinterpret_cast<float*>(base + (s0 - base_s));  // [warp][8][kOStride]
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int s = 4; s < 32; s <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], s);
+                for (int s = 4; s < 32; s <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], s);
             if (!consumer_sync(cbar, cphase, p.err, abort_flag)) break;  // all reads of the stage done
             const RowInfo ri = row_info<MQ>(p, md.b);
             StageMeta me = md;
             me.nr = ri.cnt * G;
             UnitPieces pc;
             pc.cf = 0; pc.su = 0; pc.n = 1; pc.every = true;
-            const GroupRange grs = group_of_cta(blockIdx.x, pfx, p.B, rows_per_seq<MQ>(p), p.Hkv, gridDim.x);
+            const GroupRange grs = *group;
             if (!(md.flags & kWholeUnit)) pc = unit_pieces(pfx, md.b, md.kvh, p.Hkv, p.unit_cost, grs);
             int role = kRoleAbort;
             bool stop = false;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {  // eight rows at a time
-                if (stop || 8 * n >= me.nr) continue;
-                // the previous tile's staged states are read: overwrite them
-                if (n > 0 && !consumer_sync(cbar, cphase, p.err, abort_flag)) { stop = true; continue; }
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int hr = 2 * t + c, h = 8 * n + hr;
-                    if (h >= me.nr) continue;
-                    if (g == 0) {
-                        // a NaN sum must not hide behind an empty reference
-                        st_m[warp * 16 + h] = l[n][c] == l[n][c] ? m[n][c] : 0.f;
-                        st_l[warp * 16 + h] = l[n][c];
-                    }
-                    float* r = st_o + (size_t)(warp * 8 + hr) * kOStride + 2 * g;
-#pragma unroll
-                    for (int i = 0; i < 2 * K; ++i)
-                        *reinterpret_cast<float2*>(r + 16 * i) = make_float2(o[n][i][c], o[n][i][2 + c]);
+            for (int c = 0; c < 2; ++c) {  // a warp's states of its eight rows
+                const int hr = 2 * t + c, h = 8 * tile + hr;
+                if (h >= me.nr) continue;
+                if (g == 0) {
+                    // a NaN sum must not hide behind an empty reference
+                    st_m[rw * 16 + h] = l[c] == l[c] ? m[c] : 0.f;
+                    st_l[rw * 16 + h] = l[c];
                 }
-                if (!rows_tile_merge<D, kThreadsC, 8, true>(p, me, n, ct, ticket, pc, grs, ri,
-                                                            UnitSlices<D, C::kWarps>{st_m, st_l, st_o}, st_role, cbar,
-                                                            cphase, abort_flag, role))
+                float* r = st_o + (size_t)(warp * 8 + hr) * kOStride + 2 * g;
+#pragma unroll
+                for (int i = 0; i < 2 * K; ++i)
+                    *reinterpret_cast<float2*>(r + 16 * i) = make_float2(o[i][c], o[i][2 + c]);
+            }
+            // one copy of the merge's code for both tiles: code that runs once a unit is fetched cold
+#pragma unroll 1
+            for (int n = 0; n < NT && 8 * n < me.nr; ++n) {
+                if (!rows_tile_merge<D, kThreadsC, 8, true>(
+                        p, me, n, ct, ticket, pc, grs, ri,
+                        UnitSlices<D, C::kRW>{st_m, st_l, st_o + (size_t)n * C::kRW * 8 * kOStride}, st_role, cbar, cphase,
+                        abort_flag, role)) {
                     stop = true;
+                    break;
+                }
             }
             if (stop) break;
             if (!consumer_sync(cbar, cphase, p.err, abort_flag)) break;
@@ -583,6 +590,7 @@ __global__ void __maxnreg__(168) quant_split_kernel(const __grid_constant__ Quan
     using C = QuantCfg<D, NT>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ int abort_flag;
+    __shared__ GroupRange group;  // of this CTA
     const uint32_t raw_s = smem_u32(smem_raw);
     const uint32_t base_s = (raw_s + 1023u) & ~1023u;
     uint8_t* base = smem_raw + (base_s - raw_s);
@@ -617,7 +625,7 @@ __global__ void __maxnreg__(168) quant_split_kernel(const __grid_constant__ Quan
         run_producer<C, QuantLoader<D, NT>, D, MODE>(p, base_s, L, pfx, meta, &abort_flag, begin, end, lane);
         return;
     }
-    run_quant_consumer<D, FMT, NT, MODE>(p, base_s, base, L, meta, pfx, &abort_flag, warp, lane);
+    run_quant_consumer<D, FMT, NT, MODE>(p, base_s, base, L, meta, pfx, &abort_flag, &group, warp, lane);
 }
 
 template <int D, int FMT, int NT, int MODE>

@@ -8,13 +8,22 @@
 
 namespace pda {
 
-// Shapes.  A consumer warp takes 16 KV rows of a stage per row tile.  Head
-// sizes up to 128 with 8 packed q rows run two CTAs of 4 consumer warps per
-// SM, two row tiles each; 16 packed q rows (n_tiles 2) and head size 256 run
-// one CTA of 8.
+// Shapes.  A consumer warp takes 16 KV rows of a stage per row tile, against
+// eight packed q rows.  Head sizes up to 128 run two CTAs of 4 such warps per
+// SM, two row tiles each; with 16 packed q rows (n_tiles 2) one CTA of 8, four
+// to each tile of q rows, over stages that both tiles share; head size 256 one
+// CTA of 8.  Measured against it, 32 sequences of 4096 tokens, 32 q and 8 kv
+// heads of 128, e4m3 (52.6 us): one CTA of 8 warps 53.8, 8 warps of one row
+// tile twice a SM (96 registers) 63.9, three CTAs at 128 registers 57.0, warps
+// with a ring each 51 to 57 (and 107 to 120 where the lengths are ragged: 107
+// here), two producer warps 53.9.  16 q rows, 4 queries on 2550 tokens: both
+// tiles in one warp's registers, which shares the conversions of V, 67.6 us;
+// two walks over the cache 65.4; this form 61.7 (int8 64.0, 72.4 and 66.5).
 PDA_HD constexpr int quant_warps(int D, int n_tiles) { return D == 256 || n_tiles == 2 ? 8 : 4; }
-PDA_HD constexpr int quant_row_tiles(int D, int n_tiles) { return D == 256 || n_tiles == 2 ? 1 : 2; }
-PDA_HD constexpr int quant_stage_rows(int D, int n_tiles) { return 16 * quant_warps(D, n_tiles) * quant_row_tiles(D, n_tiles); }
+PDA_HD constexpr int quant_row_tiles(int D, int n_tiles) { return D == 256 ? 1 : 2; }
+PDA_HD constexpr int quant_stage_rows(int D, int n_tiles) {
+    return 16 * quant_warps(D, n_tiles) / n_tiles * quant_row_tiles(D, n_tiles);
+}
 PDA_HD constexpr int quant_stage_bytes(int D, int n_tiles) {  // whole swizzle spans
     return (quant_stage_rows(D, n_tiles) * (2 * D + 8) + 8 * n_tiles * D * 2 + 1023) / 1024 * 1024;
 }
@@ -23,7 +32,12 @@ PDA_HD constexpr int quant_stages(int D, int n_tiles) { return n_tiles == 2 ? (D
 // fill whole 1024-byte spans (one box brings both where the pools' layout
 // allows it, with `joined`; else a box each).
 PDA_HD constexpr bool quant_boxes(int D, int bs, bool joined) { return (bs * D * (joined ? 2 : 1)) % 1024 == 0; }
-// Plan blocks added to every unit (see pda_plan.h), in quarter stages.
+// Plan blocks added to every unit (see pda_plan.h), in quarter stages: what the
+// preparation of its q rows and its merge cost a CTA (6000 and 7000 of the
+// 90000 cycles of a CTA with one unit of 30 stages).  64 sequences of 128 to
+// 32768 tokens take 108.6, 107.7, 109.1, 111 us at 6, 12, 20, 28; several
+// queries a sequence merge more rows (68.6 us at 12, 67.6 at 16).  Blocks below
+// 8 tokens come in so many copies that a stage takes as long as a unit's ends.
 PDA_HD int32_t quant_unit_cost(int D, int n_tiles, int bs, bool multi) {
     const int nb = quant_stage_rows(D, n_tiles) / bs;
     const int x4 = bs < 8 ? 2 : multi ? 16 : 12;
