@@ -13,7 +13,9 @@
 namespace pda {
 
 #define PDA_DEVERR_BAD_POSITION_ 0x8u
-constexpr int kHeadsThreads = 256;
+// 64, 128, 256: 450k tokens of 8 heads of 128 read back in 452, 410, 414 us, 64
+// tokens appended and 2900 read in 10.4, 9.3, 9.9.
+constexpr int kHeadsThreads = 128;
 
 // Where row t of a packed batch belongs: its sequence b, the end of the
 // sequence's rows and its length.  Warp-wide.  Up to 32 sequences the lanes
@@ -361,7 +363,7 @@ __device__ __forceinline__ int32_t turn_row(const HeadsParams& p, int64_t t, int
 // loads and the launch itself.
 constexpr int kRows = 2;
 template <int D, int FMT>
-__global__ void __launch_bounds__(kHeadsThreads, 4) heads_kernel(const __grid_constant__ HeadsParams p) {
+__global__ void __launch_bounds__(kHeadsThreads, 8) heads_kernel(const __grid_constant__ HeadsParams p) {
     constexpr int E = 4;
     using Work = RowWork<D, FMT, E>;
     const int nq = p.q.p ? p.Hq : 0, nk = p.k.p ? p.Hkv : 0, nv = FMT != kNoCache ? p.Hkv : 0;
@@ -570,8 +572,8 @@ __global__ void __launch_bounds__(kRingThreads) heads_ring_kernel(const __grid_c
 
 // Read-back: D / 16 lanes share a row of 16 elements each; a group takes HC
 // of a token's 2 Hkv rows, whose loads go out together.  Two bytes are written
-// for each byte read, and HBM bounds it: 377k tokens of 8 heads of 128 (int8,
-// blocks of 32; 1.4 GB read, 2.8 with what is written) take 416 us, the rate
+// for each byte read, and HBM bounds it: 450k tokens of 8 heads of 128 (int8,
+// blocks of 32; 0.9 GB read, 1.9 written) take 410 us, 6.8 TB/s, the rate
 // of a plain copy.  A small call is bound by its chain of loads: lengths, block
 // id, codes.
 template <int D, int FMT, bool F32, int HC>
@@ -746,7 +748,7 @@ cudaError_t launch_heads_fmt(int format, const HeadsParams& p, cudaStream_t stre
 
 template <int D, int FMT>
 cudaError_t launch_read_of(bool f32, const ReadParams& p, cudaStream_t stream) {
-    // two rows a group: 414 us for 377k tokens of 8 heads of 128 (1.4 GB), four 437, one 556
+    // two rows a group: 410 us for 450k tokens of 8 heads of 128, four 437, one 548
     constexpr int HC = 2;
     const int rows = (p.k_out ? p.Hkv : 0) + (p.v_out ? p.Hkv : 0);
     const int64_t items = p.rows * ((rows + HC - 1) / HC);

@@ -1909,13 +1909,12 @@ __device__ __forceinline__ void run_consumer_tc(const SplitParams& p, uint32_t b
 // ------------------------------------------------------------------ kernels
 
 // The flattened range [begin, end) of this CTA (pda_plan.h): in unit mode CTA
-// c takes unit c whole, otherwise its share of its row group's range.  Returns
-// the CTA's group (not used in unit mode).
+// c takes unit c whole, otherwise its share of its row group's range, split
+// over the first `ctas` CTAs.  Returns the CTA's group (not used in unit mode).
 template <int MODE>
 __device__ __forceinline__ GroupRange cta_range(const SplitParams& p, const int32_t* pfx, int32_t nv_max,
-                                                int stage_rows, int64_t* begin, int64_t* end) {
-    const GroupRange gr = group_of_cta(blockIdx.x, pfx, p.B, rows_per_seq<is_multi(MODE)>(p), p.Hkv,
-                                       gridDim.x);
+                                                int stage_rows, int64_t ctas, int64_t* begin, int64_t* end) {
+    const GroupRange gr = group_of_cta(blockIdx.x, pfx, p.B, rows_per_seq<is_multi(MODE)>(p), p.Hkv, ctas);
     const int64_t units = (int64_t)p.B * p.Hkv;
     if (unit_mode(units, gridDim.x, real_blocks(nv_max, p.unit_cost), stage_rows, p.bs)) {
         *begin = *end = 0;
@@ -2134,7 +2133,7 @@ __global__ void __maxnreg__(split_max_regs(D, MODE)) split_kernel(const __grid_c
     // ends with the main warps' barrier (which also publishes the stage barriers)
     const int32_t nv_max = build_prefix<is_multi(MODE), C::kMainThreads>(p, pfx, scan);
     int64_t begin, end;
-    const GroupRange gr = cta_range<MODE>(p, pfx, nv_max, C::kST, &begin, &end);
+    const GroupRange gr = cta_range<MODE>(p, pfx, nv_max, C::kST, gridDim.x, &begin, &end);
 
     if (warp == C::kConsumerWarps) {
         run_producer<C, Bf16Loader<D, ST, MODE>, D, MODE>(p, base_s, L, pfx, meta, &abort_flag, begin, end, lane);

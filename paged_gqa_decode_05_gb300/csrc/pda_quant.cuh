@@ -201,6 +201,19 @@ struct UnitSlices {
     }
 };
 
+// CTAs that a call's work is split over: not so many that a CTA gets less than
+// a stage, nor a unit more than about kMaxPieces pieces, which one CTA merges
+// four at a time (half a microsecond or more a round).  One sequence with one
+// kv head of 128: 2000 tokens take 79 us over the whole grid, 15 with a stage
+// at least to each CTA; 32768 tokens 103 without a bound on the pieces, 36, 29,
+// 34 with 64, 32, 16.  Eight kv heads, 32768 tokens: 25.3, 26.1, 33.7.
+constexpr int kMaxPieces = 40;
+template <bool MQ, int ST>
+__device__ __forceinline__ int64_t quant_plan_ctas(const SplitParams& p, const int32_t* pfx) {
+    const int64_t stages = ((int64_t)pfx[p.B] * p.Hkv * p.bs + ST - 1) / ST, units = (int64_t)p.B * p.Hkv;
+    return min((int64_t)gridDim.x, max(min(stages, units * kMaxPieces), (int64_t)rows_per_seq<MQ>(p)));
+}
+
 // Two fp16 values from bytes lo, hi (0..3) of x.  int8: x holds code ^ 0x80;
 // the byte under 0x64 reads as 1024 + code + 128.
 template <int FMT, int lo, int hi>
@@ -316,7 +329,8 @@ __device__ __forceinline__ bool quant_q_fragments(uint8_t* at, float* back, int 
 template <int D, int FMT, int NT, int MODE>
 __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_t base_s, uint8_t* base,
                                                    const SmemLayout& L, const StageMeta* meta, const int32_t* pfx,
-                                                   volatile int* abort_flag, GroupRange* group, int warp, int lane) {
+                                                   volatile int* abort_flag, const GroupRange* group, int warp,
+                                                   int lane) {
     using C = QuantCfg<D, NT>;
     constexpr int S = C::kStages, RT = C::kRT, K = C::kK;
     constexpr int kThreadsC = C::kWarps * 32, kOStride = D + 4;
@@ -375,8 +389,6 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
     uint32_t phase = 0;
     int32_t ticket = 0;
     const int ct = warp * 32 + lane;
-    // out of the loop (600 cycles a unit); the syncs of the first unit's q rows order it
-    if (ct == 0) *group = group_of_cta(blockIdx.x, pfx, p.B, rows_per_seq<MQ>(p), p.Hkv, gridDim.x);
     zero_empty_rows<D, kThreadsC>(p, pfx, ct);
 
     while (true) {
@@ -545,7 +557,7 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
             me.nr = ri.cnt * G;
             UnitPieces pc;
             pc.cf = 0; pc.su = 0; pc.n = 1; pc.every = true;
-            const GroupRange grs = *group;
+            const GroupRange grs = *group;  // of units in pieces
             if (!(md.flags & kWholeUnit)) pc = unit_pieces(pfx, md.b, md.kvh, p.Hkv, p.unit_cost, grs);
             int role = kRoleAbort;
             bool stop = false;
@@ -620,7 +632,11 @@ __global__ void __maxnreg__(168) quant_split_kernel(const __grid_constant__ Quan
     pdl_launch_dependents();
     const int32_t nv_max = build_prefix<is_multi(MODE), C::kMainThreads>(p, pfx, scan);
     int64_t begin, end;
-    cta_range<MODE>(p, pfx, nv_max, C::kST, &begin, &end);
+    int64_t ctas = gridDim.x;
+    const bool by_unit = unit_mode((int64_t)p.B * p.Hkv, ctas, real_blocks(nv_max, p.unit_cost), C::kST, p.bs);
+    if (!by_unit) ctas = quant_plan_ctas<is_multi(MODE), C::kST>(p, pfx);
+    const GroupRange gr = cta_range<MODE>(p, pfx, nv_max, C::kST, ctas, &begin, &end);
+    if (tid == 0 && !by_unit) group = gr;  // out of registers; the syncs of the first unit's q rows order it
     if (warp == C::kWarps) {
         run_producer<C, QuantLoader<D, NT>, D, MODE>(p, base_s, L, pfx, meta, &abort_flag, begin, end, lane);
         return;

@@ -348,7 +348,7 @@ def test_read_cache_bad_pages():
 # ------------------------------------------------------------------ decode
 
 LENS = {"tiny": [37, 80], "edges": [0, 1, 15, 16, 17, 63, 64, 65, 127, 128, 129], "long": [4000, 3, 9001],
-        "many": [(37 * i) % 200 for i in range(60)]}
+        "many": [(37 * i) % 200 for i in range(60)], "few": [943, 0, 2000], "one": [9001]}
 
 
 @pytest.mark.parametrize("dtype", ref.FORMATS)
@@ -357,7 +357,9 @@ LENS = {"tiny": [37, 80], "edges": [0, 1, 15, 16, 17, 63, 64, 65, 127, 128, 129]
     (4, 2, 64, 16, "tiny"), (8, 2, 128, 16, "edges"), (16, 2, 256, 16, "edges"), (8, 1, 64, 8, "edges"),
     (5, 1, 128, 32, "long"), (12, 4, 128, 1, "edges"), (2, 2, 64, 2, "edges"), (8, 4, 256, 4, "edges"),
     (3, 1, 256, 64, "long"), (16, 8, 128, 16, "many"), (8, 8, 128, 4, "edges"),
-    # batches whose units hold two or four kv heads
+    # few units, in many pieces each
+    (8, 1, 128, 16, "few"), (4, 1, 256, 4, "few"), (8, 1, 64, 16, "few"), (5, 1, 128, 1, "few"), (8, 1, 128, 16, "one"),
+    # many sequences
     (12, 6, 64, 32, "many"), (16, 4, 256, 8, "many"), (8, 8, 64, 64, "many"), (32, 4, 128, 32, "many"),
     (8, 4, 256, 4, "many"), (4, 4, 128, 4, "many"), (6, 2, 128, 64, "many")])
 def test_decode(dtype, q_len, hq, hkv, d, bs, lens):
