@@ -265,7 +265,7 @@ __device__ __forceinline__ void v_fragment(uint32_t r0, uint32_t r1, uint32_t (&
 // two, times the score scale.  A warp takes a row, an eighth of the work of
 // every warp preparing all of its own fragments, whose reads at a row's stride
 // also met on the same banks; both run once a unit and are fetched cold (16 q
-// rows, 2550 tokens: 67.5 -> 66.7 us).
+// rows, 2456 tokens: 67.5 -> 66.7 us).
 template <int D, int FMT, int NT, int W>
 __device__ __forceinline__ bool quant_q_fragments(uint8_t* at, float* back, int nr, float scale, int warp, int lane,
                                                   uint32_t cbar, uint32_t& cphase, uint32_t* err,

@@ -16,7 +16,7 @@ namespace pda {
 // heads of 128, e4m3 (52.6 us): one CTA of 8 warps 53.8, 8 warps of one row
 // tile twice a SM (96 registers) 63.9, three CTAs at 128 registers 57.0, warps
 // with a ring each 51 to 57 (and 107 to 120 where the lengths are ragged: 107
-// here), two producer warps 53.9.  16 q rows, 4 queries on 2550 tokens: both
+// here), two producer warps 53.9.  16 q rows, 4 queries on 2456 tokens: both
 // tiles in one warp's registers, which shares the conversions of V, 67.6 us;
 // two walks over the cache 65.4; this form 61.7 (int8 64.0, 72.4 and 66.5).
 PDA_HD constexpr int quant_warps(int D, int n_tiles) { return D == 256 || n_tiles == 2 ? 8 : 4; }
