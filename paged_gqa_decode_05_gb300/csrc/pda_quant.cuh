@@ -35,7 +35,12 @@
 namespace pda {
 
 constexpr float kRefBias = 6.f;
-constexpr float kLeastScale = 7.7037198e-34f;  // 2^-110: a scale of 0 counts as this, its codes are 0
+// V scales below 2^-60 count as this (the codes of a scale of 0 are 0; others'
+// elements are off by 448 * 2^-60 = 4e-16 at most).  A row adds p' / vs to the
+// sum of weights, 2^(kRefBias + kLazyLog2 + 60) at most, so 2^31 rows stay
+// inside fp32; with 2^-110, the least scale that is written, 500 rows of zeros
+// could pass it.
+constexpr float kLeastScale = 8.6736174e-19f;
 
 template <int D, int NT>
 struct QuantCfg {

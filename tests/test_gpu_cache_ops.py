@@ -430,6 +430,32 @@ def test_decode_garbage_behind_the_end():
     assert torch.equal(ctx.decode(q, kp.cuda(), vp.cuda(), *rest, scales=sc.cuda()), want)
 
 
+@pytest.mark.parametrize("dtype", ref.FORMATS)
+@pytest.mark.parametrize("hq,d", [(4, 64), (8, 128)])
+def test_decode_after_thousands_of_zero_values(dtype, hq, d):
+    """Rows of scale 0 count in the softmax's sum and add nothing, however many there are before the first value: every
+    unit whole in one CTA, whose weights of thousands of such rows add up."""
+    g, rng = gen(41), np.random.default_rng(41)
+    batch, hkv, bs, n = 400, 1, 16, 6000
+    table, pool = ref.sequences(rng, [n], bs)
+    kp, vp, sc = ref.random_cache(g, pool, bs, hkv, d, dtype)
+    blocks = table[0].long()
+    vp.view(torch.uint8)[blocks[:-8]] = 0
+    sc[blocks[:-8], :, 1] = 0
+    # scores 0 for 256 tokens, then 5.4 (7.8 in base 2): the weights after the first stages stay short of a new reference
+    q = torch.ones((1, hq, d), dtype=torch.bfloat16)
+    kp[:] = torch.ones((), dtype=torch.float32).to(dtype)
+    sc[blocks, :, 0] = 5.4 / d ** 0.5
+    sc[blocks[:16], :, 0] = 0
+    ctx = ctx_of(hq, hkv, d, bs, max_seqs=batch)
+    out = ctx.decode(q.repeat(batch, 1, 1).cuda(), kp.cuda(), vp.cuda(), table.repeat(batch, 1).cuda(),
+                     torch.full((batch,), n, dtype=torch.int32).cuda(), scales=sc.cuda(), out_dtype=torch.float32)
+    want, size = ref.decode64(q[:, None], kp, vp, sc, table, [n], bs)
+    for b in range(0, batch, 57):
+        within(out[b:b + 1], want[:, 0], DECODE * size[:, 0])
+    assert ctx.read_device_errors() == 0
+
+
 # ------------------------------------------------------------------ together
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16] + ref.FORMATS)
