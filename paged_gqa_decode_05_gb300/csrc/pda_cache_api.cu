@@ -177,16 +177,14 @@ bool encode_scales(const pda_dims& d, const pda_cache* c, CUtensorMap* tm) {
                                      CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How a call's pools load: encodes the context's maps, or returns false where
+// How a call's pools load: encodes the launch's maps, or returns false where
 // boxes do not fit (then rows are copied one by one).
-bool encode_boxes(pda_ctx* ctx, const pda_cache* c) {
-    const pda_dims& d = ctx->dims;
+bool encode_boxes(const pda_dims& d, const pda_cache* c, pda::QuantParams* p) {
     if (d.block_size < 4) return false;  // four blocks' scales must fill the 128 bytes a copy starts on
-    if (!encode_scales(d, c, &ctx->quant_s)) return false;
-    ctx->quant_joined = pda::quant_boxes(d.head_dim, d.block_size, true) && encode_joined(d, c, &ctx->quant_k);
-    return ctx->quant_joined ||
-           (pda::quant_boxes(d.head_dim, d.block_size, false) && encode_apart(d, c->k_pool, c, &ctx->quant_k) &&
-            encode_apart(d, c->v_pool, c, &ctx->quant_v));
+    if (!encode_scales(d, c, &p->tm_k1)) return false;
+    p->joined = pda::quant_boxes(d.head_dim, d.block_size, true) && encode_joined(d, c, &p->tm_k);
+    return p->joined || (pda::quant_boxes(d.head_dim, d.block_size, false) && encode_apart(d, c->k_pool, c, &p->tm_k) &&
+                         encode_apart(d, c->v_pool, c, &p->tm_v));
 }
 
 pda_status run_quant(pda_ctx* ctx, const pda_bf16* q, const pda_cache* c, const int32_t* table, int32_t max_blocks,
@@ -208,22 +206,8 @@ pda_status run_quant(pda_ctx* ctx, const pda_bf16* q, const pda_cache* c, const 
     if (Qr > grid) return fail(PDA_ERR_INVALID_ARG, "q_len %d: more launch rows per sequence than CTAs (%d)", q_len, grid);
     p.unit_cost = pda::quant_unit_cost(D, tiles, bs, multi);
     if ((st = pda::check_plan_size((int64_t)batch * q_len, max_blocks, p.unit_cost)) != PDA_OK) return st;
-    const pda_pool_key key = {c->k_pool, c->v_pool, c->num_blocks, c->blk_stride, c->tok_stride, c->kvh_stride};
-    const pda_pool_key& was = ctx->quant_key;
-    if (!(ctx->quant_maps_valid && ctx->quant_scales == c->scales && was.k == key.k && was.v == key.v &&
-          was.num_blocks == key.num_blocks && was.blk == key.blk && was.tok == key.tok && was.kvh == key.kvh)) {
-        ctx->quant_maps_valid = false;
-        ctx->quant_row_mode = encode_boxes(ctx, c) ? 0 : 2;
-        ctx->quant_scales = c->scales;
-        ctx->quant_key = key;
-        ctx->quant_maps_valid = true;
-    }
-    p.tm_k = ctx->quant_k;
-    p.tm_v = ctx->quant_v;
-    p.tm_k1 = ctx->quant_s;
-    p.row_gather = ctx->quant_row_mode;
-    p.joined = ctx->quant_joined;
-    p.v_first = ctx->quant_joined && c->v_pool < c->k_pool;
+    p.row_gather = encode_boxes(d, c, &p) ? 0 : 2;
+    p.v_first = p.joined && c->v_pool < c->k_pool;
     p.box_head = D == 256 ? 2 : 1;
     p.num_blocks = c->num_blocks;
     p.k_base = static_cast<const uint16_t*>(c->k_pool);
@@ -244,7 +228,7 @@ pda_status run_quant(pda_ctx* ctx, const pda_bf16* q, const pda_cache* c, const 
     p.G = G;
     p.rows_per_slot = qp * G;
     p.bs = bs;
-    p.prefetch = ctx->quant_row_mode == 0 && bs >= 8 && Qr == 1;
+    p.prefetch = p.row_gather == 0 && bs >= 8 && Qr == 1;
 
     // launch rows per chunk (whole sequences), as many as the partial states allow
     const int64_t fit = (ctx->part_rows / p.rows_per_slot - grid) / p.Hkv;

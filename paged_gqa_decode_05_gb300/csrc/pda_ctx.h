@@ -73,14 +73,8 @@ struct pda_ctx {
     CUtensorMap map_k, map_v;
     CUtensorMap map_k1, map_v1;  // one-slab boxes (head size 128, block boxes): the tcgen05 form
     // Decode over 8-bit caches: grids with up to 8 and 16 packed q rows per
-    // walk (0: not on this shape) and the last pool's tensor maps.
+    // walk (0: not on this shape).
     int quant_ctas[2] = {0, 0};
-    bool quant_maps_valid = false;
-    pda_pool_key quant_key;
-    int32_t quant_row_mode = 0;
-    bool quant_joined = false;  // quant_k brings K and V rows
-    const void* quant_scales = nullptr;
-    CUtensorMap quant_k, quant_v, quant_s;
 };
 
 namespace pda {

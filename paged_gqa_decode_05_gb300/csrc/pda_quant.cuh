@@ -625,9 +625,10 @@ __global__ void __maxnreg__(168) quant_split_kernel(const __grid_constant__ Quan
         fence_mbar_init();
         abort_flag = 0;
     }
-    if (tid == C::kWarps * 32) {
+    if (tid == C::kWarps * 32 && p.row_gather == 0) {
         prefetch_tensormap(&p.tm_k);
-        prefetch_tensormap(&p.tm_v);
+        prefetch_tensormap(&p.tm_k1);
+        if (!p.joined) prefetch_tensormap(&p.tm_v);
     }
     if (warp == C::kMainThreads / 32) {  // the prefetch warp: joins nothing below
         if (p.prefetch) prefetch_first_stages<MODE, TouchQuant<D, NT>>(p, lane);
