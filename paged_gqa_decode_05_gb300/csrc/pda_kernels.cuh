@@ -179,7 +179,7 @@ template <bool MQ>
 __device__ __forceinline__ int32_t tokens_of(const SplitParams& p, int s, int32_t L) {
     if constexpr (!MQ) return L;
     const RowInfo r = row_info<MQ>(p, s);
-    const int32_t len = L - p.q_len + r.first + r.cnt;
+    const int32_t len = max(L, 0) - p.q_len + r.first + r.cnt;
     return len < 0 ? 0 : len;
 }
 
@@ -195,7 +195,7 @@ __device__ __forceinline__ int32_t blocks_of(const SplitParams& p, int b, int32_
         }
         return len;
     }
-    if (len < 0) {
+    if (L < 0) {
         if (FLAG) atomicOr(p.err, PDA_DEVERR_BAD_LENGTH_);
         len = 0;
     }

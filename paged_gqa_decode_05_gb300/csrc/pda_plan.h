@@ -153,7 +153,7 @@ PDA_HD int32_t real_blocks(int32_t nv, int32_t unit_cost) { return nv > 0 ? nv -
 
 // Blocks needed for a length in tokens.
 PDA_HD int32_t blocks_for_tokens(int32_t len, int32_t block_size) {
-    return len <= 0 ? 0 : (len + block_size - 1) / block_size;
+    return len <= 0 ? 0 : (int32_t)(((uint32_t)len + (uint32_t)block_size - 1u) / (uint32_t)block_size);
 }
 
 template <typename Pfx>

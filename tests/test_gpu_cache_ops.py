@@ -430,6 +430,69 @@ def test_decode_garbage_behind_the_end():
     assert torch.equal(ctx.decode(q, kp.cuda(), vp.cuda(), *rest, scales=sc.cuda()), want)
 
 
+@pytest.mark.parametrize("q_len", [1, 4])
+@pytest.mark.parametrize("bs,d", [(16, 128), (1, 64), (4, 256)])
+def test_decode_bad_pages_are_flagged(bs, d, q_len):
+    """Block ids outside the pool and lengths past the table raise their flag; the other sequences are as without them."""
+    g, rng = gen(43), np.random.default_rng(43)
+    hq, hkv, lens = 4, 1, [70, 33, 64]
+    table, pool = ref.sequences(rng, lens, bs)
+    kp, vp, sc = ref.random_cache(g, pool, bs, hkv, d, torch.int8)
+    q = torch.randn((3, q_len, hq, d), generator=g).bfloat16().cuda()
+    ctx = ctx_of(hq, hkv, d, bs, max_seqs=3 * q_len)
+    cache = [x.cuda() for x in (kp, vp)]
+
+    def run(table, lens):
+        lens = torch.tensor(lens, dtype=torch.int32).cuda()
+        return ctx.decode_multi(q, *cache, table.cuda(), lens, scales=sc.cuda())
+
+    want = run(table, lens)
+    assert ctx.read_device_errors() == 0
+    for bad in (-1, pool, 2 ** 31 - 1):
+        broken = table.clone()
+        broken[1, 0] = bad
+        out = run(broken, lens)
+        assert ctx.read_device_errors() == pda.DEVERR_BAD_BLOCK_ID
+        assert torch.equal(out[0], want[0]) and torch.equal(out[2], want[2])
+    for bad in (-5, table.shape[1] * bs + 1, 2 ** 31 - 1):
+        out = run(table, [lens[0], bad, lens[2]])
+        assert ctx.read_device_errors() == pda.DEVERR_BAD_LENGTH
+        within(out[::2], want[::2].double().cpu(), 4 * BF16 * (1 + want[::2].double().cpu().abs()))
+
+
+def test_captured_decodes_of_split_units_replay():
+    """Two graphs of one context with units in many pieces, whose lengths change between replays."""
+    g, rng = gen(44), np.random.default_rng(44)
+    hq, hkv, d, bs = 8, 1, 128, 16
+    table, pool = ref.sequences(rng, [4000], bs)
+    kp, vp, sc = (x.cuda() for x in ref.random_cache(g, pool, bs, hkv, d, torch.float8_e4m3fn))
+    table = table.cuda()
+    q = torch.randn((1, 3, hq, d), generator=g).bfloat16().cuda()
+    ctx, other = (ctx_of(hq, hkv, d, bs, max_seqs=3) for _ in range(2))
+    lens = torch.tensor([3999], dtype=torch.int32).cuda()
+    outs = [torch.empty((1, hq, d), dtype=torch.bfloat16, device="cuda"), torch.empty_like(q)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    last = q[:, 2].contiguous()
+    with torch.cuda.graph(graphs[0], stream=side):
+        ctx.decode(last, kp, vp, table, lens, scales=sc, out=outs[0])
+    with torch.cuda.graph(graphs[1], stream=side):
+        ctx.decode_multi(q, kp, vp, table, lens, scales=sc, out=outs[1])
+    for n in (3999, 4000, 0, 1, 700, 2500):
+        lens.fill_(n)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for i in (0, 1, 0, 1, 1, 0):
+                graphs[i].replay()
+        side.synchronize()
+        assert torch.equal(outs[0], other.decode(last, kp, vp, table, lens, scales=sc))
+        assert torch.equal(outs[1], other.decode_multi(q, kp, vp, table, lens, scales=sc))
+        want, size = ref.decode64(q.cpu(), kp.cpu(), vp.cpu(), sc.cpu(), table.cpu(), [n], bs)
+        within(outs[1], want, BF16 * want.abs() + 2 * DECODE * size)
+    assert ctx.read_device_errors() == 0 and other.read_device_errors() == 0
+
+
 @pytest.mark.parametrize("dtype", ref.FORMATS)
 @pytest.mark.parametrize("hq,d", [(4, 64), (8, 128)])
 def test_decode_after_thousands_of_zero_values(dtype, hq, d):
