@@ -223,6 +223,30 @@ def test_append_prompts(dtype, hq, hkv, d, bs, rotary, times):
         check_written(kp.cpu(), sc.cpu(), 0, before, want, size, places, bs)
 
 
+@pytest.mark.parametrize("batch", [1, 2, 31, 32, 33, 64, 65, 100, 1000])
+def test_append_then_read_any_batch(batch):
+    """Whole prompts of 0 to 9 tokens written and read back: every token of every sequence in its row."""
+    rng, g = np.random.default_rng(batch), gen(batch)
+    hkv, d, bs = 2, 64, 4
+    for lens in (rng.integers(0, 10, batch), np.where(rng.random(batch) < 0.8, 0, 7), np.ones(batch, dtype=int)):
+        lens = [int(n) for n in lens]
+        table, pool = ref.sequences(rng, lens, bs)
+        total = sum(lens)
+        kv = qkv_of(g, total + 3, 0, hkv, d)
+        ctx = ctx_of(2, hkv, d, bs, max_seqs=batch)
+        kp, vp, _ = ctx.new_cache(pool, torch.bfloat16)
+        starts = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32).cuda()
+        lens_d = torch.tensor(lens, dtype=torch.int32).cuda()
+        ctx.append(kv[:, :hkv], kv[:, hkv:], kp, vp, table.cuda(), lens_d, starts=starts)
+        k, v = (torch.full((total + 3, hkv, d), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        ctx.read_cache(kp, vp, table.cuda(), lens_d, starts=starts, k_out=k, v_out=v)
+        assert ctx.read_device_errors() == 0
+        assert torch.equal(k[:total], kv[:total, :hkv]) and torch.equal(v[:total], kv[:total, hkv:])
+        assert (k[total:] == 3).all() and (v[total:] == 3).all()
+        used = sum(int(p.float().abs().sum((2, 3)).count_nonzero()) for p in (kp, vp))
+        assert used == 2 * total
+
+
 @pytest.mark.parametrize("dtype", ref.FORMATS)
 def test_append_without_starts_and_with_positions(dtype):
     """Equal shares per sequence; an explicit rotation position; a sequence shorter than its share."""
