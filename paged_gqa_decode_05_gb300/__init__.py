@@ -342,13 +342,15 @@ class Context:
             CACHE_BF16 if dtype is torch.bfloat16 else None
         if fmt is None or v_pool.dtype is not dtype:
             raise ValueError("k_pool / v_pool must both be bfloat16, float8_e4m3fn or int8")
-        self._here(k_pool, "k_pool")
-        self._here(v_pool, "v_pool")
+        if k_pool.get_device() != self._index or v_pool.get_device() != self._index:
+            self._here(k_pool, "k_pool")
+            self._here(v_pool, "v_pool")
         bs, hkv, hd = d.block_size, d.num_kv_heads, d.head_dim
         if strides is None:
-            num_blocks = k_pool.size(0)
-            shape = (num_blocks, bs, hkv, hd)
-            if k_pool.shape != shape or v_pool.shape != shape or not k_pool.is_contiguous() or not v_pool.is_contiguous():
+            shape = k_pool.shape
+            num_blocks = shape[0]
+            if shape != (num_blocks, bs, hkv, hd) or v_pool.shape != shape or not k_pool.is_contiguous() or \
+                    not v_pool.is_contiguous():
                 raise ValueError(f"k_pool / v_pool must be contiguous [num_blocks, {bs}, {hkv}, {hd}], alike")
             strides = (bs * hkv * hd, hkv * hd, hd)
         elif num_blocks is None:
@@ -396,18 +398,16 @@ class Context:
 
     def _sequences(self, block_table, seq_lens, starts):
         """Checks a block table, its lengths and token starts; returns (table width, sequences)."""
-        self._i32(block_table, "block_table", 2)
-        self._i32(seq_lens, "seq_lens", 1)
-        self._here(block_table, "block_table")
-        self._here(seq_lens, "seq_lens")
+        i32, on = _torch().int32, self._index
+        for t, name, ndim in ((block_table, "block_table", 2), (seq_lens, "seq_lens", 1), (starts, "starts", 1)):
+            if t is not None and (t.dtype is not i32 or t.get_device() != on or t.dim() != ndim or not t.is_contiguous()):
+                self._here(self._i32(t, name, ndim), name)
         B = seq_lens.size(0)
         rows, width = block_table.shape
         if rows != B:
             raise ValueError("block_table must have one row per sequence")
-        if starts is not None:
-            self._here(self._i32(starts, "starts", 1), "starts")
-            if starts.size(0) != B + 1:
-                raise ValueError("starts must hold one entry per sequence and the end")
+        if starts is not None and starts.size(0) != B + 1:
+            raise ValueError("starts must hold one entry per sequence and the end")
         return width, B
 
     def _scale(self, scale) -> float:
@@ -670,20 +670,22 @@ class Context:
             k_out, v_out = (torch.zeros((B, width * d.block_size, d.num_kv_heads, d.head_dim), device=self.device,
                                         dtype=out_dtype or torch.bfloat16) for _ in range(2))
         like = v_out if k_out is None else k_out
-        shape, dtype = like.shape, like.dtype
+        shape, dtype, ndim = like.shape, like.dtype, 4 if starts is None else 3
+        good = (dtype is torch.bfloat16 or dtype is torch.float32) and (out_dtype is None or out_dtype is dtype) and \
+            len(shape) == ndim and shape[-2] == d.num_kv_heads and shape[-1] == d.head_dim and \
+            (starts is not None or shape[0] == B)
         for t in (k_out, v_out):
             if t is None:
                 continue
-            if (dtype is not torch.bfloat16 and dtype is not torch.float32) or t.dtype is not (out_dtype or dtype) or \
-                    t.shape != shape or not t.is_contiguous() or len(shape) != (4 if starts is None else 3) or \
-                    shape[-2] != d.num_kv_heads or shape[-1] != d.head_dim or (starts is None and shape[0] != B):
+            if not good or (t is not like and (t.dtype is not dtype or t.shape != shape)) or not t.is_contiguous():
                 raise ValueError("k_out / v_out must be contiguous bfloat16 or float32 "
                                  f"[{'B, S' if starts is None else 'rows'}, {d.num_kv_heads}, {d.head_dim}], alike")
-            self._here(t, "k_out / v_out")
+            if t.get_device() != self._index:
+                self._here(t, "k_out / v_out")
         rows = shape[0] * shape[1] if starts is None else shape[0]
         status = lib().pda_read_cache(self._ctx, ctypes.addressof(cache), block_table.data_ptr(), width,
                                       seq_lens.data_ptr(), B, _ptr(starts), rows, _ptr(k_out), _ptr(v_out),
-                                      int(dtype is torch.float32), self._stream_of(stream))
+                                      dtype is torch.float32, self._stream_of(stream))
         if status:
             _check(status)
         return k_out, v_out

@@ -204,7 +204,7 @@ pda_status run_quant(pda_ctx* ctx, const pda_bf16* q, const pda_cache* c, const 
     const pda::QuantShape shape = pda::quant_shape(D, c->format, tiles, multi);
     const int grid = ctx->quant_ctas[tiles - 1];
     if (Qr > grid) return fail(PDA_ERR_INVALID_ARG, "q_len %d: more launch rows per sequence than CTAs (%d)", q_len, grid);
-    p.unit_cost = pda::quant_unit_cost(D, tiles, bs, multi);
+    p.unit_cost = pda::quant_unit_cost(D, tiles, bs);
     if ((st = pda::check_plan_size((int64_t)batch * q_len, max_blocks, p.unit_cost)) != PDA_OK) return st;
     p.row_gather = encode_boxes(d, c, &p) ? 0 : 2;
     p.v_first = p.joined && c->v_pool < c->k_pool;

@@ -35,13 +35,13 @@ PDA_HD constexpr bool quant_boxes(int D, int bs, bool joined) { return (bs * D *
 // Plan blocks added to every unit (see pda_plan.h), in quarter stages: what the
 // preparation of its q rows and its merge cost a CTA (6000 and 7000 of the
 // 90000 cycles of a CTA with one unit of 30 stages).  64 sequences of 128 to
-// 32768 tokens take 108.6, 107.7, 109.1, 111 us at 6, 12, 20, 28; several
-// queries a sequence merge more rows (68.6 us at 12, 67.6 at 16).  Blocks below
-// 8 tokens come in so many copies that a stage takes as long as a unit's ends.
-PDA_HD int32_t quant_unit_cost(int D, int n_tiles, int bs, bool multi) {
-    const int nb = quant_stage_rows(D, n_tiles) / bs;
-    const int x4 = bs < 8 ? 2 : multi ? 16 : 12;
-    return nb * x4 / 4 < 1 ? 1 : nb * x4 / 4;
+// 32768 tokens take 106.3, 106.1, 107.7, 110.5 us at 6, 9 to 12, 16, 28; 4
+// queries on 2456 tokens each 61.1, 60.7, 61.3, 63.2 at 8, 12, 16, 24.  Blocks
+// below 8 tokens come in so many copies that a stage takes as long as a unit's
+// ends.
+PDA_HD int32_t quant_unit_cost(int D, int n_tiles, int bs) {
+    const int nb = quant_stage_rows(D, n_tiles) / bs, x4 = nb * (bs < 8 ? 2 : 12);
+    return x4 < 4 ? 1 : x4 / 4;
 }
 
 struct QuantParams : SplitParams {
