@@ -409,31 +409,34 @@ __global__ void __launch_bounds__(kHeadsThreads, 8) heads_kernel(const __grid_co
 // Many tokens: one persistent CTA per SM streams them through a ring of
 // shared-memory slots, a token's rows (and its row of cosines and sines) to a
 // slot.  A producer warp looks 32 tokens up at a time and issues their bulk
-// copies, kTeams teams of kTeamWarps warps take the slots in turn and write
-// straight to memory.  The copies in flight do not depend on occupancy;
-// loading rows to registers instead, with 32 warps an SM, came to 3.9 TB/s on
-// 8191 tokens of 72 heads of 128 and no arrangement of rows per thread passed
-// it.  HBM bounds it: 8191 tokens of 64 + 8 heads of 128 take 51 us (5.9 TB/s
-// read and written), ragged prompts of 24 sequences (20k tokens of 32 + 2 * 8
-// heads, e4m3 cache) 79 us (5.9 TB/s).  Teams of 2, 3 and 4 warps (8, 5, 4 of
-// them): 53.5, 51, 52 us on the first.
+// copies, teams of warps take the slots in turn and write straight to memory.
+// The copies in flight do not depend on occupancy; loading rows to registers
+// instead, with 32 warps an SM, came to 3.9 TB/s on 8191 tokens of 72 heads of
+// 128 and no arrangement of rows per thread passed it.  HBM bounds it: those
+// tokens take 51 us (5.9 TB/s read and written), ragged prompts of 24
+// sequences (20k tokens of 32 + 2 * 8 heads, e4m3 cache) 79 us (5.8 TB/s).
 //
+// Slots of kSmallSlot bytes and more: teams of three warps (teams of 2 and 4
+// took 53.5 and 52 us on the first), copies issued by one lane after another.
 // The first fill is paced: kFillPace bytes a cycle and SM are about the share
 // of HBM that reads get once stores run too.  Issued all at once, the copies
 // delay each other, the first slot lands late and the stores start late (4096
 // tokens of 40 heads of 128: 19.4 us at once, 18.1 paced; 12 bytes 18.0, 9
-// bytes 18.6).  Slots below kSmallSlot bytes are issued kIssue at a time,
-// since one lane's issue (0.3 us a token) is slower than their traffic (4096
-// tokens of 9 heads of 128: 8.6 us, one at a time 11.4).
+// bytes 18.6).
+// Smaller slots: each warp a team of its own and kIssue lanes issuing at once,
+// since one lane's issue (0.3 us a token) and a team's turn are longer than
+// their traffic takes (8000 tokens of 16 + 2 * 2 heads of 128 appended: 20.1
+// us, as large slots 25.5; of 20 + 2 * 4 heads, past the border, 27.2 and 24.6).
 //
 // A slot belongs to one team (slots are a multiple of the teams at work): the
 // team that waits for a slot's next token has itself seen the previous one
 // land.  Copies land in any order, so another team could be a whole turn of
 // the slot ahead and take the barrier's older phase for the one it waits for.
-constexpr int kTeams = 5, kTeamWarps = 3, kMaxSlots = 20;
-constexpr uint32_t kFillPace = 16, kSmallSlot = 4096, kIssue = 4;
-constexpr int kRingThreads = (kTeams * kTeamWarps + 1) * 32;
+constexpr int kRingWarps = 15, kMaxSlots = 30, kIssue = 4;
+constexpr uint32_t kFillPace = 16;
+constexpr int kRingThreads = (kRingWarps + 1) * 32;
 static_assert(kMaxSlots <= 32, "the first fill is the producer's first 32 tokens");
+static_assert(32 % kIssue == 0, "lanes that issue together belong to one look-up");
 struct SlotMeta {
     Spot at;
     int32_t t;  // -1: padding
@@ -457,7 +460,7 @@ __global__ void __launch_bounds__(kRingThreads) heads_ring_kernel(const __grid_c
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(bars0 + 8 * s, 1);
-            mbar_init(bars0 + 8 * (S + s), kTeamWarps);
+            mbar_init(bars0 + 8 * (S + s), p.team_warps);
         }
         fence_mbar_init();
         abort_flag = 0;
@@ -466,7 +469,7 @@ __global__ void __launch_bounds__(kRingThreads) heads_ring_kernel(const __grid_c
     pdl_wait_primary();
     pdl_launch_dependents();
     const int32_t n = (int32_t)((p.T - blockIdx.x + gridDim.x - 1) / gridDim.x);  // tokens blockIdx.x, + gridDim.x, ..
-    if (warp == kTeams * kTeamWarps) {
+    if (warp == kRingWarps) {
         // side by side (one fused projection's output): one copy brings all of a token
         const bool joined = nq && nk && p.k.p == p.q.p + nq * D && p.k.tok == p.q.tok &&
                             (!nv || (p.v.p == p.k.p + nk * D && p.v.tok == p.q.tok));
@@ -527,8 +530,8 @@ __global__ void __launch_bounds__(kRingThreads) heads_ring_kernel(const __grid_c
                 return false;
             };
             int i = 0;
+            const int w = p.team_warps == 1 ? kIssue : 1;
             if (i0 == 0) {
-                const int w = slot_bytes < kSmallSlot ? (int)kIssue : 1;
                 const int64_t t0 = clock64();
                 for (; i + w <= S && i < n; i += w) {
                     while (clock64() - t0 < (int64_t)(i * slot_bytes / kFillPace)) {
@@ -536,15 +539,15 @@ __global__ void __launch_bounds__(kRingThreads) heads_ring_kernel(const __grid_c
                     if (!issue(i, w)) return;
                 }
             }
-            for (; i < 32 && i0 + i < n; ++i)
-                if (!issue(i, 1)) return;
+            for (; i < 32 && i0 + i < n; i += w)
+                if (!issue(i, w)) return;
         }
         return;
     }
-    const int team = warp / kTeamWarps, member = warp % kTeamWarps;
+    const int TW = p.team_warps, team = warp / TW, member = warp % TW;
     constexpr int G = 32 / Work::TPR;  // rows a warp takes at once
     Work work(p, threadIdx.x);
-    const int teams = min(kTeams, S);
+    const int teams = min(kRingWarps / TW, S);
     if (team >= teams) return;
     for (int32_t i = team; i < n; i += teams) {
         const int s = i % S;
@@ -559,7 +562,7 @@ __global__ void __launch_bounds__(kRingThreads) heads_ring_kernel(const __grid_c
         if (m.t >= 0) {
             const uint8_t* slot = ring_p + (size_t)s * slot_bytes;
             if (p.rotary) work.load_turn(reinterpret_cast<const float*>(slot + (size_t)rows * 2 * D));
-            for (int r = member * G + lane / Work::TPR; r < rows; r += kTeamWarps * G) {
+            for (int r = member * G + lane / Work::TPR; r < rows; r += TW * G) {
                 const uint16_t* x = reinterpret_cast<const uint16_t*>(slot) + r * D;
                 work.set(load_run<E>(x + work.a_at), load_run<E>(x + work.b_at));
                 work.finish(m.t, r, nq, nk, m.at);
@@ -706,16 +709,20 @@ constexpr int kRingBytes = 200 * 1024;  // of an SM's 227 KB
 // Bytes of heads from which the ring pays.  Short of it a launch is over before
 // the ring is under way: 512 tokens of 40 heads of 128 (5.2 MB) take 4.6 us
 // straight, 4.9 through the ring; 1024 (10.5 MB) 8.9 and 7.9; 4096 26.0 and
-// 18.1.  Tokens of 9 such heads: 2048 (4.7 MB) 5.3 and 5.2, 4096 10.0 and 8.6.
+// 18.1.  And bytes of a slot: 8000 tokens of 10 heads of 64 (1.5 KB) take 9.6
+// straight, 11.4 through the ring, of 12 such heads (1.8 KB) 16.4 and 13.8.
 constexpr int64_t kRingWork = 8 << 20;
+constexpr int kSmallSlot = 6144, kLeastSlot = 1792;
 
 template <int D, int FMT>
 cudaError_t launch_heads_of(HeadsParams p, cudaStream_t stream) {
     const int rows = (p.q.p ? p.Hq : 0) + (p.k.p ? p.Hkv : 0) + (FMT != kNoCache ? p.Hkv : 0);
     const int slot = rows * 2 * D + p.rotary * 4;
-    p.slots = kRingBytes / slot < kMaxSlots ? kRingBytes / slot : kMaxSlots;
-    if (p.slots > kTeams) p.slots -= p.slots % kTeams;
-    if (p.T * rows * 2 * D >= kRingWork && p.slots >= 4 && p.rotary % 16 == 0 && one_copy(p.q, D) && one_copy(p.k, D) &&
+    p.team_warps = slot < kSmallSlot ? 1 : 3;
+    const int teams = kRingWarps / p.team_warps, most = p.team_warps == 1 ? kMaxSlots : 20;
+    p.slots = kRingBytes / slot < most ? kRingBytes / slot : most;
+    if (p.slots > teams) p.slots -= p.slots % teams;
+    if (p.T * rows * 2 * D >= kRingWork && slot >= kLeastSlot && p.slots >= 4 && p.rotary % 16 == 0 && one_copy(p.q, D) && one_copy(p.k, D) &&
         one_copy(p.v, D) && runs_of_8(p.q_out) && runs_of_8(p.k_out)) {
         return launch_grid(heads_ring_kernel<D, FMT>, p, p.sms, kRingThreads, (size_t)p.slots * slot + 128, stream);
     }

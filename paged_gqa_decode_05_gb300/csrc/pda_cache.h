@@ -47,6 +47,7 @@ struct HeadsParams {
     int32_t max_pos, rotary, interleaved;
     int32_t sms;
     int32_t slots;            // of the ring (set at launch)
+    int32_t team_warps;  // warps that share a slot
     uint32_t* err;
 };
 

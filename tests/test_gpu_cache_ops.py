@@ -47,7 +47,7 @@ def qkv_of(g, tokens, hq, hkv, d):
     (4, 2, 64, 64, 1), (32, 8, 128, 128, 33), (5, 1, 128, 64, 257), (16, 4, 256, 256, 7), (3, 3, 64, 8, 100),
     (8, 8, 256, 24, 65), (64, 8, 128, 120, 19),
     # enough tokens for the streaming form, and (rotary 24) for the other at that size
-    (32, 8, 128, 128, 1500), (4, 2, 64, 32, 11111), (16, 4, 256, 128, 1024), (8, 1, 128, 128, 4001), (48, 16, 256, 64, 257),
+    (32, 8, 128, 128, 1500), (12, 4, 64, 32, 5111), (16, 4, 256, 128, 1024), (8, 1, 128, 128, 4001), (48, 16, 256, 64, 257),
     (2, 1, 64, 24, 23000)])
 def test_norm_rope(hq, hkv, d, rotary, tokens, interleaved):
     g = gen(tokens)
@@ -162,7 +162,7 @@ def test_append(dtype, hq, hkv, d, bs, lens, news):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16] + ref.FORMATS)
 @pytest.mark.parametrize("hq,hkv,d,bs,rotary,times", [
-    (32, 8, 128, 16, 128, 1), (4, 4, 64, 32, 16, 5), (2, 1, 256, 64, 0, 4), (5, 1, 64, 1, 64, 8)])
+    (32, 8, 128, 16, 128, 1), (4, 4, 64, 32, 16, 5), (2, 1, 256, 64, 0, 4), (5, 1, 64, 1, 64, 8), (12, 2, 64, 16, 64, 4), (10, 2, 128, 16, 0, 3)])
 def test_append_prompts(dtype, hq, hkv, d, bs, rotary, times):
     """Prompts of a prefill batch, streamed: empty sequences, a block that does not exist, a table too narrow, padding
     behind the last sequence; and the same bits as the tokens appended a few at a time."""
