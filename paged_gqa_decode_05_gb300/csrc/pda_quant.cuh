@@ -206,17 +206,21 @@ struct UnitSlices {
     }
 };
 
-// CTAs that a call's work is split over: not so many that a CTA gets less than
-// a stage, nor a unit more than about kMaxPieces pieces, which one CTA merges
-// four at a time (half a microsecond or more a round).  One sequence with one
-// kv head of 128: 2000 tokens take 79 us over the whole grid, 15 with a stage
-// at least to each CTA; 32768 tokens 103 without a bound on the pieces, 36, 29,
-// 34 with 64, 32, 16.  Eight kv heads, 32768 tokens: 25.3, 26.1, 33.7.
-constexpr int kMaxPieces = 40;
+// CTAs that a call's work is split over.  A unit of s stages in n pieces takes
+// a s / n to stream and c n for the one CTA that merges them, four a round trip:
+// n = sqrt(a s / c) is best, 2.4 sqrt(s) as measured, or 2.4 sqrt(units stages)
+// CTAs over all units of a call; twice that for blocks below 8 tokens, whose
+// stages take about four times as long; never less than a stage each.  One
+// sequence of one kv head of 128 at 2, 2.4, 3, 4 sqrt: 2000 tokens 13.1, 13.5,
+// 13.7, 15.1 us (79 over the whole grid), 32768 29.2, 29.4, 31.0, 35.7 (119), a
+// million 134, 135, 150, 160; eight kv heads, 8192 tokens 17.2, 16.3, 16.2, 17.8.
+// Two sequences of 2800 tokens, two kv heads of 256, blocks of one token: 35.4,
+// 31.8, 30.2, 28.4, with a stage each 27.7.
 template <bool MQ, int ST>
 __device__ __forceinline__ int64_t quant_plan_ctas(const SplitParams& p, const int32_t* pfx) {
     const int64_t stages = ((int64_t)pfx[p.B] * p.Hkv * p.bs + ST - 1) / ST, units = (int64_t)p.B * p.Hkv;
-    return min((int64_t)gridDim.x, max(min(stages, units * kMaxPieces), (int64_t)rows_per_seq<MQ>(p)));
+    const int64_t best = (int64_t)((p.bs < 8 ? 4.8f : 2.4f) * sqrtf((float)stages * (float)units));
+    return min((int64_t)gridDim.x, max(min(stages, best), (int64_t)rows_per_seq<MQ>(p)));
 }
 
 // Two fp16 values from bytes lo, hi (0..3) of x.  int8: x holds code ^ 0x80;
