@@ -410,6 +410,17 @@ class Context:
             raise ValueError("starts must hold one entry per sequence and the end")
         return width, B
 
+    def _make(self, fn, shape, dtype, stream):
+        """A new output, fn(shape), on the call's stream: a fill comes before the call's kernels there, and memory that
+        work of another stream may still use is not handed out."""
+        torch = _torch()
+        if stream is None:
+            return fn(shape, dtype=dtype, device=self.device)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+        with torch.cuda.stream(stream):
+            return fn(shape, dtype=dtype, device=self.device)
+
     def _scale(self, scale) -> float:
         return float("nan") if scale is None else float(scale)
 
@@ -428,8 +439,8 @@ class Context:
             B = int(seq_lens.shape[0])
             self._bf16(q, "q", (B, self.dims.num_q_heads, self.dims.head_dim))
             if out is None:
-                out = torch.empty(q.shape, device=q.device,
-                                  dtype=torch.float32 if out_dtype == torch.float32 else torch.bfloat16)
+                out = self._make(torch.empty, q.shape, torch.float32 if out_dtype == torch.float32 else torch.bfloat16,
+                                 stream)
             return self._decode_cache(q, 1, k_pool, v_pool, scales, block_table, seq_lens, scale, out, strides,
                                       num_blocks, stream)()
         d = self.dims
@@ -442,8 +453,8 @@ class Context:
         (bs_, ts_, hs_), nblk = self._pool(k_pool, v_pool, strides, num_blocks)
         f32 = out_dtype == torch.float32
         if out is None:
-            out = torch.empty((B, d.num_q_heads, d.head_dim), device=q.device,
-                              dtype=torch.float32 if f32 else torch.bfloat16)
+            out = self._make(torch.empty, (B, d.num_q_heads, d.head_dim), torch.float32 if f32 else torch.bfloat16,
+                             stream)
         L = lib()
         if f32:
             _check(L.pda_decode_f32(self._ctx, _ptr(q), _ptr(k_pool), _ptr(v_pool), nblk, bs_, ts_,
@@ -499,14 +510,14 @@ class Context:
         self._bf16(q, "q")
         if scales is not None or k_pool.dtype in (torch.float8_e4m3fn, torch.int8):
             if out is None:
-                out = torch.empty_like(q)
+                out = self._make(torch.empty, q.shape, torch.bfloat16, stream)
             return self._decode_cache(q, int(q.shape[1]), k_pool, v_pool, scales, block_table, seq_lens, scale, out,
                                       None, None, stream)()
         self._i32(block_table, "block_table", 2)
         self._i32(seq_lens, "seq_lens", 1)
         (bs_, ts_, hs_), nblk = self._pool(k_pool, v_pool, None, None)
         if out is None:
-            out = torch.empty_like(q)
+            out = self._make(torch.empty, q.shape, torch.bfloat16, stream)
         self._bf16(out, "out", tuple(q.shape))
         _check(lib().pda_decode_multi(self._ctx, _ptr(q), _ptr(k_pool), _ptr(v_pool), nblk,
                                       _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens),
@@ -527,7 +538,7 @@ class Context:
         self._bf16(k, "k")
         self._bf16(v, "v", tuple(k.shape))
         if out is None:
-            out = torch.empty((B, d.num_q_heads, d.head_dim), device=q.device, dtype=torch.bfloat16)
+            out = self._make(torch.empty, (B, d.num_q_heads, d.head_dim), torch.bfloat16, stream)
         self._bf16(out, "out", (B, d.num_q_heads, d.head_dim))
         _check(lib().pda_decode_contiguous(self._ctx, _ptr(q), _ptr(k), _ptr(v), int(k.shape[1]),
                                            _ptr(seq_lens), B, self._scale(scale), _ptr(out),
@@ -594,7 +605,7 @@ class Context:
         pairs, outs = [], []
         for x, out, name, heads in ((q, q_out, "q", d.num_q_heads), (k, k_out, "k", d.num_kv_heads)):
             if x is not None and out is None:
-                out = torch.empty(x.shape, dtype=torch.bfloat16, device=self.device)
+                out = self._make(torch.empty, x.shape, torch.bfloat16, stream)
             pairs.append((None, None) if x is None else
                          (self._heads(x, name, T, heads), self._heads(out, name + "_out", T, heads)))
             outs.append(None if x is None else out)
@@ -641,7 +652,7 @@ class Context:
         qh = qo = None
         if q is not None:
             if q_out is None:
-                q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=self.device)
+                q_out = self._make(torch.empty, q.shape, torch.bfloat16, stream)
             qh, qo = self._heads(q, "q", T, d.num_q_heads), self._heads(q_out, "q_out", T, d.num_q_heads)
         elif q_out is not None:
             raise ValueError("q_out without q")
@@ -667,8 +678,8 @@ class Context:
         if k_out is None and v_out is None:
             if starts is not None:
                 raise ValueError("starts needs k_out / v_out")
-            k_out, v_out = (torch.zeros((B, width * d.block_size, d.num_kv_heads, d.head_dim), device=self.device,
-                                        dtype=out_dtype or torch.bfloat16) for _ in range(2))
+            shape = (B, width * d.block_size, d.num_kv_heads, d.head_dim)
+            k_out, v_out = (self._make(torch.zeros, shape, out_dtype or torch.bfloat16, stream) for _ in range(2))
         like = v_out if k_out is None else k_out
         shape, dtype, ndim = like.shape, like.dtype, 4 if starts is None else 3
         good = (dtype is torch.bfloat16 or dtype is torch.float32) and (out_dtype is None or out_dtype is dtype) and \
@@ -722,8 +733,8 @@ class Context:
         d = self.dims
         f32 = out_dtype == torch.float32
         if out is None:
-            out = torch.empty((num_seqs, d.num_q_heads, d.head_dim), device=self.device,
-                              dtype=torch.float32 if f32 else torch.bfloat16)
+            out = self._make(torch.empty, (num_seqs, d.num_q_heads, d.head_dim),
+                             torch.float32 if f32 else torch.bfloat16, stream)
         fn = lib().pda_finalize_f32 if f32 else lib().pda_finalize
         _check(fn(self._ctx, _ptr(out), int(num_seqs), _stream(stream)))
         return out
@@ -736,10 +747,8 @@ class Context:
         l = sum exp(s - m), o = sum exp(s - m) v."""
         torch = _torch()
         d = self.dims
-        m = torch.empty((num_seqs, d.num_q_heads), device=self.device, dtype=torch.float32)
-        l = torch.empty_like(m)
-        o = torch.empty((num_seqs, d.num_q_heads, d.head_dim), device=self.device,
-                        dtype=torch.float32)
+        m, l = (self._make(torch.empty, (num_seqs, d.num_q_heads), torch.float32, stream) for _ in range(2))
+        o = self._make(torch.empty, (num_seqs, d.num_q_heads, d.head_dim), torch.float32, stream)
         _check(lib().pda_export_state(self._ctx, int(num_seqs), _ptr(m), _ptr(l), _ptr(o),
                                       _stream(stream)))
         return m, l, o
@@ -758,8 +767,8 @@ class Context:
                 raise ValueError(f"{name} must be a contiguous float32 CUDA tensor of shape {shape}")
         f32 = out_dtype == torch.float32
         if out is None:
-            out = torch.empty((S, d.num_q_heads, d.head_dim), device=self.device,
-                              dtype=torch.float32 if f32 else torch.bfloat16)
+            out = self._make(torch.empty, (S, d.num_q_heads, d.head_dim), torch.float32 if f32 else torch.bfloat16,
+                             stream)
         fn = lib().pda_merge_states_f32 if f32 else lib().pda_merge_states
         _check(fn(self._ctx, P_, S, _ptr(m_parts), _ptr(l_parts), _ptr(o_parts), _ptr(out),
                   _stream(stream)))
@@ -776,9 +785,8 @@ class Context:
         self._i32(seq_lens, "seq_lens", 1)
         (bs_, ts_, hs_), nblk = self._pool(k_pool, v_pool, strides, num_blocks)
         rows = int(block_table.shape[1]) * d.block_size
-        k_rows = torch.zeros((B, d.num_kv_heads, rows, d.head_dim), device=self.device,
-                             dtype=torch.bfloat16)
-        v_rows = torch.zeros_like(k_rows)
+        k_rows, v_rows = (self._make(torch.zeros, (B, d.num_kv_heads, rows, d.head_dim), torch.bfloat16, stream)
+                          for _ in range(2))
         _check(lib().pda_debug_gather(self._ctx, _ptr(k_pool), _ptr(v_pool), nblk, bs_, ts_, hs_,
                                       _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens),
                                       B, _ptr(k_rows), _ptr(v_rows), _stream(stream)))

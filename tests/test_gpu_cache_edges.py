@@ -1,0 +1,48 @@
+"""Operators around the decode at the edges of what their documentation allows: other streams, scales and rows of any
+size, masked places that hold NaN, against fp64 definitions."""
+import numpy as np
+import pytest
+import torch
+
+import cache_ref as ref
+import paged_gqa_decode_05_gb300 as pda
+
+pytestmark = pytest.mark.gpu
+
+
+def ctx_of(hq, hkv, d, bs, max_seqs=64):
+    return pda.Context(max_seqs=max_seqs, num_q_heads=hq, num_kv_heads=hkv, head_dim=d, block_size=bs)
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32).cuda()
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_calls_on_another_stream_make_their_outputs_there(handle):
+    """Work queued on the current stream does not touch what a call on another stream returned: rows read back stay,
+    and rows of no token stay zero."""
+    rng, g = np.random.default_rng(1), gen(1)
+    hq, hkv, d, bs, lens = 4, 2, 64, 16, [37, 0, 20]
+    table, pool = ref.sequences(rng, lens, bs)
+    kp, vp, sc = (t.cuda() for t in ref.random_cache(g, pool, bs, hkv, d, torch.int8))
+    table, lens_d = table.cuda(), i32(lens)
+    q = torch.randn((3, hq, d), generator=g).bfloat16().cuda()
+    ctx = ctx_of(hq, hkv, d, bs)
+    want = ctx.read_cache(kp, vp, table, lens_d, scales=sc)
+    want_o = ctx.decode(q, kp, vp, table, lens_d, scales=sc)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(20_000_000)  # what comes behind this on the current stream comes late
+    stream = side.cuda_stream if handle else side
+    got = ctx.read_cache(kp, vp, table, lens_d, scales=sc, stream=stream)
+    out = ctx.decode(q, kp, vp, table, lens_d, scales=sc, stream=stream)
+    side.synchronize()
+    for _ in range(2):
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(out, want_o)
+        torch.cuda.synchronize()
+    assert ctx.read_device_errors() == 0
