@@ -454,7 +454,9 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
                     float vs = sp[s_off[r][i] + p.bs];
                     if (partial && r0 + 16 * r + 8 * i + g >= md.n_valid) vs = 1.f;
                     lv[r][i] = lg2(max_nan(vs, kLeastScale));
-                    iv[r][i] = ex2(-lv[r][i]);
+                    // fminf drops a NaN, which stays in lv: the scores of a row of scale NaN
+                    // are NaN, but a causal query that does not see it adds 0 * iv
+                    iv[r][i] = fminf(ex2(-lv[r][i]), 1.f / kLeastScale);
                 }
             float x[RT][4];
 #pragma unroll

@@ -46,3 +46,32 @@ def test_calls_on_another_stream_make_their_outputs_there(handle):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(out, want_o)
         torch.cuda.synchronize()
     assert ctx.read_device_errors() == 0
+
+
+# ------------------------------------------------------------------ NaN that a query does not see
+
+SHAPES = [(4, 2, 64, 16), (8, 2, 128, 16), (8, 1, 128, 4), (4, 1, 256, 32), (16, 2, 64, 1), (8, 1, 128, 64)]
+
+
+@pytest.mark.parametrize("dtype", ref.FORMATS)
+@pytest.mark.parametrize("q_len", [2, 3, 4])
+@pytest.mark.parametrize("hq,hkv,d,bs", SHAPES)
+@pytest.mark.parametrize("which", [0, 1])
+def test_a_later_tokens_nan_row_stays_with_the_queries_that_see_it(dtype, q_len, hq, hkv, d, bs, which):
+    """A drafted token whose key or value holds an infinity (a row of scale NaN): the queries before it keep their
+    bits, the query that sees it is NaN."""
+    rng, g = np.random.default_rng(q_len), gen(d + bs)
+    lens = [q_len, 41, 128, 300, 1000]
+    table, pool = ref.sequences(rng, lens, bs)
+    kp, vp, sc = (t.cuda() for t in ref.random_cache(g, pool, bs, hkv, d, dtype))
+    q = torch.randn((len(lens), q_len, hq, d), generator=g).bfloat16().cuda()
+    ctx = ctx_of(hq, hkv, d, bs)
+    rest = (table.cuda(), i32(lens))
+    want = ctx.decode_multi(q, kp, vp, *rest, scales=sc)
+    rows = torch.randn((2, len(lens), hkv, d), generator=g).bfloat16().cuda()
+    rows[which, :, :, 5] = float("inf")
+    ctx.append(rows[0], rows[1], kp, vp, *rest, scales=sc)
+    got = ctx.decode_multi(q, kp, vp, *rest, scales=sc)
+    assert torch.equal(got[:, :-1], want[:, :-1]) and torch.isfinite(got[:, :-1]).all()
+    assert torch.isnan(got[:, -1]).all()
+    assert ctx.read_device_errors() == 0
