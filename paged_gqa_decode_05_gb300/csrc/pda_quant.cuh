@@ -266,6 +266,66 @@ __device__ __forceinline__ void v_fragment(uint32_t r0, uint32_t r1, uint32_t (&
     }
 }
 
+// 0xff in the bytes of x that are NaN codes of e4m3.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t x) { return __vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu); }
+
+// NaN codes in values that only some of the queries of a walk see would give the
+// others NaN, as 0 * NaN.  In rows r .. r + n - 1 (one warp's) of a stage's V part
+// at sV they become 0, and the columns of O that they make NaN for this lane's
+// queries, which see the first from0 + 1 and from1 + 1 of these rows, are noted
+// until the segment ends: bits 4 i + 2 c, + 1 are columns 16 i + 2 g and the next
+// of its c-th query.  Out of line: for the last rows of a walk, no part of the
+// loop.
+template <int W, int RW>
+struct NanNotes {
+    uint64_t cols[W * 32];  // [thread]
+    uint64_t bars[RW];      // of the warps that share KV rows
+    uint32_t phase[W];
+};
+template <int D, int NT, class Notes>
+__device__ __noinline__ void hide_nan_codes(Notes* notes, uint32_t sV, int r, int n, int lbs, int from0, int from1,
+                                            bool paired, int thread, uint32_t* err, volatile int* abort_flag) {
+    constexpr int RB = D < 128 ? D : 128, CH = D / 16, CPS = RB / 16;
+    const int lane = thread & 31, warp = thread >> 5;
+    const auto chunk = [&](int i, int c) {  // of row r + i
+        return sV + quant_row_off<D>(r + i, lbs) + (((uint32_t)(c / CPS) * RB) << lbs) + (uint32_t)(c % CPS) * 16;
+    };
+    uint32_t any = 0;
+    for (int u = lane; u < n * CH; u += 32) {
+        uint32_t x[4];
+        lds_v4(chunk(u / CH, u % CH), x);
+        any |= nan_codes(x[0]) | nan_codes(x[1]) | nan_codes(x[2]) | nan_codes(x[3]);
+    }
+    if (!__any_sync(0xffffffffu, any != 0)) return;
+    uint64_t cols = notes->cols[thread];
+    for (int i = 0; i < n; ++i)
+        for (int c = 0; c < CH; ++c) {
+            const int at = c / CPS * CPS + (c % CPS ^ quant_swz<D>(chunk(i, c / CPS * CPS)));
+            uint32_t x[4];
+            lds_v4(chunk(i, at), x);
+            const int g = lane >> 2;
+            const uint32_t bad = nan_codes(g < 2 ? x[0] : g < 4 ? x[1] : g < 6 ? x[2] : x[3]) >> (16 * (g & 1));
+            const uint32_t two = (bad & 1u) | (bad >> 7 & 2u);
+            cols |= (uint64_t)((i <= from0 ? two : 0u) | (i <= from1 ? two << 2 : 0u)) << (4 * c);
+        }
+    notes->cols[thread] = cols;
+    __syncwarp();
+    if (NT > 1 && paired) {  // the warp of the other q rows looks at these codes too
+        uint32_t phase = notes->phase[warp];
+        consumer_sync(smem_u32(&notes->bars[warp % (sizeof(notes->bars) / 8)]), phase, err, abort_flag);
+        __syncwarp();
+        if (lane == 0) notes->phase[warp] = phase;
+    }
+    for (int u = lane; u < n * CH; u += 32) {
+        const uint32_t at = chunk(u / CH, u % CH);
+        uint32_t x[4];
+        lds_v4(at, x);
+        sts_v4(at, x[0] & ~nan_codes(x[0]), x[1] & ~nan_codes(x[1]), x[2] & ~nan_codes(x[2]), x[3] & ~nan_codes(x[3]));
+    }
+    fence_proxy_async_smem();  // generic writes before the next TMA
+    __syncwarp();
+}
+
 // A unit's q rows in the stage (bf16, 8 NT of them, those from nr on zero),
 // scaled by a power of two each and turned in place into the lanes' B
 // fragments [tile of 8 rows][32-column step][lane] of 16 bytes: e4m3, four high
@@ -335,15 +395,15 @@ __device__ __forceinline__ bool quant_q_fragments(uint8_t* at, float* back, int 
     return consumer_sync(cbar, cphase, err, abort_flag);
 }
 
-template <int D, int FMT, int NT, int MODE>
+template <int D, int FMT, int NT, int MODE, class Notes>
 __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_t base_s, uint8_t* base,
                                                    const SmemLayout& L, const StageMeta* meta, const int32_t* pfx,
-                                                   volatile int* abort_flag, const GroupRange* group, int warp,
-                                                   int lane) {
+                                                   volatile int* abort_flag, const GroupRange* group,
+                                                   Notes* notes, int warp, int lane) {
     using C = QuantCfg<D, NT>;
     constexpr int S = C::kStages, RT = C::kRT, K = C::kK;
     constexpr int kThreadsC = C::kWarps * 32, kOStride = D + 4;
-    constexpr bool MQ = is_multi(MODE);
+    constexpr bool MQ = is_multi(MODE), kHide = MQ && FMT == kE4m3;
     const uint32_t full0 = base_s + L.bars, empty0 = full0 + 8 * S;
     const int g = lane >> 2, t = lane & 3;
     // warps 0 .. kRW - 1 take the first eight q rows, the next kRW the others, all of a stage's KV rows
@@ -430,17 +490,26 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
             f[1] = q_back[8 * tile + 2 * t + 1];
             m[0] = m[1] = kNegInf;
             l[0] = l[1] = 0.f;
+            if constexpr (kHide) notes->cols[ct] = 0;
 #pragma unroll
             for (int i = 0; i < 2 * K; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         }
         if (r0 < md.n_valid && (NT == 1 || 8 * tile < md.nr)) {
             const bool partial = r0 + 16 * RT > md.n_valid;
-            if (FMT == kE4m3 && partial) {
+            const int pos0 = MQ ? md.j0 * p.bs + r0 : 0;
+            const bool diagonal = MQ && pos0 + 16 * RT - 1 > md.lim;  // some queries do not see some of these rows
+            if (FMT == kE4m3 && (MQ ? partial || diagonal : partial)) {
                 // rows behind the end may hold NaN codes, and 0 * NaN would poison P V
                 for (int u = lane; u < (r0 + 16 * RT - md.n_valid) * (D / 16); u += 32) {
                     const int r = md.n_valid + u / (D / 16), c = u % (D / 16);
                     const uint32_t a = sV + quant_row_off<D>(r, lbs) + (uint32_t)(c / CPS) * hs + (uint32_t)((c % CPS) << 4);
                     asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
+                }
+                if constexpr (kHide) {
+                    const int later = max(0, md.lim + 1 - pos0);  // the first row that some query does not see
+                    hide_nan_codes<D, NT>(notes, sV, r0 + later, min(16 * RT, md.n_valid - r0) - later, lbs,
+                                          md.lim - pos0 - later + qc[0], md.lim - pos0 - later + qc[1], md.nr > 8, ct, p.err,
+                                          abort_flag);
                 }
                 __syncwarp();
             }
@@ -491,15 +560,12 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
                     for (int i = 0; i < 4; ++i)
                         if (r0 + 16 * r + 8 * (i >> 1) + g >= md.n_valid) x[r][i] = kNegInf;
             }
-            if constexpr (MQ) {  // column c is query c / G of the row: no later tokens
-                const int pos0 = md.j0 * p.bs + r0;
-                if (pos0 + 16 * RT - 1 > md.lim) {
+            if (MQ && diagonal) {  // column c is query c / G of the row: no later tokens
 #pragma unroll
-                    for (int r = 0; r < RT; ++r)
+                for (int r = 0; r < RT; ++r)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (pos0 + 16 * r + 8 * (i >> 1) + g > md.lim + qc[i & 1]) x[r][i] = kNegInf;
-                }
+                    for (int i = 0; i < 4; ++i)
+                        if (pos0 + 16 * r + 8 * (i >> 1) + g > md.lim + qc[i & 1]) x[r][i] = kNegInf;
             }
             // the references move only when a weight would pass 2^(kRefBias + kLazyLog2);
             // the columns' maxima are taken only then
@@ -572,6 +638,7 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
             if (!(md.flags & kWholeUnit)) pc = unit_pieces(pfx, md.b, md.kvh, p.Hkv, p.unit_cost, grs);
             int role = kRoleAbort;
             bool stop = false;
+            const uint64_t nan_cols = kHide ? notes->cols[ct] : 0;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {  // a warp's states of its eight rows
                 const int hr = 2 * t + c, h = 8 * tile + hr;
@@ -583,8 +650,15 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
                 }
                 float* r = st_o + (size_t)(warp * 8 + hr) * kOStride + 2 * g;
 #pragma unroll
-                for (int i = 0; i < 2 * K; ++i)
-                    *reinterpret_cast<float2*>(r + 16 * i) = make_float2(o[i][c], o[i][2 + c]);
+                for (int i = 0; i < 2 * K; ++i) {
+                    float2 v = make_float2(o[i][c], o[i][2 + c]);
+                    if constexpr (kHide) {
+                        const uint32_t bad = (uint32_t)(nan_cols >> (4 * i + 2 * c));
+                        if (bad & 1u) v.x = __int_as_float(0x7fffffff);
+                        if (bad & 2u) v.y = __int_as_float(0x7fffffff);
+                    }
+                    *reinterpret_cast<float2*>(r + 16 * i) = v;
+                }
             }
             // one copy of the merge's code for both tiles: code that runs once a unit is fetched cold
 #pragma unroll 1
@@ -614,6 +688,8 @@ __global__ void __maxnreg__(168) quant_split_kernel(const __grid_constant__ Quan
     extern __shared__ uint8_t smem_raw[];
     __shared__ int abort_flag;
     __shared__ GroupRange group;  // of this CTA
+    constexpr bool kHide = is_multi(MODE) && FMT == kE4m3;
+    __shared__ NanNotes<kHide ? C::kWarps : 1, kHide ? C::kRW : 1> notes;
     const uint32_t raw_s = smem_u32(smem_raw);
     const uint32_t base_s = (raw_s + 1023u) & ~1023u;
     uint8_t* base = smem_raw + (base_s - raw_s);
@@ -628,9 +704,12 @@ __global__ void __maxnreg__(168) quant_split_kernel(const __grid_constant__ Quan
             mbar_init(base_s + L.bars + 8 * (C::kStages + s), C::kWarps);
         }
         mbar_init(base_s + L.cbar, C::kWarps * 32);
+        if (kHide)
+            for (int i = 0; i < C::kRW; ++i) mbar_init(smem_u32(notes.bars + i), NT * 32);
         fence_mbar_init();
         abort_flag = 0;
     }
+    if (kHide && tid < C::kWarps) notes.phase[tid] = 0;
     if (tid == C::kWarps * 32 && p.row_gather == 0) {
         prefetch_tensormap(&p.tm_k);
         prefetch_tensormap(&p.tm_k1);
@@ -653,7 +732,7 @@ __global__ void __maxnreg__(168) quant_split_kernel(const __grid_constant__ Quan
         run_producer<C, QuantLoader<D, NT>, D, MODE>(p, base_s, L, pfx, meta, &abort_flag, begin, end, lane);
         return;
     }
-    run_quant_consumer<D, FMT, NT, MODE>(p, base_s, base, L, meta, pfx, &abort_flag, &group, warp, lane);
+    run_quant_consumer<D, FMT, NT, MODE>(p, base_s, base, L, meta, pfx, &abort_flag, &group, &notes, warp, lane);
 }
 
 template <int D, int FMT, int NT, int MODE>

@@ -75,3 +75,29 @@ def test_a_later_tokens_nan_row_stays_with_the_queries_that_see_it(dtype, q_len,
     assert torch.equal(got[:, :-1], want[:, :-1]) and torch.isfinite(got[:, :-1]).all()
     assert torch.isnan(got[:, -1]).all()
     assert ctx.read_device_errors() == 0
+
+
+@pytest.mark.parametrize("q_len", [2, 4, 7])
+@pytest.mark.parametrize("hq,hkv,d,bs", SHAPES)
+def test_a_later_tokens_nan_codes_stay_with_the_queries_that_see_it(q_len, hq, hkv, d, bs):
+    """e4m3 codes that read as NaN in some columns of drafted tokens' values: NaN in those columns of the queries that
+    see the token, and nowhere else."""
+    rng, g = np.random.default_rng(q_len), gen(d + bs)
+    lens = [q_len, 41, 128, 300, 1000]
+    table, pool = ref.sequences(rng, lens, bs)
+    kp, vp, sc = ref.random_cache(g, pool, bs, hkv, d, torch.float8_e4m3fn)
+    q = torch.randn((len(lens), q_len, hq, d), generator=g).bfloat16().cuda()
+    ctx = ctx_of(hq, hkv, d, bs)
+    rest = (table.cuda(), i32(lens))
+    want = ctx.decode_multi(q, kp.cuda(), vp.cuda(), *rest, scales=sc.cuda())
+    nan = torch.zeros((len(lens), q_len, hkv, d), dtype=torch.bool)
+    for b, n in enumerate(lens):
+        for back in (1, 2):  # the last token's columns 3 and d - 1, the one before's column 8
+            at = n - back
+            cols = [3, d - 1] if back == 1 else [8]
+            vp.view(torch.uint8)[table[b, at // bs].long(), at % bs, :, cols] = 0x7f if back == 1 else 0xff
+            nan[b, q_len - back:, :, cols] = True
+    got = ctx.decode_multi(q, kp.cuda(), vp.cuda(), *rest, scales=sc.cuda())
+    nan = nan.repeat_interleave(hq // hkv, 2).cuda()
+    assert torch.equal(torch.isnan(got), nan)
+    assert torch.equal(got[~nan], want[~nan])
