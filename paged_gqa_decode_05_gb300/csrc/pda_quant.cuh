@@ -6,11 +6,13 @@
 //   s_t = scale ks_t (q . k_t),   o = sum_t e^(s_t) vs_t v_t / sum_t e^(s_t),
 // so nothing is dequantised: K scales multiply the scores, V scales the
 // weights.  HBM sees D + 4 bytes per row and the tensor cores see codes:
-//   * e4m3, S^T = K q^T: q, scaled by a power of two per row into [128, 256),
-//     splits into two e4m3 parts, hi + lo, which hold all eight significant
-//     bits of a bf16 value (values below 2^-15 of the row's largest keep an
-//     absolute 2^-18 of it): two m16n8k32 products take K's bytes as they lie
-//     in shared memory.
+//   * e4m3, S^T = K q^T: q, scaled by a power of two per row so that its largest
+//     lies in [128, 256), splits into two e4m3 parts, hi + lo / 32, with sums of
+//     their own.  A residual is 8 at most, so 32 of it still fit, and what e4m3
+//     cannot hold lies below its smallest step of 2^-9: the parts hold all eight
+//     significant bits of values from 2^-7 on, 2^-14 of the largest, and smaller
+//     ones to 2^-15, 2^-22 of it.  Two m16n8k32 products take K's bytes as they
+//     lie in shared memory.
 //   * int8: codes become fp16 exactly (the byte placed under 0x64 reads as
 //     1024 + u) for m16n8k16, q in fp16 with the same power-of-two scale.
 //   * O^T += V^T P^T (m16n8k16): ldmatrix transposes pairs of bytes, so a lane
@@ -35,6 +37,7 @@
 namespace pda {
 
 constexpr float kRefBias = 6.f;
+constexpr float kLowPart = 32.f;  // times the residual of a q element in e4m3
 // V scales below 2^-60 count as this (the codes of a scale of 0 are 0; others'
 // elements are off by 448 * 2^-60 = 4e-16 at most).  A row adds p' / vs to the
 // sum of weights, 2^(kRefBias + kLazyLog2 + 60) at most, so 2^31 rows stay
@@ -377,7 +380,8 @@ __device__ __forceinline__ bool quant_q_fragments(uint8_t* at, float* back, int 
                 const float2 s = __half22float2(*reinterpret_cast<const __half2*>(&b01));
                 const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&b23));
                 u = h01 | (h23 << 16);
-                v = pack_e4m3x2(x0 - s.x, x1 - s.y) | (pack_e4m3x2(x2 - w.x, x3 - w.y) << 16);
+                v = pack_e4m3x2(kLowPart * (x0 - s.x), kLowPart * (x1 - s.y)) |
+                    (pack_e4m3x2(kLowPart * (x2 - w.x), kLowPart * (x3 - w.y)) << 16);
             } else {
                 u = pack_f16x2(x0, x1);
                 v = pack_f16x2(x2, x3);
@@ -551,7 +555,8 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
                 // x: the score in base-2 units plus log2 of the row's V scale
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    x[r][i] = fmaf(acc[0][i] + acc[1][i], ks[r][i >> 1] * f[i & 1], lv[r][i >> 1]);
+                    x[r][i] = fmaf(FMT == kE4m3 ? fmaf(acc[1][i], 1.f / kLowPart, acc[0][i]) : acc[0][i] + acc[1][i],
+                                   ks[r][i >> 1] * f[i & 1], lv[r][i >> 1]);
             }
             if (partial) {
 #pragma unroll

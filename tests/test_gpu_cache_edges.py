@@ -18,6 +18,17 @@ def gen(seed):
     return torch.Generator().manual_seed(seed)
 
 
+BF16 = 2.0 ** -8
+DECODE = 2.0 ** -10  # of sum p |v|: rounded weights and what fp32 arithmetic adds
+
+
+def within(got, want, tol):
+    got = got.double().cpu()
+    assert torch.isfinite(got).all()
+    off = (got - want).abs() - tol
+    assert off.max() <= 0, f"{off.max()} beyond its tolerance at {np.unravel_index(int(off.argmax()), off.shape)}"
+
+
 def i32(x):
     return torch.tensor(x, dtype=torch.int32).cuda()
 
@@ -101,3 +112,36 @@ def test_a_later_tokens_nan_codes_stay_with_the_queries_that_see_it(q_len, hq, h
     nan = nan.repeat_interleave(hq // hkv, 2).cuda()
     assert torch.equal(torch.isnan(got), nan)
     assert torch.equal(got[~nan], want[~nan])
+
+
+# ------------------------------------------------------------------ rows of very different size
+
+@pytest.mark.parametrize("dtype", ref.FORMATS)
+@pytest.mark.parametrize("hq,hkv,d,bs,q_len", [(8, 2, 128, 16, 1), (4, 4, 64, 8, 3), (4, 1, 256, 16, 1), (8, 2, 128, 16, 4)])
+@pytest.mark.parametrize("times", [2.0 ** 10, 2.0 ** 12, 2.0 ** 14])
+def test_q_with_one_large_element(dtype, hq, hkv, d, bs, q_len, times):
+    """A q element `times` the others, on a channel where every key is zero: the others still make the scores.  With
+    an e4m3 cache q elements below 2^-14 of the row's largest are off by 2^-22 of it at most, which moves a score by
+    scale sum |dq| |k| and a weight by twice the largest such move; else q is as exact as it came."""
+    rng, g = np.random.default_rng(3), gen(d)
+    lens = [37, 200, 64]
+    table, pool = ref.sequences(rng, lens, bs)
+    kp, vp, sc = ref.random_cache(g, pool, bs, hkv, d, dtype)
+    q = torch.randn((3, q_len, hq, d), generator=g)
+    at = torch.randint(0, d, (3, q_len, hq), generator=g)
+    q.scatter_(3, at[..., None], times)
+    kp.view(torch.uint8)[...] = torch.where(torch.zeros(d).scatter_(0, at.flatten(), 1.0).bool(), 0, kp.view(torch.uint8))
+    q = q.bfloat16()
+    ctx = ctx_of(hq, hkv, d, bs)
+    out = torch.empty(q.shape, dtype=torch.float32, device="cuda")
+    ctx.decode_multi(q.cuda(), kp.cuda(), vp.cuda(), table.cuda(), i32(lens), scales=sc.cuda(), out=out)
+    want, size = ref.decode64(q, kp, vp, sc, table, lens, bs)
+    top = q.double().abs().amax(-1, keepdim=True)
+    dq = torch.where(q.double().abs() < 2.0 ** -14 * top, 2.0 ** -22 * top, 0.0)
+    moved = torch.zeros(q.shape[:3] + (1,), dtype=torch.float64)
+    if dtype == torch.float8_e4m3fn:
+        for b, n in enumerate(lens):
+            k = ref.rows64(kp, sc, 0, table[b], n, bs).abs().amax(0).repeat_interleave(hq // hkv, 0)
+            moved[b] = 2 * d ** -0.5 * (dq[b] * k).sum(-1, keepdim=True)
+    within(out, want, (DECODE + moved) * size)
+    assert ctx.read_device_errors() == 0
