@@ -509,10 +509,13 @@ pda_status pda_decode_noalloc(const pda_bf16* q, const pda_bf16* k_pool, const p
  *   scales      [num_blocks, Hkv, 2, block_size] fp32, dense, 16-byte aligned:
  *               [.., 0, t] the K scale and [.., 1, t] the V scale of block slot
  *               t, side by side so that one copy fetches both.  Scales are
- *               >= 0 and at most 2^120; 0 makes every element of the row 0, NaN
- *               makes every element NaN.  Decode takes V scales below 2^-60 for
- *               2^-60, which rows written by pda_append do not show where their
- *               scale is 0 (their codes are 0).  NULL for PDA_CACHE_BF16.
+ *               >= 0 and below 2^122 (as any row of finite fp32 values
+ *               has); 0 makes every element of the row 0, NaN makes every
+ *               element NaN.  Decode takes V scales below 2^-60 for 2^-60: such
+ *               elements are off by 448 * 2^-60 = 4e-16 at most, and not at all
+ *               where the codes are 0, as pda_append writes them with a scale
+ *               of 0.  From there on, rows of any two V scales may meet in one
+ *               sequence.  NULL for PDA_CACHE_BF16.
  */
 enum { PDA_CACHE_BF16 = 0, PDA_CACHE_E4M3 = 1, PDA_CACHE_INT8 = 2 };
 typedef struct pda_cache {

@@ -693,13 +693,22 @@ __device__ __forceinline__ bool consumer_sync(uint32_t cbar, uint32_t& cphase, u
     return ok;
 }
 
-// Combines a partial state (mi, li, oi) into (M, Ls, Os).
+// l 2^d for d <= 0 in two steps: a sum that is large beside its reference may be
+// scaled by less than fp32 holds at once.
+__device__ __forceinline__ float scale_sum(float l, float d) {
+    const float h = ex2(0.5f * d);
+    return l * h * h;
+}
+
+// Combines a partial state (mi, li, oi) into (M, Ls, Os).  kWide: references may
+// lie further apart than fp32's exponents reach, and the sums still matter.
+template <bool kWide = false>
 __device__ __forceinline__ void merge_state(float& M, float& Ls, float4& Os, float mi, float li,
                                             const float4& oi) {
     const float Mn = fmaxf(M, mi);
     if (Mn == kNegInf) return;  // both states empty
     const float fa = ex2(M - Mn), fb = ex2(mi - Mn);
-    Ls = Ls * fa + li * fb;
+    Ls = kWide ? scale_sum(Ls, M - Mn) + scale_sum(li, mi - Mn) : Ls * fa + li * fb;
     Os.x = Os.x * fa + oi.x * fb;
     Os.y = Os.y * fa + oi.y * fb;
     Os.z = Os.z * fa + oi.z * fb;
@@ -1156,9 +1165,10 @@ struct RowSlices {
 // role (whole unit, stored partial, or the last piece, which merges every
 // stored partial with its own); each (row, 4 columns) of the tile is then
 // combined over the slices and written (bf16 o / l, or the fp32 partial).
-// Returns false when the CTA aborts.  kNan: a NaN sum of weights gives NaN,
-// not 0.
-template <int D, int kThreadsC, int kTileRows = 16, bool kNan = false, class Own>
+// Returns false when the CTA aborts.  kScaled: the states of an 8-bit cache,
+// whose references follow the V scales (merge_state's kWide), and a NaN sum of
+// weights gives NaN, not 0.
+template <int D, int kThreadsC, int kTileRows = 16, bool kScaled = false, class Own>
 __device__ __forceinline__ bool rows_tile_merge(const SplitParams& p, const StageMeta& m, int tile, int ct,
                                                 int32_t ticket, const UnitPieces& pc, const GroupRange& grs,
                                                 const RowInfo& ri, const Own& own, int32_t* st_role, uint32_t cbar,
@@ -1232,15 +1242,15 @@ __device__ __forceinline__ bool rows_tile_merge(const SplitParams& p, const Stag
                     }
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        if (mine[k]) merge_state(Mr, Lr, Or, M, Ls, Os);
-                        else merge_state(Mr, Lr, Or, mi[k], li[k], oi[k]);
+                        if (mine[k]) merge_state<kScaled>(Mr, Lr, Or, M, Ls, Os);
+                        else merge_state<kScaled>(Mr, Lr, Or, mi[k], li[k], oi[k]);
                     }
                 }
                 M = Mr;
                 Ls = Lr;
                 Os = Or;
             }
-            const float4 v = (kNan ? Ls != 0.f : Ls > 0.f) ? make_float4(Os.x / Ls, Os.y / Ls, Os.z / Ls, Os.w / Ls)
+            const float4 v = (kScaled ? Ls != 0.f : Ls > 0.f) ? make_float4(Os.x / Ls, Os.y / Ls, Os.z / Ls, Os.w / Ls)
                                       : make_float4(0.f, 0.f, 0.f, 0.f);
             const int64_t oo = qo_offset<true>(p, ri.b, ri.first + h / G, m.kvh * G + h % G, D) + d4;
             if (p.out_f32) {

@@ -20,13 +20,13 @@
 //     the product's A operand, which only permutes the rows of O.
 // A weight that multiplies V is p' = 2^(s + log2 vs - m'), with the reference
 // m' following the maximum of s + log2 vs, so that p' stays inside fp16
-// whatever the V scales are; the sum of weights adds p' / vs.  (m', l, o) is
-// an online-softmax state like any other: o / l and merges do not depend on
-// the reference.  p' enters the product as fp16, 2^-11 of it at most: an
-// eighth of the output's own bf16 half step.  References sit kRefBias below
-// the maximum they were taken at and move when a maximum passes them by more
-// than kRefBias + kLazyLog2, so p' < 2^14 and what fp16 flushes is 2^-31 of
-// the largest weight.
+// whatever the V scales are; the sum of weights adds 2^(s - m'), which may be
+// as small as 2^-116 or as large as 2^74 (see kSumBias).  (m', l, o) is an
+// online-softmax state like any other: o / l and merges do not depend on the
+// reference.  p' enters the product as fp16, 2^-11 of it at most: an eighth of
+// the output's own bf16 half step.  References sit kRefBias below the maximum
+// they were taken at and move when a maximum passes them by more than kRefBias +
+// kLazyLog2, so p' < 2^14 and what fp16 flushes is 2^-31 of the largest weight.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -39,11 +39,15 @@ namespace pda {
 constexpr float kRefBias = 6.f;
 constexpr float kLowPart = 32.f;  // times the residual of a q element in e4m3
 // V scales below 2^-60 count as this (the codes of a scale of 0 are 0; others'
-// elements are off by 448 * 2^-60 = 4e-16 at most).  A row adds p' / vs to the
-// sum of weights, 2^(kRefBias + kLazyLog2 + 60) at most, so 2^31 rows stay
-// inside fp32; with 2^-110, the least scale that is written, 500 rows of zeros
-// could pass it.
+// elements are off by 448 * 2^-60 = 4e-16 at most), and scales of finite values
+// are below 2^122 (2^128 / 127).  A row's p' is 2^(kRefBias + kLazyLog2) at
+// most, so it adds 2^74 or less to the sum of weights, and 2^31 rows 2^105; the
+// row of the largest score adds at least 2^(kRefBias - 122) = 2^-116, as its own
+// p' or another's reaches the reference.  A warp's sum is kept times 2^kSumBias,
+// so both ends, and rows 2^-30 of the largest, stay inside fp32.  References of
+// states that merge lie up to 2^182 apart: their sums are scaled in two steps.
 constexpr float kLeastScale = 8.6736174e-19f;
+constexpr float kSumBias = 20.f;
 
 template <int D, int NT>
 struct QuantCfg {
@@ -201,9 +205,9 @@ struct UnitSlices {
         if (M == kNegInf) return;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-            const float f = ex2(st_m[w * 16 + h] - M);
+            const float d = st_m[w * 16 + h] - M, f = ex2(d);
             const float4 v = *reinterpret_cast<const float4*>(st_o + (size_t)(w * 8 + hr) * (D + 4) + d4);
-            Ls += st_l[w * 16 + h] * f;
+            Ls += scale_sum(st_l[w * 16 + h], d);
             Os.x += v.x * f; Os.y += v.y * f; Os.z += v.z * f; Os.w += v.w * f;
         }
     }
@@ -517,7 +521,7 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
                 }
                 __syncwarp();
             }
-            float ks[RT][2], lv[RT][2], iv[RT][2];
+            float ks[RT][2], lv[RT][2], lw[RT][2];
             const float* sp = reinterpret_cast<const float*>(bytes + C::kSOff);
 #pragma unroll
             for (int r = 0; r < RT; ++r)
@@ -527,9 +531,10 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
                     float vs = sp[s_off[r][i] + p.bs];
                     if (partial && r0 + 16 * r + 8 * i + g >= md.n_valid) vs = 1.f;
                     lv[r][i] = lg2(max_nan(vs, kLeastScale));
-                    // fminf drops a NaN, which stays in lv: the scores of a row of scale NaN
-                    // are NaN, but a causal query that does not see it adds 0 * iv
-                    iv[r][i] = fminf(ex2(-lv[r][i]), 1.f / kLeastScale);
+                    // log2 of what takes p' to the sum of weights.  fminf drops a NaN, which
+                    // stays in lv: the scores of a row of scale NaN are NaN, but a causal
+                    // query that does not see it adds 0.
+                    lw[r][i] = fminf(kSumBias - lv[r][i], kSumBias + 60.f);
                 }
             float x[RT][4];
 #pragma unroll
@@ -582,16 +587,16 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
                 for (int r = 1; r < RT; ++r) top[c] = fmaxf(top[c], fmaxf(x[r][c], x[r][c + 2]));
             }
             if (__any_sync(0xffffffffu, top[0] > m[0] + (kLazyLog2 + kRefBias) || top[1] > m[1] + (kLazyLog2 + kRefBias))) {
-                float a[2];
+                float a[2];  // an empty column (m = -inf): 0
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
 #pragma unroll
                     for (int s = 4; s < 32; s <<= 1) top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], s));
                     const bool up = top[c] > m[c] + (kLazyLog2 + kRefBias);
-                    const float to = top[c] - kRefBias;
-                    a[c] = up ? ex2(m[c] - to) : 1.f;  // an empty column (m = -inf): 0
-                    if (up) m[c] = to;
-                    l[c] *= a[c];
+                    const float to = up ? top[c] - kRefBias : m[c];
+                    a[c] = up ? ex2(m[c] - to) : 1.f;
+                    if (up) l[c] = scale_sum(l[c], m[c] - to);
+                    m[c] = to;
                 }
 #pragma unroll
                 for (int i = 0; i < 2 * K; ++i) {
@@ -603,10 +608,10 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
             uint32_t pb[RT][2];
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-                const float p0 = ex2(x[r][0] - u0), p1 = ex2(x[r][1] - u1);
-                const float p2 = ex2(x[r][2] - u0), p3 = ex2(x[r][3] - u1);
-                l[0] += fmaf(p2, iv[r][1], p0 * iv[r][0]);
-                l[1] += fmaf(p3, iv[r][1], p1 * iv[r][0]);
+                const float d0 = x[r][0] - u0, d1 = x[r][1] - u1, d2 = x[r][2] - u0, d3 = x[r][3] - u1;
+                const float p0 = ex2(d0), p1 = ex2(d1), p2 = ex2(d2), p3 = ex2(d3);
+                l[0] += ex2(d0 + lw[r][0]) + ex2(d2 + lw[r][1]);
+                l[1] += ex2(d1 + lw[r][0]) + ex2(d3 + lw[r][1]);
                 pb[r][0] = movmatrix_trans(pack_f16x2(p0, p1));
                 pb[r][1] = movmatrix_trans(pack_f16x2(p2, p3));
             }
@@ -651,7 +656,7 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
                 if (g == 0) {
                     // a NaN sum must not hide behind an empty reference
                     st_m[rw * 16 + h] = l[c] == l[c] ? m[c] : 0.f;
-                    st_l[rw * 16 + h] = l[c];
+                    st_l[rw * 16 + h] = l[c] * (1.f / (1 << (int)kSumBias));
                 }
                 float* r = st_o + (size_t)(warp * 8 + hr) * kOStride + 2 * g;
 #pragma unroll

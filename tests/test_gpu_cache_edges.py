@@ -145,3 +145,34 @@ def test_q_with_one_large_element(dtype, hq, hkv, d, bs, q_len, times):
             moved[b] = 2 * d ** -0.5 * (dq[b] * k).sum(-1, keepdim=True)
     within(out, want, (DECODE + moved) * size)
     assert ctx.read_device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype", ref.FORMATS)
+@pytest.mark.parametrize("hq,hkv,d,bs,lens", [
+    (8, 2, 128, 16, [2, 37, 200, 5000]), (4, 1, 256, 16, [2, 300, 4000]), (2, 2, 64, 1, [2, 90]), (8, 1, 64, 16, [9001])])
+@pytest.mark.parametrize("kind", ["zeros and 2^90", "2^90 and zeros", "any"])
+@pytest.mark.parametrize("q_len", [1, 2])
+def test_values_of_any_size(dtype, hq, hkv, d, bs, lens, kind, q_len):
+    """Value rows of zeros beside rows of 2^90, and of any size from 2^-40 to 2^115: every row counts in the sum of
+    weights, whatever its V scale, in whole units and in units of many pieces."""
+    rng, g = np.random.default_rng(7), gen(d + len(lens))
+    table, pool = ref.sequences(rng, lens, bs)
+    kp, vp, sc = ref.random_cache(g, pool, bs, hkv, d, dtype)
+    for b, n in enumerate(lens):
+        if kind == "any":
+            e = torch.randint(-40, 116, (n, hkv), generator=g)
+        else:
+            e = torch.where(((torch.arange(n) < (n + 1) // 2) == (kind == "zeros and 2^90"))[:, None], -1000, 90).expand(n, hkv)
+        v = torch.randn((n, hkv, d), generator=g).clamp(-4, 4) * torch.exp2(e.double())[..., None].float()
+        codes, scale = ref.codes32(v, dtype)
+        for at in range(n):
+            blk, slot = int(table[b, at // bs]), at % bs
+            vp.view(torch.uint8)[blk, slot] = codes.view(torch.uint8)[at]
+            sc[blk, :, 1, slot] = scale[at]
+    q = 0.3 * torch.randn((len(lens), q_len, hq, d), generator=g).bfloat16()
+    ctx = ctx_of(hq, hkv, d, bs)
+    out = torch.empty(q.shape, dtype=torch.float32, device="cuda")
+    ctx.decode_multi(q.cuda(), kp.cuda(), vp.cuda(), table.cuda(), i32(lens), scales=sc.cuda(), out=out)
+    want, size = ref.decode64(q, kp, vp, sc, table, lens, bs)
+    within(out, want, DECODE * size)
+    assert ctx.read_device_errors() == 0
