@@ -630,8 +630,14 @@ pda_status pda_read_cache(pda_ctx* ctx, const pda_cache* cache, const int32_t* b
  *         unrounded) when out_f32, which PDA_CACHE_BF16 has for q_len 1 only.
  *   batch * q_len <= max_seqs.  Other arguments as pda_decode.
  * 8-bit caches are read as they are: HBM sees one byte per element and 4 per
- * row; codes become fp16 in registers (exactly), K scales multiply the scores
- * and V scales the softmax weights, in fp32.
+ * row; K scales multiply the scores and V scales the softmax weights, in fp32.
+ *   keys     int8 codes are multiplied as fp16 (exact) by q in fp16, which holds
+ *            elements of q exactly down to 2^-24 of their row's largest; e4m3
+ *            codes as they are by q in two e4m3 parts, exact down to 2^-14 of it
+ *            and to 2^-22 of it below that.
+ *   values   codes are multiplied as fp16 (exact) by the weights: in one fp16
+ *            part (2^-11) for bf16 outputs, in two (2^-22) for fp32 outputs.
+ * Products and the sum of the unrounded weights are fp32.
  */
 pda_status pda_decode_cache(pda_ctx* ctx, const pda_bf16* q, const pda_cache* cache,
                             const int32_t* block_table, int32_t max_blocks,

@@ -200,8 +200,8 @@ pda_status run_quant(pda_ctx* ctx, const pda_bf16* q, const pda_cache* c, const 
     const int tiles = q_len * G > 8 && ctx->quant_ctas[1] > 0 ? 2 : 1;
     const int qp = std::max(1, std::min(q_len, 8 * tiles / G));
     const int Qr = (q_len + qp - 1) / qp;
-    const bool multi = q_len > 1;
-    const pda::QuantShape shape = pda::quant_shape(D, c->format, tiles, multi);
+    const pda::QuantForm form = {c->format, tiles, q_len > 1, f32};
+    const pda::QuantShape shape = pda::quant_shape(D, form);
     const int grid = ctx->quant_ctas[tiles - 1];
     if (Qr > grid) return fail(PDA_ERR_INVALID_ARG, "q_len %d: more launch rows per sequence than CTAs (%d)", q_len, grid);
     p.unit_cost = pda::quant_unit_cost(D, tiles, bs);
@@ -245,7 +245,7 @@ pda_status run_quant(pda_ctx* ctx, const pda_bf16* q, const pda_cache* c, const 
         p.lens = lens + s0;
         p.out = f32 ? nullptr : static_cast<uint16_t*>(out) + s0 * q_len * Hq * D;
         p.out_f32 = f32 ? static_cast<float*>(out) + s0 * q_len * Hq * D : nullptr;
-        const cudaError_t e = pda::launch_quant(D, c->format, tiles, multi, p, grid, shape.smem(p.B), stream);
+        const cudaError_t e = pda::launch_quant(D, form, p, grid, shape.smem(p.B), stream);
         if (e != cudaSuccess) return cuda_fail(e, "decode_cache launch");
     }
     ctx->tile_steps = 0;
@@ -260,8 +260,8 @@ pda_status pda::quant_setup(pda_ctx* ctx, int optin) {
     for (int tiles = 1; tiles <= 2; ++tiles) {
         int per_sm = 1 << 30;
         for (int format : {PDA_CACHE_E4M3, PDA_CACHE_INT8})
-            for (int multi = 0; multi < 2; ++multi) {
-                const QuantShape s = quant_shape(D, format, tiles, multi != 0);
+            for (int k = 0; k < 4; ++k) {
+                const QuantShape s = quant_shape(D, {format, tiles, (k & 1) != 0, (k & 2) != 0});
                 if (!s.fn) { per_sm = 0; continue; }
                 const int limit = (int)s.smem(kMaxLaunchBatch);
                 if (limit > optin)

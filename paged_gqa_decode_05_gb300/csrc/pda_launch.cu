@@ -122,31 +122,29 @@ cudaError_t launch_merge_states(const float* m_parts, const float* l_parts, cons
 
 namespace pda {
 
-#define PDA_DECLARE_QUANT(D)                                                                       \
-    const void* quant_fn_d##D(int format, int n_tiles, bool multi);                                \
-    cudaError_t launch_quant_d##D(int format, int n_tiles, bool multi, const QuantParams& p,       \
-                                  int grid, size_t smem, cudaStream_t stream);
+#define PDA_DECLARE_QUANT(D)                                                                  \
+    const void* quant_fn_d##D(const QuantForm& form);                                         \
+    cudaError_t launch_quant_d##D(const QuantForm& form, const QuantParams& p, int grid,      \
+                                  size_t smem, cudaStream_t stream);
 PDA_DECLARE_QUANT(64)
 PDA_DECLARE_QUANT(128)
 PDA_DECLARE_QUANT(256)
 
-QuantShape quant_shape(int D, int format, int n_tiles, bool multi) {
+QuantShape quant_shape(int D, const QuantForm& form) {
     QuantShape s;
-    s.fn = D == 64 ? quant_fn_d64(format, n_tiles, multi) : D == 128 ? quant_fn_d128(format, n_tiles, multi)
-         : D == 256 ? quant_fn_d256(format, n_tiles, multi) : nullptr;
-    s.threads = (quant_warps(D, n_tiles) + 2) * 32;
-    s.stage_rows = quant_stage_rows(D, n_tiles);
-    s.stages = quant_stages(D, n_tiles);
-    s.stage_bytes = quant_stage_bytes(D, n_tiles);
+    s.fn = D == 64 ? quant_fn_d64(form) : D == 128 ? quant_fn_d128(form) : D == 256 ? quant_fn_d256(form) : nullptr;
+    s.threads = (quant_warps(D, form.n_tiles) + 2) * 32;
+    s.stage_rows = quant_stage_rows(D, form.n_tiles);
+    s.stages = quant_stages(D, form.n_tiles);
+    s.stage_bytes = quant_stage_bytes(D, form.n_tiles);
     return s;
 }
 
-cudaError_t launch_quant(int D, int format, int n_tiles, bool multi, const QuantParams& p, int grid, size_t smem,
-                         cudaStream_t stream) {
+cudaError_t launch_quant(int D, const QuantForm& form, const QuantParams& p, int grid, size_t smem, cudaStream_t stream) {
     switch (D) {
-        case 64: return launch_quant_d64(format, n_tiles, multi, p, grid, smem, stream);
-        case 128: return launch_quant_d128(format, n_tiles, multi, p, grid, smem, stream);
-        case 256: return launch_quant_d256(format, n_tiles, multi, p, grid, smem, stream);
+        case 64: return launch_quant_d64(form, p, grid, smem, stream);
+        case 128: return launch_quant_d128(form, p, grid, smem, stream);
+        case 256: return launch_quant_d256(form, p, grid, smem, stream);
         default: return cudaErrorInvalidValue;
     }
 }

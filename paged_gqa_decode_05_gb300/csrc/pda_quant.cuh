@@ -23,10 +23,13 @@
 // whatever the V scales are; the sum of weights adds 2^(s - m'), which may be
 // as small as 2^-116 or as large as 2^74 (see kSumBias).  (m', l, o) is an
 // online-softmax state like any other: o / l and merges do not depend on the
-// reference.  p' enters the product as fp16, 2^-11 of it at most: an eighth of
-// the output's own bf16 half step.  References sit kRefBias below the maximum
-// they were taken at and move when a maximum passes them by more than kRefBias +
-// kLazyLog2, so p' < 2^14 and what fp16 flushes is 2^-31 of the largest weight.
+// reference.  For bf16 outputs p' enters the product as fp16, off by 2^-11 of it
+// at most: an eighth of the output's own half step.  For fp32 outputs (FINE) it
+// enters as two fp16 parts, off by 2^-22, at twice the products with V (32
+// sequences of 4096 tokens: 53.3 us for 52.3, 4 queries on 2456: 67.9 for 63.9).
+// References sit kRefBias below the maximum they were taken at and move when a
+// maximum passes them by more than kRefBias + kLazyLog2, so p' < 2^14 and what
+// fp16 flushes is 2^-31 of the largest weight.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -403,7 +406,7 @@ __device__ __forceinline__ bool quant_q_fragments(uint8_t* at, float* back, int 
     return consumer_sync(cbar, cphase, err, abort_flag);
 }
 
-template <int D, int FMT, int NT, int MODE, class Notes>
+template <int D, int FMT, int NT, int MODE, bool FINE, class Notes>
 __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_t base_s, uint8_t* base,
                                                    const SmemLayout& L, const StageMeta* meta, const int32_t* pfx,
                                                    volatile int* abort_flag, const GroupRange* group,
@@ -605,15 +608,22 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
             }
             const float u0 = m[0] == kNegInf ? 0.f : m[0];
             const float u1 = m[1] == kNegInf ? 0.f : m[1];
-            uint32_t pb[RT][2];
+            uint32_t pb[RT][2], pl[RT][2];  // weights, and (FINE) what fp16 leaves of them
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
                 const float d0 = x[r][0] - u0, d1 = x[r][1] - u1, d2 = x[r][2] - u0, d3 = x[r][3] - u1;
                 const float p0 = ex2(d0), p1 = ex2(d1), p2 = ex2(d2), p3 = ex2(d3);
                 l[0] += ex2(d0 + lw[r][0]) + ex2(d2 + lw[r][1]);
                 l[1] += ex2(d1 + lw[r][0]) + ex2(d3 + lw[r][1]);
-                pb[r][0] = movmatrix_trans(pack_f16x2(p0, p1));
-                pb[r][1] = movmatrix_trans(pack_f16x2(p2, p3));
+                const uint32_t h01 = pack_f16x2(p0, p1), h23 = pack_f16x2(p2, p3);
+                pb[r][0] = movmatrix_trans(h01);
+                pb[r][1] = movmatrix_trans(h23);
+                if constexpr (FINE) {
+                    const float2 b01 = __half22float2(*reinterpret_cast<const __half2*>(&h01));
+                    const float2 b23 = __half22float2(*reinterpret_cast<const __half2*>(&h23));
+                    pl[r][0] = movmatrix_trans(pack_f16x2(p0 - b01.x, p1 - b01.y));
+                    pl[r][1] = movmatrix_trans(pack_f16x2(p2 - b23.x, p3 - b23.y));
+                }
             }
 #pragma unroll
             for (int kk = 0; kk < K; ++kk)
@@ -625,6 +635,10 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
                     v_fragment<FMT>(w[2], w[3], b);
                     mma_f16_16816(o[2 * kk], a, pb[r][0], pb[r][1]);
                     mma_f16_16816(o[2 * kk + 1], b, pb[r][0], pb[r][1]);
+                    if constexpr (FINE) {
+                        mma_f16_16816(o[2 * kk], a, pl[r][0], pl[r][1]);
+                        mma_f16_16816(o[2 * kk + 1], b, pl[r][0], pl[r][1]);
+                    }
                 }
             if (FMT == kE4m3 && partial) fence_proxy_async_smem();  // generic writes before the next TMA
         }
@@ -692,7 +706,7 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
     }
 }
 
-template <int D, int FMT, int NT, int MODE>
+template <int D, int FMT, int NT, int MODE, bool FINE>
 __global__ void __maxnreg__(168) quant_split_kernel(const __grid_constant__ QuantParams p) {
     using C = QuantCfg<D, NT>;
     extern __shared__ uint8_t smem_raw[];
@@ -742,10 +756,10 @@ __global__ void __maxnreg__(168) quant_split_kernel(const __grid_constant__ Quan
         run_producer<C, QuantLoader<D, NT>, D, MODE>(p, base_s, L, pfx, meta, &abort_flag, begin, end, lane);
         return;
     }
-    run_quant_consumer<D, FMT, NT, MODE>(p, base_s, base, L, meta, pfx, &abort_flag, &group, &notes, warp, lane);
+    run_quant_consumer<D, FMT, NT, MODE, FINE>(p, base_s, base, L, meta, pfx, &abort_flag, &group, &notes, warp, lane);
 }
 
-template <int D, int FMT, int NT, int MODE>
+template <int D, int FMT, int NT, int MODE, bool FINE>
 cudaError_t launch_quant_as(const QuantParams& p, int grid, size_t smem, cudaStream_t stream) {
     using C = QuantCfg<D, NT>;
     cudaLaunchConfig_t cfg = {};
@@ -758,39 +772,47 @@ cudaError_t launch_quant_as(const QuantParams& p, int grid, size_t smem, cudaStr
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, quant_split_kernel<D, FMT, NT, MODE>, p);
+    return cudaLaunchKernelEx(&cfg, quant_split_kernel<D, FMT, NT, MODE, FINE>, p);
 }
 
-template <int D, int FMT, int NT>
-const void* quant_fn_of(bool multi) {
-    if constexpr (NT == 1)
-        if (!multi) return reinterpret_cast<const void*>(&quant_split_kernel<D, FMT, 1, kOneShot>);
-    return reinterpret_cast<const void*>(&quant_split_kernel<D, FMT, NT, kMulti>);
-}
-
-template <int D>
-const void* quant_fn(int format, int n_tiles, bool multi) {
-    if (n_tiles == 2) {
-        if constexpr (D <= 128) return format == kE4m3 ? quant_fn_of<D, kE4m3, 2>(true) : quant_fn_of<D, kInt8, 2>(true);
-        return nullptr;
-    }
-    return format == kE4m3 ? quant_fn_of<D, kE4m3, 1>(multi) : quant_fn_of<D, kInt8, 1>(multi);
-}
-
-template <int D, int FMT>
-cudaError_t launch_quant_fmt(int n_tiles, bool multi, const QuantParams& p, int grid, size_t smem, cudaStream_t s) {
+// visit(instance) of the form, or `none` where it does not exist: one tile of
+// q rows has a form for single queries, head size 256 no second tile.
+template <int FMT, int NT, int MODE, bool FINE>
+struct QuantInstance {
+    static constexpr int fmt = FMT, nt = NT, mode = MODE;
+    static constexpr bool fine = FINE;
+};
+template <int D, int FMT, bool FINE, class R, class Visit>
+R visit_quant_tiles(const QuantForm& form, R none, const Visit& visit) {
+    if (form.n_tiles == 1)
+        return form.multi ? visit(QuantInstance<FMT, 1, kMulti, FINE>()) : visit(QuantInstance<FMT, 1, kOneShot, FINE>());
     if constexpr (D <= 128)
-        if (n_tiles == 2) return launch_quant_as<D, FMT, 2, kMulti>(p, grid, smem, s);
-    if (n_tiles != 1) return cudaErrorInvalidValue;
-    return multi ? launch_quant_as<D, FMT, 1, kMulti>(p, grid, smem, s)
-                 : launch_quant_as<D, FMT, 1, kOneShot>(p, grid, smem, s);
+        if (form.n_tiles == 2) return visit(QuantInstance<FMT, 2, kMulti, FINE>());
+    return none;
+}
+template <int D, class R, class Visit>
+R visit_quant(const QuantForm& form, R none, const Visit& visit) {
+    if (form.format == kE4m3)
+        return form.fine ? visit_quant_tiles<D, kE4m3, true>(form, none, visit)
+                         : visit_quant_tiles<D, kE4m3, false>(form, none, visit);
+    return form.fine ? visit_quant_tiles<D, kInt8, true>(form, none, visit)
+                     : visit_quant_tiles<D, kInt8, false>(form, none, visit);
 }
 
 template <int D>
-cudaError_t launch_quant_of(int format, int n_tiles, bool multi, const QuantParams& p, int grid, size_t smem,
-                            cudaStream_t stream) {
-    return format == kE4m3 ? launch_quant_fmt<D, kE4m3>(n_tiles, multi, p, grid, smem, stream)
-                           : launch_quant_fmt<D, kInt8>(n_tiles, multi, p, grid, smem, stream);
+const void* quant_fn(const QuantForm& form) {
+    return visit_quant<D>(form, (const void*)nullptr, [](auto i) {
+        using I = decltype(i);
+        return reinterpret_cast<const void*>(&quant_split_kernel<D, I::fmt, I::nt, I::mode, I::fine>);
+    });
+}
+
+template <int D>
+cudaError_t launch_quant_of(const QuantForm& form, const QuantParams& p, int grid, size_t smem, cudaStream_t stream) {
+    return visit_quant<D>(form, cudaErrorInvalidValue, [&](auto i) {
+        using I = decltype(i);
+        return launch_quant_as<D, I::fmt, I::nt, I::mode, I::fine>(p, grid, smem, stream);
+    });
 }
 
 }  // namespace pda

@@ -53,17 +53,22 @@ struct QuantParams : SplitParams {
     int32_t joined, v_first, box_head;
 };
 
+// An instance of the kernel.
+struct QuantForm {
+    int format;   // kE4m3 / kInt8
+    int n_tiles;  // 1: up to 8 q rows per walk, 2: 16 (head sizes up to 128)
+    bool multi;   // several causal queries per sequence
+    bool fine;    // weights in two fp16 parts: fp32 outputs
+};
+
 struct QuantShape {
-    const void* fn;
+    const void* fn;   // null: no such instance
     int threads;      // with the prefetch warp
     int stage_rows, stages, stage_bytes;
     uint32_t smem(int B) const { return smem_layout_of((uint32_t)stage_bytes, kOneShot, stages, B).total; }
 };
 
-// format kE4m3 / kInt8; n_tiles 1 (up to 8 q rows per walk) or 2 (16, head
-// sizes up to 128); multi: several causal queries per sequence.
-QuantShape quant_shape(int D, int format, int n_tiles, bool multi);
-cudaError_t launch_quant(int D, int format, int n_tiles, bool multi, const QuantParams& p, int grid,
-                         size_t smem, cudaStream_t stream);
+QuantShape quant_shape(int D, const QuantForm& form);
+cudaError_t launch_quant(int D, const QuantForm& form, const QuantParams& p, int grid, size_t smem, cudaStream_t stream);
 
 }  // namespace pda

@@ -3,11 +3,10 @@
 
 namespace pda {
 
-const void* quant_fn_d128(int format, int n_tiles, bool multi) { return quant_fn<128>(format, n_tiles, multi); }
+const void* quant_fn_d128(const QuantForm& form) { return quant_fn<128>(form); }
 
-cudaError_t launch_quant_d128(int format, int n_tiles, bool multi, const QuantParams& p, int grid, size_t smem,
-                            cudaStream_t stream) {
-    return launch_quant_of<128>(format, n_tiles, multi, p, grid, smem, stream);
+cudaError_t launch_quant_d128(const QuantForm& form, const QuantParams& p, int grid, size_t smem, cudaStream_t stream) {
+    return launch_quant_of<128>(form, p, grid, smem, stream);
 }
 
 }  // namespace pda

@@ -176,3 +176,32 @@ def test_values_of_any_size(dtype, hq, hkv, d, bs, lens, kind, q_len):
     want, size = ref.decode64(q, kp, vp, sc, table, lens, bs)
     within(out, want, DECODE * size)
     assert ctx.read_device_errors() == 0
+
+
+# ------------------------------------------------------------------ fp32 outputs
+
+# Of sum p |v|: weights in two fp16 parts 2^-22; the two exponentials of a weight, their arguments (below 2^5, three
+# roundings of 2^-24 of them) and log2 of its V scale 2^-18; scores of up to 2^5 in base 2, summed in fp32 over at most
+# 16 products' partial sums, 2^-16.  What fp16 flushes is 2^-31 of the largest weight for every code.
+FINE = 2.0 ** -15
+
+
+@pytest.mark.parametrize("dtype", ref.FORMATS)
+@pytest.mark.parametrize("hq,hkv,d,bs,q_len", [(8, 2, 128, 16, 1), (8, 1, 128, 16, 2), (4, 1, 256, 4, 1), (8, 2, 64, 1, 1),
+                                               (4, 2, 64, 64, 4)])
+@pytest.mark.parametrize("lens", [[2, 3, 5, 9], [33, 64, 100], [5000]])
+def test_fp32_outputs_are_unrounded(dtype, hq, hkv, d, bs, q_len, lens):
+    rng, g = np.random.default_rng(2), gen(d + q_len)
+    table, pool = ref.sequences(rng, lens, bs)
+    kp, vp, sc = ref.random_cache(g, pool, bs, hkv, d, dtype)
+    q = torch.randn((len(lens), q_len, hq, d), generator=g).bfloat16()
+    ctx = ctx_of(hq, hkv, d, bs)
+    args = (kp.cuda(), vp.cuda(), table.cuda(), i32(lens))
+    out = torch.empty(q.shape, dtype=torch.float32, device="cuda")
+    ctx.decode_multi(q.cuda(), *args, scales=sc.cuda(), out=out)
+    want, size = ref.decode64(q, kp, vp, sc, table, lens, bs)
+    heavy = ref.decode64(q, kp, (vp.float().abs()).to(dtype), sc, table, lens, bs)[0]  # sum p |v|
+    within(out, want, FINE * heavy + 2.0 ** -10 * (size - heavy))
+    # and the bf16 output is its rounding, up to what bf16 outputs' weights lose
+    rounded = ctx.decode_multi(q.cuda(), *args, scales=sc.cuda())
+    within(rounded, want, BF16 * want.abs() + 2.0 ** -9 * size)
