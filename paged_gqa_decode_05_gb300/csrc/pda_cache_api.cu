@@ -237,6 +237,10 @@ pda_status run_quant(pda_ctx* ctx, const pda_bf16* q, const pda_cache* c, const 
     if (chunk < 1)
         return fail(PDA_ERR_UNSUPPORTED, "q_len %d: a sequence's %d launch rows exceed the partial-state buffers", q_len,
                     Qr);
+    const bool timing = ctx->ev_begin && ctx->ev_split && ctx->ev_end;
+    if (timing)
+        if (const cudaError_t e = cudaEventRecord(ctx->ev_begin, stream); e != cudaSuccess)
+            return cuda_fail(e, "cudaEventRecord");
     for (int32_t c0 = 0; c0 < rows_total; c0 += chunk) {
         const int64_t s0 = c0 / Qr;  // first sequence of the chunk
         p.B = std::min(chunk, rows_total - c0);
@@ -248,6 +252,10 @@ pda_status run_quant(pda_ctx* ctx, const pda_bf16* q, const pda_cache* c, const 
         const cudaError_t e = pda::launch_quant(D, form, p, grid, shape.smem(p.B), stream);
         if (e != cudaSuccess) return cuda_fail(e, "decode_cache launch");
     }
+    if (timing)
+        for (const cudaEvent_t ev : {ctx->ev_split, ctx->ev_end})
+            if (const cudaError_t e = cudaEventRecord(ev, stream); e != cudaSuccess)
+                return cuda_fail(e, "cudaEventRecord");
     ctx->tile_steps = 0;
     return PDA_OK;
 }

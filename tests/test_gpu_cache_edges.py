@@ -205,3 +205,30 @@ def test_fp32_outputs_are_unrounded(dtype, hq, hkv, d, bs, q_len, lens):
     # and the bf16 output is its rounding, up to what bf16 outputs' weights lose
     rounded = ctx.decode_multi(q.cuda(), *args, scales=sc.cuda())
     within(rounded, want, BF16 * want.abs() + 2.0 ** -9 * size)
+
+
+# ------------------------------------------------------------------ timing events
+
+@pytest.mark.parametrize("q_len", [1, 3])
+@pytest.mark.parametrize("dtype", ref.FORMATS)
+def test_timing_events_are_recorded(dtype, q_len):
+    """set_timing_events times decodes over 8-bit caches as it does others, one launch or several."""
+    g, rng = gen(5), np.random.default_rng(5)
+    hq, hkv, d, bs, B = 4, 2, 64, 16, 1100 // q_len
+    table, pool = ref.sequences(rng, [40] * B, bs)
+    kp, vp, sc = (t.cuda() for t in ref.random_cache(g, pool, bs, hkv, d, dtype))
+    q = torch.randn((B, q_len, hq, d), generator=g).bfloat16().cuda()
+    ctx = ctx_of(hq, hkv, d, bs, max_seqs=B * q_len)
+    evs = [torch.cuda.Event(enable_timing=True) for _ in range(3)]
+    for e in evs:
+        e.record()  # creates the underlying events
+    torch.cuda.synchronize()
+    around = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    ctx.set_timing_events(*evs)
+    around[0].record()
+    ctx.decode_multi(q, kp, vp, table.cuda(), i32([40] * B), scales=sc)
+    around[1].record()
+    torch.cuda.synchronize()
+    assert 0 < evs[0].elapsed_time(evs[1]) <= evs[0].elapsed_time(evs[2]) <= around[0].elapsed_time(around[1])
+    assert 0 <= around[0].elapsed_time(evs[0])
+    ctx.set_timing_events()
