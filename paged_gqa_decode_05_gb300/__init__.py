@@ -421,6 +421,17 @@ class Context:
         with torch.cuda.stream(stream):
             return fn(shape, dtype=dtype, device=self.device)
 
+    def _out(self, out, shape, f32, stream):
+        """`out` as a contiguous CUDA tensor of bfloat16, or float32 where f32, with room for shape; a new one if None."""
+        torch = _torch()
+        dtype = torch.float32 if f32 else torch.bfloat16
+        if out is None:
+            return self._make(torch.empty, shape, dtype, stream)
+        shape = torch.Size(shape)
+        if out.dtype != dtype or not out.is_cuda or not out.is_contiguous() or out.shape.numel() < shape.numel():
+            raise ValueError(f"out must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)}")
+        return out
+
     def _scale(self, scale) -> float:
         return float("nan") if scale is None else float(scale)
 
@@ -438,9 +449,8 @@ class Context:
         if scales is not None or k_pool.dtype in (torch.float8_e4m3fn, torch.int8):
             B = int(seq_lens.shape[0])
             self._bf16(q, "q", (B, self.dims.num_q_heads, self.dims.head_dim))
-            if out is None:
-                out = self._make(torch.empty, q.shape, torch.float32 if out_dtype == torch.float32 else torch.bfloat16,
-                                 stream)
+            if out is None or out_dtype is not None:
+                out = self._out(out, q.shape, out_dtype == torch.float32, stream)
             return self._decode_cache(q, 1, k_pool, v_pool, scales, block_table, seq_lens, scale, out, strides,
                                       num_blocks, stream)()
         d = self.dims
@@ -452,9 +462,7 @@ class Context:
             raise ValueError("block_table must have one row per sequence")
         (bs_, ts_, hs_), nblk = self._pool(k_pool, v_pool, strides, num_blocks)
         f32 = out_dtype == torch.float32
-        if out is None:
-            out = self._make(torch.empty, (B, d.num_q_heads, d.head_dim), torch.float32 if f32 else torch.bfloat16,
-                             stream)
+        out = self._out(out, (B, d.num_q_heads, d.head_dim), f32, stream)
         L = lib()
         if f32:
             _check(L.pda_decode_f32(self._ctx, _ptr(q), _ptr(k_pool), _ptr(v_pool), nblk, bs_, ts_,
@@ -732,9 +740,7 @@ class Context:
         torch = _torch()
         d = self.dims
         f32 = out_dtype == torch.float32
-        if out is None:
-            out = self._make(torch.empty, (num_seqs, d.num_q_heads, d.head_dim),
-                             torch.float32 if f32 else torch.bfloat16, stream)
+        out = self._out(out, (num_seqs, d.num_q_heads, d.head_dim), f32, stream)
         fn = lib().pda_finalize_f32 if f32 else lib().pda_finalize
         _check(fn(self._ctx, _ptr(out), int(num_seqs), _stream(stream)))
         return out
@@ -766,9 +772,7 @@ class Context:
                     tuple(t.shape) != shape:
                 raise ValueError(f"{name} must be a contiguous float32 CUDA tensor of shape {shape}")
         f32 = out_dtype == torch.float32
-        if out is None:
-            out = self._make(torch.empty, (S, d.num_q_heads, d.head_dim), torch.float32 if f32 else torch.bfloat16,
-                             stream)
+        out = self._out(out, (S, d.num_q_heads, d.head_dim), f32, stream)
         fn = lib().pda_merge_states_f32 if f32 else lib().pda_merge_states
         _check(fn(self._ctx, P_, S, _ptr(m_parts), _ptr(l_parts), _ptr(o_parts), _ptr(out),
                   _stream(stream)))
