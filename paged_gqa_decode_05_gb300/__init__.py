@@ -506,21 +506,25 @@ class Context:
                       (q, k_pool, v_pool, block_table, seq_lens, out))
 
     def decode_multi(self, q, k_pool, v_pool, block_table, seq_lens, scale: Optional[float] = None,
-                     out=None, stream=None, scales=None):
+                     out=None, stream=None, scales=None, strides: Optional[Sequence[int]] = None,
+                     num_blocks: Optional[int] = None, out_dtype=None):
         """Causal multi-query decode: q [B, q_len, Hq, D] are each sequence's last q_len
         tokens; query i sees tokens up to seq_lens[b] - q_len + i.  Returns [B, q_len, Hq, D].
-        Pools in 8 bits come with their ``scales``, as for decode."""
+        Pools in 8 bits come with their ``scales``, ``strides`` and ``num_blocks`` place
+        pools of other layouts, and ``out_dtype=torch.float32`` returns o / l unrounded, as for
+        decode (over bfloat16 pools for q_len 1 only)."""
         torch = _torch()
         d = self.dims
         B = int(seq_lens.shape[0])
         if q.dim() != 4 or q.shape[0] != B or q.shape[2:] != (d.num_q_heads, d.head_dim):
             raise ValueError("q must be [B, q_len, Hq, D]")
         self._bf16(q, "q")
-        if scales is not None or k_pool.dtype in (torch.float8_e4m3fn, torch.int8):
-            if out is None:
-                out = self._make(torch.empty, q.shape, torch.bfloat16, stream)
+        f32 = out_dtype == torch.float32
+        if scales is not None or strides is not None or f32 or k_pool.dtype in (torch.float8_e4m3fn, torch.int8):
+            if out is None or out_dtype is not None:
+                out = self._out(out, q.shape, f32, stream)
             return self._decode_cache(q, int(q.shape[1]), k_pool, v_pool, scales, block_table, seq_lens, scale, out,
-                                      None, None, stream)()
+                                      strides, num_blocks, stream)()
         self._i32(block_table, "block_table", 2)
         self._i32(seq_lens, "seq_lens", 1)
         (bs_, ts_, hs_), nblk = self._pool(k_pool, v_pool, None, None)

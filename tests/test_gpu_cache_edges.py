@@ -232,3 +232,64 @@ def test_timing_events_are_recorded(dtype, q_len):
     assert 0 < evs[0].elapsed_time(evs[1]) <= evs[0].elapsed_time(evs[2]) <= around[0].elapsed_time(around[1])
     assert 0 <= around[0].elapsed_time(evs[0])
     ctx.set_timing_events()
+
+
+# ------------------------------------------------------------------ one call, any format and layout
+
+def slots_of(kp, vp):
+    """The pools as one, [slot, K | V, Hkv, bs, D] (slot_strides)."""
+    raw = [p.view(torch.int8 if p.element_size() == 1 else torch.int16).transpose(1, 2) for p in (kp, vp)]
+    return torch.stack(raw, 1).contiguous().view(kp.dtype).flatten().cuda()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16] + ref.FORMATS)
+@pytest.mark.parametrize("q_len", [1, 2, 5])
+@pytest.mark.parametrize("hq,hkv,d,bs", [(8, 2, 128, 16), (4, 4, 64, 4), (4, 1, 256, 8)])
+def test_decode_multi_of_other_strides(dtype, q_len, hq, hkv, d, bs):
+    """Several queries over the slot layout give the dense pools' bits, in every format; fp32 outputs."""
+    rng, g = np.random.default_rng(9), gen(d)
+    lens = [37, 200, 3, 0]
+    table, pool = ref.sequences(rng, lens, bs)
+    if dtype == torch.bfloat16:
+        kp, vp = (torch.randn((pool, bs, hkv, d), generator=g).bfloat16() for _ in range(2))
+        sc = None
+    else:
+        kp, vp, sc = ref.random_cache(g, pool, bs, hkv, d, dtype)
+    scales = None if sc is None else sc.cuda()
+    q = torch.randn((len(lens), q_len, hq, d), generator=g).bfloat16()
+    ctx = ctx_of(hq, hkv, d, bs)
+    rest = (table.cuda(), i32(lens))
+    want, size = ref.decode64(q, kp, vp, sc, table, lens, bs)
+    dense = ctx.decode_multi(q.cuda(), kp.cuda(), vp.cuda(), *rest, scales=scales)
+    within(dense, want, BF16 * want.abs() + 2 * DECODE * size)
+    both = slots_of(kp, vp)
+    layout = dict(strides=pda.slot_strides(num_q_heads=hq, num_kv_heads=hkv, head_dim=d, block_size=bs), num_blocks=pool)
+    assert torch.equal(ctx.decode_multi(q.cuda(), both, both[hkv * bs * d:], *rest, scales=scales, **layout), dense)
+    if dtype == torch.bfloat16 and q_len > 1:
+        with pytest.raises(pda.PdaError) as e:
+            ctx.decode_multi(q.cuda(), both, both[hkv * bs * d:], *rest, out_dtype=torch.float32, **layout)
+        assert e.value.status == pda.ERR_UNSUPPORTED
+        return
+    fine = ctx.decode_multi(q.cuda(), both, both[hkv * bs * d:], *rest, scales=scales, out_dtype=torch.float32, **layout)
+    assert fine.dtype == torch.float32
+    within(fine, want, DECODE * size)
+    if q_len == 1:
+        one = ctx.decode(q[:, 0].contiguous().cuda(), kp.cuda(), vp.cuda(), *rest, scales=scales, out_dtype=torch.float32)
+        assert torch.equal(fine[:, 0], one)
+    assert ctx.read_device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype", ref.FORMATS)
+@pytest.mark.parametrize("scale", [0.0, 0.3, -0.05, 1.0])
+def test_scales_of_the_scores(dtype, scale):
+    """A softmax scale other than the default; 0 takes the mean of the values."""
+    rng, g = np.random.default_rng(10), gen(10)
+    hq, hkv, d, bs, lens = 8, 2, 128, 16, [37, 200, 3, 2000]
+    table, pool = ref.sequences(rng, lens, bs)
+    kp, vp, sc = ref.random_cache(g, pool, bs, hkv, d, dtype)
+    q = 0.2 * torch.randn((len(lens), 2, hq, d), generator=g).bfloat16()
+    ctx = ctx_of(hq, hkv, d, bs)
+    got = ctx.decode_multi(q.cuda(), kp.cuda(), vp.cuda(), table.cuda(), i32(lens), scales=sc.cuda(), scale=scale,
+                           out_dtype=torch.float32)
+    want, size = ref.decode64(q, kp, vp, sc, table, lens, bs, scale=scale)
+    within(got, want, DECODE * size)
