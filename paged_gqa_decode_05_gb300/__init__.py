@@ -142,7 +142,10 @@ def lib() -> ctypes.CDLL:
         "pda_plan_units": (I32, [P, I32, I32, I32, I32, I32, I32, I32, P, P, ctypes.POINTER(I64)]),
     }
     for name, (res, args) in sig.items():
-        fn = getattr(L, name)
+        try:
+            fn = getattr(L, name)
+        except AttributeError:  # entry points are added within an ABI version
+            raise RuntimeError(f"{_LIBPATH} is older than this binding, which calls {name}: rebuild it") from None
         fn.restype = res
         fn.argtypes = args
     if L.pda_abi_version() != ABI_VERSION:
