@@ -616,7 +616,9 @@ pda_status pda_append(pda_ctx* ctx, const pda_heads* k, const pda_heads* v, cons
  *                 sequence b is row starts[b] + t, and rows of sequence b end
  *                 before starts[b+1].  NULL: num_rows / batch (exact) rows for
  *                 each sequence.  Rows of no token are left as they were.
- * A block id outside the pool reads as zeros, with the flag set.
+ * A block id outside the pool reads as zeros, with the flag set.  A length below
+ * 0 or beyond the table's width * block size raises PDA_DEVERR_BAD_LENGTH where
+ * the sequence has rows at all; tokens past its rows are not read.
  */
 pda_status pda_read_cache(pda_ctx* ctx, const pda_cache* cache, const int32_t* block_table,
                           int32_t max_blocks, const int32_t* seq_lens, int32_t batch,

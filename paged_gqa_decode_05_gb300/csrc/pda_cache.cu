@@ -594,8 +594,10 @@ __global__ void __launch_bounds__(kHeadsThreads) read_kernel(const __grid_consta
     const Place place = p.c.starts ? find_seq(p.c, t, lane) : share_of(p.c, t, live);
     const int32_t b = place.b;
     const int64_t at = t - place.begin;
-    live = live && at >= 0 && t < place.end && at < place.len;
-    if (!live) return;
+    live = live && at >= 0 && t < place.end;
+    if (live && at == 0 && r0 == 0 && l == 0 && (place.len < 0 || place.len > (int64_t)p.c.table_stride << p.c.lbs))
+        atomicOr(p.err, PDA_DEVERR_BAD_LENGTH_);  // whichever of its rows are asked for
+    if (!live || at >= place.len) return;
     const int64_t j = at >> p.c.lbs;
     const int slot = (int)at & ((1 << p.c.lbs) - 1);
     if (j >= p.c.table_stride) {

@@ -293,3 +293,36 @@ def test_scales_of_the_scores(dtype, scale):
                            out_dtype=torch.float32)
     want, size = ref.decode64(q, kp, vp, sc, table, lens, bs, scale=scale)
     within(got, want, DECODE * size)
+
+
+# ------------------------------------------------------------------ read_cache
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16] + ref.FORMATS)
+def test_read_cache_flags_bad_lengths(dtype, packed):
+    """A negative length and one past the table raise their flag, as in decode, and the rest is read."""
+    hkv, d, bs = 2, 64, 8
+    ctx = ctx_of(2, hkv, d, bs)
+    kp, vp, sc = ctx.new_cache(4, dtype)
+    kv = torch.randn((32, 2 * hkv, d), generator=gen(3)).bfloat16().cuda()
+    table = i32([[0, 1], [2, 3]])
+    ctx.append(kv[:, :hkv], kv[:, hkv:], kp, vp, table, i32([16, 16]), scales=sc)
+    kw = dict(scales=sc)
+    if packed:  # 16 rows each: none asks for more than the table holds
+        kw.update(starts=i32([0, 16, 32]))
+
+    def read(lens):
+        if packed:
+            kw.update({k: torch.full((32, hkv, d), 3.0, dtype=torch.bfloat16, device="cuda") for k in ("k_out", "v_out")})
+        return [x.reshape(2, 16, hkv, d) for x in ctx.read_cache(kp, vp, table, i32(lens), **kw)]
+
+    want = read([16, 16])
+    assert ctx.read_device_errors() == 0
+    for bad in (-1, -2 ** 31, 17, 2 ** 31 - 1):
+        got = read([16, bad])
+        assert ctx.read_device_errors() == pda.DEVERR_BAD_LENGTH, bad
+        for x, w in zip(got, want):
+            assert torch.equal(x[0], w[0])
+            assert torch.equal(x[1], w[1] if bad > 0 else torch.full_like(w[1], 3.0 if packed else 0.0))
+    read([0, 16])
+    assert ctx.read_device_errors() == 0
