@@ -326,3 +326,45 @@ def test_read_cache_flags_bad_lengths(dtype, packed):
             assert torch.equal(x[1], w[1] if bad > 0 else torch.full_like(w[1], 3.0 if packed else 0.0))
     read([0, 16])
     assert ctx.read_device_errors() == 0
+
+
+# ------------------------------------------------------------------ garbage
+
+@pytest.mark.parametrize("dtype", ref.FORMATS)
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("bs", [1, 4, 16, 64])
+@pytest.mark.parametrize("hq,q_len", [(8, 1), (8, 4), (1, 4)])
+@pytest.mark.parametrize("apart", [False, True])
+def test_garbage_outside_the_sequences(dtype, d, bs, hq, q_len, apart):
+    """NaN codes, NaN and infinite scales behind every end and in blocks of no sequence, ids of no block in the table
+    past a sequence's blocks: the output's bits do not change, whichever way the pools load (as one, or each alone)."""
+    hkv = 1
+    rng, g = np.random.default_rng(bs), gen(d)
+    lens = [37, 0, 81, 130, q_len, 64, 1000]
+    table, pool = ref.sequences(rng, lens, bs)
+    kp, vp, sc = ref.random_cache(g, pool, bs, hkv, d, dtype)
+    q = torch.randn((len(lens), q_len, hq, d), generator=g).bfloat16().cuda()
+    ctx = ctx_of(hq, hkv, d, bs)
+
+    def run(table):
+        pools = [p.cuda() for p in (kp, vp)]
+        if apart:  # rows wider than the head: no joined loads at head size 256
+            wide = torch.zeros((2, pool, bs, hkv, d + 16), dtype=torch.int8, device="cuda")
+            for w, p in zip(wide, pools):
+                w[..., :d] = p.view(torch.int8)
+            pools = [w.view(dtype).flatten() for w in wide]
+        return ctx.decode_multi(q, *pools, table.cuda(), i32(lens), scales=sc.cuda(), out_dtype=torch.float32,
+                                strides=[s * (d + 16 * apart) for s in (bs * hkv, hkv, 1)], num_blocks=pool)
+
+    want = run(table)
+    assert torch.isfinite(want).all()
+    live = torch.zeros((pool, bs), dtype=torch.bool)
+    for b, n in enumerate(lens):
+        for t in range(n):
+            live[int(table[b, t // bs]), t % bs] = True
+        table[b, -(-n // bs):] = torch.tensor([-1, 2 ** 31 - 1, pool]).repeat(table.shape[1])[:table.shape[1] - -(-n // bs)]
+    for p in (kp, vp):
+        p.view(torch.uint8)[~live] = 0x7f
+    sc.permute(0, 3, 1, 2)[~live] = torch.tensor([float("nan"), float("inf")])
+    assert torch.equal(run(table), want)
+    assert ctx.read_device_errors() == 0
