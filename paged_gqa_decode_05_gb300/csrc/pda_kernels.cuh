@@ -1946,8 +1946,9 @@ __device__ __forceinline__ GroupRange cta_range(const SplitParams& p, const int3
 constexpr int kPrefetchStages = PDA_PREFETCH_STAGES;  // stages of blocks prefetched
 
 // The prefetch warp: a speculative L2 prefetch of the blocks of the CTA's
-// first stages, before the grid-dependency wait, so that while the previous
-// kernel finishes, those blocks' K/V rows move towards L2.  It builds its own
+// first stages (of an even split over the whole grid; 8-bit decode of few units
+// walks a coarser one), before the grid-dependency wait, so that while the
+// previous kernel finishes, those blocks' K/V rows move towards L2.  It builds its own
 // plan in registers (lengths read from L2, so no L1 line of them outlives the
 // wait; no flags raised), reads the first block ids from L2 and prefetches
 // their boxes, then exits: it shares no barrier with the other warps, which

@@ -226,6 +226,11 @@ struct UnitSlices {
 // million 134, 135, 150, 160; eight kv heads, 8192 tokens 17.2, 16.3, 16.2, 17.8.
 // Two sequences of 2800 tokens, two kv heads of 256, blocks of one token: 35.4,
 // 31.8, 30.2, 28.4, with a stage each 27.7.
+// The prefetch warp cuts the work by the whole grid all the same: where fewer
+// CTAs walk it, a CTA warms blocks that another one walks.  Cut by these CTAs
+// instead, 8192 tokens of one kv head took 15.2 us for 15.1, 4 x 3000 of four
+// 14.25 for 14.2, half a million of one 70.6 for 73.3; with no prefetch 15.0,
+// 14.25 and 69.6 (replayed back to back, the first two from L2).
 template <bool MQ, int ST>
 __device__ __forceinline__ int64_t quant_plan_ctas(const SplitParams& p, const int32_t* pfx) {
     const int64_t stages = ((int64_t)pfx[p.B] * p.Hkv * p.bs + ST - 1) / ST, units = (int64_t)p.B * p.Hkv;
