@@ -284,13 +284,33 @@ __device__ __forceinline__ void v_fragment(uint32_t r0, uint32_t r1, uint32_t (&
 // 0xff in the bytes of x that are NaN codes of e4m3.
 __device__ __forceinline__ uint32_t nan_codes(uint32_t x) { return __vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu); }
 
+// Where chunk c (16 bytes) of row r lies in a stage's V part at sV, before the
+// swizzle of a row's chunks.
+template <int D>
+__device__ __forceinline__ uint32_t quant_chunk(uint32_t sV, int r, int c, int lbs) {
+    constexpr int RB = D < 128 ? D : 128, CPS = RB / 16;
+    return sV + quant_row_off<D>(r, lbs) + (((uint32_t)(c / CPS) * RB) << lbs) + (uint32_t)(c % CPS) * 16;
+}
+// Whether rows r .. r + n - 1 hold a NaN code (one warp's answer).
+template <int D>
+__device__ __forceinline__ bool any_nan_code(uint32_t sV, int r, int n, int lbs, int lane) {
+    uint32_t any = 0;
+#pragma unroll 1
+    for (int u = lane; u < n * (D / 16); u += 32) {
+        uint32_t x[4];
+        lds_v4(quant_chunk<D>(sV, r + u / (D / 16), u % (D / 16), lbs), x);
+        any |= nan_codes(x[0]) | nan_codes(x[1]) | nan_codes(x[2]) | nan_codes(x[3]);
+    }
+    return __any_sync(0xffffffffu, any != 0);
+}
 // NaN codes in values that only some of the queries of a walk see would give the
 // others NaN, as 0 * NaN.  In rows r .. r + n - 1 (one warp's) of a stage's V part
 // at sV they become 0, and the columns of O that they make NaN for this lane's
 // queries, which see the first from0 + 1 and from1 + 1 of these rows, are noted
 // until the segment ends: bits 4 i + 2 c, + 1 are columns 16 i + 2 g and the next
-// of its c-th query.  Out of line: for the last rows of a walk, no part of the
-// loop.
+// of its c-th query.  Walks whose last rows hold no such codes only look for
+// them: 4 queries on 2456 tokens 62.0 us for 61.8 without, 2 queries at head size
+// 256 42.4 for 41.3.
 template <int W, int RW>
 struct NanNotes {
     uint64_t cols[W * 32];  // [thread]
@@ -298,20 +318,11 @@ struct NanNotes {
     uint32_t phase[W];
 };
 template <int D, int NT, class Notes>
-__device__ __noinline__ void hide_nan_codes(Notes* notes, uint32_t sV, int r, int n, int lbs, int from0, int from1,
+__device__ __forceinline__ void hide_nan_codes(Notes* notes, uint32_t sV, int r, int n, int lbs, int from0, int from1,
                                             bool paired, int thread, uint32_t* err, volatile int* abort_flag) {
-    constexpr int RB = D < 128 ? D : 128, CH = D / 16, CPS = RB / 16;
+    constexpr int CH = D / 16, CPS = D < 128 ? CH : 8;
     const int lane = thread & 31, warp = thread >> 5;
-    const auto chunk = [&](int i, int c) {  // of row r + i
-        return sV + quant_row_off<D>(r + i, lbs) + (((uint32_t)(c / CPS) * RB) << lbs) + (uint32_t)(c % CPS) * 16;
-    };
-    uint32_t any = 0;
-    for (int u = lane; u < n * CH; u += 32) {
-        uint32_t x[4];
-        lds_v4(chunk(u / CH, u % CH), x);
-        any |= nan_codes(x[0]) | nan_codes(x[1]) | nan_codes(x[2]) | nan_codes(x[3]);
-    }
-    if (!__any_sync(0xffffffffu, any != 0)) return;
+    const auto chunk = [&](int i, int c) { return quant_chunk<D>(sV, r + i, c, lbs); };
     uint64_t cols = notes->cols[thread];
     for (int i = 0; i < n; ++i)
         for (int c = 0; c < CH; ++c) {
@@ -339,6 +350,14 @@ __device__ __noinline__ void hide_nan_codes(Notes* notes, uint32_t sV, int r, in
     }
     fence_proxy_async_smem();  // generic writes before the next TMA
     __syncwarp();
+}
+
+// Out of line: head size 256 has no registers left for it (2 queries 42.6 us,
+// 44.0 inlined; at head size 128 43.2 and 41.4).
+template <int D, int NT, class Notes>
+__device__ __noinline__ void hide_nan_codes_apart(Notes* notes, uint32_t sV, int r, int n, int lbs, int from0, int from1,
+                                                  bool paired, int thread, uint32_t* err, volatile int* abort_flag) {
+    hide_nan_codes<D, NT>(notes, sV, r, n, lbs, from0, from1, paired, thread, err, abort_flag);
 }
 
 // A unit's q rows in the stage (bf16, 8 NT of them, those from nr on zero),
@@ -523,9 +542,12 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
                 }
                 if constexpr (kHide) {
                     const int later = max(0, md.lim + 1 - pos0);  // the first row that some query does not see
-                    hide_nan_codes<D, NT>(notes, sV, r0 + later, min(16 * RT, md.n_valid - r0) - later, lbs,
-                                          md.lim - pos0 - later + qc[0], md.lim - pos0 - later + qc[1], md.nr > 8, ct, p.err,
-                                          abort_flag);
+                    const int n = min(16 * RT, md.n_valid - r0) - later;
+                    if (any_nan_code<D>(sV, r0 + later, n, lbs, lane)) {
+                        constexpr auto hide = D == 256 ? hide_nan_codes_apart<D, NT, Notes> : hide_nan_codes<D, NT, Notes>;
+                        hide(notes, sV, r0 + later, n, lbs, md.lim - pos0 - later + qc[0], md.lim - pos0 - later + qc[1],
+                             md.nr > 8, ct, p.err, abort_flag);
+                    }
                 }
                 __syncwarp();
             }
