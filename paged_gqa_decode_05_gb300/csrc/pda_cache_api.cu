@@ -180,6 +180,7 @@ bool encode_scales(const pda_dims& d, const pda_cache* c, CUtensorMap* tm) {
 // How a call's pools load: encodes the launch's maps, or returns false where
 // boxes do not fit (then rows are copied one by one).
 bool encode_boxes(const pda_dims& d, const pda_cache* c, pda::QuantParams* p) {
+    if (!pda::tensor_map_encoder()) return false;
     if (d.block_size < 4) return false;  // four blocks' scales must fill the 128 bytes a copy starts on
     if (!encode_scales(d, c, &p->tm_k1)) return false;
     p->joined = pda::quant_boxes(d.head_dim, d.block_size, true) && encode_joined(d, c, &p->tm_k);
