@@ -26,7 +26,7 @@
 // reference.  For bf16 outputs p' enters the product as fp16, off by 2^-11 of it
 // at most: an eighth of the output's own half step.  For fp32 outputs (FINE) it
 // enters as two fp16 parts, off by 2^-22, at twice the products with V (32
-// sequences of 4096 tokens: 53.3 us for 52.3, 4 queries on 2456: 67.9 for 63.9).
+// sequences of 4096 tokens: 54.2 us for 53.1, 4 queries on 2456: 66.3 for 63.7).
 // References sit kRefBias below the maximum they were taken at and move when a
 // maximum passes them by more than kRefBias + kLazyLog2, so p' < 2^14 and what
 // fp16 flushes is 2^-31 of the largest weight.

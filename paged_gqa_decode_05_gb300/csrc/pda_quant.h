@@ -18,7 +18,8 @@ namespace pda {
 // with a ring each 51 to 57 (and 107 to 120 where the lengths are ragged: 107
 // here), two producer warps 53.9.  16 q rows, 4 queries on 2456 tokens: both
 // tiles in one warp's registers, which shares the conversions of V, 67.6 us;
-// two walks over the cache 65.4; this form 61.7 (int8 64.0, 72.4 and 66.5).
+// two walks over the cache 65.4; this form 61.7 (int8 64.0, 72.4 and 66.5); it
+// takes 62.0 (64.3) since its sums hold for every V scale.
 PDA_HD constexpr int quant_warps(int D, int n_tiles) { return D == 256 || n_tiles == 2 ? 8 : 4; }
 PDA_HD constexpr int quant_row_tiles(int D, int n_tiles) { return D == 256 ? 1 : 2; }
 PDA_HD constexpr int quant_stage_rows(int D, int n_tiles) {
