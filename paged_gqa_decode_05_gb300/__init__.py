@@ -420,7 +420,9 @@ class Context:
         if stream is None:
             return fn(shape, dtype=dtype, device=self.device)
         if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+            # (a handle of 0 is the default stream, which ExternalStream does not take)
+            stream = torch.cuda.ExternalStream(int(stream), device=self.device) if int(stream) else \
+                torch.cuda.default_stream(self.device)
         with torch.cuda.stream(stream):
             return fn(shape, dtype=dtype, device=self.device)
 

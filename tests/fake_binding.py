@@ -57,10 +57,14 @@ def ctx(monkeypatch):
     def stream_of(handle, device=None):
         return types.SimpleNamespace(cuda_stream=int(handle))
 
+    def external(handle, device=None):  # torch takes a handle of 0 for none and gives a stream of its pool
+        return stream_of(handle or 99)
+
     fake = types.SimpleNamespace(
         bfloat16=torch.bfloat16, float32=torch.float32, float8_e4m3fn=torch.float8_e4m3fn, int8=torch.int8,
         int32=torch.int32, Size=torch.Size, empty=make, zeros=make, empty_like=like, zeros_like=like,
-        cuda=types.SimpleNamespace(stream=on, ExternalStream=stream_of, current_stream=lambda: stream_of(0)),
+        cuda=types.SimpleNamespace(stream=on, ExternalStream=external, default_stream=lambda device=None: stream_of(0),
+                                   current_stream=lambda: stream_of(current[0])),
         _C=types.SimpleNamespace(_cuda_getCurrentRawStream=lambda index: current[0]))
     monkeypatch.setattr(pda, "_TORCH", fake)
 
@@ -77,7 +81,7 @@ def ctx(monkeypatch):
     c = object.__new__(pda.Context)
     c.dims = pda.Dims(16, HQ, HKV, D, BS, 4)
     c.device, c._index, c._ctx, c.G = torch.device("cuda", 0), 0, 1, HQ // HKV
-    c.made, c.calls, c.stream_of = made, calls, stream_of
+    c.made, c.calls, c.stream_of, c.current = made, calls, stream_of, current
     yield c
     c._ctx = None
 

@@ -27,7 +27,8 @@ CALLS = {
 
 @pytest.mark.parametrize("name", CALLS)
 def test_new_outputs_are_made_on_the_calls_stream(ctx, name):
-    for stream, where in ((None, 0), (CALL, CALL), (ctx.stream_of(CALL), CALL)):
+    for stream, where in ((None, 5), (CALL, CALL), (ctx.stream_of(CALL), CALL), (0, 0), (ctx.stream_of(0), 0)):
         del ctx.made[:]
+        ctx.current[0] = 5
         CALLS[name](ctx, stream)
         assert ctx.made and all(t.made_on == where for t in ctx.made), (name, [t.made_on for t in ctx.made])

@@ -59,6 +59,23 @@ def test_calls_on_another_stream_make_their_outputs_there(handle):
     assert ctx.read_device_errors() == 0
 
 
+def test_calls_on_the_default_streams_handle():
+    """stream=0 is the default stream, also for what the call makes itself, while another stream is current."""
+    g = gen(1)
+    ctx = ctx_of(4, 2, 64, 16)
+    kp, vp, sc = (t.cuda() for t in ref.random_cache(g, 4, 16, 2, 64, torch.int8))
+    table, lens = i32([[0, 1], [2, 3]]), i32([20, 9])
+    want = ctx.read_cache(kp, vp, table, lens, scales=sc)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        torch.cuda._sleep(20_000_000)
+        got = ctx.read_cache(kp, vp, table, lens, scales=sc, stream=0)
+    torch.cuda.default_stream().synchronize()
+    for _ in range(2):
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+        torch.cuda.synchronize()
+
+
 # ------------------------------------------------------------------ NaN that a query does not see
 
 SHAPES = [(4, 2, 64, 16), (8, 2, 128, 16), (8, 1, 128, 4), (4, 1, 256, 32), (16, 2, 64, 1), (8, 1, 128, 64)]
