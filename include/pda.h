@@ -640,6 +640,9 @@ pda_status pda_read_cache(pda_ctx* ctx, const pda_cache* cache, const int32_t* b
  *   values   codes are multiplied as fp16 (exact) by the weights: in one fp16
  *            part (2^-11) for bf16 outputs, in two (2^-22) for fp32 outputs.
  * Products and the sum of the unrounded weights are fp32.
+ * A NaN in a cached row (an 8-bit row's scale or code) reaches the queries that
+ * see its token and no others.  PDA_CACHE_BF16 is as pda_decode_multi: there a
+ * NaN or infinity in a value reaches every query that shares the walk.
  */
 pda_status pda_decode_cache(pda_ctx* ctx, const pda_bf16* q, const pda_cache* cache,
                             const int32_t* block_table, int32_t max_blocks,
