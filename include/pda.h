@@ -649,6 +649,117 @@ pda_status pda_decode_cache(pda_ctx* ctx, const pda_bf16* q, const pda_cache* ca
                             const int32_t* seq_lens, int32_t batch, int32_t q_len, float scale,
                             void* out, int32_t out_f32, pda_stream stream);
 
+/* ---------------------------------------------------------------------------
+ * Long and shared contexts: scores that are capped or biased, the attention
+ * weight that every cached token gets, eviction by it, and batches whose
+ * sequences begin with the same blocks.
+ */
+
+/*
+ * What happens to a score s = scale * q . k before the softmax:
+ *   softcap  > 0: s = softcap * tanh(s / softcap); 0 leaves s as it is.
+ *            From 1e-3 to 1e6.
+ *   slopes   [Hq] fp32 (device) or NULL: s += slopes[h] * (t - i), where t is
+ *            the key's token and i the query's own (seq_len - q_len + its
+ *            index), so t - i <= 0.  After the cap.
+ * Both are taken in fp32; tanh is off by a few 2^-24 of the cap.
+ */
+typedef struct pda_scoring {
+    float softcap;
+    int32_t reserved; /* 0 */
+    const float* slopes;
+} pda_scoring;
+
+/*
+ * Decode with such scores, over a cache of any format: the last q_len tokens
+ * of each sequence attend causally, as in pda_decode_cache.
+ *   scoring   or NULL: scores as they are.
+ *   out       bf16, or fp32 when out_f32 (every format and q_len).
+ * With weights_out it also sums the attention weight that each cached token
+ * got, over the call's queries and the G q heads of the token's kv head:
+ *   weights_out[block, g, slot] = old + sum p,   p = softmax(s) of this call,
+ *   weights_in,
+ *   weights_out  [num_blocks, Hkv, block_size] fp32, placed as the tokens are;
+ *             weights_in may be weights_out (sums in place), or NULL (old = 0).
+ *   old       weights_in's, except that the last q_len tokens, the queries' own,
+ *             start from 0: what a reused slot held does not count.  Entries
+ *             of no token of the batch are left as they were.
+ *   scratch   16-byte aligned, pda_decode_scored_scratch() bytes for the call's
+ *             batch, q_len and max_blocks: the scores, 4 bytes for each token
+ *             and q head of a table of that width.  Not needed without weights.
+ * No two sequences of the call may share a block whose weights they sum.
+ * Every sum is taken in one order: a call's weights do not vary from run to run.
+ * batch * q_len <= max_seqs.  Other arguments as pda_decode_cache; scores are as
+ * exact as there (bf16 caches: products and sums in fp32, weights in two bf16
+ * parts).
+ */
+pda_status pda_decode_scored_scratch(const pda_ctx* ctx, int32_t batch, int32_t q_len, int32_t max_blocks,
+                                     int64_t* bytes);
+pda_status pda_decode_scored(pda_ctx* ctx, const pda_bf16* q, const pda_cache* cache,
+                             const int32_t* block_table, int32_t max_blocks, const int32_t* seq_lens,
+                             int32_t batch, int32_t q_len, float scale, const pda_scoring* scoring,
+                             const float* weights_in, float* weights_out, void* scratch, int64_t scratch_bytes,
+                             void* out, int32_t out_f32, pda_stream stream);
+
+/*
+ * Decode of a batch whose sequences begin with the same blocks: what
+ * pda_decode_scored computes without weights, each shared prefix read once for
+ * all the queries of its group.
+ *   shared_blocks  [groups] int32 (device): the first shared_blocks[p] entries
+ *                  of the table rows of group p are taken to be the same; those
+ *                  of its first sequence are read.  Other entries, and seq_lens,
+ *                  are the whole sequences', as everywhere.  Outside [0,
+ *                  max_blocks] it is clamped and raises PDA_DEVERR_BAD_LENGTH.
+ *   starts         [groups + 1] int32 (device), not decreasing: group p is the
+ *                  sequences starts[p] .. starts[p+1] - 1; sequences of no group
+ *                  share nothing.  NULL: batch / groups (exact) each.  Values
+ *                  outside [0, batch], or below the one before, are clamped with
+ *                  the same flag.
+ *   groups         1 .. 1024.
+ *   scratch        16-byte aligned, pda_decode_shared_scratch() bytes.
+ * A sequence may end inside the prefix, or be empty.  A NaN or an infinity in a
+ * value of the prefix reaches every sequence of its group.  V scales of an 8-bit
+ * prefix enter the weights in fp32 times 2^-40; what falls below 2^-126 then,
+ * values below 2^-86, counts as 0.
+ */
+pda_status pda_decode_shared_scratch(const pda_ctx* ctx, int32_t batch, int32_t q_len, int32_t groups,
+                                     int64_t* bytes);
+pda_status pda_decode_shared(pda_ctx* ctx, const pda_bf16* q, const pda_cache* cache,
+                             const int32_t* block_table, int32_t max_blocks, const int32_t* seq_lens,
+                             int32_t batch, int32_t q_len, const int32_t* shared_blocks, const int32_t* starts,
+                             int32_t groups, float scale, const pda_scoring* scoring, void* scratch,
+                             int64_t scratch_bytes, void* out, int32_t out_f32, pda_stream stream);
+
+/*
+ * Cuts sequences down to a budget of tokens, by their sums of attention weights
+ * (pda_decode_scored), for each kv head on its own.  A sequence of more than
+ * `keep` tokens keeps its first `first`, its last `recent` and, of those
+ * between, the ones with the largest sums, keep in all; of equal sums the
+ * lowest index, and NaN counts as the largest.  The others keep every token.
+ * Kept tokens stay in order and become tokens 0 .. new_len - 1 of the sequence,
+ * with their keys, values, scales and sums.
+ *   cache         any format; its pools are written.
+ *   weights       [num_blocks, Hkv, block_size] fp32.
+ *   keep          >= 1; first, recent >= 0 and first + recent <= keep.
+ *   out_table     [batch, out_blocks] int32 (device): where the kept tokens go,
+ *                 blocks that are no sequence's of the call and named once; it
+ *                 must hold min(keep, max_blocks * block_size) tokens.  The
+ *                 sequences' own blocks are then left as they were.  NULL (or
+ *                 block_table): in place, to the front of the sequence's own
+ *                 blocks, which no other sequence may share; what lies behind
+ *                 new_len is left as it was.
+ *   kept          [batch, Hkv, keep] int32 out (device): the former index of
+ *                 each token, -1 from new_len on.
+ *   new_lens      [batch] int32 out (device), min(seq_len, keep); not seq_lens.
+ * The token of a bad block id counts as zeros of sum 0.  Rotary positions are in
+ * the keys and stay; a distance bias (pda_scoring) does not fit a cache whose
+ * tokens have moved up.
+ */
+pda_status pda_evict(pda_ctx* ctx, const pda_cache* cache, float* weights, const int32_t* block_table,
+                     int32_t max_blocks, const int32_t* seq_lens, int32_t batch, int32_t keep, int32_t first,
+                     int32_t recent, const int32_t* out_table, int32_t out_blocks, int32_t* kept,
+                     int32_t* new_lens, pda_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

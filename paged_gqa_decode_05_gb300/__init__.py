@@ -82,6 +82,10 @@ class _Heads(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("tok_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
+class _Scoring(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("reserved", ctypes.c_int32), ("slopes", ctypes.c_void_p)]
+
+
 class _Prep(ctypes.Structure):
     _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("weights_f32", ctypes.c_int32),
                 ("eps", ctypes.c_float), ("cos_sin", ctypes.c_void_p), ("max_positions", ctypes.c_int32),
@@ -131,6 +135,11 @@ def lib() -> ctypes.CDLL:
         "pda_append": (I32, [P, P, P, P, P, I32, P, I32, P, P, I64, P, P, P, P]),
         "pda_read_cache": (I32, [P, P, P, I32, P, I32, P, I64, P, P, I32, P]),
         "pda_decode_cache": (I32, [P, P, P, P, I32, P, I32, I32, F, P, I32, P]),
+        "pda_decode_scored_scratch": (I32, [P, I32, I32, I32, ctypes.POINTER(I64)]),
+        "pda_decode_scored": (I32, [P, P, P, P, I32, P, I32, I32, F, P, P, P, P, I64, P, I32, P]),
+        "pda_decode_shared_scratch": (I32, [P, I32, I32, I32, ctypes.POINTER(I64)]),
+        "pda_decode_shared": (I32, [P, P, P, P, I32, P, I32, I32, P, P, I32, F, P, P, I64, P, I32, P]),
+        "pda_evict": (I32, [P, P, P, P, I32, P, I32, I32, I32, I32, P, I32, P, P, P]),
         "pda_debug_gather": (I32, [P, P, P, I64, I64, I64, I64, P, I32, P, I32, P, P, P]),
         "pda_read_device_errors": (I32, [P, ctypes.POINTER(ctypes.c_uint32), I32, P]),
         "pda_set_timing_events": (I32, [P, P, P, P]),
@@ -717,6 +726,182 @@ class Context:
         if status:
             _check(status)
         return k_out, v_out
+
+    # -- long and shared contexts
+    def _scoring(self, softcap, alibi_slopes) -> Optional[_Scoring]:
+        if not softcap and alibi_slopes is None:
+            return None
+        if alibi_slopes is not None:
+            hq = self.dims.num_q_heads
+            if alibi_slopes.dtype != _torch().float32 or tuple(alibi_slopes.shape) != (hq,) or \
+                    not alibi_slopes.is_contiguous():
+                raise ValueError(f"alibi_slopes must be a contiguous float32 [{hq}] tensor")
+            self._here(alibi_slopes, "alibi_slopes")
+        return _Scoring(float(softcap or 0.0), 0, _ptr(alibi_slopes))
+
+    def _weights(self, t, name, num_blocks):
+        shape = (num_blocks, self.dims.num_kv_heads, self.dims.block_size)
+        if t.dtype != _torch().float32 or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous float32 tensor of shape {shape}")
+        return self._here(t, name)
+
+    def _scored_args(self, q, k_pool, v_pool, block_table, seq_lens, out, scales, out_dtype, strides, num_blocks, stream):
+        """What the scored calls check alike: (cache, table width, sequences, queries of each, out)."""
+        torch = _torch()
+        d = self.dims
+        width, B = self._sequences(block_table, seq_lens, None)
+        if q.dim() not in (3, 4) or q.shape[0] != B or tuple(q.shape[-2:]) != (d.num_q_heads, d.head_dim):
+            raise ValueError("q must be [B, Hq, D] or [B, q_len, Hq, D]")
+        self._here(self._bf16(q, "q"), "q")
+        cache = self._cache(k_pool, v_pool, scales, strides, num_blocks)
+        if out_dtype not in (None, torch.bfloat16, torch.float32):
+            raise ValueError("out_dtype must be bfloat16 or float32")
+        if out is None:
+            out = self._make(torch.empty, q.shape, out_dtype or torch.bfloat16, stream)
+        if out.dtype not in (torch.bfloat16, torch.float32) or (out_dtype is not None and out.dtype != out_dtype) or \
+                out.shape != q.shape or not out.is_contiguous():
+            raise ValueError(f"out must be a contiguous {out_dtype or 'bfloat16 or float32'} tensor of shape {tuple(q.shape)}")
+        self._here(out, "out")
+        return cache, width, B, int(q.shape[1]) if q.dim() == 4 else 1, out
+
+    def _scratch(self, scratch, fn, args, stream):
+        """`scratch`, a uint8 tensor with room for what fn tells, or a new one."""
+        torch = _torch()
+        need = ctypes.c_int64()
+        if not self._ctx:
+            raise PdaError(ERR_INVALID_ARG, "the context is closed")
+        _check(fn(self._ctx, *args, ctypes.byref(need)))
+        if scratch is None:
+            return self._make(torch.empty, (need.value,), torch.uint8, stream)
+        if scratch.dtype != torch.uint8 or not scratch.is_contiguous() or scratch.numel() < need.value:
+            raise ValueError(f"scratch must be a contiguous uint8 tensor of {need.value} bytes")
+        return self._here(scratch, "scratch")
+
+    def new_weights(self, num_blocks: int):
+        """Zeroed sums of attention weights beside a cache of num_blocks blocks: float32
+        [num_blocks, Hkv, block_size], for decode_scored and evict."""
+        d = self.dims
+        return _torch().zeros((int(num_blocks), d.num_kv_heads, d.block_size), device=self.device)
+
+    def decode_scored(self, q, k_pool, v_pool, block_table, seq_lens, *, softcap: Optional[float] = None,
+                      alibi_slopes=None, weights=None, weights_from=None, scale: Optional[float] = None, out=None,
+                      out_dtype=None, scales=None, strides: Optional[Sequence[int]] = None,
+                      num_blocks: Optional[int] = None, scratch=None, stream=None):
+        """Decode of q [B, Hq, D], or causally of [B, q_len, Hq, D], over a cache of any format
+        (8-bit pools with their ``scales``), with scores softcap * tanh(s / softcap) where a
+        softcap is given, plus alibi_slopes[h] ([Hq] float32) times the key's token index less
+        the query's.
+
+        With ``weights`` (new_weights) the attention weight that each cached token got, summed
+        over the queries and the q heads of its kv head, is added to its sum there; the sums
+        before are weights_from's where given.  Those of the queries' own tokens, the last
+        q_len of each sequence, start from 0 (pda_decode_scored)."""
+        return self.bind_decode_scored(q, k_pool, v_pool, block_table, seq_lens, out, softcap=softcap,
+                                       alibi_slopes=alibi_slopes, weights=weights, weights_from=weights_from, scale=scale,
+                                       out_dtype=out_dtype, scales=scales, strides=strides, num_blocks=num_blocks,
+                                       scratch=scratch, stream=stream)()
+
+    def bind_decode_scored(self, q, k_pool, v_pool, block_table, seq_lens, out=None, *, softcap: Optional[float] = None,
+                           alibi_slopes=None, weights=None, weights_from=None, scale: Optional[float] = None,
+                           out_dtype=None, scales=None, strides: Optional[Sequence[int]] = None,
+                           num_blocks: Optional[int] = None, scratch=None, stream=None):
+        """decode_scored with its tensors validated once: a callable as bind_decode's."""
+        cache, width, B, q_len, out = self._scored_args(q, k_pool, v_pool, block_table, seq_lens, out, scales, out_dtype,
+                                                        strides, num_blocks, stream)
+        scoring = self._scoring(softcap, alibi_slopes)
+        if weights is None:
+            if weights_from is not None:
+                raise ValueError("weights_from without weights")
+            scratch = None
+        else:
+            self._weights(weights, "weights", cache.num_blocks)
+            weights_from = weights if weights_from is None else self._weights(weights_from, "weights_from", cache.num_blocks)
+            scratch = self._scratch(scratch, lib().pda_decode_scored_scratch, (B, q_len, width), stream)
+        args = (_ptr(q), ctypes.addressof(cache), _ptr(block_table), width, _ptr(seq_lens), B, q_len, self._scale(scale),
+                None if scoring is None else ctypes.addressof(scoring), _ptr(weights_from), _ptr(weights), _ptr(scratch),
+                0 if scratch is None else scratch.numel(), _ptr(out), int(out.dtype == _torch().float32),
+                self._stream_of(stream))
+        return _Bound(self, lib().pda_decode_scored, args,
+                      (cache, scoring, q, k_pool, v_pool, scales, block_table, seq_lens, alibi_slopes, weights, weights_from,
+                       scratch), out)
+
+    def decode_shared(self, q, k_pool, v_pool, block_table, seq_lens, shared_blocks, *, starts=None,
+                      softcap: Optional[float] = None, alibi_slopes=None, scale: Optional[float] = None, out=None,
+                      out_dtype=None, scales=None, strides: Optional[Sequence[int]] = None,
+                      num_blocks: Optional[int] = None, scratch=None, stream=None):
+        """decode_scored of a batch whose sequences begin with the same blocks, each shared prefix
+        read once: the first shared_blocks[p] ([groups] int32) entries of the table rows of
+        sequences starts[p] .. starts[p+1] - 1 ([groups + 1] int32; None: B / groups each) are the
+        same (pda_decode_shared)."""
+        return self.bind_decode_shared(q, k_pool, v_pool, block_table, seq_lens, shared_blocks, out, starts=starts,
+                                       softcap=softcap, alibi_slopes=alibi_slopes, scale=scale, out_dtype=out_dtype,
+                                       scales=scales, strides=strides, num_blocks=num_blocks, scratch=scratch,
+                                       stream=stream)()
+
+    def bind_decode_shared(self, q, k_pool, v_pool, block_table, seq_lens, shared_blocks, out=None, *, starts=None,
+                           softcap: Optional[float] = None, alibi_slopes=None, scale: Optional[float] = None,
+                           out_dtype=None, scales=None, strides: Optional[Sequence[int]] = None,
+                           num_blocks: Optional[int] = None, scratch=None, stream=None):
+        """decode_shared with its tensors validated once: a callable as bind_decode's."""
+        cache, width, B, q_len, out = self._scored_args(q, k_pool, v_pool, block_table, seq_lens, out, scales, out_dtype,
+                                                        strides, num_blocks, stream)
+        scoring = self._scoring(softcap, alibi_slopes)
+        self._here(self._i32(shared_blocks, "shared_blocks", 1), "shared_blocks")
+        groups = int(shared_blocks.shape[0])
+        if starts is not None:
+            self._here(self._i32(starts, "starts", 1), "starts")
+            if starts.shape[0] != groups + 1:
+                raise ValueError("starts must hold one entry per group and the end")
+        scratch = self._scratch(scratch, lib().pda_decode_shared_scratch, (B, q_len, groups), stream)
+        args = (_ptr(q), ctypes.addressof(cache), _ptr(block_table), width, _ptr(seq_lens), B, q_len, _ptr(shared_blocks),
+                _ptr(starts), groups, self._scale(scale), None if scoring is None else ctypes.addressof(scoring),
+                _ptr(scratch), scratch.numel(), _ptr(out), int(out.dtype == _torch().float32), self._stream_of(stream))
+        return _Bound(self, lib().pda_decode_shared, args,
+                      (cache, scoring, q, k_pool, v_pool, scales, block_table, seq_lens, shared_blocks, starts, alibi_slopes,
+                       scratch), out)
+
+    def evict(self, k_pool, v_pool, weights, block_table, seq_lens, keep: int, *, first: int = 0, recent: int = 0,
+              scales=None, out_table=None, kept=None, new_lens=None, strides: Optional[Sequence[int]] = None,
+              num_blocks: Optional[int] = None, stream=None):
+        """Cuts every sequence of more than `keep` tokens down to its first `first`, its last
+        `recent` and, of those between, the ones with the largest sums in `weights`
+        (decode_scored), keep in all, per kv head.  Kept tokens move, in order, to the front of
+        their blocks, or to those of out_table [B, blocks] int32 where given, with their keys,
+        values, scales and sums.  Returns (new_lens [B], kept [B, Hkv, keep]): the lengths, and
+        the former index of every token, -1 behind them (pda_evict)."""
+        return self.bind_evict(k_pool, v_pool, weights, block_table, seq_lens, keep, first=first, recent=recent,
+                               scales=scales, out_table=out_table, kept=kept, new_lens=new_lens, strides=strides,
+                               num_blocks=num_blocks, stream=stream)()
+
+    def bind_evict(self, k_pool, v_pool, weights, block_table, seq_lens, keep: int, *, first: int = 0, recent: int = 0,
+                   scales=None, out_table=None, kept=None, new_lens=None, strides: Optional[Sequence[int]] = None,
+                   num_blocks: Optional[int] = None, stream=None):
+        """evict with its tensors validated once: a callable as bind_decode's."""
+        torch = _torch()
+        width, B = self._sequences(block_table, seq_lens, None)
+        cache = self._cache(k_pool, v_pool, scales, strides, num_blocks)
+        self._weights(weights, "weights", cache.num_blocks)
+        keep, first, recent = int(keep), int(first), int(recent)
+        if keep < 1 or min(first, recent) < 0 or first + recent > keep:
+            raise ValueError("keep must be at least 1 and hold first + recent tokens")
+        out_width = 0
+        if out_table is not None:
+            self._here(self._i32(out_table, "out_table", 2), "out_table")
+            rows, out_width = out_table.shape
+            if rows != B:
+                raise ValueError("out_table must have one row per sequence")
+        made = []
+        for t, name, shape in ((kept, "kept", (B, self.dims.num_kv_heads, keep)), (new_lens, "new_lens", (B,))):
+            if t is None:
+                t = self._make(torch.empty, shape, torch.int32, stream)
+            elif tuple(self._i32(t, name, len(shape)).shape) != shape:
+                raise ValueError(f"{name} must be an int32 tensor of shape {shape}")
+            made.append(self._here(t, name))
+        kept, new_lens = made
+        args = (ctypes.addressof(cache), _ptr(weights), _ptr(block_table), width, _ptr(seq_lens), B, keep, first, recent,
+                _ptr(out_table), out_width, _ptr(kept), _ptr(new_lens), self._stream_of(stream))
+        return _Bound(self, lib().pda_evict, args,
+                      (cache, k_pool, v_pool, scales, weights, block_table, seq_lens, out_table), (new_lens, kept))
 
     # -- tiled lifecycle
     def set_tile_overlap(self, enable: bool) -> None:

@@ -181,6 +181,26 @@ void set_pool_params(pda::SplitParams& p, const pda_dims& d, const PoolArgs& a, 
     p.row_kvh = a.kvh / d.head_dim;
 }
 
+// The context's tensor maps of the last pool, encoded anew for another one.
+pda_status pool_maps(pda_ctx* ctx, const PoolArgs& a) {
+    const pda_dims& d = ctx->dims;
+    const pda_pool_key key = {a.k, a.v, a.num_blocks, a.blk, a.tok, a.kvh};
+    const pda_pool_key& mk = ctx->maps_key;
+    if (ctx->maps_valid && mk.k == key.k && mk.v == key.v && mk.num_blocks == key.num_blocks && mk.blk == key.blk &&
+        mk.tok == key.tok && mk.kvh == key.kvh)
+        return PDA_OK;
+    ctx->maps_valid = false;
+    pda_status st = encode_loader(d, a, &ctx->map_k, &ctx->map_v, &ctx->maps_row_mode);
+    if (st == PDA_OK && ctx->maps_row_mode == 0 && d.head_dim == 128 && ctx->tc_ctas > 0) {
+        st = encode_pool(d, a.k, a, &ctx->map_k1, true);
+        if (st == PDA_OK) st = encode_pool(d, a.v, a, &ctx->map_v1, true);
+    }
+    if (st != PDA_OK) return st;
+    ctx->maps_key = key;
+    ctx->maps_valid = true;
+    return PDA_OK;
+}
+
 // Dynamic shared memory allowed for a split-kernel shape and mode: what a
 // launch of a full batch (max_launch_rows(mode) sequences) uses, so every
 // caller sets the same value and none lowers it below what another launches
@@ -300,20 +320,7 @@ pda_status run(pda_ctx* ctx, const RunArgs& r) {
 
     pda::SplitParams p;
     std::memset(&p, 0, sizeof p);
-    const pda_pool_key key = {r.pool.k, r.pool.v, r.pool.num_blocks, r.pool.blk, r.pool.tok, r.pool.kvh};
-    const pda_pool_key& mk = ctx->maps_key;
-    if (!(ctx->maps_valid && mk.k == key.k && mk.v == key.v && mk.num_blocks == key.num_blocks &&
-          mk.blk == key.blk && mk.tok == key.tok && mk.kvh == key.kvh)) {
-        ctx->maps_valid = false;
-        st = encode_loader(d, r.pool, &ctx->map_k, &ctx->map_v, &ctx->maps_row_mode);
-        if (st == PDA_OK && ctx->maps_row_mode == 0 && d.head_dim == 128 && ctx->tc_ctas > 0) {
-            st = encode_pool(d, r.pool.k, r.pool, &ctx->map_k1, true);
-            if (st == PDA_OK) st = encode_pool(d, r.pool.v, r.pool, &ctx->map_v1, true);
-        }
-        if (st != PDA_OK) return st;
-        ctx->maps_key = key;
-        ctx->maps_valid = true;
-    }
+    if ((st = pool_maps(ctx, r.pool)) != PDA_OK) return st;
     p.tm_k = ctx->map_k;
     p.tm_v = ctx->map_v;
     p.tm_k1 = ctx->map_k1;
@@ -536,7 +543,8 @@ PDA_EXPORT pda_status pda_create(const pda_dims* dims, pda_ctx** out_ctx) {
         ctx->tc_ctas = n * ctx->num_sms;
         ctx->tc_stages = pda::split_stages(D, ctx->stage_rows, pda::kMultiTc);
     }
-    if ((st = pda::quant_setup(ctx, (int)prop.sharedMemPerBlockOptin)) != PDA_OK) {
+    if ((st = pda::quant_setup(ctx, (int)prop.sharedMemPerBlockOptin)) != PDA_OK ||
+        (st = pda::scored_setup(ctx, (int)prop.sharedMemPerBlockOptin)) != PDA_OK) {
         delete ctx;
         return st;
     }
@@ -896,6 +904,18 @@ PDA_EXPORT pda_status pda_decode_multi(pda_ctx* ctx, const pda_bf16* q, const pd
                  block_table, max_blocks, seq_lens, 0, nullptr, batch, scale, out, nullptr,
                  nullptr, nullptr, (cudaStream_t)stream, false, q_len};
     return run(ctx, r);
+}
+
+pda_status pda::set_bf16_pools(pda_ctx* ctx, const pda_cache* c, SplitParams* p) {
+    const PoolArgs a = {static_cast<const pda_bf16*>(c->k_pool), static_cast<const pda_bf16*>(c->v_pool), c->num_blocks,
+                        c->blk_stride, c->tok_stride, c->kvh_stride};
+    pda_status st = check_pool(a);
+    if (st == PDA_OK) st = pool_maps(ctx, a);
+    if (st != PDA_OK) return st;
+    p->tm_k = ctx->map_k;
+    p->tm_v = ctx->map_v;
+    set_pool_params(*p, ctx->dims, a, ctx->maps_row_mode);
+    return PDA_OK;
 }
 
 pda_status pda::decode_bf16_multi(pda_ctx* ctx, const pda_bf16* q, const pda_cache* c, const int32_t* block_table,

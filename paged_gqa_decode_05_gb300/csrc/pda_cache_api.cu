@@ -10,23 +10,13 @@
 #include "pda_ctx.h"
 #include "pda_quant.h"
 
+using pda::DeviceGuard;
 using pda::aligned;
+using pda::check_cache;
 using pda::cuda_fail;
 using pda::fail;
 
 namespace {
-
-// Makes the context's device current for a call.
-struct DeviceGuard {
-    int prev = -1;
-    explicit DeviceGuard(int dev) {
-        int now = -1;
-        if (cudaGetDevice(&now) == cudaSuccess && now != dev && cudaSetDevice(dev) == cudaSuccess) prev = now;
-    }
-    ~DeviceGuard() {
-        if (prev >= 0) cudaSetDevice(prev);
-    }
-};
 
 pda_status check_heads(const pda_heads* h, const char* name) {
     if (!h->data || !aligned(h->data, 8))
@@ -54,7 +44,9 @@ pda_status check_prep(const pda_prep* p, int D) {
     return PDA_OK;
 }
 
-pda_status check_cache(const pda_cache* c) {
+}  // namespace
+
+pda_status pda::check_cache(const pda_cache* c) {
     if (!c) return fail(PDA_ERR_INVALID_ARG, "cache is NULL");
     if (c->format != PDA_CACHE_BF16 && c->format != PDA_CACHE_E4M3 && c->format != PDA_CACHE_INT8)
         return fail(PDA_ERR_INVALID_ARG, "unknown cache format %d", c->format);
@@ -72,6 +64,8 @@ pda_status check_cache(const pda_cache* c) {
         return fail(PDA_ERR_INVALID_ARG, "scales must be non-NULL and 16-byte aligned for an 8-bit cache");
     return PDA_OK;
 }
+
+namespace {
 
 pda_status check_sequences(const pda_ctx* ctx, const int32_t* table, int32_t max_blocks, const int32_t* lens,
                            int32_t batch, const int32_t* starts, int64_t rows) {
@@ -207,16 +201,7 @@ pda_status run_quant(pda_ctx* ctx, const pda_bf16* q, const pda_cache* c, const 
     if (Qr > grid) return fail(PDA_ERR_INVALID_ARG, "q_len %d: more launch rows per sequence than CTAs (%d)", q_len, grid);
     p.unit_cost = pda::quant_unit_cost(D, tiles, bs);
     if ((st = pda::check_plan_size((int64_t)batch * q_len, max_blocks, p.unit_cost)) != PDA_OK) return st;
-    p.row_gather = encode_boxes(d, c, &p) ? 0 : 2;
-    p.v_first = p.joined && c->v_pool < c->k_pool;
-    p.box_head = D == 256 ? 2 : 1;
-    p.num_blocks = c->num_blocks;
-    p.k_base = static_cast<const uint16_t*>(c->k_pool);
-    p.v_base = static_cast<const uint16_t*>(c->v_pool);
-    p.blk_s = c->blk_stride;
-    p.tok_s = c->tok_stride;
-    p.kvh_s = c->kvh_stride;
-    p.scales = c->scales;
+    pda::set_quant_pools(ctx, c, &p);
     p.part_o = ctx->part_o;
     p.part_ml = ctx->part_ml;
     p.unit_sync = ctx->unit_sync;
@@ -262,6 +247,19 @@ pda_status run_quant(pda_ctx* ctx, const pda_bf16* q, const pda_cache* c, const 
 }
 
 }  // namespace
+
+void pda::set_quant_pools(const pda_ctx* ctx, const pda_cache* c, QuantParams* p) {
+    p->row_gather = encode_boxes(ctx->dims, c, p) ? 0 : 2;
+    p->v_first = p->joined && c->v_pool < c->k_pool;
+    p->box_head = ctx->dims.head_dim == 256 ? 2 : 1;
+    p->num_blocks = c->num_blocks;
+    p->k_base = static_cast<const uint16_t*>(c->k_pool);
+    p->v_base = static_cast<const uint16_t*>(c->v_pool);
+    p->blk_s = c->blk_stride;
+    p->tok_s = c->tok_stride;
+    p->kvh_s = c->kvh_stride;
+    p->scales = c->scales;
+}
 
 pda_status pda::quant_setup(pda_ctx* ctx, int optin) {
     const int D = ctx->dims.head_dim;

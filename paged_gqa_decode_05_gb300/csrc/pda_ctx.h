@@ -11,6 +11,8 @@
 
 namespace pda {
 
+struct QuantParams;
+
 // Sets the calling thread's pda_last_error() and returns st.
 pda_status fail(pda_status st, const char* fmt, ...);
 pda_status cuda_fail(cudaError_t e, const char* what);
@@ -75,11 +77,31 @@ struct pda_ctx {
     // Decode over 8-bit caches: grids with up to 8 and 16 packed q rows per
     // walk (0: not on this shape).
     int quant_ctas[2] = {0, 0};
+    // Scored decode: grids by cache format (bf16; 8-bit).
+    int scored_ctas[2] = {0, 0};
 };
 
 namespace pda {
 // Launch attributes and grids of the 8-bit kernels of a context's shape.
 pda_status quant_setup(pda_ctx* ctx, int smem_optin);
+pda_status scored_setup(pda_ctx* ctx, int smem_optin);
+pda_status check_cache(const pda_cache* c);
+// The pool fields and tensor maps of a launch over a bf16 or an 8-bit cache.
+pda_status set_bf16_pools(pda_ctx* ctx, const pda_cache* c, SplitParams* p);
+void set_quant_pools(const pda_ctx* ctx, const pda_cache* c, QuantParams* p);
+
+// Makes the context's device current for a call.
+struct DeviceGuard {
+    int prev = -1;
+    explicit DeviceGuard(int dev) {
+        int now = -1;
+        if (cudaGetDevice(&now) == cudaSuccess && now != dev && cudaSetDevice(dev) == cudaSuccess) prev = now;
+    }
+    ~DeviceGuard() {
+        if (prev >= 0) cudaSetDevice(prev);
+    }
+};
+
 // Causal multi-query decode over a bf16 cache of any stride triple.
 pda_status decode_bf16_multi(pda_ctx* ctx, const pda_bf16* q, const pda_cache* cache, const int32_t* block_table,
                              int32_t max_blocks, const int32_t* seq_lens, int32_t batch, int32_t q_len, float scale,

@@ -1,0 +1,405 @@
+// pda_evict.cu -- eviction from a paged cache by accumulated attention weight.
+//
+// choose_kernel: a CTA per (sequence, kv head).  The tokens between the first
+// and the last ones that stay anyway are ranked by their sums as 32-bit keys of
+// the same order; the key of the last one to stay is found digit by digit (11,
+// 11 and 10 bits) from histograms in shared memory, so that a token is looked
+// at three times whatever the budget.  Ties go to the lowest index: warps own
+// consecutive runs of tokens and count theirs before they write.
+//
+// move_kernel: rows to other blocks, in any order.  pack_kernel: rows to the
+// front of their own blocks.  There token kept[i] moves to i <= kept[i], so a
+// source is never behind its destination: a CTA that takes a unit's rows in
+// order may read as far ahead as it likes and overwrites only what it, or an
+// earlier step of its own, has read.  K and V, and parts of their rows, are
+// independent of each other, which is where its CTAs come from.
+#include "pda_evict.h"
+#include "pda_params.h"
+#include "pda_ptx.cuh"
+
+namespace pda {
+
+namespace {
+
+constexpr uint32_t kBadBlock = 0x1u, kBadLength = 0x2u;
+constexpr int kBins = 2048;
+constexpr uint32_t kForced = 0xffffffffu;
+
+struct Unit {
+    int b, kvh;
+    int32_t n, m;  // tokens, tokens that stay
+    bool bad;
+};
+__device__ __forceinline__ Unit unit_of(const EvictParams& p, int64_t u) {
+    Unit r;
+    r.b = (int)(u / p.Hkv);
+    r.kvh = (int)(u - (int64_t)r.b * p.Hkv);
+    const int32_t len = p.lens[r.b];
+    const int64_t most = (int64_t)p.table_stride << p.lbs;
+    r.bad = len < 0 || len > most;
+    r.n = (int32_t)min((int64_t)max(len, 0), most);
+    r.m = min(r.n, p.keep);
+    return r;
+}
+
+// A sum as a key of the same order: NaN the largest but for tokens that stay anyway, -0 as 0.
+__device__ __forceinline__ uint32_t key_of(float w) {
+    if (w != w) return 0xfffffffeu;
+    const uint32_t x = __float_as_uint(w + 0.f);
+    return (x & 0x80000000u) ? ~x : x | 0x80000000u;
+}
+
+// The slot of token t of a sequence: block * bs + place in the block, or -1 (a bad block id).
+__device__ __forceinline__ int64_t slot_of(const EvictParams& p, const int32_t* row, int32_t t) {
+    const int32_t id = row[t >> p.lbs];
+    if (id < 0 || (int64_t)id >= p.num_blocks) {
+        atomicOr(p.err, kBadBlock);
+        return -1;
+    }
+    return ((int64_t)id << p.lbs) + (t & ((1 << p.lbs) - 1));
+}
+__device__ __forceinline__ int64_t weight_at(const EvictParams& p, int64_t slot, int kvh) {
+    return ((((slot >> p.lbs) * p.Hkv) + kvh) << p.lbs) + (slot & ((1 << p.lbs) - 1));
+}
+__device__ __forceinline__ int64_t scale_at(const EvictParams& p, int64_t slot, int kvh, int which) {
+    return (((((slot >> p.lbs) * p.Hkv) + kvh) * 2 + which) << p.lbs) + (slot & ((1 << p.lbs) - 1));
+}
+__device__ __forceinline__ int64_t row_at(const EvictParams& p, int64_t slot, int kvh) {
+    return (slot >> p.lbs) * p.blk + (slot & ((1 << p.lbs) - 1)) * p.tok + kvh * p.kvh;
+}
+
+// The sum over a block's threads; every thread gets it.  `sums` holds a word per warp.
+template <int THREADS>
+__device__ __forceinline__ int block_prefix(int x, int* sums, int& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int y = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int z = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) y += z;
+    }
+    if (lane == 31) sums[warp] = y;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) before += sums[w];
+        all += sums[w];
+    }
+    __syncthreads();
+    total = all;
+    return before + y - x;
+}
+
+// cached: how many keys fit behind the histogram.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) choose_kernel(const EvictParams p, int32_t cached) {
+    extern __shared__ uint32_t keys[];
+    __shared__ int hist[kBins];
+    __shared__ int sums[THREADS / 32], eqs[THREADS / 32];
+    __shared__ int digit, above;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    const Unit u = unit_of(p, blockIdx.x);
+    if (tid == 0 && u.kvh == 0) {
+        p.new_lens[u.b] = u.m;
+        if (u.bad) atomicOr(p.err, kBadLength);
+    }
+    int32_t* kept = p.kept + (int64_t)blockIdx.x * p.keep;
+    if (u.n <= p.keep) {
+        for (int32_t i = tid; i < p.keep; i += THREADS) kept[i] = i < u.n ? i : -1;
+        return;
+    }
+    const int32_t* row = p.table + (int64_t)u.b * p.table_stride;
+    auto load_key = [&](int32_t t) {
+        const int64_t s = slot_of(p, row, t);
+        if (t < p.first || t >= u.n - p.recent) return kForced;
+        return key_of(s < 0 ? 0.f : p.weights[weight_at(p, s, u.kvh)]);
+    };
+    const int32_t here = min(u.n, cached);
+    for (int32_t t = tid; t < here; t += 4 * THREADS) {  // four loads in flight
+        uint32_t k[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) k[i] = t + i * THREADS < here ? load_key(t + i * THREADS) : 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (t + i * THREADS < here) keys[t + i * THREADS] = k[i];
+    }
+    auto key = [&](int32_t t) { return t < cached ? keys[t] : load_key(t); };
+    // The key of the keep-th token in descending order: `prefix` under `mask`, `left` of them still to take
+    uint32_t prefix = 0, mask = 0;
+    int left = p.keep;
+#pragma unroll 1
+    for (int shift = 21; shift >= 0; shift = shift == 21 ? 10 : shift - 10) {
+        const int bins = shift == 0 ? 1024 : kBins;
+        for (int i = tid; i < kBins; i += THREADS) hist[i] = 0;
+        __syncthreads();
+        for (int32_t t0 = 0; t0 < u.n; t0 += THREADS) {
+            const int32_t t = t0 + tid;
+            const uint32_t k = t < u.n ? key(t) : 0u;
+            const bool mine = t < u.n && (k & mask) == prefix;
+            const uint32_t bin = (k >> shift) & (uint32_t)(bins - 1);
+            // one addition for a warp of equal digits, which would meet on one bin otherwise
+            int same = 0;
+            __match_all_sync(0xffffffffu, mine ? bin : 0xffffffffu, &same);
+            if (same) {
+                if (mine && lane == 0) atomicAdd(&hist[bin], 32);
+            } else if (mine) {
+                atomicAdd(&hist[bin], 1);
+            }
+        }
+        __syncthreads();
+        // bins in descending order: thread i takes a run of them
+        constexpr int kPer = kBins / THREADS > 0 ? kBins / THREADS : 1;
+        int count[kPer], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int d = bins - 1 - (tid * kPer + i);
+            count[i] = d >= 0 ? hist[d] : 0;
+            sum += count[i];
+        }
+        int total, before = block_prefix<THREADS>(sum, sums, total);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if (before < left && left <= before + count[i]) {
+                digit = bins - 1 - (tid * kPer + i);
+                above = before;
+            }
+            before += count[i];
+        }
+        __syncthreads();
+        prefix |= (uint32_t)digit << shift;
+        mask |= (uint32_t)(bins - 1) << shift;
+        left -= above;
+        __syncthreads();
+    }
+    // Every key above `prefix` stays, and the first `left` of its own.
+    const int32_t run = ((u.n + THREADS - 1) / THREADS) * 32;  // tokens of a warp
+    const int32_t lo = min(u.n, warp * run), hi = min(u.n, lo + run);
+    int more = 0, equal = 0;
+    for (int32_t t = lo + lane; t < hi; t += 32) {
+        const uint32_t k = key(t);
+        more += k > prefix;
+        equal += k == prefix;
+    }
+    more = __reduce_add_sync(0xffffffffu, more);
+    equal = __reduce_add_sync(0xffffffffu, equal);
+    if (lane == 0) {
+        sums[warp] = more;
+        eqs[warp] = equal;
+    }
+    __syncthreads();
+    int at = 0, taken = 0;
+    for (int w = 0; w < warp; ++w) {
+        at += sums[w];
+        taken += eqs[w];
+    }
+    at += min(taken, left);
+    for (int32_t t0 = lo; t0 < hi; t0 += 32) {
+        const int32_t t = t0 + lane;
+        const uint32_t k = t < hi ? key(t) : 0u;
+        const uint32_t eq = __ballot_sync(0xffffffffu, t < hi && k == prefix), below = (1u << lane) - 1u;
+        const bool stays = t < hi && (k > prefix || (k == prefix && taken + __popc(eq & below) < left));
+        const uint32_t ones = __ballot_sync(0xffffffffu, stays);
+        if (stays) kept[at + __popc(ones & below)] = t;
+        at += __popc(ones);
+        taken += __popc(eq);
+    }
+}
+
+__device__ __forceinline__ uint4 ld16(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
+
+// 64 destination rows of a unit to other blocks.
+constexpr int kMoveThreads = 256, kMoveRows = 64;
+template <int RB>  // bytes of a row
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p, int32_t chunks) {
+    constexpr int CH = 2 * RB / 16;                                // 16-byte pieces of a token: K, then V
+    constexpr int N = kMoveRows * CH / kMoveThreads;               // pieces of a thread
+    constexpr int U = N < 8 ? N : 8;                               // in flight
+    __shared__ int64_t src[kMoveRows], dst[kMoveRows];
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    const int64_t unit = blockIdx.x / chunks;
+    const int32_t i0 = (int32_t)(blockIdx.x % chunks) * kMoveRows;
+    const Unit u = unit_of(p, unit);
+    if (i0 >= u.m) return;
+    const int tid = threadIdx.x;
+    if (tid < kMoveRows) {
+        int64_t a = -1, b = -1;
+        const int32_t i = i0 + tid;
+        if (i < u.m) {
+            const int32_t t = __ldcg(p.kept + unit * p.keep + i);
+            a = slot_of(p, p.table + (int64_t)u.b * p.table_stride, t);
+            b = slot_of(p, p.out_table + (int64_t)u.b * p.out_stride, i);
+            if (b >= 0) {
+                p.weights[weight_at(p, b, u.kvh)] = a < 0 ? 0.f : p.weights[weight_at(p, a, u.kvh)];
+                if (p.scales)
+                    for (int w = 0; w < 2; ++w)
+                        p.scales[scale_at(p, b, u.kvh, w)] = a < 0 ? 0.f : p.scales[scale_at(p, a, u.kvh, w)];
+            }
+        }
+        src[tid] = a < 0 ? -1 : row_at(p, a, u.kvh);
+        dst[tid] = b < 0 ? -1 : row_at(p, b, u.kvh);
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int k0 = 0; k0 < N; k0 += U) {
+        uint4 x[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int e = (k0 + k) * kMoveThreads + tid, r = e / CH, c = e % CH;
+            const int64_t s = src[r];
+            x[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (s >= 0) x[k] = ld16((c < CH / 2 ? p.k : p.v) + s + (c % (CH / 2)) * 16);
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int e = (k0 + k) * kMoveThreads + tid, r = e / CH, c = e % CH;
+            const int64_t d = dst[r];
+            if (d >= 0) *reinterpret_cast<uint4*>((c < CH / 2 ? p.k : p.v) + d + (c % (CH / 2)) * 16) = x[k];
+        }
+    }
+}
+
+// A unit's K or V rows, SB bytes of each, to the front of its blocks: steps of
+// R rows in order, the next step's loads ahead of this one's stores.
+constexpr int kPackThreads = 256;
+template <int SB>
+__global__ void __launch_bounds__(kPackThreads) pack_kernel(const EvictParams p, int32_t parts) {
+    constexpr int CH = SB / 16, U = 4, R = U * kPackThreads / CH;  // pieces of a row, of a thread; rows of a step
+    __shared__ int64_t src[2][R], dst[2][R];
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    const int64_t unit = blockIdx.x / (2 * parts);
+    const int which = (int)(blockIdx.x / parts) & 1, part = (int)(blockIdx.x % parts);
+    const Unit u = unit_of(p, unit);
+    if (u.n <= p.keep) return;  // nothing moves
+    const int tid = threadIdx.x;
+    uint8_t* pool = (which ? p.v : p.k) + part * SB;
+    const int32_t* row = p.table + (int64_t)u.b * p.table_stride;
+    const int32_t* kept = p.kept + unit * p.keep;
+    uint4 x[2][U];
+    constexpr int kF = R / kPackThreads > 0 ? R / kPackThreads : 1;  // rows whose place a thread looks up
+    float w[2][kF], sc[2][kF];
+    int64_t wd[2][kF], sd[2][kF];
+    auto load = [&](int s, int32_t i0) {  // step s & 1
+#pragma unroll
+        for (int f = 0; f < kF; ++f) {
+            const int r = f * kPackThreads + tid;
+            wd[s][f] = sd[s][f] = -1;
+            if (r < R) {
+                int64_t a = -1, b = -1;
+                const int32_t i = i0 + r;
+                bool moves = false;
+                if (i < u.m) {
+                    const int32_t t = __ldcg(kept + i);
+                    moves = t != i;
+                    if (moves) {
+                        a = slot_of(p, row, t);
+                        b = slot_of(p, row, i);
+                    }
+                }
+                if (part == 0 && b >= 0) {
+                    if (which == 0) {
+                        wd[s][f] = weight_at(p, b, u.kvh);
+                        w[s][f] = a < 0 ? 0.f : p.weights[weight_at(p, a, u.kvh)];
+                    }
+                    if (p.scales) {
+                        sd[s][f] = scale_at(p, b, u.kvh, which);
+                        sc[s][f] = a < 0 ? 0.f : p.scales[scale_at(p, a, u.kvh, which)];
+                    }
+                }
+                src[s][r] = a < 0 ? -1 : row_at(p, a, u.kvh);
+                dst[s][r] = b < 0 ? -1 : row_at(p, b, u.kvh);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int e = k * kPackThreads + tid, r = e / CH, c = e % CH;
+            x[s][k] = make_uint4(0u, 0u, 0u, 0u);
+            if (src[s][r] >= 0) x[s][k] = ld16(pool + src[s][r] + c * 16);
+        }
+    };
+    auto store = [&](int s) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int e = k * kPackThreads + tid, r = e / CH, c = e % CH;
+            if (dst[s][r] >= 0) *reinterpret_cast<uint4*>(pool + dst[s][r] + c * 16) = x[s][k];
+        }
+#pragma unroll
+        for (int f = 0; f < kF; ++f) {
+            if (wd[s][f] >= 0) p.weights[wd[s][f]] = w[s][f];
+            if (sd[s][f] >= 0) p.scales[sd[s][f]] = sc[s][f];
+        }
+    };
+    load(0, 0);
+#pragma unroll 1
+    for (int32_t i0 = 0; i0 < u.m; i0 += 2 * R) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int32_t i = i0 + s * R;
+            if (i >= u.m) break;
+            if (i + R < u.m) load(s ^ 1, i + R);  // (its barrier, or the one below, orders every load of this step before its stores)
+            else __syncthreads();
+            store(s);
+            __syncthreads();
+        }
+    }
+}
+
+template <class K, class... Args>
+cudaError_t launch(K kernel, int64_t grid, int threads, size_t smem, cudaStream_t stream, Args... args) {
+    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+constexpr int kMostKeys = 49152;  // 192 KB of keys beside the histogram
+
+}  // namespace
+
+cudaError_t evict_setup() {
+    return cudaFuncSetAttribute(choose_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostKeys * 4);
+}
+
+cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
+    const int64_t units = (int64_t)p.B * p.Hkv, tokens = (int64_t)p.table_stride << p.lbs;
+    cudaError_t e;
+    if (tokens <= 8192) e = launch(choose_kernel<256>, units, 256, (size_t)tokens * 4, stream, p, (int32_t)tokens);
+    else {
+        const int32_t cached = (int32_t)(tokens < kMostKeys ? tokens : kMostKeys);
+        e = launch(choose_kernel<1024>, units, 1024, (size_t)cached * 4, stream, p, cached);
+    }
+    if (e != cudaSuccess) return e;
+    if (!p.in_place) {
+        const int32_t most = (int32_t)(tokens < p.keep ? tokens : p.keep), chunks = (most + kMoveRows - 1) / kMoveRows;
+        switch (p.row_bytes) {
+            case 64: return launch(move_kernel<64>, units * chunks, kMoveThreads, 0, stream, p, chunks);
+            case 128: return launch(move_kernel<128>, units * chunks, kMoveThreads, 0, stream, p, chunks);
+            case 256: return launch(move_kernel<256>, units * chunks, kMoveThreads, 0, stream, p, chunks);
+            case 512: return launch(move_kernel<512>, units * chunks, kMoveThreads, 0, stream, p, chunks);
+            default: return cudaErrorInvalidValue;
+        }
+    }
+    // whole rows where there are CTAs enough, else 64-byte parts of them
+    const int32_t part = units * 2 >= 2 * p.sms || p.row_bytes < 128 ? p.row_bytes : 64, parts = p.row_bytes / part;
+    switch (part) {
+        case 64: return launch(pack_kernel<64>, units * 2 * parts, kPackThreads, 0, stream, p, parts);
+        case 128: return launch(pack_kernel<128>, units * 2 * parts, kPackThreads, 0, stream, p, parts);
+        case 256: return launch(pack_kernel<256>, units * 2 * parts, kPackThreads, 0, stream, p, parts);
+        case 512: return launch(pack_kernel<512>, units * 2 * parts, kPackThreads, 0, stream, p, parts);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace pda

@@ -183,6 +183,27 @@ __device__ __forceinline__ int32_t tokens_of(const SplitParams& p, int s, int32_
     return len < 0 ? 0 : len;
 }
 
+// The group that launch sequence b (of the launch) belongs to, or -1 (kScored;
+// groups' starts do not decrease, empty ones stand before the one they equal).
+__device__ __forceinline__ int group_of_seq(const Scoring& sc, int b) {
+    if (sc.groups == nullptr) return -1;
+    b += sc.seq0;
+    int lo = 0, hi = sc.n_groups;
+    while (lo < hi) {  // the first entry whose start is past b
+        const int mid = (lo + hi) >> 1;
+        if (__ldcg(&sc.groups[mid].start) <= b) lo = mid + 1; else hi = mid;
+    }
+    return lo > 0 && b < __ldcg(&sc.groups[sc.n_groups].start) ? lo - 1 : -1;
+}
+
+// Blocks of launch row s that the walk leaves out: those that its group shares.
+template <int MODE>
+__device__ __forceinline__ int32_t skip_of(const SplitParams& p, int s) {
+    if constexpr (MODE != kScored) return 0;
+    const int g = group_of_seq(p.sc, row_info<is_multi(MODE)>(p, s).b);
+    return g < 0 ? 0 : __ldcg(&p.sc.groups[g].blocks);
+}
+
 // Blocks of sequence b with length entry L, validated and clamped (flags
 // bad lengths, unless FLAG is false: a speculative read).
 template <bool MQ, bool FLAG = true>
@@ -217,6 +238,7 @@ __device__ __forceinline__ int32_t last_entry(const SplitParams& p, int b) {
 }
 
 // Valid slots of sequence b's last block (1..bs) from its last_entry e.
+// (nb counts the blocks that the walk leaves out, too)
 template <bool MQ>
 __device__ __forceinline__ int32_t last_block_slots(const SplitParams& p, int b, int32_t nb, int32_t e) {
     if (p.lens_are_blocks) {
@@ -239,9 +261,10 @@ __device__ __forceinline__ int32_t last_block_slots(const SplitParams& p, int b,
 // Run by the kThreads threads of the consumer and producer warps (threads
 // 0 .. kThreads-1), synchronised by named barrier 1; ends with that barrier
 // (which also publishes the stage barriers).
-template <bool MQ, int kThreads>
+template <int MODE, int kThreads>
 __device__ __forceinline__ int32_t build_prefix(const SplitParams& p, int32_t* pfx, int32_t* scan) {
     constexpr int kPer = (kMaxLaunchBatch + kThreads - 1) / kThreads;
+    constexpr bool MQ = is_multi(MODE);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.B + kThreads - 1) / kThreads;  // <= kPer
     const int lo = min(p.B, tid * per), hi = min(p.B, lo + per);
@@ -252,7 +275,7 @@ __device__ __forceinline__ int32_t build_prefix(const SplitParams& p, int32_t* p
 #pragma unroll
     for (int k = 0; k < kPer; ++k)
         if (lo + k < hi) {
-            const int32_t v = plan_blocks(blocks_of<MQ>(p, lo + k, L[k]), p.unit_cost);
+            const int32_t v = plan_blocks(blocks_of<MQ>(p, lo + k, L[k]) - skip_of<MODE>(p, lo + k), p.unit_cost);
             pfx[lo + k] = v;
             sum += v;
             big = max(big, v);
@@ -434,6 +457,7 @@ __device__ __forceinline__ void run_producer(const SplitParams& p, uint32_t base
     int32_t w[4], f[4], nx[4];
     int32_t lv = bs;   // valid slots of this sequence's last block
     int32_t nle = 0;   // the next sequence's last_entry, loaded a unit ahead
+    int32_t sk = 0, skn = 0;  // blocks that the walks of b and bn leave out (kScored)
     int bn = p.B;               // next non-empty sequence
     // The launch rows of b and bn (multi-query: table row, first query, query
     // count) and b's causal limit, computed once per sequence, not per stage.
@@ -447,11 +471,11 @@ __device__ __forceinline__ void run_producer(const SplitParams& p, uint32_t base
         return p.table[(int64_t)row * p.table_stride + idx];
     };
     // entries [from, from + 128) of table row `row` (nbs blocks), lane-strided
-    auto load_ids = [&](int32_t* dst, int row, int32_t from, int32_t nbs) {
+    auto load_ids = [&](int32_t* dst, int row, int32_t from, int32_t nbs, int32_t skip) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int32_t e = from + 32 * k + lane;
-            dst[k] = e < nbs ? table_at(row, e) : 0;
+            dst[k] = e < nbs ? table_at(row, e + skip) : 0;
         }
     };
     auto next_seq = [&](int s) {
@@ -488,15 +512,17 @@ __device__ __forceinline__ void run_producer(const SplitParams& p, uint32_t base
         rn = bn < p.B ? row_info<MQ>(p, bn) : ri;
         const int32_t e_cur = last_entry<MQ>(p, b);
         nle = bn < p.B ? last_entry<MQ>(p, bn) : 0;
-        load_ids(w, ri.b, win, nb);
+        sk = skip_of<MODE>(p, b);
+        skn = bn < p.B ? skip_of<MODE>(p, bn) : 0;
+        load_ids(w, ri.b, win, nb, sk);
         if (win == 0) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) f[k] = w[k];
         } else {
-            load_ids(f, ri.b, 0, nb);
+            load_ids(f, ri.b, 0, nb, sk);
         }
-        if (bn < p.B) load_ids(nx, rn.b, 0, real_blocks(pfx[bn + 1] - pfx[bn], p.unit_cost));
-        lv = last_block_slots<MQ>(p, b, nb, e_cur);
+        if (bn < p.B) load_ids(nx, rn.b, 0, real_blocks(pfx[bn + 1] - pfx[bn], p.unit_cost), skn);
+        lv = last_block_slots<MQ>(p, b, nb + sk, e_cur);
         if constexpr (MQ) lim = e_cur - p.q_len + ri.first;
     }
     // Past a unit's last block: skip its cost tail and move to the next unit
@@ -515,13 +541,15 @@ __device__ __forceinline__ void run_producer(const SplitParams& p, uint32_t base
             for (int k = 0; k < 4; ++k) w[k] = f[k] = nx[k];
             if (b < p.B && pos < end) {
                 ri = rn;
-                lv = last_block_slots<MQ>(p, b, nb, nle);
+                sk = skn;
+                lv = last_block_slots<MQ>(p, b, nb + sk, nle);
                 if constexpr (MQ) lim = nle - p.q_len + ri.first;
                 bn = next_seq(b);
                 if (bn < p.B) {
                     rn = row_info<MQ>(p, bn);
                     nle = last_entry<MQ>(p, bn);
-                    load_ids(nx, rn.b, 0, real_blocks(pfx[bn + 1] - pfx[bn], p.unit_cost));
+                    skn = skip_of<MODE>(p, bn);
+                    load_ids(nx, rn.b, 0, real_blocks(pfx[bn + 1] - pfx[bn], p.unit_cost), skn);
                 }
             }
         } else {
@@ -561,7 +589,7 @@ __device__ __forceinline__ void run_producer(const SplitParams& p, uint32_t base
             m.n_valid = (n - 1) * bs + lastv;
             m.flags = (seg_begin ? kSegBegin : 0) | (seg_end ? kSegEnd : 0) | (whole ? kWholeUnit : 0);
             m.slot = b * Hkv + kvh + (int)blockIdx.x;
-            m.j0 = j;
+            m.j0 = j + sk;
             m.lim = lim;
             m.nr = MQ ? ri.cnt * p.G : p.G;
             meta[stage] = m;
@@ -594,7 +622,7 @@ __device__ __forceinline__ void run_producer(const SplitParams& p, uint32_t base
 #pragma unroll
             for (int k = 2; k < 4; ++k) {
                 const int32_t e = win + 32 * k + lane;
-                w[k] = e < nb ? table_at(ri.b, e) : 0;
+                w[k] = e < nb ? table_at(ri.b, e + sk) : 0;
             }
         }
         if (++stage == S) { stage = 0; phase ^= 1u; }
@@ -716,6 +744,100 @@ __device__ __forceinline__ void merge_state(float& M, float& Ls, float4& Os, flo
     M = Mn;
 }
 
+// ---- kScored: scores capped and biased, and the states of a shared prefix
+
+// A score in base-2 units, capped to cap * tanh(s / cap) and with slope * far
+// added (far: the token's place less the query's).  tanh from its definition,
+// (1 - e) / (1 + e) with e = exp(-2 |s| / cap): off by a few 2^-24 of the cap
+// for any s, where the hardware's tanh is off by 2^-11 of it (0.02 in the
+// exponent at a cap of 50).
+__device__ __forceinline__ float score_of(const Scoring& sc, float s, float slope, float far) {
+    if (sc.cap != 0.f) {
+        const float e = ex2(fabsf(s) * sc.inv_cap * -2.885390082f);  // -2 log2 e
+        s = copysignf(__fdividef(sc.cap * (1.f - e), 1.f + e), s);
+    }
+    return fmaf(slope, far, s);
+}
+
+// The slope of score column `col` of a segment (base-2 units).
+__device__ __forceinline__ float column_slope(const SplitParams& p, const StageMeta& m, int col) {
+    if (p.sc.slopes == nullptr || col >= m.nr) return 0.f;
+    return (p.sc.slopes[m.kvh * p.G + col % p.G]) * 1.4426950408889634f;
+}
+
+// Scores of row `row` of a stage, columns col and col + 1.
+__device__ __forceinline__ void put_scores(const SplitParams& p, const StageMeta& m, int row, int col, float a, float b) {
+    const int64_t tokens = (int64_t)p.table_stride * p.bs, unit = (int64_t)m.b * p.Hkv + m.kvh;
+    float* at = p.sc.scores + (unit * tokens + (int64_t)m.j0 * p.bs + row) * p.rows_per_slot + col;
+    if (col + 1 < m.nr && (p.rows_per_slot & 1) == 0) {
+        *reinterpret_cast<float2*>(at) = make_float2(a, b);
+    } else {
+        if (col < m.nr) at[0] = a;
+        if (col + 1 < m.nr) at[1] = b;
+    }
+}
+
+// Joins the state of an output row's shared prefix, which the prefix kernel
+// left in pieces, to (M, Ls, Os), columns d4 .. d4 + 3; and hands out the
+// row's (m, l).  Row r of a q tile and chunk d4 / 4 of it lie at [chunk][r].
+template <int D, bool kWide>
+__device__ __forceinline__ void join_prefix(const SplitParams& p, int b, int qi, int head, int d4, float& M, float& Ls,
+                                            float4& Os) {
+    const Scoring& sc = p.sc;
+    const int g = group_of_seq(sc, b);
+    if (g >= 0) {
+        const PrefixGroup* at = sc.groups + g;  // (read from L2: the prefix kernel has just written it)
+        PrefixGroup pg;
+        pg.start = __ldcg(&at->start);
+        pg.tiles = __ldcg(&at->tiles);
+        pg.unit = __ldcg(&at->unit);
+        pg.work = __ldcg(&at->work);
+        if (pg.tiles > 0) {
+            constexpr int kSub = prefix_streams(D);  // q tiles of a slot
+            const int kvh = head / p.G;
+            const int row = ((b + sc.seq0 - pg.start) * p.q_len + qi) * p.G + head - kvh * p.G;
+            const int tile = row >> 7, r = row & 127;
+            const int64_t W = __ldcg(&sc.groups[sc.n_groups].work), P = prefix_plan_ctas(W, sc.prefix_ctas);
+            const int unit = tile / kSub * p.Hkv + kvh;
+            const int64_t first = pg.work + (int64_t)unit * pg.tiles;
+            const int64_t c0 = cta_of_block(first, W, P), c1 = cta_of_block(first + pg.tiles - 1, W, P);
+            const int64_t slot0 = (int64_t)pg.unit + unit;
+            for (int64_t c = c0; c <= c1; c += 8) {
+                float mi[8], li[8];
+                float4 oi[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    mi[k] = kNegInf;
+                    li[k] = 0.f;
+                    oi[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (c + k > c1) continue;
+                    const int64_t at = (slot0 + c + k) * kSub + tile % kSub;
+                    const float2 ml = __ldcg(reinterpret_cast<const float2*>(sc.prefix_ml) + at * 128 + r);
+                    mi[k] = ml.x;
+                    li[k] = ml.y;
+                    oi[k] = __ldcg(reinterpret_cast<const float4*>(sc.prefix_o) + (at * (D / 4) + d4 / 4) * 128 + r);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) merge_state<kWide>(M, Ls, Os, mi[k], li[k], oi[k]);
+            }
+        }
+    }
+    if (sc.row_ml && d4 == 0)
+        *reinterpret_cast<float2*>(sc.row_ml + (((int64_t)b * p.q_len + qi) * p.Hq + head) * 2) = make_float2(M, Ls);
+}
+
+// An output row without a token of its own: its prefix's o / l, or zeros.
+template <int D, bool kWide>
+__device__ __forceinline__ void write_unwalked(const SplitParams& p, int b, int qi, int head, int d4, int64_t o) {
+    float M = kNegInf, L = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    join_prefix<D, kWide>(p, b, qi, head, d4, M, L, v);
+    if (kWide ? L != 0.f : L > 0.f) v = make_float4(v.x / L, v.y / L, v.z / L, v.w / L);
+    else v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p.out_f32) *reinterpret_cast<float4*>(p.out_f32 + o) = v;
+    else *reinterpret_cast<uint2*>(p.out + o) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+
 // Segment-end roles (see the epilogue in run_consumer).
 enum SegRole : int32_t { kRoleWhole = 0, kRoleStore = 1, kRoleMerge = 2, kRoleAbort = -1 };
 
@@ -730,13 +852,14 @@ __device__ __forceinline__ void run_consumer(const SplitParams& p, uint32_t base
     const uint32_t full0 = base_s + L.bars, empty0 = full0 + 8 * S;
     const int g = lane >> 2, t = lane & 3;
     const int r0 = warp * 16;
-    constexpr bool MQ = MODE == kMulti;
+    constexpr bool MQ = is_multi(MODE), kExt = MODE == kScored;
     static_assert(C::kQTiles == 0, "n8 form");
     const int G = p.G;
     const float sl2 = p.scale_log2;
     // multi-query: the queries of this lane's two score columns (column n is
     // query n / G of the row), fixed for the whole launch
     const int qc0 = MQ ? (2 * t) / G : 0, qc1 = MQ ? (2 * t + 1) / G : 0;
+    float slope0 = 0.f, slope1 = 0.f;  // of the lane's two columns (kExt)
     // ldmatrix row addresses: QK reads K as the A operand (rows = tokens),
     // PV reads V transposed as the A operand (rows of V = tokens = k index).
     const int qk_row = r0 + (lane & 7) + (((lane >> 3) & 1) << 3);
@@ -784,6 +907,10 @@ __device__ __forceinline__ void run_consumer(const SplitParams& p, uint32_t base
                 const int h = (4 * i4) / D, d4 = 4 * i4 - h * D;
                 const int64_t o = MQ ? qo_offset<MQ>(p, ri.b, ri.first + h / G, kvh * G + h % G, D) + d4
                                      : qo_offset<MQ>(p, sq, 0, kvh * G, D) + 4 * i4;
+                if constexpr (kExt) {
+                    write_unwalked<D, false>(p, ri.b, ri.first + h / G, kvh * G + h % G, d4, o);
+                    continue;
+                }
                 if (p.out_f32) *reinterpret_cast<float4*>(p.out_f32 + o) = make_float4(0.f, 0.f, 0.f, 0.f);
                 else *reinterpret_cast<uint2*>(p.out + o) = make_uint2(0u, 0u);
             }
@@ -817,6 +944,10 @@ __device__ __forceinline__ void run_consumer(const SplitParams& p, uint32_t base
             if (m.flags & kSegBegin) {
                 m0 = m1 = kNegInf;
                 l0 = l1 = 0.f;
+                if constexpr (kExt) {
+                    slope0 = column_slope(p, m, 2 * t);
+                    slope1 = column_slope(p, m, 2 * t + 1);
+                }
                 const uint8_t* sq = base + (sV - base_s) + C::kTileBytes;
 #pragma unroll
                 for (int kk = 0; kk < KS; ++kk) {
@@ -853,6 +984,14 @@ __device__ __forceinline__ void run_consumer(const SplitParams& p, uint32_t base
                 float s1 = (acc[0][1] + acc[1][1]) * sl2;
                 float s2 = (acc[0][2] + acc[1][2]) * sl2;
                 float s3 = (acc[0][3] + acc[1][3]) * sl2;
+                if constexpr (kExt) {
+                    const float far0 = (float)(m.j0 * p.bs + r0 + g - m.lim - qc0);
+                    const float far1 = (float)(m.j0 * p.bs + r0 + g - m.lim - qc1);
+                    s0 = score_of(p.sc, s0, slope0, far0);
+                    s1 = score_of(p.sc, s1, slope1, far1);
+                    s2 = score_of(p.sc, s2, slope0, far0 + 8.f);
+                    s3 = score_of(p.sc, s3, slope1, far1 + 8.f);
+                }
                 if (m.n_valid < C::kST) {  // a stage that ends mid-way: mask the rows past it
                     if (r0 + g >= m.n_valid) { s0 = kNegInf; s1 = kNegInf; }
                     if (r0 + g + 8 >= m.n_valid) { s2 = kNegInf; s3 = kNegInf; }
@@ -866,6 +1005,12 @@ __device__ __forceinline__ void run_consumer(const SplitParams& p, uint32_t base
                         if (pos > lim1) s1 = kNegInf;
                         if (pos + 8 > lim0) s2 = kNegInf;
                         if (pos + 8 > lim1) s3 = kNegInf;
+                    }
+                }
+                if constexpr (kExt) {
+                    if (p.sc.scores) {
+                        if (r0 + g < m.n_valid) put_scores(p, m, r0 + g, 2 * t, s0, s1);
+                        if (r0 + g + 8 < m.n_valid) put_scores(p, m, r0 + g + 8, 2 * t, s2, s3);
                     }
                 }
                 // column max over the 16 tokens (lanes sharing t)
@@ -1077,6 +1222,8 @@ __device__ __forceinline__ void run_consumer(const SplitParams& p, uint32_t base
                         p.l_state[row] = Lo;
                     }
                 } else {
+                    if constexpr (kExt)
+                        join_prefix<D, false>(p, ri.b, ri.first + h / G, m.kvh * G + h % G, d4, M, Ls, Os);
                     const float4 v = Ls > 0.f ? make_float4(Os.x / Ls, Os.y / Ls, Os.z / Ls, Os.w / Ls)
                                               : make_float4(0.f, 0.f, 0.f, 0.f);
                     const int64_t o = MQ ? qo_offset<MQ>(p, ri.b, ri.first + h / G, m.kvh * G + h % G, D) + d4
@@ -1122,7 +1269,7 @@ __device__ __forceinline__ void run_consumer(const SplitParams& p, uint32_t base
 
 // Zero output rows of the units with no tokens (they have no segment), shared
 // round-robin over the grid: the stores overlap the wait for the first stage.
-template <int D, int kThreadsC>
+template <int D, int kThreadsC, bool kExt = false>
 __device__ __forceinline__ void zero_empty_rows(const SplitParams& p, const int32_t* pfx, int ct) {
     for (int u = blockIdx.x; u < p.B * p.Hkv; u += gridDim.x) {
         const int sq = u / p.Hkv, kvh = u - sq * p.Hkv;
@@ -1132,6 +1279,10 @@ __device__ __forceinline__ void zero_empty_rows(const SplitParams& p, const int3
         for (int i4 = ct; i4 < NR * D / 4; i4 += kThreadsC) {
             const int h = (4 * i4) / D, d4 = 4 * i4 - h * D;
             const int64_t o = qo_offset<true>(p, ri.b, ri.first + h / p.G, kvh * p.G + h % p.G, D) + d4;
+            if constexpr (kExt) {
+                write_unwalked<D, true>(p, ri.b, ri.first + h / p.G, kvh * p.G + h % p.G, d4, o);
+                continue;
+            }
             if (p.out_f32) *reinterpret_cast<float4*>(p.out_f32 + o) = make_float4(0.f, 0.f, 0.f, 0.f);
             else *reinterpret_cast<uint2*>(p.out + o) = make_uint2(0u, 0u);
         }
@@ -1168,7 +1319,7 @@ struct RowSlices {
 // Returns false when the CTA aborts.  kScaled: the states of an 8-bit cache,
 // whose references follow the V scales (merge_state's kWide), and a NaN sum of
 // weights gives NaN, not 0.
-template <int D, int kThreadsC, int kTileRows = 16, bool kScaled = false, class Own>
+template <int D, int kThreadsC, int kTileRows = 16, bool kScaled = false, bool kExt = false, class Own>
 __device__ __forceinline__ bool rows_tile_merge(const SplitParams& p, const StageMeta& m, int tile, int ct,
                                                 int32_t ticket, const UnitPieces& pc, const GroupRange& grs,
                                                 const RowInfo& ri, const Own& own, int32_t* st_role, uint32_t cbar,
@@ -1250,6 +1401,8 @@ __device__ __forceinline__ bool rows_tile_merge(const SplitParams& p, const Stag
                 Ls = Lr;
                 Os = Or;
             }
+            if constexpr (kExt)
+                join_prefix<D, kScaled>(p, ri.b, ri.first + h / G, m.kvh * G + h % G, d4, M, Ls, Os);
             const float4 v = (kScaled ? Ls != 0.f : Ls > 0.f) ? make_float4(Os.x / Ls, Os.y / Ls, Os.z / Ls, Os.w / Ls)
                                       : make_float4(0.f, 0.f, 0.f, 0.f);
             const int64_t oo = qo_offset<true>(p, ri.b, ri.first + h / G, m.kvh * G + h % G, D) + d4;
@@ -2142,7 +2295,7 @@ __global__ void __maxnreg__(split_max_regs(D, MODE)) split_kernel(const __grid_c
         if (MODE != kGather) pdl_launch_dependents();
     }
     // ends with the main warps' barrier (which also publishes the stage barriers)
-    const int32_t nv_max = build_prefix<is_multi(MODE), C::kMainThreads>(p, pfx, scan);
+    const int32_t nv_max = build_prefix<MODE, C::kMainThreads>(p, pfx, scan);
     int64_t begin, end;
     const GroupRange gr = cta_range<MODE>(p, pfx, nv_max, C::kST, gridDim.x, &begin, &end);
 

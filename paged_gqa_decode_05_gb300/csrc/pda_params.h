@@ -30,12 +30,16 @@ constexpr int kMaxRowsPerWalk = 32;                      // q rows one KV walk s
 // M, in one or two tiles of 16 rows, so that one walk over the KV serves up
 // to 32 q rows.  kMultiTc is the row form of 32 q rows on the tcgen05
 // tensor cores: accumulators in tensor memory, one thread issues the MMAs.
+// kScored is the n8 form of one or several causal queries with what
+// ScoredParams adds: capped and distance-biased scores, scores written out, a
+// shared prefix's state joined at the end.
 enum Mode : int {
-    kOneShot = 0, kTiled = 1, kGather = 2, kMulti = 3, kMultiRows16 = 4, kMultiRows32 = 5, kMultiTc = 6
+    kOneShot = 0, kTiled = 1, kGather = 2, kMulti = 3, kMultiRows16 = 4, kMultiRows32 = 5, kMultiTc = 6, kScored = 7
 };
-constexpr int kNumModes = 7;
+constexpr int kNumModes = 7;  // of the context's split kernels; kScored is set up on its own
 __host__ __device__ constexpr bool is_multi(int mode) {
-    return mode == kMulti || mode == kMultiRows16 || mode == kMultiRows32 || mode == kMultiTc;
+    return mode == kMulti || mode == kMultiRows16 || mode == kMultiRows32 || mode == kMultiTc ||
+           mode == kScored;
 }
 __host__ __device__ constexpr bool is_tc(int mode) { return mode == kMultiTc; }
 __host__ __device__ constexpr bool writes_output(int mode) { return mode == kOneShot || is_multi(mode); }
@@ -84,6 +88,31 @@ struct StageMeta {
 };
 enum MetaFlags : int32_t { kSegBegin = 1, kSegEnd = 2, kWholeUnit = 4, kDone = 8 };
 
+// The batch's groups of sequences with a shared prefix, as the prefix kernel
+// plans them (pda_prefix.h); the entry after the last group holds the totals.
+struct PrefixGroup {
+    int32_t start;   // first sequence
+    int32_t blocks;  // shared blocks
+    int32_t tiles;   // token tiles of the prefix
+    int32_t pairs;   // units per kv head (pairs of q tiles; single ones at head size 256)
+    int32_t unit;    // first unit
+    int32_t work;    // first position of the plan
+};
+
+// What kScored adds to a launch.  Scores are in base-2 units.
+struct Scoring {
+    float cap, inv_cap;          // cap * log2 e and its inverse; 0: scores as they are
+    const float* slopes;         // [Hq] or null: score += slope * (token - the query's own)
+    float* scores;               // [launch row][Hkv][tokens][rows_per_slot] out, or null
+    float* row_ml;               // [B * q_len * Hq][2] out: (m, l) of every output row, or null
+    const PrefixGroup* groups;   // [n_groups + 1], or null: no shared prefix
+    int32_t n_groups;
+    int32_t seq0;                // first sequence of this launch
+    int32_t prefix_ctas;         // CTAs of the prefix kernel
+    const float* prefix_o;       // [slots][tiles][D / 4][128][4]
+    const float* prefix_ml;      // [slots][tiles][128][2]
+};
+
 struct SplitParams {
     CUtensorMap tm_k;            // K pool, 5-D {64, bs, D/64, Hkv, num_blocks}, box {64, bs, D/64, 1, 1};
                                  // for gather4 2-D {D, rows}, box {64, 1}
@@ -126,6 +155,7 @@ struct SplitParams {
     int32_t early_inputs;        // tiled: read the inputs before the previous kernel completes
                                  // (a tile step right behind another of the same step)
     float scale_log2;            // softmax scale * log2(e)
+    Scoring sc;                  // kScored
 };
 
 struct SmemLayout {

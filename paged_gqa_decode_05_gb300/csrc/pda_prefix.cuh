@@ -1,0 +1,711 @@
+// pda_prefix.cuh -- attention of a group of sequences over the prefix they
+// share, on the tcgen05 tensor cores.
+//
+// The q rows of a group and kv head (its sequences x queries x G heads) meet
+// every token of the prefix, so they are tiles of 128 rows of a matrix product:
+//   S = Q K^T   (M = 128 q rows, N = a tile of kT tokens; Q and K in shared
+//                memory, S in tensor memory)
+//   softmax     (a thread per q row, 128 lanes of tensor memory: no shuffles;
+//                it reads its row of S and writes P over it, as bf16 high and
+//                low parts, p = hi + lo to 2^-17)
+//   O += P V    (P as the A operand in tensor memory, V as an MN-major B)
+// and the result is an online-softmax state (m, l, o) per row, which the
+// scored decode of the sequences' own tokens joins (join_prefix).
+//
+// Work: units (pair of q tiles, kv head) of one position per token tile, cut
+// evenly over one CTA per SM.  Each CTA runs two streams of four softmax warps
+// with an S and an O each.  A unit of two q tiles gives each stream one, so
+// that a tile of K and V serves 256 q rows; a unit of one q tile gives the
+// streams alternate token tiles, and their states join at the segment's end.
+// While one stream's softmax runs, the other's products do.  Head size 256,
+// whose O takes half the tensor memory, runs one stream.
+//
+// K and V go through a ring of slots of a token tile each, K and V apart so
+// that K's is free once S is there.  Four loader warps fill it with 16-byte
+// cp.async in the swizzle of the tensor cores' operands; rows come one by one
+// through the block table, so any block size and any strides do.  Rows behind
+// the prefix's end are zero-filled, as are those of bad block ids.  The codes of 8-bit caches
+// land in their own slot and are spread to bf16 there, which holds them
+// exactly (4 and 8 significant bits); K scales multiply the scores, V scales
+// the weights.  2^-40 of them is taken: weights reach 2^8 (the reference lags),
+// scales 2^122, codes 448, and the sum over any number of tokens stays inside
+// fp32.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "pda_kernels.cuh"
+#include "pda_prefix.h"
+
+namespace pda {
+
+template <int D, int FMT>
+struct PrefixCfg {
+    static constexpr int kT = prefix_tile_tokens(D);     // tokens of a tile
+    static constexpr int kStreams = prefix_streams(D);
+    static constexpr int kPart = 64;                     // scores of a row that a thread holds at a time
+    static constexpr int kSoftWarps = 4 * kStreams, kLoadWarps = 4;
+    static constexpr int kThreads = (kSoftWarps + kLoadWarps + 1) * 32;
+    static constexpr int kSlabs = D / 64;                // 64-column slabs, 128 bytes a row
+    static constexpr int kSlotBytes = kT * D * 2;        // K or V of a tile
+    static constexpr int kQTileBytes = 128 * D * 2;
+    static constexpr int kSlots = D == 64 ? 10 : FMT == kBf16 ? 5 : 4;
+    static constexpr int kScaleTiles = FMT == kBf16 ? 0 : kSlots / 2 + 2;  // ring of scales, [K | V][kT] a tile
+    static constexpr int kRW = kT / kLoadWarps;          // rows of a loader warp
+    // tensor memory: S of a stream, then O
+    static constexpr uint32_t kTmO = 256;
+    static_assert(kStreams * kT <= 256 && kStreams * D <= 256, "tensor memory columns");
+    // shared memory after the 1024-byte aligned base
+    static constexpr uint32_t kSlot0 = kStreams * kQTileBytes;
+    static constexpr uint32_t kScale0 = kSlot0 + kSlots * kSlotBytes;
+    static constexpr uint32_t kBars = kScale0 + kScaleTiles * kT * 8;
+    // full, empty [kSlots], landed [loader warp][kSlots] (8-bit), then the rest
+    static constexpr uint32_t kFull = kBars, kEmpty = kFull + 8 * kSlots, kLanded = kEmpty + 8 * kSlots;
+    static constexpr uint32_t kS = kLanded + 8 * kSlots * (FMT == kBf16 ? 0 : kLoadWarps), kP = kS + 16, kO = kP + 16,
+                              kQ = kO + 8, kSync = kQ + 8, kFin = kSync + 8, kTm = kFin + 8, kEnd = kTm + 16;
+    static constexpr uint32_t kSmem = kEnd + (1024 - 16);  // (dynamic shared memory starts on 16 bytes)
+    static_assert(kSmem <= 232448, "shared memory of an SM");
+};
+
+// One run of a CTA over token tiles of a unit.
+struct PrefixSegment {
+    int start;        // the group's first sequence
+    int rows;         // its q rows of a kv head
+    int tokens;       // of the prefix
+    int kvh, pair;
+    int j0, n;        // token tiles j0 .. j0 + n - 1
+    int64_t slot;     // of its state
+    bool dual;        // two q tiles
+};
+
+template <int D, int FMT>
+struct PrefixWalk {
+    using C = PrefixCfg<D, FMT>;
+    int64_t pos, end;
+    __device__ __forceinline__ explicit PrefixWalk(const PrefixParams& p) {
+        const int64_t W = p.groups[p.n_groups].work, P = prefix_plan_ctas(W, gridDim.x), c = blockIdx.x;
+        pos = c < P ? cta_begin(c, W, P) : 0;
+        end = c < P ? cta_begin(c + 1, W, P) : 0;
+    }
+    __device__ __forceinline__ bool next(const PrefixParams& p, PrefixSegment& s) {
+        if (pos >= end) return false;
+        int lo = 0, hi = p.n_groups - 1;  // the last group that starts at or before pos (groups without work precede)
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (p.groups[mid].work <= pos) lo = mid; else hi = mid - 1;
+        }
+        const PrefixGroup g = p.groups[lo];
+        const int rem = (int)pos - g.work, unit = rem / g.tiles;
+        s.start = g.start;
+        s.rows = (p.groups[lo + 1].start - g.start) * p.q_len * p.G;
+        s.tokens = g.blocks << p.lbs;
+        s.pair = unit / p.Hkv;
+        s.kvh = unit - s.pair * p.Hkv;
+        s.j0 = rem - unit * g.tiles;
+        s.n = min(g.tiles - s.j0, (int)(end - pos));
+        s.slot = (int64_t)g.unit + unit + blockIdx.x;
+        s.dual = C::kStreams == 2 && s.rows > (2 * s.pair + 1) * 128;
+        pos += s.n;
+        return true;
+    }
+};
+
+// The plan of the groups.  Every CTA writes all of it, the same values, so that
+// each reads its own stores and the decode that follows finds it.  Run by warp 0.
+template <int D, int FMT>
+__device__ __forceinline__ void prefix_plan(const PrefixParams& p, int lane) {
+    using C = PrefixCfg<D, FMT>;
+    int32_t top = 0, units = 0, work = 0;  // over the groups before
+    bool bad = false;
+    for (int g0 = 0; g0 <= p.n_groups; g0 += 32) {
+        const int g = g0 + lane;
+        int32_t s = p.B, blocks = 0;
+        if (g <= p.n_groups) {
+            s = p.starts ? p.starts[g] : g * (p.B / p.n_groups);
+            if (s < 0 || s > p.B) bad = true;
+            s = min(max(s, 0), p.B);
+        }
+        if (g < p.n_groups) {
+            blocks = p.shared[g];
+            if (blocks < 0 || blocks > p.table_stride) bad = true;
+            blocks = min(max(blocks, 0), p.table_stride);
+        }
+        int32_t m = s;  // starts that do not decrease
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t y = __shfl_up_sync(0xffffffffu, m, o);
+            if (lane >= o) m = max(m, y);
+        }
+        m = max(m, top);
+        if (g <= p.n_groups && m != s) bad = true;
+        int32_t e = __shfl_down_sync(0xffffffffu, m, 1);
+        if (lane == 31 && g < p.n_groups) {
+            const int32_t raw = p.starts ? p.starts[g + 1] : (g + 1) * (p.B / p.n_groups);
+            e = max(m, min(max(raw, 0), p.B));
+        }
+        const int32_t rows = g < p.n_groups ? (e - m) * p.q_len * p.G : 0;
+        PrefixGroup out;
+        out.start = m;
+        out.blocks = blocks;
+        out.pairs = (rows + 128 * C::kStreams - 1) / (128 * C::kStreams);
+        out.tiles = out.pairs > 0 ? (int32_t)((((int64_t)blocks << p.lbs) + C::kT - 1) / C::kT) : 0;
+        const int32_t u = out.tiles > 0 ? out.pairs * p.Hkv : 0, w = u * out.tiles;
+        int32_t us = u, wsum = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t a = __shfl_up_sync(0xffffffffu, us, o), b = __shfl_up_sync(0xffffffffu, wsum, o);
+            if (lane >= o) { us += a; wsum += b; }
+        }
+        out.unit = units + us - u;
+        out.work = work + wsum - w;
+        if (g <= p.n_groups) p.groups[g] = out;
+        top = __shfl_sync(0xffffffffu, m, 31);
+        units += __shfl_sync(0xffffffffu, us, 31);
+        work += __shfl_sync(0xffffffffu, wsum, 31);
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.err, PDA_DEVERR_BAD_LENGTH_);
+}
+
+// 16 bytes, or 16 zero bytes where !use.
+__device__ __forceinline__ void cp_async_16_or_0(uint32_t dst, const void* src, bool use) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(use ? 16 : 0) : "memory");
+}
+
+// Four codes as bf16, which holds them exactly.
+template <int FMT>
+__device__ __forceinline__ void codes_to_bf16(uint32_t x, uint32_t& lo, uint32_t& hi) {
+    uint32_t a, b;
+    if constexpr (FMT == kE4m3) {
+        a = e4m3x2_to_f16x2((uint16_t)x);
+        b = e4m3x2_to_f16x2((uint16_t)(x >> 16));
+    } else {
+        // the byte under 0x64 reads as 1024 + code + 128
+        const uint32_t u = x ^ 0x80808080u, c = 0x64806480u;
+        asm("sub.f16x2 %0, %1, %2;" : "=r"(a) : "r"(__byte_perm(u, 0x64646464u, 0x4140)), "r"(c));
+        asm("sub.f16x2 %0, %1, %2;" : "=r"(b) : "r"(__byte_perm(u, 0x64646464u, 0x4342)), "r"(c));
+    }
+    const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&a));
+    const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&b));
+    lo = pack_bf16x2(fa.x, fa.y);
+    hi = pack_bf16x2(fb.x, fb.y);
+}
+
+// ------------------------------------------------------------------ loaders
+
+template <int D, int FMT>
+__device__ __forceinline__ void prefix_load(const PrefixParams& p, uint32_t base, volatile int* abort_flag, int w, int lane) {
+    using C = PrefixCfg<D, FMT>;
+    constexpr int RW = C::kRW, ES = FMT == kBf16 ? 2 : 1;  // rows of this warp; bytes of an element
+    constexpr int CH = D * ES / 16, RPI = 32 / CH;         // 16-byte chunks of a row; rows of an instruction
+    static_assert(RPI >= 1 && RW % RPI == 0 && RW <= 32, "rows of a warp");
+    PrefixWalk<D, FMT> walk(p);
+    PrefixSegment s = {};
+    int j = 0, left = 0;  // tiles of the segment
+    // the next tile's rows: lane r holds row r of this warp (element offset, or -1), and its scales
+    int64_t off = -1;
+    float ks = 0.f, vs = 0.f;
+    auto rows_of = [&](int tile) {
+        off = -1;
+        ks = vs = 0.f;
+        const int64_t t = (int64_t)tile * C::kT + w * RW + lane;
+        if (lane < RW && t < s.tokens) {
+            const int32_t id = p.table[(int64_t)s.start * p.table_stride + (t >> p.lbs)];
+            const int slot = (int)t & ((1 << p.lbs) - 1);
+            if (id < 0 || (int64_t)id >= p.num_blocks) {
+                atomicOr(p.err, PDA_DEVERR_BAD_BLOCK_ID_);
+                return;
+            }
+            off = (int64_t)id * p.blk_s + (int64_t)slot * p.tok_s + (int64_t)s.kvh * p.kvh_s;
+            if constexpr (FMT != kBf16) {
+                const float* sc = p.scales + (((((int64_t)id * p.Hkv + s.kvh) * 2) << p.lbs) + slot);
+                ks = sc[0];
+                vs = sc[(int64_t)1 << p.lbs];
+            }
+        }
+    };
+    auto advance = [&]() {  // to the next tile; false at the end
+        if (left == 0) {
+            if (!walk.next(p, s)) return false;
+            j = s.j0;
+            left = s.n;
+        } else {
+            ++j;
+        }
+        --left;
+        rows_of(j);
+        return true;
+    };
+    const int chunk = lane % CH, sub = lane / CH;
+    uint32_t issued = 0, spread = 0, tiles = 0;  // slots filled, slots converted (8-bit), tiles begun
+    int64_t now = -1;                            // the current tile's rows
+    // (8-bit) codes in their slot: the warp's rows back to back over its parts of the slabs
+    auto code_at = [&](uint32_t slot, int o) {
+        return slot + (uint32_t)(o / (RW * 128)) * (C::kT * 128) + (uint32_t)(w * RW * 128 + o % (RW * 128));
+    };
+    auto fill = [&](uint32_t n) {  // slot number n, its K or V
+        const uint32_t slot = base + C::kSlot0 + (n % C::kSlots) * C::kSlotBytes;
+        const uint8_t* pool = (n & 1) ? p.v_base : p.k_base;
+#pragma unroll 4
+        for (int r0 = 0; r0 < RW; r0 += RPI) {
+            const int r = r0 + sub;
+            const int64_t o = __shfl_sync(0xffffffffu, now, r);
+            uint32_t dst;
+            if constexpr (FMT == kBf16) {
+                const int t = w * RW + r;
+                dst = slot + (uint32_t)(chunk >> 3) * (C::kT * 128) + (uint32_t)t * 128 + (uint32_t)(((chunk & 7) ^ (t & 7)) << 4);
+            } else {
+                dst = code_at(slot, r * D + chunk * 16);
+            }
+            cp_async_16_or_0(dst, pool + (o < 0 ? 0 : o * ES) + chunk * 16, o >= 0);
+        }
+        if constexpr (FMT == kBf16) cp_async_mbar_arrive_noinc(base + C::kFull + 8 * (n % C::kSlots));
+        else cp_async_mbar_arrive_noinc(base + C::kLanded + 8 * (w * C::kSlots + n % C::kSlots));
+    };
+    auto convert = [&](uint32_t n) {
+        if constexpr (FMT != kBf16) {
+            const uint32_t slot = base + C::kSlot0 + (n % C::kSlots) * C::kSlotBytes;
+            constexpr int N = RW * D / 16 / 32;  // 16-code chunks of a lane
+            uint32_t x[N][4];
+#pragma unroll
+            for (int i = 0; i < N; ++i) lds_v4(code_at(slot, (lane + 32 * i) * 16), x[i]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int at = lane + 32 * i, t = w * RW + at / CH, c = 2 * (at % CH);  // row, first 8-column chunk
+                const uint32_t row = slot + (uint32_t)(c >> 3) * (C::kT * 128) + (uint32_t)t * 128;
+                uint32_t y[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) codes_to_bf16<FMT>(x[i][k], y[2 * k], y[2 * k + 1]);
+                sts_v4(row + (uint32_t)(((c & 7) ^ (t & 7)) << 4), y[0], y[1], y[2], y[3]);
+                sts_v4(row + (uint32_t)((((c & 7) + 1) ^ (t & 7)) << 4), y[4], y[5], y[6], y[7]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(base + C::kFull + 8 * (n % C::kSlots));
+        }
+    };
+    bool ok = true, more = advance();
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (warp_wait(bar, parity)) return true;
+        atomicOr(p.err, PDA_DEVERR_TIMEOUT_);
+        *abort_flag = 1;
+        return false;
+    };
+    while (ok && (more || (issued & 1) || spread < issued)) {
+        if (__any_sync(0xffffffffu, *abort_flag)) break;
+        bool can = more || (issued & 1);
+        const uint32_t empty = base + C::kEmpty + 8 * (issued % C::kSlots), parity = ((issued / C::kSlots) & 1u) ^ 1u;
+        if (can && FMT != kBf16 && spread < issued) can = __all_sync(0xffffffffu, mbar_test_wait(empty, parity));
+        if (can) {
+            if (!(ok = wait(empty, parity))) break;
+            if (!(issued & 1)) {  // K, the tile's first half
+                now = off;
+                if constexpr (FMT != kBf16) {
+                    if (lane < RW) {
+                        const uint32_t sc = base + C::kScale0 + (tiles % C::kScaleTiles) * (C::kT * 8) + (uint32_t)(w * RW + lane) * 4;
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc), "f"(ks) : "memory");
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc + C::kT * 4), "f"(vs * 9.094947e-13f) : "memory");  // 2^-40
+                    }
+                }
+                ++tiles;
+                more = advance();
+            }
+            fill(issued);
+            ++issued;
+            if (FMT == kBf16) spread = issued;
+        } else {
+            if (!(ok = wait(base + C::kLanded + 8 * (w * C::kSlots + spread % C::kSlots), (spread / C::kSlots) & 1u))) break;
+            convert(spread);
+            ++spread;
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// ------------------------------------------------------------------ products
+
+template <int D, int FMT>
+__device__ __forceinline__ void prefix_mma(const PrefixParams& p, uint32_t base, volatile int* abort_flag, uint32_t tmem) {
+    using C = PrefixCfg<D, FMT>;
+    constexpr uint32_t idS = umma_idesc_bf16(128, C::kT, false), idO = umma_idesc_bf16(128, D, true);
+    PrefixWalk<D, FMT> walk(p);
+    PrefixSegment s;
+    uint32_t tile0 = 0, segs = 0, p_phase = 0;  // p_phase: bit per stream
+    bool ok = true;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (*abort_flag == 0 && mbar_wait_bounded(bar, parity, kWaitLimitNs)) return true;
+        if (*abort_flag == 0) atomicOr(p.err, PDA_DEVERR_TIMEOUT_);
+        *abort_flag = 1;
+        return ok = false;
+    };
+    while (ok && walk.next(p, s)) {
+        const int items = s.dual ? 2 * s.n : s.n;
+        if (!wait(base + C::kQ, segs & 1u)) break;
+        ++segs;
+        auto first_of = [&](int k) { return !s.dual || (k & 1) == 0; };
+        auto last_of = [&](int k) { return !s.dual || (k & 1) == 1; };
+        auto qk = [&](int k) {
+            const uint32_t n = 2 * (tile0 + (s.dual ? k >> 1 : k)), slot = n % C::kSlots;
+            if (first_of(k) && !wait(base + C::kFull + 8 * slot, (n / C::kSlots) & 1u)) return;
+            fence_proxy_async_smem();  // the loaders' cp.async writes
+            tc_fence_after();
+            const int st = C::kStreams == 2 ? k & 1 : 0;
+            const uint32_t sQ = base + (s.dual ? st : 0) * C::kQTileBytes, sK = base + C::kSlot0 + slot * C::kSlotBytes;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+                umma_bf16_ss(tmem + st * C::kT, umma_sdesc(sQ + (ks >> 2) * (128 * 128) + (ks & 3) * 32, 16, 1024),
+                             umma_sdesc(sK + (ks >> 2) * (C::kT * 128) + (ks & 3) * 32, 16, 1024), idS, ks > 0);
+            umma_commit(base + C::kS + 8 * st);
+            if (last_of(k)) umma_commit(base + C::kEmpty + 8 * slot);
+        };
+        for (int k = 0; ok && k < min(C::kStreams, items); ++k) qk(k);
+        for (int k = 0; ok && k < items; ++k) {
+            const int st = C::kStreams == 2 ? k & 1 : 0;
+            const uint32_t n = 2 * (tile0 + (s.dual ? k >> 1 : k)) + 1, slot = n % C::kSlots;
+            if (!wait(base + C::kP + 8 * st, (p_phase >> st) & 1u)) break;
+            p_phase ^= 1u << st;
+            if (first_of(k) && !wait(base + C::kFull + 8 * slot, (n / C::kSlots) & 1u)) break;
+            fence_proxy_async_smem();
+            tc_fence_after();
+            const uint32_t sV = base + C::kSlot0 + slot * C::kSlotBytes, tP = tmem + st * C::kT;
+            const uint32_t tO = tmem + C::kTmO + st * D;
+            bool acc = k >= C::kStreams;
+#pragma unroll 4
+            for (int ks = 0; ks < C::kT / 16; ++ks) {
+                const uint64_t v = umma_sdesc(sV + 2048 * ks, C::kT * 128, 1024);
+                const uint32_t part = tP + ks / (C::kPart / 16) * C::kPart + ks % (C::kPart / 16) * 8;
+                umma_bf16_ts(tO, part, v, idO, acc);
+                umma_bf16_ts(tO, part + C::kPart / 2, v, idO, true);
+                acc = true;
+            }
+            if (last_of(k)) umma_commit(base + C::kEmpty + 8 * slot);
+            if (k == items - 1) umma_commit(base + C::kO);
+            if (k + C::kStreams < items) qk(k + C::kStreams);
+        }
+        tile0 += s.n;
+    }
+    // every product has completed before the tensor memory is freed
+    umma_commit(base + C::kFin);
+    if (!mbar_wait_bounded(base + C::kFin, 0, kWaitLimitNs)) atomicOr(p.err, PDA_DEVERR_TIMEOUT_);
+}
+
+// ------------------------------------------------------------------ softmax
+
+template <int N>
+__device__ __forceinline__ void tmem_ld_row(uint32_t taddr, float (&v)[N]) {
+#pragma unroll
+    for (int c = 0; c < N; c += 16) {
+        uint32_t* r = reinterpret_cast<uint32_t*>(v) + c;
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+              "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(taddr + c)
+            : "memory");
+    }
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    // (no use of the loaded registers moves ahead of the wait)
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_st_row(uint32_t taddr, const float (&v)[N]) {
+#pragma unroll
+    for (int c = 0; c < N; c += 16) tmem_st16(taddr + c, *reinterpret_cast<const float(*)[16]>(v + c));
+}
+
+template <int D, int FMT>
+__device__ __forceinline__ void prefix_softmax(const PrefixParams& p, uint32_t base, uint8_t* smem, volatile int* abort_flag,
+                                               uint32_t tmem, int warp, int lane) {
+    using C = PrefixCfg<D, FMT>;
+    constexpr int kT = C::kT, kPart = C::kPart;
+    constexpr float kBack = FMT == kBf16 ? 1.f : 1.0995116e12f;  // 2^40
+    const int st = warp >> 2, w = warp & 3, row = 32 * w + lane;
+    const uint32_t tl = tmem + ((uint32_t)(32 * w) << 16), tS = tl + st * kT;
+    float* ml = reinterpret_cast<float*>(smem);  // [stream][2][128], over the q rows once they are used
+    PrefixWalk<D, FMT> walk(p);
+    PrefixSegment s;
+    Scoring sc = {};
+    sc.cap = p.cap;
+    sc.inv_cap = p.inv_cap;
+    const bool plain = p.cap == 0.f && p.slopes == nullptr;
+    uint32_t tile0 = 0, segs = 0, s_phase = 0, cphase = 0;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (warp_wait(bar, parity)) return true;
+        atomicOr(p.err, PDA_DEVERR_TIMEOUT_);
+        *abort_flag = 1;
+        return false;
+    };
+    auto sync_all = [&]() {
+        const bool ok = consumer_sync(base + C::kSync, cphase, p.err, abort_flag);
+        return __all_sync(0xffffffffu, ok ? 1 : 0) != 0;
+    };
+    while (walk.next(p, s)) {
+        if (__any_sync(0xffffffffu, *abort_flag)) return;
+        const int tile = s.pair * C::kStreams + (s.dual ? st : 0);
+        // the segment's q rows, in the swizzle of the products' operand: a
+        // stream its own tile, or both streams one
+        {
+            const int threads = s.dual ? 128 : 128 * C::kStreams, t0 = s.dual ? row : warp * 32 + lane;
+            const uint32_t sQ = base + (s.dual ? st : 0) * C::kQTileBytes;
+            for (int i = t0; i < 128 * (D / 8); i += threads) {
+                const int r = i / (D / 8), c = i % (D / 8), g = tile * 128 + r;
+                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                if (g < s.rows) {
+                    const int bq = g / p.G, h = g - bq * p.G;
+                    x = *reinterpret_cast<const uint4*>(
+                        p.q + (((int64_t)s.start * p.q_len + bq) * p.Hq + s.kvh * p.G + h) * D + c * 8);
+                }
+                sts_v4(sQ + (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), x.x, x.y, x.z, x.w);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(base + C::kQ);
+        }
+        // this thread's q row: how much of the prefix it sees, and its bias
+        const int g = tile * 128 + row;
+        int vis = 0, own = 0;
+        float slope = 0.f;
+        if (g < s.rows) {
+            const int bq = g / p.G, h = g - bq * p.G, b = bq / p.q_len, qi = bq - b * p.q_len;
+            own = max(p.lens[s.start + b], 0) - p.q_len + qi;
+            vis = min(max(own + 1, 0), s.tokens);
+            if (p.slopes) slope = p.slopes[s.kvh * p.G + h] * 1.4426950408889634f;
+        }
+        const bool idle = tile * 128 + 32 * w >= s.rows;  // a warp without rows
+        const int items = s.dual ? 2 * s.n : s.n;
+        float m = kNegInf, l = 0.f;
+        for (int k = st; k < items; k += C::kStreams) {
+            const int jj = s.dual ? k >> 1 : k;
+            if (!wait(base + C::kS + 8 * st, s_phase & 1u)) return;
+            ++s_phase;
+            tc_fence_after();
+            if (!idle) {
+                const int t0 = (s.j0 + jj) * kT, seen = vis - t0;  // the tile's first token; tokens of it in sight
+                const float* kscale = nullptr;
+                if constexpr (FMT != kBf16) {
+                    // (the scales are there once V is: V's slot stays until this row's P is read)
+                    const uint32_t n = 2 * (tile0 + jj) + 1;
+                    if (!wait(base + C::kFull + 8 * (n % C::kSlots), (n / C::kSlots) & 1u)) return;
+                    kscale = reinterpret_cast<const float*>(smem + C::kScale0) + ((tile0 + jj) % C::kScaleTiles) * (2 * kT);
+                }
+                // the row's largest score, a part of the row at a time; scores that
+                // are more than a product go back to tensor memory for the second pass
+                const bool bare = FMT == kBf16 && plain && !__any_sync(0xffffffffu, seen < kT);
+                const float f = bare ? p.scale_log2 : 1.f;
+                float top = kNegInf;
+#pragma unroll
+                for (int c = 0; c < kT; c += kPart) {
+                    float v[kPart];
+                    tmem_ld_row(tS + c, v);
+                    if (bare) {
+#pragma unroll
+                        for (int i = 0; i < kPart; ++i) top = fmaxf(top, v[i] * f);
+                        continue;
+                    }
+#pragma unroll
+                    for (int i = 0; i < kPart; i += 4) {
+                        float4 x = make_float4(1.f, 1.f, 1.f, 1.f);
+                        if constexpr (FMT != kBf16) x = *reinterpret_cast<const float4*>(kscale + c + i);
+                        v[i] *= x.x * p.scale_log2;
+                        v[i + 1] *= x.y * p.scale_log2;
+                        v[i + 2] *= x.z * p.scale_log2;
+                        v[i + 3] *= x.w * p.scale_log2;
+                    }
+                    if (!plain) {
+                        const float far = (float)(t0 + c - own);
+#pragma unroll
+                        for (int i = 0; i < kPart; ++i) v[i] = score_of(sc, v[i], slope, far + (float)i);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kPart; ++i) {
+                        if (c + i >= seen) v[i] = kNegInf;
+                        top = fmaxf(top, v[i]);
+                    }
+                    tmem_st_row(tS + c, v);
+                }
+                tmem_wait_st();
+                // lazy reference (kLazyLog2); this stream's last product with V is
+                // done: it was issued before this S
+                const bool up = top > m + kLazyLog2, scale_o = up && m != kNegInf;
+                if (__any_sync(0xffffffffu, scale_o)) {
+                    const float a = scale_o ? ex2(m - top) : 1.f;
+                    l *= a;
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        float o[16];
+                        tmem_ld16(tl + C::kTmO + st * D + c, o);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] *= a;
+                        tmem_st16(tl + C::kTmO + st * D + c, o);
+                    }
+                }
+                if (up) m = top;
+                const float u = m == kNegInf ? 0.f : m;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < kT; c += kPart) {  // P over its own part of S: high parts, low parts
+                    float v[kPart];
+                    tmem_ld_row(tS + c, v);
+#pragma unroll
+                    for (int e = 0; e < kPart; e += 32) {
+                        uint32_t hi[16], lo[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float p0 = ex2(fmaf(v[e + 2 * i], f, -u)), p1 = ex2(fmaf(v[e + 2 * i + 1], f, -u));
+                            sum[i & 3] += p0 + p1;
+                            if constexpr (FMT != kBf16) {
+                                const float2 x = *reinterpret_cast<const float2*>(kscale + kT + c + e + 2 * i);
+                                p0 *= x.x;
+                                p1 *= x.y;
+                            }
+                            hi[i] = pack_bf16x2(p0, p1);
+                            lo[i] = pack_bf16x2(p0 - bf16_lo(hi[i]), p1 - bf16_hi(hi[i]));
+                        }
+                        tmem_st16u(tS + c + e / 2, hi);
+                        tmem_st16u(tS + c + kPart / 2 + e / 2, lo);
+                    }
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_wait_st();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(base + C::kP + 8 * st);
+        }
+        // ---- the segment's end: every product of it is done
+        if (!wait(base + C::kO, segs & 1u)) return;
+        ++segs;
+        tile0 += s.n;
+        tc_fence_after();
+        const bool joined = C::kStreams == 2 && !s.dual;
+        float f0 = 1.f, f1 = 0.f;
+        bool two = false;
+        if (joined) {  // the streams' states of the same rows
+            ml[st * 256 + row] = m;
+            ml[st * 256 + 128 + row] = l;
+            if (!sync_all()) return;
+            two = items > 1;
+            const float m0 = ml[row], m1 = two ? ml[256 + row] : kNegInf;
+            m = fmaxf(m0, m1);
+            f0 = m0 == kNegInf ? 0.f : ex2(m0 - m);
+            f1 = m1 == kNegInf ? 0.f : ex2(m1 - m);
+            l = ml[128 + row] * f0 + (two ? ml[256 + 128 + row] * f1 : 0.f);
+        }
+        if (!idle) {
+            const int64_t at = s.slot * C::kStreams + (s.dual ? st : 0);
+            const int c0 = joined ? st * (D / 2) : 0, c1 = joined ? c0 + D / 2 : D;
+            const uint32_t tO = tl + C::kTmO + (joined ? 0 : st * D);
+#pragma unroll 1
+            for (int c = c0; c < c1; c += 16) {
+                float o[16], x[16];
+                tmem_ld16(tO + c, o);
+                if (two) tmem_ld16(tO + D + c, x);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    o[i] = (o[i] * f0 + (two ? x[i] * f1 : 0.f)) * kBack;
+                    if (m == kNegInf) o[i] = 0.f;  // a row that sees none of these tokens
+                }
+                if (g < s.rows) {
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4)
+                        reinterpret_cast<float4*>(p.part_o)[(at * (D / 4) + (c + i) / 4) * 128 + row] =
+                            make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                }
+            }
+            if (g < s.rows && (!joined || st == 0))
+                reinterpret_cast<float2*>(p.part_ml)[at * 128 + row] = make_float2(m, l);
+        }
+        tc_fence_before();
+        if (!sync_all()) return;  // both streams have read both states
+    }
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(PrefixCfg<D, FMT>::kThreads, 1) prefix_kernel(const __grid_constant__ PrefixParams p) {
+    using C = PrefixCfg<D, FMT>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int abort_flag;
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kSlots; ++i) {
+            mbar_init(base + C::kFull + 8 * i, FMT == kBf16 ? C::kLoadWarps * 32 : C::kLoadWarps);
+            mbar_init(base + C::kEmpty + 8 * i, 1);
+        }
+        if (FMT != kBf16)
+            for (int i = 0; i < C::kSlots * C::kLoadWarps; ++i) mbar_init(base + C::kLanded + 8 * i, 32);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(base + C::kS + 8 * i, 1);
+            mbar_init(base + C::kP + 8 * i, 4);
+        }
+        mbar_init(base + C::kO, 1);
+        mbar_init(base + C::kQ, C::kSoftWarps);
+        mbar_init(base + C::kSync, C::kSoftWarps * 32);
+        mbar_init(base + C::kFin, 1);
+        fence_mbar_init();
+        abort_flag = 0;
+    }
+    constexpr int kMmaWarp = C::kSoftWarps + C::kLoadWarps;
+    if (warp == kMmaWarp) {
+        tmem_alloc(base + C::kTm, 512);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    if (warp == 0) prefix_plan<D, FMT>(p, lane);
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + C::kTm);
+    if (warp < C::kSoftWarps) {
+        prefix_softmax<D, FMT>(p, base, smem, &abort_flag, tmem, warp, lane);
+        tc_fence_before();
+    } else if (warp < kMmaWarp) {
+        prefix_load<D, FMT>(p, base, &abort_flag, warp - C::kSoftWarps, lane);
+    } else {
+        if (lane == 0) prefix_mma<D, FMT>(p, base, &abort_flag, tmem);
+        __syncwarp();
+    }
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D, int FMT>
+PrefixShape prefix_shape_as() {
+    using C = PrefixCfg<D, FMT>;
+    return {reinterpret_cast<const void*>(&prefix_kernel<D, FMT>), C::kThreads, (int)C::kSmem};
+}
+template <int D>
+PrefixShape prefix_shape_of(int format) {
+    return format == kBf16 ? prefix_shape_as<D, kBf16>() : format == kE4m3 ? prefix_shape_as<D, kE4m3>() : prefix_shape_as<D, kInt8>();
+}
+
+template <int D, int FMT>
+cudaError_t launch_prefix_as(const PrefixParams& p, int ctas, cudaStream_t stream) {
+    using C = PrefixCfg<D, FMT>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas, 1, 1);
+    cfg.blockDim = dim3(C::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, prefix_kernel<D, FMT>, p);
+}
+template <int D>
+cudaError_t launch_prefix_of(int format, const PrefixParams& p, int ctas, cudaStream_t stream) {
+    return format == kBf16   ? launch_prefix_as<D, kBf16>(p, ctas, stream)
+           : format == kE4m3 ? launch_prefix_as<D, kE4m3>(p, ctas, stream)
+                             : launch_prefix_as<D, kInt8>(p, ctas, stream);
+}
+
+}  // namespace pda

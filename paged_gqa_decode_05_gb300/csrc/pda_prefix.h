@@ -1,0 +1,44 @@
+// pda_prefix.h -- the kernel that walks the prefix a group of sequences
+// shares, once for all their queries (pda_prefix.cuh): parameters, plan
+// limits and launch entry points.
+#pragma once
+
+#include "pda_cache.h"
+#include "pda_params.h"
+
+namespace pda {
+
+struct PrefixParams {
+    const uint16_t* q;          // [B, q_len, Hq, D] bf16
+    const uint8_t* k_base;      // pools, elements of the cache's format
+    const uint8_t* v_base;
+    const float* scales;        // [num_blocks, Hkv, 2, bs]; 8-bit formats
+    int64_t blk_s, tok_s, kvh_s, num_blocks;
+    const int32_t* table;       // [B, table_stride]
+    const int32_t* lens;        // [B]
+    const int32_t* shared;      // [n_groups] blocks
+    const int32_t* starts;      // [n_groups + 1] or null: B / n_groups sequences each
+    PrefixGroup* groups;        // [n_groups + 1] out
+    float* part_o;              // [slots][streams][D / 4][128][4]
+    float* part_ml;             // [slots][streams][128][2]
+    uint32_t* err;
+    int32_t table_stride, lbs;
+    int32_t B, q_len, Hq, Hkv, G, n_groups;
+    float scale_log2, cap, inv_cap;
+    const float* slopes;
+};
+
+struct PrefixShape {
+    const void* fn;
+    int threads, smem;
+};
+PrefixShape prefix_shape(int D, int format);
+cudaError_t launch_prefix(int D, int format, const PrefixParams& p, int ctas, cudaStream_t stream);
+
+// Units of a call at most: pairs of q tiles (single ones at head size 256) per
+// kv head, one more for every group whose rows do not fill their last.
+PDA_HD int64_t prefix_units(int D, int64_t rows, int64_t groups, int64_t Hkv) {
+    return Hkv * (rows / (128 * prefix_streams(D)) + groups);
+}
+
+}  // namespace pda

@@ -438,7 +438,7 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
     using C = QuantCfg<D, NT>;
     constexpr int S = C::kStages, RT = C::kRT, K = C::kK;
     constexpr int kThreadsC = C::kWarps * 32, kOStride = D + 4;
-    constexpr bool MQ = is_multi(MODE), kHide = MQ && FMT == kE4m3;
+    constexpr bool MQ = is_multi(MODE), kHide = MQ && FMT == kE4m3, kExt = MODE == kScored;
     const uint32_t full0 = base_s + L.bars, empty0 = full0 + 8 * S;
     const int g = lane >> 2, t = lane & 3;
     // warps 0 .. kRW - 1 take the first eight q rows, the next kRW the others, all of a stage's KV rows
@@ -479,6 +479,7 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
 
     float o[2 * K][4];
     uint32_t qf[K][4];
+    float slope[2] = {0.f, 0.f};  // of the lane's two columns (kExt)
     float f[2] = {0.f, 0.f}, m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 2 * K; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -493,7 +494,7 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
     uint32_t phase = 0;
     int32_t ticket = 0;
     const int ct = warp * 32 + lane;
-    zero_empty_rows<D, kThreadsC>(p, pfx, ct);
+    zero_empty_rows<D, kThreadsC, kExt>(p, pfx, ct);
 
     while (true) {
         if (*abort_flag) break;
@@ -525,6 +526,10 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
             f[1] = q_back[8 * tile + 2 * t + 1];
             m[0] = m[1] = kNegInf;
             l[0] = l[1] = 0.f;
+            if constexpr (kExt) {
+                slope[0] = column_slope(p, md, 2 * t);
+                slope[1] = column_slope(p, md, 2 * t + 1);
+            }
             if constexpr (kHide) notes->cols[ct] = 0;
 #pragma unroll
             for (int i = 0; i < 2 * K; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -589,9 +594,25 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
                 }
                 // x: the score in base-2 units plus log2 of the row's V scale
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    x[r][i] = fmaf(FMT == kE4m3 ? fmaf(acc[1][i], 1.f / kLowPart, acc[0][i]) : acc[0][i] + acc[1][i],
-                                   ks[r][i >> 1] * f[i & 1], lv[r][i >> 1]);
+                for (int i = 0; i < 4; ++i) {
+                    const float dot = FMT == kE4m3 ? fmaf(acc[1][i], 1.f / kLowPart, acc[0][i]) : acc[0][i] + acc[1][i];
+                    if constexpr (kExt) {  // the score on its own first
+                        const int far = md.j0 * p.bs + r0 + 16 * r + 8 * (i >> 1) + g - md.lim - qc[i & 1];
+                        x[r][i] = score_of(p.sc, dot * (ks[r][i >> 1] * f[i & 1]), slope[i & 1], (float)far);
+                    } else {
+                        x[r][i] = fmaf(dot, ks[r][i >> 1] * f[i & 1], lv[r][i >> 1]);
+                    }
+                }
+                if constexpr (kExt) {
+#pragma unroll
+                    for (int i = 0; i < 4; i += 2) {
+                        const int at = r0 + 16 * r + 8 * (i >> 1) + g, far = md.j0 * p.bs + at - md.lim;
+                        if (p.sc.scores && at < md.n_valid)
+                            put_scores(p, md, at, 2 * t, far > qc[0] ? kNegInf : x[r][i], far > qc[1] ? kNegInf : x[r][i + 1]);
+                        x[r][i] += lv[r][i >> 1];
+                        x[r][i + 1] += lv[r][i >> 1];
+                    }
+                }
             }
             if (partial) {
 #pragma unroll
@@ -714,7 +735,7 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
             // one copy of the merge's code for both tiles: code that runs once a unit is fetched cold
 #pragma unroll 1
             for (int n = 0; n < NT && 8 * n < me.nr; ++n) {
-                if (!rows_tile_merge<D, kThreadsC, 8, true>(
+                if (!rows_tile_merge<D, kThreadsC, 8, true, kExt>(
                         p, me, n, ct, ticket, pc, grs, ri,
                         UnitSlices<D, C::kRW>{st_m, st_l, st_o + (size_t)n * C::kRW * 8 * kOStride}, st_role, cbar, cphase,
                         abort_flag, role)) {
@@ -772,7 +793,7 @@ __global__ void __maxnreg__(168) quant_split_kernel(const __grid_constant__ Quan
     }
     pdl_wait_primary();
     pdl_launch_dependents();
-    const int32_t nv_max = build_prefix<is_multi(MODE), C::kMainThreads>(p, pfx, scan);
+    const int32_t nv_max = build_prefix<MODE, C::kMainThreads>(p, pfx, scan);
     int64_t begin, end;
     int64_t ctas = gridDim.x;
     const bool by_unit = unit_mode((int64_t)p.B * p.Hkv, ctas, real_blocks(nv_max, p.unit_cost), C::kST, p.bs);
