@@ -183,25 +183,12 @@ __device__ __forceinline__ int32_t tokens_of(const SplitParams& p, int s, int32_
     return len < 0 ? 0 : len;
 }
 
-// The group that launch sequence b (of the launch) belongs to, or -1 (kScored;
-// groups' starts do not decrease, empty ones stand before the one they equal).
-__device__ __forceinline__ int group_of_seq(const Scoring& sc, int b) {
-    if (sc.groups == nullptr) return -1;
-    b += sc.seq0;
-    int lo = 0, hi = sc.n_groups;
-    while (lo < hi) {  // the first entry whose start is past b
-        const int mid = (lo + hi) >> 1;
-        if (__ldcg(&sc.groups[mid].start) <= b) lo = mid + 1; else hi = mid;
-    }
-    return lo > 0 && b < __ldcg(&sc.groups[sc.n_groups].start) ? lo - 1 : -1;
-}
-
-// Blocks of launch row s that the walk leaves out: those that its group shares.
+// Blocks of launch row s that the walk leaves out (kScored): those that its group shares.
 template <int MODE>
 __device__ __forceinline__ int32_t skip_of(const SplitParams& p, int s) {
     if constexpr (MODE != kScored) return 0;
-    const int g = group_of_seq(p.sc, row_info<is_multi(MODE)>(p, s).b);
-    return g < 0 ? 0 : __ldcg(&p.sc.groups[g].blocks);
+    if (p.sc.seqs == nullptr) return 0;
+    return __ldcg(&p.sc.seqs[p.sc.seq0 + row_info<is_multi(MODE)>(p, s).b].blocks);
 }
 
 // Blocks of sequence b with length entry L, validated and clamped (flags
@@ -746,17 +733,16 @@ __device__ __forceinline__ void merge_state(float& M, float& Ls, float4& Os, flo
 
 // ---- kScored: scores capped and biased, and the states of a shared prefix
 
-// A score in base-2 units, capped to cap * tanh(s / cap) and with slope * far
-// added (far: the token's place less the query's).  tanh from its definition,
-// (1 - e) / (1 + e) with e = exp(-2 |s| / cap): off by a few 2^-24 of the cap
-// for any s, where the hardware's tanh is off by 2^-11 of it (0.02 in the
-// exponent at a cap of 50).
+// cap * tanh(s / cap), s in base-2 units, from the definition, 1 - 2 / (1 + e)
+// with e = exp(2 s / cap): off by a few 2^-24 of the cap for any s, where the
+// hardware's tanh is off by 2^-11 of it (0.02 in the exponent at a cap of 50).
+__device__ __forceinline__ float capped(const Scoring& sc, float s) {
+    return fmaf(-2.f * sc.cap, rcp_approx(1.f + ex2(s * sc.inv_cap)), sc.cap);
+}
+// A score in base-2 units, capped and with slope * far added (far: the token's
+// place less the query's).
 __device__ __forceinline__ float score_of(const Scoring& sc, float s, float slope, float far) {
-    if (sc.cap != 0.f) {
-        const float e = ex2(fabsf(s) * sc.inv_cap * -2.885390082f);  // -2 log2 e
-        s = copysignf(__fdividef(sc.cap * (1.f - e), 1.f + e), s);
-    }
-    return fmaf(slope, far, s);
+    return fmaf(slope, far, sc.cap != 0.f ? capped(sc, s) : s);
 }
 
 // The slope of score column `col` of a segment (base-2 units).
@@ -777,49 +763,51 @@ __device__ __forceinline__ void put_scores(const SplitParams& p, const StageMeta
     }
 }
 
+// The shared prefix of sequence b of the launch (from L2: the prefix kernel has
+// just written it).
+__device__ __forceinline__ PrefixSeq prefix_of(const SplitParams& p, int b) {
+    PrefixSeq ps = {};
+    if (p.sc.seqs) {
+        const int4* at = reinterpret_cast<const int4*>(p.sc.seqs + p.sc.seq0 + b);
+        const int4 x = __ldcg(at), y = __ldcg(at + 1);
+        ps = {x.x, x.y, x.z, x.w, y.x, y.y, {0, 0}};
+    }
+    return ps;
+}
+
 // Joins the state of an output row's shared prefix, which the prefix kernel
 // left in pieces, to (M, Ls, Os), columns d4 .. d4 + 3; and hands out the
 // row's (m, l).  Row r of a q tile and chunk d4 / 4 of it lie at [chunk][r].
 template <int D, bool kWide>
-__device__ __forceinline__ void join_prefix(const SplitParams& p, int b, int qi, int head, int d4, float& M, float& Ls,
-                                            float4& Os) {
+__device__ __forceinline__ void join_prefix(const SplitParams& p, const PrefixSeq& ps, int b, int qi, int head, int d4,
+                                            float& M, float& Ls, float4& Os) {
     const Scoring& sc = p.sc;
-    const int g = group_of_seq(sc, b);
-    if (g >= 0) {
-        const PrefixGroup* at = sc.groups + g;  // (read from L2: the prefix kernel has just written it)
-        PrefixGroup pg;
-        pg.start = __ldcg(&at->start);
-        pg.tiles = __ldcg(&at->tiles);
-        pg.unit = __ldcg(&at->unit);
-        pg.work = __ldcg(&at->work);
-        if (pg.tiles > 0) {
-            constexpr int kSub = prefix_streams(D);  // q tiles of a slot
-            const int kvh = head / p.G;
-            const int row = ((b + sc.seq0 - pg.start) * p.q_len + qi) * p.G + head - kvh * p.G;
-            const int tile = row >> 7, r = row & 127;
-            const int64_t W = __ldcg(&sc.groups[sc.n_groups].work), P = prefix_plan_ctas(W, sc.prefix_ctas);
-            const int unit = tile / kSub * p.Hkv + kvh;
-            const int64_t first = pg.work + (int64_t)unit * pg.tiles;
-            const int64_t c0 = cta_of_block(first, W, P), c1 = cta_of_block(first + pg.tiles - 1, W, P);
-            const int64_t slot0 = (int64_t)pg.unit + unit;
-            for (int64_t c = c0; c <= c1; c += 8) {
-                float mi[8], li[8];
-                float4 oi[8];
+    if (ps.tiles > 0) {
+        constexpr int kSub = prefix_streams(D);  // q tiles of a slot
+        const int kvh = head / p.G;
+        const int row = ((b + sc.seq0 - ps.start) * p.q_len + qi) * p.G + head - kvh * p.G;
+        const int tile = row >> 7, r = row & 127;
+        const int64_t W = ps.total, P = prefix_plan_ctas(W, sc.prefix_ctas);
+        const int unit = tile / kSub * p.Hkv + kvh;
+        const int64_t first = ps.work + (int64_t)unit * ps.tiles;
+        const int c0 = (int)cta_of_block(first, W, P), n = (int)cta_of_block(first + ps.tiles - 1, W, P) - c0 + 1;
+        const int64_t at = ((int64_t)ps.unit + unit + c0) * kSub + tile % kSub;
+        const float2* ml = reinterpret_cast<const float2*>(sc.prefix_ml) + at * 128 + r;
+        const float4* po = reinterpret_cast<const float4*>(sc.prefix_o) + (at * (D / 4) + d4 / 4) * 128 + r;
+        for (int c = 0; c < n; c += 8) {
+            float2 si[8];
+            float4 oi[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    mi[k] = kNegInf;
-                    li[k] = 0.f;
-                    oi[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (c + k > c1) continue;
-                    const int64_t at = (slot0 + c + k) * kSub + tile % kSub;
-                    const float2 ml = __ldcg(reinterpret_cast<const float2*>(sc.prefix_ml) + at * 128 + r);
-                    mi[k] = ml.x;
-                    li[k] = ml.y;
-                    oi[k] = __ldcg(reinterpret_cast<const float4*>(sc.prefix_o) + (at * (D / 4) + d4 / 4) * 128 + r);
+            for (int k = 0; k < 8; ++k) {
+                si[k] = make_float2(kNegInf, 0.f);
+                oi[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (c + k < n) {
+                    si[k] = __ldcg(ml + (int64_t)(c + k) * kSub * 128);
+                    oi[k] = __ldcg(po + (int64_t)(c + k) * kSub * (D / 4) * 128);
                 }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) merge_state<kWide>(M, Ls, Os, mi[k], li[k], oi[k]);
             }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) merge_state<kWide>(M, Ls, Os, si[k].x, si[k].y, oi[k]);
         }
     }
     if (sc.row_ml && d4 == 0)
@@ -831,7 +819,7 @@ template <int D, bool kWide>
 __device__ __forceinline__ void write_unwalked(const SplitParams& p, int b, int qi, int head, int d4, int64_t o) {
     float M = kNegInf, L = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    join_prefix<D, kWide>(p, b, qi, head, d4, M, L, v);
+    join_prefix<D, kWide>(p, prefix_of(p, b), b, qi, head, d4, M, L, v);
     if (kWide ? L != 0.f : L > 0.f) v = make_float4(v.x / L, v.y / L, v.z / L, v.w / L);
     else v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (p.out_f32) *reinterpret_cast<float4*>(p.out_f32 + o) = v;
@@ -1112,6 +1100,8 @@ __device__ __forceinline__ void run_consumer(const SplitParams& p, uint32_t base
             }
             const bool whole = (m.flags & kWholeUnit) != 0;
             const int u = m.b * p.Hkv + m.kvh;
+            PrefixSeq ps = {};
+            if constexpr (kExt) ps = prefix_of(p, row_info<MQ>(p, m.b).b);  // (its round trip overlaps the merge's)
             UnitPieces pc;
             pc.cf = 0; pc.su = 0; pc.n = 1; pc.every = true;
             if (!whole) pc = unit_pieces(pfx, m.b, m.kvh, p.Hkv, p.unit_cost, gr);
@@ -1223,7 +1213,7 @@ __device__ __forceinline__ void run_consumer(const SplitParams& p, uint32_t base
                     }
                 } else {
                     if constexpr (kExt)
-                        join_prefix<D, false>(p, ri.b, ri.first + h / G, m.kvh * G + h % G, d4, M, Ls, Os);
+                        join_prefix<D, false>(p, ps, ri.b, ri.first + h / G, m.kvh * G + h % G, d4, M, Ls, Os);
                     const float4 v = Ls > 0.f ? make_float4(Os.x / Ls, Os.y / Ls, Os.z / Ls, Os.w / Ls)
                                               : make_float4(0.f, 0.f, 0.f, 0.f);
                     const int64_t o = MQ ? qo_offset<MQ>(p, ri.b, ri.first + h / G, m.kvh * G + h % G, D) + d4
@@ -1327,6 +1317,8 @@ __device__ __forceinline__ bool rows_tile_merge(const SplitParams& p, const Stag
     const bool whole = (m.flags & kWholeUnit) != 0;
     const int u = m.b * p.Hkv + m.kvh;
     const int NR = m.nr, SR = p.rows_per_slot, G = p.G;
+    PrefixSeq ps = {};
+    if constexpr (kExt) ps = prefix_of(p, ri.b);  // (its round trip overlaps the role's)
         if (tile == 0 && ct == 0) {
             int32_t r = whole ? kRoleWhole : ticket == pc.n - 1 ? kRoleMerge : kRoleStore;
             if (r == kRoleMerge) {
@@ -1402,7 +1394,7 @@ __device__ __forceinline__ bool rows_tile_merge(const SplitParams& p, const Stag
                 Os = Or;
             }
             if constexpr (kExt)
-                join_prefix<D, kScaled>(p, ri.b, ri.first + h / G, m.kvh * G + h % G, d4, M, Ls, Os);
+                join_prefix<D, kScaled>(p, ps, ri.b, ri.first + h / G, m.kvh * G + h % G, d4, M, Ls, Os);
             const float4 v = (kScaled ? Ls != 0.f : Ls > 0.f) ? make_float4(Os.x / Ls, Os.y / Ls, Os.z / Ls, Os.w / Ls)
                                       : make_float4(0.f, 0.f, 0.f, 0.f);
             const int64_t oo = qo_offset<true>(p, ri.b, ri.first + h / G, m.kvh * G + h % G, D) + d4;

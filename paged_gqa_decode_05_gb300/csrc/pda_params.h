@@ -99,14 +99,19 @@ struct PrefixGroup {
     int32_t work;    // first position of the plan
 };
 
+// What a sequence needs of it: its group's entry and the plan's size.
+struct alignas(16) PrefixSeq {
+    int32_t start, blocks, tiles, unit;
+    int32_t work, total, pad[2];
+};
+
 // What kScored adds to a launch.  Scores are in base-2 units.
 struct Scoring {
-    float cap, inv_cap;          // cap * log2 e and its inverse; 0: scores as they are
+    float cap, inv_cap;          // cap * log2 e, and 2 log2 e over that; 0: scores as they are
     const float* slopes;         // [Hq] or null: score += slope * (token - the query's own)
     float* scores;               // [launch row][Hkv][tokens][rows_per_slot] out, or null
     float* row_ml;               // [B * q_len * Hq][2] out: (m, l) of every output row, or null
-    const PrefixGroup* groups;   // [n_groups + 1], or null: no shared prefix
-    int32_t n_groups;
+    const PrefixSeq* seqs;       // [sequences of the call], or null: no shared prefix
     int32_t seq0;                // first sequence of this launch
     int32_t prefix_ctas;         // CTAs of the prefix kernel
     const float* prefix_o;       // [slots][tiles][D / 4][128][4]

@@ -14,17 +14,18 @@
 //
 // Work: units (pair of q tiles, kv head) of one position per token tile, cut
 // evenly over one CTA per SM.  Each CTA runs two streams of four softmax warps
-// with an S and an O each.  A unit of two q tiles gives each stream one, so
+// with two S and an O each.  A unit of two q tiles gives each stream one, so
 // that a tile of K and V serves 256 q rows; a unit of one q tile gives the
 // streams alternate token tiles, and their states join at the segment's end.
-// While one stream's softmax runs, the other's products do.  Head size 256,
-// whose O takes half the tensor memory, runs one stream.
+// A stream's next S is there when it has written a P.  Head size 256, whose O
+// takes half the tensor memory, runs one stream.
 //
-// K and V go through a ring of slots of a token tile each, K and V apart so
-// that K's is free once S is there.  Four loader warps fill it with 16-byte
-// cp.async in the swizzle of the tensor cores' operands; rows come one by one
-// through the block table, so any block size and any strides do.  Rows behind
-// the prefix's end are zero-filled, as are those of bad block ids.  The codes of 8-bit caches
+// K and V go through one ring of slots, in the order in which the products use
+// them (K runs `ahead` tiles before V), so that every slot but those in use is
+// one on its way.  Four loader warps fill it with 16-byte cp.async in the
+// swizzle of the tensor cores' operands; rows come one by one through the block
+// table, so any block size and any strides do.  Rows behind the prefix's end
+// are zero-filled, as are those of bad block ids.  The codes of 8-bit caches
 // land in their own slot and are spread to bf16 there, which holds them
 // exactly (4 and 8 significant bits); K scales multiply the scores, V scales
 // the weights.  2^-40 of them is taken: weights reach 2^8 (the reference lags),
@@ -41,30 +42,35 @@ namespace pda {
 
 template <int D, int FMT>
 struct PrefixCfg {
-    static constexpr int kT = prefix_tile_tokens(D);     // tokens of a tile
+    static constexpr int kT = kPrefixTile;               // tokens of a tile
     static constexpr int kStreams = prefix_streams(D);
-    static constexpr int kPart = 64;                     // scores of a row that a thread holds at a time
     static constexpr int kSoftWarps = 4 * kStreams, kLoadWarps = 4;
     static constexpr int kThreads = (kSoftWarps + kLoadWarps + 1) * 32;
-    static constexpr int kSlabs = D / 64;                // 64-column slabs, 128 bytes a row
     static constexpr int kSlotBytes = kT * D * 2;        // K or V of a tile
     static constexpr int kQTileBytes = 128 * D * 2;
-    static constexpr int kSlots = D == 64 ? 10 : FMT == kBf16 ? 5 : 4;
-    static constexpr int kScaleTiles = FMT == kBf16 ? 0 : kSlots / 2 + 2;  // ring of scales, [K | V][kT] a tile
+    static constexpr int kSlots = D == 64 ? 20 : D == 256 ? (FMT == kBf16 ? 5 : 4) : FMT == kBf16 ? 10 : 9;
+    // ring of scales, [K | V][kT] a tile: from when K's slot is filled until the
+    // softmax, `ahead` + kSlots / 2 tiles at most
+    static constexpr int kScaleTiles = FMT == kBf16 ? 0 : 16;
     static constexpr int kRW = kT / kLoadWarps;          // rows of a loader warp
-    // tensor memory: S of a stream, then O
+    // tensor memory: two S of a stream, then its O
     static constexpr uint32_t kTmO = 256;
-    static_assert(kStreams * kT <= 256 && kStreams * D <= 256, "tensor memory columns");
+    static_assert(kStreams * 2 * kT <= 256 && kStreams * D <= 256, "tensor memory columns");
+    static_assert(kScaleTiles == 0 || kScaleTiles > 4 + kSlots / 2, "scales of the tiles under way");
     // shared memory after the 1024-byte aligned base
     static constexpr uint32_t kSlot0 = kStreams * kQTileBytes;
     static constexpr uint32_t kScale0 = kSlot0 + kSlots * kSlotBytes;
     static constexpr uint32_t kBars = kScale0 + kScaleTiles * kT * 8;
-    // full, empty [kSlots], landed [loader warp][kSlots] (8-bit), then the rest
+    // full, empty [kSlots], landed [loader warp][kSlots] (8-bit), S and P
+    // [stream][2], P V [stream], then the rest
     static constexpr uint32_t kFull = kBars, kEmpty = kFull + 8 * kSlots, kLanded = kEmpty + 8 * kSlots;
-    static constexpr uint32_t kS = kLanded + 8 * kSlots * (FMT == kBf16 ? 0 : kLoadWarps), kP = kS + 16, kO = kP + 16,
-                              kQ = kO + 8, kSync = kQ + 8, kFin = kSync + 8, kTm = kFin + 8, kEnd = kTm + 16;
+    static constexpr uint32_t kS = kLanded + 8 * kSlots * (FMT == kBf16 ? 0 : kLoadWarps), kP = kS + 32, kPV = kP + 32,
+                              kO = kPV + 16, kQ = kO + 8, kSync = kQ + 8, kFin = kSync + 8, kTm = kFin + 8, kEnd = kTm + 16;
     static constexpr uint32_t kSmem = kEnd + (1024 - 16);  // (dynamic shared memory starts on 16 bytes)
     static_assert(kSmem <= 232448, "shared memory of an SM");
+    // tiles that K runs ahead of V: a stream's two S
+    static __device__ __forceinline__ int ahead(bool dual) { return dual || kStreams == 1 ? 2 : 4; }
+    static_assert(kSlots >= 4 + 1 || kStreams == 1, "the ring holds what the products need at once");
 };
 
 // One run of a CTA over token tiles of a unit.
@@ -198,53 +204,56 @@ __device__ __forceinline__ void prefix_load(const PrefixParams& p, uint32_t base
     constexpr int RW = C::kRW, ES = FMT == kBf16 ? 2 : 1;  // rows of this warp; bytes of an element
     constexpr int CH = D * ES / 16, RPI = 32 / CH;         // 16-byte chunks of a row; rows of an instruction
     static_assert(RPI >= 1 && RW % RPI == 0 && RW <= 32, "rows of a warp");
-    PrefixWalk<D, FMT> walk(p);
-    PrefixSegment s = {};
-    int j = 0, left = 0;  // tiles of the segment
-    // the next tile's rows: lane r holds row r of this warp (element offset, or -1), and its scales
-    int64_t off = -1;
-    float ks = 0.f, vs = 0.f;
-    auto rows_of = [&](int tile) {
-        off = -1;
-        ks = vs = 0.f;
-        const int64_t t = (int64_t)tile * C::kT + w * RW + lane;
-        if (lane < RW && t < s.tokens) {
-            const int32_t id = p.table[(int64_t)s.start * p.table_stride + (t >> p.lbs)];
+    // K's and V's places: the tile whose slot is filled next, its rows looked up a
+    // slot ahead.  Lane r holds row r of this warp (element offset, or -1).
+    struct Place {
+        PrefixWalk<D, FMT> walk;
+        PrefixSegment s;
+        int j, left;       // tile, tiles of the segment after it
+        bool more;         // there is such a tile
+        int64_t off;
+        float ks, vs;      // K's place: the row's scales
+    };
+    Place pk = {PrefixWalk<D, FMT>(p), {}, 0, 0, true, -1, 0.f, 0.f}, pv = pk;
+    auto advance = [&](Place& at, bool scales) {
+        if (at.left == 0) {
+            at.more = at.walk.next(p, at.s);
+            at.j = at.s.j0;
+            at.left = at.s.n;
+            if (!at.more) return;
+        } else {
+            ++at.j;
+        }
+        --at.left;
+        at.off = -1;
+        at.ks = at.vs = 0.f;
+        const int64_t t = (int64_t)at.j * C::kT + w * RW + lane;
+        if (lane < RW && t < at.s.tokens) {
+            const int32_t id = p.table[(int64_t)at.s.start * p.table_stride + (t >> p.lbs)];
             const int slot = (int)t & ((1 << p.lbs) - 1);
             if (id < 0 || (int64_t)id >= p.num_blocks) {
                 atomicOr(p.err, PDA_DEVERR_BAD_BLOCK_ID_);
                 return;
             }
-            off = (int64_t)id * p.blk_s + (int64_t)slot * p.tok_s + (int64_t)s.kvh * p.kvh_s;
-            if constexpr (FMT != kBf16) {
-                const float* sc = p.scales + (((((int64_t)id * p.Hkv + s.kvh) * 2) << p.lbs) + slot);
-                ks = sc[0];
-                vs = sc[(int64_t)1 << p.lbs];
+            at.off = (int64_t)id * p.blk_s + (int64_t)slot * p.tok_s + (int64_t)at.s.kvh * p.kvh_s;
+            if (FMT != kBf16 && scales) {
+                const float* sc = p.scales + (((((int64_t)id * p.Hkv + at.s.kvh) * 2) << p.lbs) + slot);
+                at.ks = sc[0];
+                at.vs = sc[(int64_t)1 << p.lbs];
             }
         }
     };
-    auto advance = [&]() {  // to the next tile; false at the end
-        if (left == 0) {
-            if (!walk.next(p, s)) return false;
-            j = s.j0;
-            left = s.n;
-        } else {
-            ++j;
-        }
-        --left;
-        rows_of(j);
-        return true;
-    };
+    advance(pk, true);
+    advance(pv, false);
     const int chunk = lane % CH, sub = lane / CH;
-    uint32_t issued = 0, spread = 0, tiles = 0;  // slots filled, slots converted (8-bit), tiles begun
-    int64_t now = -1;                            // the current tile's rows
+    uint32_t issued = 0, spread = 0, tiles = 0;  // slots filled, slots converted (8-bit), tiles whose K is filled
+    int ki = 0;  // K tiles of V's segment that are filled
     // (8-bit) codes in their slot: the warp's rows back to back over its parts of the slabs
     auto code_at = [&](uint32_t slot, int o) {
         return slot + (uint32_t)(o / (RW * 128)) * (C::kT * 128) + (uint32_t)(w * RW * 128 + o % (RW * 128));
     };
-    auto fill = [&](uint32_t n) {  // slot number n, its K or V
+    auto fill = [&](uint32_t n, const uint8_t* pool, int64_t now) {  // slot number n
         const uint32_t slot = base + C::kSlot0 + (n % C::kSlots) * C::kSlotBytes;
-        const uint8_t* pool = (n & 1) ? p.v_base : p.k_base;
 #pragma unroll 4
         for (int r0 = 0; r0 < RW; r0 += RPI) {
             const int r = r0 + sub;
@@ -284,33 +293,43 @@ __device__ __forceinline__ void prefix_load(const PrefixParams& p, uint32_t base
             if (lane == 0) mbar_arrive(base + C::kFull + 8 * (n % C::kSlots));
         }
     };
-    bool ok = true, more = advance();
+    bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
         if (warp_wait(bar, parity)) return true;
         atomicOr(p.err, PDA_DEVERR_TIMEOUT_);
         *abort_flag = 1;
         return false;
     };
-    while (ok && (more || (issued & 1) || spread < issued)) {
+    // The order of a segment's n tiles: K of tile i once V of tile i - ahead is
+    // filled, and V of tile i once K has run `ahead` tiles past it or out of tiles.
+    int vi = 0;  // V's tile within its segment
+    while (ok && (pv.more || spread < issued)) {
         if (__any_sync(0xffffffffu, *abort_flag)) break;
-        bool can = more || (issued & 1);
+        bool can = pv.more;
         const uint32_t empty = base + C::kEmpty + 8 * (issued % C::kSlots), parity = ((issued / C::kSlots) & 1u) ^ 1u;
         if (can && FMT != kBf16 && spread < issued) can = __all_sync(0xffffffffu, mbar_test_wait(empty, parity));
         if (can) {
             if (!(ok = wait(empty, parity))) break;
-            if (!(issued & 1)) {  // K, the tile's first half
-                now = off;
+            if (ki < min(pv.s.n, vi + C::ahead(pv.s.dual))) {
                 if constexpr (FMT != kBf16) {
                     if (lane < RW) {
                         const uint32_t sc = base + C::kScale0 + (tiles % C::kScaleTiles) * (C::kT * 8) + (uint32_t)(w * RW + lane) * 4;
-                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc), "f"(ks) : "memory");
-                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc + C::kT * 4), "f"(vs * 9.094947e-13f) : "memory");  // 2^-40
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc), "f"(pk.ks) : "memory");
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc + C::kT * 4), "f"(pk.vs * 9.094947e-13f) : "memory");  // 2^-40
                     }
                 }
                 ++tiles;
-                more = advance();
+                ++ki;
+                const int64_t now = pk.off;
+                advance(pk, true);
+                fill(issued, p.k_base, now);
+            } else {
+                const int64_t now = pv.off;
+                const int n = pv.s.n;
+                if (++vi == n) vi = ki = 0;
+                advance(pv, false);
+                fill(issued, p.v_base, now);
             }
-            fill(issued);
             ++issued;
             if (FMT == kBf16) spread = issued;
         } else {
@@ -330,7 +349,8 @@ __device__ __forceinline__ void prefix_mma(const PrefixParams& p, uint32_t base,
     constexpr uint32_t idS = umma_idesc_bf16(128, C::kT, false), idO = umma_idesc_bf16(128, D, true);
     PrefixWalk<D, FMT> walk(p);
     PrefixSegment s;
-    uint32_t tile0 = 0, segs = 0, p_phase = 0;  // p_phase: bit per stream
+    uint32_t next = 0, segs = 0;           // the ring's next slot; segments begun
+    uint32_t sc[2] = {0, 0}, pc[2] = {0, 0};  // S and P V issued, per stream
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
         if (*abort_flag == 0 && mbar_wait_bounded(bar, parity, kWaitLimitNs)) return true;
@@ -338,51 +358,59 @@ __device__ __forceinline__ void prefix_mma(const PrefixParams& p, uint32_t base,
         *abort_flag = 1;
         return ok = false;
     };
+    auto take = [&](uint32_t& slot) {  // the next slot, once it is full
+        slot = next % C::kSlots;
+        if (!wait(base + C::kFull + 8 * slot, (next / C::kSlots) & 1u)) return false;
+        ++next;
+        fence_proxy_async_smem();  // the loaders' cp.async writes
+        return true;
+    };
     while (ok && walk.next(p, s)) {
-        const int items = s.dual ? 2 * s.n : s.n;
+        // item k: stream k % kStreams, its tile k / 2 (two q tiles) or k
+        const int items = s.dual ? 2 * s.n : s.n, look = min(2 * C::kStreams, items);
         if (!wait(base + C::kQ, segs & 1u)) break;
         ++segs;
-        auto first_of = [&](int k) { return !s.dual || (k & 1) == 0; };
-        auto last_of = [&](int k) { return !s.dual || (k & 1) == 1; };
+        uint32_t k_slot = 0, v_slot = 0;
         auto qk = [&](int k) {
-            const uint32_t n = 2 * (tile0 + (s.dual ? k >> 1 : k)), slot = n % C::kSlots;
-            if (first_of(k) && !wait(base + C::kFull + 8 * slot, (n / C::kSlots) & 1u)) return;
-            fence_proxy_async_smem();  // the loaders' cp.async writes
+            const bool first = !s.dual || (k & 1) == 0, last = !s.dual || (k & 1) == 1;
+            if (first && !take(k_slot)) return;
             tc_fence_after();
             const int st = C::kStreams == 2 ? k & 1 : 0;
-            const uint32_t sQ = base + (s.dual ? st : 0) * C::kQTileBytes, sK = base + C::kSlot0 + slot * C::kSlotBytes;
+            const uint32_t buf = sc[st] & 1u;
+            const uint32_t sQ = base + (s.dual ? st : 0) * C::kQTileBytes, sK = base + C::kSlot0 + k_slot * C::kSlotBytes;
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks)
-                umma_bf16_ss(tmem + st * C::kT, umma_sdesc(sQ + (ks >> 2) * (128 * 128) + (ks & 3) * 32, 16, 1024),
+                umma_bf16_ss(tmem + st * 2 * C::kT + buf * C::kT,
+                             umma_sdesc(sQ + (ks >> 2) * (128 * 128) + (ks & 3) * 32, 16, 1024),
                              umma_sdesc(sK + (ks >> 2) * (C::kT * 128) + (ks & 3) * 32, 16, 1024), idS, ks > 0);
-            umma_commit(base + C::kS + 8 * st);
-            if (last_of(k)) umma_commit(base + C::kEmpty + 8 * slot);
+            umma_commit(base + C::kS + 16 * st + 8 * buf);
+            if (last) umma_commit(base + C::kEmpty + 8 * k_slot);
+            ++sc[st];
         };
-        for (int k = 0; ok && k < min(C::kStreams, items); ++k) qk(k);
+        for (int k = 0; ok && k < look; ++k) qk(k);
         for (int k = 0; ok && k < items; ++k) {
+            const bool first = !s.dual || (k & 1) == 0, last = !s.dual || (k & 1) == 1;
             const int st = C::kStreams == 2 ? k & 1 : 0;
-            const uint32_t n = 2 * (tile0 + (s.dual ? k >> 1 : k)) + 1, slot = n % C::kSlots;
-            if (!wait(base + C::kP + 8 * st, (p_phase >> st) & 1u)) break;
-            p_phase ^= 1u << st;
-            if (first_of(k) && !wait(base + C::kFull + 8 * slot, (n / C::kSlots) & 1u)) break;
-            fence_proxy_async_smem();
+            const uint32_t buf = pc[st] & 1u;
+            if (first && !take(v_slot)) break;
+            if (!wait(base + C::kP + 16 * st + 8 * buf, (pc[st] >> 1) & 1u)) break;
             tc_fence_after();
-            const uint32_t sV = base + C::kSlot0 + slot * C::kSlotBytes, tP = tmem + st * C::kT;
+            const uint32_t sV = base + C::kSlot0 + v_slot * C::kSlotBytes, tP = tmem + st * 2 * C::kT + buf * C::kT;
             const uint32_t tO = tmem + C::kTmO + st * D;
             bool acc = k >= C::kStreams;
-#pragma unroll 4
+#pragma unroll
             for (int ks = 0; ks < C::kT / 16; ++ks) {
                 const uint64_t v = umma_sdesc(sV + 2048 * ks, C::kT * 128, 1024);
-                const uint32_t part = tP + ks / (C::kPart / 16) * C::kPart + ks % (C::kPart / 16) * 8;
-                umma_bf16_ts(tO, part, v, idO, acc);
-                umma_bf16_ts(tO, part + C::kPart / 2, v, idO, true);
+                umma_bf16_ts(tO, tP + 8 * ks, v, idO, acc);
+                umma_bf16_ts(tO, tP + C::kT / 2 + 8 * ks, v, idO, true);
                 acc = true;
             }
-            if (last_of(k)) umma_commit(base + C::kEmpty + 8 * slot);
+            if (last) umma_commit(base + C::kEmpty + 8 * v_slot);
+            umma_commit(base + C::kPV + 8 * st);
             if (k == items - 1) umma_commit(base + C::kO);
-            if (k + C::kStreams < items) qk(k + C::kStreams);
+            ++pc[st];
+            if (k + look < items) qk(k + look);
         }
-        tile0 += s.n;
     }
     // every product has completed before the tensor memory is freed
     umma_commit(base + C::kFin);
@@ -409,20 +437,14 @@ __device__ __forceinline__ void tmem_ld_row(uint32_t taddr, float (&v)[N]) {
     for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
 }
 
-template <int N>
-__device__ __forceinline__ void tmem_st_row(uint32_t taddr, const float (&v)[N]) {
-#pragma unroll
-    for (int c = 0; c < N; c += 16) tmem_st16(taddr + c, *reinterpret_cast<const float(*)[16]>(v + c));
-}
-
 template <int D, int FMT>
 __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, uint32_t base, uint8_t* smem, volatile int* abort_flag,
                                                uint32_t tmem, int warp, int lane) {
     using C = PrefixCfg<D, FMT>;
-    constexpr int kT = C::kT, kPart = C::kPart;
+    constexpr int kT = C::kT;
     constexpr float kBack = FMT == kBf16 ? 1.f : 1.0995116e12f;  // 2^40
     const int st = warp >> 2, w = warp & 3, row = 32 * w + lane;
-    const uint32_t tl = tmem + ((uint32_t)(32 * w) << 16), tS = tl + st * kT;
+    const uint32_t tl = tmem + ((uint32_t)(32 * w) << 16);
     float* ml = reinterpret_cast<float*>(smem);  // [stream][2][128], over the q rows once they are used
     PrefixWalk<D, FMT> walk(p);
     PrefixSegment s;
@@ -430,7 +452,7 @@ __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, uint32_t b
     sc.cap = p.cap;
     sc.inv_cap = p.inv_cap;
     const bool plain = p.cap == 0.f && p.slopes == nullptr;
-    uint32_t tile0 = 0, segs = 0, s_phase = 0, cphase = 0;
+    uint32_t tile0 = 0, segs = 0, done = 0, cphase = 0;  // done: items of this stream
     auto wait = [&](uint32_t bar, uint32_t parity) {
         if (warp_wait(bar, parity)) return true;
         atomicOr(p.err, PDA_DEVERR_TIMEOUT_);
@@ -478,58 +500,63 @@ __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, uint32_t b
         float m = kNegInf, l = 0.f;
         for (int k = st; k < items; k += C::kStreams) {
             const int jj = s.dual ? k >> 1 : k;
-            if (!wait(base + C::kS + 8 * st, s_phase & 1u)) return;
-            ++s_phase;
+            const uint32_t buf = done & 1u, tS = tl + st * 2 * kT + buf * kT;
+            if (!wait(base + C::kS + 16 * st + 8 * buf, (done >> 1) & 1u)) return;
             tc_fence_after();
             if (!idle) {
                 const int t0 = (s.j0 + jj) * kT, seen = vis - t0;  // the tile's first token; tokens of it in sight
-                const float* kscale = nullptr;
-                if constexpr (FMT != kBf16) {
-                    // (the scales are there once V is: V's slot stays until this row's P is read)
-                    const uint32_t n = 2 * (tile0 + jj) + 1;
-                    if (!wait(base + C::kFull + 8 * (n % C::kSlots), (n / C::kSlots) & 1u)) return;
-                    kscale = reinterpret_cast<const float*>(smem + C::kScale0) + ((tile0 + jj) % C::kScaleTiles) * (2 * kT);
+                float v[kT];
+                tmem_ld_row(tS, v);
+                // scores in base-2 units; a bare product is scaled when its weight is taken
+                const bool cut = __any_sync(0xffffffffu, seen < kT), bare = FMT == kBf16 && plain && !cut;
+                const float* kscale = reinterpret_cast<const float*>(smem + C::kScale0) +
+                                      (FMT == kBf16 ? 0 : (tile0 + jj) % C::kScaleTiles * (2 * kT));
+                float top;
+                if (bare) {
+                    float hi = v[0], lo = v[0];
+#pragma unroll
+                    for (int i = 1; i < kT; ++i) {
+                        if (p.scale_log2 >= 0.f) hi = fmaxf(hi, v[i]);
+                        else lo = fminf(lo, v[i]);
+                    }
+                    top = (p.scale_log2 >= 0.f ? hi : lo) * p.scale_log2;
+                } else {
+                    float two[2] = {kNegInf, kNegInf};
+#pragma unroll
+                    for (int i = 0; i < kT; i += 4) {
+                        float4 x = make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
+                        if constexpr (FMT != kBf16) {
+                            const float4 y = *reinterpret_cast<const float4*>(kscale + i);
+                            x = make_float4(x.x * y.x, x.y * y.y, x.z * y.z, x.w * y.w);
+                        }
+                        v[i] *= x.x;
+                        v[i + 1] *= x.y;
+                        v[i + 2] *= x.z;
+                        v[i + 3] *= x.w;
+                    }
+                    if (p.cap != 0.f) {
+#pragma unroll
+                        for (int i = 0; i < kT; ++i) v[i] = capped(sc, v[i]);
+                    }
+                    if (p.slopes) {
+                        const float far = (float)(t0 - own);
+#pragma unroll
+                        for (int i = 0; i < kT; ++i) v[i] = fmaf(slope, far + (float)i, v[i]);
+                    }
+                    if (cut) {
+#pragma unroll
+                        for (int i = 0; i < kT; ++i)
+                            if (i >= seen) v[i] = kNegInf;
+                    }
+#pragma unroll
+                    for (int i = 0; i < kT; ++i) two[i & 1] = fmaxf(two[i & 1], v[i]);
+                    top = fmaxf(two[0], two[1]);
                 }
-                // the row's largest score, a part of the row at a time; scores that
-                // are more than a product go back to tensor memory for the second pass
-                const bool bare = FMT == kBf16 && plain && !__any_sync(0xffffffffu, seen < kT);
-                const float f = bare ? p.scale_log2 : 1.f;
-                float top = kNegInf;
-#pragma unroll
-                for (int c = 0; c < kT; c += kPart) {
-                    float v[kPart];
-                    tmem_ld_row(tS + c, v);
-                    if (bare) {
-#pragma unroll
-                        for (int i = 0; i < kPart; ++i) top = fmaxf(top, v[i] * f);
-                        continue;
-                    }
-#pragma unroll
-                    for (int i = 0; i < kPart; i += 4) {
-                        float4 x = make_float4(1.f, 1.f, 1.f, 1.f);
-                        if constexpr (FMT != kBf16) x = *reinterpret_cast<const float4*>(kscale + c + i);
-                        v[i] *= x.x * p.scale_log2;
-                        v[i + 1] *= x.y * p.scale_log2;
-                        v[i + 2] *= x.z * p.scale_log2;
-                        v[i + 3] *= x.w * p.scale_log2;
-                    }
-                    if (!plain) {
-                        const float far = (float)(t0 + c - own);
-#pragma unroll
-                        for (int i = 0; i < kPart; ++i) v[i] = score_of(sc, v[i], slope, far + (float)i);
-                    }
-#pragma unroll
-                    for (int i = 0; i < kPart; ++i) {
-                        if (c + i >= seen) v[i] = kNegInf;
-                        top = fmaxf(top, v[i]);
-                    }
-                    tmem_st_row(tS + c, v);
-                }
-                tmem_wait_st();
-                // lazy reference (kLazyLog2); this stream's last product with V is
-                // done: it was issued before this S
+                // lazy reference (kLazyLog2); O is scaled once this stream's last product with V is done
                 const bool up = top > m + kLazyLog2, scale_o = up && m != kNegInf;
                 if (__any_sync(0xffffffffu, scale_o)) {
+                    if (!wait(base + C::kPV + 8 * st, (done - 1u) & 1u)) return;
+                    tc_fence_after();
                     const float a = scale_o ? ex2(m - top) : 1.f;
                     l *= a;
 #pragma unroll 1
@@ -542,37 +569,33 @@ __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, uint32_t b
                     }
                 }
                 if (up) m = top;
-                const float u = m == kNegInf ? 0.f : m;
+                const float u = m == kNegInf ? 0.f : m, f = bare ? p.scale_log2 : 1.f;
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int c = 0; c < kT; c += kPart) {  // P over its own part of S: high parts, low parts
-                    float v[kPart];
-                    tmem_ld_row(tS + c, v);
+                for (int c = 0; c < kT; c += 32) {  // P over its S: high parts, then low parts
+                    uint32_t hi[16], lo[16];
 #pragma unroll
-                    for (int e = 0; e < kPart; e += 32) {
-                        uint32_t hi[16], lo[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float p0 = ex2(fmaf(v[e + 2 * i], f, -u)), p1 = ex2(fmaf(v[e + 2 * i + 1], f, -u));
-                            sum[i & 3] += p0 + p1;
-                            if constexpr (FMT != kBf16) {
-                                const float2 x = *reinterpret_cast<const float2*>(kscale + kT + c + e + 2 * i);
-                                p0 *= x.x;
-                                p1 *= x.y;
-                            }
-                            hi[i] = pack_bf16x2(p0, p1);
-                            lo[i] = pack_bf16x2(p0 - bf16_lo(hi[i]), p1 - bf16_hi(hi[i]));
+                    for (int i = 0; i < 16; ++i) {
+                        float p0 = ex2(fmaf(v[c + 2 * i], f, -u)), p1 = ex2(fmaf(v[c + 2 * i + 1], f, -u));
+                        sum[i & 3] += p0 + p1;
+                        if constexpr (FMT != kBf16) {
+                            const float2 x = *reinterpret_cast<const float2*>(kscale + kT + c + 2 * i);
+                            p0 *= x.x;
+                            p1 *= x.y;
                         }
-                        tmem_st16u(tS + c + e / 2, hi);
-                        tmem_st16u(tS + c + kPart / 2 + e / 2, lo);
+                        hi[i] = pack_bf16x2(p0, p1);
+                        lo[i] = pack_bf16x2(p0 - bf16_lo(hi[i]), p1 - bf16_hi(hi[i]));
                     }
+                    tmem_st16u(tS + c / 2, hi);
+                    tmem_st16u(tS + kT / 2 + c / 2, lo);
                 }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 tmem_wait_st();
             }
+            ++done;
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(base + C::kP + 8 * st);
+            if (lane == 0) mbar_arrive(base + C::kP + 16 * st + 8 * buf);
         }
         // ---- the segment's end: every product of it is done
         if (!wait(base + C::kO, segs & 1u)) return;
@@ -637,10 +660,11 @@ __global__ void __launch_bounds__(PrefixCfg<D, FMT>::kThreads, 1) prefix_kernel(
         }
         if (FMT != kBf16)
             for (int i = 0; i < C::kSlots * C::kLoadWarps; ++i) mbar_init(base + C::kLanded + 8 * i, 32);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(base + C::kS + 8 * i, 1);
             mbar_init(base + C::kP + 8 * i, 4);
         }
+        for (int i = 0; i < 2; ++i) mbar_init(base + C::kPV + 8 * i, 1);
         mbar_init(base + C::kO, 1);
         mbar_init(base + C::kQ, C::kSoftWarps);
         mbar_init(base + C::kSync, C::kSoftWarps * 32);
@@ -659,6 +683,19 @@ __global__ void __launch_bounds__(PrefixCfg<D, FMT>::kThreads, 1) prefix_kernel(
     if (warp == 0) prefix_plan<D, FMT>(p, lane);
     __syncthreads();
     tc_fence_after();
+    for (int b = blockIdx.x * C::kThreads + threadIdx.x; b < p.B; b += gridDim.x * C::kThreads) {
+        int lo = 0, hi = p.n_groups;  // the first entry that starts past b
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (p.groups[mid].start <= b) lo = mid + 1; else hi = mid;
+        }
+        PrefixSeq s = {};
+        if (lo > 0 && b < p.groups[p.n_groups].start) {
+            const PrefixGroup g = p.groups[lo - 1];
+            s = {g.start, g.blocks, g.tiles, g.unit, g.work, p.groups[p.n_groups].work, {0, 0}};
+        }
+        p.seqs[b] = s;
+    }
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + C::kTm);
     if (warp < C::kSoftWarps) {
         prefix_softmax<D, FMT>(p, base, smem, &abort_flag, tmem, warp, lane);

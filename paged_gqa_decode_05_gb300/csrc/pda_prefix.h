@@ -19,6 +19,7 @@ struct PrefixParams {
     const int32_t* shared;      // [n_groups] blocks
     const int32_t* starts;      // [n_groups + 1] or null: B / n_groups sequences each
     PrefixGroup* groups;        // [n_groups + 1] out
+    PrefixSeq* seqs;            // [B] out
     float* part_o;              // [slots][streams][D / 4][128][4]
     float* part_ml;             // [slots][streams][128][2]
     uint32_t* err;

@@ -348,6 +348,13 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// 1 / x with the hardware approximation (rcp.approx, flush-to-zero); 1 / inf = 0.
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // log2(x) with the hardware approximation (lg2.approx, flush-to-zero).
 __device__ __forceinline__ float lg2(float x) {
     float y;

@@ -118,7 +118,7 @@ pda_status run_scored(pda_ctx* ctx, const Call& c, const pda::Scoring& sc, const
     p.G = ctx->G;
     p.bs = bs;
     // (the prefetch warp knows no blocks that a walk leaves out)
-    p.prefetch = p.row_gather == 0 && bs >= 8 && rows.Qr == 1 && !sc.groups;
+    p.prefetch = p.row_gather == 0 && bs >= 8 && rows.Qr == 1 && !sc.seqs;
     for (int32_t s0 = 0; s0 < c.batch; s0 += chunk) {
         const int32_t n = std::min(chunk, c.batch - s0);
         const int64_t rows0 = (int64_t)s0 * c.q_len * Hq;
@@ -141,7 +141,7 @@ pda::Scoring scoring_of(const pda_scoring* s) {
     pda::Scoring sc = {};
     if (!s) return sc;
     sc.cap = s->softcap * kLog2e;
-    sc.inv_cap = s->softcap > 0.f ? 1.f / sc.cap : 0.f;
+    sc.inv_cap = s->softcap > 0.f ? 2.f * kLog2e / sc.cap : 0.f;
     sc.slopes = s->slopes;
     return sc;
 }
@@ -163,7 +163,7 @@ WeightsScratch weights_scratch(const pda_ctx* ctx, int32_t batch, int32_t q_len,
 
 // Scratch of a shared prefix: the plan, and the states of its pieces.
 struct SharedScratch {
-    int64_t groups, ml, o, total;
+    int64_t groups, seqs, ml, o, total;
 };
 SharedScratch shared_scratch(const pda_ctx* ctx, int32_t batch, int32_t q_len, int32_t n_groups) {
     const int D = ctx->dims.head_dim;
@@ -171,9 +171,10 @@ SharedScratch shared_scratch(const pda_ctx* ctx, int32_t batch, int32_t q_len, i
     const int64_t rows = (units + ctx->num_sms) * pda::prefix_streams(D) * 128;
     SharedScratch s;
     s.groups = round256(((int64_t)n_groups + 1) * (int64_t)sizeof(pda::PrefixGroup));
+    s.seqs = round256((int64_t)batch * (int64_t)sizeof(pda::PrefixSeq));
     s.ml = round256(rows * 8);
     s.o = round256(rows * D * 4);
-    s.total = s.groups + s.ml + s.o;
+    s.total = s.groups + s.seqs + s.ml + s.o;
     return s;
 }
 
@@ -310,7 +311,7 @@ PDA_EXPORT pda_status pda_decode_shared(pda_ctx* ctx, const pda_bf16* q, const p
         return fail(PDA_ERR_INVALID_ARG, "without starts batch (%d) must be a multiple of groups (%d)", batch, groups);
     const pda_dims& d = ctx->dims;
     const int D = d.head_dim;
-    const int64_t tiles = ((int64_t)max_blocks * d.block_size + pda::prefix_tile_tokens(D) - 1) / pda::prefix_tile_tokens(D);
+    const int64_t tiles = ((int64_t)max_blocks * d.block_size + pda::kPrefixTile - 1) / pda::kPrefixTile;
     if (pda::prefix_units(D, (int64_t)batch * q_len * ctx->G, groups, d.num_kv_heads) * tiles > INT32_MAX)
         return fail(PDA_ERR_INVALID_ARG, "block table width %d is too large for a shared prefix", max_blocks);
     const SharedScratch ss = shared_scratch(ctx, batch, q_len, groups);
@@ -335,8 +336,9 @@ PDA_EXPORT pda_status pda_decode_shared(pda_ctx* ctx, const pda_bf16* q, const p
     pp.shared = shared_blocks;
     pp.starts = starts;
     pp.groups = reinterpret_cast<pda::PrefixGroup*>(base);
-    pp.part_ml = reinterpret_cast<float*>(base + ss.groups);
-    pp.part_o = reinterpret_cast<float*>(base + ss.groups + ss.ml);
+    pp.seqs = reinterpret_cast<pda::PrefixSeq*>(base + ss.groups);
+    pp.part_ml = reinterpret_cast<float*>(base + ss.groups + ss.seqs);
+    pp.part_o = reinterpret_cast<float*>(base + ss.groups + ss.seqs + ss.ml);
     pp.err = ctx->err;
     pp.table_stride = max_blocks;
     while ((1 << pp.lbs) < d.block_size) ++pp.lbs;
@@ -349,8 +351,7 @@ PDA_EXPORT pda_status pda_decode_shared(pda_ctx* ctx, const pda_bf16* q, const p
     pp.cap = sc.cap;
     pp.inv_cap = sc.inv_cap;
     pp.slopes = sc.slopes;
-    sc.groups = pp.groups;
-    sc.n_groups = groups;
+    sc.seqs = pp.seqs;
     sc.prefix_ctas = ctx->num_sms;
     sc.prefix_o = pp.part_o;
     sc.prefix_ml = pp.part_ml;
