@@ -77,6 +77,11 @@ struct pda_ctx {
     // Decode over 8-bit caches: grids with up to 8 and 16 packed q rows per
     // walk (0: not on this shape).
     int quant_ctas[2] = {0, 0};
+    // The shared-prefix kernel's maps of the last cache, as above.
+    bool prefix_valid = false, prefix_boxes = false;
+    int32_t prefix_format = 0;
+    pda_pool_key prefix_key;
+    CUtensorMap prefix_k, prefix_v;
     // Scored decode: grids by cache format (bf16; 8-bit).
     int scored_ctas[2] = {0, 0};
 };

@@ -22,15 +22,17 @@
 //
 // K and V go through one ring of slots, in the order in which the products use
 // them (K runs `ahead` tiles before V), so that every slot but those in use is
-// one on its way.  Four loader warps fill it with 16-byte cp.async in the
-// swizzle of the tensor cores' operands; rows come one by one through the block
-// table, so any block size and any strides do.  Rows behind the prefix's end
-// are zero-filled, as are those of bad block ids.  The codes of 8-bit caches
-// land in their own slot and are spread to bf16 there, which holds them
-// exactly (4 and 8 significant bits); K scales multiply the scores, V scales
-// the weights.  2^-40 of them is taken: weights reach 2^8 (the reference lags),
-// scales 2^122, codes 448, and the sum over any number of tokens stays inside
-// fp32.
+// one on its way.  Four loader warps, two for K and two for V, fill 32 rows of a
+// slot each, with TMA boxes of up to 32 rows and one 64-column slab, or, for block sizes below 8, row by
+// row with 16-byte cp.async in the same swizzle.  (Row by row for all, 32768
+// tokens of 8 kv heads of 128 took 50 us in this kernel: a slot's copies kept a
+// warp 1900 cycles.)  Rows behind the prefix's end and of bad block ids are zero-
+// filled, by coordinates outside the pool where boxes load.  The codes of 8-bit
+// caches land in the warp's own part of their slot, which spreads them to bf16
+// there; bf16 holds them exactly (4 and 8 significant bits).  K scales multiply
+// the scores, V scales the weights; weights are taken 2^-40 times, as they reach
+// 2^8 (the reference lags), scales 2^122 and codes 448, and the sum over any
+// number of tokens stays inside fp32.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -51,8 +53,8 @@ struct PrefixCfg {
     static constexpr int kSlots = D == 64 ? 20 : D == 256 ? (FMT == kBf16 ? 5 : 4) : FMT == kBf16 ? 10 : 9;
     // ring of scales, [K | V][kT] a tile: from when K's slot is filled until the
     // softmax, `ahead` + kSlots / 2 tiles at most
-    static constexpr int kScaleTiles = FMT == kBf16 ? 0 : 16;
-    static constexpr int kRW = kT / kLoadWarps;          // rows of a loader warp
+    static constexpr int kRing = 16, kScaleTiles = FMT == kBf16 ? 0 : kRing;
+    static constexpr int kRW = kT / 2;                   // rows of a loader warp
     // tensor memory: two S of a stream, then its O
     static constexpr uint32_t kTmO = 256;
     static_assert(kStreams * 2 * kT <= 256 && kStreams * D <= 256, "tensor memory columns");
@@ -61,10 +63,10 @@ struct PrefixCfg {
     static constexpr uint32_t kSlot0 = kStreams * kQTileBytes;
     static constexpr uint32_t kScale0 = kSlot0 + kSlots * kSlotBytes;
     static constexpr uint32_t kBars = kScale0 + kScaleTiles * kT * 8;
-    // full, empty [kSlots], landed [loader warp][kSlots] (8-bit), S and P
+    // full, empty [kSlots], landed [kSlots][half of the rows] (8-bit), S and P
     // [stream][2], P V [stream], then the rest
     static constexpr uint32_t kFull = kBars, kEmpty = kFull + 8 * kSlots, kLanded = kEmpty + 8 * kSlots;
-    static constexpr uint32_t kS = kLanded + 8 * kSlots * (FMT == kBf16 ? 0 : kLoadWarps), kP = kS + 32, kPV = kP + 32,
+    static constexpr uint32_t kS = kLanded + 8 * kSlots * (FMT == kBf16 ? 0 : 2), kP = kS + 32, kPV = kP + 32,
                               kO = kPV + 16, kQ = kO + 8, kSync = kQ + 8, kFin = kSync + 8, kTm = kFin + 8, kEnd = kTm + 16;
     static constexpr uint32_t kSmem = kEnd + (1024 - 16);  // (dynamic shared memory starts on 16 bytes)
     static_assert(kSmem <= 232448, "shared memory of an SM");
@@ -177,6 +179,10 @@ __device__ __forceinline__ void cp_async_16_or_0(uint32_t dst, const void* src, 
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(use ? 16 : 0) : "memory");
 }
 
+__device__ __forceinline__ void cp_async_4_or_0(uint32_t dst, const void* src, bool use) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(use ? 4 : 0) : "memory");
+}
+
 // Four codes as bf16, which holds them exactly.
 template <int FMT>
 __device__ __forceinline__ void codes_to_bf16(uint32_t x, uint32_t& lo, uint32_t& hi) {
@@ -196,145 +202,167 @@ __device__ __forceinline__ void codes_to_bf16(uint32_t x, uint32_t& lo, uint32_t
     hi = pack_bf16x2(fb.x, fb.y);
 }
 
+// A bounded wait whose outcome the warp shares.
+__device__ __forceinline__ bool lane_wait(uint32_t bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity) ? 1 : 0)) return true;
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kWaitLimitNs) ? 1 : 0) != 0;
+}
+
 // ------------------------------------------------------------------ loaders
 
+// Loader warp w fills 32 rows (half w & 1) of the slots of K (w < 2) or of V.
 template <int D, int FMT>
 __device__ __forceinline__ void prefix_load(const PrefixParams& p, uint32_t base, volatile int* abort_flag, int w, int lane) {
     using C = PrefixCfg<D, FMT>;
     constexpr int RW = C::kRW, ES = FMT == kBf16 ? 2 : 1;  // rows of this warp; bytes of an element
     constexpr int CH = D * ES / 16, RPI = 32 / CH;         // 16-byte chunks of a row; rows of an instruction
-    static_assert(RPI >= 1 && RW % RPI == 0 && RW <= 32, "rows of a warp");
-    // K's and V's places: the tile whose slot is filled next, its rows looked up a
-    // slot ahead.  Lane r holds row r of this warp (element offset, or -1).
-    struct Place {
-        PrefixWalk<D, FMT> walk;
-        PrefixSegment s;
-        int j, left;       // tile, tiles of the segment after it
-        bool more;         // there is such a tile
-        int64_t off;
-        float ks, vs;      // K's place: the row's scales
-    };
-    Place pk = {PrefixWalk<D, FMT>(p), {}, 0, 0, true, -1, 0.f, 0.f}, pv = pk;
-    auto advance = [&](Place& at, bool scales) {
-        if (at.left == 0) {
-            at.more = at.walk.next(p, at.s);
-            at.j = at.s.j0;
-            at.left = at.s.n;
-            if (!at.more) return;
-        } else {
-            ++at.j;
-        }
-        --at.left;
-        at.off = -1;
-        at.ks = at.vs = 0.f;
-        const int64_t t = (int64_t)at.j * C::kT + w * RW + lane;
-        if (lane < RW && t < at.s.tokens) {
-            const int32_t id = p.table[(int64_t)at.s.start * p.table_stride + (t >> p.lbs)];
-            const int slot = (int)t & ((1 << p.lbs) - 1);
-            if (id < 0 || (int64_t)id >= p.num_blocks) {
-                atomicOr(p.err, PDA_DEVERR_BAD_BLOCK_ID_);
-                return;
-            }
-            at.off = (int64_t)id * p.blk_s + (int64_t)slot * p.tok_s + (int64_t)at.s.kvh * p.kvh_s;
-            if (FMT != kBf16 && scales) {
-                const float* sc = p.scales + (((((int64_t)id * p.Hkv + at.s.kvh) * 2) << p.lbs) + slot);
-                at.ks = sc[0];
-                at.vs = sc[(int64_t)1 << p.lbs];
-            }
-        }
-    };
-    advance(pk, true);
-    advance(pv, false);
+    constexpr int RC = D < 128 ? D : 128;                  // codes of a row in one piece (8-bit)
+    static_assert(RW == 32 && RPI >= 1, "a lane a row");
+    const bool k = w < 2;
+    const int half = w & 1, row0 = half * RW;
+    const uint8_t* pool = k ? p.k_base : p.v_base;
+    const CUtensorMap* map = k ? &p.tm_k : &p.tm_v;
+    const uint64_t once = policy_evict_first(), keep = policy_evict_normal();  // rows that one unit reads, or several
     const int chunk = lane % CH, sub = lane / CH;
-    uint32_t issued = 0, spread = 0, tiles = 0;  // slots filled, slots converted (8-bit), tiles whose K is filled
-    int ki = 0;  // K tiles of V's segment that are filled
-    // (8-bit) codes in their slot: the warp's rows back to back over its parts of the slabs
-    auto code_at = [&](uint32_t slot, int o) {
-        return slot + (uint32_t)(o / (RW * 128)) * (C::kT * 128) + (uint32_t)(w * RW * 128 + o % (RW * 128));
+    const int bs = 1 << p.lbs, rb = min(bs, RW);  // rows of a block, of a box
+    // The tile to fill and, looked up a tile ahead, the block id of this lane's
+    // row of it as read (checked when it is used, so that nothing waits for it).
+    constexpr int32_t kNoRow = INT32_MIN;
+    PrefixWalk<D, FMT> walk(p);
+    PrefixSegment s = {}, s2 = {};
+    bool more = walk.next(p, s), more2 = more && walk.next(p, s2);
+    int32_t id_next = kNoRow;
+    auto look_up = [&](const PrefixSegment& at, int tile) {
+        const int64_t t = (int64_t)tile * C::kT + row0 + lane;
+        id_next = t < at.tokens ? p.table[(int64_t)at.start * p.table_stride + (t >> p.lbs)] : kNoRow;
     };
-    auto fill = [&](uint32_t n, const uint8_t* pool, int64_t now) {  // slot number n
-        const uint32_t slot = base + C::kSlot0 + (n % C::kSlots) * C::kSlotBytes;
-#pragma unroll 4
-        for (int r0 = 0; r0 < RW; r0 += RPI) {
-            const int r = r0 + sub;
-            const int64_t o = __shfl_sync(0xffffffffu, now, r);
-            uint32_t dst;
-            if constexpr (FMT == kBf16) {
-                const int t = w * RW + r;
-                dst = slot + (uint32_t)(chunk >> 3) * (C::kT * 128) + (uint32_t)t * 128 + (uint32_t)(((chunk & 7) ^ (t & 7)) << 4);
-            } else {
-                dst = code_at(slot, r * D + chunk * 16);
-            }
-            cp_async_16_or_0(dst, pool + (o < 0 ? 0 : o * ES) + chunk * 16, o >= 0);
-        }
-        if constexpr (FMT == kBf16) cp_async_mbar_arrive_noinc(base + C::kFull + 8 * (n % C::kSlots));
-        else cp_async_mbar_arrive_noinc(base + C::kLanded + 8 * (w * C::kSlots + n % C::kSlots));
+    if (more) look_up(s, s.j0);
+    // (8-bit) codes in their slot: up to 128 of a row at a time over the warp's part of a slab each
+    auto code_at = [&](uint32_t slot, int r, int c) {
+        return slot + (uint32_t)(c / RC) * (C::kT * 128) + (uint32_t)(row0 * 128 + r * RC + c % RC);
     };
-    auto convert = [&](uint32_t n) {
+    auto convert = [&](uint32_t slot) {
         if constexpr (FMT != kBf16) {
-            const uint32_t slot = base + C::kSlot0 + (n % C::kSlots) * C::kSlotBytes;
             constexpr int N = RW * D / 16 / 32;  // 16-code chunks of a lane
             uint32_t x[N][4];
 #pragma unroll
-            for (int i = 0; i < N; ++i) lds_v4(code_at(slot, (lane + 32 * i) * 16), x[i]);
+            for (int i = 0; i < N; ++i) lds_v4(code_at(slot, (lane + 32 * i) / CH, (lane + 32 * i) % CH * 16), x[i]);
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const int at = lane + 32 * i, t = w * RW + at / CH, c = 2 * (at % CH);  // row, first 8-column chunk
+                const int at = lane + 32 * i, t = row0 + at / CH, c = 2 * (at % CH);  // row, first 8-column chunk
                 const uint32_t row = slot + (uint32_t)(c >> 3) * (C::kT * 128) + (uint32_t)t * 128;
                 uint32_t y[8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) codes_to_bf16<FMT>(x[i][k], y[2 * k], y[2 * k + 1]);
+                for (int e = 0; e < 4; ++e) codes_to_bf16<FMT>(x[i][e], y[2 * e], y[2 * e + 1]);
                 sts_v4(row + (uint32_t)(((c & 7) ^ (t & 7)) << 4), y[0], y[1], y[2], y[3]);
                 sts_v4(row + (uint32_t)((((c & 7) + 1) ^ (t & 7)) << 4), y[4], y[5], y[6], y[7]);
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(base + C::kFull + 8 * (n % C::kSlots));
         }
     };
-    bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (warp_wait(bar, parity)) return true;
+        if (lane_wait(bar, parity)) return true;
         atomicOr(p.err, PDA_DEVERR_TIMEOUT_);
         *abort_flag = 1;
         return false;
     };
-    // The order of a segment's n tiles: K of tile i once V of tile i - ahead is
-    // filled, and V of tile i once K has run `ahead` tiles past it or out of tiles.
-    int vi = 0;  // V's tile within its segment
-    while (ok && (pv.more || spread < issued)) {
-        if (__any_sync(0xffffffffu, *abort_flag)) break;
-        bool can = pv.more;
-        const uint32_t empty = base + C::kEmpty + 8 * (issued % C::kSlots), parity = ((issued / C::kSlots) & 1u) ^ 1u;
-        if (can && FMT != kBf16 && spread < issued) can = __all_sync(0xffffffffu, mbar_test_wait(empty, parity));
+    // A segment's slots, from number `first` on, are in the order in which the
+    // products use them: K of tiles 0 .. ahead - 1, then V of tile i and K of
+    // tile i + ahead in turn while there are any, then the other V.  K of tile i
+    // comes after i of K and i - ahead + 1 of V; V of tile i after i of V and
+    // i + ahead of K, as many as there are.
+    uint32_t first = 0, tiles = 0;  // slots of the segments before; tiles whose K is filled
+    uint32_t issued = 0, spread = 0, queue = 0;  // (8-bit) slots filled, converted; lane l & 31: the l-th one's number
+    int i = 0;                      // tile of the segment
+    bool ok = true;
+    while (ok && (more || spread != issued)) {
+        const int ahead = C::ahead(s.dual);
+        const uint32_t n = first + (k ? i + max(0, i - ahead + 1) : i + min(i + ahead, s.n));
+        const uint32_t at = n % C::kSlots, slot = base + C::kSlot0 + at * C::kSlotBytes;
+        const uint32_t empty = base + C::kEmpty + 8 * at, parity = ((n / C::kSlots) & 1u) ^ 1u;
+        bool can = more;
+        if (FMT != kBf16 && can && spread != issued) can = __all_sync(0xffffffffu, mbar_test_wait(empty, parity));
         if (can) {
             if (!(ok = wait(empty, parity))) break;
-            if (ki < min(pv.s.n, vi + C::ahead(pv.s.dual))) {
-                if constexpr (FMT != kBf16) {
-                    if (lane < RW) {
-                        const uint32_t sc = base + C::kScale0 + (tiles % C::kScaleTiles) * (C::kT * 8) + (uint32_t)(w * RW + lane) * 4;
-                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc), "f"(pk.ks) : "memory");
-                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(sc + C::kT * 4), "f"(pk.vs * 9.094947e-13f) : "memory");  // 2^-40
-                    }
-                }
-                ++tiles;
-                ++ki;
-                const int64_t now = pk.off;
-                advance(pk, true);
-                fill(issued, p.k_base, now);
-            } else {
-                const int64_t now = pv.off;
-                const int n = pv.s.n;
-                if (++vi == n) vi = ki = 0;
-                advance(pv, false);
-                fill(issued, p.v_base, now);
+            const int tile = s.j0 + i;
+            int32_t id = id_next;
+            if (i + 1 < s.n) look_up(s, tile + 1);
+            else if (more2) look_up(s2, s2.j0);
+            if (id < 0 || (int64_t)id >= p.num_blocks) {
+                if (id != kNoRow) atomicOr(p.err, PDA_DEVERR_BAD_BLOCK_ID_);
+                id = -1;  // zeros
             }
-            ++issued;
-            if (FMT == kBf16) spread = issued;
-        } else {
-            if (!(ok = wait(base + C::kLanded + 8 * (w * C::kSlots + spread % C::kSlots), (spread / C::kSlots) & 1u))) break;
-            convert(spread);
+            const uint32_t bar = FMT == kBf16 ? base + C::kFull + 8 * at : base + C::kLanded + 8 * (2 * at + half);
+            const uint32_t to = base + C::kScale0 + (FMT == kBf16 ? 0 : tiles % C::kRing) * (C::kT * 8) + (uint32_t)row0 * 4;
+            if (p.boxes) {
+                // lane b * pieces + h: box b, piece h of its columns
+                constexpr int kPieces = FMT == kBf16 ? D / 64 : D / RC;
+                const int b = lane / kPieces, h = lane % kPieces, r = min(b * rb, RW - 1);
+                const bool box = b * rb < RW;
+                const int32_t bid = __shfl_sync(0xffffffffu, id, r);
+                const bool scaled = FMT != kBf16 && k && box && h == 0;
+                uint32_t bytes = RW * D * ES;
+                if constexpr (FMT != kBf16) bytes += __popc(__ballot_sync(0xffffffffu, scaled && bid >= 0)) * 2u * rb * 4u;
+                if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+                __syncwarp();
+                if (box) {
+                    const int in = (row0 + r) & (bs - 1);  // the box's first row in its block (tiles hold whole blocks)
+                    if (scaled) {
+                        const float* sc = p.scales + (((((int64_t)bid * p.Hkv + s.kvh) * 2) << p.lbs) + in);
+                        if (bid >= 0) {
+                            bulk_load(to + 4 * r, sc, 4 * rb, bar);
+                            bulk_load(to + C::kT * 4 + 4 * r, sc + bs, 4 * rb, bar);
+                        } else {
+                            for (int e = 0; e < rb; e += 4) {
+                                sts_v4(to + 4 * (r + e), 0u, 0u, 0u, 0u);
+                                sts_v4(to + C::kT * 4 + 4 * (r + e), 0u, 0u, 0u, 0u);
+                            }
+                        }
+                    }
+                    const uint32_t dst = FMT == kBf16 ? slot + (uint32_t)h * (C::kT * 128) + (uint32_t)(row0 + r) * 128
+                                                      : code_at(slot, r, h * RC);
+                    // (the id past the last one is outside the view: zeros)
+                    tma_load_5d(dst, map, 0, in, h, s.kvh, bid < 0 ? (int32_t)p.num_blocks : bid, bar,
+                                s.dual || s.pair > 0 ? keep : once);
+                }
+            } else {
+                const int in = (row0 + lane) & (bs - 1);
+                const int64_t off = id < 0 ? -1 : (int64_t)id * p.blk_s + (int64_t)in * p.tok_s + (int64_t)s.kvh * p.kvh_s;
+                if (FMT != kBf16 && k) {
+                    const float* sc = p.scales + (id < 0 ? 0 : ((((int64_t)id * p.Hkv + s.kvh) * 2) << p.lbs) + in);
+                    cp_async_4_or_0(to + 4 * lane, sc, id >= 0);
+                    cp_async_4_or_0(to + C::kT * 4 + 4 * lane, sc + (id < 0 ? 0 : bs), id >= 0);
+                }
+#pragma unroll 2
+                for (int r0 = 0; r0 < RW; r0 += RPI) {
+                    const int r = r0 + sub, t = row0 + r;
+                    const int64_t o = __shfl_sync(0xffffffffu, off, r);
+                    const uint32_t dst = FMT == kBf16 ? slot + (uint32_t)(chunk >> 3) * (C::kT * 128) + (uint32_t)t * 128 +
+                                                            (uint32_t)(((chunk & 7) ^ (t & 7)) << 4)
+                                                      : code_at(slot, r, chunk * 16);
+                    cp_async_16_or_0(dst, pool + (o < 0 ? 0 : o * ES) + chunk * 16, o >= 0);
+                }
+                cp_async_mbar_arrive_noinc(bar);
+            }
+            ++tiles;
+            if constexpr (FMT != kBf16) {
+                if (lane == (int)(issued & 31u)) queue = n;
+                ++issued;
+            }
+            if (++i == s.n) {
+                first += 2 * s.n;
+                i = 0;
+                s = s2;
+                more = more2;
+                more2 = more && walk.next(p, s2);
+            }
+        } else if constexpr (FMT != kBf16) {
+            const uint32_t m = __shfl_sync(0xffffffffu, queue, spread & 31u), c = m % C::kSlots;
+            if (!(ok = wait(base + C::kLanded + 8 * (2 * c + half), (m / C::kSlots) & 1u))) break;
+            convert(base + C::kSlot0 + c * C::kSlotBytes);
+            if (lane == 0) mbar_arrive(base + C::kFull + 8 * c);
             ++spread;
         }
     }
@@ -349,12 +377,13 @@ __device__ __forceinline__ void prefix_mma(const PrefixParams& p, uint32_t base,
     constexpr uint32_t idS = umma_idesc_bf16(128, C::kT, false), idO = umma_idesc_bf16(128, D, true);
     PrefixWalk<D, FMT> walk(p);
     PrefixSegment s;
-    uint32_t next = 0, segs = 0;           // the ring's next slot; segments begun
+    uint32_t next = 0, segs = 0;              // the ring's next slot; segments begun
     uint32_t sc[2] = {0, 0}, pc[2] = {0, 0};  // S and P V issued, per stream
+    const bool one = elect_one();
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (*abort_flag == 0 && mbar_wait_bounded(bar, parity, kWaitLimitNs)) return true;
-        if (*abort_flag == 0) atomicOr(p.err, PDA_DEVERR_TIMEOUT_);
+        if (lane_wait(bar, parity)) return true;
+        if (one) atomicOr(p.err, PDA_DEVERR_TIMEOUT_);
         *abort_flag = 1;
         return ok = false;
     };
@@ -366,55 +395,64 @@ __device__ __forceinline__ void prefix_mma(const PrefixParams& p, uint32_t base,
         return true;
     };
     while (ok && walk.next(p, s)) {
-        // item k: stream k % kStreams, its tile k / 2 (two q tiles) or k
-        const int items = s.dual ? 2 * s.n : s.n, look = min(2 * C::kStreams, items);
+        // item k: stream k % kStreams, its tile k / 2 (two q tiles) or k.  Its S
+        // comes `look` items before its P V, its stream's P V before last.
+        const int items = s.dual ? 2 * s.n : s.n, look = 2 * C::kStreams;
         if (!wait(base + C::kQ, segs & 1u)) break;
         ++segs;
         uint32_t k_slot = 0, v_slot = 0;
-        auto qk = [&](int k) {
-            const bool first = !s.dual || (k & 1) == 0, last = !s.dual || (k & 1) == 1;
-            if (first && !take(k_slot)) return;
-            tc_fence_after();
-            const int st = C::kStreams == 2 ? k & 1 : 0;
-            const uint32_t buf = sc[st] & 1u;
-            const uint32_t sQ = base + (s.dual ? st : 0) * C::kQTileBytes, sK = base + C::kSlot0 + k_slot * C::kSlotBytes;
+#pragma unroll 1
+        for (int k = -look; ok && k < items; ++k) {
+            if (k >= 0) {
+                const bool first = !s.dual || (k & 1) == 0, last = !s.dual || (k & 1) == 1;
+                const int st = C::kStreams == 2 ? k & 1 : 0;
+                const uint32_t buf = pc[st] & 1u;
+                if (first && !take(v_slot)) break;
+                if (!wait(base + C::kP + 16 * st + 8 * buf, (pc[st] >> 1) & 1u)) break;
+                tc_fence_after();
+                const uint32_t tP = tmem + st * 2 * C::kT + buf * C::kT, tO = tmem + C::kTmO + st * D;
+                const uint64_t v = umma_sdesc(base + C::kSlot0 + v_slot * C::kSlotBytes, C::kT * 128, 1024);
+                if (one) {
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-                umma_bf16_ss(tmem + st * 2 * C::kT + buf * C::kT,
-                             umma_sdesc(sQ + (ks >> 2) * (128 * 128) + (ks & 3) * 32, 16, 1024),
-                             umma_sdesc(sK + (ks >> 2) * (C::kT * 128) + (ks & 3) * 32, 16, 1024), idS, ks > 0);
-            umma_commit(base + C::kS + 16 * st + 8 * buf);
-            if (last) umma_commit(base + C::kEmpty + 8 * k_slot);
-            ++sc[st];
-        };
-        for (int k = 0; ok && k < look; ++k) qk(k);
-        for (int k = 0; ok && k < items; ++k) {
-            const bool first = !s.dual || (k & 1) == 0, last = !s.dual || (k & 1) == 1;
-            const int st = C::kStreams == 2 ? k & 1 : 0;
-            const uint32_t buf = pc[st] & 1u;
-            if (first && !take(v_slot)) break;
-            if (!wait(base + C::kP + 16 * st + 8 * buf, (pc[st] >> 1) & 1u)) break;
-            tc_fence_after();
-            const uint32_t sV = base + C::kSlot0 + v_slot * C::kSlotBytes, tP = tmem + st * 2 * C::kT + buf * C::kT;
-            const uint32_t tO = tmem + C::kTmO + st * D;
-            bool acc = k >= C::kStreams;
-#pragma unroll
-            for (int ks = 0; ks < C::kT / 16; ++ks) {
-                const uint64_t v = umma_sdesc(sV + 2048 * ks, C::kT * 128, 1024);
-                umma_bf16_ts(tO, tP + 8 * ks, v, idO, acc);
-                umma_bf16_ts(tO, tP + C::kT / 2 + 8 * ks, v, idO, true);
-                acc = true;
+                    for (int ks = 0; ks < C::kT / 16; ++ks) {
+                        const uint32_t part = tP + ks / 2 * 32 + ks % 2 * 8;
+                        umma_bf16_ts(tO, part, v + 128 * ks, idO, ks > 0 || k >= C::kStreams);  // 16 rows of 128 bytes
+                        umma_bf16_ts(tO, part + 16, v + 128 * ks, idO, true);
+                    }
+                    if (last) umma_commit(base + C::kEmpty + 8 * v_slot);
+                    umma_commit(base + C::kPV + 8 * st);
+                    if (k == items - 1) umma_commit(base + C::kO);
+                }
+                __syncwarp();
+                ++pc[st];
             }
-            if (last) umma_commit(base + C::kEmpty + 8 * v_slot);
-            umma_commit(base + C::kPV + 8 * st);
-            if (k == items - 1) umma_commit(base + C::kO);
-            ++pc[st];
-            if (k + look < items) qk(k + look);
+            const int i = k + look;
+            if (i < items) {
+                const bool first = !s.dual || (i & 1) == 0, last = !s.dual || (i & 1) == 1;
+                const int st = C::kStreams == 2 ? i & 1 : 0;
+                const uint32_t buf = sc[st] & 1u;
+                if (first && !take(k_slot)) break;
+                tc_fence_after();
+                const uint32_t tS = tmem + st * 2 * C::kT + buf * C::kT;
+                const uint64_t q = umma_sdesc(base + (s.dual ? st : 0) * C::kQTileBytes, 16, 1024);
+                const uint64_t kk = umma_sdesc(base + C::kSlot0 + k_slot * C::kSlotBytes, 16, 1024);
+                if (one) {
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks)  // 32 bytes a step, slabs of 128 and of kT rows
+                        umma_bf16_ss(tS, q + (ks >> 2) * (128 * 8) + (ks & 3) * 2, kk + (ks >> 2) * (C::kT * 8) + (ks & 3) * 2,
+                                     idS, ks > 0);
+                    umma_commit(base + C::kS + 16 * st + 8 * buf);
+                    if (last) umma_commit(base + C::kEmpty + 8 * k_slot);
+                }
+                __syncwarp();
+                ++sc[st];
+            }
         }
     }
     // every product has completed before the tensor memory is freed
-    umma_commit(base + C::kFin);
-    if (!mbar_wait_bounded(base + C::kFin, 0, kWaitLimitNs)) atomicOr(p.err, PDA_DEVERR_TIMEOUT_);
+    if (one) umma_commit(base + C::kFin);
+    __syncwarp();
+    if (!lane_wait(base + C::kFin, 0) && one) atomicOr(p.err, PDA_DEVERR_TIMEOUT_);
 }
 
 // ------------------------------------------------------------------ softmax
@@ -441,8 +479,8 @@ template <int D, int FMT>
 __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, uint32_t base, uint8_t* smem, volatile int* abort_flag,
                                                uint32_t tmem, int warp, int lane) {
     using C = PrefixCfg<D, FMT>;
-    constexpr int kT = C::kT;
-    constexpr float kBack = FMT == kBf16 ? 1.f : 1.0995116e12f;  // 2^40
+    constexpr int kT = C::kT, kPart = 32;
+    constexpr float kDown = FMT == kBf16 ? 0.f : 40.f, kBack = FMT == kBf16 ? 1.f : 1.0995116e12f;  // 2^40
     const int st = warp >> 2, w = warp & 3, row = 32 * w + lane;
     const uint32_t tl = tmem + ((uint32_t)(32 * w) << 16);
     float* ml = reinterpret_cast<float*>(smem);  // [stream][2][128], over the q rows once they are used
@@ -454,7 +492,7 @@ __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, uint32_t b
     const bool plain = p.cap == 0.f && p.slopes == nullptr;
     uint32_t tile0 = 0, segs = 0, done = 0, cphase = 0;  // done: items of this stream
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (warp_wait(bar, parity)) return true;
+        if (lane_wait(bar, parity)) return true;
         atomicOr(p.err, PDA_DEVERR_TIMEOUT_);
         *abort_flag = 1;
         return false;
@@ -464,7 +502,6 @@ __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, uint32_t b
         return __all_sync(0xffffffffu, ok ? 1 : 0) != 0;
     };
     while (walk.next(p, s)) {
-        if (__any_sync(0xffffffffu, *abort_flag)) return;
         const int tile = s.pair * C::kStreams + (s.dual ? st : 0);
         // the segment's q rows, in the swizzle of the products' operand: a
         // stream its own tile, or both streams one
@@ -505,53 +542,53 @@ __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, uint32_t b
             tc_fence_after();
             if (!idle) {
                 const int t0 = (s.j0 + jj) * kT, seen = vis - t0;  // the tile's first token; tokens of it in sight
-                float v[kT];
-                tmem_ld_row(tS, v);
-                // scores in base-2 units; a bare product is scaled when its weight is taken
+                // scores in base-2 units, a part of the row at a time (unrolled, the loop
+                // would not stay in the instruction caches beside the other warps'); what
+                // is more than a product goes back to tensor memory for the second pass
                 const bool cut = __any_sync(0xffffffffu, seen < kT), bare = FMT == kBf16 && plain && !cut;
                 const float* kscale = reinterpret_cast<const float*>(smem + C::kScale0) +
-                                      (FMT == kBf16 ? 0 : (tile0 + jj) % C::kScaleTiles * (2 * kT));
-                float top;
-                if (bare) {
-                    float hi = v[0], lo = v[0];
+                                      (FMT == kBf16 ? 0 : (tile0 + jj) % C::kRing * (2 * kT));
+                const float f = bare ? p.scale_log2 : 1.f;
+                float top = kNegInf;
+#pragma unroll 1
+                for (int c = 0; c < kT; c += kPart) {
+                    float v[kPart], two[2] = {kNegInf, kNegInf};
+                    tmem_ld_row(tS + c, v);
+                    if (!bare) {
 #pragma unroll
-                    for (int i = 1; i < kT; ++i) {
-                        if (p.scale_log2 >= 0.f) hi = fmaxf(hi, v[i]);
-                        else lo = fminf(lo, v[i]);
-                    }
-                    top = (p.scale_log2 >= 0.f ? hi : lo) * p.scale_log2;
-                } else {
-                    float two[2] = {kNegInf, kNegInf};
-#pragma unroll
-                    for (int i = 0; i < kT; i += 4) {
-                        float4 x = make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
-                        if constexpr (FMT != kBf16) {
-                            const float4 y = *reinterpret_cast<const float4*>(kscale + i);
-                            x = make_float4(x.x * y.x, x.y * y.y, x.z * y.z, x.w * y.w);
+                        for (int i = 0; i < kPart; i += 4) {
+                            float4 x = make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
+                            if constexpr (FMT != kBf16) {
+                                const float4 y = *reinterpret_cast<const float4*>(kscale + c + i);
+                                x = make_float4(x.x * y.x, x.y * y.y, x.z * y.z, x.w * y.w);
+                            }
+                            v[i] *= x.x;
+                            v[i + 1] *= x.y;
+                            v[i + 2] *= x.z;
+                            v[i + 3] *= x.w;
                         }
-                        v[i] *= x.x;
-                        v[i + 1] *= x.y;
-                        v[i + 2] *= x.z;
-                        v[i + 3] *= x.w;
-                    }
-                    if (p.cap != 0.f) {
+                        if (p.cap != 0.f) {
 #pragma unroll
-                        for (int i = 0; i < kT; ++i) v[i] = capped(sc, v[i]);
-                    }
-                    if (p.slopes) {
-                        const float far = (float)(t0 - own);
+                            for (int i = 0; i < kPart; ++i) v[i] = capped(sc, v[i]);
+                        }
+                        if (p.slopes) {
+                            const float far = (float)(t0 + c - own);
 #pragma unroll
-                        for (int i = 0; i < kT; ++i) v[i] = fmaf(slope, far + (float)i, v[i]);
-                    }
-                    if (cut) {
+                            for (int i = 0; i < kPart; ++i) v[i] = fmaf(slope, far + (float)i, v[i]);
+                        }
+                        if (cut) {
 #pragma unroll
-                        for (int i = 0; i < kT; ++i)
-                            if (i >= seen) v[i] = kNegInf;
+                            for (int i = 0; i < kPart; ++i)
+                                if (i >= seen - c) v[i] = kNegInf;
+                        }
+#pragma unroll
+                        for (int i = 0; i < kPart; i += 16) tmem_st16(tS + c + i, *reinterpret_cast<const float(*)[16]>(v + i));
                     }
 #pragma unroll
-                    for (int i = 0; i < kT; ++i) two[i & 1] = fmaxf(two[i & 1], v[i]);
-                    top = fmaxf(two[0], two[1]);
+                    for (int i = 0; i < kPart; ++i) two[i & 1] = fmaxf(two[i & 1], v[i] * f);
+                    top = fmaxf(top, fmaxf(two[0], two[1]));
                 }
+                if (!bare) tmem_wait_st();
                 // lazy reference (kLazyLog2); O is scaled once this stream's last product with V is done
                 const bool up = top > m + kLazyLog2, scale_o = up && m != kNegInf;
                 if (__any_sync(0xffffffffu, scale_o)) {
@@ -569,14 +606,16 @@ __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, uint32_t b
                     }
                 }
                 if (up) m = top;
-                const float u = m == kNegInf ? 0.f : m, f = bare ? p.scale_log2 : 1.f;
+                const float u = (m == kNegInf ? 0.f : m) + kDown;
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                for (int c = 0; c < kT; c += kPart) {  // P over its part of S: high parts, then low parts
+                    float v[kPart];
+                    uint32_t hi[kPart / 2], lo[kPart / 2];
+                    tmem_ld_row(tS + c, v);
 #pragma unroll
-                for (int c = 0; c < kT; c += 32) {  // P over its S: high parts, then low parts
-                    uint32_t hi[16], lo[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float p0 = ex2(fmaf(v[c + 2 * i], f, -u)), p1 = ex2(fmaf(v[c + 2 * i + 1], f, -u));
+                    for (int i = 0; i < kPart / 2; ++i) {
+                        float p0 = ex2(fmaf(v[2 * i], f, -u)), p1 = ex2(fmaf(v[2 * i + 1], f, -u));
                         sum[i & 3] += p0 + p1;
                         if constexpr (FMT != kBf16) {
                             const float2 x = *reinterpret_cast<const float2*>(kscale + kT + c + 2 * i);
@@ -586,8 +625,8 @@ __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, uint32_t b
                         hi[i] = pack_bf16x2(p0, p1);
                         lo[i] = pack_bf16x2(p0 - bf16_lo(hi[i]), p1 - bf16_hi(hi[i]));
                     }
-                    tmem_st16u(tS + c / 2, hi);
-                    tmem_st16u(tS + kT / 2 + c / 2, lo);
+                    tmem_st16u(tS + c, hi);
+                    tmem_st16u(tS + c + kPart / 2, lo);
                 }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 tmem_wait_st();
@@ -638,7 +677,7 @@ __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, uint32_t b
                 }
             }
             if (g < s.rows && (!joined || st == 0))
-                reinterpret_cast<float2*>(p.part_ml)[at * 128 + row] = make_float2(m, l);
+                reinterpret_cast<float2*>(p.part_ml)[at * 128 + row] = make_float2(m, l * kBack);
         }
         tc_fence_before();
         if (!sync_all()) return;  // both streams have read both states
@@ -655,11 +694,11 @@ __global__ void __launch_bounds__(PrefixCfg<D, FMT>::kThreads, 1) prefix_kernel(
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
-            mbar_init(base + C::kFull + 8 * i, FMT == kBf16 ? C::kLoadWarps * 32 : C::kLoadWarps);
+            mbar_init(base + C::kFull + 8 * i, FMT == kBf16 && !p.boxes ? 64 : 2);
             mbar_init(base + C::kEmpty + 8 * i, 1);
         }
         if (FMT != kBf16)
-            for (int i = 0; i < C::kSlots * C::kLoadWarps; ++i) mbar_init(base + C::kLanded + 8 * i, 32);
+            for (int i = 0; i < C::kSlots * 2; ++i) mbar_init(base + C::kLanded + 8 * i, p.boxes ? 1 : 32);
         for (int i = 0; i < 4; ++i) {
             mbar_init(base + C::kS + 8 * i, 1);
             mbar_init(base + C::kP + 8 * i, 4);
@@ -673,6 +712,10 @@ __global__ void __launch_bounds__(PrefixCfg<D, FMT>::kThreads, 1) prefix_kernel(
         abort_flag = 0;
     }
     constexpr int kMmaWarp = C::kSoftWarps + C::kLoadWarps;
+    if (p.boxes && threadIdx.x == C::kSoftWarps * 32) {
+        prefetch_tensormap(&p.tm_k);
+        prefetch_tensormap(&p.tm_v);
+    }
     if (warp == kMmaWarp) {
         tmem_alloc(base + C::kTm, 512);
         tmem_relinquish();
@@ -703,8 +746,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, FMT>::kThreads, 1) prefix_kernel(
     } else if (warp < kMmaWarp) {
         prefix_load<D, FMT>(p, base, &abort_flag, warp - C::kSoftWarps, lane);
     } else {
-        if (lane == 0) prefix_mma<D, FMT>(p, base, &abort_flag, tmem);
-        __syncwarp();
+        prefix_mma<D, FMT>(p, base, &abort_flag, tmem);
     }
     __syncthreads();
     if (warp == kMmaWarp) {

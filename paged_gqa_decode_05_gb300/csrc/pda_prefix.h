@@ -9,6 +9,7 @@
 namespace pda {
 
 struct PrefixParams {
+    CUtensorMap tm_k, tm_v;     // boxes of min(block size, 32) rows (prefix_box in pda_scored_api.cu); with `boxes`
     const uint16_t* q;          // [B, q_len, Hq, D] bf16
     const uint8_t* k_base;      // pools, elements of the cache's format
     const uint8_t* v_base;
@@ -24,6 +25,7 @@ struct PrefixParams {
     float* part_ml;             // [slots][streams][128][2]
     uint32_t* err;
     int32_t table_stride, lbs;
+    int32_t boxes;              // rows come as TMA boxes (block sizes from 8), else one by one
     int32_t B, q_len, Hq, Hkv, G, n_groups;
     float scale_log2, cap, inv_cap;
     const float* slopes;

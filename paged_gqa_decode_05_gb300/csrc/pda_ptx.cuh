@@ -266,6 +266,15 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
         : "memory");
 }
 
+// Whether this is the warp's one elected thread (every lane calls).  Products
+// issued under it take their operands as the warp's; under `lane == 0` the
+// compiler has to expect several threads, each with operands of its own.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+
 // One arrival on the mbarrier once every tcgen05 operation this thread issued
 // before it has completed.
 __device__ __forceinline__ void umma_commit(uint32_t bar) {

@@ -178,6 +178,44 @@ SharedScratch shared_scratch(const pda_ctx* ctx, int32_t batch, int32_t q_len, i
     return s;
 }
 
+// A pool as boxes of the shared-prefix kernel: up to 32 rows of a block and kv
+// head, one 64-column slab in the swizzle of the products' operands (bf16), or
+// up to 128 codes a row as they are.
+bool encode_box(const pda_dims& d, const void* base, const pda_cache* c, CUtensorMap* tm) {
+    const bool bf16 = c->format == PDA_CACHE_BF16;
+    const cuuint64_t es = bf16 ? 2 : 1, cols = bf16 ? 64 : std::min(d.head_dim, 128);
+    const cuuint64_t dims[5] = {cols, (cuuint64_t)d.block_size, d.head_dim / cols, (cuuint64_t)d.num_kv_heads,
+                                (cuuint64_t)c->num_blocks};
+    const cuuint64_t strides[4] = {(cuuint64_t)c->tok_stride * es, cols * es, (cuuint64_t)c->kvh_stride * es,
+                                   (cuuint64_t)c->blk_stride * es};
+    const cuuint32_t box[5] = {(cuuint32_t)cols, (cuuint32_t)std::min(d.block_size, 32), 1, 1, 1}, one[5] = {1, 1, 1, 1, 1};
+    return pda::tensor_map_encoder()(tm, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 5,
+                                     const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                     bf16 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The maps of a cache for the shared-prefix kernel, encoded when it is another
+// than the last call's.  (Blocks below 8 rows do not fill a swizzle span, and an
+// id outside the pool, which reads as zeros, has to be an int32.)
+void prefix_maps(pda_ctx* ctx, const pda_cache* c, pda::PrefixParams* p) {
+    const pda_pool_key& k = ctx->prefix_key;
+    if (!(ctx->prefix_valid && ctx->prefix_format == c->format && k.k == c->k_pool && k.v == c->v_pool &&
+          k.num_blocks == c->num_blocks && k.blk == c->blk_stride && k.tok == c->tok_stride && k.kvh == c->kvh_stride)) {
+        ctx->prefix_boxes = ctx->dims.block_size >= 8 && c->num_blocks < INT32_MAX && pda::tensor_map_encoder() &&
+                            encode_box(ctx->dims, c->k_pool, c, &ctx->prefix_k) &&
+                            encode_box(ctx->dims, c->v_pool, c, &ctx->prefix_v);
+        ctx->prefix_key = {c->k_pool, c->v_pool, c->num_blocks, c->blk_stride, c->tok_stride, c->kvh_stride};
+        ctx->prefix_format = c->format;
+        ctx->prefix_valid = true;
+    }
+    p->boxes = ctx->prefix_boxes;
+    if (p->boxes) {
+        p->tm_k = ctx->prefix_k;
+        p->tm_v = ctx->prefix_v;
+    }
+}
+
 }  // namespace
 
 pda_status pda::scored_setup(pda_ctx* ctx, int optin) {
@@ -355,6 +393,7 @@ PDA_EXPORT pda_status pda_decode_shared(pda_ctx* ctx, const pda_bf16* q, const p
     sc.prefix_ctas = ctx->num_sms;
     sc.prefix_o = pp.part_o;
     sc.prefix_ml = pp.part_ml;
+    prefix_maps(ctx, cache, &pp);
     ctx->tile_steps = 0;
     if ((st = record(ctx, ctx->ev_begin, c.stream)) != PDA_OK) return st;
     const cudaError_t e = pda::launch_prefix(D, cache->format, pp, ctx->num_sms, c.stream);
