@@ -42,12 +42,14 @@
 
 namespace pda {
 
+constexpr int kPlanHere = 16;  // groups whose plan is kept in shared memory
+
 template <int D, int FMT>
 struct PrefixCfg {
     static constexpr int kT = kPrefixTile;               // tokens of a tile
     static constexpr int kStreams = prefix_streams(D);
     static constexpr int kSoftWarps = 4 * kStreams, kLoadWarps = 4;
-    static constexpr int kThreads = (kSoftWarps + kLoadWarps + 1) * 32;
+    static constexpr int kThreads = (kSoftWarps + kLoadWarps + kStreams) * 32;  // + a warp a stream that issues products
     static constexpr int kSlotBytes = kT * D * 2;        // K or V of a tile
     static constexpr int kQTileBytes = 128 * D * 2;
     static constexpr int kSlots = D == 64 ? 20 : D == 256 ? (FMT == kBf16 ? 5 : 4) : FMT == kBf16 ? 10 : 9;
@@ -69,7 +71,7 @@ struct PrefixCfg {
     static constexpr uint32_t kS = kLanded + 8 * kSlots * (FMT == kBf16 ? 0 : 2), kP = kS + 32, kPV = kP + 32,
                               kO = kPV + 16, kQ = kO + 8, kSync = kQ + 8, kFin = kSync + 8, kTm = kFin + 8, kEnd = kTm + 16;
     static constexpr uint32_t kSmem = kEnd + (1024 - 16);  // (dynamic shared memory starts on 16 bytes)
-    static_assert(kSmem <= 232448, "shared memory of an SM");
+    static_assert(kSmem + (kPlanHere + 1) * sizeof(PrefixGroup) + 16 <= 232448, "shared memory of an SM");
     // tiles that K runs ahead of V: a stream's two S
     static __device__ __forceinline__ int ahead(bool dual) { return dual || kStreams == 1 ? 2 : 4; }
     static_assert(kSlots >= 4 + 1 || kStreams == 1, "the ring holds what the products need at once");
@@ -90,22 +92,22 @@ template <int D, int FMT>
 struct PrefixWalk {
     using C = PrefixCfg<D, FMT>;
     int64_t pos, end;
-    __device__ __forceinline__ explicit PrefixWalk(const PrefixParams& p) {
-        const int64_t W = p.groups[p.n_groups].work, P = prefix_plan_ctas(W, gridDim.x), c = blockIdx.x;
+    __device__ __forceinline__ PrefixWalk(const PrefixParams& p, const PrefixGroup* groups) {
+        const int64_t W = groups[p.n_groups].work, P = prefix_plan_ctas(W, gridDim.x), c = blockIdx.x;
         pos = c < P ? cta_begin(c, W, P) : 0;
         end = c < P ? cta_begin(c + 1, W, P) : 0;
     }
-    __device__ __forceinline__ bool next(const PrefixParams& p, PrefixSegment& s) {
+    __device__ __forceinline__ bool next(const PrefixParams& p, const PrefixGroup* groups, PrefixSegment& s) {
         if (pos >= end) return false;
         int lo = 0, hi = p.n_groups - 1;  // the last group that starts at or before pos (groups without work precede)
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (p.groups[mid].work <= pos) lo = mid; else hi = mid - 1;
+            if (groups[mid].work <= pos) lo = mid; else hi = mid - 1;
         }
-        const PrefixGroup g = p.groups[lo];
+        const PrefixGroup g = groups[lo];
         const int rem = (int)pos - g.work, unit = rem / g.tiles;
         s.start = g.start;
-        s.rows = (p.groups[lo + 1].start - g.start) * p.q_len * p.G;
+        s.rows = (groups[lo + 1].start - g.start) * p.q_len * p.G;
         s.tokens = g.blocks << p.lbs;
         s.pair = unit / p.Hkv;
         s.kvh = unit - s.pair * p.Hkv;
@@ -118,10 +120,11 @@ struct PrefixWalk {
     }
 };
 
-// The plan of the groups.  Every CTA writes all of it, the same values, so that
-// each reads its own stores and the decode that follows finds it.  Run by warp 0.
+// The plan of the groups.  Every CTA makes all of it, in shared memory or, where
+// there are more than kPlanHere groups, in the call's scratch: the same values,
+// so that each reads its own stores.  Run by one warp.
 template <int D, int FMT>
-__device__ __forceinline__ void prefix_plan(const PrefixParams& p, int lane) {
+__device__ __forceinline__ void prefix_plan(const PrefixParams& p, PrefixGroup* groups, int lane) {
     using C = PrefixCfg<D, FMT>;
     int32_t top = 0, units = 0, work = 0;  // over the groups before
     bool bad = false;
@@ -166,7 +169,7 @@ __device__ __forceinline__ void prefix_plan(const PrefixParams& p, int lane) {
         }
         out.unit = units + us - u;
         out.work = work + wsum - w;
-        if (g <= p.n_groups) p.groups[g] = out;
+        if (g <= p.n_groups) groups[g] = out;
         top = __shfl_sync(0xffffffffu, m, 31);
         units += __shfl_sync(0xffffffffu, us, 31);
         work += __shfl_sync(0xffffffffu, wsum, 31);
@@ -212,7 +215,7 @@ __device__ __forceinline__ bool lane_wait(uint32_t bar, uint32_t parity) {
 
 // Loader warp w fills 32 rows (half w & 1) of the slots of K (w < 2) or of V.
 template <int D, int FMT>
-__device__ __forceinline__ void prefix_load(const PrefixParams& p, uint32_t base, volatile int* abort_flag, int w, int lane) {
+__device__ __forceinline__ void prefix_load(const PrefixParams& p, const PrefixGroup* groups, uint32_t base, volatile int* abort_flag, int w, int lane) {
     using C = PrefixCfg<D, FMT>;
     constexpr int RW = C::kRW, ES = FMT == kBf16 ? 2 : 1;  // rows of this warp; bytes of an element
     constexpr int CH = D * ES / 16, RPI = 32 / CH;         // 16-byte chunks of a row; rows of an instruction
@@ -228,9 +231,9 @@ __device__ __forceinline__ void prefix_load(const PrefixParams& p, uint32_t base
     // The tile to fill and, looked up a tile ahead, the block id of this lane's
     // row of it as read (checked when it is used, so that nothing waits for it).
     constexpr int32_t kNoRow = INT32_MIN;
-    PrefixWalk<D, FMT> walk(p);
+    PrefixWalk<D, FMT> walk(p, groups);
     PrefixSegment s = {}, s2 = {};
-    bool more = walk.next(p, s), more2 = more && walk.next(p, s2);
+    bool more = walk.next(p, groups, s), more2 = more && walk.next(p, groups, s2);
     int32_t id_next = kNoRow;
     auto look_up = [&](const PrefixSegment& at, int tile) {
         const int64_t t = (int64_t)tile * C::kT + row0 + lane;
@@ -356,7 +359,7 @@ __device__ __forceinline__ void prefix_load(const PrefixParams& p, uint32_t base
                 i = 0;
                 s = s2;
                 more = more2;
-                more2 = more && walk.next(p, s2);
+                more2 = more && walk.next(p, groups, s2);
             }
         } else if constexpr (FMT != kBf16) {
             const uint32_t m = __shfl_sync(0xffffffffu, queue, spread & 31u), c = m % C::kSlots;
@@ -371,15 +374,21 @@ __device__ __forceinline__ void prefix_load(const PrefixParams& p, uint32_t base
 
 // ------------------------------------------------------------------ products
 
+// The products of stream st.  A warp each, so that one's waits pass under the
+// other's products (one warp for both streams: 32 us for 26, 32768 tokens of 8
+// kv heads of 128 and 128 q rows).
 template <int D, int FMT>
-__device__ __forceinline__ void prefix_mma(const PrefixParams& p, uint32_t base, volatile int* abort_flag, uint32_t tmem) {
+__device__ __forceinline__ void prefix_mma(const PrefixParams& p, const PrefixGroup* groups, uint32_t base,
+                                           volatile int* abort_flag, uint32_t tmem, int st) {
     using C = PrefixCfg<D, FMT>;
     constexpr uint32_t idS = umma_idesc_bf16(128, C::kT, false), idO = umma_idesc_bf16(128, D, true);
-    PrefixWalk<D, FMT> walk(p);
+    PrefixWalk<D, FMT> walk(p, groups);
     PrefixSegment s;
-    uint32_t next = 0, segs = 0;              // the ring's next slot; segments begun
-    uint32_t sc[2] = {0, 0}, pc[2] = {0, 0};  // S and P V issued, per stream
+    uint32_t first = 0, segs = 0;   // slots of the segments before, segments
+    uint32_t sn = 0, pn = 0;        // S and P V issued
     const bool one = elect_one();
+    const uint32_t tS0 = tmem + st * 2 * C::kT, tO = tmem + C::kTmO + st * D;
+    const uint32_t kS = base + C::kS + 16 * st, kP = base + C::kP + 16 * st;
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
         if (lane_wait(bar, parity)) return true;
@@ -387,67 +396,64 @@ __device__ __forceinline__ void prefix_mma(const PrefixParams& p, uint32_t base,
         *abort_flag = 1;
         return ok = false;
     };
-    auto take = [&](uint32_t& slot) {  // the next slot, once it is full
-        slot = next % C::kSlots;
-        if (!wait(base + C::kFull + 8 * slot, (next / C::kSlots) & 1u)) return false;
-        ++next;
-        fence_proxy_async_smem();  // the loaders' cp.async writes
-        return true;
-    };
-    while (ok && walk.next(p, s)) {
-        // item k: stream k % kStreams, its tile k / 2 (two q tiles) or k.  Its S
-        // comes `look` items before its P V, its stream's P V before last.
-        const int items = s.dual ? 2 * s.n : s.n, look = 2 * C::kStreams;
+    while (ok && walk.next(p, groups, s)) {
+        // item k of this stream: tile k (two q tiles, or one stream) or every other one
+        const bool every = s.dual || C::kStreams == 1;
+        const int ahead = C::ahead(s.dual), items = every ? s.n : (s.n - st + 1) / 2;
+        const uint64_t q = umma_sdesc(base + (s.dual ? st : 0) * C::kQTileBytes, 16, 1024);
         if (!wait(base + C::kQ, segs & 1u)) break;
         ++segs;
-        uint32_t k_slot = 0, v_slot = 0;
+        // S of item k comes before P V of item k - 1: two S ahead of their P V
 #pragma unroll 1
-        for (int k = -look; ok && k < items; ++k) {
+        for (int k = -2; ok && k < items; ++k) {
             if (k >= 0) {
-                const bool first = !s.dual || (k & 1) == 0, last = !s.dual || (k & 1) == 1;
-                const int st = C::kStreams == 2 ? k & 1 : 0;
-                const uint32_t buf = pc[st] & 1u;
-                if (first && !take(v_slot)) break;
-                if (!wait(base + C::kP + 16 * st + 8 * buf, (pc[st] >> 1) & 1u)) break;
+                const int t = every ? k : 2 * k + st;
+                const uint32_t n = first + t + min(t + ahead, s.n), slot = n % C::kSlots, buf = pn & 1u;
+                if (!wait(base + C::kFull + 8 * slot, (n / C::kSlots) & 1u)) break;
+                if (!wait(kP + 8 * buf, (pn >> 1) & 1u)) break;
+                fence_proxy_async_smem();  // cp.async writes of the loaders
                 tc_fence_after();
-                const uint32_t tP = tmem + st * 2 * C::kT + buf * C::kT, tO = tmem + C::kTmO + st * D;
-                const uint64_t v = umma_sdesc(base + C::kSlot0 + v_slot * C::kSlotBytes, C::kT * 128, 1024);
+                const uint32_t tP = tS0 + buf * C::kT;
+                const uint64_t v = umma_sdesc(base + C::kSlot0 + slot * C::kSlotBytes, C::kT * 128, 1024);
                 if (one) {
 #pragma unroll
                     for (int ks = 0; ks < C::kT / 16; ++ks) {
                         const uint32_t part = tP + ks / 2 * 32 + ks % 2 * 8;
-                        umma_bf16_ts(tO, part, v + 128 * ks, idO, ks > 0 || k >= C::kStreams);  // 16 rows of 128 bytes
+                        umma_bf16_ts(tO, part, v + 128 * ks, idO, ks > 0 || k > 0);  // 16 rows of 128 bytes
                         umma_bf16_ts(tO, part + 16, v + 128 * ks, idO, true);
                     }
-                    if (last) umma_commit(base + C::kEmpty + 8 * v_slot);
+                    umma_commit(base + C::kEmpty + 8 * slot);
+                    if (C::kStreams == 2 && !s.dual) mbar_arrive(base + C::kEmpty + 8 * slot);  // for the other stream
                     umma_commit(base + C::kPV + 8 * st);
                     if (k == items - 1) umma_commit(base + C::kO);
                 }
                 __syncwarp();
-                ++pc[st];
+                ++pn;
             }
-            const int i = k + look;
+            const int i = k + 2;
             if (i < items) {
-                const bool first = !s.dual || (i & 1) == 0, last = !s.dual || (i & 1) == 1;
-                const int st = C::kStreams == 2 ? i & 1 : 0;
-                const uint32_t buf = sc[st] & 1u;
-                if (first && !take(k_slot)) break;
+                const int t = every ? i : 2 * i + st;
+                const uint32_t n = first + t + max(0, t - ahead + 1), slot = n % C::kSlots, buf = sn & 1u;
+                if (!wait(base + C::kFull + 8 * slot, (n / C::kSlots) & 1u)) break;
+                fence_proxy_async_smem();
                 tc_fence_after();
-                const uint32_t tS = tmem + st * 2 * C::kT + buf * C::kT;
-                const uint64_t q = umma_sdesc(base + (s.dual ? st : 0) * C::kQTileBytes, 16, 1024);
-                const uint64_t kk = umma_sdesc(base + C::kSlot0 + k_slot * C::kSlotBytes, 16, 1024);
+                const uint32_t tS = tS0 + buf * C::kT;
+                const uint64_t kk = umma_sdesc(base + C::kSlot0 + slot * C::kSlotBytes, 16, 1024);
                 if (one) {
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks)  // 32 bytes a step, slabs of 128 and of kT rows
                         umma_bf16_ss(tS, q + (ks >> 2) * (128 * 8) + (ks & 3) * 2, kk + (ks >> 2) * (C::kT * 8) + (ks & 3) * 2,
                                      idS, ks > 0);
-                    umma_commit(base + C::kS + 16 * st + 8 * buf);
-                    if (last) umma_commit(base + C::kEmpty + 8 * k_slot);
+                    umma_commit(kS + 8 * buf);
+                    umma_commit(base + C::kEmpty + 8 * slot);
+                    if (C::kStreams == 2 && !s.dual) mbar_arrive(base + C::kEmpty + 8 * slot);
                 }
                 __syncwarp();
-                ++sc[st];
+                ++sn;
             }
         }
+        if (one && ok && items == 0) mbar_arrive(base + C::kO);
+        first += 2 * s.n;
     }
     // every product has completed before the tensor memory is freed
     if (one) umma_commit(base + C::kFin);
@@ -476,7 +482,7 @@ __device__ __forceinline__ void tmem_ld_row(uint32_t taddr, float (&v)[N]) {
 }
 
 template <int D, int FMT>
-__device__ __forceinline__ void prefix_softmax(const PrefixParams& p, uint32_t base, uint8_t* smem, volatile int* abort_flag,
+__device__ __forceinline__ void prefix_softmax(const PrefixParams& p, const PrefixGroup* groups, uint32_t base, uint8_t* smem, volatile int* abort_flag,
                                                uint32_t tmem, int warp, int lane) {
     using C = PrefixCfg<D, FMT>;
     constexpr int kT = C::kT, kPart = 32;
@@ -484,7 +490,7 @@ __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, uint32_t b
     const int st = warp >> 2, w = warp & 3, row = 32 * w + lane;
     const uint32_t tl = tmem + ((uint32_t)(32 * w) << 16);
     float* ml = reinterpret_cast<float*>(smem);  // [stream][2][128], over the q rows once they are used
-    PrefixWalk<D, FMT> walk(p);
+    PrefixWalk<D, FMT> walk(p, groups);
     PrefixSegment s;
     Scoring sc = {};
     sc.cap = p.cap;
@@ -501,7 +507,7 @@ __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, uint32_t b
         const bool ok = consumer_sync(base + C::kSync, cphase, p.err, abort_flag);
         return __all_sync(0xffffffffu, ok ? 1 : 0) != 0;
     };
-    while (walk.next(p, s)) {
+    while (walk.next(p, groups, s)) {
         const int tile = s.pair * C::kStreams + (s.dual ? st : 0);
         // the segment's q rows, in the swizzle of the products' operand: a
         // stream its own tile, or both streams one
@@ -684,18 +690,33 @@ __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, uint32_t b
     }
 }
 
+__device__ __forceinline__ PrefixSeq prefix_seq(const PrefixParams& p, const PrefixGroup* groups, int b) {
+    int lo = 0, hi = p.n_groups;  // the first entry that starts past b
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (groups[mid].start <= b) lo = mid + 1; else hi = mid;
+    }
+    PrefixSeq s = {};
+    if (lo > 0 && b < groups[p.n_groups].start) {
+        const PrefixGroup g = groups[lo - 1];
+        s = {g.start, g.blocks, g.tiles, g.unit, g.work, groups[p.n_groups].work, {0, 0}};
+    }
+    return s;
+}
+
 template <int D, int FMT>
 __global__ void __launch_bounds__(PrefixCfg<D, FMT>::kThreads, 1) prefix_kernel(const __grid_constant__ PrefixParams p) {
     using C = PrefixCfg<D, FMT>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ int abort_flag;
+    __shared__ PrefixGroup plan[kPlanHere + 1];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (base - raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
             mbar_init(base + C::kFull + 8 * i, FMT == kBf16 && !p.boxes ? 64 : 2);
-            mbar_init(base + C::kEmpty + 8 * i, 1);
+            mbar_init(base + C::kEmpty + 8 * i, C::kStreams);
         }
         if (FMT != kBf16)
             for (int i = 0; i < C::kSlots * 2; ++i) mbar_init(base + C::kLanded + 8 * i, p.boxes ? 1 : 32);
@@ -704,10 +725,10 @@ __global__ void __launch_bounds__(PrefixCfg<D, FMT>::kThreads, 1) prefix_kernel(
             mbar_init(base + C::kP + 8 * i, 4);
         }
         for (int i = 0; i < 2; ++i) mbar_init(base + C::kPV + 8 * i, 1);
-        mbar_init(base + C::kO, 1);
+        mbar_init(base + C::kO, C::kStreams);
         mbar_init(base + C::kQ, C::kSoftWarps);
         mbar_init(base + C::kSync, C::kSoftWarps * 32);
-        mbar_init(base + C::kFin, 1);
+        mbar_init(base + C::kFin, C::kStreams);
         fence_mbar_init();
         abort_flag = 0;
     }
@@ -723,30 +744,22 @@ __global__ void __launch_bounds__(PrefixCfg<D, FMT>::kThreads, 1) prefix_kernel(
     }
     pdl_wait_primary();
     pdl_launch_dependents();
-    if (warp == 0) prefix_plan<D, FMT>(p, lane);
+    PrefixGroup* groups = p.n_groups <= kPlanHere ? plan : p.groups;
+    if (warp == 0) prefix_plan<D, FMT>(p, groups, lane);
     __syncthreads();
     tc_fence_after();
-    for (int b = blockIdx.x * C::kThreads + threadIdx.x; b < p.B; b += gridDim.x * C::kThreads) {
-        int lo = 0, hi = p.n_groups;  // the first entry that starts past b
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (p.groups[mid].start <= b) lo = mid + 1; else hi = mid;
-        }
-        PrefixSeq s = {};
-        if (lo > 0 && b < p.groups[p.n_groups].start) {
-            const PrefixGroup g = p.groups[lo - 1];
-            s = {g.start, g.blocks, g.tiles, g.unit, g.work, p.groups[p.n_groups].work, {0, 0}};
-        }
-        p.seqs[b] = s;
-    }
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + C::kTm);
     if (warp < C::kSoftWarps) {
-        prefix_softmax<D, FMT>(p, base, smem, &abort_flag, tmem, warp, lane);
+        prefix_softmax<D, FMT>(p, groups, base, smem, &abort_flag, tmem, warp, lane);
         tc_fence_before();
     } else if (warp < kMmaWarp) {
-        prefix_load<D, FMT>(p, base, &abort_flag, warp - C::kSoftWarps, lane);
+        prefix_load<D, FMT>(p, groups, base, &abort_flag, warp - C::kSoftWarps, lane);
     } else {
-        prefix_mma<D, FMT>(p, base, &abort_flag, tmem);
+        // what the sequences' own decode needs of the plan, while the first rows are on their way
+        if (warp == kMmaWarp)
+            for (int b = blockIdx.x * 32 + lane; b < p.B; b += gridDim.x * 32) p.seqs[b] = prefix_seq(p, groups, b);
+        __syncwarp();
+        prefix_mma<D, FMT>(p, groups, base, &abort_flag, tmem, warp - kMmaWarp);
     }
     __syncthreads();
     if (warp == kMmaWarp) {
