@@ -375,7 +375,8 @@ cudaError_t evict_setup() {
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
     const int64_t units = (int64_t)p.B * p.Hkv, tokens = (int64_t)p.table_stride << p.lbs;
     cudaError_t e;
-    if (tokens <= 8192) e = launch(choose_kernel<256>, units, 256, (size_t)tokens * 4, stream, p, (int32_t)tokens);
+    // threads for 4 tokens each, up to 1024: 256 units of 4096 tokens 27 us with 256, 8.1 with 1024
+    if (tokens <= 1024) e = launch(choose_kernel<256>, units, 256, (size_t)tokens * 4, stream, p, (int32_t)tokens);
     else {
         const int32_t cached = (int32_t)(tokens < kMostKeys ? tokens : kMostKeys);
         e = launch(choose_kernel<1024>, units, 1024, (size_t)cached * 4, stream, p, cached);
@@ -391,13 +392,12 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
             default: return cudaErrorInvalidValue;
         }
     }
-    // whole rows where there are CTAs enough, else 64-byte parts of them
-    const int32_t part = units * 2 >= 2 * p.sms || p.row_bytes < 128 ? p.row_bytes : 64, parts = p.row_bytes / part;
+    // 128-byte parts of rows (a step then takes 128 rows), or of 64 bytes where CTAs are few
+    const int32_t row = p.row_bytes < 128 ? p.row_bytes : 128;
+    const int32_t part = units * 2 * (p.row_bytes / row) >= 2 * p.sms ? row : 64, parts = p.row_bytes / part;
     switch (part) {
         case 64: return launch(pack_kernel<64>, units * 2 * parts, kPackThreads, 0, stream, p, parts);
         case 128: return launch(pack_kernel<128>, units * 2 * parts, kPackThreads, 0, stream, p, parts);
-        case 256: return launch(pack_kernel<256>, units * 2 * parts, kPackThreads, 0, stream, p, parts);
-        case 512: return launch(pack_kernel<512>, units * 2 * parts, kPackThreads, 0, stream, p, parts);
         default: return cudaErrorInvalidValue;
     }
 }

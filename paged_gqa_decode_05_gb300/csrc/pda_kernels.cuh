@@ -183,12 +183,13 @@ __device__ __forceinline__ int32_t tokens_of(const SplitParams& p, int s, int32_
     return len < 0 ? 0 : len;
 }
 
-// Blocks of launch row s that the walk leaves out (kScored): those that its group shares.
+// Blocks of launch row s that the walk leaves out: those that its group shares
+// (from L2: the prefix kernel has just written them).
 template <int MODE>
 __device__ __forceinline__ int32_t skip_of(const SplitParams& p, int s) {
-    if constexpr (MODE != kScored) return 0;
+    if constexpr (!is_scored(MODE)) return 0;
     if (p.sc.seqs == nullptr) return 0;
-    return __ldcg(&p.sc.seqs[p.sc.seq0 + row_info<is_multi(MODE)>(p, s).b].blocks);
+    return __ldcg(&p.sc.seqs[row_info<is_multi(MODE)>(p, s).b].blocks);
 }
 
 // Blocks of sequence b with length entry L, validated and clamped (flags
@@ -444,7 +445,7 @@ __device__ __forceinline__ void run_producer(const SplitParams& p, uint32_t base
     int32_t w[4], f[4], nx[4];
     int32_t lv = bs;   // valid slots of this sequence's last block
     int32_t nle = 0;   // the next sequence's last_entry, loaded a unit ahead
-    int32_t sk = 0, skn = 0;  // blocks that the walks of b and bn leave out (kScored)
+    int32_t sk = 0, skn = 0;  // blocks that the walks of b and bn leave out (the scored modes)
     int bn = p.B;               // next non-empty sequence
     // The launch rows of b and bn (multi-query: table row, first query, query
     // count) and b's causal limit, computed once per sequence, not per stage.
@@ -510,7 +511,7 @@ __device__ __forceinline__ void run_producer(const SplitParams& p, uint32_t base
         }
         if (bn < p.B) load_ids(nx, rn.b, 0, real_blocks(pfx[bn + 1] - pfx[bn], p.unit_cost), skn);
         lv = last_block_slots<MQ>(p, b, nb + sk, e_cur);
-        if constexpr (MQ) lim = e_cur - p.q_len + ri.first;
+        if constexpr (MQ || is_scored(MODE)) lim = e_cur - p.q_len + ri.first;
     }
     // Past a unit's last block: skip its cost tail and move to the next unit
     // (the next kv head reuses the row's first ids; the next sequence's ids
@@ -530,7 +531,7 @@ __device__ __forceinline__ void run_producer(const SplitParams& p, uint32_t base
                 ri = rn;
                 sk = skn;
                 lv = last_block_slots<MQ>(p, b, nb + sk, nle);
-                if constexpr (MQ) lim = nle - p.q_len + ri.first;
+                if constexpr (MQ || is_scored(MODE)) lim = nle - p.q_len + ri.first;
                 bn = next_seq(b);
                 if (bn < p.B) {
                     rn = row_info<MQ>(p, bn);
@@ -731,7 +732,7 @@ __device__ __forceinline__ void merge_state(float& M, float& Ls, float4& Os, flo
     M = Mn;
 }
 
-// ---- kScored: scores capped and biased, and the states of a shared prefix
+// ---- the scored modes: scores capped and biased, written out; states handed on
 
 // cap * tanh(s / cap), s in base-2 units, from the definition, 1 - 2 / (1 + e)
 // with e = exp(2 s / cap): off by a few 2^-24 of the cap for any s, where the
@@ -739,91 +740,36 @@ __device__ __forceinline__ void merge_state(float& M, float& Ls, float4& Os, flo
 __device__ __forceinline__ float capped(const Scoring& sc, float s) {
     return fmaf(-2.f * sc.cap, rcp_approx(1.f + ex2(s * sc.inv_cap)), sc.cap);
 }
-// A score in base-2 units, capped and with slope * far added (far: the token's
-// place less the query's).
-__device__ __forceinline__ float score_of(const Scoring& sc, float s, float slope, float far) {
-    return fmaf(slope, far, sc.cap != 0.f ? capped(sc, s) : s);
-}
-
 // The slope of score column `col` of a segment (base-2 units).
 __device__ __forceinline__ float column_slope(const SplitParams& p, const StageMeta& m, int col) {
     if (p.sc.slopes == nullptr || col >= m.nr) return 0.f;
     return (p.sc.slopes[m.kvh * p.G + col % p.G]) * 1.4426950408889634f;
 }
 
-// Scores of row `row` of a stage, columns col and col + 1.
-__device__ __forceinline__ void put_scores(const SplitParams& p, const StageMeta& m, int row, int col, float a, float b) {
+// Where column `col` of a segment's scores lies for token 0; null: not asked for.
+__device__ __forceinline__ float* scores_of(const SplitParams& p, const StageMeta& m, int col) {
+    if (p.sc.scores == nullptr) return nullptr;
     const int64_t tokens = (int64_t)p.table_stride * p.bs, unit = (int64_t)m.b * p.Hkv + m.kvh;
-    float* at = p.sc.scores + (unit * tokens + (int64_t)m.j0 * p.bs + row) * p.rows_per_slot + col;
-    if (col + 1 < m.nr && (p.rows_per_slot & 1) == 0) {
+    return p.sc.scores + unit * tokens * p.rows_per_slot + col;
+}
+// Scores of columns col and col + 1 of a token, at its first.
+__device__ __forceinline__ void put_scores(float* at, bool pairs, bool first, bool second, float a, float b) {
+    if (pairs && second) {
         *reinterpret_cast<float2*>(at) = make_float2(a, b);
     } else {
-        if (col < m.nr) at[0] = a;
-        if (col + 1 < m.nr) at[1] = b;
+        if (first) at[0] = a;
+        if (second) at[1] = b;
     }
 }
 
-// The shared prefix of sequence b of the launch (from L2: the prefix kernel has
-// just written it).
-__device__ __forceinline__ PrefixSeq prefix_of(const SplitParams& p, int b) {
-    PrefixSeq ps = {};
-    if (p.sc.seqs) {
-        const int4* at = reinterpret_cast<const int4*>(p.sc.seqs + p.sc.seq0 + b);
-        const int4 x = __ldcg(at), y = __ldcg(at + 1);
-        ps = {x.x, x.y, x.z, x.w, y.x, y.y, {0, 0}};
-    }
-    return ps;
-}
-
-// Joins the state of an output row's shared prefix, which the prefix kernel
-// left in pieces, to (M, Ls, Os), columns d4 .. d4 + 3; and hands out the
-// row's (m, l).  Row r of a q tile and chunk d4 / 4 of it lie at [chunk][r].
-template <int D, bool kWide>
-__device__ __forceinline__ void join_prefix(const SplitParams& p, const PrefixSeq& ps, int b, int qi, int head, int d4,
-                                            float& M, float& Ls, float4& Os) {
-    const Scoring& sc = p.sc;
-    if (ps.tiles > 0) {
-        constexpr int kSub = prefix_streams(D);  // q tiles of a slot
-        const int kvh = head / p.G;
-        const int row = ((b + sc.seq0 - ps.start) * p.q_len + qi) * p.G + head - kvh * p.G;
-        const int tile = row >> 7, r = row & 127;
-        const int64_t W = ps.total, P = prefix_plan_ctas(W, sc.prefix_ctas);
-        const int unit = tile / kSub * p.Hkv + kvh;
-        const int64_t first = ps.work + (int64_t)unit * ps.tiles;
-        const int c0 = (int)cta_of_block(first, W, P), n = (int)cta_of_block(first + ps.tiles - 1, W, P) - c0 + 1;
-        const int64_t at = ((int64_t)ps.unit + unit + c0) * kSub + tile % kSub;
-        const float2* ml = reinterpret_cast<const float2*>(sc.prefix_ml) + at * 128 + r;
-        const float4* po = reinterpret_cast<const float4*>(sc.prefix_o) + (at * (D / 4) + d4 / 4) * 128 + r;
-        for (int c = 0; c < n; c += 8) {
-            float2 si[8];
-            float4 oi[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                si[k] = make_float2(kNegInf, 0.f);
-                oi[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (c + k < n) {
-                    si[k] = __ldcg(ml + (int64_t)(c + k) * kSub * 128);
-                    oi[k] = __ldcg(po + (int64_t)(c + k) * kSub * (D / 4) * 128);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) merge_state<kWide>(M, Ls, Os, si[k].x, si[k].y, oi[k]);
-        }
-    }
-    if (sc.row_ml && d4 == 0)
-        *reinterpret_cast<float2*>(sc.row_ml + (((int64_t)b * p.q_len + qi) * p.Hq + head) * 2) = make_float2(M, Ls);
-}
-
-// An output row without a token of its own: its prefix's o / l, or zeros.
-template <int D, bool kWide>
-__device__ __forceinline__ void write_unwalked(const SplitParams& p, int b, int qi, int head, int d4, int64_t o) {
-    float M = kNegInf, L = 0.f;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    join_prefix<D, kWide>(p, prefix_of(p, b), b, qi, head, d4, M, L, v);
-    if (kWide ? L != 0.f : L > 0.f) v = make_float4(v.x / L, v.y / L, v.z / L, v.w / L);
-    else v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (p.out_f32) *reinterpret_cast<float4*>(p.out_f32 + o) = v;
-    else *reinterpret_cast<uint2*>(p.out + o) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+// What is left of output row `row`, columns d4 .. d4 + 3, from its state: (m, l),
+// and o where that is asked for.  Returns whether o is.
+template <int D>
+__device__ __forceinline__ bool put_state(const SplitParams& p, int64_t row, int d4, float M, float Ls, const float4& Os) {
+    if (p.sc.row_ml && d4 == 0) *reinterpret_cast<float2*>(p.sc.row_ml + row * 2) = make_float2(M, Ls);
+    if (p.sc.row_o == nullptr) return false;
+    *reinterpret_cast<float4*>(p.sc.row_o + row * D + d4) = Os;
+    return true;
 }
 
 // Segment-end roles (see the epilogue in run_consumer).
@@ -840,7 +786,7 @@ __device__ __forceinline__ void run_consumer(const SplitParams& p, uint32_t base
     const uint32_t full0 = base_s + L.bars, empty0 = full0 + 8 * S;
     const int g = lane >> 2, t = lane & 3;
     const int r0 = warp * 16;
-    constexpr bool MQ = is_multi(MODE), kExt = MODE == kScored;
+    constexpr bool MQ = is_multi(MODE), kExt = is_scored(MODE);
     static_assert(C::kQTiles == 0, "n8 form");
     const int G = p.G;
     const float sl2 = p.scale_log2;
@@ -848,6 +794,7 @@ __device__ __forceinline__ void run_consumer(const SplitParams& p, uint32_t base
     // query n / G of the row), fixed for the whole launch
     const int qc0 = MQ ? (2 * t) / G : 0, qc1 = MQ ? (2 * t + 1) / G : 0;
     float slope0 = 0.f, slope1 = 0.f;  // of the lane's two columns (kExt)
+    float* scores = nullptr;           // the segment's, of these columns (kExt)
     // ldmatrix row addresses: QK reads K as the A operand (rows = tokens),
     // PV reads V transposed as the A operand (rows of V = tokens = k index).
     const int qk_row = r0 + (lane & 7) + (((lane >> 3) & 1) << 3);
@@ -895,10 +842,8 @@ __device__ __forceinline__ void run_consumer(const SplitParams& p, uint32_t base
                 const int h = (4 * i4) / D, d4 = 4 * i4 - h * D;
                 const int64_t o = MQ ? qo_offset<MQ>(p, ri.b, ri.first + h / G, kvh * G + h % G, D) + d4
                                      : qo_offset<MQ>(p, sq, 0, kvh * G, D) + 4 * i4;
-                if constexpr (kExt) {
-                    write_unwalked<D, false>(p, ri.b, ri.first + h / G, kvh * G + h % G, d4, o);
-                    continue;
-                }
+                if constexpr (kExt)
+                    if (put_state<D>(p, o / D, d4, kNegInf, 0.f, make_float4(0.f, 0.f, 0.f, 0.f))) continue;
                 if (p.out_f32) *reinterpret_cast<float4*>(p.out_f32 + o) = make_float4(0.f, 0.f, 0.f, 0.f);
                 else *reinterpret_cast<uint2*>(p.out + o) = make_uint2(0u, 0u);
             }
@@ -935,6 +880,7 @@ __device__ __forceinline__ void run_consumer(const SplitParams& p, uint32_t base
                 if constexpr (kExt) {
                     slope0 = column_slope(p, m, 2 * t);
                     slope1 = column_slope(p, m, 2 * t + 1);
+                    scores = scores_of(p, m, 2 * t);
                 }
                 const uint8_t* sq = base + (sV - base_s) + C::kTileBytes;
 #pragma unroll
@@ -973,12 +919,20 @@ __device__ __forceinline__ void run_consumer(const SplitParams& p, uint32_t base
                 float s2 = (acc[0][2] + acc[1][2]) * sl2;
                 float s3 = (acc[0][3] + acc[1][3]) * sl2;
                 if constexpr (kExt) {
-                    const float far0 = (float)(m.j0 * p.bs + r0 + g - m.lim - qc0);
-                    const float far1 = (float)(m.j0 * p.bs + r0 + g - m.lim - qc1);
-                    s0 = score_of(p.sc, s0, slope0, far0);
-                    s1 = score_of(p.sc, s1, slope1, far1);
-                    s2 = score_of(p.sc, s2, slope0, far0 + 8.f);
-                    s3 = score_of(p.sc, s3, slope1, far1 + 8.f);
+                    if (p.sc.cap != 0.f) {
+                        s0 = capped(p.sc, s0);
+                        s1 = capped(p.sc, s1);
+                        s2 = capped(p.sc, s2);
+                        s3 = capped(p.sc, s3);
+                    }
+                    if (p.sc.slopes) {  // times the token's place less the query's
+                        const int far = m.j0 * p.bs + r0 + g - m.lim;
+                        const float far0 = (float)(far - qc0), far1 = (float)(far - qc1);
+                        s0 = fmaf(slope0, far0, s0);
+                        s1 = fmaf(slope1, far1, s1);
+                        s2 = fmaf(slope0, far0 + 8.f, s2);
+                        s3 = fmaf(slope1, far1 + 8.f, s3);
+                    }
                 }
                 if (m.n_valid < C::kST) {  // a stage that ends mid-way: mask the rows past it
                     if (r0 + g >= m.n_valid) { s0 = kNegInf; s1 = kNegInf; }
@@ -996,9 +950,11 @@ __device__ __forceinline__ void run_consumer(const SplitParams& p, uint32_t base
                     }
                 }
                 if constexpr (kExt) {
-                    if (p.sc.scores) {
-                        if (r0 + g < m.n_valid) put_scores(p, m, r0 + g, 2 * t, s0, s1);
-                        if (r0 + g + 8 < m.n_valid) put_scores(p, m, r0 + g + 8, 2 * t, s2, s3);
+                    if (scores) {
+                        float* at = scores + ((int64_t)m.j0 * p.bs + r0 + g) * p.rows_per_slot;
+                        const bool first = 2 * t < m.nr, second = 2 * t + 1 < m.nr, pairs = (p.rows_per_slot & 1) == 0;
+                        if (r0 + g < m.n_valid) put_scores(at, pairs, first, second, s0, s1);
+                        if (r0 + g + 8 < m.n_valid) put_scores(at + 8 * p.rows_per_slot, pairs, first, second, s2, s3);
                     }
                 }
                 // column max over the 16 tokens (lanes sharing t)
@@ -1100,8 +1056,6 @@ __device__ __forceinline__ void run_consumer(const SplitParams& p, uint32_t base
             }
             const bool whole = (m.flags & kWholeUnit) != 0;
             const int u = m.b * p.Hkv + m.kvh;
-            PrefixSeq ps = {};
-            if constexpr (kExt) ps = prefix_of(p, row_info<MQ>(p, m.b).b);  // (its round trip overlaps the merge's)
             UnitPieces pc;
             pc.cf = 0; pc.su = 0; pc.n = 1; pc.every = true;
             if (!whole) pc = unit_pieces(pfx, m.b, m.kvh, p.Hkv, p.unit_cost, gr);
@@ -1212,12 +1166,12 @@ __device__ __forceinline__ void run_consumer(const SplitParams& p, uint32_t base
                         p.l_state[row] = Lo;
                     }
                 } else {
-                    if constexpr (kExt)
-                        join_prefix<D, false>(p, ps, ri.b, ri.first + h / G, m.kvh * G + h % G, d4, M, Ls, Os);
                     const float4 v = Ls > 0.f ? make_float4(Os.x / Ls, Os.y / Ls, Os.z / Ls, Os.w / Ls)
                                               : make_float4(0.f, 0.f, 0.f, 0.f);
                     const int64_t o = MQ ? qo_offset<MQ>(p, ri.b, ri.first + h / G, m.kvh * G + h % G, D) + d4
                                          : qo_offset<MQ>(p, m.b, 0, m.kvh * G, D) + 4 * i4;
+                    if constexpr (kExt)
+                        if (put_state<D>(p, o / D, d4, M, Ls, Os)) continue;
                     if (p.out_f32) {
                         *reinterpret_cast<float4*>(p.out_f32 + o) = v;
                     } else {
@@ -1269,10 +1223,8 @@ __device__ __forceinline__ void zero_empty_rows(const SplitParams& p, const int3
         for (int i4 = ct; i4 < NR * D / 4; i4 += kThreadsC) {
             const int h = (4 * i4) / D, d4 = 4 * i4 - h * D;
             const int64_t o = qo_offset<true>(p, ri.b, ri.first + h / p.G, kvh * p.G + h % p.G, D) + d4;
-            if constexpr (kExt) {
-                write_unwalked<D, true>(p, ri.b, ri.first + h / p.G, kvh * p.G + h % p.G, d4, o);
-                continue;
-            }
+            if constexpr (kExt)
+                if (put_state<D>(p, o / D, d4, kNegInf, 0.f, make_float4(0.f, 0.f, 0.f, 0.f))) continue;
             if (p.out_f32) *reinterpret_cast<float4*>(p.out_f32 + o) = make_float4(0.f, 0.f, 0.f, 0.f);
             else *reinterpret_cast<uint2*>(p.out + o) = make_uint2(0u, 0u);
         }
@@ -1317,8 +1269,6 @@ __device__ __forceinline__ bool rows_tile_merge(const SplitParams& p, const Stag
     const bool whole = (m.flags & kWholeUnit) != 0;
     const int u = m.b * p.Hkv + m.kvh;
     const int NR = m.nr, SR = p.rows_per_slot, G = p.G;
-    PrefixSeq ps = {};
-    if constexpr (kExt) ps = prefix_of(p, ri.b);  // (its round trip overlaps the role's)
         if (tile == 0 && ct == 0) {
             int32_t r = whole ? kRoleWhole : ticket == pc.n - 1 ? kRoleMerge : kRoleStore;
             if (r == kRoleMerge) {
@@ -1393,11 +1343,11 @@ __device__ __forceinline__ bool rows_tile_merge(const SplitParams& p, const Stag
                 Ls = Lr;
                 Os = Or;
             }
-            if constexpr (kExt)
-                join_prefix<D, kScaled>(p, ps, ri.b, ri.first + h / G, m.kvh * G + h % G, d4, M, Ls, Os);
             const float4 v = (kScaled ? Ls != 0.f : Ls > 0.f) ? make_float4(Os.x / Ls, Os.y / Ls, Os.z / Ls, Os.w / Ls)
                                       : make_float4(0.f, 0.f, 0.f, 0.f);
             const int64_t oo = qo_offset<true>(p, ri.b, ri.first + h / G, m.kvh * G + h % G, D) + d4;
+            if constexpr (kExt)
+                if (put_state<D>(p, oo / D, d4, M, Ls, Os)) continue;
             if (p.out_f32) {
                 *reinterpret_cast<float4*>(p.out_f32 + oo) = v;
             } else {

@@ -30,19 +30,21 @@ constexpr int kMaxRowsPerWalk = 32;                      // q rows one KV walk s
 // M, in one or two tiles of 16 rows, so that one walk over the KV serves up
 // to 32 q rows.  kMultiTc is the row form of 32 q rows on the tcgen05
 // tensor cores: accumulators in tensor memory, one thread issues the MMAs.
-// kScored is the n8 form of one or several causal queries with what
-// ScoredParams adds: capped and distance-biased scores, scores written out, a
-// shared prefix's state joined at the end.
+// kScored and kScoredMulti are the n8 form of one and of several causal queries
+// with what Scoring adds: capped and distance-biased scores, scores written
+// out, a shared prefix left out and the state of the rest handed on.
 enum Mode : int {
-    kOneShot = 0, kTiled = 1, kGather = 2, kMulti = 3, kMultiRows16 = 4, kMultiRows32 = 5, kMultiTc = 6, kScored = 7
+    kOneShot = 0, kTiled = 1, kGather = 2, kMulti = 3, kMultiRows16 = 4, kMultiRows32 = 5, kMultiTc = 6, kScored = 7,
+    kScoredMulti = 8
 };
-constexpr int kNumModes = 7;  // of the context's split kernels; kScored is set up on its own
+constexpr int kNumModes = 7;  // of the context's split kernels; the scored ones are set up on their own
 __host__ __device__ constexpr bool is_multi(int mode) {
     return mode == kMulti || mode == kMultiRows16 || mode == kMultiRows32 || mode == kMultiTc ||
-           mode == kScored;
+           mode == kScoredMulti;
 }
+__host__ __device__ constexpr bool is_scored(int mode) { return mode == kScored || mode == kScoredMulti; }
 __host__ __device__ constexpr bool is_tc(int mode) { return mode == kMultiTc; }
-__host__ __device__ constexpr bool writes_output(int mode) { return mode == kOneShot || is_multi(mode); }
+__host__ __device__ constexpr bool writes_output(int mode) { return mode == kOneShot || mode == kScored || is_multi(mode); }
 // 16-row q tiles of the row form (0: the n8 form); the tcgen05 form's segment
 // end merges its 32 rows in two such tiles.
 __host__ __device__ constexpr int q_tiles(int mode) {
@@ -105,17 +107,14 @@ struct alignas(16) PrefixSeq {
     int32_t work, total, pad[2];
 };
 
-// What kScored adds to a launch.  Scores are in base-2 units.
+// What the scored modes add to a launch.  Scores are in base-2 units.
 struct Scoring {
     float cap, inv_cap;          // cap * log2 e, and 2 log2 e over that; 0: scores as they are
     const float* slopes;         // [Hq] or null: score += slope * (token - the query's own)
     float* scores;               // [launch row][Hkv][tokens][rows_per_slot] out, or null
     float* row_ml;               // [B * q_len * Hq][2] out: (m, l) of every output row, or null
-    const PrefixSeq* seqs;       // [sequences of the call], or null: no shared prefix
-    int32_t seq0;                // first sequence of this launch
-    int32_t prefix_ctas;         // CTAs of the prefix kernel
-    const float* prefix_o;       // [slots][tiles][D / 4][128][4]
-    const float* prefix_ml;      // [slots][tiles][128][2]
+    float* row_o;                // [B * q_len * Hq][D] out, instead of the output: o of every row, or null
+    const PrefixSeq* seqs;       // [B], or null: no shared prefix
 };
 
 struct SplitParams {
@@ -160,7 +159,7 @@ struct SplitParams {
     int32_t early_inputs;        // tiled: read the inputs before the previous kernel completes
                                  // (a tile step right behind another of the same step)
     float scale_log2;            // softmax scale * log2(e)
-    Scoring sc;                  // kScored
+    Scoring sc;                  // the scored modes
 };
 
 struct SmemLayout {

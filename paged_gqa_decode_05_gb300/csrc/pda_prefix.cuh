@@ -215,7 +215,8 @@ __device__ __forceinline__ bool lane_wait(uint32_t bar, uint32_t parity) {
 
 // Loader warp w fills 32 rows (half w & 1) of the slots of K (w < 2) or of V.
 template <int D, int FMT>
-__device__ __forceinline__ void prefix_load(const PrefixParams& p, const PrefixGroup* groups, uint32_t base, volatile int* abort_flag, int w, int lane) {
+__device__ __forceinline__ void prefix_load(const PrefixParams& p, const PrefixGroup* groups, uint32_t base, uint8_t* smem,
+                                            volatile int* abort_flag, int w, int lane) {
     using C = PrefixCfg<D, FMT>;
     constexpr int RW = C::kRW, ES = FMT == kBf16 ? 2 : 1;  // rows of this warp; bytes of an element
     constexpr int CH = D * ES / 16, RPI = 32 / CH;         // 16-byte chunks of a row; rows of an instruction
@@ -364,6 +365,10 @@ __device__ __forceinline__ void prefix_load(const PrefixParams& p, const PrefixG
         } else if constexpr (FMT != kBf16) {
             const uint32_t m = __shfl_sync(0xffffffffu, queue, spread & 31u), c = m % C::kSlots;
             if (!(ok = wait(base + C::kLanded + 8 * (2 * c + half), (m / C::kSlots) & 1u))) break;
+            if (k) {  // K's scales times what every score is multiplied by
+                float* ks = reinterpret_cast<float*>(smem + C::kScale0) + spread % C::kRing * (2 * C::kT) + row0 + lane;
+                *ks *= p.score_mult;
+            }
             convert(base + C::kSlot0 + c * C::kSlotBytes);
             if (lane == 0) mbar_arrive(base + C::kFull + 8 * c);
             ++spread;
@@ -463,10 +468,11 @@ __device__ __forceinline__ void prefix_mma(const PrefixParams& p, const PrefixGr
 
 // ------------------------------------------------------------------ softmax
 
+// 2 N columns of this thread's lane.
 template <int N>
-__device__ __forceinline__ void tmem_ld_row(uint32_t taddr, float (&v)[N]) {
+__device__ __forceinline__ void tmem_ld_row(uint32_t taddr, float2 (&v)[N]) {
 #pragma unroll
-    for (int c = 0; c < N; c += 16) {
+    for (int c = 0; c < 2 * N; c += 16) {
         uint32_t* r = reinterpret_cast<uint32_t*>(v) + c;
         asm volatile(
             "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -478,7 +484,7 @@ __device__ __forceinline__ void tmem_ld_row(uint32_t taddr, float (&v)[N]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
     // (no use of the loaded registers moves ahead of the wait)
 #pragma unroll
-    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i].x), "+f"(v[i].y));
 }
 
 template <int D, int FMT>
@@ -492,9 +498,6 @@ __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, const Pref
     float* ml = reinterpret_cast<float*>(smem);  // [stream][2][128], over the q rows once they are used
     PrefixWalk<D, FMT> walk(p, groups);
     PrefixSegment s;
-    Scoring sc = {};
-    sc.cap = p.cap;
-    sc.inv_cap = p.inv_cap;
     const bool plain = p.cap == 0.f && p.slopes == nullptr;
     uint32_t tile0 = 0, segs = 0, done = 0, cphase = 0;  // done: items of this stream
     auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -514,15 +517,26 @@ __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, const Pref
         {
             const int threads = s.dual ? 128 : 128 * C::kStreams, t0 = s.dual ? row : warp * 32 + lane;
             const uint32_t sQ = base + (s.dual ? st : 0) * C::kQTileBytes;
-            for (int i = t0; i < 128 * (D / 8); i += threads) {
-                const int r = i / (D / 8), c = i % (D / 8), g = tile * 128 + r;
-                uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (g < s.rows) {
-                    const int bq = g / p.G, h = g - bq * p.G;
-                    x = *reinterpret_cast<const uint4*>(
-                        p.q + (((int64_t)s.start * p.q_len + bq) * p.Hq + s.kvh * p.G + h) * D + c * 8);
+            constexpr int U = 8;  // pieces in flight: a round trip each would be most of the kernel's start
+#pragma unroll 1
+            for (int i0 = t0; i0 < 128 * (D / 8); i0 += U * threads) {
+                uint4 x[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int i = i0 + u * threads, r = i / (D / 8), c = i % (D / 8), g = tile * 128 + r;
+                    x[u] = make_uint4(0u, 0u, 0u, 0u);
+                    if (g < s.rows && r < 128) {
+                        const int bq = g / p.G, h = g - bq * p.G;
+                        x[u] = *reinterpret_cast<const uint4*>(
+                            p.q + (((int64_t)s.start * p.q_len + bq) * p.Hq + s.kvh * p.G + h) * D + c * 8);
+                    }
                 }
-                sts_v4(sQ + (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), x.x, x.y, x.z, x.w);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int i = i0 + u * threads, r = i / (D / 8), c = i % (D / 8);
+                    if (r < 128)
+                        sts_v4(sQ + (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), x[u].x, x[u].y, x[u].z, x[u].w);
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -554,44 +568,52 @@ __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, const Pref
                 const bool cut = __any_sync(0xffffffffu, seen < kT), bare = FMT == kBf16 && plain && !cut;
                 const float* kscale = reinterpret_cast<const float*>(smem + C::kScale0) +
                                       (FMT == kBf16 ? 0 : (tile0 + jj) % C::kRing * (2 * kT));
-                const float f = bare ? p.scale_log2 : 1.f;
+                const float f = bare ? p.score_mult : 1.f;
                 float top = kNegInf;
 #pragma unroll 1
                 for (int c = 0; c < kT; c += kPart) {
-                    float v[kPart], two[2] = {kNegInf, kNegInf};
+                    float2 v[kPart / 2];
                     tmem_ld_row(tS + c, v);
+                    float two[2] = {kNegInf, kNegInf};
                     if (!bare) {
+                        // times the score scale (8-bit: and the K scale), under a cap over half of it
 #pragma unroll
-                        for (int i = 0; i < kPart; i += 4) {
-                            float4 x = make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
-                            if constexpr (FMT != kBf16) {
-                                const float4 y = *reinterpret_cast<const float4*>(kscale + c + i);
-                                x = make_float4(x.x * y.x, x.y * y.y, x.z * y.z, x.w * y.w);
-                            }
-                            v[i] *= x.x;
-                            v[i + 1] *= x.y;
-                            v[i + 2] *= x.z;
-                            v[i + 3] *= x.w;
+                        for (int i = 0; i < kPart / 2; i += 2) {
+                            float4 x = make_float4(p.score_mult, p.score_mult, p.score_mult, p.score_mult);
+                            if constexpr (FMT != kBf16) x = *reinterpret_cast<const float4*>(kscale + c + 2 * i);
+                            v[i] = __fmul2_rn(v[i], make_float2(x.x, x.y));
+                            v[i + 1] = __fmul2_rn(v[i + 1], make_float2(x.z, x.w));
                         }
-                        if (p.cap != 0.f) {
+                        if (p.cap != 0.f) {  // (see capped)
 #pragma unroll
-                            for (int i = 0; i < kPart; ++i) v[i] = capped(sc, v[i]);
+                            for (int i = 0; i < kPart / 2; ++i) {
+                                const float2 e = __fadd2_rn(make_float2(ex2(v[i].x), ex2(v[i].y)), make_float2(1.f, 1.f));
+                                v[i] = __ffma2_rn(make_float2(rcp_approx(e.x), rcp_approx(e.y)),
+                                                  make_float2(-2.f * p.cap, -2.f * p.cap), make_float2(p.cap, p.cap));
+                            }
                         }
                         if (p.slopes) {
                             const float far = (float)(t0 + c - own);
 #pragma unroll
-                            for (int i = 0; i < kPart; ++i) v[i] = fmaf(slope, far + (float)i, v[i]);
+                            for (int i = 0; i < kPart / 2; ++i)
+                                v[i] = __ffma2_rn(make_float2(slope, slope), make_float2(far + (float)(2 * i), far + (float)(2 * i + 1)), v[i]);
                         }
                         if (cut) {
 #pragma unroll
-                            for (int i = 0; i < kPart; ++i)
-                                if (i >= seen - c) v[i] = kNegInf;
+                            for (int i = 0; i < kPart / 2; ++i) {
+                                if (2 * i >= seen - c) v[i].x = kNegInf;
+                                if (2 * i + 1 >= seen - c) v[i].y = kNegInf;
+                            }
                         }
+                        const float* x = reinterpret_cast<const float*>(v);
 #pragma unroll
-                        for (int i = 0; i < kPart; i += 16) tmem_st16(tS + c + i, *reinterpret_cast<const float(*)[16]>(v + i));
+                        for (int i = 0; i < kPart; i += 16) tmem_st16(tS + c + i, *reinterpret_cast<const float(*)[16]>(x + i));
                     }
 #pragma unroll
-                    for (int i = 0; i < kPart; ++i) two[i & 1] = fmaxf(two[i & 1], v[i] * f);
+                    for (int i = 0; i < kPart / 2; ++i) {
+                        two[0] = fmaxf(two[0], v[i].x * f);
+                        two[1] = fmaxf(two[1], v[i].y * f);
+                    }
                     top = fmaxf(top, fmaxf(two[0], two[1]));
                 }
                 if (!bare) tmem_wait_st();
@@ -613,28 +635,26 @@ __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, const Pref
                 }
                 if (up) m = top;
                 const float u = (m == kNegInf ? 0.f : m) + kDown;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
                 for (int c = 0; c < kT; c += kPart) {  // P over its part of S: high parts, then low parts
-                    float v[kPart];
+                    float2 v[kPart / 2];
                     uint32_t hi[kPart / 2], lo[kPart / 2];
                     tmem_ld_row(tS + c, v);
 #pragma unroll
                     for (int i = 0; i < kPart / 2; ++i) {
-                        float p0 = ex2(fmaf(v[2 * i], f, -u)), p1 = ex2(fmaf(v[2 * i + 1], f, -u));
-                        sum[i & 3] += p0 + p1;
-                        if constexpr (FMT != kBf16) {
-                            const float2 x = *reinterpret_cast<const float2*>(kscale + kT + c + 2 * i);
-                            p0 *= x.x;
-                            p1 *= x.y;
-                        }
-                        hi[i] = pack_bf16x2(p0, p1);
-                        lo[i] = pack_bf16x2(p0 - bf16_lo(hi[i]), p1 - bf16_hi(hi[i]));
+                        const float2 x = __ffma2_rn(v[i], make_float2(f, f), make_float2(-u, -u));
+                        float2 e = make_float2(ex2(x.x), ex2(x.y));
+                        sum[i & 1] = __fadd2_rn(sum[i & 1], e);
+                        if constexpr (FMT != kBf16) e = __fmul2_rn(e, *reinterpret_cast<const float2*>(kscale + kT + c + 2 * i));
+                        hi[i] = pack_bf16x2(e.x, e.y);
+                        const float2 r = __ffma2_rn(make_float2(bf16_lo(hi[i]), bf16_hi(hi[i])), make_float2(-1.f, -1.f), e);
+                        lo[i] = pack_bf16x2(r.x, r.y);
                     }
                     tmem_st16u(tS + c, hi);
                     tmem_st16u(tS + c + kPart / 2, lo);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 tmem_wait_st();
             }
             ++done;
@@ -678,7 +698,7 @@ __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, const Pref
                 if (g < s.rows) {
 #pragma unroll
                     for (int i = 0; i < 16; i += 4)
-                        reinterpret_cast<float4*>(p.part_o)[(at * (D / 4) + (c + i) / 4) * 128 + row] =
+                        *reinterpret_cast<float4*>(p.part_o + (at * 128 + row) * D + c + i) =
                             make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                 }
             }
@@ -753,7 +773,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, FMT>::kThreads, 1) prefix_kernel(
         prefix_softmax<D, FMT>(p, groups, base, smem, &abort_flag, tmem, warp, lane);
         tc_fence_before();
     } else if (warp < kMmaWarp) {
-        prefix_load<D, FMT>(p, groups, base, &abort_flag, warp - C::kSoftWarps, lane);
+        prefix_load<D, FMT>(p, groups, base, smem, &abort_flag, warp - C::kSoftWarps, lane);
     } else {
         // what the sequences' own decode needs of the plan, while the first rows are on their way
         if (warp == kMmaWarp)

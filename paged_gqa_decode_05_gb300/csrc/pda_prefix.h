@@ -21,13 +21,14 @@ struct PrefixParams {
     const int32_t* starts;      // [n_groups + 1] or null: B / n_groups sequences each
     PrefixGroup* groups;        // [n_groups + 1] out
     PrefixSeq* seqs;            // [B] out
-    float* part_o;              // [slots][streams][D / 4][128][4]
+    float* part_o;              // [slots][streams][128][D]
     float* part_ml;             // [slots][streams][128][2]
     uint32_t* err;
     int32_t table_stride, lbs;
     int32_t boxes;              // rows come as TMA boxes (block sizes from 8), else one by one
     int32_t B, q_len, Hq, Hkv, G, n_groups;
-    float scale_log2, cap, inv_cap;
+    float score_mult;           // score scale in base-2 units; under a cap, what capped() takes the exponential of
+    float cap;                  // in base-2 units
     const float* slopes;
 };
 
@@ -37,6 +38,20 @@ struct PrefixShape {
 };
 PrefixShape prefix_shape(int D, int format);
 cudaError_t launch_prefix(int D, int format, const PrefixParams& p, int ctas, cudaStream_t stream);
+
+// Joins the pieces of the prefixes with the states of the sequences' own tokens.
+struct JoinParams {
+    const PrefixSeq* seqs;      // [B]
+    const float* row_ml;        // [rows][2], [rows][D]: states of the own tokens
+    const float* row_o;
+    const float* part_ml;       // as in PrefixParams
+    const float* part_o;
+    uint16_t* out;              // [rows][D] bf16, or
+    float* out_f32;             // fp32 when not null
+    int64_t rows;               // B * q_len * Hq
+    int32_t q_len, Hq, Hkv, G, ctas;  // ctas: of the prefix kernel
+};
+cudaError_t launch_join(int D, const JoinParams& p, cudaStream_t stream);
 
 // Units of a call at most: pairs of q tiles (single ones at head size 256) per
 // kv head, one more for every group whose rows do not fill their last.

@@ -438,7 +438,7 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
     using C = QuantCfg<D, NT>;
     constexpr int S = C::kStages, RT = C::kRT, K = C::kK;
     constexpr int kThreadsC = C::kWarps * 32, kOStride = D + 4;
-    constexpr bool MQ = is_multi(MODE), kHide = MQ && FMT == kE4m3, kExt = MODE == kScored;
+    constexpr bool MQ = is_multi(MODE), kHide = MQ && FMT == kE4m3, kExt = is_scored(MODE);
     const uint32_t full0 = base_s + L.bars, empty0 = full0 + 8 * S;
     const int g = lane >> 2, t = lane & 3;
     // warps 0 .. kRW - 1 take the first eight q rows, the next kRW the others, all of a stage's KV rows
@@ -480,6 +480,7 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
     float o[2 * K][4];
     uint32_t qf[K][4];
     float slope[2] = {0.f, 0.f};  // of the lane's two columns (kExt)
+    float* scores = nullptr;      // the segment's, of these columns (kExt)
     float f[2] = {0.f, 0.f}, m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 2 * K; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -529,6 +530,7 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
             if constexpr (kExt) {
                 slope[0] = column_slope(p, md, 2 * t);
                 slope[1] = column_slope(p, md, 2 * t + 1);
+                scores = scores_of(p, md, 2 * t);
             }
             if constexpr (kHide) notes->cols[ct] = 0;
 #pragma unroll
@@ -536,7 +538,7 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
         }
         if (r0 < md.n_valid && (NT == 1 || 8 * tile < md.nr)) {
             const bool partial = r0 + 16 * RT > md.n_valid;
-            const int pos0 = MQ ? md.j0 * p.bs + r0 : 0;
+            const int pos0 = MQ || kExt ? md.j0 * p.bs + r0 : 0;
             const bool diagonal = MQ && pos0 + 16 * RT - 1 > md.lim;  // some queries do not see some of these rows
             if (FMT == kE4m3 && (MQ ? partial || diagonal : partial)) {
                 // rows behind the end may hold NaN codes, and 0 * NaN would poison P V
@@ -597,21 +599,36 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
                 for (int i = 0; i < 4; ++i) {
                     const float dot = FMT == kE4m3 ? fmaf(acc[1][i], 1.f / kLowPart, acc[0][i]) : acc[0][i] + acc[1][i];
                     if constexpr (kExt) {  // the score on its own first
-                        const int far = md.j0 * p.bs + r0 + 16 * r + 8 * (i >> 1) + g - md.lim - qc[i & 1];
-                        x[r][i] = score_of(p.sc, dot * (ks[r][i >> 1] * f[i & 1]), slope[i & 1], (float)far);
+                        x[r][i] = dot * (ks[r][i >> 1] * f[i & 1]);
                     } else {
                         x[r][i] = fmaf(dot, ks[r][i >> 1] * f[i & 1], lv[r][i >> 1]);
                     }
                 }
                 if constexpr (kExt) {
+                    if (p.sc.cap != 0.f) {
 #pragma unroll
-                    for (int i = 0; i < 4; i += 2) {
-                        const int at = r0 + 16 * r + 8 * (i >> 1) + g, far = md.j0 * p.bs + at - md.lim;
-                        if (p.sc.scores && at < md.n_valid)
-                            put_scores(p, md, at, 2 * t, far > qc[0] ? kNegInf : x[r][i], far > qc[1] ? kNegInf : x[r][i + 1]);
-                        x[r][i] += lv[r][i >> 1];
-                        x[r][i + 1] += lv[r][i >> 1];
+                        for (int i = 0; i < 4; ++i) x[r][i] = capped(p.sc, x[r][i]);
                     }
+                    const int far = pos0 + 16 * r + g - md.lim;  // the token's place less the first query's
+                    if (p.sc.slopes) {
+                        const float far0 = (float)(far - qc[0]), far1 = (float)(far - qc[1]);
+                        x[r][0] = fmaf(slope[0], far0, x[r][0]);
+                        x[r][1] = fmaf(slope[1], far1, x[r][1]);
+                        x[r][2] = fmaf(slope[0], far0 + 8.f, x[r][2]);
+                        x[r][3] = fmaf(slope[1], far1 + 8.f, x[r][3]);
+                    }
+                    if (scores) {
+                        float* at = scores + ((int64_t)pos0 + 16 * r + g) * p.rows_per_slot;
+                        const bool first = 2 * t < md.nr, second = 2 * t + 1 < md.nr, pairs = (p.rows_per_slot & 1) == 0;
+#pragma unroll
+                        for (int i = 0; i < 4; i += 2)
+                            if (r0 + 16 * r + 4 * i + g < md.n_valid)
+                                put_scores(at + 4 * i * p.rows_per_slot, pairs, first, second,
+                                           MQ && far + 4 * i > qc[0] ? kNegInf : x[r][i],
+                                           MQ && far + 4 * i > qc[1] ? kNegInf : x[r][i + 1]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[r][i] += lv[r][i >> 1];
                 }
             }
             if (partial) {

@@ -16,12 +16,16 @@ struct ScoredShape {
     uint32_t smem(int B) const { return smem_layout_of(stage_bytes, kScored, stages, B).total; }
 };
 
-// The kScored instance of a head size for stages of st rows (bf16 caches) and
-// a cache format; fine: weights in two fp16 parts (8-bit caches, fp32 outputs).
-ScoredShape scored_shape(int D, int st, int format, bool fine);
+// An instance: stages of st rows (bf16 caches), a cache format, several causal
+// queries or one, and (8-bit caches) weights in two fp16 parts, for outputs and
+// states in fp32.
+struct ScoredForm {
+    int st, format;
+    bool multi, fine;
+};
+ScoredShape scored_shape(int D, const ScoredForm& form);
 // p is a QuantParams; bf16 kernels take its SplitParams.
-cudaError_t launch_scored(int D, int st, int format, bool fine, const QuantParams& p, int grid, size_t smem,
-                          cudaStream_t stream);
+cudaError_t launch_scored(int D, const ScoredForm& form, const QuantParams& p, int grid, size_t smem, cudaStream_t stream);
 
 // The sums of attention weights of a decode's cached tokens.
 struct WeightsParams {

@@ -86,13 +86,14 @@ template <class After>
 pda_status run_scored(pda_ctx* ctx, const Call& c, const pda::Scoring& sc, const After& after) {
     const pda_dims& d = ctx->dims;
     const int D = d.head_dim, Hq = d.num_q_heads, bs = d.block_size;
-    const bool bf16 = c.cache->format == PDA_CACHE_BF16, fine = !bf16 && c.f32;
+    const bool bf16 = c.cache->format == PDA_CACHE_BF16;
+    const pda::ScoredForm form = {ctx->stage_rows, c.cache->format, c.q_len > 1, !bf16 && (c.f32 || sc.row_o)};
     pda::QuantParams p = {};
     p.sc = sc;
     pda_status st = pda::check_scale(c.scale, D, &p.scale_log2);
     if (st != PDA_OK) return st;
     const Rows rows = rows_of(ctx, c.q_len);
-    const pda::ScoredShape shape = pda::scored_shape(D, ctx->stage_rows, c.cache->format, fine);
+    const pda::ScoredShape shape = pda::scored_shape(D, form);
     const int grid = ctx->scored_ctas[bf16 ? 0 : 1];
     if (rows.Qr > grid)
         return fail(PDA_ERR_INVALID_ARG, "q_len %d: more launch rows per sequence than CTAs (%d)", c.q_len, grid);
@@ -128,9 +129,12 @@ pda_status run_scored(pda_ctx* ctx, const Call& c, const pda::Scoring& sc, const
         p.lens = c.lens + s0;
         p.out = c.f32 ? nullptr : static_cast<uint16_t*>(c.out) + rows0 * D;
         p.out_f32 = c.f32 ? static_cast<float*>(c.out) + rows0 * D : nullptr;
-        p.sc.seq0 = s0;
-        const cudaError_t e =
-            pda::launch_scored(D, ctx->stage_rows, c.cache->format, fine, p, grid, shape.smem(p.B), c.stream);
+        if (sc.seqs) p.sc.seqs = sc.seqs + s0;
+        if (sc.row_o) {  // (the scores' own (m, l) are a launch's)
+            p.sc.row_o = sc.row_o + rows0 * D;
+            p.sc.row_ml = sc.row_ml + rows0 * 2;
+        }
+        const cudaError_t e = pda::launch_scored(D, form, p, grid, shape.smem(p.B), c.stream);
         if (e != cudaSuccess) return cuda_fail(e, "scored decode launch");
         if ((st = after(p, s0, n)) != PDA_OK) return st;
     }
@@ -161,9 +165,10 @@ WeightsScratch weights_scratch(const pda_ctx* ctx, int32_t batch, int32_t q_len,
     return s;
 }
 
-// Scratch of a shared prefix: the plan, and the states of its pieces.
+// Scratch of a shared prefix: the plan, the states of its pieces and those of
+// the sequences' own tokens.
 struct SharedScratch {
-    int64_t groups, seqs, ml, o, total;
+    int64_t groups, seqs, ml, o, row_ml, row_o, total;
 };
 SharedScratch shared_scratch(const pda_ctx* ctx, int32_t batch, int32_t q_len, int32_t n_groups) {
     const int D = ctx->dims.head_dim;
@@ -174,7 +179,10 @@ SharedScratch shared_scratch(const pda_ctx* ctx, int32_t batch, int32_t q_len, i
     s.seqs = round256((int64_t)batch * (int64_t)sizeof(pda::PrefixSeq));
     s.ml = round256(rows * 8);
     s.o = round256(rows * D * 4);
-    s.total = s.groups + s.seqs + s.ml + s.o;
+    const int64_t out = (int64_t)batch * q_len * ctx->dims.num_q_heads;
+    s.row_ml = round256(out * 8);
+    s.row_o = round256(out * D * 4);
+    s.total = s.groups + s.seqs + s.ml + s.o + s.row_ml + s.row_o;
     return s;
 }
 
@@ -223,9 +231,10 @@ pda_status pda::scored_setup(pda_ctx* ctx, int optin) {
     for (int k = 0; k < 2; ++k) {
         int per_sm = 1 << 30;
         for (int format : {PDA_CACHE_BF16, PDA_CACHE_E4M3, PDA_CACHE_INT8})
-            for (bool fine : {false, true}) {
-                if ((format == PDA_CACHE_BF16) != (k == 0) || (format == PDA_CACHE_BF16 && fine)) continue;
-                const ScoredShape s = scored_shape(D, ctx->stage_rows, format, fine);
+            for (int f = 0; f < 4; ++f) {
+                const ScoredForm form = {ctx->stage_rows, format, (f & 1) != 0, (f & 2) != 0};
+                if ((format == PDA_CACHE_BF16) != (k == 0) || (format == PDA_CACHE_BF16 && form.fine)) continue;
+                const ScoredShape s = scored_shape(D, form);
                 if (!s.fn) return fail(PDA_ERR_UNSUPPORTED, "no scored decode kernel");
                 const int limit = (int)s.smem(kMaxLaunchBatch);
                 if (limit > optin)
@@ -358,7 +367,7 @@ PDA_EXPORT pda_status pda_decode_shared(pda_ctx* ctx, const pda_bf16* q, const p
                     (long long)ss.total, (long long)scratch_bytes);
     DeviceGuard on(ctx->device);
     pda::PrefixParams pp = {};
-    if ((st = pda::check_scale(scale, D, &pp.scale_log2)) != PDA_OK) return st;
+    if ((st = pda::check_scale(scale, D, &pp.score_mult)) != PDA_OK) return st;
     uint8_t* base = static_cast<uint8_t*>(scratch);
     pda::Scoring sc = scoring_of(scoring);
     pp.q = q;
@@ -387,19 +396,35 @@ PDA_EXPORT pda_status pda_decode_shared(pda_ctx* ctx, const pda_bf16* q, const p
     pp.G = ctx->G;
     pp.n_groups = groups;
     pp.cap = sc.cap;
-    pp.inv_cap = sc.inv_cap;
+    if (sc.cap != 0.f) pp.score_mult *= sc.inv_cap;
     pp.slopes = sc.slopes;
     sc.seqs = pp.seqs;
-    sc.prefix_ctas = ctx->num_sms;
-    sc.prefix_o = pp.part_o;
-    sc.prefix_ml = pp.part_ml;
+    sc.row_ml = reinterpret_cast<float*>(base + ss.groups + ss.seqs + ss.ml + ss.o);
+    sc.row_o = reinterpret_cast<float*>(base + ss.groups + ss.seqs + ss.ml + ss.o + ss.row_ml);
     prefix_maps(ctx, cache, &pp);
     ctx->tile_steps = 0;
     if ((st = record(ctx, ctx->ev_begin, c.stream)) != PDA_OK) return st;
-    const cudaError_t e = pda::launch_prefix(D, cache->format, pp, ctx->num_sms, c.stream);
+    cudaError_t e = pda::launch_prefix(D, cache->format, pp, ctx->num_sms, c.stream);
     if (e != cudaSuccess) return cuda_fail(e, "shared prefix launch");
     if ((st = record(ctx, ctx->ev_split, c.stream)) != PDA_OK) return st;
     st = run_scored(ctx, c, sc, [](const pda::SplitParams&, int32_t, int32_t) -> pda_status { return PDA_OK; });
+    if (st != PDA_OK) return st;
+    pda::JoinParams j = {};
+    j.seqs = pp.seqs;
+    j.row_ml = sc.row_ml;
+    j.row_o = sc.row_o;
+    j.part_ml = pp.part_ml;
+    j.part_o = pp.part_o;
+    j.out = out_f32 ? nullptr : static_cast<uint16_t*>(out);
+    j.out_f32 = out_f32 ? static_cast<float*>(out) : nullptr;
+    j.rows = (int64_t)batch * q_len * d.num_q_heads;
+    j.q_len = q_len;
+    j.Hq = d.num_q_heads;
+    j.Hkv = d.num_kv_heads;
+    j.G = ctx->G;
+    j.ctas = ctx->num_sms;
+    e = pda::launch_join(D, j, c.stream);
+    if (e != cudaSuccess) return cuda_fail(e, "shared prefix join launch");
     return st == PDA_OK ? record(ctx, ctx->ev_end, c.stream) : st;
 }
 

@@ -1,5 +1,5 @@
 // pda_weights.cu -- the sums of attention weights beside a cache, and the
-// head-size dispatch of the kScored and shared-prefix kernels.
+// head-size dispatch of the scored and shared-prefix kernels.
 //
 //   out[t, g] = (t is one of the queries' own tokens ? 0 : in[t, g])
 //             + sum over the queries i that see t and the G q heads h of kv
@@ -16,31 +16,28 @@
 
 namespace pda {
 
-#define PDA_DECLARE_SCORED(D)                                                   \
-    ScoredShape scored_shape_d##D(int st, int format, bool fine);               \
-    cudaError_t launch_scored_d##D(int st, int format, bool fine, const QuantParams& p, int grid, size_t smem, \
-                                   cudaStream_t stream);
-PDA_DECLARE_SCORED(64)
-PDA_DECLARE_SCORED(128)
-PDA_DECLARE_SCORED(256)
+#define PDA_DECLARE_SCORED(FORMAT, D)                                                                       \
+    ScoredShape scored_shape_##FORMAT##_d##D(const ScoredForm& f);                                          \
+    cudaError_t launch_scored_##FORMAT##_d##D(const ScoredForm& f, const QuantParams& p, int grid, size_t smem, \
+                                              cudaStream_t stream);
+#define PDA_FOR_SCORED(F) F(bf16, 64) F(bf16, 128) F(bf16, 256) F(e4m3, 64) F(e4m3, 128) F(e4m3, 256) F(int8, 64) F(int8, 128) F(int8, 256)
+PDA_FOR_SCORED(PDA_DECLARE_SCORED)
 
-ScoredShape scored_shape(int D, int st, int format, bool fine) {
-    switch (D) {
-        case 64: return scored_shape_d64(st, format, fine);
-        case 128: return scored_shape_d128(st, format, fine);
-        case 256: return scored_shape_d256(st, format, fine);
-        default: return {};
-    }
+namespace {
+constexpr int bf16 = kBf16, e4m3 = kE4m3, int8 = kInt8;
 }
 
-cudaError_t launch_scored(int D, int st, int format, bool fine, const QuantParams& p, int grid, size_t smem,
-                          cudaStream_t stream) {
-    switch (D) {
-        case 64: return launch_scored_d64(st, format, fine, p, grid, smem, stream);
-        case 128: return launch_scored_d128(st, format, fine, p, grid, smem, stream);
-        case 256: return launch_scored_d256(st, format, fine, p, grid, smem, stream);
-        default: return cudaErrorInvalidValue;
-    }
+ScoredShape scored_shape(int D, const ScoredForm& f) {
+#define PDA_SCORED_SHAPE(FORMAT, DIM) if (f.format == FORMAT && D == DIM) return scored_shape_##FORMAT##_d##DIM(f);
+    PDA_FOR_SCORED(PDA_SCORED_SHAPE)
+    return {};
+}
+
+cudaError_t launch_scored(int D, const ScoredForm& f, const QuantParams& p, int grid, size_t smem, cudaStream_t stream) {
+#define PDA_SCORED_LAUNCH(FORMAT, DIM) \
+    if (f.format == FORMAT && D == DIM) return launch_scored_##FORMAT##_d##DIM(f, p, grid, smem, stream);
+    PDA_FOR_SCORED(PDA_SCORED_LAUNCH)
+    return cudaErrorInvalidValue;
 }
 
 #define PDA_DECLARE_PREFIX(D)              \
@@ -70,11 +67,31 @@ cudaError_t launch_prefix(int D, int format, const PrefixParams& p, int ctas, cu
 
 namespace {
 
-constexpr int kThreads = 256;  // tokens of a chunk: one (sequence, kv head)'s
+cudaLaunchConfig_t pdl_config(int grid, int threads, cudaStream_t stream, cudaLaunchAttribute* attr) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.stream = stream;
+    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr->val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
 
+// A CTA takes chunks of kChunk tokens of a (sequence, kv head), kTok a thread
+// with their loads together.  32 sequences of 4096 tokens, 4 q heads to each of
+// 8 kv heads: 1, 2, 4 tokens a thread 14.1, 10.2, 8.3 us.
+constexpr int kThreads = 256, kTok = 4, kChunk = kThreads * kTok;
+
+__device__ __forceinline__ int32_t chunks_of(int32_t n) { return (int32_t)(((int64_t)n + kChunk - 1) / kChunk); }
+
+// kSR: rows_per_slot where it is a power of two (the scores of a token in one or two loads), 0: any.
+template <int kSR>
 __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p) {
     __shared__ int32_t pfx[kMaxLaunchBatch + 1];  // chunks before each sequence, one kv head
     __shared__ int32_t sums[kThreads / 32];
+    __shared__ float2 ml[kMaxGroup];              // (m, log2 l) of a launch row's q rows
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait_primary();
     pdl_launch_dependents();
@@ -85,7 +102,7 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p
     int32_t mine = 0;
 #pragma unroll
     for (int k = 0; k < kPer; ++k)
-        if (k < per && tid * per + k < p.B) mine += (int32_t)(((int64_t)tokens(tid * per + k) + kThreads - 1) / kThreads);
+        if (k < per && tid * per + k < p.B) mine += chunks_of(tokens(tid * per + k));
     int32_t x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -101,14 +118,14 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p
         const int b = tid * per + k;
         if (k < per && b < p.B) {
             pfx[b] = run;
-            run += (int32_t)(((int64_t)tokens(b) + kThreads - 1) / kThreads);
+            run += chunks_of(tokens(b));
             if (b == p.B - 1) pfx[p.B] = run;
         }
     }
     __syncthreads();
     const int64_t chunks = (int64_t)pfx[p.B] * p.Hkv;
     const int64_t T = (int64_t)p.table_stride << p.lbs;
-    const int Qr = (p.q_len + p.qp - 1) / p.qp;
+    const int Qr = (p.q_len + p.qp - 1) / p.qp, SR = kSR > 0 ? kSR : p.rows_per_slot;
     for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
         int lo = 0, hi = p.B - 1;  // the largest b with pfx[b] * Hkv <= c
         while (lo < hi) {
@@ -116,54 +133,160 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p
             if ((int64_t)pfx[mid] * p.Hkv <= c) lo = mid; else hi = mid - 1;
         }
         const int b = lo, n = pfx[b + 1] - pfx[b];
-        const int64_t rem = c - (int64_t)pfx[b] * p.Hkv;
-        const int kvh = (int)(rem / n);
-        const int64_t t = (rem - (int64_t)kvh * n) * kThreads + tid;
+        const int rem = (int)(c - (int64_t)pfx[b] * p.Hkv);
+        const int kvh = rem / n;
+        const int64_t t0 = (int64_t)(rem - kvh * n) * kChunk + tid;
         const int32_t raw = p.lens[b], len = tokens(b);
-        if (t >= len) continue;
-        const int32_t id = p.table[(int64_t)b * p.table_stride + (t >> p.lbs)];
-        const bool good = id >= 0 && id < p.num_blocks;  // the decode raised the flag
-        const int64_t at = (((int64_t)id * p.Hkv + kvh) << p.lbs) + (t & ((1 << p.lbs) - 1));
-        const float old = good && p.in && t < (int64_t)raw - p.q_len ? p.in[at] : 0.f;
-        float w = 0.f;  // summed apart from the old sum, whose last place may be above a weight's first
-        for (int r = 0; r < Qr; ++r) {
-            const int first = r * p.qp, cnt = min(p.qp, p.q_len - first);
-            if (t >= (int64_t)raw - p.q_len + first + cnt) continue;  // past what the launch row's queries see
-            const float* s = p.scores + ((((int64_t)r * p.B + b) * p.Hkv + kvh) * T + t) * p.rows_per_slot;
-            const float2* ml = reinterpret_cast<const float2*>(p.row_ml) + ((int64_t)b * p.q_len + first) * p.Hq + kvh * p.G;
-            auto add = [&](int col, float score) {
-                const float2 z = __ldg(ml + (int64_t)(col / p.G) * p.Hq + col % p.G);
-                if (score != __int_as_float(0xff800000)) w += ex2((score - z.x) - lg2(z.y));
-            };
-            if ((p.rows_per_slot & 3) == 0) {
-                for (int i = 0; i < cnt * p.G; i += 4) {
-                    const float4 v = *reinterpret_cast<const float4*>(s + i);
-                    add(i, v.x);
-                    if (i + 1 < cnt * p.G) add(i + 1, v.y);
-                    if (i + 2 < cnt * p.G) add(i + 2, v.z);
-                    if (i + 3 < cnt * p.G) add(i + 3, v.w);
-                }
-            } else {
-                for (int i = 0; i < cnt * p.G; ++i) add(i, s[i]);
+        int64_t at[kTok];  // -1: no token, or a bad block id (the decode raised the flag)
+        float old[kTok], w[kTok];
+#pragma unroll
+        for (int k = 0; k < kTok; ++k) {
+            const int64_t t = t0 + k * kThreads;
+            at[k] = -1;
+            w[k] = 0.f;
+            if (t < len) {
+                const int32_t id = p.table[(int64_t)b * p.table_stride + (t >> p.lbs)];
+                if (id >= 0 && id < p.num_blocks) at[k] = (((int64_t)id * p.Hkv + kvh) << p.lbs) + (t & ((1 << p.lbs) - 1));
             }
         }
-        if (good) p.out[at] = old + w;
+#pragma unroll
+        for (int k = 0; k < kTok; ++k)
+            old[k] = at[k] >= 0 && p.in && t0 + k * kThreads < (int64_t)raw - p.q_len ? p.in[at[k]] : 0.f;
+        for (int r = 0; r < Qr; ++r) {
+            const int first = r * p.qp, rows = min(p.qp, p.q_len - first) * p.G;
+            __syncthreads();
+            if (tid < rows) {
+                const float2 z = reinterpret_cast<const float2*>(
+                    p.row_ml)[((int64_t)b * p.q_len + first + tid / p.G) * p.Hq + kvh * p.G + tid % p.G];
+                ml[tid] = make_float2(z.x, lg2(z.y));
+            }
+            __syncthreads();
+            const int64_t seen = (int64_t)raw - p.q_len + first + rows / p.G;  // tokens that the launch row's queries see
+            const float* s = p.scores + ((((int64_t)r * p.B + b) * p.Hkv + kvh) * T + t0) * SR;
+            auto add = [&](float& sum, int col, float score) {
+                const float2 z = ml[col];
+                // (a row that sees nothing has no finite score)
+                if (col < rows && score != __int_as_float(0xff800000)) sum += ex2((score - z.x) - z.y);
+            };
+            if constexpr (kSR >= 4) {
+                float4 v[kTok][kSR / 4];
+#pragma unroll
+                for (int k = 0; k < kTok; ++k)
+#pragma unroll
+                    for (int i = 0; i < kSR / 4; ++i)
+                        if (at[k] >= 0 && t0 + k * kThreads < seen)
+                            v[k][i] = *reinterpret_cast<const float4*>(s + (int64_t)k * kThreads * kSR + 4 * i);
+#pragma unroll
+                for (int k = 0; k < kTok; ++k) {
+                    if (at[k] < 0 || t0 + k * kThreads >= seen) continue;
+#pragma unroll
+                    for (int i = 0; i < kSR / 4; ++i) {
+                        add(w[k], 4 * i, v[k][i].x);
+                        add(w[k], 4 * i + 1, v[k][i].y);
+                        add(w[k], 4 * i + 2, v[k][i].z);
+                        add(w[k], 4 * i + 3, v[k][i].w);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < kTok; ++k) {
+                    if (at[k] < 0 || t0 + k * kThreads >= seen) continue;
+                    for (int i = 0; i < rows; ++i) add(w[k], i, s[(int64_t)k * kThreads * SR + i]);
+                }
+            }
+        }
+        // summed apart from the old sum, whose last place may be above a weight's first
+#pragma unroll
+        for (int k = 0; k < kTok; ++k)
+            if (at[k] >= 0) p.out[at[k]] = old[k] + w[k];
     }
 }
 
 }  // namespace
 
 cudaError_t launch_weights(const WeightsParams& p, int sms, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(sms * 8), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, weights_kernel, p);
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = pdl_config(sms * 8, kThreads, stream, &attr);
+    return cudaLaunchKernelEx(&cfg, p.rows_per_slot == 8 ? weights_kernel<8> : p.rows_per_slot == 4 ? weights_kernel<4> : weights_kernel<0>, p);
+}
+
+// ---- joining a shared prefix
+//
+// out = o / l of the prefix's pieces and the state of the sequence's own tokens.
+// A thread takes four columns of an output row, sixteen pieces a round trip; a
+// prefix that fills the GPU leaves about 152 / units of them.  (In the split
+// kernel's segment ends instead, it cost that kernel its registers: 32 sequences
+// of 4096 tokens without any prefix 89 us for 81.)
+
+namespace {
+
+__device__ __forceinline__ void join(float& M, float& L, float4& O, float m, float l, const float4& o) {
+    const float t = fmaxf(M, m);
+    if (t == __int_as_float(0xff800000)) return;  // both empty
+    // references may lie further apart than fp32's exponents reach, and the sums still matter
+    const float fa = ex2(M - t), fb = ex2(m - t), ha = ex2(0.5f * (M - t)), hb = ex2(0.5f * (m - t));
+    L = L * ha * ha + l * hb * hb;
+    O.x = O.x * fa + o.x * fb;
+    O.y = O.y * fa + o.y * fb;
+    O.z = O.z * fa + o.z * fb;
+    O.w = O.w * fa + o.w * fb;
+    M = t;
+}
+
+template <int D>
+__global__ void __launch_bounds__(128) join_kernel(const JoinParams p) {
+    constexpr int kIn = 16;
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;
+    const int64_t row = i / (D / 4);
+    const int c = (int)(i % (D / 4));
+    if (row >= p.rows) return;
+    const int per = p.q_len * p.Hq, b = (int)(row / per), in = (int)(row - (int64_t)b * per), qi = in / p.Hq, head = in - qi * p.Hq;
+    const PrefixSeq s = p.seqs[b];
+    const float2 own = reinterpret_cast<const float2*>(p.row_ml)[row];
+    float4 O = reinterpret_cast<const float4*>(p.row_o)[row * (D / 4) + c];
+    float M = own.x, L = own.y;
+    if (s.tiles > 0) {
+        constexpr int kSub = prefix_streams(D);  // q tiles of a slot
+        const int kvh = head / p.G, r = ((b - s.start) * p.q_len + qi) * p.G + head - kvh * p.G, tile = r >> 7;
+        const int64_t W = s.total, P = prefix_plan_ctas(W, p.ctas);
+        const int unit = tile / kSub * p.Hkv + kvh;
+        const int64_t first = s.work + (int64_t)unit * s.tiles;
+        const int c0 = (int)cta_of_block(first, W, P), n = (int)cta_of_block(first + s.tiles - 1, W, P) - c0 + 1;
+        const int64_t at = (((int64_t)s.unit + unit + c0) * kSub + tile % kSub) * 128 + (r & 127);
+        const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + at;
+        const float4* po = reinterpret_cast<const float4*>(p.part_o) + at * (D / 4) + c;
+        for (int k0 = 0; k0 < n; k0 += kIn) {
+            float2 si[kIn];
+            float4 oi[kIn];
+#pragma unroll
+            for (int k = 0; k < kIn; ++k) {
+                si[k] = make_float2(__int_as_float(0xff800000), 0.f);
+                oi[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k0 + k < n) {
+                    si[k] = ml[(int64_t)(k0 + k) * kSub * 128];
+                    oi[k] = po[(int64_t)(k0 + k) * kSub * 128 * (D / 4)];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kIn; ++k) join(M, L, O, si[k].x, si[k].y, oi[k]);
+        }
+    }
+    // (a NaN sum gives NaN, no sum 0)
+    const float4 v = L != 0.f ? make_float4(O.x / L, O.y / L, O.z / L, O.w / L) : make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p.out_f32) reinterpret_cast<float4*>(p.out_f32)[row * (D / 4) + c] = v;
+    else reinterpret_cast<uint2*>(p.out)[row * (D / 4) + c] = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+
+}  // namespace
+
+cudaError_t launch_join(int D, const JoinParams& p, cudaStream_t stream) {
+    cudaLaunchAttribute attr;
+    const int64_t grid = (p.rows * (D / 4) + 127) / 128;
+    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    const cudaLaunchConfig_t cfg = pdl_config((int)grid, 128, stream, &attr);
+    return cudaLaunchKernelEx(&cfg, D == 64 ? join_kernel<64> : D == 128 ? join_kernel<128> : join_kernel<256>, p);
 }
 
 }  // namespace pda
