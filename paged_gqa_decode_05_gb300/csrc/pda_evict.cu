@@ -68,26 +68,25 @@ __device__ __forceinline__ int64_t row_at(const EvictParams& p, int64_t slot, in
     return (slot >> p.lbs) * p.blk + (slot & ((1 << p.lbs) - 1)) * p.tok + kvh * p.kvh;
 }
 
-// The sum over a block's threads; every thread gets it.  `sums` holds a word per warp.
-template <int THREADS>
-__device__ __forceinline__ int block_prefix(int x, int* sums, int& total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int y = x;
+__device__ __forceinline__ int warp_sums(int x) {  // of the lanes up to this one
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int z = __shfl_up_sync(0xffffffffu, y, o);
-        if (lane >= o) y += z;
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
     }
+    return x;
+}
+
+// The sum over the block's threads before this one.  `sums` holds a word per warp.
+template <int THREADS>
+__device__ __forceinline__ int block_before(int x, int* sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, y = warp_sums(x);
     if (lane == 31) sums[warp] = y;
     __syncthreads();
-    int before = 0, all = 0;
-    for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) before += sums[w];
-        all += sums[w];
-    }
-    __syncthreads();
-    total = all;
-    return before + y - x;
+    const int z = warp_sums(lane < THREADS / 32 ? sums[lane] : 0);
+    const int before = __shfl_sync(0xffffffffu, z, (warp + 31) & 31);
+    return (warp > 0 ? before : 0) + y - x;
 }
 
 // cached: how many keys fit behind the histogram.
@@ -158,7 +157,7 @@ __global__ void __launch_bounds__(THREADS) choose_kernel(const EvictParams p, in
             count[i] = d >= 0 ? hist[d] : 0;
             sum += count[i];
         }
-        int total, before = block_prefix<THREADS>(sum, sums, total);
+        int before = block_before<THREADS>(sum, sums);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             if (before < left && left <= before + count[i]) {
@@ -189,11 +188,9 @@ __global__ void __launch_bounds__(THREADS) choose_kernel(const EvictParams p, in
         eqs[warp] = equal;
     }
     __syncthreads();
-    int at = 0, taken = 0;
-    for (int w = 0; w < warp; ++w) {
-        at += sums[w];
-        taken += eqs[w];
-    }
+    int at = warp_sums(lane < warp ? sums[lane] : 0), taken = warp_sums(lane < warp ? eqs[lane] : 0);
+    at = __shfl_sync(0xffffffffu, at, 31);
+    taken = __shfl_sync(0xffffffffu, taken, 31);
     at += min(taken, left);
     for (int32_t t0 = lo; t0 < hi; t0 += 32) {
         const int32_t t = t0 + lane;

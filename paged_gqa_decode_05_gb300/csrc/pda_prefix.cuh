@@ -584,12 +584,20 @@ __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, const Pref
                             v[i] = __fmul2_rn(v[i], make_float2(x.x, x.y));
                             v[i + 1] = __fmul2_rn(v[i + 1], make_float2(x.z, x.w));
                         }
-                        if (p.cap != 0.f) {  // (see capped)
+                        if (p.cap != 0.f) {
+                            // (see capped; four scores share a reciprocal, which takes twice an
+                            // exponential's time: at 2^30 and above tanh is 1, and four fit fp32)
+                            const float2 one = make_float2(1.f, 1.f), c0 = make_float2(p.cap, p.cap),
+                                         c2 = make_float2(-2.f * p.cap, -2.f * p.cap);
 #pragma unroll
-                            for (int i = 0; i < kPart / 2; ++i) {
-                                const float2 e = __fadd2_rn(make_float2(ex2(v[i].x), ex2(v[i].y)), make_float2(1.f, 1.f));
-                                v[i] = __ffma2_rn(make_float2(rcp_approx(e.x), rcp_approx(e.y)),
-                                                  make_float2(-2.f * p.cap, -2.f * p.cap), make_float2(p.cap, p.cap));
+                            for (int i = 0; i < kPart / 2; i += 2) {
+                                const float2 a = __fadd2_rn(make_float2(ex2(min_nan(v[i].x, 30.f)), ex2(min_nan(v[i].y, 30.f))), one);
+                                const float2 b = __fadd2_rn(make_float2(ex2(min_nan(v[i + 1].x, 30.f)), ex2(min_nan(v[i + 1].y, 30.f))), one);
+                                const float2 ab = __fmul2_rn(a, b);
+                                const float r = rcp_approx(ab.x * ab.y);
+                                const float2 q = __fmul2_rn(make_float2(ab.y, ab.x), make_float2(r, r));  // 1 / ab
+                                v[i] = __ffma2_rn(__fmul2_rn(q, b), c2, c0);
+                                v[i + 1] = __ffma2_rn(__fmul2_rn(q, a), c2, c0);
                             }
                         }
                         if (p.slopes) {
@@ -608,11 +616,14 @@ __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, const Pref
                         const float* x = reinterpret_cast<const float*>(v);
 #pragma unroll
                         for (int i = 0; i < kPart; i += 16) tmem_st16(tS + c + i, *reinterpret_cast<const float(*)[16]>(x + i));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kPart / 2; ++i) v[i] = __fmul2_rn(v[i], make_float2(f, f));
                     }
 #pragma unroll
                     for (int i = 0; i < kPart / 2; ++i) {
-                        two[0] = fmaxf(two[0], v[i].x * f);
-                        two[1] = fmaxf(two[1], v[i].y * f);
+                        two[0] = fmaxf(two[0], v[i].x);
+                        two[1] = fmaxf(two[1], v[i].y);
                     }
                     top = fmaxf(top, fmaxf(two[0], two[1]));
                 }

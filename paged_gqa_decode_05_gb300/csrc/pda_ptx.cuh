@@ -378,6 +378,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return y;
 }
 
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
 // Packs (lo, hi) as fp16x2 with round-to-nearest-even; lo in the low half.
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t d;

@@ -169,6 +169,9 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p
                 if (col < rows && score != __int_as_float(0xff800000)) sum += ex2((score - z.x) - z.y);
             };
             if constexpr (kSR >= 4) {
+                float2 z[kSR];
+#pragma unroll
+                for (int i = 0; i < kSR; ++i) z[i] = i < rows ? ml[i] : make_float2(0.f, 0.f);
                 float4 v[kTok][kSR / 4];
 #pragma unroll
                 for (int k = 0; k < kTok; ++k)
@@ -179,13 +182,16 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p
 #pragma unroll
                 for (int k = 0; k < kTok; ++k) {
                     if (at[k] < 0 || t0 + k * kThreads >= seen) continue;
+                    float sum = 0.f;
 #pragma unroll
-                    for (int i = 0; i < kSR / 4; ++i) {
-                        add(w[k], 4 * i, v[k][i].x);
-                        add(w[k], 4 * i + 1, v[k][i].y);
-                        add(w[k], 4 * i + 2, v[k][i].z);
-                        add(w[k], 4 * i + 3, v[k][i].w);
+                    for (int i = 0; i < kSR; ++i) {
+                        const float4 f = v[k][i / 4];
+                        const float score = i % 4 == 0 ? f.x : i % 4 == 1 ? f.y : i % 4 == 2 ? f.z : f.w;
+                        // (columns past the launch row's rows were never written; a row
+                        // that sees nothing has no finite score)
+                        if (i < rows && score != __int_as_float(0xff800000)) sum += ex2((score - z[i].x) - z[i].y);
                     }
+                    w[k] += sum;
                 }
             } else {
 #pragma unroll
