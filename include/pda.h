@@ -708,17 +708,17 @@ pda_status pda_decode_scored(pda_ctx* ctx, const pda_bf16* q, const pda_cache* c
  *   shared_blocks  [groups] int32 (device): the first shared_blocks[p] entries
  *                  of the table rows of group p are taken to be the same; those
  *                  of its first sequence are read.  Other entries, and seq_lens,
- *                  are the whole sequences', as everywhere.  Outside [0,
- *                  max_blocks] it is clamped and raises PDA_DEVERR_BAD_LENGTH.
+ *                  are the whole sequences', as everywhere.
  *   starts         [groups + 1] int32 (device), not decreasing: group p is the
  *                  sequences starts[p] .. starts[p+1] - 1; sequences of no group
- *                  share nothing.  NULL: batch / groups (exact) each.  Values
- *                  outside [0, batch], or below the one before, are clamped with
- *                  the same flag.
+ *                  share nothing.  NULL: batch / groups (exact) each.
+ *                  Starts outside [0, batch] or that decrease, and counts outside
+ *                  [0, max_blocks], raise PDA_DEVERR_BAD_LENGTH, and the call takes
+ *                  nothing as shared.
  *   groups         1 .. 1024.
  *   scratch        16-byte aligned, pda_decode_shared_scratch() bytes.
  * A sequence may end inside the prefix, or be empty.  A NaN or an infinity in a
- * value of the prefix reaches every sequence of its group.  V scales of an 8-bit
+ * key or value of the prefix may reach any sequence of its group.  V scales of an 8-bit
  * prefix enter the weights in fp32 times 2^-40; what falls below 2^-126 then,
  * values below 2^-86, counts as 0.
  */

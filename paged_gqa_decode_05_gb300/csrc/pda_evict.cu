@@ -49,9 +49,8 @@ __device__ __forceinline__ uint32_t key_of(float w) {
     return (x & 0x80000000u) ? ~x : x | 0x80000000u;
 }
 
-// The slot of token t of a sequence: block * bs + place in the block, or -1 (a bad block id).
-__device__ __forceinline__ int64_t slot_of(const EvictParams& p, const int32_t* row, int32_t t) {
-    const int32_t id = row[t >> p.lbs];
+// The slot of token t, in block `id`: block * bs + place in the block, or -1 (a bad block id).
+__device__ __forceinline__ int64_t slot_of(const EvictParams& p, int32_t id, int32_t t) {
     if (id < 0 || (int64_t)id >= p.num_blocks) {
         atomicOr(p.err, kBadBlock);
         return -1;
@@ -99,6 +98,13 @@ __global__ void __launch_bounds__(THREADS) choose_kernel(const EvictParams p, in
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait_primary();
     pdl_launch_dependents();
+    const int32_t* row = p.table + (int64_t)(blockIdx.x / p.Hkv) * p.table_stride;
+    int32_t ids[4];  // of the first tokens, looked up beside the length
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t e = (tid + i * THREADS) >> p.lbs;
+        ids[i] = e < p.table_stride ? row[e] : -1;
+    }
     const Unit u = unit_of(p, blockIdx.x);
     if (tid == 0 && u.kvh == 0) {
         p.new_lens[u.b] = u.m;
@@ -109,9 +115,8 @@ __global__ void __launch_bounds__(THREADS) choose_kernel(const EvictParams p, in
         for (int32_t i = tid; i < p.keep; i += THREADS) kept[i] = i < u.n ? i : -1;
         return;
     }
-    const int32_t* row = p.table + (int64_t)u.b * p.table_stride;
-    auto load_key = [&](int32_t t) {
-        const int64_t s = slot_of(p, row, t);
+    auto load_key = [&](int32_t t, int32_t id) {
+        const int64_t s = slot_of(p, id, t);
         if (t < p.first || t >= u.n - p.recent) return kForced;
         return key_of(s < 0 ? 0.f : p.weights[weight_at(p, s, u.kvh)]);
     };
@@ -119,12 +124,15 @@ __global__ void __launch_bounds__(THREADS) choose_kernel(const EvictParams p, in
     for (int32_t t = tid; t < here; t += 4 * THREADS) {  // four loads in flight
         uint32_t k[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) k[i] = t + i * THREADS < here ? load_key(t + i * THREADS) : 0u;
+        for (int i = 0; i < 4; ++i)
+            if (t >= 4 * THREADS && t + i * THREADS < here) ids[i] = row[(t + i * THREADS) >> p.lbs];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) k[i] = t + i * THREADS < here ? load_key(t + i * THREADS, ids[i]) : 0u;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (t + i * THREADS < here) keys[t + i * THREADS] = k[i];
     }
-    auto key = [&](int32_t t) { return t < cached ? keys[t] : load_key(t); };
+    auto key = [&](int32_t t) { return t < cached ? keys[t] : load_key(t, row[t >> p.lbs]); };
     // The key of the keep-th token in descending order: `prefix` under `mask`, `left` of them still to take
     uint32_t prefix = 0, mask = 0;
     int left = p.keep;
@@ -226,8 +234,8 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p,
         const int32_t i = i0 + tid;
         if (i < u.m) {
             const int32_t t = __ldcg(p.kept + unit * p.keep + i);
-            a = slot_of(p, p.table + (int64_t)u.b * p.table_stride, t);
-            b = slot_of(p, p.out_table + (int64_t)u.b * p.out_stride, i);
+            a = slot_of(p, p.table[(int64_t)u.b * p.table_stride + (t >> p.lbs)], t);
+            b = slot_of(p, p.out_table[(int64_t)u.b * p.out_stride + (i >> p.lbs)], i);
             if (b >= 0) {
                 p.weights[weight_at(p, b, u.kvh)] = a < 0 ? 0.f : p.weights[weight_at(p, a, u.kvh)];
                 if (p.scales)
@@ -263,7 +271,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p,
 constexpr int kPackThreads = 256;
 template <int SB>
 __global__ void __launch_bounds__(kPackThreads) pack_kernel(const EvictParams p, int32_t parts) {
-    constexpr int CH = SB / 16, U = 4, R = U * kPackThreads / CH;  // pieces of a row, of a thread; rows of a step
+    constexpr int CH = SB / 16, U = 8, R = U * kPackThreads / CH;  // pieces of a row, of a thread; rows of a step
     __shared__ int64_t src[2][R], dst[2][R];
     pdl_wait_primary();
     pdl_launch_dependents();
@@ -292,8 +300,8 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const EvictParams p,
                     const int32_t t = __ldcg(kept + i);
                     moves = t != i;
                     if (moves) {
-                        a = slot_of(p, row, t);
-                        b = slot_of(p, row, i);
+                        a = slot_of(p, row[t >> p.lbs], t);
+                        b = slot_of(p, row[i >> p.lbs], i);
                     }
                 }
                 if (part == 0 && b >= 0) {

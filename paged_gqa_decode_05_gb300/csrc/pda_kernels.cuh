@@ -183,13 +183,52 @@ __device__ __forceinline__ int32_t tokens_of(const SplitParams& p, int s, int32_
     return len < 0 ? 0 : len;
 }
 
-// Blocks of launch row s that the walk leaves out: those that its group shares
-// (from L2: the prefix kernel has just written them).
+// Where group g of a shared prefix starts.
+__device__ __forceinline__ int32_t group_start(const int32_t* starts, int g, int n_groups, int all_seqs) {
+    return starts ? starts[g] : g * (all_seqs / n_groups);
+}
+// Whether entry g of the groups is none: a start outside the batch or above the
+// next one, blocks outside the table.  One such entry, and nothing is shared.
+__device__ __forceinline__ bool bad_group(const int32_t* shared, const int32_t* starts, int g, int n_groups, int all_seqs,
+                                          int table_stride) {
+    const int32_t s = group_start(starts, g, n_groups, all_seqs);
+    if (s < 0 || s > all_seqs) return true;
+    if (g == n_groups) return false;
+    return shared[g] < 0 || shared[g] > table_stride || group_start(starts, g + 1, n_groups, all_seqs) < s;
+}
+
+// Blocks of launch row s that the walk leaves out (the scored modes): those that
+// its group shares, where anything is shared.
 template <int MODE>
-__device__ __forceinline__ int32_t skip_of(const SplitParams& p, int s) {
+__device__ __forceinline__ int32_t skip_of(const SplitParams& p, int s, bool shares) {
     if constexpr (!is_scored(MODE)) return 0;
-    if (p.sc.seqs == nullptr) return 0;
-    return __ldcg(&p.sc.seqs[row_info<is_multi(MODE)>(p, s).b].blocks);
+    if (!shares) return 0;
+    const Scoring& sc = p.sc;
+    const int b = sc.seq0 + row_info<is_multi(MODE)>(p, s).b;
+    int lo = 0, hi = sc.n_groups;  // the first entry that starts past b
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (group_start(sc.starts, mid, sc.n_groups, sc.all_seqs) <= b) lo = mid + 1; else hi = mid;
+    }
+    return lo > 0 && b < group_start(sc.starts, sc.n_groups, sc.n_groups, sc.all_seqs) ? sc.shared[lo - 1] : 0;
+}
+
+// Whether the launch leaves a shared prefix out (the scored modes; every main
+// thread calls).
+template <int MODE, int kThreads>
+__device__ __forceinline__ bool shares_prefix(const SplitParams& p) {
+    if constexpr (!is_scored(MODE)) return false;
+    const Scoring& sc = p.sc;
+    if (sc.shared == nullptr) return false;
+    bool bad = false;
+    for (int g = threadIdx.x; g <= sc.n_groups; g += kThreads)
+        bad |= bad_group(sc.shared, sc.starts, g, sc.n_groups, sc.all_seqs, p.table_stride);
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbar.red.or.pred p, 1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(any) : "r"(bad ? 1u : 0u), "n"(kThreads) : "memory");
+    if (bad) atomicOr(p.err, PDA_DEVERR_BAD_LENGTH_);
+    return any == 0;
 }
 
 // Blocks of sequence b with length entry L, validated and clamped (flags
@@ -250,7 +289,7 @@ __device__ __forceinline__ int32_t last_block_slots(const SplitParams& p, int b,
 // 0 .. kThreads-1), synchronised by named barrier 1; ends with that barrier
 // (which also publishes the stage barriers).
 template <int MODE, int kThreads>
-__device__ __forceinline__ int32_t build_prefix(const SplitParams& p, int32_t* pfx, int32_t* scan) {
+__device__ __forceinline__ int32_t build_prefix(const SplitParams& p, int32_t* pfx, int32_t* scan, bool shares) {
     constexpr int kPer = (kMaxLaunchBatch + kThreads - 1) / kThreads;
     constexpr bool MQ = is_multi(MODE);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -263,7 +302,7 @@ __device__ __forceinline__ int32_t build_prefix(const SplitParams& p, int32_t* p
 #pragma unroll
     for (int k = 0; k < kPer; ++k)
         if (lo + k < hi) {
-            const int32_t v = plan_blocks(blocks_of<MQ>(p, lo + k, L[k]) - skip_of<MODE>(p, lo + k), p.unit_cost);
+            const int32_t v = plan_blocks(blocks_of<MQ>(p, lo + k, L[k]) - skip_of<MODE>(p, lo + k, shares), p.unit_cost);
             pfx[lo + k] = v;
             sum += v;
             big = max(big, v);
@@ -413,7 +452,7 @@ template <class C, class Loader, int D, int MODE>
 __device__ __forceinline__ void run_producer(const SplitParams& p, uint32_t base_s, const SmemLayout& L,
                                              const int32_t* pfx, StageMeta* meta,
                                              volatile int* abort_flag, int64_t begin, int64_t end,
-                                             int lane) {
+                                             int lane, bool shares) {
     // The whole warp walks the plan in lockstep; lane 0 issues the barrier
     // operations, the lanes issue the copies.  Block ids come from registers,
     // loaded well before they are used so that table reads do not stall the
@@ -500,8 +539,8 @@ __device__ __forceinline__ void run_producer(const SplitParams& p, uint32_t base
         rn = bn < p.B ? row_info<MQ>(p, bn) : ri;
         const int32_t e_cur = last_entry<MQ>(p, b);
         nle = bn < p.B ? last_entry<MQ>(p, bn) : 0;
-        sk = skip_of<MODE>(p, b);
-        skn = bn < p.B ? skip_of<MODE>(p, bn) : 0;
+        sk = skip_of<MODE>(p, b, shares);
+        skn = bn < p.B ? skip_of<MODE>(p, bn, shares) : 0;
         load_ids(w, ri.b, win, nb, sk);
         if (win == 0) {
 #pragma unroll
@@ -536,7 +575,7 @@ __device__ __forceinline__ void run_producer(const SplitParams& p, uint32_t base
                 if (bn < p.B) {
                     rn = row_info<MQ>(p, bn);
                     nle = last_entry<MQ>(p, bn);
-                    skn = skip_of<MODE>(p, bn);
+                    skn = skip_of<MODE>(p, bn, shares);
                     load_ids(nx, rn.b, 0, real_blocks(pfx[bn + 1] - pfx[bn], p.unit_cost), skn);
                 }
             }
@@ -2237,12 +2276,13 @@ __global__ void __maxnreg__(split_max_regs(D, MODE)) split_kernel(const __grid_c
         if (MODE != kGather) pdl_launch_dependents();
     }
     // ends with the main warps' barrier (which also publishes the stage barriers)
-    const int32_t nv_max = build_prefix<MODE, C::kMainThreads>(p, pfx, scan);
+    const bool shares = shares_prefix<MODE, C::kMainThreads>(p);
+    const int32_t nv_max = build_prefix<MODE, C::kMainThreads>(p, pfx, scan, shares);
     int64_t begin, end;
     const GroupRange gr = cta_range<MODE>(p, pfx, nv_max, C::kST, gridDim.x, &begin, &end);
 
     if (warp == C::kConsumerWarps) {
-        run_producer<C, Bf16Loader<D, ST, MODE>, D, MODE>(p, base_s, L, pfx, meta, &abort_flag, begin, end, lane);
+        run_producer<C, Bf16Loader<D, ST, MODE>, D, MODE>(p, base_s, L, pfx, meta, &abort_flag, begin, end, lane, shares);
         return;
     }
     if constexpr (C::kTc) {

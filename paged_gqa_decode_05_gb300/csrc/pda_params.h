@@ -101,7 +101,7 @@ struct PrefixGroup {
     int32_t work;    // first position of the plan
 };
 
-// What a sequence needs of it: its group's entry and the plan's size.
+// What the join needs of it for a sequence: its group's entry and the plan's size.
 struct alignas(16) PrefixSeq {
     int32_t start, blocks, tiles, unit;
     int32_t work, total, pad[2];
@@ -114,7 +114,10 @@ struct Scoring {
     float* scores;               // [launch row][Hkv][tokens][rows_per_slot] out, or null
     float* row_ml;               // [B * q_len * Hq][2] out: (m, l) of every output row, or null
     float* row_o;                // [B * q_len * Hq][D] out, instead of the output: o of every row, or null
-    const PrefixSeq* seqs;       // [B], or null: no shared prefix
+    const int32_t* shared;       // [n_groups] blocks that each group shares, or null: none
+    const int32_t* starts;       // [n_groups + 1], or null: all_seqs / n_groups sequences each
+    int32_t n_groups, all_seqs;  // (sequences of the call)
+    int32_t seq0;                // first sequence of this launch
 };
 
 struct SplitParams {

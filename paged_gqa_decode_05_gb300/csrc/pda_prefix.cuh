@@ -126,40 +126,20 @@ struct PrefixWalk {
 template <int D, int FMT>
 __device__ __forceinline__ void prefix_plan(const PrefixParams& p, PrefixGroup* groups, int lane) {
     using C = PrefixCfg<D, FMT>;
-    int32_t top = 0, units = 0, work = 0;  // over the groups before
     bool bad = false;
+    for (int g = lane; g <= p.n_groups; g += 32) bad |= bad_group(p.shared, p.starts, g, p.n_groups, p.B, p.table_stride);
+    const bool none = __any_sync(0xffffffffu, bad);  // (the decode of the own tokens has raised the flag)
+    int32_t units = 0, work = 0;  // of the groups before
     for (int g0 = 0; g0 <= p.n_groups; g0 += 32) {
         const int g = g0 + lane;
-        int32_t s = p.B, blocks = 0;
-        if (g <= p.n_groups) {
-            s = p.starts ? p.starts[g] : g * (p.B / p.n_groups);
-            if (s < 0 || s > p.B) bad = true;
-            s = min(max(s, 0), p.B);
+        PrefixGroup out = {};
+        out.start = none || g > p.n_groups ? 0 : group_start(p.starts, g, p.n_groups, p.B);
+        if (!none && g < p.n_groups) {
+            const int32_t rows = (group_start(p.starts, g + 1, p.n_groups, p.B) - out.start) * p.q_len * p.G;
+            out.blocks = p.shared[g];
+            out.pairs = (rows + 128 * C::kStreams - 1) / (128 * C::kStreams);
+            out.tiles = out.pairs > 0 ? (int32_t)((((int64_t)out.blocks << p.lbs) + C::kT - 1) / C::kT) : 0;
         }
-        if (g < p.n_groups) {
-            blocks = p.shared[g];
-            if (blocks < 0 || blocks > p.table_stride) bad = true;
-            blocks = min(max(blocks, 0), p.table_stride);
-        }
-        int32_t m = s;  // starts that do not decrease
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int32_t y = __shfl_up_sync(0xffffffffu, m, o);
-            if (lane >= o) m = max(m, y);
-        }
-        m = max(m, top);
-        if (g <= p.n_groups && m != s) bad = true;
-        int32_t e = __shfl_down_sync(0xffffffffu, m, 1);
-        if (lane == 31 && g < p.n_groups) {
-            const int32_t raw = p.starts ? p.starts[g + 1] : (g + 1) * (p.B / p.n_groups);
-            e = max(m, min(max(raw, 0), p.B));
-        }
-        const int32_t rows = g < p.n_groups ? (e - m) * p.q_len * p.G : 0;
-        PrefixGroup out;
-        out.start = m;
-        out.blocks = blocks;
-        out.pairs = (rows + 128 * C::kStreams - 1) / (128 * C::kStreams);
-        out.tiles = out.pairs > 0 ? (int32_t)((((int64_t)blocks << p.lbs) + C::kT - 1) / C::kT) : 0;
         const int32_t u = out.tiles > 0 ? out.pairs * p.Hkv : 0, w = u * out.tiles;
         int32_t us = u, wsum = w;
 #pragma unroll
@@ -170,11 +150,9 @@ __device__ __forceinline__ void prefix_plan(const PrefixParams& p, PrefixGroup* 
         out.unit = units + us - u;
         out.work = work + wsum - w;
         if (g <= p.n_groups) groups[g] = out;
-        top = __shfl_sync(0xffffffffu, m, 31);
         units += __shfl_sync(0xffffffffu, us, 31);
         work += __shfl_sync(0xffffffffu, wsum, 31);
     }
-    if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.err, PDA_DEVERR_BAD_LENGTH_);
 }
 
 // 16 bytes, or 16 zero bytes where !use.
@@ -773,7 +751,10 @@ __global__ void __launch_bounds__(PrefixCfg<D, FMT>::kThreads, 1) prefix_kernel(
         tmem_relinquish();
         tc_fence_before();
     }
-    pdl_wait_primary();
+    // Launched behind the decode of the sequences' own tokens, which waited for all
+    // before it and hands this kernel nothing: it starts as SMs come free.  It
+    // waits for that decode before it ends, so that the join, which waits for this
+    // kernel, finds both done.
     pdl_launch_dependents();
     PrefixGroup* groups = p.n_groups <= kPlanHere ? plan : p.groups;
     if (warp == 0) prefix_plan<D, FMT>(p, groups, lane);
@@ -797,6 +778,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, FMT>::kThreads, 1) prefix_kernel(
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    pdl_wait_primary();
 }
 
 template <int D, int FMT>

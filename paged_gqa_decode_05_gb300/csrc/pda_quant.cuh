@@ -810,7 +810,8 @@ __global__ void __maxnreg__(168) quant_split_kernel(const __grid_constant__ Quan
     }
     pdl_wait_primary();
     pdl_launch_dependents();
-    const int32_t nv_max = build_prefix<MODE, C::kMainThreads>(p, pfx, scan);
+    const bool shares = shares_prefix<MODE, C::kMainThreads>(p);
+    const int32_t nv_max = build_prefix<MODE, C::kMainThreads>(p, pfx, scan, shares);
     int64_t begin, end;
     int64_t ctas = gridDim.x;
     const bool by_unit = unit_mode((int64_t)p.B * p.Hkv, ctas, real_blocks(nv_max, p.unit_cost), C::kST, p.bs);
@@ -818,7 +819,7 @@ __global__ void __maxnreg__(168) quant_split_kernel(const __grid_constant__ Quan
     const GroupRange gr = cta_range<MODE>(p, pfx, nv_max, C::kST, ctas, &begin, &end);
     if (tid == 0 && !by_unit) group = gr;  // out of registers; the syncs of the first unit's q rows order it
     if (warp == C::kWarps) {
-        run_producer<C, QuantLoader<D, NT>, D, MODE>(p, base_s, L, pfx, meta, &abort_flag, begin, end, lane);
+        run_producer<C, QuantLoader<D, NT>, D, MODE>(p, base_s, L, pfx, meta, &abort_flag, begin, end, lane, shares);
         return;
     }
     run_quant_consumer<D, FMT, NT, MODE, FINE>(p, base_s, base, L, meta, pfx, &abort_flag, &group, &notes, warp, lane);

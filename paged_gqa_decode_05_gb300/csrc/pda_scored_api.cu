@@ -87,7 +87,7 @@ pda_status run_scored(pda_ctx* ctx, const Call& c, const pda::Scoring& sc, const
     const pda_dims& d = ctx->dims;
     const int D = d.head_dim, Hq = d.num_q_heads, bs = d.block_size;
     const bool bf16 = c.cache->format == PDA_CACHE_BF16;
-    const pda::ScoredForm form = {ctx->stage_rows, c.cache->format, c.q_len > 1, !bf16 && (c.f32 || sc.row_o)};
+    const pda::ScoredForm form = {ctx->stage_rows, c.cache->format, c.q_len > 1, !bf16 && c.f32};
     pda::QuantParams p = {};
     p.sc = sc;
     pda_status st = pda::check_scale(c.scale, D, &p.scale_log2);
@@ -119,7 +119,7 @@ pda_status run_scored(pda_ctx* ctx, const Call& c, const pda::Scoring& sc, const
     p.G = ctx->G;
     p.bs = bs;
     // (the prefetch warp knows no blocks that a walk leaves out)
-    p.prefetch = p.row_gather == 0 && bs >= 8 && rows.Qr == 1 && !sc.seqs;
+    p.prefetch = p.row_gather == 0 && bs >= 8 && rows.Qr == 1 && !sc.shared;
     for (int32_t s0 = 0; s0 < c.batch; s0 += chunk) {
         const int32_t n = std::min(chunk, c.batch - s0);
         const int64_t rows0 = (int64_t)s0 * c.q_len * Hq;
@@ -129,7 +129,7 @@ pda_status run_scored(pda_ctx* ctx, const Call& c, const pda::Scoring& sc, const
         p.lens = c.lens + s0;
         p.out = c.f32 ? nullptr : static_cast<uint16_t*>(c.out) + rows0 * D;
         p.out_f32 = c.f32 ? static_cast<float*>(c.out) + rows0 * D : nullptr;
-        if (sc.seqs) p.sc.seqs = sc.seqs + s0;
+        p.sc.seq0 = s0;
         if (sc.row_o) {  // (the scores' own (m, l) are a launch's)
             p.sc.row_o = sc.row_o + rows0 * D;
             p.sc.row_ml = sc.row_ml + rows0 * 2;
@@ -398,17 +398,21 @@ PDA_EXPORT pda_status pda_decode_shared(pda_ctx* ctx, const pda_bf16* q, const p
     pp.cap = sc.cap;
     if (sc.cap != 0.f) pp.score_mult *= sc.inv_cap;
     pp.slopes = sc.slopes;
-    sc.seqs = pp.seqs;
+    sc.shared = shared_blocks;
+    sc.starts = starts;
+    sc.n_groups = groups;
+    sc.all_seqs = batch;
     sc.row_ml = reinterpret_cast<float*>(base + ss.groups + ss.seqs + ss.ml + ss.o);
     sc.row_o = reinterpret_cast<float*>(base + ss.groups + ss.seqs + ss.ml + ss.o + ss.row_ml);
     prefix_maps(ctx, cache, &pp);
     ctx->tile_steps = 0;
     if ((st = record(ctx, ctx->ev_begin, c.stream)) != PDA_OK) return st;
-    cudaError_t e = pda::launch_prefix(D, cache->format, pp, ctx->num_sms, c.stream);
-    if (e != cudaSuccess) return cuda_fail(e, "shared prefix launch");
-    if ((st = record(ctx, ctx->ev_split, c.stream)) != PDA_OK) return st;
+    // own tokens first: the prefix kernel's start, which needs nothing of them, passes under their end
     st = run_scored(ctx, c, sc, [](const pda::SplitParams&, int32_t, int32_t) -> pda_status { return PDA_OK; });
     if (st != PDA_OK) return st;
+    if ((st = record(ctx, ctx->ev_split, c.stream)) != PDA_OK) return st;
+    cudaError_t e = pda::launch_prefix(D, cache->format, pp, ctx->num_sms, c.stream);
+    if (e != cudaSuccess) return cuda_fail(e, "shared prefix launch");
     pda::JoinParams j = {};
     j.seqs = pp.seqs;
     j.row_ml = sc.row_ml;

@@ -79,19 +79,18 @@ cudaLaunchConfig_t pdl_config(int grid, int threads, cudaStream_t stream, cudaLa
     return cfg;
 }
 
-// A CTA takes chunks of kChunk tokens of a (sequence, kv head), kTok a thread
-// with their loads together.  32 sequences of 4096 tokens, 4 q heads to each of
-// 8 kv heads: 1, 2, 4 tokens a thread 14.1, 10.2, 8.3 us.
+// A CTA takes chunks of kThreads * kTok tokens of a (sequence, kv head), kTok a
+// thread with their loads together.
 constexpr int kThreads = 256, kTok = 4, kChunk = kThreads * kTok;
 
-__device__ __forceinline__ int32_t chunks_of(int32_t n) { return (int32_t)(((int64_t)n + kChunk - 1) / kChunk); }
+__device__ __forceinline__ int32_t chunks_of(int32_t n) { return (int32_t)(((uint32_t)n + kChunk - 1) / kChunk); }
 
-// kSR: rows_per_slot where it is a power of two (the scores of a token in one or two loads), 0: any.
+// kSR: rows_per_slot where it is 4 or 8 (a token's scores in one or two loads), 0: any.
 template <int kSR>
 __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p) {
     __shared__ int32_t pfx[kMaxLaunchBatch + 1];  // chunks before each sequence, one kv head
     __shared__ int32_t sums[kThreads / 32];
-    __shared__ float2 ml[kMaxGroup];              // (m, log2 l) of a launch row's q rows
+    __shared__ float2 ml[2][kMaxGroup];           // (m, log2 l) of a launch row's q rows
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait_primary();
     pdl_launch_dependents();
@@ -125,7 +124,7 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p
     __syncthreads();
     const int64_t chunks = (int64_t)pfx[p.B] * p.Hkv;
     const int64_t T = (int64_t)p.table_stride << p.lbs;
-    const int Qr = (p.q_len + p.qp - 1) / p.qp, SR = kSR > 0 ? kSR : p.rows_per_slot;
+    const int Qr = (p.q_len + p.qp - 1) / p.qp, SR = kSR > 0 ? kSR : p.rows_per_slot, mask = (1 << p.lbs) - 1;
     for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
         int lo = 0, hi = p.B - 1;  // the largest b with pfx[b] * Hkv <= c
         while (lo < hi) {
@@ -134,77 +133,81 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p
         }
         const int b = lo, n = pfx[b + 1] - pfx[b];
         const int rem = (int)(c - (int64_t)pfx[b] * p.Hkv);
-        const int kvh = rem / n;
-        const int64_t t0 = (int64_t)(rem - kvh * n) * kChunk + tid;
+        const int kvh = rem / n, t0 = (rem - kvh * n) * kChunk + tid;  // this thread's tokens: t0 + k kThreads
         const int32_t raw = p.lens[b], len = tokens(b);
+        const int32_t* ids = p.table + (int64_t)b * p.table_stride;
         int64_t at[kTok];  // -1: no token, or a bad block id (the decode raised the flag)
         float old[kTok], w[kTok];
 #pragma unroll
         for (int k = 0; k < kTok; ++k) {
-            const int64_t t = t0 + k * kThreads;
-            at[k] = -1;
+            const int t = t0 + k * kThreads;
+            const int32_t id = t < len ? ids[t >> p.lbs] : -1;
+            at[k] = id >= 0 && id < p.num_blocks ? (((int64_t)id * p.Hkv + kvh) << p.lbs) + (t & mask) : -1;
             w[k] = 0.f;
-            if (t < len) {
-                const int32_t id = p.table[(int64_t)b * p.table_stride + (t >> p.lbs)];
-                if (id >= 0 && id < p.num_blocks) at[k] = (((int64_t)id * p.Hkv + kvh) << p.lbs) + (t & ((1 << p.lbs) - 1));
-            }
         }
 #pragma unroll
         for (int k = 0; k < kTok; ++k)
-            old[k] = at[k] >= 0 && p.in && t0 + k * kThreads < (int64_t)raw - p.q_len ? p.in[at[k]] : 0.f;
+            old[k] = at[k] >= 0 && p.in && t0 + k * kThreads < raw - p.q_len ? p.in[at[k]] : 0.f;
         for (int r = 0; r < Qr; ++r) {
             const int first = r * p.qp, rows = min(p.qp, p.q_len - first) * p.G;
-            __syncthreads();
             if (tid < rows) {
                 const float2 z = reinterpret_cast<const float2*>(
                     p.row_ml)[((int64_t)b * p.q_len + first + tid / p.G) * p.Hq + kvh * p.G + tid % p.G];
-                ml[tid] = make_float2(z.x, lg2(z.y));
+                // (a query that sees nothing has scores of -inf only: weights of 0)
+                ml[r & 1][tid] = z.y == 0.f ? make_float2(0.f, 0.f) : make_float2(-z.x, -lg2(z.y));
             }
-            __syncthreads();
-            const int64_t seen = (int64_t)raw - p.q_len + first + rows / p.G;  // tokens that the launch row's queries see
+            const int seen = min(len, raw - p.q_len + first + rows / p.G);  // tokens that the launch row's queries see
             const float* s = p.scores + ((((int64_t)r * p.B + b) * p.Hkv + kvh) * T + t0) * SR;
-            auto add = [&](float& sum, int col, float score) {
-                const float2 z = ml[col];
-                // (a row that sees nothing has no finite score)
-                if (col < rows && score != __int_as_float(0xff800000)) sum += ex2((score - z.x) - z.y);
-            };
-            if constexpr (kSR >= 4) {
-                float2 z[kSR];
-#pragma unroll
-                for (int i = 0; i < kSR; ++i) z[i] = i < rows ? ml[i] : make_float2(0.f, 0.f);
-                float4 v[kTok][kSR / 4];
+            float4 v[kTok][kSR > 0 ? kSR / 4 : 1];
+            if constexpr (kSR > 0) {
 #pragma unroll
                 for (int k = 0; k < kTok; ++k)
+                    if (t0 + k * kThreads < seen) {
 #pragma unroll
-                    for (int i = 0; i < kSR / 4; ++i)
-                        if (at[k] >= 0 && t0 + k * kThreads < seen)
-                            v[k][i] = *reinterpret_cast<const float4*>(s + (int64_t)k * kThreads * kSR + 4 * i);
-#pragma unroll
-                for (int k = 0; k < kTok; ++k) {
-                    if (at[k] < 0 || t0 + k * kThreads >= seen) continue;
-                    float sum = 0.f;
-#pragma unroll
-                    for (int i = 0; i < kSR; ++i) {
-                        const float4 f = v[k][i / 4];
-                        const float score = i % 4 == 0 ? f.x : i % 4 == 1 ? f.y : i % 4 == 2 ? f.z : f.w;
-                        // (columns past the launch row's rows were never written; a row
-                        // that sees nothing has no finite score)
-                        if (i < rows && score != __int_as_float(0xff800000)) sum += ex2((score - z[i].x) - z[i].y);
+                        for (int i = 0; i < kSR / 4; ++i) v[k][i] = reinterpret_cast<const float4*>(s + k * kThreads * kSR)[i];
                     }
-                    w[k] += sum;
-                }
-            } else {
+            }
+            __syncthreads();  // (the other half of ml is read until the next row's barrier)
+            if constexpr (kSR > 0) {
+                float2 sum[kTok];
 #pragma unroll
-                for (int k = 0; k < kTok; ++k) {
-                    if (at[k] < 0 || t0 + k * kThreads >= seen) continue;
-                    for (int i = 0; i < rows; ++i) add(w[k], i, s[(int64_t)k * kThreads * SR + i]);
+                for (int k = 0; k < kTok; ++k) sum[k] = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < kSR; i += 2) {
+                    const float4 z = *reinterpret_cast<const float4*>(&ml[r & 1][i]);
+                    const bool both = i + 1 < rows;
+                    if (i < rows) {
+#pragma unroll
+                        for (int k = 0; k < kTok; ++k) {
+                            const float4 f = v[k][i / 4];
+                            float2 y = i % 4 == 0 ? make_float2(f.x, f.y) : make_float2(f.z, f.w);
+                            y = __fadd2_rn(__fadd2_rn(y, make_float2(z.x, z.z)), make_float2(z.y, z.w));
+                            sum[k] = __fadd2_rn(sum[k], make_float2(ex2(y.x), both ? ex2(y.y) : 0.f));
+                        }
+                    }
                 }
+#pragma unroll
+                for (int k = 0; k < kTok; ++k)
+                    if (t0 + k * kThreads < seen) w[k] += sum[k].x + sum[k].y;
+            } else {
+                float sum[kTok];
+#pragma unroll
+                for (int k = 0; k < kTok; ++k) sum[k] = 0.f;
+                for (int i = 0; i < rows; ++i) {
+                    const float2 z = ml[r & 1][i];
+#pragma unroll
+                    for (int k = 0; k < kTok; ++k)
+                        if (t0 + k * kThreads < seen) sum[k] += ex2((s[(int64_t)k * kThreads * SR + i] + z.x) + z.y);
+                }
+#pragma unroll
+                for (int k = 0; k < kTok; ++k) w[k] += sum[k];
             }
         }
         // summed apart from the old sum, whose last place may be above a weight's first
 #pragma unroll
         for (int k = 0; k < kTok; ++k)
             if (at[k] >= 0) p.out[at[k]] = old[k] + w[k];
+        if (Qr & 1) __syncthreads();  // the next chunk's first row takes the half that the last one reads
     }
 }
 
