@@ -151,6 +151,7 @@ PDA_HD bool unit_mode(int64_t units, int64_t ctas, int32_t max_unit_blocks, int3
 // for each of a CTA's streams, have 128 rows.
 PDA_HD constexpr int prefix_streams(int head_dim) { return head_dim == 256 ? 1 : 2; }
 constexpr int kPrefixTile = 64;  // tokens
+PDA_HD constexpr int prefix_slab(int head_dim) { return head_dim == 64 ? 32 : 64; }  // columns of a state's slabs
 PDA_HD int64_t prefix_plan_ctas(int64_t W, int64_t ctas) { return W < ctas ? W : ctas; }
 
 // Plan blocks of a unit with nb blocks.

@@ -565,18 +565,27 @@ __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, const Pref
                         if (p.cap != 0.f) {
                             // (see capped; four scores share a reciprocal, which takes twice an
                             // exponential's time: at 2^30 and above tanh is 1, and four fit fp32)
+                            float high = kNegInf;
+#pragma unroll
+                            for (int i = 0; i < kPart / 2; ++i) high = fmaxf(high, fmaxf(v[i].x, v[i].y));
+                            if (__any_sync(0xffffffffu, high > 30.f)) {
+#pragma unroll
+                                for (int i = 0; i < kPart / 2; ++i) v[i] = make_float2(min_nan(v[i].x, 30.f), min_nan(v[i].y, 30.f));
+                            }
                             const float2 one = make_float2(1.f, 1.f), c0 = make_float2(p.cap, p.cap),
                                          c2 = make_float2(-2.f * p.cap, -2.f * p.cap);
 #pragma unroll
                             for (int i = 0; i < kPart / 2; i += 2) {
-                                const float2 a = __fadd2_rn(make_float2(ex2(min_nan(v[i].x, 30.f)), ex2(min_nan(v[i].y, 30.f))), one);
-                                const float2 b = __fadd2_rn(make_float2(ex2(min_nan(v[i + 1].x, 30.f)), ex2(min_nan(v[i + 1].y, 30.f))), one);
+                                const float2 a = __fadd2_rn(make_float2(ex2(v[i].x), ex2(v[i].y)), one);
+                                const float2 b = __fadd2_rn(make_float2(ex2(v[i + 1].x), ex2(v[i + 1].y)), one);
                                 const float2 ab = __fmul2_rn(a, b);
-                                const float r = rcp_approx(ab.x * ab.y);
-                                const float2 q = __fmul2_rn(make_float2(ab.y, ab.x), make_float2(r, r));  // 1 / ab
+                                const float x = rcp_approx(ab.x * ab.y);
+                                const float2 q = __fmul2_rn(make_float2(ab.y, ab.x), make_float2(x, x));  // 1 / ab
                                 v[i] = __ffma2_rn(__fmul2_rn(q, b), c2, c0);
                                 v[i + 1] = __ffma2_rn(__fmul2_rn(q, a), c2, c0);
                             }
+                            if (!p.slopes && !cut)  // (the cap does not decrease)
+                                two[0] = fmaf(-2.f * p.cap, rcp_approx(1.f + ex2(fminf(high, 30.f))), p.cap);
                         }
                         if (p.slopes) {
                             const float far = (float)(t0 + c - own);
@@ -598,10 +607,12 @@ __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, const Pref
 #pragma unroll
                         for (int i = 0; i < kPart / 2; ++i) v[i] = __fmul2_rn(v[i], make_float2(f, f));
                     }
+                    if (p.cap == 0.f || p.slopes || cut) {  // (else the cap's largest is known)
 #pragma unroll
-                    for (int i = 0; i < kPart / 2; ++i) {
-                        two[0] = fmaxf(two[0], v[i].x);
-                        two[1] = fmaxf(two[1], v[i].y);
+                        for (int i = 0; i < kPart / 2; ++i) {
+                            two[0] = fmaxf(two[0], v[i].x);
+                            two[1] = fmaxf(two[1], v[i].y);
+                        }
                     }
                     top = fmaxf(top, fmaxf(two[0], two[1]));
                 }
@@ -670,30 +681,45 @@ __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, const Pref
             f1 = m1 == kNegInf ? 0.f : ex2(m1 - m);
             l = ml[128 + row] * f0 + (two ? ml[256 + 128 + row] * f1 : 0.f);
         }
-        if (!idle) {
-            const int64_t at = s.slot * C::kStreams + (s.dual ? st : 0);
-            const int c0 = joined ? st * (D / 2) : 0, c1 = joined ? c0 + D / 2 : D;
-            const uint32_t tO = tl + C::kTmO + (joined ? 0 : st * D);
+        // Slabs of 64 columns (32 at head size 64) go out through the q rows' memory,
+        // a stream's own tile of it, as bulk copies: [slab][row][columns], the 16-byte
+        // pieces of a row XORed with its index (8 rows in a column would meet on
+        // four banks).  Written row by row from registers instead they took 4 us.
+        constexpr int kCols = prefix_slab(D), kRowBytes = kCols * 4;
+        static_assert(128 * kRowBytes <= C::kQTileBytes, "a slab fits a q tile");
+        const int64_t at = s.slot * C::kStreams + (s.dual ? st : 0);
+        const uint32_t stage = base + st * C::kQTileBytes;
+        if (joined && !sync_all()) return;  // (the states just read lie there)
 #pragma unroll 1
-            for (int c = c0; c < c1; c += 16) {
+        for (int slab = joined ? st : 0; slab < D / kCols; slab += joined ? 2 : 1) {
+            if (!joined && slab > 0) {  // the warp's copy before has read its rows' memory
+                if (lane == 0) bulk_wait_read();
+                __syncwarp();
+            }
+#pragma unroll 1
+            for (int c = 0; c < kCols; c += 16) {
                 float o[16], x[16];
-                tmem_ld16(tO + c, o);
-                if (two) tmem_ld16(tO + D + c, x);
+                tmem_ld16(tl + C::kTmO + (joined ? 0 : st * D) + slab * kCols + c, o);
+                if (two) tmem_ld16(tl + C::kTmO + D + slab * kCols + c, x);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     o[i] = (o[i] * f0 + (two ? x[i] * f1 : 0.f)) * kBack;
                     if (m == kNegInf) o[i] = 0.f;  // a row that sees none of these tokens
                 }
-                if (g < s.rows) {
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4)
-                        *reinterpret_cast<float4*>(p.part_o + (at * 128 + row) * D + c + i) =
-                            make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-                }
+                for (int i = 0; i < 16; i += 4)
+                    sts_v4(stage + row * kRowBytes + ((((c + i) >> 2) ^ (row & 7)) << 4), __float_as_uint(o[i]), __float_as_uint(o[i + 1]),
+                           __float_as_uint(o[i + 2]), __float_as_uint(o[i + 3]));
             }
-            if (g < s.rows && (!joined || st == 0))
-                reinterpret_cast<float2*>(p.part_ml)[at * 128 + row] = make_float2(m, l * kBack);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)  // this warp's 32 rows
+                bulk_store(p.part_o + ((at * (D / kCols) + slab) * 128 + 32 * w) * kCols, stage + w * 32 * kRowBytes, 32 * kRowBytes);
         }
+        if (g < s.rows && (!joined || st == 0))
+            reinterpret_cast<float2*>(p.part_ml)[at * 128 + row] = make_float2(m, l * kBack);
+        if (lane == 0) bulk_wait_read();  // before the next segment's q rows
+        __syncwarp();
         tc_fence_before();
         if (!sync_all()) return;  // both streams have read both states
     }
@@ -763,6 +789,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, FMT>::kThreads, 1) prefix_kernel(
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + C::kTm);
     if (warp < C::kSoftWarps) {
         prefix_softmax<D, FMT>(p, groups, base, smem, &abort_flag, tmem, warp, lane);
+        if (lane == 0) bulk_wait();  // the states are written before the kernel ends
         tc_fence_before();
     } else if (warp < kMmaWarp) {
         prefix_load<D, FMT>(p, groups, base, smem, &abort_flag, warp - C::kSoftWarps, lane);

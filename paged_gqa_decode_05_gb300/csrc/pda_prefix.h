@@ -21,7 +21,7 @@ struct PrefixParams {
     const int32_t* starts;      // [n_groups + 1] or null: B / n_groups sequences each
     PrefixGroup* groups;        // [n_groups + 1] out
     PrefixSeq* seqs;            // [B] out
-    float* part_o;              // [slots][streams][128][D]
+    float* part_o;              // [slots][streams][D / slab][128][slab], pieces of 4 XORed with the row
     float* part_ml;             // [slots][streams][128][2]
     uint32_t* err;
     int32_t table_stride, lbs;

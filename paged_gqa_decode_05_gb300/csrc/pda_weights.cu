@@ -90,7 +90,7 @@ template <int kSR>
 __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p) {
     __shared__ int32_t pfx[kMaxLaunchBatch + 1];  // chunks before each sequence, one kv head
     __shared__ int32_t sums[kThreads / 32];
-    __shared__ float2 ml[2][kMaxGroup];           // (m, log2 l) of a launch row's q rows
+    __shared__ alignas(16) float2 ml[2][kMaxGroup];  // (-m, -log2 l) of a launch row's q rows
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait_primary();
     pdl_launch_dependents();
@@ -265,7 +265,9 @@ __global__ void __launch_bounds__(128) join_kernel(const JoinParams p) {
         const int c0 = (int)cta_of_block(first, W, P), n = (int)cta_of_block(first + s.tiles - 1, W, P) - c0 + 1;
         const int64_t at = (((int64_t)s.unit + unit + c0) * kSub + tile % kSub) * 128 + (r & 127);
         const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + at;
-        const float4* po = reinterpret_cast<const float4*>(p.part_o) + at * (D / 4) + c;
+        constexpr int kPieces = prefix_slab(D) / 4;  // 16-byte pieces of a row in a slab, XORed with the row
+        const float4* po = reinterpret_cast<const float4*>(p.part_o) + (at - (r & 127)) * (D / 4) +
+                           (c / kPieces * 128 + (r & 127)) * kPieces + (c % kPieces ^ (r & 7));
         for (int k0 = 0; k0 < n; k0 += kIn) {
             float2 si[kIn];
             float4 oi[kIn];
