@@ -289,6 +289,8 @@ PDA_EXPORT pda_status pda_decode_scored(pda_ctx* ctx, const pda_bf16* q, const p
     if (!aligned(weights_in, 4) || !aligned(weights_out, 4))
         return fail(PDA_ERR_INVALID_ARG, "weights must be 4-byte aligned");
     if (batch == 0) return PDA_OK;
+    if (weights_out && (int64_t)max_blocks * ctx->dims.block_size > (int64_t(1) << 30))
+        return fail(PDA_ERR_INVALID_ARG, "block table width %d is too large for sums of weights", max_blocks);
     const WeightsScratch ws = weights_scratch(ctx, batch, q_len, max_blocks);
     if (weights_out && (!scratch || !aligned(scratch, 16) || scratch_bytes < ws.total))
         return fail(PDA_ERR_INVALID_ARG, "weights need %lld bytes of 16-byte aligned scratch (got %lld)", (long long)ws.total,

@@ -80,7 +80,8 @@ cudaLaunchConfig_t pdl_config(int grid, int threads, cudaStream_t stream, cudaLa
 }
 
 // A CTA takes chunks of kThreads * kTok tokens of a (sequence, kv head), kTok a
-// thread with their loads together.
+// thread with their loads together.  With 1, 2, 3, 4 a thread the whole decode of
+// 32 sequences of 4096 tokens takes 105, 99.3, 100, 99.0 us.
 constexpr int kThreads = 256, kTok = 4, kChunk = kThreads * kTok;
 
 __device__ __forceinline__ int32_t chunks_of(int32_t n) { return (int32_t)(((uint32_t)n + kChunk - 1) / kChunk); }
@@ -136,37 +137,49 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p
         const int kvh = rem / n, t0 = (rem - kvh * n) * kChunk + tid;  // this thread's tokens: t0 + k kThreads
         const int32_t raw = p.lens[b], len = tokens(b);
         const int32_t* ids = p.table + (int64_t)b * p.table_stride;
-        int64_t at[kTok];  // -1: no token, or a bad block id (the decode raised the flag)
-        float old[kTok], w[kTok];
+        // loads in the order of what hangs on them: block ids, the first launch row's
+        // scores (of no id), then what lies at the ids
+        int32_t id[kTok];
+        float4 v[kTok][kSR > 0 ? kSR / 4 : 1];
+        float w[kTok];
 #pragma unroll
         for (int k = 0; k < kTok; ++k) {
             const int t = t0 + k * kThreads;
-            const int32_t id = t < len ? ids[t >> p.lbs] : -1;
-            at[k] = id >= 0 && id < p.num_blocks ? (((int64_t)id * p.Hkv + kvh) << p.lbs) + (t & mask) : -1;
+            id[k] = t < len ? ids[t >> p.lbs] : -1;
             w[k] = 0.f;
         }
-#pragma unroll
-        for (int k = 0; k < kTok; ++k)
-            old[k] = at[k] >= 0 && p.in && t0 + k * kThreads < raw - p.q_len ? p.in[at[k]] : 0.f;
-        for (int r = 0; r < Qr; ++r) {
-            const int first = r * p.qp, rows = min(p.qp, p.q_len - first) * p.G;
-            if (tid < rows) {
+        auto scores_of = [&](int r) { return p.scores + ((((int64_t)r * p.B + b) * p.Hkv + kvh) * T + t0) * SR; };
+        auto rows_of = [&](int r) { return min(p.qp, p.q_len - r * p.qp) * p.G; };
+        auto seen_of = [&](int r) { return min(len, raw - p.q_len + r * p.qp + rows_of(r) / p.G); };  // by the launch row's queries
+        auto fetch = [&](int r) {
+            if (tid < rows_of(r)) {
                 const float2 z = reinterpret_cast<const float2*>(
-                    p.row_ml)[((int64_t)b * p.q_len + first + tid / p.G) * p.Hq + kvh * p.G + tid % p.G];
+                    p.row_ml)[((int64_t)b * p.q_len + r * p.qp + tid / p.G) * p.Hq + kvh * p.G + tid % p.G];
                 // (a query that sees nothing has scores of -inf only: weights of 0)
                 ml[r & 1][tid] = z.y == 0.f ? make_float2(0.f, 0.f) : make_float2(-z.x, -lg2(z.y));
             }
-            const int seen = min(len, raw - p.q_len + first + rows / p.G);  // tokens that the launch row's queries see
-            const float* s = p.scores + ((((int64_t)r * p.B + b) * p.Hkv + kvh) * T + t0) * SR;
-            float4 v[kTok][kSR > 0 ? kSR / 4 : 1];
             if constexpr (kSR > 0) {
+                const float* s = scores_of(r);
+                const int seen = seen_of(r);
 #pragma unroll
                 for (int k = 0; k < kTok; ++k)
                     if (t0 + k * kThreads < seen) {
 #pragma unroll
-                        for (int i = 0; i < kSR / 4; ++i) v[k][i] = reinterpret_cast<const float4*>(s + k * kThreads * kSR)[i];
+                        for (int i = 0; i < kSR / 4; ++i) v[k][i] = __ldcs(reinterpret_cast<const float4*>(s + k * kThreads * kSR) + i);
                     }
             }
+        };
+        fetch(0);
+        int64_t at[kTok];  // -1: no token, or a bad block id (the decode raised the flag)
+        float old[kTok];
+#pragma unroll
+        for (int k = 0; k < kTok; ++k) {
+            at[k] = id[k] >= 0 && id[k] < p.num_blocks ? (((int64_t)id[k] * p.Hkv + kvh) << p.lbs) + ((t0 + k * kThreads) & mask) : -1;
+            old[k] = at[k] >= 0 && p.in && t0 + k * kThreads < raw - p.q_len ? p.in[at[k]] : 0.f;
+        }
+        for (int r = 0; r < Qr; ++r) {
+            if (r > 0) fetch(r);
+            const int rows = rows_of(r), seen = seen_of(r);
             __syncthreads();  // (the other half of ml is read until the next row's barrier)
             if constexpr (kSR > 0) {
                 float2 sum[kTok];
@@ -190,6 +203,7 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p
                 for (int k = 0; k < kTok; ++k)
                     if (t0 + k * kThreads < seen) w[k] += sum[k].x + sum[k].y;
             } else {
+                const float* s = scores_of(r);
                 float sum[kTok];
 #pragma unroll
                 for (int k = 0; k < kTok; ++k) sum[k] = 0.f;
