@@ -717,10 +717,10 @@ pda_status pda_decode_scored(pda_ctx* ctx, const pda_bf16* q, const pda_cache* c
  *                  nothing as shared.
  *   groups         1 .. 1024.
  *   scratch        16-byte aligned, pda_decode_shared_scratch() bytes.
- * A sequence may end inside the prefix, or be empty.  A NaN or an infinity in a
- * key or value of the prefix may reach any sequence of its group.  V scales of an 8-bit
- * prefix enter the weights in fp32 times 2^-40; what falls below 2^-126 then,
- * values below 2^-86, counts as 0.
+ * A sequence may end inside the prefix, or be empty: one whose first query does
+ * not see all of the prefix is decoded alone.  V scales of an 8-bit prefix enter
+ * the weights in fp32 times 2^-40; what falls below 2^-126 then, values below
+ * 2^-86, counts as 0.
  */
 pda_status pda_decode_shared_scratch(const pda_ctx* ctx, int32_t batch, int32_t q_len, int32_t groups,
                                      int64_t* bytes);

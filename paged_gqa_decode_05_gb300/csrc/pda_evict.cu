@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(THREADS) choose_kernel(const EvictParams p, in
     }
     int32_t* kept = p.kept + (int64_t)blockIdx.x * p.keep;
     if (u.n <= p.keep) {
-        for (int32_t i = tid; i < p.keep; i += THREADS) kept[i] = i < u.n ? i : -1;
+        for (int64_t i = tid; i < p.keep; i += THREADS) kept[i] = i < u.n ? (int32_t)i : -1;  // (keep may be near 2^31)
         return;
     }
     auto load_key = [&](int32_t t, int32_t id) {

@@ -197,10 +197,17 @@ __device__ __forceinline__ bool bad_group(const int32_t* shared, const int32_t* 
     return shared[g] < 0 || shared[g] > table_stride || group_start(starts, g + 1, n_groups, all_seqs) < s;
 }
 
-// Blocks of launch row s that the walk leaves out (the scored modes): those that
-// its group shares, where anything is shared.
+// Whether a sequence of length entry `len` shares its group's prefix: each of its
+// queries sees all of it.  (So what one sequence masks is another's only where
+// both may see it.)
+__device__ __forceinline__ bool sees_prefix(int32_t len, int32_t q_len, int64_t tokens) {
+    return (int64_t)len - q_len + 1 >= tokens;
+}
+
+// Blocks of launch row s, of length entry `len`, that the walk leaves out (the
+// scored modes): those that its group shares, where anything is shared.
 template <int MODE>
-__device__ __forceinline__ int32_t skip_of(const SplitParams& p, int s, bool shares) {
+__device__ __forceinline__ int32_t skip_of(const SplitParams& p, int s, int32_t len, bool shares) {
     if constexpr (!is_scored(MODE)) return 0;
     if (!shares) return 0;
     const Scoring& sc = p.sc;
@@ -210,7 +217,9 @@ __device__ __forceinline__ int32_t skip_of(const SplitParams& p, int s, bool sha
         const int mid = (lo + hi) >> 1;
         if (group_start(sc.starts, mid, sc.n_groups, sc.all_seqs) <= b) lo = mid + 1; else hi = mid;
     }
-    return lo > 0 && b < group_start(sc.starts, sc.n_groups, sc.n_groups, sc.all_seqs) ? sc.shared[lo - 1] : 0;
+    if (lo == 0 || b >= group_start(sc.starts, sc.n_groups, sc.n_groups, sc.all_seqs)) return 0;
+    const int32_t n = sc.shared[lo - 1];
+    return sees_prefix(len, p.q_len, (int64_t)n * p.bs) ? n : 0;
 }
 
 // Whether the launch leaves a shared prefix out (the scored modes; every main
@@ -302,7 +311,7 @@ __device__ __forceinline__ int32_t build_prefix(const SplitParams& p, int32_t* p
 #pragma unroll
     for (int k = 0; k < kPer; ++k)
         if (lo + k < hi) {
-            const int32_t v = plan_blocks(blocks_of<MQ>(p, lo + k, L[k]) - skip_of<MODE>(p, lo + k, shares), p.unit_cost);
+            const int32_t v = plan_blocks(blocks_of<MQ>(p, lo + k, L[k]) - skip_of<MODE>(p, lo + k, L[k], shares), p.unit_cost);
             pfx[lo + k] = v;
             sum += v;
             big = max(big, v);
@@ -539,8 +548,8 @@ __device__ __forceinline__ void run_producer(const SplitParams& p, uint32_t base
         rn = bn < p.B ? row_info<MQ>(p, bn) : ri;
         const int32_t e_cur = last_entry<MQ>(p, b);
         nle = bn < p.B ? last_entry<MQ>(p, bn) : 0;
-        sk = skip_of<MODE>(p, b, shares);
-        skn = bn < p.B ? skip_of<MODE>(p, bn, shares) : 0;
+        sk = skip_of<MODE>(p, b, e_cur, shares);
+        skn = bn < p.B ? skip_of<MODE>(p, bn, nle, shares) : 0;
         load_ids(w, ri.b, win, nb, sk);
         if (win == 0) {
 #pragma unroll
@@ -575,7 +584,7 @@ __device__ __forceinline__ void run_producer(const SplitParams& p, uint32_t base
                 if (bn < p.B) {
                     rn = row_info<MQ>(p, bn);
                     nle = last_entry<MQ>(p, bn);
-                    skn = skip_of<MODE>(p, bn, shares);
+                    skn = skip_of<MODE>(p, bn, nle, shares);
                     load_ids(nx, rn.b, 0, real_blocks(pfx[bn + 1] - pfx[bn], p.unit_cost), skn);
                 }
             }
@@ -1205,7 +1214,8 @@ __device__ __forceinline__ void run_consumer(const SplitParams& p, uint32_t base
                         p.l_state[row] = Lo;
                     }
                 } else {
-                    const float4 v = Ls > 0.f ? make_float4(Os.x / Ls, Os.y / Ls, Os.z / Ls, Os.w / Ls)
+                    // (the scored modes hand a NaN sum on, as the 8-bit kernels do)
+                    const float4 v = (kExt ? Ls != 0.f : Ls > 0.f) ? make_float4(Os.x / Ls, Os.y / Ls, Os.z / Ls, Os.w / Ls)
                                               : make_float4(0.f, 0.f, 0.f, 0.f);
                     const int64_t o = MQ ? qo_offset<MQ>(p, ri.b, ri.first + h / G, m.kvh * G + h % G, D) + d4
                                          : qo_offset<MQ>(p, m.b, 0, m.kvh * G, D) + 4 * i4;

@@ -43,6 +43,7 @@
 namespace pda {
 
 constexpr int kPlanHere = 16;  // groups whose plan is kept in shared memory
+constexpr uint64_t kDrainLimitNs = 10000000ull;  // a copy lands in microseconds; a phase since reused does not show
 
 template <int D, int FMT>
 struct PrefixCfg {
@@ -194,7 +195,7 @@ __device__ __forceinline__ bool lane_wait(uint32_t bar, uint32_t parity) {
 // Loader warp w fills 32 rows (half w & 1) of the slots of K (w < 2) or of V.
 template <int D, int FMT>
 __device__ __forceinline__ void prefix_load(const PrefixParams& p, const PrefixGroup* groups, uint32_t base, uint8_t* smem,
-                                            volatile int* abort_flag, int w, int lane) {
+                                            volatile int* abort_flag, int w, int lane, uint32_t& filled, uint32_t& parities) {
     using C = PrefixCfg<D, FMT>;
     constexpr int RW = C::kRW, ES = FMT == kBf16 ? 2 : 1;  // rows of this warp; bytes of an element
     constexpr int CH = D * ES / 16, RPI = 32 / CH;         // 16-byte chunks of a row; rows of an instruction
@@ -329,6 +330,8 @@ __device__ __forceinline__ void prefix_load(const PrefixParams& p, const PrefixG
                 cp_async_mbar_arrive_noinc(bar);
             }
             ++tiles;
+            filled |= 1u << at;
+            parities = (parities & ~(1u << at)) | ((n / C::kSlots) & 1u) << at;
             if constexpr (FMT != kBf16) {
                 if (lane == (int)(issued & 31u)) queue = n;
                 ++issued;
@@ -520,14 +523,16 @@ __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, const Pref
             __syncwarp();
             if (lane == 0) mbar_arrive(base + C::kQ);
         }
-        // this thread's q row: how much of the prefix it sees, and its bias
+        // this thread's q row: whether its sequence shares the prefix (else the decode of the
+        // own tokens takes it), and its bias
         const int g = tile * 128 + row;
         int vis = 0, own = 0;
         float slope = 0.f;
         if (g < s.rows) {
             const int bq = g / p.G, h = g - bq * p.G, b = bq / p.q_len, qi = bq - b * p.q_len;
-            own = max(p.lens[s.start + b], 0) - p.q_len + qi;
-            vis = min(max(own + 1, 0), s.tokens);
+            const int32_t len = p.lens[s.start + b];
+            own = max(len, 0) - p.q_len + qi;
+            vis = sees_prefix(len, p.q_len, s.tokens) ? s.tokens : 0;
             if (p.slopes) slope = p.slopes[s.kvh * p.G + h] * 1.4426950408889634f;
         }
         const bool idle = tile * 128 + 32 * w >= s.rows;  // a warp without rows
@@ -787,12 +792,13 @@ __global__ void __launch_bounds__(PrefixCfg<D, FMT>::kThreads, 1) prefix_kernel(
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + C::kTm);
+    uint32_t filled = 0, parities = 0;  // of a loader: the slots it filled, the phase of each
     if (warp < C::kSoftWarps) {
         prefix_softmax<D, FMT>(p, groups, base, smem, &abort_flag, tmem, warp, lane);
         if (lane == 0) bulk_wait();  // the states are written before the kernel ends
         tc_fence_before();
     } else if (warp < kMmaWarp) {
-        prefix_load<D, FMT>(p, groups, base, smem, &abort_flag, warp - C::kSoftWarps, lane);
+        prefix_load<D, FMT>(p, groups, base, smem, &abort_flag, warp - C::kSoftWarps, lane, filled, parities);
     } else {
         // what the sequences' own decode needs of the plan, while the first rows are on their way
         if (warp == kMmaWarp)
@@ -801,6 +807,13 @@ __global__ void __launch_bounds__(PrefixCfg<D, FMT>::kThreads, 1) prefix_kernel(
         prefix_mma<D, FMT>(p, groups, base, &abort_flag, tmem, warp - kMmaWarp);
     }
     __syncthreads();
+    if (abort_flag) {  // a wait gave up: copies may be on their way to slots that nobody waits for any more
+        const int half = (warp - C::kSoftWarps) & 1;
+        for (int i = 0; i < C::kSlots; ++i)
+            if (filled & (1u << i))
+                mbar_wait_bounded(base + (FMT == kBf16 ? C::kFull + 8 * i : C::kLanded + 8 * (2 * i + half)), (parities >> i) & 1u,
+                                  kDrainLimitNs);
+    }
     if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);

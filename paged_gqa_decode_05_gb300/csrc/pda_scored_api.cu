@@ -27,8 +27,9 @@ struct Rows {
     int32_t qp, Qr, SR;  // queries per launch row, launch rows per sequence, q rows per launch row
 };
 Rows rows_of(const pda_ctx* ctx, int32_t q_len) {
-    const int32_t qp = std::max(1, std::min(q_len, pda::kMaxGroup / ctx->G));
-    return {qp, (q_len + qp - 1) / qp, qp * ctx->G};
+    const int32_t G = ctx->dims.num_q_heads / ctx->dims.num_kv_heads;
+    const int32_t qp = std::max(1, std::min(q_len, pda::kMaxGroup / G));
+    return {qp, (q_len + qp - 1) / qp, qp * G};
 }
 
 // Sequences per launch: whole ones, as many as the partial states allow.
@@ -71,7 +72,8 @@ pda_status check_call(const pda_ctx* ctx, const Call& c) {
     if (!c.table || !c.lens || !aligned(c.table, 4) || !aligned(c.lens, 4))
         return fail(PDA_ERR_INVALID_ARG, "block_table / seq_lens must be non-NULL and 4-byte aligned");
     if (c.max_blocks < 1) return fail(PDA_ERR_INVALID_ARG, "block table width must be >= 1 (got %d)", c.max_blocks);
-    return PDA_OK;
+    float scale_log2;
+    return pda::check_scale(c.scale, ctx->dims.head_dim, &scale_log2);
 }
 
 pda_status record(const pda_ctx* ctx, cudaEvent_t ev, cudaStream_t stream) {
@@ -157,12 +159,17 @@ struct WeightsScratch {
 };
 WeightsScratch weights_scratch(const pda_ctx* ctx, int32_t batch, int32_t q_len, int32_t max_blocks) {
     const Rows r = rows_of(ctx, q_len);
-    const int64_t n = std::min(batch, std::max(1, chunk_of(ctx, r, std::max(ctx->scored_ctas[0], ctx->scored_ctas[1]))));
+    const int64_t n = std::min(batch, std::max(1, chunk_of(ctx, r, std::min(ctx->scored_ctas[0], ctx->scored_ctas[1]))));
     WeightsScratch s;
     s.scores = round256(n * r.Qr * ctx->dims.num_kv_heads * (int64_t)max_blocks * ctx->dims.block_size * r.SR * 4);
     s.row_ml = round256(n * q_len * ctx->dims.num_q_heads * 8);
     s.total = s.scores + s.row_ml;
     return s;
+}
+
+pda_status check_weights_width(const pda_ctx* ctx, int32_t max_blocks) {
+    if ((int64_t)max_blocks * ctx->dims.block_size <= (int64_t(1) << 30)) return PDA_OK;
+    return fail(PDA_ERR_INVALID_ARG, "block table width %d is too large for sums of weights", max_blocks);
 }
 
 // Scratch of a shared prefix: the plan, the states of its pieces and those of
@@ -172,7 +179,8 @@ struct SharedScratch {
 };
 SharedScratch shared_scratch(const pda_ctx* ctx, int32_t batch, int32_t q_len, int32_t n_groups) {
     const int D = ctx->dims.head_dim;
-    const int64_t units = pda::prefix_units(D, (int64_t)batch * q_len * ctx->G, n_groups, ctx->dims.num_kv_heads);
+    const int64_t G = ctx->dims.num_q_heads / ctx->dims.num_kv_heads;
+    const int64_t units = pda::prefix_units(D, batch * q_len * G, n_groups, ctx->dims.num_kv_heads);
     const int64_t rows = (units + ctx->num_sms) * pda::prefix_streams(D) * 128;
     SharedScratch s;
     s.groups = round256(((int64_t)n_groups + 1) * (int64_t)sizeof(pda::PrefixGroup));
@@ -271,8 +279,9 @@ PDA_EXPORT pda_status pda_decode_scored_scratch(const pda_ctx* ctx, int32_t batc
         (int64_t)batch * q_len > ctx->dims.max_seqs)
         return fail(PDA_ERR_INVALID_ARG, "batch %d x q_len %d outside [0, max_seqs=%d] or table width %d < 1", batch, q_len,
                     ctx->dims.max_seqs, max_blocks);
-    *bytes = weights_scratch(ctx, batch, q_len, max_blocks).total;
-    return PDA_OK;
+    const pda_status st = check_weights_width(ctx, max_blocks);
+    if (st == PDA_OK) *bytes = weights_scratch(ctx, batch, q_len, max_blocks).total;
+    return st;
 }
 
 PDA_EXPORT pda_status pda_decode_scored(pda_ctx* ctx, const pda_bf16* q, const pda_cache* cache,
@@ -289,8 +298,7 @@ PDA_EXPORT pda_status pda_decode_scored(pda_ctx* ctx, const pda_bf16* q, const p
     if (!aligned(weights_in, 4) || !aligned(weights_out, 4))
         return fail(PDA_ERR_INVALID_ARG, "weights must be 4-byte aligned");
     if (batch == 0) return PDA_OK;
-    if (weights_out && (int64_t)max_blocks * ctx->dims.block_size > (int64_t(1) << 30))
-        return fail(PDA_ERR_INVALID_ARG, "block table width %d is too large for sums of weights", max_blocks);
+    if (weights_out && (st = check_weights_width(ctx, max_blocks)) != PDA_OK) return st;
     const WeightsScratch ws = weights_scratch(ctx, batch, q_len, max_blocks);
     if (weights_out && (!scratch || !aligned(scratch, 16) || scratch_bytes < ws.total))
         return fail(PDA_ERR_INVALID_ARG, "weights need %lld bytes of 16-byte aligned scratch (got %lld)", (long long)ws.total,
@@ -361,7 +369,7 @@ PDA_EXPORT pda_status pda_decode_shared(pda_ctx* ctx, const pda_bf16* q, const p
     const pda_dims& d = ctx->dims;
     const int D = d.head_dim;
     const int64_t tiles = ((int64_t)max_blocks * d.block_size + pda::kPrefixTile - 1) / pda::kPrefixTile;
-    if (pda::prefix_units(D, (int64_t)batch * q_len * ctx->G, groups, d.num_kv_heads) * tiles > INT32_MAX)
+    if (pda::prefix_units(D, (int64_t)batch * q_len * (d.num_q_heads / d.num_kv_heads), groups, d.num_kv_heads) * tiles > INT32_MAX)
         return fail(PDA_ERR_INVALID_ARG, "block table width %d is too large for a shared prefix", max_blocks);
     const SharedScratch ss = shared_scratch(ctx, batch, q_len, groups);
     if (!scratch || !aligned(scratch, 16) || scratch_bytes < ss.total)
