@@ -84,7 +84,7 @@ cudaLaunchConfig_t pdl_config(int grid, int threads, cudaStream_t stream, cudaLa
 // 32 sequences of 4096 tokens takes 105, 99.3, 100, 99.0 us.
 constexpr int kThreads = 256, kTok = 4, kChunk = kThreads * kTok;
 
-__device__ __forceinline__ int32_t chunks_of(int32_t n) { return (int32_t)(((uint32_t)n + kChunk - 1) / kChunk); }
+__host__ __device__ __forceinline__ int32_t chunks_of(int32_t n) { return (int32_t)(((uint32_t)n + kChunk - 1) / kChunk); }
 
 // kSR: rows_per_slot where it is 4 or 8 (a token's scores in one or two loads), 0: any.
 template <int kSR>
@@ -93,8 +93,9 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p
     __shared__ int32_t sums[kThreads / 32];
     __shared__ alignas(16) float2 ml[2][kMaxGroup];  // (-m, -log2 l) of a launch row's q rows
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    pdl_wait_primary();
-    pdl_launch_dependents();
+    // Launched behind the decode, which waited for all before it: lengths, tables and
+    // the sums so far are there, so the plan and the first chunk's sums are read
+    // under its end; only its scores and row sums are waited for.
     const int32_t most = (int32_t)min((int64_t)p.table_stride << p.lbs, (int64_t)0x7fffffff);
     auto tokens = [&](int b) { return min(max(p.lens[b], 0), most); };
     constexpr int kPer = kMaxLaunchBatch / kThreads;
@@ -126,6 +127,7 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p
     const int64_t chunks = (int64_t)pfx[p.B] * p.Hkv;
     const int64_t T = (int64_t)p.table_stride << p.lbs;
     const int Qr = (p.q_len + p.qp - 1) / p.qp, SR = kSR > 0 ? kSR : p.rows_per_slot, mask = (1 << p.lbs) - 1;
+    bool waited = false;
     for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
         int lo = 0, hi = p.B - 1;  // the largest b with pfx[b] * Hkv <= c
         while (lo < hi) {
@@ -137,8 +139,6 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p
         const int kvh = rem / n, t0 = (rem - kvh * n) * kChunk + tid;  // this thread's tokens: t0 + k kThreads
         const int32_t raw = p.lens[b], len = tokens(b);
         const int32_t* ids = p.table + (int64_t)b * p.table_stride;
-        // loads in the order of what hangs on them: block ids, the first launch row's
-        // scores (of no id), then what lies at the ids
         int32_t id[kTok];
         float4 v[kTok][kSR > 0 ? kSR / 4 : 1];
         float w[kTok];
@@ -169,13 +169,21 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p
                     }
             }
         };
-        fetch(0);
+        // (loads in the order of what hangs on them: scores, of no id, before what lies at the ids)
+        const bool first = !waited;
+        if (!first) fetch(0);
         int64_t at[kTok];  // -1: no token, or a bad block id (the decode raised the flag)
         float old[kTok];
 #pragma unroll
         for (int k = 0; k < kTok; ++k) {
             at[k] = id[k] >= 0 && id[k] < p.num_blocks ? (((int64_t)id[k] * p.Hkv + kvh) << p.lbs) + ((t0 + k * kThreads) & mask) : -1;
             old[k] = at[k] >= 0 && p.in && t0 + k * kThreads < raw - p.q_len ? p.in[at[k]] : 0.f;
+        }
+        if (first) {
+            pdl_wait_primary();
+            pdl_launch_dependents();
+            waited = true;
+            fetch(0);
         }
         for (int r = 0; r < Qr; ++r) {
             if (r > 0) fetch(r);
@@ -223,13 +231,18 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p
             if (at[k] >= 0) p.out[at[k]] = old[k] + w[k];
         if (Qr & 1) __syncthreads();  // the next chunk's first row takes the half that the last one reads
     }
+    if (!waited) {
+        pdl_wait_primary();
+        pdl_launch_dependents();
+    }
 }
 
 }  // namespace
 
 cudaError_t launch_weights(const WeightsParams& p, int sms, cudaStream_t stream) {
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = pdl_config(sms * 8, kThreads, stream, &attr);
+    const int64_t most = (int64_t)p.B * p.Hkv * chunks_of((int32_t)((int64_t)p.table_stride << p.lbs));
+    const cudaLaunchConfig_t cfg = pdl_config((int)(most < sms * 8 ? most : sms * 8), kThreads, stream, &attr);
     return cudaLaunchKernelEx(&cfg, p.rows_per_slot == 8 ? weights_kernel<8> : p.rows_per_slot == 4 ? weights_kernel<4> : weights_kernel<0>, p);
 }
 
