@@ -257,20 +257,23 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p,
     constexpr int N = kMoveRows * CH / kMoveThreads;               // pieces of a thread
     constexpr int U = N < 8 ? N : 8;                               // in flight
     __shared__ int64_t src[kMoveRows], dst[kMoveRows];
-    pdl_wait_primary();
-    pdl_launch_dependents();
+    // (launched behind choose_kernel, which waited for all before it: lengths and
+    // tables are there, and only `kept` is waited for)
     const int64_t unit = blockIdx.x / chunks;
     const int32_t i0 = (int32_t)(blockIdx.x % chunks) * kMoveRows;
     const Unit u = unit_of(p, unit);
-    if (i0 >= u.m) return;
     const int tid = threadIdx.x;
+    const int32_t i = i0 + tid;
+    int64_t b = -1;
+    if (tid < kMoveRows && i < u.m) b = slot_of(p, p.out_table[(int64_t)u.b * p.out_stride + (i >> p.lbs)], i);
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    if (i0 >= u.m) return;
     if (tid < kMoveRows) {
-        int64_t a = -1, b = -1;
-        const int32_t i = i0 + tid;
+        int64_t a = -1;
         if (i < u.m) {
             const int32_t t = __ldcg(p.kept + unit * p.keep + i);
             a = slot_of(p, p.table[(int64_t)u.b * p.table_stride + (t >> p.lbs)], t);
-            b = slot_of(p, p.out_table[(int64_t)u.b * p.out_stride + (i >> p.lbs)], i);
             if (b >= 0) {
                 p.weights[weight_at(p, b, u.kvh)] = a < 0 ? 0.f : p.weights[weight_at(p, a, u.kvh)];
                 if (p.scales)
@@ -308,11 +311,11 @@ template <int SB>
 __global__ void __launch_bounds__(kPackThreads) pack_kernel(const EvictParams p, int32_t parts) {
     constexpr int CH = SB / 16, U = 8, R = U * kPackThreads / CH;  // pieces of a row, of a thread; rows of a step
     __shared__ int64_t src[2][R], dst[2][R];
-    pdl_wait_primary();
-    pdl_launch_dependents();
     const int64_t unit = blockIdx.x / (2 * parts);
     const int which = (int)(blockIdx.x / parts) & 1, part = (int)(blockIdx.x % parts);
-    const Unit u = unit_of(p, unit);
+    const Unit u = unit_of(p, unit);  // (as in move_kernel)
+    pdl_wait_primary();
+    pdl_launch_dependents();
     if (u.n <= p.keep) return;  // nothing moves
     const int tid = threadIdx.x;
     uint8_t* pool = (which ? p.v : p.k) + part * SB;
