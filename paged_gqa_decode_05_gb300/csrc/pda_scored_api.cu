@@ -369,7 +369,8 @@ PDA_EXPORT pda_status pda_decode_shared(pda_ctx* ctx, const pda_bf16* q, const p
     const pda_dims& d = ctx->dims;
     const int D = d.head_dim;
     const int64_t tiles = ((int64_t)max_blocks * d.block_size + pda::kPrefixTile - 1) / pda::kPrefixTile;
-    if (pda::prefix_units(D, (int64_t)batch * q_len * (d.num_q_heads / d.num_kv_heads), groups, d.num_kv_heads) * tiles > INT32_MAX)
+    const int64_t most = pda::prefix_units(D, (int64_t)batch * q_len * (d.num_q_heads / d.num_kv_heads), groups, d.num_kv_heads) * tiles;
+    if (most > INT32_MAX)
         return fail(PDA_ERR_INVALID_ARG, "block table width %d is too large for a shared prefix", max_blocks);
     const SharedScratch ss = shared_scratch(ctx, batch, q_len, groups);
     if (!scratch || !aligned(scratch, 16) || scratch_bytes < ss.total)
@@ -421,7 +422,8 @@ PDA_EXPORT pda_status pda_decode_shared(pda_ctx* ctx, const pda_bf16* q, const p
     st = run_scored(ctx, c, sc, [](const pda::SplitParams&, int32_t, int32_t) -> pda_status { return PDA_OK; });
     if (st != PDA_OK) return st;
     if ((st = record(ctx, ctx->ev_split, c.stream)) != PDA_OK) return st;
-    cudaError_t e = pda::launch_prefix(D, cache->format, pp, ctx->num_sms, c.stream);
+    const int ctas = (int)std::min<int64_t>(most, ctx->num_sms);  // none that no plan gives work
+    cudaError_t e = pda::launch_prefix(D, cache->format, pp, ctas, c.stream);
     if (e != cudaSuccess) return cuda_fail(e, "shared prefix launch");
     pda::JoinParams j = {};
     j.seqs = pp.seqs;
@@ -436,7 +438,7 @@ PDA_EXPORT pda_status pda_decode_shared(pda_ctx* ctx, const pda_bf16* q, const p
     j.Hq = d.num_q_heads;
     j.Hkv = d.num_kv_heads;
     j.G = ctx->G;
-    j.ctas = ctx->num_sms;
+    j.ctas = ctas;
     e = pda::launch_join(D, j, c.stream);
     if (e != cudaSuccess) return cuda_fail(e, "shared prefix join launch");
     return st == PDA_OK ? record(ctx, ctx->ev_end, c.stream) : st;
