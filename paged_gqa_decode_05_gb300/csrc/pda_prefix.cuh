@@ -127,18 +127,33 @@ struct PrefixWalk {
 template <int D, int FMT>
 __device__ __forceinline__ void prefix_plan(const PrefixParams& p, PrefixGroup* groups, int lane) {
     using C = PrefixCfg<D, FMT>;
-    bool bad = false;
-    for (int g = lane; g <= p.n_groups; g += 32) bad |= bad_group(p.shared, p.starts, g, p.n_groups, p.B, p.table_stride);
+    // a group's entries, loaded together; the first 32 groups' once
+    struct Entry { int32_t start, end, blocks; };
+    auto entry = [&](int g) {
+        Entry e = {};
+        if (g <= p.n_groups) e.start = e.end = group_start(p.starts, g, p.n_groups, p.B);
+        if (g < p.n_groups) {
+            e.end = group_start(p.starts, g + 1, p.n_groups, p.B);
+            e.blocks = p.shared[g];
+        }
+        return e;
+    };
+    auto wrong = [&](const Entry& e) {  // (bad_group)
+        return e.start < 0 || e.start > p.B || e.end < e.start || e.blocks < 0 || e.blocks > p.table_stride;
+    };
+    const Entry mine = entry(lane);
+    bool bad = wrong(mine);
+    for (int g = lane + 32; g <= p.n_groups; g += 32) bad |= wrong(entry(g));
     const bool none = __any_sync(0xffffffffu, bad);  // (the decode of the own tokens has raised the flag)
     int32_t units = 0, work = 0;  // of the groups before
     for (int g0 = 0; g0 <= p.n_groups; g0 += 32) {
         const int g = g0 + lane;
         PrefixGroup out = {};
-        out.start = none || g > p.n_groups ? 0 : group_start(p.starts, g, p.n_groups, p.B);
-        if (!none && g < p.n_groups) {
-            const int32_t rows = (group_start(p.starts, g + 1, p.n_groups, p.B) - out.start) * p.q_len * p.G;
-            out.blocks = p.shared[g];
-            out.pairs = (rows + 128 * C::kStreams - 1) / (128 * C::kStreams);
+        if (!none) {
+            const Entry e = g0 == 0 ? mine : entry(g);
+            out.start = e.start;
+            out.blocks = e.blocks;
+            out.pairs = ((e.end - e.start) * p.q_len * p.G + 128 * C::kStreams - 1) / (128 * C::kStreams);
             out.tiles = out.pairs > 0 ? (int32_t)((((int64_t)out.blocks << p.lbs) + C::kT - 1) / C::kT) : 0;
         }
         const int32_t u = out.tiles > 0 ? out.pairs * p.Hkv : 0, w = u * out.tiles;
@@ -397,7 +412,7 @@ __device__ __forceinline__ void prefix_mma(const PrefixParams& p, const PrefixGr
                 const uint32_t n = first + t + min(t + ahead, s.n), slot = n % C::kSlots, buf = pn & 1u;
                 if (!wait(base + C::kFull + 8 * slot, (n / C::kSlots) & 1u)) break;
                 if (!wait(kP + 8 * buf, (pn >> 1) & 1u)) break;
-                fence_proxy_async_smem();  // cp.async writes of the loaders
+                fence_proxy_async_smem();  // cp.async writes of the loaders, and of the q rows
                 tc_fence_after();
                 const uint32_t tP = tS0 + buf * C::kT;
                 const uint64_t v = umma_sdesc(base + C::kSlot0 + slot * C::kSlotBytes, C::kT * 128, 1024);
@@ -498,30 +513,18 @@ __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, const Pref
         {
             const int threads = s.dual ? 128 : 128 * C::kStreams, t0 = s.dual ? row : warp * 32 + lane;
             const uint32_t sQ = base + (s.dual ? st : 0) * C::kQTileBytes;
-            constexpr int U = 8;  // pieces in flight: a round trip each would be most of the kernel's start
+            const int g0 = tile * 128, bq0 = g0 / p.G, h0 = g0 - bq0 * p.G;
+            const uint32_t over = 65536u / p.G + 1;  // x / G = x * over >> 16 for x < 136
+            const uint16_t* q0 = p.q + (((int64_t)s.start * p.q_len + bq0) * p.Hq + s.kvh * p.G) * D;
 #pragma unroll 1
-            for (int i0 = t0; i0 < 128 * (D / 8); i0 += U * threads) {
-                uint4 x[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int i = i0 + u * threads, r = i / (D / 8), c = i % (D / 8), g = tile * 128 + r;
-                    x[u] = make_uint4(0u, 0u, 0u, 0u);
-                    if (g < s.rows && r < 128) {
-                        const int bq = g / p.G, h = g - bq * p.G;
-                        x[u] = *reinterpret_cast<const uint4*>(
-                            p.q + (((int64_t)s.start * p.q_len + bq) * p.Hq + s.kvh * p.G + h) * D + c * 8);
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int i = i0 + u * threads, r = i / (D / 8), c = i % (D / 8);
-                    if (r < 128)
-                        sts_v4(sQ + (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4), x[u].x, x[u].y, x[u].z, x[u].w);
-                }
+            for (int i = t0; i < 128 * (D / 8); i += threads) {
+                const int r = i / (D / 8), c = i % (D / 8);
+                const int x = h0 + r, bq = (int)((uint32_t)x * over >> 16), h = x - bq * p.G;
+                const bool use = g0 + r < s.rows;
+                cp_async_16_or_0(sQ + (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                                 use ? q0 + (int64_t)bq * p.Hq * D + h * D + c * 8 : p.q, use);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(base + C::kQ);
+            cp_async_mbar_arrive_noinc(base + C::kQ);
         }
         // this thread's q row: whether its sequence shares the prefix (else the decode of the
         // own tokens takes it), and its bias
@@ -766,7 +769,7 @@ __global__ void __launch_bounds__(PrefixCfg<D, FMT>::kThreads, 1) prefix_kernel(
         }
         for (int i = 0; i < 2; ++i) mbar_init(base + C::kPV + 8 * i, 1);
         mbar_init(base + C::kO, C::kStreams);
-        mbar_init(base + C::kQ, C::kSoftWarps);
+        mbar_init(base + C::kQ, C::kSoftWarps * 32);
         mbar_init(base + C::kSync, C::kSoftWarps * 32);
         mbar_init(base + C::kFin, C::kStreams);
         fence_mbar_init();

@@ -271,7 +271,10 @@ __device__ __forceinline__ void join(float& M, float& L, float4& O, float m, flo
 
 template <int D>
 __global__ void __launch_bounds__(128) join_kernel(const JoinParams p) {
-    constexpr int kIn = 16;
+#ifndef PDA_KIN
+#define PDA_KIN 16
+#endif
+    constexpr int kIn = PDA_KIN;
     pdl_wait_primary();
     pdl_launch_dependents();
     const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;
