@@ -480,7 +480,6 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
     float o[2 * K][4];
     uint32_t qf[K][4];
     float slope[2] = {0.f, 0.f};  // of the lane's two columns (kExt)
-    float* scores = nullptr;      // the segment's, of these columns (kExt)
     float f[2] = {0.f, 0.f}, m[2] = {kNegInf, kNegInf}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 2 * K; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -530,7 +529,6 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
             if constexpr (kExt) {
                 slope[0] = column_slope(p, md, 2 * t);
                 slope[1] = column_slope(p, md, 2 * t + 1);
-                scores = scores_of(p, md, 2 * t);
             }
             if constexpr (kHide) notes->cols[ct] = 0;
 #pragma unroll
@@ -617,8 +615,8 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
                         x[r][2] = fmaf(slope[0], far0 + 8.f, x[r][2]);
                         x[r][3] = fmaf(slope[1], far1 + 8.f, x[r][3]);
                     }
-                    if (scores) {
-                        float* at = scores + ((int64_t)pos0 + 16 * r + g) * p.rows_per_slot;
+                    if (p.sc.scores) {
+                        float* at = scores_of(p, md, 2 * t) + ((int64_t)pos0 + 16 * r + g) * p.rows_per_slot;
                         const bool first = 2 * t < md.nr, second = 2 * t + 1 < md.nr, pairs = (p.rows_per_slot & 1) == 0;
 #pragma unroll
                         for (int i = 0; i < 4; i += 2)
