@@ -2,10 +2,12 @@
 //
 // choose_kernel: a CTA per (sequence, kv head).  The tokens between the first
 // and the last ones that stay anyway are ranked by their sums as 32-bit keys of
-// the same order; the key of the last one to stay is found digit by digit (11,
-// 11 and 10 bits) from histograms in shared memory, so that a token is looked
-// at three times whatever the budget.  Ties go to the lowest index: warps own
-// consecutive runs of tokens and count theirs before they write.
+// the same order; the key of the last one to stay is found digit by digit, 11
+// bits each from the highest in which the keys differ, from histograms in shared
+// memory, until the keys that are left are few enough to compare each with all.
+// Sums of one size differ late, so that one digit leaves a few where the exponent
+// alone would leave hundreds.  Ties go to the lowest index: warps own consecutive runs of tokens
+// and count theirs before they write.
 //
 // move_kernel: rows to other blocks, in any order.  pack_kernel: rows to the
 // front of their own blocks.  There token kept[i] moves to i <= kept[i], so a
@@ -22,7 +24,7 @@ namespace pda {
 namespace {
 
 constexpr uint32_t kBadBlock = 0x1u, kBadLength = 0x2u;
-constexpr int kBins = 2048, kFew = 256;
+constexpr int kDigit = 11, kBins = 1 << kDigit, kFew = 128;
 constexpr uint32_t kForced = 0xffffffffu;
 
 struct Unit {
@@ -88,12 +90,23 @@ __device__ __forceinline__ int block_before(int x, int* sums) {
     return (warp > 0 ? before : 0) + y - x;
 }
 
+// The key of token t of a unit, from memory.  (A call where it is rare: beside the
+// keys in shared memory its code would be most of what the search fetches.)
+__device__ __noinline__ uint32_t far_key(const float* weights, const int32_t* row, int64_t num_blocks, int32_t lbs, int32_t Hkv,
+                                         int32_t kvh, int32_t t, bool forced) {
+    if (forced) return kForced;
+    const int32_t id = row[t >> lbs];
+    const bool bad = id < 0 || (int64_t)id >= num_blocks;  // (flagged when the keys were first read)
+    return key_of(bad ? 0.f : weights[(((int64_t)id * Hkv + kvh) << lbs) + (t & ((1 << lbs) - 1))]);
+}
+
 // cached: how many keys fit behind the histogram.
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS) choose_kernel(const EvictParams p, int32_t cached) {
     extern __shared__ uint32_t keys[];
     __shared__ int hist[kBins];
     __shared__ int sums[THREADS / 32], eqs[THREADS / 32];
+    __shared__ uint32_t least[THREADS / 32], most[THREADS / 32];
     __shared__ int digit, above;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait_primary();
@@ -120,6 +133,13 @@ __global__ void __launch_bounds__(THREADS) choose_kernel(const EvictParams p, in
         if (t < p.first || t >= u.n - p.recent) return kForced;
         return key_of(s < 0 ? 0.f : p.weights[weight_at(p, s, u.kvh)]);
     };
+    for (int i = tid; i < kBins; i += THREADS) hist[i] = 0;
+    uint32_t low = kForced, high = 0;  // of the keys between
+    auto seen = [&](uint32_t k) {
+        if (k == kForced) return;
+        low = min(low, k);
+        high = max(high, k);
+    };
     const int32_t here = min(u.n, cached);
     for (int32_t t = tid; t < here; t += 4 * THREADS) {  // four loads in flight
         uint32_t k[4];
@@ -130,21 +150,38 @@ __global__ void __launch_bounds__(THREADS) choose_kernel(const EvictParams p, in
         for (int i = 0; i < 4; ++i) k[i] = t + i * THREADS < here ? load_key(t + i * THREADS, ids[i]) : 0u;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (t + i * THREADS < here) keys[t + i * THREADS] = k[i];
+            if (t + i * THREADS < here) {
+                keys[t + i * THREADS] = k[i];
+                seen(k[i]);
+            }
     }
-    auto key = [&](int32_t t) { return t < cached ? keys[t] : load_key(t, row[t >> p.lbs]); };
-    // The key of the keep-th token in descending order: `prefix` under `mask`, `left` of them still to take
-    uint32_t prefix = 0, mask = 0;
-    int left = p.keep;
+    for (int32_t t = here + tid; t < u.n; t += THREADS) seen(load_key(t, row[t >> p.lbs]));
+    auto key = [&](int32_t t) {
+        return t < cached ? keys[t]
+                          : far_key(p.weights, row, p.num_blocks, p.lbs, p.Hkv, u.kvh, t, t < p.first || t >= u.n - p.recent);
+    };
+    low = __reduce_min_sync(0xffffffffu, low);
+    high = __reduce_max_sync(0xffffffffu, high);
+    if (lane == 0) {
+        least[warp] = low;
+        most[warp] = high;
+    }
+    __syncthreads();
+    low = __reduce_min_sync(0xffffffffu, least[lane % (THREADS / 32)]);
+    high = __reduce_max_sync(0xffffffffu, most[lane % (THREADS / 32)]);
+    // The key of the last one to stay: `prefix` but for its lowest `bits`, and
+    // `left` of the keys that begin so still to take.  (None to take: the largest
+    // key, of which none stays.)
+    int left = p.keep - p.first - p.recent, bits = left > 0 ? 32 - __clz(low ^ high) : 0;
+    uint32_t prefix = bits == 32 ? 0u : high >> bits << bits;
 #pragma unroll 1
-    for (int shift = 21; shift >= 0; shift = shift == 21 ? 10 : shift - 10) {
-        const int bins = shift == 0 ? 1024 : kBins;
-        for (int i = tid; i < kBins; i += THREADS) hist[i] = 0;
-        __syncthreads();
+    while (bits > 0) {
+        const int take = min(bits, kDigit), shift = bits - take, bins = 1 << take;
+        const uint32_t mask = bits == 32 ? 0u : ~0u << bits;
         for (int32_t t0 = 0; t0 < u.n; t0 += THREADS) {
             const int32_t t = t0 + tid;
-            const uint32_t k = t < u.n ? key(t) : 0u;
-            const bool mine = t < u.n && (k & mask) == prefix;
+            const uint32_t k = t < u.n ? key(t) : kForced;
+            const bool mine = k != kForced && (k & mask) == prefix;
             const uint32_t bin = (k >> shift) & (uint32_t)(bins - 1);
             // one addition for a warp of equal digits, which would meet on one bin otherwise
             const uint32_t bin0 = __shfl_sync(0xffffffffu, bin, 0);
@@ -156,7 +193,7 @@ __global__ void __launch_bounds__(THREADS) choose_kernel(const EvictParams p, in
         }
         __syncthreads();
         // bins in descending order: thread i takes a run of them
-        constexpr int kPer = kBins / THREADS > 0 ? kBins / THREADS : 1;
+        constexpr int kPer = kBins / THREADS;
         int count[kPer], sum = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
@@ -175,45 +212,49 @@ __global__ void __launch_bounds__(THREADS) choose_kernel(const EvictParams p, in
         }
         __syncthreads();
         prefix |= (uint32_t)digit << shift;
-        mask |= (uint32_t)(bins - 1) << shift;
         left -= above;
+        bits = shift;
         const int same = hist[digit];
         __syncthreads();
-        if (shift == 21 && same <= kFew) {
-            // few keys share the digit: one warp finds the other bits among them, a vote a
-            // bit (1.1 us less than two more rounds of histograms, 256 units of 4096 tokens)
-            uint32_t* few = reinterpret_cast<uint32_t*>(hist);
-            if (tid == 0) above = 0;
+        if (same == left || bits == 0) break;  // all of them stay
+        if (same > kFew) {
+            for (int i = tid; i < kBins; i += THREADS) hist[i] = 0;
             __syncthreads();
-            for (int32_t t0 = 0; t0 < u.n; t0 += THREADS) {
-                const int32_t t = t0 + tid;
-                const uint32_t k = t < u.n ? key(t) : 0u;
-                if (t < u.n && (k & mask) == prefix) few[atomicAdd(&above, 1)] = k;
-            }
-            __syncthreads();
-            if (warp == 0) {
-                uint32_t mine[kFew / 32], found = prefix;
-#pragma unroll
-                for (int i = 0; i < kFew / 32; ++i) mine[i] = 32 * i + lane < same ? few[32 * i + lane] : 0u;
-                auto at_least = [&](uint32_t x) {
-                    int n = 0;
-#pragma unroll
-                    for (int i = 0; i < kFew / 32; ++i) n += __popc(__ballot_sync(0xffffffffu, mine[i] >= x));
-                    return n;
-                };
-                for (int bit = 20; bit >= 0; --bit)
-                    if (at_least(found | 1u << bit) >= left) found |= 1u << bit;
-                const int more = found == 0xffffffffu ? 0 : at_least(found + 1u);
-                if (lane == 0) {
-                    few[0] = found;
-                    above = more;
-                }
-            }
-            __syncthreads();
-            prefix = few[0];
-            left -= above;
-            break;
+            continue;
         }
+        // Few keys: each is compared with all, by kEach threads; the one with fewer than
+        // `left` above it, and as many with its equals, is the last.
+        uint32_t* few = reinterpret_cast<uint32_t*>(hist);
+        if (tid == 0) above = 0;
+        __syncthreads();
+        for (int32_t t = tid; t < u.n; t += THREADS) {
+            const uint32_t k = key(t);
+            if (k != kForced && k >> bits == prefix >> bits) few[atomicAdd(&above, 1)] = k;
+        }
+        __syncthreads();
+        constexpr int kEach = THREADS / kFew;
+        const int mine = tid / kEach;
+        const uint32_t k = mine < same ? few[mine] : 0u;
+        int more = 0, equal = 0;
+        if (warp * 32 / kEach < same)  // (whole warps)
+            for (int i = tid % kEach; i < same; i += kEach) {
+                const uint32_t x = few[i];
+                more += x > k;
+                equal += x == k;
+            }
+#pragma unroll
+        for (int o = 1; o < kEach; o <<= 1) {
+            more += __shfl_xor_sync(0xffffffffu, more, o);
+            equal += __shfl_xor_sync(0xffffffffu, equal, o);
+        }
+        if (mine < same && tid % kEach == 0 && more < left && left <= more + equal) {
+            digit = (int)k;
+            above = more;
+        }
+        __syncthreads();
+        prefix = (uint32_t)digit;
+        left -= above;
+        break;
     }
     // Every key above `prefix` stays, and the first `left` of its own.
     const int32_t run = ((u.n + THREADS - 1) / THREADS) * 32;  // tokens of a warp
