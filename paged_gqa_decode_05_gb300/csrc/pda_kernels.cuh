@@ -2084,6 +2084,19 @@ __device__ __forceinline__ GroupRange cta_range(const SplitParams& p, const int3
     return gr;
 }
 
+// CTAs that the scored modes split a call over, by the 8-bit kernels' rule
+// (quant_plan_ctas), for its reasons: two sequences of 2047 to 4095 tokens, one
+// kv head of 64, 13.7 us at 1.5 sqrt, 13.9 at 2.4, 14.3 at 4, and 31.8 over the whole
+// grid; 32000 tokens of one of 128 34 and 105.  Twice that for blocks below 8 tokens:
+// 8000 of one of 128, blocks of one token, 23.3 us for 26.5, 32000 of two 38.9 for
+// 43.9, though 3000 of two of 256 24.5 for 20.5.
+template <bool MQ, int ST>
+__device__ __forceinline__ int64_t scored_plan_ctas(const SplitParams& p, const int32_t* pfx) {
+    const int64_t stages = ((int64_t)pfx[p.B] * p.Hkv * p.bs + ST - 1) / ST, units = (int64_t)p.B * p.Hkv;
+    const int64_t best = (int64_t)((p.bs < 8 ? 2.f : 1.f) * 2.4f * sqrtf((float)stages * (float)units));
+    return min((int64_t)gridDim.x, max(min(stages, best), (int64_t)rows_per_seq<MQ>(p)));
+}
+
 #ifndef PDA_PREFETCH_STAGES
 #define PDA_PREFETCH_STAGES 8
 #endif
@@ -2288,8 +2301,11 @@ __global__ void __maxnreg__(split_max_regs(D, MODE)) split_kernel(const __grid_c
     // ends with the main warps' barrier (which also publishes the stage barriers)
     const bool shares = shares_prefix<MODE, C::kMainThreads>(p);
     const int32_t nv_max = build_prefix<MODE, C::kMainThreads>(p, pfx, scan, shares);
-    int64_t begin, end;
-    const GroupRange gr = cta_range<MODE>(p, pfx, nv_max, C::kST, gridDim.x, &begin, &end);
+    int64_t begin, end, ctas = gridDim.x;
+    if constexpr (is_scored(MODE))
+        if (!unit_mode((int64_t)p.B * p.Hkv, ctas, real_blocks(nv_max, p.unit_cost), C::kST, p.bs))
+            ctas = scored_plan_ctas<is_multi(MODE), C::kST>(p, pfx);
+    const GroupRange gr = cta_range<MODE>(p, pfx, nv_max, C::kST, ctas, &begin, &end);
 
     if (warp == C::kConsumerWarps) {
         run_producer<C, Bf16Loader<D, ST, MODE>, D, MODE>(p, base_s, L, pfx, meta, &abort_flag, begin, end, lane, shares);

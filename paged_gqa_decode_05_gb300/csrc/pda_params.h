@@ -104,7 +104,7 @@ struct PrefixGroup {
 // What the join needs of it for a sequence: its group's entry and the plan's size.
 struct alignas(16) PrefixSeq {
     int32_t start, blocks, tiles, unit;
-    int32_t work, total, pad[2];
+    int32_t work, total, ctas, pad;
 };
 
 // What the scored modes add to a launch.  Scores are in base-2 units.

@@ -146,13 +146,12 @@ PDA_HD bool unit_mode(int64_t units, int64_t ctas, int32_t max_unit_blocks, int3
 }
 
 // The shared-prefix kernel's plan: units of (group, pair of q tiles, kv head),
-// each as many positions as the prefix has token tiles, one after another,
-// split evenly over P CTAs, none without a position.  A unit's q tiles, one
-// for each of a CTA's streams, have 128 rows.
+// each as many positions as the prefix has token tiles, one after another, split
+// evenly over CTAs (prefix_ctas).  A unit's q tiles, one for each of a CTA's
+// streams, have 128 rows.
 PDA_HD constexpr int prefix_streams(int head_dim) { return head_dim == 256 ? 1 : 2; }
 constexpr int kPrefixTile = 64;  // tokens
 PDA_HD constexpr int prefix_slab(int head_dim) { return head_dim == 64 ? 32 : 64; }  // columns of a state's slabs
-PDA_HD int64_t prefix_plan_ctas(int64_t W, int64_t ctas) { return W < ctas ? W : ctas; }
 
 // Plan blocks of a unit with nb blocks.
 PDA_HD int32_t plan_blocks(int32_t nb, int32_t unit_cost) { return nb > 0 ? nb + unit_cost : 0; }

@@ -9,8 +9,8 @@
 //                it reads its row of S and writes P over it, as bf16 high and
 //                low parts, p = hi + lo to 2^-17)
 //   O += P V    (P as the A operand in tensor memory, V as an MN-major B)
-// and the result is an online-softmax state (m, l, o) per row, which the
-// scored decode of the sequences' own tokens joins (join_prefix).
+// and the result is an online-softmax state (m, l, o) per row, which join_kernel
+// (pda_weights.cu) joins with those of the sequences' own tokens.
 //
 // Work: units (pair of q tiles, kv head) of one position per token tile, cut
 // evenly over one CTA per SM.  Each CTA runs two streams of four softmax warps
@@ -23,16 +23,26 @@
 // K and V go through one ring of slots, in the order in which the products use
 // them (K runs `ahead` tiles before V), so that every slot but those in use is
 // one on its way.  Four loader warps, two for K and two for V, fill 32 rows of a
-// slot each, with TMA boxes of up to 32 rows and one 64-column slab, or, for block sizes below 8, row by
-// row with 16-byte cp.async in the same swizzle.  (Row by row for all, 32768
-// tokens of 8 kv heads of 128 took 50 us in this kernel: a slot's copies kept a
-// warp 1900 cycles.)  Rows behind the prefix's end and of bad block ids are zero-
-// filled, by coordinates outside the pool where boxes load.  The codes of 8-bit
-// caches land in the warp's own part of their slot, which spreads them to bf16
-// there; bf16 holds them exactly (4 and 8 significant bits).  K scales multiply
-// the scores, V scales the weights; weights are taken 2^-40 times, as they reach
-// 2^8 (the reference lags), scales 2^122 and codes 448, and the sum over any
-// number of tokens stays inside fp32.
+// slot each, with TMA boxes of up to 32 rows and one 64-column slab, or, for
+// block sizes below 8, row by row with 16-byte cp.async in the same swizzle.
+// (Row by row for all, a call over 32768 tokens of 8 kv heads of 128 took 101 us
+// for 79: a slot's copies kept a warp 1900 cycles.)  Rows behind the prefix's end
+// and of bad block ids are zero-filled, by coordinates outside the pool where
+// boxes load.  The codes of 8-bit caches land in the warp's own part of their
+// slot, which spreads them to bf16 there; bf16 holds them exactly (4 and 8
+// significant bits).  K scales multiply the scores, V scales the weights; weights
+// are taken 2^-40 times, as they reach 2^8 (the reference lags), scales 2^122 and
+// codes 448, and the sum over any number of tokens stays inside fp32.
+//
+// Bounds.  One q tile in bf16: memory; 32768 tokens of 8 kv heads of 128 (134 MB,
+// 19.8 us at the measured copy rate) take 20 us of token tiles, with 3 before the
+// first and 2 behind the last.  Two q tiles in 8 bits: the softmax; 16384 tokens of
+// 8 kv heads and 512 rows take 77 us, 54 tiles of 64 tokens a stream of 1260 cycles
+// to the maximum (capped) and 720 for the weights, in which the two warps of a
+// scheduler keep the exponential unit 1280 cycles and the fp32 units 1150; 26 us
+// are the products'.  Sixteen softmax warps instead of eight: 155 us a call for 124;
+// P's parts 16 tokens wide instead of 32: no faster; all of a row unrolled: slower,
+// its code no longer stays in the instruction caches.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -89,12 +99,26 @@ struct PrefixSegment {
     bool dual;        // two q tiles
 };
 
+// CTAs that W positions of `units` units are split over: none without a position,
+// and no more pieces of a unit than the join takes for the tiles they save, as
+// many for every unit where there are CTAs enough (one that walks into a second
+// unit loads q rows and writes a state twice).  3 sqrt(W units): 16000 tokens of
+// one kv head of 128 in 19.1 us, 29.3 over the whole grid, 5586 of four of 256
+// 36.8 and 48.2, 8000 of four of 64 in e4m3 21.1 and 26.4; at 2.5 sqrt 19.6, 36.4
+// and 22.6, at 4 sqrt 19.3, 47.6, 26.4.  Units cut alike: 16 units of 16384 tokens
+// in e4m3 112.6 us for 115.2.
+__device__ __forceinline__ int64_t prefix_ctas(int64_t W, int64_t units) {
+    const int64_t best = (int64_t)(3.f * sqrtf((float)W * (float)units));
+    const int64_t P = min(min(W, (int64_t)gridDim.x), max(best, (int64_t)1));
+    return units < P ? P / units * units : P;
+}
+
 template <int D, int FMT>
 struct PrefixWalk {
     using C = PrefixCfg<D, FMT>;
     int64_t pos, end;
     __device__ __forceinline__ PrefixWalk(const PrefixParams& p, const PrefixGroup* groups) {
-        const int64_t W = groups[p.n_groups].work, P = prefix_plan_ctas(W, gridDim.x), c = blockIdx.x;
+        const int64_t W = groups[p.n_groups].work, P = prefix_ctas(W, groups[p.n_groups].unit), c = blockIdx.x;
         pos = c < P ? cta_begin(c, W, P) : 0;
         end = c < P ? cta_begin(c + 1, W, P) : 0;
     }
@@ -376,8 +400,8 @@ __device__ __forceinline__ void prefix_load(const PrefixParams& p, const PrefixG
 // ------------------------------------------------------------------ products
 
 // The products of stream st.  A warp each, so that one's waits pass under the
-// other's products (one warp for both streams: 32 us for 26, 32768 tokens of 8
-// kv heads of 128 and 128 q rows).
+// other's products (one warp for both streams: a call over 32768 tokens of 8 kv
+// heads of 128 and 128 q rows 70 us for 63).
 template <int D, int FMT>
 __device__ __forceinline__ void prefix_mma(const PrefixParams& p, const PrefixGroup* groups, uint32_t base,
                                            volatile int* abort_flag, uint32_t tmem, int st) {
@@ -692,14 +716,15 @@ __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, const Pref
         // Slabs of 64 columns (32 at head size 64) go out through the q rows' memory,
         // a stream's own tile of it, as bulk copies: [slab][row][columns], the 16-byte
         // pieces of a row XORed with its index (8 rows in a column would meet on
-        // four banks).  Written row by row from registers instead they took 4 us.
+        // four banks; written from registers a lane its row, a store's 32 rows are 32
+        // sectors).
         constexpr int kCols = prefix_slab(D), kRowBytes = kCols * 4;
         static_assert(128 * kRowBytes <= C::kQTileBytes, "a slab fits a q tile");
         const int64_t at = s.slot * C::kStreams + (s.dual ? st : 0);
         const uint32_t stage = base + st * C::kQTileBytes;
         if (joined && !sync_all()) return;  // (the states just read lie there)
 #pragma unroll 1
-        for (int slab = joined ? st : 0; slab < D / kCols; slab += joined ? 2 : 1) {
+        for (int slab = idle ? D / kCols : joined ? st : 0; slab < D / kCols; slab += joined ? 2 : 1) {
             if (!joined && slab > 0) {  // the warp's copy before has read its rows' memory
                 if (lane == 0) bulk_wait_read();
                 __syncwarp();
@@ -742,7 +767,8 @@ __device__ __forceinline__ PrefixSeq prefix_seq(const PrefixParams& p, const Pre
     PrefixSeq s = {};
     if (lo > 0 && b < groups[p.n_groups].start) {
         const PrefixGroup g = groups[lo - 1];
-        s = {g.start, g.blocks, g.tiles, g.unit, g.work, groups[p.n_groups].work, {0, 0}};
+        const PrefixGroup all = groups[p.n_groups];
+        s = {g.start, g.blocks, g.tiles, g.unit, g.work, all.work, (int32_t)prefix_ctas(all.work, all.unit), 0};
     }
     return s;
 }

@@ -9,7 +9,7 @@
 namespace pda {
 
 struct PrefixParams {
-    CUtensorMap tm_k, tm_v;     // boxes of min(block size, 32) rows (prefix_box in pda_scored_api.cu); with `boxes`
+    CUtensorMap tm_k, tm_v;     // boxes of min(block size, 32) rows (encode_box in pda_scored_api.cu); with `boxes`
     const uint16_t* q;          // [B, q_len, Hq, D] bf16
     const uint8_t* k_base;      // pools, elements of the cache's format
     const uint8_t* v_base;
@@ -49,7 +49,7 @@ struct JoinParams {
     uint16_t* out;              // [rows][D] bf16, or
     float* out_f32;             // fp32 when not null
     int64_t rows;               // B * q_len * Hq
-    int32_t q_len, Hq, Hkv, G, ctas;  // ctas: of the prefix kernel
+    int32_t q_len, Hq, Hkv, G;
 };
 cudaError_t launch_join(int D, const JoinParams& p, cudaStream_t stream);
 

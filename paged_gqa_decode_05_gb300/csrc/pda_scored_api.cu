@@ -438,7 +438,6 @@ PDA_EXPORT pda_status pda_decode_shared(pda_ctx* ctx, const pda_bf16* q, const p
     j.Hq = d.num_q_heads;
     j.Hkv = d.num_kv_heads;
     j.G = ctx->G;
-    j.ctas = ctas;
     e = pda::launch_join(D, j, c.stream);
     if (e != cudaSuccess) return cuda_fail(e, "shared prefix join launch");
     return st == PDA_OK ? record(ctx, ctx->ev_end, c.stream) : st;

@@ -249,10 +249,12 @@ cudaError_t launch_weights(const WeightsParams& p, int sms, cudaStream_t stream)
 // ---- joining a shared prefix
 //
 // out = o / l of the prefix's pieces and the state of the sequence's own tokens.
-// A thread takes four columns of an output row, sixteen pieces a round trip; a
-// prefix that fills the GPU leaves about 152 / units of them.  (In the split
-// kernel's segment ends instead, it cost that kernel its registers: 32 sequences
-// of 4096 tokens without any prefix 89 us for 81.)
+// A thread takes four columns of an output row and, where rows are few, every
+// kJ-th piece, eight of them a round trip; a prefix that fills the GPU leaves about
+// 152 / units pieces.  Whole calls with a CTA a row and a row a thread's columns:
+// 1024 rows of 19 pieces 51.7 and 54.3 us, 4096 of 9 122 and 115.
+// (In the split kernel's segment ends instead, it cost that kernel its registers:
+// 32 sequences of 4096 tokens without any prefix 89 us for 81.)
 
 namespace {
 
@@ -269,65 +271,83 @@ __device__ __forceinline__ void join(float& M, float& L, float4& O, float m, flo
     M = t;
 }
 
-template <int D>
-__global__ void __launch_bounds__(128) join_kernel(const JoinParams p) {
-#ifndef PDA_KIN
-#define PDA_KIN 16
-#endif
-    constexpr int kIn = PDA_KIN;
+template <int D, int THREADS, int kJ>
+__global__ void __launch_bounds__(THREADS) join_kernel(const JoinParams p) {
+    constexpr int kC = D / 4, kIn = kJ > 1 ? 8 : 16;  // threads of a row's columns; pieces in flight
+    __shared__ float4 others[kJ][kC];
+    __shared__ float2 other_ml[kJ][kC];
     pdl_wait_primary();
     pdl_launch_dependents();
-    const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;
-    const int64_t row = i / (D / 4);
-    const int c = (int)(i % (D / 4));
-    if (row >= p.rows) return;
+    static_assert(kJ == 1 || THREADS == kC * kJ, "a row a CTA, or a row a thread's columns");
+    const int64_t row = kJ > 1 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * (THREADS / kC) + threadIdx.x / kC;
+    const int c = threadIdx.x % kC, part = kJ > 1 ? threadIdx.x / kC : 0;
+    if (kJ == 1 && row >= p.rows) return;
     const int per = p.q_len * p.Hq, b = (int)(row / per), in = (int)(row - (int64_t)b * per), qi = in / p.Hq, head = in - qi * p.Hq;
     const PrefixSeq s = p.seqs[b];
-    const float2 own = reinterpret_cast<const float2*>(p.row_ml)[row];
-    float4 O = reinterpret_cast<const float4*>(p.row_o)[row * (D / 4) + c];
-    float M = own.x, L = own.y;
+    float M = __int_as_float(0xff800000), L = 0.f;
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (part == 0) {
+        const float2 own = reinterpret_cast<const float2*>(p.row_ml)[row];
+        O = reinterpret_cast<const float4*>(p.row_o)[row * kC + c];
+        M = own.x;
+        L = own.y;
+    }
     if (s.tiles > 0) {
         constexpr int kSub = prefix_streams(D);  // q tiles of a slot
         const int kvh = head / p.G, r = ((b - s.start) * p.q_len + qi) * p.G + head - kvh * p.G, tile = r >> 7;
-        const int64_t W = s.total, P = prefix_plan_ctas(W, p.ctas);
         const int unit = tile / kSub * p.Hkv + kvh;
         const int64_t first = s.work + (int64_t)unit * s.tiles;
-        const int c0 = (int)cta_of_block(first, W, P), n = (int)cta_of_block(first + s.tiles - 1, W, P) - c0 + 1;
+        const int c0 = (int)cta_of_block(first, s.total, s.ctas), n = (int)cta_of_block(first + s.tiles - 1, s.total, s.ctas) - c0 + 1;
         const int64_t at = (((int64_t)s.unit + unit + c0) * kSub + tile % kSub) * 128 + (r & 127);
         const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + at;
         constexpr int kPieces = prefix_slab(D) / 4;  // 16-byte pieces of a row in a slab, XORed with the row
-        const float4* po = reinterpret_cast<const float4*>(p.part_o) + (at - (r & 127)) * (D / 4) +
+        const float4* po = reinterpret_cast<const float4*>(p.part_o) + (at - (r & 127)) * kC +
                            (c / kPieces * 128 + (r & 127)) * kPieces + (c % kPieces ^ (r & 7));
-        for (int k0 = 0; k0 < n; k0 += kIn) {
+        for (int k0 = part; k0 < n; k0 += kIn * kJ) {
             float2 si[kIn];
             float4 oi[kIn];
 #pragma unroll
             for (int k = 0; k < kIn; ++k) {
                 si[k] = make_float2(__int_as_float(0xff800000), 0.f);
                 oi[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (k0 + k < n) {
-                    si[k] = ml[(int64_t)(k0 + k) * kSub * 128];
-                    oi[k] = po[(int64_t)(k0 + k) * kSub * 128 * (D / 4)];
+                if (k0 + k * kJ < n) {
+                    si[k] = ml[(int64_t)(k0 + k * kJ) * kSub * 128];
+                    oi[k] = po[(int64_t)(k0 + k * kJ) * kSub * 128 * kC];
                 }
             }
 #pragma unroll
             for (int k = 0; k < kIn; ++k) join(M, L, O, si[k].x, si[k].y, oi[k]);
         }
+        if (kJ > 1 && part > 0) {
+            others[part][c] = O;
+            other_ml[part][c] = make_float2(M, L);
+        }
+        if (kJ > 1) __syncthreads();
+        if (part == 0)
+            for (int k = 1; k < kJ; ++k) join(M, L, O, other_ml[k][c].x, other_ml[k][c].y, others[k][c]);
     }
+    if (part > 0) return;
     // (a NaN sum gives NaN, no sum 0)
     const float4 v = L != 0.f ? make_float4(O.x / L, O.y / L, O.z / L, O.w / L) : make_float4(0.f, 0.f, 0.f, 0.f);
-    if (p.out_f32) reinterpret_cast<float4*>(p.out_f32)[row * (D / 4) + c] = v;
-    else reinterpret_cast<uint2*>(p.out)[row * (D / 4) + c] = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    if (p.out_f32) reinterpret_cast<float4*>(p.out_f32)[row * kC + c] = v;
+    else reinterpret_cast<uint2*>(p.out)[row * kC + c] = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
 }  // namespace
 
-cudaError_t launch_join(int D, const JoinParams& p, cudaStream_t stream) {
-    cudaLaunchAttribute attr;
-    const int64_t grid = (p.rows * (D / 4) + 127) / 128;
+template <int D>
+cudaError_t launch_join_as(const JoinParams& p, cudaStream_t stream) {
+    constexpr int kC = D / 4, kT = 128;
+    const bool few = p.rows < 2048;
+    const int64_t grid = few ? p.rows : (p.rows * kC + 127) / 128;
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    const cudaLaunchConfig_t cfg = pdl_config((int)grid, 128, stream, &attr);
-    return cudaLaunchKernelEx(&cfg, D == 64 ? join_kernel<64> : D == 128 ? join_kernel<128> : join_kernel<256>, p);
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = pdl_config((int)grid, few ? kT : 128, stream, &attr);
+    return cudaLaunchKernelEx(&cfg, few ? join_kernel<D, kT, kT / kC> : join_kernel<D, 128, 1>, p);
+}
+
+cudaError_t launch_join(int D, const JoinParams& p, cudaStream_t stream) {
+    return D == 64 ? launch_join_as<64>(p, stream) : D == 128 ? launch_join_as<128>(p, stream) : launch_join_as<256>(p, stream);
 }
 
 }  // namespace pda
