@@ -82,8 +82,9 @@ struct pda_ctx {
     int32_t prefix_format = 0;
     pda_pool_key prefix_key;
     CUtensorMap prefix_k, prefix_v;
-    // Scored decode: grids by cache format (bf16; 8-bit).
-    int scored_ctas[2] = {0, 0};
+    // Scored decode: grids of the bf16 forms (launch rows of up to 8, 16 and 32 q
+    // rows; 0: not on this shape) and of the 8-bit ones.
+    int scored_ctas[4] = {0, 0, 0, 0};
 };
 
 namespace pda {

@@ -1392,7 +1392,7 @@ __device__ __forceinline__ bool rows_tile_merge(const SplitParams& p, const Stag
                 Ls = Lr;
                 Os = Or;
             }
-            const float4 v = (kScaled ? Ls != 0.f : Ls > 0.f) ? make_float4(Os.x / Ls, Os.y / Ls, Os.z / Ls, Os.w / Ls)
+            const float4 v = (kScaled || kExt ? Ls != 0.f : Ls > 0.f) ? make_float4(Os.x / Ls, Os.y / Ls, Os.z / Ls, Os.w / Ls)
                                       : make_float4(0.f, 0.f, 0.f, 0.f);
             const int64_t oo = qo_offset<true>(p, ri.b, ri.first + h / G, m.kvh * G + h % G, D) + d4;
             if constexpr (kExt)
@@ -1409,12 +1409,33 @@ __device__ __forceinline__ bool rows_tile_merge(const SplitParams& p, const Stag
     return true;
 }
 
+// CTAs that the scored modes split a call over, by the 8-bit kernels' rule
+// (quant_plan_ctas), for its reasons: two sequences of 2047 to 4095 tokens, one
+// kv head of 64, 13.7 us at 1.5 sqrt, 13.9 at 2.4, 14.3 at 4, and 31.8 over the whole
+// grid; 32000 tokens of one of 128 34 and 105.  Twice that for blocks below 8 tokens:
+// 8000 of one of 128, blocks of one token, 23.3 us for 26.5, 32000 of two 38.9 for
+// 43.9, though 3000 of two of 256 24.5 for 20.5.
+template <bool MQ, int ST>
+__device__ __forceinline__ int64_t scored_plan_ctas(const SplitParams& p, const int32_t* pfx) {
+    const int64_t stages = ((int64_t)pfx[p.B] * p.Hkv * p.bs + ST - 1) / ST, units = (int64_t)p.B * p.Hkv;
+    const int64_t best = (int64_t)((p.bs < 8 ? 2.f : 1.f) * 2.4f * sqrtf((float)stages * (float)units));
+    return min((int64_t)gridDim.x, max(min(stages, best), (int64_t)rows_per_seq<MQ>(p)));
+}
+
+// CTAs that a call's work is split over, outside unit mode.
+template <int MODE, int ST>
+__device__ __forceinline__ int64_t plan_ctas(const SplitParams& p, const int32_t* pfx) {
+    if constexpr (is_scored(MODE)) return scored_plan_ctas<is_multi(MODE), ST>(p, pfx);
+    return gridDim.x;
+}
+
 template <int D, int ST, int MODE>
 __device__ __forceinline__ void run_consumer_rows(const SplitParams& p, uint32_t base_s, uint8_t* base,
                                                   const SmemLayout& L, const StageMeta* meta,
                                                   const int32_t* pfx, volatile int* abort_flag, int warp,
                                                   int lane) {
     using C = Cfg<D, ST, MODE>;
+    constexpr bool kExt = is_scored(MODE);
     constexpr int S = C::kStages;
     constexpr int KS = C::kKSteps;       // 16-column steps of D
     constexpr int NT = D / 8;            // n8 tiles of O over D
@@ -1461,7 +1482,8 @@ __device__ __forceinline__ void run_consumer_rows(const SplitParams& p, uint32_t
     uint32_t phase = 0;
     int32_t ticket = 0;  // consumer thread 0: this piece's ticket for its split unit
     const int ct = warp * 32 + lane;
-    zero_empty_rows<D, kThreadsC>(p, pfx, ct);
+    zero_empty_rows<D, kThreadsC, kExt>(p, pfx, ct);
+    float slope0 = 0.f, slope1 = 0.f;  // of the lane's two rows (kExt)
 
     while (true) {
         if (*abort_flag) break;
@@ -1480,6 +1502,10 @@ __device__ __forceinline__ void run_consumer_rows(const SplitParams& p, uint32_t
         if (m.flags & kSegBegin) {  // (m, l, o) are reset: at the start and after each segment end
             const uint8_t* sq = base + (sV - base_s) + C::kTileBytes;  // [nr][D] bf16
             const bool v0 = row0 < m.nr, v1 = row1 < m.nr;
+            if constexpr (kExt) {
+                slope0 = column_slope(p, m, row0);
+                slope1 = column_slope(p, m, row1);
+            }
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) {
                 const uint8_t* ra = sq + (size_t)(row0 * D + 16 * kk + 2 * t) * 2;
@@ -1514,11 +1540,27 @@ __device__ __forceinline__ void run_consumer_rows(const SplitParams& p, uint32_t
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[j][e] *= sl2;
+            const int pos0 = m.j0 * p.bs + r0;  // the warp's first token
+            if constexpr (kExt) {
+                if (p.sc.cap != 0.f) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[j][e] = capped(p.sc, s[j][e]);
+                }
+                if (p.sc.slopes) {  // times the token's place less the query's
+                    const float far0 = (float)(pos0 + 2 * t - m.lim - qc0), far1 = (float)(pos0 + 2 * t - m.lim - qc1);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            s[j][e] = fmaf(e < 2 ? slope0 : slope1, (e < 2 ? far0 : far1) + (float)(8 * j + (e & 1)), s[j][e]);
+                }
+            }
             // Masks: the rows past the stage's valid ones and, causally, the tokens
             // past a row's query (query qi of the launch row sees tokens up to
             // m.lim + qi).  Element [j][e] stays iff 8j + (e & 1) <= th(e); the
             // thresholds are taken once, and stages that need no mask skip it.
-            const int pos0 = m.j0 * p.bs + r0;  // the warp's first token
             if (partial || pos0 + 15 > m.lim) {
                 const int tv = m.n_valid - 1 - r0 - 2 * t;
                 const int th0 = min(tv, m.lim + qc0 - pos0 - 2 * t);
@@ -1528,6 +1570,18 @@ __device__ __forceinline__ void run_consumer_rows(const SplitParams& p, uint32_t
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (8 * j + (e & 1) > (e < 2 ? th0 : th1)) s[j][e] = kNegInf;
+            }
+            if constexpr (kExt) {
+                if (p.sc.scores) {  // (eight lanes' rows of a token side by side)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int row = e < 2 ? row0 : row1, at = r0 + 8 * j + 2 * t + (e & 1);
+                            if (row < m.nr && at < m.n_valid)
+                                scores_of(p, m, row)[((int64_t)m.j0 * p.bs + at) * p.rows_per_slot] = s[j][e];
+                        }
+                }
             }
             // row max over the 16 tokens (the quad's lanes)
             float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
@@ -1609,7 +1663,7 @@ __device__ __forceinline__ void run_consumer_rows(const SplitParams& p, uint32_t
             UnitPieces pc;
             pc.cf = 0; pc.su = 0; pc.n = 1; pc.every = true;
             // the CTA's group, recomputed here rather than kept in registers over the loop
-            const GroupRange grs = group_of_cta(blockIdx.x, pfx, p.B, rows_per_seq<true>(p), p.Hkv, gridDim.x);
+            const GroupRange grs = group_of_cta(blockIdx.x, pfx, p.B, rows_per_seq<true>(p), p.Hkv, plan_ctas<MODE, ST>(p, pfx));
             if (!whole) pc = unit_pieces(pfx, m.b, m.kvh, p.Hkv, p.unit_cost, grs);
             const RowInfo ri = row_info<true>(p, m.b);
             int role = kRoleAbort;
@@ -1635,9 +1689,9 @@ __device__ __forceinline__ void run_consumer_rows(const SplitParams& p, uint32_t
                     m0 = m1 = kNegInf;
                     l0 = l1 = 0.f;
                 }
-                if (!rows_tile_merge<D, kThreadsC>(p, m, tile, ct, ticket, pc, grs, ri,
-                                                   RowSlices<D, kSlices>{st_m, st_l, st_o}, st_role, cbar, cphase,
-                                                   abort_flag, role)) {
+                if (!rows_tile_merge<D, kThreadsC, 16, false, kExt>(p, m, tile, ct, ticket, pc, grs, ri,
+                                                                    RowSlices<D, kSlices>{st_m, st_l, st_o}, st_role,
+                                                                    cbar, cphase, abort_flag, role)) {
                     stop = true;
                     break;
                 }
@@ -2084,19 +2138,6 @@ __device__ __forceinline__ GroupRange cta_range(const SplitParams& p, const int3
     return gr;
 }
 
-// CTAs that the scored modes split a call over, by the 8-bit kernels' rule
-// (quant_plan_ctas), for its reasons: two sequences of 2047 to 4095 tokens, one
-// kv head of 64, 13.7 us at 1.5 sqrt, 13.9 at 2.4, 14.3 at 4, and 31.8 over the whole
-// grid; 32000 tokens of one of 128 34 and 105.  Twice that for blocks below 8 tokens:
-// 8000 of one of 128, blocks of one token, 23.3 us for 26.5, 32000 of two 38.9 for
-// 43.9, though 3000 of two of 256 24.5 for 20.5.
-template <bool MQ, int ST>
-__device__ __forceinline__ int64_t scored_plan_ctas(const SplitParams& p, const int32_t* pfx) {
-    const int64_t stages = ((int64_t)pfx[p.B] * p.Hkv * p.bs + ST - 1) / ST, units = (int64_t)p.B * p.Hkv;
-    const int64_t best = (int64_t)((p.bs < 8 ? 2.f : 1.f) * 2.4f * sqrtf((float)stages * (float)units));
-    return min((int64_t)gridDim.x, max(min(stages, best), (int64_t)rows_per_seq<MQ>(p)));
-}
-
 #ifndef PDA_PREFETCH_STAGES
 #define PDA_PREFETCH_STAGES 8
 #endif
@@ -2283,7 +2324,7 @@ __global__ void __maxnreg__(split_max_regs(D, MODE)) split_kernel(const __grid_c
     if (warp == C::kMainThreads / 32) {  // the prefetch warp: joins nothing below
         // (not in the two-q-tile row forms: the call alone costs its main loop
         // registers, and its consumers set its time)
-        if constexpr (MODE != kGather && MODE != kMultiRows32 && !C::kTc)
+        if constexpr (MODE != kGather && q_tiles(MODE) != 2)
             if (!early && p.prefetch) prefetch_first_stages<MODE, TouchBoxes<ST>>(p, lane);
         return;
     }
@@ -2304,7 +2345,7 @@ __global__ void __maxnreg__(split_max_regs(D, MODE)) split_kernel(const __grid_c
     int64_t begin, end, ctas = gridDim.x;
     if constexpr (is_scored(MODE))
         if (!unit_mode((int64_t)p.B * p.Hkv, ctas, real_blocks(nv_max, p.unit_cost), C::kST, p.bs))
-            ctas = scored_plan_ctas<is_multi(MODE), C::kST>(p, pfx);
+            ctas = plan_ctas<MODE, C::kST>(p, pfx);
     const GroupRange gr = cta_range<MODE>(p, pfx, nv_max, C::kST, ctas, &begin, &end);
 
     if (warp == C::kConsumerWarps) {

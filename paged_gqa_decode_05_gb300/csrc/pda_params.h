@@ -31,24 +31,25 @@ constexpr int kMaxRowsPerWalk = 32;                      // q rows one KV walk s
 // to 32 q rows.  kMultiTc is the row form of 32 q rows on the tcgen05
 // tensor cores: accumulators in tensor memory, one thread issues the MMAs.
 // kScored and kScoredMulti are the n8 form of one and of several causal queries
-// with what Scoring adds: capped and distance-biased scores, scores written
+// and kScoredRows16 / kScoredRows32 the row form, with what Scoring adds: capped and distance-biased scores, scores written
 // out, a shared prefix left out and the state of the rest handed on.
 enum Mode : int {
     kOneShot = 0, kTiled = 1, kGather = 2, kMulti = 3, kMultiRows16 = 4, kMultiRows32 = 5, kMultiTc = 6, kScored = 7,
-    kScoredMulti = 8
+    kScoredMulti = 8, kScoredRows16 = 9, kScoredRows32 = 10
 };
 constexpr int kNumModes = 7;  // of the context's split kernels; the scored ones are set up on their own
 __host__ __device__ constexpr bool is_multi(int mode) {
     return mode == kMulti || mode == kMultiRows16 || mode == kMultiRows32 || mode == kMultiTc ||
-           mode == kScoredMulti;
+           mode == kScoredMulti || mode == kScoredRows16 || mode == kScoredRows32;
 }
-__host__ __device__ constexpr bool is_scored(int mode) { return mode == kScored || mode == kScoredMulti; }
+__host__ __device__ constexpr bool is_scored(int mode) { return mode >= kScored && mode <= kScoredRows32; }
 __host__ __device__ constexpr bool is_tc(int mode) { return mode == kMultiTc; }
 __host__ __device__ constexpr bool writes_output(int mode) { return mode == kOneShot || mode == kScored || is_multi(mode); }
 // 16-row q tiles of the row form (0: the n8 form); the tcgen05 form's segment
 // end merges its 32 rows in two such tiles.
 __host__ __device__ constexpr int q_tiles(int mode) {
-    return mode == kMultiRows16 ? 1 : (mode == kMultiRows32 || mode == kMultiTc) ? 2 : 0;
+    return mode == kMultiRows16 || mode == kScoredRows16                           ? 1
+           : mode == kMultiRows32 || mode == kMultiTc || mode == kScoredRows32 ? 2 : 0;
 }
 // q rows a stage's q area holds.
 __host__ __device__ constexpr int stage_q_rows(int mode) { return q_tiles(mode) ? 16 * q_tiles(mode) : kMaxGroup; }
@@ -70,7 +71,7 @@ PDA_HD int stage_tokens(int D, int block_size) { return D == 256 && !block_boxes
 // runs two CTAs per SM with three 36 KB stages at head size 128, the tcgen05
 // form one CTA with five 40 KB stages, which leaves room for a 512-entry
 // block prefix.
-PDA_HD int max_launch_rows(int mode) { return (mode == kMultiRows16 || mode == kMultiTc) ? 512 : kMaxLaunchBatch; }
+PDA_HD int max_launch_rows(int mode) { return (q_tiles(mode) == 1 || mode == kMultiTc) ? 512 : kMaxLaunchBatch; }
 // The unit-cost class of a mode (pda_plan.h).
 PDA_HD int32_t cost_class(int mode) {
     return mode == kMulti ? kCostMultiN8 : mode == kMultiRows16 ? kCostRows16

@@ -14,15 +14,21 @@ template <int N>
 using Int = std::integral_constant<int, N>;
 template <int D, class R, class Visit>
 R visit_scored_bf16(const ScoredForm& f, R none, const Visit& visit) {
-    if (f.st == 64) return f.multi ? visit(Int<64>(), Int<kScoredMulti>()) : visit(Int<64>(), Int<kScored>());
-    if constexpr (D == 256)
-        if (f.st == 32) return f.multi ? visit(Int<32>(), Int<kScoredMulti>()) : visit(Int<32>(), Int<kScored>());
+    if (f.st == 64) {
+        if (f.rows == 1) return visit(Int<64>(), Int<kScored>());
+        if (f.rows == 8) return visit(Int<64>(), Int<kScoredMulti>());
+        if constexpr (D <= 128) return f.rows == 16 ? visit(Int<64>(), Int<kScoredRows16>()) : visit(Int<64>(), Int<kScoredRows32>());
+    }
+    if constexpr (D == 256) {
+        if (f.st == 32 && f.rows == 1) return visit(Int<32>(), Int<kScored>());
+        if (f.st == 32 && f.rows == 8) return visit(Int<32>(), Int<kScoredMulti>());
+    }
     return none;
 }
 template <class R, class Visit>
 R visit_scored_quant(const ScoredForm& f, const Visit& visit) {
-    if (f.fine) return f.multi ? visit(Int<kScoredMulti>(), std::true_type()) : visit(Int<kScored>(), std::true_type());
-    return f.multi ? visit(Int<kScoredMulti>(), std::false_type()) : visit(Int<kScored>(), std::false_type());
+    if (f.fine) return f.rows > 1 ? visit(Int<kScoredMulti>(), std::true_type()) : visit(Int<kScored>(), std::true_type());
+    return f.rows > 1 ? visit(Int<kScoredMulti>(), std::false_type()) : visit(Int<kScored>(), std::false_type());
 }
 
 template <int D>
@@ -30,7 +36,7 @@ ScoredShape scored_shape_bf16(const ScoredForm& f) {
     return visit_scored_bf16<D>(f, ScoredShape{}, [](auto rows, auto mode) -> ScoredShape {
         using C = Cfg<D, rows(), mode()>;
         return {reinterpret_cast<const void*>(&split_kernel<D, rows(), mode()>), C::kThreads, C::kST, C::kStages,
-                (uint32_t)C::kStageBytes};
+                (uint32_t)C::kStageBytes, max_launch_rows(mode())};
     });
 }
 template <int D>
@@ -45,7 +51,7 @@ ScoredShape scored_shape_quant(const ScoredForm& f) {
     return visit_scored_quant<ScoredShape>(f, [](auto mode, auto fine) -> ScoredShape {
         using C = QuantCfg<D, 1>;
         return {reinterpret_cast<const void*>(&quant_split_kernel<D, FMT, 1, mode(), fine()>), C::kThreads, C::kST,
-                C::kStages, (uint32_t)C::kStageBytes};
+                C::kStages, (uint32_t)C::kStageBytes, max_launch_rows(mode())};
     });
 }
 template <int D, int FMT>

@@ -13,15 +13,17 @@ struct ScoredShape {
     int threads;     // with the prefetch warp
     int stage_rows, stages;
     uint32_t stage_bytes;
+    int max_rows;    // launch rows of a launch
     uint32_t smem(int B) const { return smem_layout_of(stage_bytes, kScored, stages, B).total; }
 };
 
-// An instance: stages of st rows (bf16 caches), a cache format, several causal
-// queries or one, and (8-bit caches) weights in two fp16 parts, for outputs and
-// states in fp32.
+// An instance: stages of st rows (bf16 caches), a cache format, the q rows of a
+// launch row (1: one query; 8: several causal ones; bf16 at head sizes up to 128
+// 16 and 32), and (8-bit caches) weights in two fp16 parts, for outputs and states
+// in fp32.
 struct ScoredForm {
-    int st, format;
-    bool multi, fine;
+    int st, format, rows;
+    bool fine;
 };
 ScoredShape scored_shape(int D, const ScoredForm& form);
 // p is a QuantParams; bf16 kernels take its SplitParams.

@@ -22,20 +22,43 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
 
-// Launch rows of scored decode: up to 8 q rows of a sequence each.
+// Launch rows of scored decode: up to 8 q rows of a sequence each, or, over bf16
+// caches of head sizes up to 128 where a sequence has more, up to 32 (one walk
+// over K and V for four).  3 sequences of 8000 tokens with 40 q and 8 kv heads of
+// 128 and 4 queries: 39.7 us, 62.8 in rows of 8; blocks of 4 tokens 52.6 and 88.8.
+// Over 8-bit caches rows of 8 stay: their wider forms are bound by the consumer
+// warps, not by the walks (12 rows, 5000 tokens of 256 in int8: 43.0 us for the
+// wide form's 41.6 without scores).
 struct Rows {
     int32_t qp, Qr, SR;  // queries per launch row, launch rows per sequence, q rows per launch row
+    int32_t form;        // ScoredForm::rows
+    int grid;
 };
-Rows rows_of(const pda_ctx* ctx, int32_t q_len) {
+constexpr int kQuantGrid = 3;  // (scored_ctas)
+Rows rows_of(const pda_ctx* ctx, bool bf16, int32_t q_len) {
     const int32_t G = ctx->dims.num_q_heads / ctx->dims.num_kv_heads;
-    const int32_t qp = std::max(1, std::min(q_len, pda::kMaxGroup / G));
-    return {qp, (q_len + qp - 1) / qp, qp * G};
+    Rows r;
+    int k = bf16 ? 0 : kQuantGrid;
+    if (bf16 && q_len * G > pda::kMaxGroup && ctx->scored_ctas[2] > 0) {
+        r.qp = std::min(q_len, pda::kMaxRowsPerWalk / G);
+        k = r.qp * G <= 16 && ctx->scored_ctas[1] > 0 ? 1 : 2;
+        r.form = 16 * k;
+    } else {
+        r.qp = std::max(1, std::min(q_len, pda::kMaxGroup / G));
+        r.form = q_len > 1 ? pda::kMaxGroup : 1;
+    }
+    r.Qr = (q_len + r.qp - 1) / r.qp;
+    r.SR = r.qp * G;
+    r.grid = ctx->scored_ctas[k];
+    return r;
 }
 
-// Sequences per launch: whole ones, as many as the partial states allow.
-int32_t chunk_of(const pda_ctx* ctx, const Rows& r, int grid) {
-    const int64_t fit = (ctx->part_rows / r.SR - grid) / ctx->dims.num_kv_heads;
-    return (int32_t)(std::min<int64_t>(pda::kMaxLaunchBatch, fit) / r.Qr);
+// Sequences per launch: whole ones, as many as the kernel's launch rows and the
+// partial states allow.
+int32_t chunk_of(const pda_ctx* ctx, const Rows& r) {
+    const int64_t fit = (ctx->part_rows / r.SR - r.grid) / ctx->dims.num_kv_heads;
+    const int64_t most = r.form == 16 ? pda::max_launch_rows(pda::kScoredRows16) : pda::kMaxLaunchBatch;
+    return (int32_t)(std::min(most, fit) / r.Qr);
 }
 
 struct Call {
@@ -89,20 +112,23 @@ pda_status run_scored(pda_ctx* ctx, const Call& c, const pda::Scoring& sc, const
     const pda_dims& d = ctx->dims;
     const int D = d.head_dim, Hq = d.num_q_heads, bs = d.block_size;
     const bool bf16 = c.cache->format == PDA_CACHE_BF16;
-    const pda::ScoredForm form = {ctx->stage_rows, c.cache->format, c.q_len > 1, !bf16 && c.f32};
+    const Rows rows = rows_of(ctx, bf16, c.q_len);
+    const pda::ScoredForm form = {ctx->stage_rows, c.cache->format, rows.form, !bf16 && c.f32};
     pda::QuantParams p = {};
     p.sc = sc;
     pda_status st = pda::check_scale(c.scale, D, &p.scale_log2);
     if (st != PDA_OK) return st;
-    const Rows rows = rows_of(ctx, c.q_len);
     const pda::ScoredShape shape = pda::scored_shape(D, form);
-    const int grid = ctx->scored_ctas[bf16 ? 0 : 1];
+    const int grid = rows.grid;
     if (rows.Qr > grid)
         return fail(PDA_ERR_INVALID_ARG, "q_len %d: more launch rows per sequence than CTAs (%d)", c.q_len, grid);
-    p.unit_cost = bf16 ? pda::unit_cost_blocks(ctx->stage_rows, D, bs, c.q_len > 1 ? pda::kCostMultiN8 : pda::kCostDecode)
+    const int32_t cost = rows.form == 1   ? pda::kCostDecode
+                         : rows.form == 8 ? pda::kCostMultiN8
+                         : rows.form == 16 ? pda::kCostRows16 : pda::kCostRows32;
+    p.unit_cost = bf16 ? pda::unit_cost_blocks(ctx->stage_rows, D, bs, cost)
                        : pda::quant_unit_cost(D, 1, bs);
     if ((st = pda::check_plan_size((int64_t)c.batch * rows.Qr, c.max_blocks, p.unit_cost)) != PDA_OK) return st;
-    const int32_t chunk = chunk_of(ctx, rows, grid);
+    const int32_t chunk = chunk_of(ctx, rows);
     if (chunk < 1)
         return fail(PDA_ERR_UNSUPPORTED, "q_len %d: a sequence's %d launch rows exceed the partial-state buffers", c.q_len,
                     rows.Qr);
@@ -121,7 +147,7 @@ pda_status run_scored(pda_ctx* ctx, const Call& c, const pda::Scoring& sc, const
     p.G = ctx->G;
     p.bs = bs;
     // (the prefetch warp knows no blocks that a walk leaves out)
-    p.prefetch = p.row_gather == 0 && bs >= 8 && rows.Qr == 1 && !sc.shared;
+    p.prefetch = p.row_gather == 0 && bs >= 8 && rows.Qr == 1 && rows.form != 32 && !sc.shared;
     for (int32_t s0 = 0; s0 < c.batch; s0 += chunk) {
         const int32_t n = std::min(chunk, c.batch - s0);
         const int64_t rows0 = (int64_t)s0 * c.q_len * Hq;
@@ -157,9 +183,9 @@ pda::Scoring scoring_of(const pda_scoring* s) {
 struct WeightsScratch {
     int64_t scores, row_ml, total;  // bytes; row_ml lies after the scores
 };
-WeightsScratch weights_scratch(const pda_ctx* ctx, int32_t batch, int32_t q_len, int32_t max_blocks) {
-    const Rows r = rows_of(ctx, q_len);
-    const int64_t n = std::min(batch, std::max(1, chunk_of(ctx, r, std::min(ctx->scored_ctas[0], ctx->scored_ctas[1]))));
+WeightsScratch weights_scratch(const pda_ctx* ctx, bool bf16, int32_t batch, int32_t q_len, int32_t max_blocks) {
+    const Rows r = rows_of(ctx, bf16, q_len);
+    const int64_t n = std::min(batch, std::max(1, chunk_of(ctx, r)));
     WeightsScratch s;
     s.scores = round256(n * r.Qr * ctx->dims.num_kv_heads * (int64_t)max_blocks * ctx->dims.block_size * r.SR * 4);
     s.row_ml = round256(n * q_len * ctx->dims.num_q_heads * 8);
@@ -236,30 +262,35 @@ void prefix_maps(pda_ctx* ctx, const pda_cache* c, pda::PrefixParams* p) {
 
 pda_status pda::scored_setup(pda_ctx* ctx, int optin) {
     const int D = ctx->dims.head_dim;
-    for (int k = 0; k < 2; ++k) {
+    const auto setup = [&](const ScoredForm& form, int* per_sm) -> pda_status {
+        const ScoredShape s = scored_shape(D, form);
+        if (!s.fn) return fail(PDA_ERR_UNSUPPORTED, "no scored decode kernel");
+        const int limit = (int)s.smem(s.max_rows);
+        if (limit > optin)
+            return fail(PDA_ERR_UNSUPPORTED, "needs %d bytes of shared memory per CTA (device allows %d)", limit, optin);
+        int n = 0;
+        cudaError_t e = cudaFuncSetAttribute(s.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, limit);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(s.fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, s.fn, s.threads, limit);
+        if (e != cudaSuccess) return cuda_fail(e, "scored decode attributes");
+        if (n < 1) return fail(PDA_ERR_UNSUPPORTED, "scored decode kernel does not fit on an SM");
+        *per_sm = std::min(*per_sm, n);
+        return PDA_OK;
+    };
+    // the partial states of a context are sized for its other kernels' grids
+    const int most[4] = {ctx->split_ctas, ctx->rows_ctas[0], ctx->rows_ctas[1], ctx->quant_ctas[0]};
+    for (int k = 0; k < 4; ++k) {
+        if (most[k] == 0) continue;
         int per_sm = 1 << 30;
-        for (int format : {PDA_CACHE_BF16, PDA_CACHE_E4M3, PDA_CACHE_INT8})
-            for (int f = 0; f < 4; ++f) {
-                const ScoredForm form = {ctx->stage_rows, format, (f & 1) != 0, (f & 2) != 0};
-                if ((format == PDA_CACHE_BF16) != (k == 0) || (format == PDA_CACHE_BF16 && form.fine)) continue;
-                const ScoredShape s = scored_shape(D, form);
-                if (!s.fn) return fail(PDA_ERR_UNSUPPORTED, "no scored decode kernel");
-                const int limit = (int)s.smem(kMaxLaunchBatch);
-                if (limit > optin)
-                    return fail(PDA_ERR_UNSUPPORTED, "needs %d bytes of shared memory per CTA (device allows %d)", limit,
-                                optin);
-                int n = 0;
-                cudaError_t e = cudaFuncSetAttribute(s.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, limit);
-                if (e == cudaSuccess)
-                    e = cudaFuncSetAttribute(s.fn, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                             cudaSharedmemCarveoutMaxShared);
-                if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, s.fn, s.threads, limit);
-                if (e != cudaSuccess) return cuda_fail(e, "scored decode attributes");
-                per_sm = std::min(per_sm, n);
-            }
-        if (per_sm < 1) return fail(PDA_ERR_UNSUPPORTED, "scored decode kernel does not fit on an SM");
-        // the partial states of a context are sized for its other kernels' grids
-        ctx->scored_ctas[k] = std::min(per_sm * ctx->num_sms, k == 0 ? ctx->split_ctas : ctx->quant_ctas[0]);
+        for (int f = 0; f < (k == 0 ? 2 : k == kQuantGrid ? 8 : 1); ++f) {
+            const ScoredForm form = {ctx->stage_rows, k < kQuantGrid ? PDA_CACHE_BF16 : f & 1 ? PDA_CACHE_INT8 : PDA_CACHE_E4M3,
+                                     k == 0             ? (f ? kMaxGroup : 1)
+                                     : k == kQuantGrid ? (f & 2 ? kMaxGroup : 1) : 16 * k,
+                                     (f & 4) != 0};
+            if (const pda_status st = setup(form, &per_sm); st != PDA_OK) return st;
+        }
+        ctx->scored_ctas[k] = std::min(per_sm * ctx->num_sms, most[k]);
     }
     if (const cudaError_t e = evict_setup(); e != cudaSuccess) return cuda_fail(e, "eviction kernel attributes");
     for (int format : {PDA_CACHE_BF16, PDA_CACHE_E4M3, PDA_CACHE_INT8}) {
@@ -280,7 +311,9 @@ PDA_EXPORT pda_status pda_decode_scored_scratch(const pda_ctx* ctx, int32_t batc
         return fail(PDA_ERR_INVALID_ARG, "batch %d x q_len %d outside [0, max_seqs=%d] or table width %d < 1", batch, q_len,
                     ctx->dims.max_seqs, max_blocks);
     const pda_status st = check_weights_width(ctx, max_blocks);
-    if (st == PDA_OK) *bytes = weights_scratch(ctx, batch, q_len, max_blocks).total;
+    if (st == PDA_OK)  // over caches of any format
+        *bytes = std::max(weights_scratch(ctx, true, batch, q_len, max_blocks).total,
+                          weights_scratch(ctx, false, batch, q_len, max_blocks).total);
     return st;
 }
 
@@ -299,7 +332,7 @@ PDA_EXPORT pda_status pda_decode_scored(pda_ctx* ctx, const pda_bf16* q, const p
         return fail(PDA_ERR_INVALID_ARG, "weights must be 4-byte aligned");
     if (batch == 0) return PDA_OK;
     if (weights_out && (st = check_weights_width(ctx, max_blocks)) != PDA_OK) return st;
-    const WeightsScratch ws = weights_scratch(ctx, batch, q_len, max_blocks);
+    const WeightsScratch ws = weights_scratch(ctx, cache->format == PDA_CACHE_BF16, batch, q_len, max_blocks);
     if (weights_out && (!scratch || !aligned(scratch, 16) || scratch_bytes < ws.total))
         return fail(PDA_ERR_INVALID_ARG, "weights need %lld bytes of 16-byte aligned scratch (got %lld)", (long long)ws.total,
                     (long long)scratch_bytes);

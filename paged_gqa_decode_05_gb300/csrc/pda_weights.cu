@@ -86,12 +86,16 @@ constexpr int kThreads = 256, kTok = 4, kChunk = kThreads * kTok;
 
 __host__ __device__ __forceinline__ int32_t chunks_of(int32_t n) { return (int32_t)(((uint32_t)n + kChunk - 1) / kChunk); }
 
-// kSR: rows_per_slot where it is 4 or 8 (a token's scores in one or two loads), 0: any.
-template <int kSR>
+// A launch row's q rows are taken kSub at a time.  kSR: kSub where rows_per_slot is
+// a multiple of 8 or of 4 (a token's scores in one or two loads), 0: any.  kOne:
+// a launch row is one step (with the steps' arithmetic for all, 2.8 M tokens of 8
+// q rows took 190.8 us for 183.6).
+template <int kSR, bool kOne>
 __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p) {
     __shared__ int32_t pfx[kMaxLaunchBatch + 1];  // chunks before each sequence, one kv head
     __shared__ int32_t sums[kThreads / 32];
-    __shared__ alignas(16) float2 ml[2][kMaxGroup];  // (-m, -log2 l) of a launch row's q rows
+    constexpr int kSub = kSR > 0 ? kSR : kMaxGroup;
+    __shared__ alignas(16) float2 ml[2][kSub];  // (-m, -log2 l) of the q rows
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // Launched behind the decode, which waited for all before it: lengths, tables and
     // the sums so far are there, so the plan and the first chunk's sums are read
@@ -126,7 +130,8 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p
     __syncthreads();
     const int64_t chunks = (int64_t)pfx[p.B] * p.Hkv;
     const int64_t T = (int64_t)p.table_stride << p.lbs;
-    const int Qr = (p.q_len + p.qp - 1) / p.qp, SR = kSR > 0 ? kSR : p.rows_per_slot, mask = (1 << p.lbs) - 1;
+    const int SR = kOne && kSR > 0 ? kSR : p.rows_per_slot, subs = kOne ? 1 : (SR + kSub - 1) / kSub, mask = (1 << p.lbs) - 1;
+    const int steps = (p.q_len + p.qp - 1) / p.qp * subs;  // a step: kSub rows, from sub_of on, of launch row step / subs
     bool waited = false;
     for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
         int lo = 0, hi = p.B - 1;  // the largest b with pfx[b] * Hkv <= c
@@ -148,13 +153,19 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p
             id[k] = t < len ? ids[t >> p.lbs] : -1;
             w[k] = 0.f;
         }
-        auto scores_of = [&](int r) { return p.scores + ((((int64_t)r * p.B + b) * p.Hkv + kvh) * T + t0) * SR; };
-        auto rows_of = [&](int r) { return min(p.qp, p.q_len - r * p.qp) * p.G; };
-        auto seen_of = [&](int r) { return min(len, raw - p.q_len + r * p.qp + rows_of(r) / p.G); };  // by the launch row's queries
+        auto sub_of = [&](int e) { return kOne ? 0 : e % subs * kSub; };
+        auto row_of = [&](int e) { return kOne ? e : e / subs; };
+        auto scores_of = [&](int e) {
+            return p.scores + ((((int64_t)row_of(e) * p.B + b) * p.Hkv + kvh) * T + t0) * SR + sub_of(e);
+        };
+        auto queries_of = [&](int r) { return min(p.qp, p.q_len - r * p.qp); };
+        auto rows_of = [&](int e) { return min(kSub, queries_of(row_of(e)) * p.G - sub_of(e)); };  // (may be none)
+        auto seen_of = [&](int e) { return min(len, raw - p.q_len + row_of(e) * p.qp + queries_of(row_of(e))); };  // by the launch row
         auto fetch = [&](int r) {
             if (tid < rows_of(r)) {
                 const float2 z = reinterpret_cast<const float2*>(
-                    p.row_ml)[((int64_t)b * p.q_len + r * p.qp + tid / p.G) * p.Hq + kvh * p.G + tid % p.G];
+                    p.row_ml)[((int64_t)b * p.q_len + row_of(r) * p.qp + (sub_of(r) + tid) / p.G) * p.Hq + kvh * p.G +
+                              (sub_of(r) + tid) % p.G];
                 // (a query that sees nothing has scores of -inf only: weights of 0)
                 ml[r & 1][tid] = z.y == 0.f ? make_float2(0.f, 0.f) : make_float2(-z.x, -lg2(z.y));
             }
@@ -165,7 +176,7 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p
                 for (int k = 0; k < kTok; ++k)
                     if (t0 + k * kThreads < seen) {
 #pragma unroll
-                        for (int i = 0; i < kSR / 4; ++i) v[k][i] = __ldcs(reinterpret_cast<const float4*>(s + k * kThreads * kSR) + i);
+                        for (int i = 0; i < kSR / 4; ++i) v[k][i] = __ldcs(reinterpret_cast<const float4*>(s + (int64_t)k * kThreads * SR) + i);
                     }
             }
         };
@@ -185,7 +196,7 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p
             waited = true;
             fetch(0);
         }
-        for (int r = 0; r < Qr; ++r) {
+        for (int r = 0; r < steps; ++r) {
             if (r > 0) fetch(r);
             const int rows = rows_of(r), seen = seen_of(r);
             __syncthreads();  // (the other half of ml is read until the next row's barrier)
@@ -229,7 +240,7 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p
 #pragma unroll
         for (int k = 0; k < kTok; ++k)
             if (at[k] >= 0) p.out[at[k]] = old[k] + w[k];
-        if (Qr & 1) __syncthreads();  // the next chunk's first row takes the half that the last one reads
+        if (steps & 1) __syncthreads();  // the next chunk's first row takes the half that the last one reads
     }
     if (!waited) {
         pdl_wait_primary();
@@ -243,7 +254,13 @@ cudaError_t launch_weights(const WeightsParams& p, int sms, cudaStream_t stream)
     cudaLaunchAttribute attr;
     const int64_t most = (int64_t)p.B * p.Hkv * chunks_of((int32_t)((int64_t)p.table_stride << p.lbs));
     const cudaLaunchConfig_t cfg = pdl_config((int)(most < sms * 8 ? most : sms * 8), kThreads, stream, &attr);
-    return cudaLaunchKernelEx(&cfg, p.rows_per_slot == 8 ? weights_kernel<8> : p.rows_per_slot == 4 ? weights_kernel<4> : weights_kernel<0>, p);
+    const int SR = p.rows_per_slot;
+    const auto kernel = SR == 8       ? weights_kernel<8, true>
+                        : SR == 4     ? weights_kernel<4, true>
+                        : SR < 8      ? weights_kernel<0, true>
+                        : SR % 8 == 0 ? weights_kernel<8, false>
+                        : SR % 4 == 0 ? weights_kernel<4, false> : weights_kernel<0, false>;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 // ---- joining a shared prefix

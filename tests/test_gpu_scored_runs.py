@@ -194,7 +194,7 @@ def test_timing_events_stand_around_each_decode():
 # ------------------------------------------------------------------ several launches
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.int8])
-@pytest.mark.parametrize("B,n,G", [(1500, 1, 2), (150, 20, 4), (90, 37, 5)])
+@pytest.mark.parametrize("B,n,G", [(1500, 1, 2), (150, 20, 4), (90, 37, 5), (600, 2, 8), (1100, 3, 8)])
 def test_batches_of_several_launches(dtype, B, n, G):
     hkv, d, bs = 2, 64, 16
     hq = G * hkv
