@@ -163,9 +163,9 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p
         auto seen_of = [&](int e) { return min(len, raw - p.q_len + row_of(e) * p.qp + queries_of(row_of(e))); };  // by the launch row
         auto fetch = [&](int r) {
             if (tid < rows_of(r)) {
-                const float2 z = reinterpret_cast<const float2*>(
-                    p.row_ml)[((int64_t)b * p.q_len + row_of(r) * p.qp + (sub_of(r) + tid) / p.G) * p.Hq + kvh * p.G +
-                              (sub_of(r) + tid) % p.G];
+                const float2 z = __ldcg(reinterpret_cast<const float2*>(p.row_ml) +
+                                        ((int64_t)b * p.q_len + row_of(r) * p.qp + (sub_of(r) + tid) / p.G) * p.Hq +
+                                        kvh * p.G + (sub_of(r) + tid) % p.G);
                 // (a query that sees nothing has scores of -inf only: weights of 0)
                 ml[r & 1][tid] = z.y == 0.f ? make_float2(0.f, 0.f) : make_float2(-z.x, -lg2(z.y));
             }
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p
 #pragma unroll
         for (int k = 0; k < kTok; ++k) {
             at[k] = id[k] >= 0 && id[k] < p.num_blocks ? (((int64_t)id[k] * p.Hkv + kvh) << p.lbs) + ((t0 + k * kThreads) & mask) : -1;
-            old[k] = at[k] >= 0 && p.in && t0 + k * kThreads < raw - p.q_len ? p.in[at[k]] : 0.f;
+            old[k] = at[k] >= 0 && p.in && t0 + k * kThreads < raw - p.q_len ? __ldcg(p.in + at[k]) : 0.f;
         }
         if (first) {
             pdl_wait_primary();
@@ -300,12 +300,14 @@ __global__ void __launch_bounds__(THREADS) join_kernel(const JoinParams p) {
     const int c = threadIdx.x % kC, part = kJ > 1 ? threadIdx.x / kC : 0;
     if (kJ == 1 && row >= p.rows) return;
     const int per = p.q_len * p.Hq, b = (int)(row / per), in = (int)(row - (int64_t)b * per), qi = in / p.Hq, head = in - qi * p.Hq;
-    const PrefixSeq s = p.seqs[b];
+    // (from L2 all: the CTA may have come to its SM before they were written)
+    const int4 lo = __ldcg(reinterpret_cast<const int4*>(p.seqs + b)), hi = __ldcg(reinterpret_cast<const int4*>(p.seqs + b) + 1);
+    const PrefixSeq s = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
     float M = __int_as_float(0xff800000), L = 0.f;
     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
     if (part == 0) {
-        const float2 own = reinterpret_cast<const float2*>(p.row_ml)[row];
-        O = reinterpret_cast<const float4*>(p.row_o)[row * kC + c];
+        const float2 own = __ldcg(reinterpret_cast<const float2*>(p.row_ml) + row);
+        O = __ldcg(reinterpret_cast<const float4*>(p.row_o) + row * kC + c);
         M = own.x;
         L = own.y;
     }
@@ -328,8 +330,8 @@ __global__ void __launch_bounds__(THREADS) join_kernel(const JoinParams p) {
                 si[k] = make_float2(__int_as_float(0xff800000), 0.f);
                 oi[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (k0 + k * kJ < n) {
-                    si[k] = ml[(int64_t)(k0 + k * kJ) * kSub * 128];
-                    oi[k] = po[(int64_t)(k0 + k * kJ) * kSub * 128 * kC];
+                    si[k] = __ldcg(ml + (int64_t)(k0 + k * kJ) * kSub * 128);
+                    oi[k] = __ldcg(po + (int64_t)(k0 + k * kJ) * kSub * 128 * kC);
                 }
             }
 #pragma unroll
