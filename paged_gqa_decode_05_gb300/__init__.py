@@ -26,6 +26,14 @@ A layer's step over a cache in 8 bits (one scale per token and kv head)::
     q = ctx.append(k, v, k_pool, v_pool, block_table, seq_lens, scales=scales, q=q,
                    q_weight=wq, k_weight=wk, cos_sin=pda.rope_table(max_len, 128))
     out = ctx.decode(q, k_pool, v_pool, block_table, seq_lens, scales=scales)
+
+Long contexts: capped or biased scores, the attention weight of every cached token, a cache cut
+down by it, and batches whose sequences begin with the same blocks::
+
+    weights = ctx.new_weights(num_blocks)
+    out = ctx.decode_scored(q, k_pool, v_pool, block_table, seq_lens, softcap=50.0, weights=weights)
+    seq_lens, kept = ctx.evict(k_pool, v_pool, weights, block_table, seq_lens, 2048, first=4, recent=256)
+    out = ctx.decode_shared(q, k_pool, v_pool, block_table, seq_lens, shared_blocks)
 """
 from __future__ import annotations
 

@@ -80,9 +80,11 @@ cudaLaunchConfig_t pdl_config(int grid, int threads, cudaStream_t stream, cudaLa
 }
 
 // A CTA takes chunks of kThreads * kTok tokens of a (sequence, kv head), kTok a
-// thread with their loads together.  With 1, 2, 3, 4 a thread the whole decode of
-// 32 sequences of 4096 tokens takes 105, 99.3, 100, 99.0 us.
-constexpr int kThreads = 256, kTok = 4, kChunk = kThreads * kTok;
+// thread with their loads together, kCtas a SM.  Whole decodes of 32 sequences of
+// 4096 tokens, and of 64 of 128 to 32768 with 8 q rows: 128 threads 97.7 and 176.4
+// us, 256 101.1 and 180.8; (another board) 5, 8 and 16 CTAs a SM 97.0, 99.4, 101.5 and
+// 192, 184, 187; 3 tokens a thread 99.5 and 187, 6 101.1 and 185.5.
+constexpr int kCtas = 8, kThreads = 128, kTok = 4, kChunk = kThreads * kTok;
 
 __host__ __device__ __forceinline__ int32_t chunks_of(int32_t n) { return (int32_t)(((uint32_t)n + kChunk - 1) / kChunk); }
 
@@ -253,7 +255,7 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p
 cudaError_t launch_weights(const WeightsParams& p, int sms, cudaStream_t stream) {
     cudaLaunchAttribute attr;
     const int64_t most = (int64_t)p.B * p.Hkv * chunks_of((int32_t)((int64_t)p.table_stride << p.lbs));
-    const cudaLaunchConfig_t cfg = pdl_config((int)(most < sms * 8 ? most : sms * 8), kThreads, stream, &attr);
+    const cudaLaunchConfig_t cfg = pdl_config((int)(most < sms * kCtas ? most : sms * kCtas), kThreads, stream, &attr);
     const int SR = p.rows_per_slot;
     const auto kernel = SR == 8       ? weights_kernel<8, true>
                         : SR == 4     ? weights_kernel<4, true>
