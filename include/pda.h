@@ -686,7 +686,8 @@ typedef struct pda_scoring {
  *             of no token of the batch are left as they were.
  *   scratch   16-byte aligned, pda_decode_scored_scratch() bytes for the call's
  *             batch, q_len and max_blocks: the scores, 4 bytes for each token
- *             and q head of a table of that width.  Not needed without weights.
+ *             and q head of a table of that width.  Not needed without weights;
+ *             no two calls that may run at the same time share it.
  * No two sequences of the call may share a block whose weights they sum.
  * Every sum is taken in one order: a call's weights do not vary from run to run.
  * batch * q_len <= max_seqs.  Other arguments as pda_decode_cache; scores are as
@@ -716,7 +717,8 @@ pda_status pda_decode_scored(pda_ctx* ctx, const pda_bf16* q, const pda_cache* c
  *                  [0, max_blocks], raise PDA_DEVERR_BAD_LENGTH, and the call takes
  *                  nothing as shared.
  *   groups         1 .. 1024.
- *   scratch        16-byte aligned, pda_decode_shared_scratch() bytes.
+ *   scratch        16-byte aligned, pda_decode_shared_scratch() bytes; no two calls
+ *                  that may run at the same time share it.
  * A sequence may end inside the prefix, or be empty: one whose first query does
  * not see all of the prefix is decoded alone.  V scales of an 8-bit prefix enter
  * the weights in fp32 times 2^-40; what falls below 2^-126 then, values below
