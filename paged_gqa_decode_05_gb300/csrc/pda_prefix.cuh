@@ -20,9 +20,9 @@
 // A stream's next S is there when it has written a P.  Head size 256, whose O
 // takes half the tensor memory, runs one stream.
 //
-// K and V go through one ring of slots, in the order in which the products use
-// them (K runs `ahead` tiles before V), so that every slot but those in use is
-// one on its way.  Four loader warps, two for K and two for V, fill 32 rows of a
+// K and V go through rings of slots (PrefixRing), in the order in which the
+// products use them (K runs two tiles before V), so that every slot but those in
+// use is one on its way.  Four loader warps, two for K and two for V, fill 32 rows of a
 // slot each, with TMA boxes of up to 32 rows and one 64-column slab, or, for
 // block sizes below 8, row by row with 16-byte cp.async in the same swizzle.
 // (Row by row for all, a call over 32768 tokens of 8 kv heads of 128 took 101 us
@@ -65,7 +65,7 @@ struct PrefixCfg {
     static constexpr int kQTileBytes = 128 * D * 2;
     static constexpr int kSlots = D == 64 ? 20 : D == 256 ? (FMT == kBf16 ? 5 : 4) : FMT == kBf16 ? 10 : 9;
     // ring of scales, [K | V][kT] a tile: from when K's slot is filled until the
-    // softmax, `ahead` + kSlots / 2 tiles at most
+    // softmax, 4 + kSlots / 2 tiles at most
     static constexpr int kRing = 16, kScaleTiles = FMT == kBf16 ? 0 : kRing;
     static constexpr int kRW = kT / 2;                   // rows of a loader warp
     // tensor memory: two S of a stream, then its O
@@ -83,9 +83,6 @@ struct PrefixCfg {
                               kO = kPV + 16, kQ = kO + 8, kSync = kQ + 8, kFin = kSync + 8, kTm = kFin + 8, kEnd = kTm + 16;
     static constexpr uint32_t kSmem = kEnd + (1024 - 16);  // (dynamic shared memory starts on 16 bytes)
     static_assert(kSmem + (kPlanHere + 1) * sizeof(PrefixGroup) + 16 <= 232448, "shared memory of an SM");
-    // tiles that K runs ahead of V: a stream's two S
-    static __device__ __forceinline__ int ahead(bool dual) { return dual || kStreams == 1 ? 2 : 4; }
-    static_assert(kSlots >= 4 + 1 || kStreams == 1, "the ring holds what the products need at once");
 };
 
 // One run of a CTA over token tiles of a unit.
@@ -112,6 +109,49 @@ __device__ __forceinline__ int64_t prefix_ctas(int64_t W, int64_t units) {
     const int64_t P = min(min(W, (int64_t)gridDim.x), max(best, (int64_t)1));
     return units < P ? P / units * units : P;
 }
+
+// The ring of slots.  Two q tiles, or one stream: both streams use every slot, all
+// slots in a ring.  One q tile for two streams: a stream's tiles have half of the
+// slots for a ring of their own.  So whoever waits for a slot's phase has seen the
+// phase before it, without which a parity does not say which phase it is (with one
+// ring for alternate tiles a stream that ran ahead took a slot that was still to be
+// filled for the other one).  Uses of a ring are numbered in the order in which the
+// products take them: K of tiles 0 and 1, then V of tile i and K of tile i + 2 in
+// turn, then the last V.  A loader that fills every second use or so of a ring knows
+// from the last one it filled that the phase before the one it waits for is over; at a
+// segment's start, where rings begin anew and may change, it waits for all products of
+// the segment before, and the streams do by their q rows.
+template <int SLOTS, bool TWO>
+struct PrefixRing {
+    uint32_t parity = 0;  // of every slot's uses in the segments before
+    static __device__ __forceinline__ int k_use(int i) { return i + max(0, i - 1); }
+    static __device__ __forceinline__ int v_use(int i, int items) { return i + min(i + 2, items); }
+    // The slot of a use, and the parity of its phase.
+    __device__ __forceinline__ uint32_t slot(bool shared, int st, int use, uint32_t& phase) const {
+        uint32_t at = (uint32_t)use % SLOTS, round = (uint32_t)use / SLOTS;
+        if (TWO && !shared) {
+            at = (uint32_t)use % (SLOTS / 2) + st * (SLOTS / 2);
+            round = (uint32_t)use / (SLOTS / 2);
+        }
+        phase = ((parity >> at) ^ round) & 1u;
+        return at;
+    }
+    // Past a segment of n tiles.
+    __device__ __forceinline__ void next(bool shared, int n) {
+#pragma unroll 1
+        for (int at = 0; at < SLOTS; ++at) {
+            int uses = 2 * n, size = SLOTS, i = at;
+            if (TWO && !shared) {
+                size = SLOTS / 2;
+                if (at >= 2 * size) break;
+                const int st = at >= size;
+                i = at - st * size;
+                uses = (n - st + 1) / 2 * 2;
+            }
+            if (uses > i) parity ^= (uint32_t)(((uses - i + size - 1) / size) & 1) << at;
+        }
+    }
+};
 
 template <int D, int FMT>
 struct PrefixWalk {
@@ -290,21 +330,22 @@ __device__ __forceinline__ void prefix_load(const PrefixParams& p, const PrefixG
         *abort_flag = 1;
         return false;
     };
-    // A segment's slots, from number `first` on, are in the order in which the
-    // products use them: K of tiles 0 .. ahead - 1, then V of tile i and K of
-    // tile i + ahead in turn while there are any, then the other V.  K of tile i
-    // comes after i of K and i - ahead + 1 of V; V of tile i after i of V and
-    // i + ahead of K, as many as there are.
-    uint32_t first = 0, tiles = 0;  // slots of the segments before; tiles whose K is filled
-    uint32_t issued = 0, spread = 0, queue = 0;  // (8-bit) slots filled, converted; lane l & 31: the l-th one's number
+    PrefixRing<C::kSlots, C::kStreams == 2> ring;
+    uint32_t tiles = 0, segs = 0;   // tiles that are filled; segments before
+    uint32_t issued = 0, spread = 0, queue = 0;  // (8-bit) slots filled, converted; lane l & 31: the l-th one's 2 slot + phase
     int i = 0;                      // tile of the segment
     bool ok = true;
     while (ok && (more || spread != issued)) {
-        const int ahead = C::ahead(s.dual);
-        const uint32_t n = first + (k ? i + max(0, i - ahead + 1) : i + min(i + ahead, s.n));
-        const uint32_t at = n % C::kSlots, slot = base + C::kSlot0 + at * C::kSlotBytes;
-        const uint32_t empty = base + C::kEmpty + 8 * at, parity = ((n / C::kSlots) & 1u) ^ 1u;
+        const bool shared = s.dual || C::kStreams == 1;  // by both streams
+        const int st = shared ? 0 : i & 1, own = shared ? i : i >> 1, items = shared ? s.n : (s.n - st + 1) / 2;
+        uint32_t phase;
+        const uint32_t at = ring.slot(shared, st, k ? ring.k_use(own) : ring.v_use(own, items), phase);
+        const uint32_t slot = base + C::kSlot0 + at * C::kSlotBytes, empty = base + C::kEmpty + 8 * at, parity = phase ^ 1u;
         bool can = more;
+        if (can && i == 0 && segs > 0) {  // a segment's first, once every product of the one before is done
+            if (FMT != kBf16 && spread != issued) can = __all_sync(0xffffffffu, mbar_test_wait(base + C::kO, (segs - 1) & 1u));
+            else if (!(ok = wait(base + C::kO, (segs - 1) & 1u))) break;
+        }
         if (FMT != kBf16 && can && spread != issued) can = __all_sync(0xffffffffu, mbar_test_wait(empty, parity));
         if (can) {
             if (!(ok = wait(empty, parity))) break;
@@ -370,21 +411,22 @@ __device__ __forceinline__ void prefix_load(const PrefixParams& p, const PrefixG
             }
             ++tiles;
             filled |= 1u << at;
-            parities = (parities & ~(1u << at)) | ((n / C::kSlots) & 1u) << at;
+            parities = (parities & ~(1u << at)) | phase << at;
             if constexpr (FMT != kBf16) {
-                if (lane == (int)(issued & 31u)) queue = n;
+                if (lane == (int)(issued & 31u)) queue = 2 * at + phase;
                 ++issued;
             }
             if (++i == s.n) {
-                first += 2 * s.n;
+                if (more2) ring.next(shared, s.n);
+                ++segs;
                 i = 0;
                 s = s2;
                 more = more2;
                 more2 = more && walk.next(p, groups, s2);
             }
         } else if constexpr (FMT != kBf16) {
-            const uint32_t m = __shfl_sync(0xffffffffu, queue, spread & 31u), c = m % C::kSlots;
-            if (!(ok = wait(base + C::kLanded + 8 * (2 * c + half), (m / C::kSlots) & 1u))) break;
+            const uint32_t m = __shfl_sync(0xffffffffu, queue, spread & 31u), c = m >> 1;
+            if (!(ok = wait(base + C::kLanded + 8 * (2 * c + half), m & 1u))) break;
             if (k) {  // K's scales times what every score is multiplied by
                 float* ks = reinterpret_cast<float*>(smem + C::kScale0) + spread % C::kRing * (2 * C::kT) + row0 + lane;
                 *ks *= p.score_mult;
@@ -409,7 +451,10 @@ __device__ __forceinline__ void prefix_mma(const PrefixParams& p, const PrefixGr
     constexpr uint32_t idS = umma_idesc_bf16(128, C::kT, false), idO = umma_idesc_bf16(128, D, true);
     PrefixWalk<D, FMT> walk(p, groups);
     PrefixSegment s;
-    uint32_t first = 0, segs = 0;   // slots of the segments before, segments
+    PrefixRing<C::kSlots, C::kStreams == 2> ring;
+    uint32_t segs = 0;
+    bool every_before = false;
+    int n_before = 0;
     uint32_t sn = 0, pn = 0;        // S and P V issued
     const bool one = elect_one();
     const uint32_t tS0 = tmem + st * 2 * C::kT, tO = tmem + C::kTmO + st * D;
@@ -424,7 +469,8 @@ __device__ __forceinline__ void prefix_mma(const PrefixParams& p, const PrefixGr
     while (ok && walk.next(p, groups, s)) {
         // item k of this stream: tile k (two q tiles, or one stream) or every other one
         const bool every = s.dual || C::kStreams == 1;
-        const int ahead = C::ahead(s.dual), items = every ? s.n : (s.n - st + 1) / 2;
+        const int items = every ? s.n : (s.n - st + 1) / 2;
+        if (segs > 0) ring.next(every_before, n_before);
         const uint64_t q = umma_sdesc(base + (s.dual ? st : 0) * C::kQTileBytes, 16, 1024);
         if (!wait(base + C::kQ, segs & 1u)) break;
         ++segs;
@@ -432,9 +478,9 @@ __device__ __forceinline__ void prefix_mma(const PrefixParams& p, const PrefixGr
 #pragma unroll 1
         for (int k = -2; ok && k < items; ++k) {
             if (k >= 0) {
-                const int t = every ? k : 2 * k + st;
-                const uint32_t n = first + t + min(t + ahead, s.n), slot = n % C::kSlots, buf = pn & 1u;
-                if (!wait(base + C::kFull + 8 * slot, (n / C::kSlots) & 1u)) break;
+                uint32_t phase;
+                const uint32_t slot = ring.slot(every, st, ring.v_use(k, items), phase), buf = pn & 1u;
+                if (!wait(base + C::kFull + 8 * slot, phase)) break;
                 if (!wait(kP + 8 * buf, (pn >> 1) & 1u)) break;
                 fence_proxy_async_smem();  // cp.async writes of the loaders, and of the q rows
                 tc_fence_after();
@@ -457,9 +503,9 @@ __device__ __forceinline__ void prefix_mma(const PrefixParams& p, const PrefixGr
             }
             const int i = k + 2;
             if (i < items) {
-                const int t = every ? i : 2 * i + st;
-                const uint32_t n = first + t + max(0, t - ahead + 1), slot = n % C::kSlots, buf = sn & 1u;
-                if (!wait(base + C::kFull + 8 * slot, (n / C::kSlots) & 1u)) break;
+                uint32_t phase;
+                const uint32_t slot = ring.slot(every, st, ring.k_use(i), phase), buf = sn & 1u;
+                if (!wait(base + C::kFull + 8 * slot, phase)) break;
                 fence_proxy_async_smem();
                 tc_fence_after();
                 const uint32_t tS = tS0 + buf * C::kT;
@@ -478,7 +524,8 @@ __device__ __forceinline__ void prefix_mma(const PrefixParams& p, const PrefixGr
             }
         }
         if (one && ok && items == 0) mbar_arrive(base + C::kO);
-        first += 2 * s.n;
+        every_before = every;
+        n_before = s.n;
     }
     // every product has completed before the tensor memory is freed
     if (one) umma_commit(base + C::kFin);
@@ -651,8 +698,10 @@ __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, const Pref
                 if (!bare) tmem_wait_st();
                 // lazy reference (kLazyLog2); O is scaled once this stream's last product with V is done
                 const bool up = top > m + kLazyLog2, scale_o = up && m != kNegInf;
+                // (waited for every time, long over as a rule: a parity tells a phase from the one
+                // before only to who has seen that)
+                if (done > 0 && !wait(base + C::kPV + 8 * st, (done - 1u) & 1u)) return;
                 if (__any_sync(0xffffffffu, scale_o)) {
-                    if (!wait(base + C::kPV + 8 * st, (done - 1u) & 1u)) return;
                     tc_fence_after();
                     const float a = scale_o ? ex2(m - top) : 1.f;
                     l *= a;

@@ -314,3 +314,35 @@ def test_a_context_serves_several_shapes():
                     assert all(torch.equal(a, b) for a, b in zip(out, seen[dtype, k]))
                 seen[dtype, k] = out
     assert ctx.read_device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float8_e4m3fn])
+def test_a_long_prefix_again_and_again(dtype):
+    """One q tile for both of the prefix kernel's streams, over caches that do not fit L2 together: thousands of calls, all
+    alike (a copy that lands late must not be taken for one that has)."""
+    hq, hkv, d, bs = 32, 8, 128, 16
+    own, prefix = [17, 40, 5, 100], 1024  # blocks
+    runs = []
+    for seed in range(2):
+        table, lens, pool = ref.shared_table(np.random.default_rng(seed), own, bs, [0, 4], [prefix])
+        ctx = ctx_of(hq, hkv, d, bs)
+        g = torch.Generator("cuda").manual_seed(seed)
+        kp, vp, sc = ctx.new_cache(pool, dtype)
+        for x in (kp, vp):
+            x.copy_(torch.randn(x.shape, generator=g, device="cuda"))
+        if sc is not None:
+            sc.copy_(torch.rand(sc.shape, generator=g, device="cuda") + 0.5)
+        q = torch.randn((4, hq, d), generator=g, device="cuda").bfloat16()
+        out = torch.empty_like(q)
+        runs.append((ctx, ctx.bind_decode_shared(q, kp, vp, table.cuda(), i32(lens), i32([prefix]), out, scales=sc), out,
+                     ctx.decode_scored(q, kp, vp, table.cuda(), i32(lens), scales=sc)))
+    first = [call().clone() for _, call, _, _ in runs]
+    for (_, _, _, alone), x in zip(runs, first):
+        assert torch.isfinite(x).all() and (x.float() - alone.float()).abs().max() < 0.05
+    for _ in range(20):
+        for _ in range(150):
+            for _, call, _, _ in runs:
+                call()
+        for (ctx, _, out, _), x in zip(runs, first):
+            assert torch.equal(out, x)
+    assert all(ctx.read_device_errors() == 0 for ctx, _, _, _ in runs)
