@@ -346,3 +346,33 @@ def test_a_long_prefix_again_and_again(dtype):
         for (ctx, _, out, _), x in zip(runs, first):
             assert torch.equal(out, x)
     assert all(ctx.read_device_errors() == 0 for ctx, _, _, _ in runs)
+
+
+def test_calls_at_once():
+    """Three contexts on three streams at once, each with scratch of its own: the outputs of each alone."""
+    hq, hkv, d, bs = 16, 4, 128, 16
+    own = [30, 200, 7, 90, 64, 11]
+    jobs = []
+    for i, dtype in enumerate((torch.bfloat16, torch.float8_e4m3fn, torch.bfloat16)):
+        table, lens, pool = ref.shared_table(np.random.default_rng(i), own, bs, [0, 6], [200])
+        ctx = ctx_of(hq, hkv, d, bs)
+        kp, vp, sc = up(*ref.random_cache(gen(i), pool, bs, hkv, d, dtype))
+        q = torch.randn((6, hq, d), generator=gen(i)).bfloat16().cuda()
+        t, ln, out = table.cuda(), i32(lens), torch.empty_like(q)
+        stream = torch.cuda.Stream()
+        if i < 2:
+            args, bind = (q, kp, vp, t, ln, i32([200]), out), ctx.bind_decode_shared
+        else:
+            args, bind = (q, kp, vp, t, ln, out), ctx.bind_decode_scored
+        alone = bind(*args, scales=sc, softcap=20.0)().clone()
+        torch.cuda.synchronize()
+        jobs.append((ctx, bind(*args, scales=sc, softcap=20.0, stream=stream), out, alone))
+    for _ in range(10):
+        for _ in range(50):
+            for _, call, _, _ in jobs:
+                call()
+        torch.cuda.synchronize()
+        for ctx, _, out, alone in jobs:
+            assert torch.equal(out, alone) and ctx.read_device_errors() == 0
+            out.zero_()
+        torch.cuda.synchronize()
