@@ -782,6 +782,11 @@ __device__ __forceinline__ void merge_state(float& M, float& Ls, float4& Os, flo
 
 // ---- the scored modes: scores capped and biased, written out; states handed on
 
+// The reference that a state of sum l leaves with.  Maxima drop NaN, so a row all
+// of whose scores are NaN has an empty state's reference; at 0 its NaN sum counts
+// wherever states are combined.
+__device__ __forceinline__ float seen_reference(float m, float l) { return l == l ? m : 0.f; }
+
 // cap * tanh(s / cap), s in base-2 units, from the definition, 1 - 2 / (1 + e)
 // with e = exp(2 s / cap): off by a few 2^-24 of the cap for any s, where the
 // hardware's tanh is off by 2^-11 of it (0.02 in the exponent at a cap of 50).
@@ -1085,8 +1090,8 @@ __device__ __forceinline__ void run_consumer(const SplitParams& p, uint32_t base
             const int h0 = 2 * t, h1 = 2 * t + 1;
             const int NR = MQ ? m.nr : G;  // q rows of the unit
             if (g == 0) {
-                if (h0 < NR) { st_m[warp * kMaxGroup + h0] = m0; st_l[warp * kMaxGroup + h0] = l0; }
-                if (h1 < NR) { st_m[warp * kMaxGroup + h1] = m1; st_l[warp * kMaxGroup + h1] = l1; }
+                if (h0 < NR) { st_m[warp * kMaxGroup + h0] = kExt ? seen_reference(m0, l0) : m0; st_l[warp * kMaxGroup + h0] = l0; }
+                if (h1 < NR) { st_m[warp * kMaxGroup + h1] = kExt ? seen_reference(m1, l1) : m1; st_l[warp * kMaxGroup + h1] = l1; }
             }
 #pragma unroll
             for (int mt = 0; mt < KS; ++mt) {
@@ -1214,7 +1219,7 @@ __device__ __forceinline__ void run_consumer(const SplitParams& p, uint32_t base
                         p.l_state[row] = Lo;
                     }
                 } else {
-                    // (the scored modes hand a NaN sum on, as the 8-bit kernels do)
+                    // (the scored modes hand a NaN sum on, as the 8-bit kernels do, see seen_reference)
                     const float4 v = (kExt ? Ls != 0.f : Ls > 0.f) ? make_float4(Os.x / Ls, Os.y / Ls, Os.z / Ls, Os.w / Ls)
                                               : make_float4(0.f, 0.f, 0.f, 0.f);
                     const int64_t o = MQ ? qo_offset<MQ>(p, ri.b, ri.first + h / G, m.kvh * G + h % G, D) + d4
@@ -1673,8 +1678,8 @@ __device__ __forceinline__ void run_consumer_rows(const SplitParams& p, uint32_t
                 if (tile > 0 && !consumer_sync(cbar, cphase, p.err, abort_flag)) { stop = true; break; }
                 if (qt == tile) {
                     if (t == 0) {
-                        st_m[ts * kMaxRowsPerWalk + row0] = m0;
-                        st_m[ts * kMaxRowsPerWalk + row1] = m1;
+                        st_m[ts * kMaxRowsPerWalk + row0] = kExt ? seen_reference(m0, l0) : m0;
+                        st_m[ts * kMaxRowsPerWalk + row1] = kExt ? seen_reference(m1, l1) : m1;
                         st_l[ts * kMaxRowsPerWalk + row0] = l0;
                         st_l[ts * kMaxRowsPerWalk + row1] = l1;
                     }

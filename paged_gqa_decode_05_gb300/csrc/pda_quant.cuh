@@ -732,7 +732,7 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
                 if (h >= me.nr) continue;
                 if (g == 0) {
                     // a NaN sum must not hide behind an empty reference
-                    st_m[rw * 16 + h] = l[c] == l[c] ? m[c] : 0.f;
+                    st_m[rw * 16 + h] = seen_reference(m[c], l[c]);
                     st_l[rw * 16 + h] = l[c] * (1.f / (1 << (int)kSumBias));
                 }
                 float* r = st_o + (size_t)(warp * 8 + hr) * kOStride + 2 * g;

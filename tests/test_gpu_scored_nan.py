@@ -1,0 +1,78 @@
+"""NaN in scored decode, in sums of attention weights and behind a shared prefix: a query that is NaN, or that sees NaN
+keys only, gets NaN, and nobody else notices.  What is not NaN is equal to the bit to the same call without NaN: rows of
+q, and tokens of a sum, are computed apart."""
+import numpy as np
+import pytest
+import torch
+
+import scored_ref as ref
+from test_gpu_scored import ctx_of, formats, gen, inputs, up
+
+pytestmark = pytest.mark.gpu
+NAN = float("nan")
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32).cuda()
+
+
+FORMS = [  # hq, hkv, d, bs, q_len, lens: walks of one query, of 8, 16 and 32 rows, of several launch rows; units in pieces
+    (4, 2, 64, 16, 1, [3000, 37, 1]),
+    (8, 1, 128, 16, 1, [5000]),
+    (8, 2, 128, 16, 2, [2500, 40]),
+    (8, 2, 128, 16, 3, [1500, 50]),
+    (40, 8, 64, 16, 4, [2100, 30]),
+    (8, 2, 256, 8, 2, [900, 45]),
+    (3, 1, 128, 2, 7, [1200, 9]),
+    (8, 2, 64, 16, 11, [700, 20]),
+]
+forms = pytest.mark.parametrize("hq,hkv,d,bs,n,lens", FORMS)
+
+
+def poison_keys(cache, table, b, tokens, bs, head):
+    """NaN keys of one sequence and kv head: values in bf16, scales in 8 bits."""
+    for t in tokens:
+        block, slot = int(table[b, t // bs]), t % bs
+        if cache[2] is None:
+            cache[0][block, slot, head] = NAN
+        else:
+            cache[2][block, head, 0, slot] = NAN
+
+
+@formats
+@forms
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+def test_a_nan_query_gives_nan(dtype, hq, hkv, d, bs, n, lens, softcap):
+    _, table, pool, cache, q, slopes = inputs(d + n, dtype, hq, hkv, d, bs, lens, n)
+    ctx = ctx_of(hq, hkv, d, bs)
+    kp, vp, sc, t, sl = up(*cache, table, slopes)
+    kw = dict(softcap=softcap, alibi_slopes=sl if softcap else None, scales=sc)
+    for out_dtype in (torch.bfloat16, torch.float32):
+        clean = ctx.decode_scored(q.cuda(), kp, vp, t, i32(lens), out_dtype=out_dtype, **kw)
+        for b in range(len(lens)):
+            bad, i, h = q.clone(), n // 2, hq - 1
+            bad[b, i, h, 5] = NAN
+            out = ctx.decode_scored(bad.cuda(), kp, vp, t, i32(lens), out_dtype=out_dtype, **kw)
+            rest = torch.ones(q.shape[:3], dtype=torch.bool)
+            rest[b, i, h] = lens[b] - n + i < 0  # (a query in front of the sequence sees nothing)
+            assert torch.isnan(out[~rest.cuda()]).all()
+            assert torch.equal(out[rest.cuda()], clean[rest.cuda()])
+    assert ctx.read_device_errors() == 0
+
+
+@formats
+@forms
+def test_nan_keys_of_a_whole_piece_give_nan(dtype, hq, hkv, d, bs, n, lens):
+    """The middle half of a sequence, one that several CTAs share, and all of it."""
+    _, table, pool, cache, q, _ = inputs(d + n, dtype, hq, hkv, d, bs, lens, n)
+    ctx = ctx_of(hq, hkv, d, bs)
+    G, L = hq // hkv, lens[0]
+    kp, vp, sc, t, qq = up(*cache, table, q)
+    clean = ctx.decode_scored(qq, kp, vp, t, i32(lens), scales=sc)
+    for tokens in (range(L // 4, 3 * L // 4), range(L)):
+        bad = [None if c is None else c.clone() for c in cache]
+        poison_keys(bad, table, 0, tokens, bs, hkv - 1)
+        kp, vp, sc = up(*bad)
+        out = ctx.decode_scored(qq, kp, vp, t, i32(lens), scales=sc)
+        assert torch.isnan(out[0, :, -G:]).all()
+        assert torch.equal(out[0, :, :-G], clean[0, :, :-G]) and torch.equal(out[1:], clean[1:])
