@@ -88,6 +88,12 @@ constexpr int kCtas = 8, kThreads = 128, kTok = 4, kChunk = kThreads * kTok;
 
 __host__ __device__ __forceinline__ int32_t chunks_of(int32_t n) { return (int32_t)(((uint32_t)n + kChunk - 1) / kChunk); }
 
+// A score's weight, z the (-m, -log2 l) of its row: 0 where the query does not see the
+// token, whatever that row's sum is.
+__device__ __forceinline__ float weight(float s, const float2& z) {
+    return s == __int_as_float(0xff800000) ? 0.f : ex2((s + z.x) + z.y);
+}
+
 // A launch row's q rows are taken kSub at a time.  kSR: kSub where rows_per_slot is
 // a multiple of 8 or of 4 (a token's scores in one or two loads), 0: any.  kOne:
 // a launch row is one step (with the steps' arithmetic for all, 2.8 M tokens of 8
@@ -222,7 +228,20 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p
                 }
 #pragma unroll
                 for (int k = 0; k < kTok; ++k)
-                    if (t0 + k * kThreads < seen) w[k] += sum[k].x + sum[k].y;
+                    if (t0 + k * kThreads < seen) {
+                        float x = sum[k].x + sum[k].y;
+                        if (x != x) {  // rare: -inf plus a NaN sum's logarithm is NaN (again in the same order)
+                            float even = 0.f, odd = 0.f;
+                            const float* s = scores_of(r) + (int64_t)k * kThreads * SR;
+#pragma unroll 1
+                            for (int i = 0; i < rows; i += 2) {
+                                even += weight(__ldcs(s + i), ml[r & 1][i]);
+                                if (i + 1 < rows) odd += weight(__ldcs(s + i + 1), ml[r & 1][i + 1]);
+                            }
+                            x = even + odd;
+                        }
+                        w[k] += x;
+                    }
             } else {
                 const float* s = scores_of(r);
                 float sum[kTok];
@@ -232,7 +251,7 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p
                     const float2 z = ml[r & 1][i];
 #pragma unroll
                     for (int k = 0; k < kTok; ++k)
-                        if (t0 + k * kThreads < seen) sum[k] += ex2((s[(int64_t)k * kThreads * SR + i] + z.x) + z.y);
+                        if (t0 + k * kThreads < seen) sum[k] += weight(s[(int64_t)k * kThreads * SR + i], z);
                 }
 #pragma unroll
                 for (int k = 0; k < kTok; ++k) w[k] += sum[k];

@@ -76,3 +76,28 @@ def test_nan_keys_of_a_whole_piece_give_nan(dtype, hq, hkv, d, bs, n, lens):
         out = ctx.decode_scored(qq, kp, vp, t, i32(lens), scales=sc)
         assert torch.isnan(out[0, :, -G:]).all()
         assert torch.equal(out[0, :, :-G], clean[0, :, :-G]) and torch.equal(out[1:], clean[1:])
+
+
+@formats
+@forms
+def test_a_nan_query_reaches_the_sums_of_what_it_sees_only(dtype, hq, hkv, d, bs, n, lens):
+    """The tokens behind it, which later queries of its launch row see, keep their sums."""
+    g, table, pool, cache, q, _ = inputs(d + n, dtype, hq, hkv, d, bs, lens, n)
+    ctx = ctx_of(hq, hkv, d, bs)
+    kp, vp, sc, t = up(*cache, table)
+    old = torch.rand((pool, hkv, bs), generator=g).cuda()
+    clean = old.clone()
+    ctx.decode_scored(q.cuda(), kp, vp, t, i32(lens), weights=clean, scales=sc)
+    assert torch.isfinite(clean).all()
+    for b, L in enumerate(lens):
+        for i in {0, n // 2, n - 1}:
+            bad, seen = q.clone(), max(0, L - n + i + 1)
+            bad[b, i, hq - 1, 5] = NAN
+            sums = old.clone()
+            ctx.decode_scored(bad.cuda(), kp, vp, t, i32(lens), weights=sums, scales=sc)
+            want = clean.clone()
+            at = torch.arange(seen)
+            want[table[b].long()[at // bs].cuda(), hkv - 1, (at % bs).cuda()] = NAN
+            assert torch.equal(torch.isnan(sums), torch.isnan(want))
+            assert torch.equal(sums.nan_to_num(-1.0), want.nan_to_num(-1.0))
+    assert ctx.read_device_errors() == 0
