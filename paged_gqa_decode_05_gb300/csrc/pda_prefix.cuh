@@ -748,6 +748,7 @@ __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, const Pref
         ++segs;
         tile0 += s.n;
         tc_fence_after();
+        m = seen_reference(m, l);
         const bool joined = C::kStreams == 2 && !s.dual;
         float f0 = 1.f, f1 = 0.f;
         bool two = false;

@@ -101,3 +101,60 @@ def test_a_nan_query_reaches_the_sums_of_what_it_sees_only(dtype, hq, hkv, d, bs
             assert torch.equal(torch.isnan(sums), torch.isnan(want))
             assert torch.equal(sums.nan_to_num(-1.0), want.nan_to_num(-1.0))
     assert ctx.read_device_errors() == 0
+
+
+SHARED = [  # hq, hkv, d, bs, q_len, shared blocks, own tokens: pieces on many CTAs and on one, one stream and two
+    (8, 2, 128, 16, 1, 200, [0, 30, 0, 5]),
+    (4, 2, 64, 16, 1, 4, [3, 0]),
+    (16, 4, 256, 8, 1, 300, [0, 9, 1]),
+    (32, 8, 128, 16, 2, 700, [2 + i for i in range(24)]),
+    (64, 8, 128, 32, 1, 40, [0] * 40),
+]
+shapes = pytest.mark.parametrize("hq,hkv,d,bs,n,blocks,own", SHARED)
+
+
+def shared_rig(dtype, hq, hkv, d, bs, n, blocks, own):
+    g = gen(d + n)
+    table, lens, pool = ref.shared_table(np.random.default_rng(d), own, bs, [0, len(own)], [blocks])
+    cache = ref.random_cache(g, pool, bs, hkv, d, dtype)
+    q = torch.randn((len(own), n, hq, d), generator=g).bfloat16()
+    return table, lens, cache, q
+
+
+@formats
+@shapes
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+def test_a_nan_query_behind_a_prefix(dtype, hq, hkv, d, bs, n, blocks, own, softcap):
+    table, lens, cache, q = shared_rig(dtype, hq, hkv, d, bs, n, blocks, own)
+    ctx = ctx_of(hq, hkv, d, bs)
+    kp, vp, sc, t = up(*cache, table)
+    run = lambda x: ctx.decode_shared(x.cuda(), kp, vp, t, i32(lens), i32([blocks]), softcap=softcap, scales=sc)  # noqa: E731
+    clean = run(q)
+    assert torch.isfinite(clean).all()
+    for b in {0, 1, len(own) - 1}:
+        bad = q.clone()
+        bad[b, n // 2, hq - 1, 5] = NAN
+        out = run(bad)
+        rest = torch.ones(q.shape[:3], dtype=torch.bool)
+        rest[b, n // 2, hq - 1] = False
+        assert torch.isnan(out[~rest.cuda()]).all()
+        assert torch.equal(out[rest.cuda()], clean[rest.cuda()])
+    assert ctx.read_device_errors() == 0
+
+
+@formats
+@shapes
+def test_nan_keys_all_over_a_prefix(dtype, hq, hkv, d, bs, n, blocks, own):
+    """Its second quarter, and all of it: pieces without a score that is a number."""
+    table, lens, cache, q = shared_rig(dtype, hq, hkv, d, bs, n, blocks, own)
+    ctx = ctx_of(hq, hkv, d, bs)
+    G, L = hq // hkv, blocks * bs
+    kp, vp, sc, t, qq = up(*cache, table, q)
+    clean = ctx.decode_shared(qq, kp, vp, t, i32(lens), i32([blocks]), scales=sc)
+    for tokens in (range(L // 4, L // 2), range(L)):
+        bad = [None if c is None else c.clone() for c in cache]
+        poison_keys(bad, table, 0, tokens, bs, hkv - 1)
+        kp, vp, sc = up(*bad)
+        out = ctx.decode_shared(qq, kp, vp, t, i32(lens), i32([blocks]), scales=sc)
+        assert torch.isnan(out[:, :, -G:]).all()
+        assert torch.equal(out[:, :, :-G], clean[:, :, :-G])
