@@ -662,7 +662,8 @@ pda_status pda_decode_cache(pda_ctx* ctx, const pda_bf16* q, const pda_cache* ca
  *   slopes   [Hq] fp32 (device) or NULL: s += slopes[h] * (t - i), where t is
  *            the key's token and i the query's own (seq_len - q_len + its
  *            index), so t - i <= 0.  After the cap.
- * Both are taken in fp32; tanh is off by a few 2^-24 of the cap.
+ * Both are taken in fp32; the capped score is off by a few 2^-24 of the cap, or, for
+ * caps above 128, by 2^-19 of itself.
  */
 typedef struct pda_scoring {
     float softcap;

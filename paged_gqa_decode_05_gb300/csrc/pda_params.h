@@ -108,9 +108,14 @@ struct alignas(16) PrefixSeq {
     int32_t work, total, ctas, pad;
 };
 
+// Caps above this are wide: tanh's definition, off by a few 2^-24 of the cap, would
+// be off by 2^-14 and more, which is an error of a weight's exponent.
+constexpr float kPlainCap = 128.f;
+
 // What the scored modes add to a launch.  Scores are in base-2 units.
 struct Scoring {
-    float cap, inv_cap;          // cap * log2 e, and 2 log2 e over that; 0: scores as they are
+    float cap, wide_cap;         // cap * log2 e, up to and above kPlainCap; both 0: scores as they are
+    float inv_cap;               // 2 log2 e over that
     const float* slopes;         // [Hq] or null: score += slope * (token - the query's own)
     float* scores;               // [launch row][Hkv][tokens][rows_per_slot] out, or null
     float* row_ml;               // [B * q_len * Hq][2] out: (m, l) of every output row, or null

@@ -554,6 +554,34 @@ __device__ __forceinline__ void tmem_ld_row(uint32_t taddr, float2 (&v)[N]) {
     for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i].x), "+f"(v[i].y));
 }
 
+// A tile under a wide cap, in place: this thread's row at `t` becomes what times its
+// multiplier (the score scale, 8-bit: with the K scale) is the capped score, so that
+// the passes below know nothing of it (two roundings more).  A call where no part of
+// the row is in registers, four columns at a time, so that its code is small: with the
+// series beside the other cap's code 64 sequences behind 16384 tokens in e4m3, at a cap
+// of 50, took 126.8 us for 117.8 without it; so 119.8.
+template <int FMT>
+__device__ __noinline__ void prefix_wide_cap(uint32_t t, const float* kscale, float mult, float cap) {
+    const float unit = cap * 0.34657359f;  // ln 2 / 2: z back to the score
+#pragma unroll 1
+    for (int c = 0; c < kPrefixTile; c += 4) {
+        float x[4];
+        uint32_t* r = reinterpret_cast<uint32_t*>(x);
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(t + c) : "memory");
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            asm volatile("" : "+f"(x[i]));  // (not used ahead of the wait)
+            const float f = FMT == kBf16 ? mult : kscale[c + i], z = x[i] * f;
+            x[i] = f == 0.f ? z : capped_wide(cap, z * unit, z) / f;
+        }
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};"
+                     ::"r"(t + c), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+    }
+    tmem_wait_st();
+}
+
 template <int D, int FMT>
 __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, const PrefixGroup* groups, uint32_t base, uint8_t* smem, volatile int* abort_flag,
                                                uint32_t tmem, int warp, int lane) {
@@ -626,6 +654,7 @@ __device__ __forceinline__ void prefix_softmax(const PrefixParams& p, const Pref
                 const float* kscale = reinterpret_cast<const float*>(smem + C::kScale0) +
                                       (FMT == kBf16 ? 0 : (tile0 + jj) % C::kRing * (2 * kT));
                 const float f = bare ? p.score_mult : 1.f;
+                if (p.wide_cap != 0.f) prefix_wide_cap<FMT>(tS, kscale, p.score_mult, p.wide_cap);
                 float top = kNegInf;
 #pragma unroll 1
                 for (int c = 0; c < kT; c += kPart) {

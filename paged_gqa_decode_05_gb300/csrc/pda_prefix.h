@@ -28,7 +28,7 @@ struct PrefixParams {
     int32_t boxes;              // rows come as TMA boxes (block sizes from 8), else one by one
     int32_t B, q_len, Hq, Hkv, G, n_groups;
     float score_mult;           // score scale in base-2 units; under a cap, what capped() takes the exponential of
-    float cap;                  // in base-2 units
+    float cap, wide_cap;        // in base-2 units (Scoring)
     const float* slopes;
 };
 

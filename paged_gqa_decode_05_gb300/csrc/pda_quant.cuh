@@ -603,9 +603,14 @@ __device__ __forceinline__ void run_quant_consumer(const QuantParams& p, uint32_
                     }
                 }
                 if constexpr (kExt) {
-                    if (p.sc.cap != 0.f) {
+                    if (p.sc.inv_cap != 0.f) {
+                        if (p.sc.wide_cap == 0.f) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) x[r][i] = capped(p.sc, x[r][i]);
+                            for (int i = 0; i < 4; ++i) x[r][i] = capped(p.sc, x[r][i]);
+                        } else {
+                            const float4 y = capped_wide4(p.sc.wide_cap, p.sc.inv_cap, make_float4(x[r][0], x[r][1], x[r][2], x[r][3]));
+                            x[r][0] = y.x; x[r][1] = y.y; x[r][2] = y.z; x[r][3] = y.w;
+                        }
                     }
                     const int far = pos0 + 16 * r + g - md.lim;  // the token's place less the first query's
                     if (p.sc.slopes) {

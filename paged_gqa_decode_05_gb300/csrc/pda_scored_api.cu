@@ -172,8 +172,9 @@ pda_status run_scored(pda_ctx* ctx, const Call& c, const pda::Scoring& sc, const
 pda::Scoring scoring_of(const pda_scoring* s) {
     pda::Scoring sc = {};
     if (!s) return sc;
-    sc.cap = s->softcap * kLog2e;
-    sc.inv_cap = s->softcap > 0.f ? 2.f * kLog2e / sc.cap : 0.f;
+    const float cap = s->softcap * kLog2e;
+    (s->softcap > pda::kPlainCap ? sc.wide_cap : sc.cap) = cap;
+    sc.inv_cap = s->softcap > 0.f ? 2.f * kLog2e / cap : 0.f;
     sc.slopes = s->slopes;
     return sc;
 }
@@ -440,7 +441,8 @@ PDA_EXPORT pda_status pda_decode_shared(pda_ctx* ctx, const pda_bf16* q, const p
     pp.G = ctx->G;
     pp.n_groups = groups;
     pp.cap = sc.cap;
-    if (sc.cap != 0.f) pp.score_mult *= sc.inv_cap;
+    pp.wide_cap = sc.wide_cap;
+    if (sc.inv_cap != 0.f) pp.score_mult *= sc.inv_cap;
     pp.slopes = sc.slopes;
     sc.shared = shared_blocks;
     sc.starts = starts;
