@@ -709,8 +709,8 @@ pda_status pda_decode_scored(pda_ctx* ctx, const pda_bf16* q, const pda_cache* c
  * all the queries of its group.
  *   shared_blocks  [groups] int32 (device): the first shared_blocks[p] entries
  *                  of the table rows of group p are taken to be the same; those
- *                  of its first sequence are read.  Other entries, and seq_lens,
- *                  are the whole sequences', as everywhere.
+ *                  of the first sequence that sees all of them are read.  Other
+ *                  entries, and seq_lens, are the whole sequences', as everywhere.
  *   starts         [groups + 1] int32 (device), not decreasing: group p is the
  *                  sequences starts[p] .. starts[p+1] - 1; sequences of no group
  *                  share nothing.  NULL: batch / groups (exact) each.
@@ -721,7 +721,8 @@ pda_status pda_decode_scored(pda_ctx* ctx, const pda_bf16* q, const pda_cache* c
  *   scratch        16-byte aligned, pda_decode_shared_scratch() bytes; no two calls
  *                  that may run at the same time share it.
  * A sequence may end inside the prefix, or be empty: one whose first query does
- * not see all of the prefix is decoded alone.  V scales of an 8-bit prefix enter
+ * not see all of the prefix is decoded alone, from its own table row, of which
+ * nothing past its length is read.  V scales of an 8-bit prefix enter
  * the weights in fp32 times 2^-40; what falls below 2^-126 then, values below
  * 2^-86, counts as 0.
  */
