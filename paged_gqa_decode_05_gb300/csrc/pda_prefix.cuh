@@ -219,7 +219,9 @@ __device__ __forceinline__ void prefix_plan(const PrefixParams& p, PrefixGroup* 
             out.start = e.start;
             out.blocks = e.blocks;
             out.pairs = ((e.end - e.start) * p.q_len * p.G + 128 * C::kStreams - 1) / (128 * C::kStreams);
-            out.tiles = out.pairs > 0 ? (int32_t)((((int64_t)out.blocks << p.lbs) + C::kT - 1) / C::kT) : 0;
+            // (a prefix of 2^31 tokens and more is longer than any sequence: nobody shares it)
+            const int64_t tokens = (int64_t)out.blocks << p.lbs;
+            out.tiles = out.pairs > 0 && tokens <= INT32_MAX ? (int32_t)((tokens + C::kT - 1) / C::kT) : 0;
         }
         const int32_t u = out.tiles > 0 ? out.pairs * p.Hkv : 0, w = u * out.tiles;
         int32_t us = u, wsum = w;

@@ -51,3 +51,23 @@ def test_groups_that_others_lead(dtype, case, hq, hkv, d, bs, n, pad):
         got = ctx.decode_shared(qq, kp, vp, t, i32(lens), i32(shared), starts=i32(starts), scales=sc)
         assert ctx.read_device_errors() == 0
         within(got, want, BF16 * want.abs() + product(dtype) * size)
+
+
+@formats
+@pytest.mark.parametrize("shared", [1 << 25, (1 << 26) + 1, (1 << 26) + 2])
+def test_prefixes_past_31_bits_of_tokens(dtype, shared):
+    """2^31 and 2^32 + 64 tokens, as a table of that width may be told to share: longer than any sequence, so that all
+    are decoded alone, where 32 bits of tokens wrap to a prefix of nothing, one or two blocks."""
+    hq, hkv, d, bs, lens = 4, 1, 64, 64, [200]
+    g = gen(3)
+    cache = ref.random_cache(g, 5, bs, hkv, d, dtype)
+    q = torch.randn((1, 1, hq, d), generator=g).bfloat16()
+    row = torch.tensor([[3, 0, 2, 1]], dtype=torch.int32)
+    want, size, _ = ref.scored64(q, *cache, row, lens, bs)
+    kp, vp, sc, qq = up(*cache, q)
+    table = torch.zeros((1, (1 << 26) + 8), dtype=torch.int32, device="cuda")
+    table[:, :4] = row.cuda()
+    ctx = ctx_of(hq, hkv, d, bs)
+    got = ctx.decode_shared(qq, kp, vp, table, i32(lens), i32([shared]), scales=sc)
+    within(got, want, BF16 * want.abs() + product(dtype) * size)
+    assert ctx.read_device_errors() == 0
