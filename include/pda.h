@@ -681,7 +681,8 @@ typedef struct pda_scoring {
  *   weights_out[block, g, slot] = old + sum p,   p = softmax(s) of this call,
  *   weights_in,
  *   weights_out  [num_blocks, Hkv, block_size] fp32, placed as the tokens are;
- *             weights_in may be weights_out (sums in place), or NULL (old = 0).
+ *             weights_in may be weights_out (sums in place) or apart from it, or
+ *             NULL (old = 0).
  *   old       weights_in's, except that the last q_len tokens, the queries' own,
  *             start from 0: what a reused slot held does not count.  Entries
  *             of no token of the batch are left as they were.
@@ -689,7 +690,8 @@ typedef struct pda_scoring {
  *             batch, q_len and max_blocks: the scores, 4 bytes for each token
  *             and q head of a table of that width.  Not needed without weights;
  *             no two calls that may run at the same time share it.
- * No two sequences of the call may share a block whose weights they sum.
+ * No two sequences of the call may share a block whose weights they sum, nor may one
+ * name a block of its tokens twice.
  * Every sum is taken in one order: a call's weights do not vary from run to run.
  * batch * q_len <= max_seqs.  Other arguments as pda_decode_cache; scores are as
  * exact as there (bf16 caches: products and sums in fp32, weights in two bf16
@@ -750,11 +752,11 @@ pda_status pda_decode_shared(pda_ctx* ctx, const pda_bf16* q, const pda_cache* c
  *                 must hold min(keep, max_blocks * block_size) tokens.  The
  *                 sequences' own blocks are then left as they were.  NULL (or
  *                 block_table): in place, to the front of the sequence's own
- *                 blocks, which no other sequence may share; what lies behind
- *                 new_len is left as it was.
+ *                 blocks, which no other sequence may share nor its own row name
+ *                 twice; what lies behind new_len is left as it was.
  *   kept          [batch, Hkv, keep] int32 out (device): the former index of
  *                 each token, -1 from new_len on.
- *   new_lens      [batch] int32 out (device), min(seq_len, keep); not seq_lens.
+ *   new_lens      [batch] int32 out (device), min(seq_len, keep); apart from seq_lens.
  * The token of a bad block id counts as zeros of sum 0.  Rotary positions are in
  * the keys and stay; a distance bias (pda_scoring) does not fit a cache whose
  * tokens have moved up.

@@ -22,6 +22,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
 
+bool overlap(const void* a, const void* b, int64_t bytes) {
+    const int64_t d = (int64_t)((uintptr_t)a - (uintptr_t)b);
+    return d < bytes && d > -bytes;
+}
+
 // Launch rows of scored decode: up to 8 q rows of a sequence each, or, over bf16
 // caches of head sizes up to 128 where a sequence has more, up to 32 (one walk
 // over K and V for four).  3 sequences of 8000 tokens with 40 q and 8 kv heads of
@@ -331,6 +336,9 @@ PDA_EXPORT pda_status pda_decode_scored(pda_ctx* ctx, const pda_bf16* q, const p
     if (weights_in && !weights_out) return fail(PDA_ERR_INVALID_ARG, "weights_in without weights_out");
     if (!aligned(weights_in, 4) || !aligned(weights_out, 4))
         return fail(PDA_ERR_INVALID_ARG, "weights must be 4-byte aligned");
+    if (weights_in && weights_in != weights_out &&
+        overlap(weights_in, weights_out, cache->num_blocks * ctx->dims.num_kv_heads * ctx->dims.block_size * 4))
+        return fail(PDA_ERR_INVALID_ARG, "weights_in must be weights_out, or apart from it");
     if (batch == 0) return PDA_OK;
     if (weights_out && (st = check_weights_width(ctx, max_blocks)) != PDA_OK) return st;
     const WeightsScratch ws = weights_scratch(ctx, cache->format == PDA_CACHE_BF16, batch, q_len, max_blocks);
@@ -496,7 +504,7 @@ PDA_EXPORT pda_status pda_evict(pda_ctx* ctx, const pda_cache* cache, float* wei
     for (const void* a : {(const void*)weights, (const void*)block_table, (const void*)seq_lens, (const void*)out_table,
                           (const void*)kept, (const void*)new_lens})
         if (!aligned(a, 4)) return fail(PDA_ERR_INVALID_ARG, "eviction arrays must be 4-byte aligned");
-    if (new_lens == seq_lens) return fail(PDA_ERR_INVALID_ARG, "new_lens must not be seq_lens");
+    if (overlap(new_lens, seq_lens, (int64_t)batch * 4)) return fail(PDA_ERR_INVALID_ARG, "new_lens must not overlap seq_lens");
     if (max_blocks < 1 || (out_table && out_blocks < 1))
         return fail(PDA_ERR_INVALID_ARG, "block table width must be >= 1 (got %d, %d)", max_blocks, out_blocks);
     const int64_t tokens = (int64_t)max_blocks * d.block_size;
