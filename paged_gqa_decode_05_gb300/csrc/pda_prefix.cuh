@@ -37,12 +37,13 @@
 // Bounds.  One q tile in bf16: memory; 32768 tokens of 8 kv heads of 128 (134 MB,
 // 19.8 us at the measured copy rate) take 20 us of token tiles, with 3 before the
 // first and 2 behind the last.  Two q tiles in 8 bits: the softmax; 16384 tokens of
-// 8 kv heads and 512 rows take 74 us (26 at the products' rate), 54 tiles of 64 tokens
-// a stream of 1260 cycles to the maximum (capped) and 720 for the weights.  No pipe is
-// full (fp32 35 %, exponentials 26 %, tensor 33 %, issue slots 53 %): a scheduler's two
-// softmax warps have 0.9 ready between them.  Sixteen softmax warps instead of eight:
-// 155 us a call for 124; P's parts 16 tokens wide instead of 32: no faster; all of a row
-// unrolled: slower, its code no longer stays in the instruction caches.
+// 8 kv heads and 512 rows take 74 us (26 at the products' rate), 28 tiles of 64 tokens
+// a stream, each of 2300 cycles to the maximum (capped), 1450 for the weights and 500 of
+// waits.  No pipe is full (fp32 35 %, exponentials 26 %, tensor 33 %, issue slots 53 %): a
+// scheduler's two softmax warps have 0.9 ready between them.  Sixteen softmax warps
+// instead of eight: 155 us a call for 124; P's parts 16 tokens wide instead of 32: no
+// faster; all of a row unrolled: slower, its code no longer stays in the instruction
+// caches.
 #pragma once
 
 #include <cuda_fp16.h>

@@ -19,8 +19,8 @@ struct ScoredShape {
 
 // An instance: stages of st rows (bf16 caches), a cache format, the q rows of a
 // launch row (1: one query; 8: several causal ones; bf16 at head sizes up to 128
-// 16 and 32), and (8-bit caches) weights in two fp16 parts, for outputs and states
-// in fp32.
+// 16 and 32), and (8-bit caches) weights in two fp16 parts, for calls whose output is
+// in fp32 (the states that a shared prefix's bf16 outputs come from take one, too).
 struct ScoredForm {
     int st, format, rows;
     bool fine;

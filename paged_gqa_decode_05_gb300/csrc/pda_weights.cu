@@ -289,8 +289,10 @@ cudaError_t launch_weights(const WeightsParams& p, int sms, cudaStream_t stream)
 // out = o / l of the prefix's pieces and the state of the sequence's own tokens.
 // A thread takes four columns of an output row and, where rows are few, every
 // kJ-th piece, eight of them a round trip; a prefix that fills the GPU leaves about
-// 152 / units pieces.  Whole calls with a CTA a row and a row a thread's columns:
-// 1024 rows of 19 pieces 51.7 and 54.3 us, 4096 of 9 122 and 115.
+// 152 / units pieces.  Whole calls behind 8192 tokens, 8 kv heads of 128, with a CTA a
+// row and a row a thread's columns: 1024 rows 34.1 and 36.6 us, 1536 46.1 and 46.7, 2048
+// 52.4 and 51.8, 4096 74.5 and 69.5; 4 kv heads of 64 in e4m3 34.1 and 37.7, 42.1 and
+// 42.8, 45.1 and 44.5, 69.9 and 61.7.
 // (In the split kernel's segment ends instead, it cost that kernel its registers:
 // 32 sequences of 4096 tokens without any prefix 89 us for 81.)
 
