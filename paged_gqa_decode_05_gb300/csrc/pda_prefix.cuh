@@ -402,6 +402,7 @@ __device__ __forceinline__ void prefix_load(const PrefixParams& p, const PrefixG
             const uint32_t m = __shfl_sync(0xffffffffu, queue, spread & 31u), c = m >> 1;
             if (!(ok = wait(base + C::kLanded + 8 * (2 * c + half), m & 1u))) break;
             if (k) {  // K's scales times what every score is multiplied by
+                __syncwarp();  // (another lane's zeros, of a bad block id, among them)
                 float* ks = reinterpret_cast<float*>(smem + C::kScale0) + spread % C::kRing * (2 * C::kT) + row0 + lane;
                 *ks *= p.score_mult;
             }
