@@ -693,6 +693,9 @@ typedef struct pda_scoring {
  * No two sequences of the call may share a block whose weights they sum, nor may one
  * name a block of its tokens twice.
  * Every sum is taken in one order: a call's weights do not vary from run to run.
+ * NaN reaches outputs as in pda_decode_cache; a query whose scores hold one makes the
+ * sums of the tokens that it sees NaN, as does, over an 8-bit cache, a V scale that is
+ * NaN for the queries that see its row.
  * batch * q_len <= max_seqs.  Other arguments as pda_decode_cache; scores are as
  * exact as there (bf16 caches: products and sums in fp32, weights in two bf16
  * parts).
